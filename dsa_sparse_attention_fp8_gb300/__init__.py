@@ -9,8 +9,13 @@ and raises if it was not built (there is no CPU fallback).
 from . import binding  # noqa: F401
 from .binding import (  # noqa: F401
     DsaError,
+    add_rms_norm,
+    alloc_attention_workspace,
+    build_block_tables,
+    kv_write,
     layer_is_full,
     layer_stack_run,
+    paged_attention,
     quantize_fp8_blocks,
     score_topk,
     workspace_bytes,

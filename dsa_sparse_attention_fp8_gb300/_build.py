@@ -44,21 +44,33 @@ def up_to_date() -> bool:
 
 
 def build_library(quiet: bool = False, force: bool = False) -> Path:
-    """Compile csrc/dsa_indexer.cu into _lib/libdsa_indexer.so unless it is current."""
+    """Compile csrc/*.cu (in parallel) into _lib/libdsa_indexer.so unless it is current."""
     if not force and up_to_date():
         return LIB
     LIB_DIR.mkdir(parents=True, exist_ok=True)
     tmp = LIB.with_suffix(f".so.tmp{os.getpid()}")
-    cmd = [
-        _nvcc(), *ARCH_FLAGS, "-O3", "-lineinfo", "-std=c++17",
-        "-Xcompiler", "-fPIC", "-shared", "-I", str(INCLUDE),
-        "-o", str(tmp), str(CSRC / "dsa_indexer.cu"),
-    ]
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError("nvcc failed:\n" + " ".join(cmd) + "\n" + res.stdout + res.stderr)
-    if not quiet and res.stderr.strip():
-        print(res.stderr)
+    flags = [*ARCH_FLAGS, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
+             "-I", str(INCLUDE)]
+    objs = {src: LIB_DIR / f"{src.stem}.{os.getpid()}.o" for src in sorted(CSRC.glob("*.cu"))}
+    jobs = []
+    for src, obj in objs.items():
+        cmd = [_nvcc(), *flags, "-c", "-o", str(obj), str(src)]
+        jobs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT,
+                                           text=True)))
+    said = [(cmd, proc.communicate()[0], proc.returncode) for cmd, proc in jobs]
+    try:
+        for cmd, text, rc in said:
+            if rc != 0:
+                raise RuntimeError("nvcc failed:\n" + " ".join(cmd) + "\n" + text)
+            if not quiet and text.strip():
+                print(text)
+        cmd = [_nvcc(), *ARCH_FLAGS, "-shared", "-o", str(tmp), *map(str, objs.values())]
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        if res.returncode != 0:
+            raise RuntimeError("nvcc failed:\n" + " ".join(cmd) + "\n" + res.stdout + res.stderr)
+    finally:
+        for obj in objs.values():
+            obj.unlink(missing_ok=True)
     os.replace(tmp, LIB)
     STAMP.write_text(_stamp_text())
     return LIB

@@ -33,6 +33,7 @@ ERRORS = {
 STATUS_BAD_PAGE = 0x1
 STATUS_BAD_METADATA = 0x2
 STATUS_TIMEOUT = 0x4
+STATUS_NO_PAGES = 0x8
 
 # every symbol declared in include/dsa_indexer.h
 EXPORTS = (
@@ -54,6 +55,11 @@ EXPORTS = (
     "dsa_layer_stack_run_compressed",
     "dsa_mla_write_kv",
     "dsa_sparse_mla_attention",
+    "dsa_block_tables_build",
+    "dsa_kv_write",
+    "dsa_paged_attention_workspace_bytes",
+    "dsa_paged_attention",
+    "dsa_add_rms_norm",
 )
 
 
@@ -86,6 +92,17 @@ class LayerIOBf16(ctypes.Structure):
         ("score_begin", ctypes.c_void_p),
         ("score_end", ctypes.c_void_p),
     ]
+
+
+class KvCache(ctypes.Structure):
+    _fields_ = (
+        [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale")]
+        + [(n, ctypes.c_int64) for n in (
+            "k_page_stride", "k_token_stride", "k_head_stride",
+            "v_page_stride", "v_token_stride", "v_head_stride",
+            "k_scale_page_stride", "k_scale_head_stride",
+            "v_scale_page_stride", "v_scale_head_stride", "num_pages")]
+        + [(n, ctypes.c_int) for n in ("num_kv_heads", "head_dim", "type")])
 
 
 _lib: Optional[ctypes.CDLL] = None
@@ -142,6 +159,21 @@ def _declare(lib: ctypes.CDLL) -> None:
     lib.dsa_sparse_mla_attention.restype = _I
     lib.dsa_sparse_mla_attention.argtypes = [
         _P, _I, _I, _P, _I64, _P, _P, _I, _P, _I, _P, _I, ctypes.c_float, _P, _P, _P, _P]
+    _F = ctypes.c_float
+    lib.dsa_block_tables_build.restype = _I
+    lib.dsa_block_tables_build.argtypes = [_P, _P, _I, _P, _I, _P, _I, _I, _P, _P, _P, _P, _P, _P]
+    lib.dsa_kv_write.restype = _I
+    lib.dsa_kv_write.argtypes = [
+        _P, _I64, _I64, _P, _I64, _I64, _I, _I, _P, ctypes.POINTER(KvCache), _P, _P]
+    lib.dsa_paged_attention_workspace_bytes.restype = _SZ
+    lib.dsa_paged_attention_workspace_bytes.argtypes = []
+    lib.dsa_paged_attention.restype = _I
+    lib.dsa_paged_attention.argtypes = [
+        _P, _I64, _I64, _I, _I, _I, ctypes.POINTER(KvCache), _P, _P, _I, _P, _I, _F, _I, _I, _P,
+        _I64, _I64, _P, _P, _SZ, _P, _P]
+    lib.dsa_add_rms_norm.restype = _I
+    lib.dsa_add_rms_norm.argtypes = [
+        _P, _I64, _P, _I64, _P, _I, _I, _I, _F, _P, _I64, _P, _I64, _P, _P, _P]
     lib.dsa_layer_stack_run_bf16.restype = _I
     lib.dsa_layer_stack_run_bf16.argtypes = [
         _I, ctypes.c_char_p, _I, _I, ctypes.POINTER(LayerIOBf16), _I, _I, _P, _P, _I, _P, _I,
@@ -577,3 +609,191 @@ def sparse_mla_attention(q: torch.Tensor, kv_cache: torch.Tensor, query_start_lo
         topk_indices.shape[1], float(softmax_scale), _ptr(out), _ptr(lse), _ptr(status),
         _stream(stream)))
     return out, lse
+
+
+# ------------------------------------------- tables, K/V cache, attention, norm
+TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+TYPE_E4M3 = 3
+NORM_GROUP = 128
+
+
+def _same_device(*tensors: Optional[torch.Tensor]) -> None:
+    dev = tensors[0].device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors lie on {dev} and {t.device}")
+
+
+def _type_of(t: torch.Tensor, name: str, most: int = 1) -> int:
+    kind = TYPES.get(t.dtype)
+    if kind is None or kind > most:
+        wanted = ", ".join(str(d) for d, k in TYPES.items() if k <= most)
+        raise TypeError(f"{name} must be one of {wanted}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return kind
+
+
+def _need_like(t: torch.Tensor, name: str, like: torch.Tensor, shape) -> None:
+    """`t` has like's dtype, this shape and a contiguous last dimension."""
+    if t.dtype != like.dtype:
+        raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+
+
+def build_block_tables(query_lens: torch.Tensor, seq_lens: torch.Tensor, free_pages: torch.Tensor,
+                       block_table: torch.Tensor, query_start_loc: torch.Tensor,
+                       positions: torch.Tensor, slot_mapping: torch.Tensor,
+                       pages_used: torch.Tensor, status: Optional[torch.Tensor] = None,
+                       stream=None) -> None:
+    """A step's block tables and slot maps from the requests' lengths
+    (dsa_block_tables_build): block_table [R, max_blocks] gains the new pages
+    (taken from free_pages in request order), and query_start_loc [R+1],
+    positions [T], slot_mapping [T] and pages_used [1] are written."""
+    R, T = query_lens.shape[0], positions.shape[0]
+    _need(query_lens, "query_lens", torch.int32, (R,))
+    _need(seq_lens, "seq_lens", torch.int32, (R,))
+    _need(free_pages, "free_pages", torch.int32, (None,))
+    _need(block_table, "block_table", torch.int32, (R, None))
+    _need(query_start_loc, "query_start_loc", torch.int32, (R + 1,))
+    _need(positions, "positions", torch.int32, (T,))
+    _need(slot_mapping, "slot_mapping", torch.int64, (T,))
+    _need(pages_used, "pages_used", torch.int32, (1,))
+    if status is not None:
+        _need(status, "status", torch.int32)
+    _same_device(query_lens, seq_lens, free_pages, block_table, query_start_loc, positions,
+                 slot_mapping, pages_used, status)
+    _check(load().dsa_block_tables_build(
+        _ptr(query_lens), _ptr(seq_lens), R, _ptr(free_pages), free_pages.shape[0],
+        _ptr(block_table), block_table.shape[1], T, _ptr(query_start_loc), _ptr(positions),
+        _ptr(slot_mapping), _ptr(pages_used), _ptr(status), _stream(stream)))
+
+
+def _kv_cache(k_cache, v_cache, k_scale, v_scale, like, heads, dim) -> KvCache:
+    """The C description of a paged K/V cache after checking its tensors."""
+    pages = k_cache.shape[0]
+    shape = (pages, PAGE_TOKENS, heads, dim)
+    if k_cache.dtype == torch.uint8:
+        if k_scale is None or v_scale is None:
+            raise ValueError("a uint8 (E4M3) cache needs k_scale and v_scale")
+        kind = TYPE_E4M3
+        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if t.dtype != torch.float32:
+                raise TypeError(f"{name} must be torch.float32, got {t.dtype}")
+            _need_like(t, name, t, (pages, heads, PAGE_TOKENS))
+        sk, sv = k_scale.stride(), v_scale.stride()
+        scales = (k_scale.data_ptr(), v_scale.data_ptr())
+    else:
+        if k_scale is not None or v_scale is not None:
+            raise ValueError("scales go with a uint8 (E4M3) cache")
+        kind = TYPES.get(k_cache.dtype)
+        if k_cache.dtype != like.dtype:
+            raise TypeError(f"k_cache must be {like.dtype} or torch.uint8, got {k_cache.dtype}")
+        sk = sv = (0, 0)
+        scales = (None, None)
+    _need_like(k_cache, "k_cache", k_cache, shape)
+    _need_like(v_cache, "v_cache", k_cache, shape)
+    _same_device(like, k_cache, v_cache, k_scale, v_scale)
+    a, b = k_cache.stride(), v_cache.stride()
+    return KvCache(k_cache.data_ptr(), v_cache.data_ptr(), *scales, a[0], a[1], a[2], b[0], b[1],
+                   b[2], sk[0], sk[1], sv[0], sv[1], pages, heads, dim, kind)
+
+
+def kv_write(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor, k_cache: torch.Tensor,
+             v_cache: torch.Tensor, k_scale: Optional[torch.Tensor] = None,
+             v_scale: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+             stream=None) -> None:
+    """Store the new tokens' keys and values (k, v [T, Hkv, D], BF16 or FP16)
+    at their slots of k_cache, v_cache [num_pages, 64, Hkv, D] (dsa_kv_write):
+    copied into caches of the same type, or quantised into uint8 (E4M3) caches
+    with scales [num_pages, Hkv, 64]."""
+    kind = _type_of(k, "k")
+    T, heads, dim = k.shape
+    _need_like(k, "k", k, (T, heads, dim))
+    _need_like(v, "v", k, (T, heads, dim))
+    _need(slot_mapping, "slot_mapping", torch.int64, (T,))
+    cache = _kv_cache(k_cache, v_cache, k_scale, v_scale, k, heads, dim)
+    if status is not None:
+        _need(status, "status", torch.int32)
+    _same_device(k, v, slot_mapping, status)
+    _check(load().dsa_kv_write(
+        k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1), kind, T,
+        slot_mapping.data_ptr(), ctypes.byref(cache), _ptr(status), _stream(stream)))
+
+
+def attention_workspace_bytes() -> int:
+    return int(load().dsa_paged_attention_workspace_bytes())
+
+
+def alloc_attention_workspace(device="cuda") -> torch.Tensor:
+    """A zeroed workspace for paged_attention, whatever the batch."""
+    return torch.zeros(attention_workspace_bytes(), dtype=torch.uint8, device=device)
+
+
+def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                    query_start_loc: torch.Tensor, seq_lens: torch.Tensor,
+                    block_table: torch.Tensor, softmax_scale: float, workspace: torch.Tensor,
+                    window: int = 0, num_sinks: int = 0, k_scale: Optional[torch.Tensor] = None,
+                    v_scale: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                    lse: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                    stream=None):
+    """Attention of the step's query rows (q [T, Hq, D], BF16 or FP16) over the
+    paged K/V cache [num_pages, 64, Hkv, D], causal; window > 0 keeps the last
+    `window` tokens and the first `num_sinks` (dsa_paged_attention).  Returns
+    (out [T, Hq, D] like q, lse [T, Hq] FP32)."""
+    kind = _type_of(q, "q")
+    T, Hq, dim = q.shape
+    R = seq_lens.shape[0]
+    _need_like(q, "q", q, (T, Hq, dim))
+    cache = _kv_cache(k_cache, v_cache, k_scale, v_scale, q, k_cache.shape[2], dim)
+    _need(query_start_loc, "query_start_loc", torch.int32, (R + 1,))
+    _need(seq_lens, "seq_lens", torch.int32, (R,))
+    _need(block_table, "block_table", torch.int32, (R, None))
+    _need(workspace, "workspace", torch.uint8)
+    if out is None:
+        out = torch.empty((T, Hq, dim), dtype=q.dtype, device=q.device)
+    if lse is None:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+    _need_like(out, "out", q, (T, Hq, dim))
+    _need(lse, "lse", torch.float32, (T, Hq))
+    if status is not None:
+        _need(status, "status", torch.int32)
+    _same_device(q, query_start_loc, seq_lens, block_table, workspace, out, lse, status)
+    _check(load().dsa_paged_attention(
+        q.data_ptr(), q.stride(0), q.stride(1), kind, T, Hq, ctypes.byref(cache),
+        query_start_loc.data_ptr(), seq_lens.data_ptr(), R, block_table.data_ptr(),
+        block_table.shape[1], softmax_scale, window, num_sinks, out.data_ptr(), out.stride(0),
+        out.stride(1), lse.data_ptr(), workspace.data_ptr(), workspace.numel(), _ptr(status),
+        _stream(stream)))
+    return out, lse
+
+
+def add_rms_norm(x: torch.Tensor, residual: Optional[torch.Tensor], weight: torch.Tensor,
+                 eps: float, residual_out: Optional[torch.Tensor] = None,
+                 out: Optional[torch.Tensor] = None, codes: Optional[torch.Tensor] = None,
+                 scales: Optional[torch.Tensor] = None, stream=None) -> None:
+    """h = x + residual (rounded to x's type, written to residual_out) and its
+    root-mean-square norm y (dsa_add_rms_norm): rounded to `out`, and / or
+    quantised to codes [T, N] uint8 (E4M3) with scales [T, ceil(N/128)].  x,
+    residual, residual_out, out [T, N] may have any row stride; residual_out
+    may be x or residual."""
+    kind = _type_of(x, "x", most=2)
+    T, N = x.shape
+    strides = []
+    for t, name in ((x, "x"), (residual, "residual"), (residual_out, "residual_out"), (out, "out")):
+        if t is not None:
+            _need_like(t, name, x, (T, N))
+        strides.append(N if t is None or T == 1 else t.stride(0))
+    _need_like(weight, "weight", x, (N,))
+    if codes is not None:
+        _need(codes, "codes", torch.uint8, (T, N))
+    if scales is not None:
+        _need(scales, "scales", torch.float32, (T, -(-N // NORM_GROUP)))
+    _same_device(x, residual, weight, residual_out, out, codes, scales)
+    _check(load().dsa_add_rms_norm(
+        x.data_ptr(), strides[0], _ptr(residual), strides[1], weight.data_ptr(), kind, T, N, eps,
+        _ptr(residual_out), strides[2], _ptr(out), strides[3], _ptr(codes), _ptr(scales),
+        _stream(stream)))

@@ -14,15 +14,16 @@
 #include <string>
 
 #include "dsa_indexer.h"
+#include "host.h"
 #include "kwrite.cuh"
 #include "mla.cuh"
 #include "plan.cuh"
 #include "score_topk.cuh"
 
-namespace {
+namespace dsa_host {
 
-thread_local std::string g_last_error;
-thread_local int g_last_launches = 0;
+static thread_local std::string g_last_error;
+static thread_local int g_last_launches = 0;
 
 int fail(int code, const char* fmt, ...) {
   char buf[512];
@@ -47,20 +48,6 @@ int sm_count() {
   return n;
 }
 
-// CTAs of the scoring launch: one per SM, at most kMaxCtas.  Without a
-// device (sizing only) the bound itself is used, which over-sizes safely.
-int grid_ctas() {
-  const int n = sm_count();
-  if (n <= 0 || n > dsa::kMaxCtas) return dsa::kMaxCtas;
-  return n;
-}
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-bool supported_heads(int H) {
-  return H == 4 || H == 8 || H == 16 || H == 32 || H == 64 || H == 128;
-}
-
 // ---------------------------------------------------------------- tensor maps
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
@@ -74,6 +61,26 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
       fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
   });
   return fn;
+}
+
+void set_last_launches(int n) { g_last_launches = n; }
+
+}  // namespace dsa_host
+
+namespace {
+
+using namespace dsa_host;
+
+// CTAs of the scoring launch: one per SM, at most kMaxCtas.  Without a
+// device (sizing only) the bound itself is used, which over-sizes safely.
+int grid_ctas() {
+  const int n = sm_count();
+  if (n <= 0 || n > dsa::kMaxCtas) return dsa::kMaxCtas;
+  return n;
+}
+
+bool supported_heads(int H) {
+  return H == 4 || H == 8 || H == 16 || H == 32 || H == 64 || H == 128;
 }
 
 // 2-D uint8 view [rows, 128] with a box of `box_rows` x 128 bytes, 128-byte
@@ -675,7 +682,7 @@ extern "C" {
 
 int dsa_abi_version(void) { return 100; }
 
-const char* dsa_last_error(void) { return g_last_error.c_str(); }
+const char* dsa_last_error(void) { return dsa_host::g_last_error.c_str(); }
 
 int dsa_last_launch_count(void) { return g_last_launches; }
 

@@ -1,0 +1,27 @@
+// Host-side pieces shared by the library's translation units: the calling
+// thread's last error and launch count, device queries and the tensor-map
+// encoder.  Defined in dsa_indexer.cu.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+
+#include <cstdint>
+
+namespace dsa_host {
+
+// Records the message of a failing call and returns its code.
+int fail(int code, const char* fmt, ...);
+// DSA_OK, or DSA_ERR_CUDA with the pending launch error's message.
+int check_launch(const char* what);
+// SMs of the current device (0 without one).
+int sm_count();
+// The driver's cuTensorMapEncodeTiled, or null.
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn();
+// The value dsa_last_launch_count() reports.
+void set_last_launches(int n);
+
+inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+}  // namespace dsa_host

@@ -15,22 +15,14 @@
 #include <cuda_fp8.h>
 #include <cstdint>
 
+#include "common.cuh"
 #include "ptx.cuh"
 
 namespace dsa {
 
 constexpr int kHeadDim = 128;
-constexpr int kPageTokens = 64;
 constexpr int kPageBytes = 8448;
 constexpr int kPageScaleOffset = 8192;
-
-constexpr int kStatusBadPage = 0x1;
-constexpr int kStatusBadMetadata = 0x2;
-constexpr int kStatusTimeout = 0x4;
-
-__device__ __forceinline__ void raise_status(int32_t* status, int bits) {
-  if (status) atomicOr(status, bits);
-}
 
 // Quantise this lane's 4 elements of a 128-element block.  Returns the 4 E4M3
 // codes packed little-endian (element 4*lane first) and the block scale.
@@ -47,16 +39,6 @@ __device__ __forceinline__ uint32_t quantize_lane4(float4 v, float* scale_out) {
   uint32_t c23 = __nv_cvt_float2_to_fp8x2(hi, __NV_SATFINITE, __NV_E4M3);
   *scale_out = s;
   return (c01 & 0xFFFFu) | ((c23 & 0xFFFFu) << 16);
-}
-
-// Request that owns query row t: the last r with query_start_loc[r] <= t.
-__device__ __forceinline__ int find_request(const int32_t* __restrict__ qsl, int R, int t) {
-  int lo = 0, hi = R - 1;
-  while (lo < hi) {
-    int mid = (lo + hi + 1) >> 1;
-    if (__ldg(qsl + mid) <= t) lo = mid; else hi = mid - 1;
-  }
-  return lo;
 }
 
 // The same search over a copy of query_start_loc in shared memory.

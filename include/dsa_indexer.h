@@ -93,6 +93,7 @@ typedef struct CUstream_st* dsa_stream_t; /* same type as cudaStream_t */
 #define DSA_STATUS_BAD_PAGE 0x1      /* block_table entry outside [0, num_pages) */
 #define DSA_STATUS_BAD_METADATA 0x2  /* q_len < 0, seq_len < q_len, seq_len > 64*max_blocks */
 #define DSA_STATUS_TIMEOUT 0x4       /* a bounded on-chip wait gave up; results invalid */
+#define DSA_STATUS_NO_PAGES 0x8      /* dsa_block_tables_build ran out of free pages */
 
 /* Version of this ABI (major*100 + minor). */
 int dsa_abi_version(void);
@@ -411,6 +412,140 @@ int dsa_sparse_mla_attention(const void* q, int T, int Hq, const uint8_t* kv_cac
                              int max_blocks, const int32_t* topk_indices, int index_topk,
                              float softmax_scale, void* out, float* lse, int32_t* dev_status,
                              dsa_stream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Around the caches: block tables and slot maps, an ordinary K/V cache with
+ * its attention, and the norm that makes 8-bit rows.  [HBM] §2.3 and §2.5
+ * (block tables and slot mapping of a step), §5 (the window channel beside
+ * the compressed ones).
+ * ---------------------------------------------------------------------------
+ */
+#define DSA_TYPE_BF16 0
+#define DSA_TYPE_FP16 1
+#define DSA_TYPE_FP32 2
+#define DSA_TYPE_E4M3 3
+
+/*
+ * Block tables and slot maps of a step from the requests' lengths: request r
+ * brings query_lens[r] new tokens and holds seq_lens[r] after the step.  Its
+ * block-table row lists the ceil((seq - q) / 64) pages it had; the pages it
+ * needs beyond those are taken from free_pages[0 .. num_free), in request
+ * order, and appended to the row (the entries after them are left alone).
+ *   query_start_loc [R+1]  exclusive sums of query_lens, the total last.
+ *   positions [T] int32    position of each new token in its request.
+ *   slot_mapping [T] int64 page*64 + pos%64 of each new token.
+ *   pages_used [1]         free pages needed; the caller drops that many.
+ * Rows from the total to T (a batch padded to a fixed T) get position 0 and
+ * slot -1.  Nothing is read but the lengths, the listed free pages and the
+ * table entries that hold the new tokens, so a call repeated with the same
+ * arguments gives the same answer.  R <= 16384.
+ * Faults: lengths that make no sense (q < 0, q > T, seq < q, seq > 64 *
+ * max_blocks), or more tokens than T: DSA_STATUS_BAD_METADATA; such a
+ * request takes no pages and its tokens get slot -1 (q counts as 0 where
+ * q < 0 or q > T).  Too few free pages: DSA_STATUS_NO_PAGES; the entries
+ * without a page are -1, their tokens' slots too.  A negative entry under a
+ * new token: DSA_STATUS_BAD_PAGE, slot -1.
+ * Errors: INVALID_ARG, UNSUPPORTED (R), CUDA.
+ */
+int dsa_block_tables_build(const int32_t* query_lens, const int32_t* seq_lens, int R,
+                           const int32_t* free_pages, int num_free, int32_t* block_table,
+                           int max_blocks, int T, int32_t* query_start_loc, int32_t* positions,
+                           int64_t* slot_mapping, int32_t* pages_used, int32_t* dev_status,
+                           dsa_stream_t stream);
+
+/*
+ * A layer's paged K/V cache.  k and v: [num_pages, 64, num_kv_heads, head_dim]
+ * of `type` (BF16, FP16 or E4M3 codes), any strides that are multiples of 16
+ * bytes (so tokens-first and heads-first pools, and k and v interleaved in
+ * one pool, all fit), the last dimension contiguous.  E4M3 caches have one
+ * FP32 scale per (token, head): k_scale and v_scale [num_pages,
+ * num_kv_heads, 64], the last dimension contiguous; value = code * scale.
+ * Strides are in elements.  head_dim: a multiple of 16 in [16, 128].
+ */
+typedef struct {
+  void* k;
+  void* v;
+  float* k_scale; /* NULL for 16-bit caches */
+  float* v_scale;
+  int64_t k_page_stride, k_token_stride, k_head_stride;
+  int64_t v_page_stride, v_token_stride, v_head_stride;
+  int64_t k_scale_page_stride, k_scale_head_stride;
+  int64_t v_scale_page_stride, v_scale_head_stride;
+  int64_t num_pages;
+  int num_kv_heads, head_dim, type;
+} dsa_kv_cache;
+
+/*
+ * Store each new token's key and value heads (k, v [T, num_kv_heads,
+ * head_dim], BF16 or FP16 as `type` says, strides in elements, multiples of
+ * 8) at its slot.  Into a cache of the same type they are copied; into an
+ * E4M3 cache each head is quantised with the rule of the indexer cache
+ * (s = amax/448, s = 1 for an all-zero head, codes E4M3(x/s) RNE,
+ * saturating).  slot_mapping [T]: page*64 + offset; negative slots write
+ * nothing, slots past the pool set DSA_STATUS_BAD_PAGE and write nothing.
+ * Two tokens with one slot leave either's row.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA.
+ */
+int dsa_kv_write(const void* k, int64_t k_token_stride, int64_t k_head_stride, const void* v,
+                 int64_t v_token_stride, int64_t v_head_stride, int type, int T,
+                 const int64_t* slot_mapping, const dsa_kv_cache* cache, int32_t* dev_status,
+                 dsa_stream_t stream);
+
+/*
+ * Attention of a step's new tokens over the paged K/V cache (which holds the
+ * new tokens too).  For query row t at position p of its request and head h
+ * (key head h / (Hq / num_kv_heads)), over the tokens s the row sees:
+ *   lse[t, h]    = ln sum_s exp(softmax_scale * q[t,h] . k_s)
+ *   out[t, h, :] = sum_s exp(softmax_scale * q[t,h] . k_s - lse) * v_s
+ * The row sees s <= p; with window > 0 only s > p - window and the first
+ * num_sinks tokens (pages outside both are never read: their table entries
+ * may be stale).  Rows that see nothing (rows past query_start_loc[R], those
+ * of requests with bad metadata, rows all of whose pages are bad) give
+ * out = 0, lse = -inf.
+ *   q   [T, Hq, head_dim] BF16 or FP16, strides in elements (multiples of 8),
+ *       16-byte aligned; Hq a multiple of num_kv_heads, at most 128 times it.
+ *       The cache has q's type, or is E4M3 with BF16 queries.
+ *   out as q; lse [T, Hq] FP32 or NULL.
+ *   workspace: dsa_paged_attention_workspace_bytes() bytes, 256-byte aligned,
+ *       zeroed once before its first use; every call leaves it ready for the
+ *       next.  Calls that share one must not overlap on the GPU.
+ * Requests may bring any number of new tokens (none, one, thousands).  Cache
+ * contents that no row of the request sees may hold anything; keys and
+ * values that some row sees must be finite.
+ * Faults: q_len < 0, query_start_loc outside [0, T], seq_len < q_len, seq_len
+ * > 64*max_blocks: DSA_STATUS_BAD_METADATA; a table entry outside the pool
+ * under a token that is seen: DSA_STATUS_BAD_PAGE, its tokens are skipped.
+ * Computation: tensor-core products with FP32 accumulation, FP32 softmax
+ * statistics, probabilities rounded to 16 bits.
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE_TOO_SMALL, CUDA.
+ */
+size_t dsa_paged_attention_workspace_bytes(void);
+int dsa_paged_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride, int type, int T,
+                        int Hq, const dsa_kv_cache* cache, const int32_t* query_start_loc,
+                        const int32_t* seq_lens, int R, const int32_t* block_table, int max_blocks,
+                        float softmax_scale, int window, int num_sinks, void* out,
+                        int64_t out_token_stride, int64_t out_head_stride, float* lse,
+                        void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                        dsa_stream_t stream);
+
+/*
+ * Residual addition, root-mean-square norm and block quantisation of rows:
+ *   h = round(x + residual) to `type` (h = x where residual is NULL)
+ *   y = h * weight / sqrt(mean(h^2) + eps)          (FP32)
+ *   residual_out = h; out = y rounded to `type`; codes, scales = y quantised
+ *   per 128 elements with the rule of the indexer cache (a last group of
+ *   fewer elements has its own scale).
+ * x, residual, residual_out, out: [T, N] of `type` (BF16, FP16, FP32), row
+ * strides in elements, >= N; weight [N] of `type`; codes [T, N] and scales
+ * [T, ceil(N/128)] contiguous.  residual, residual_out, out may each be NULL,
+ * codes and scales both; out or codes must be given.  residual_out may be x
+ * or residual itself.  N <= 32768.  Errors: INVALID_ARG, UNSUPPORTED, CUDA.
+ */
+int dsa_add_rms_norm(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                     const void* weight, int type, int T, int N, float eps, void* residual_out,
+                     int64_t residual_out_stride, void* out, int64_t out_stride, uint8_t* codes,
+                     float* scales, dsa_stream_t stream);
 
 /*
  * Number of kernel launches the last successful call of each entry point on
