@@ -72,6 +72,72 @@ void set_cache(P* p, const dsa_kv_cache* c) {
   p->num_pages = c->num_pages;
 }
 
+// ---------------------------------------------------------------- attention
+int attention_grid() {
+  const int n = sm_count();
+  return n <= 0 || n > dsa::kAttnMaxGrid ? dsa::kAttnMaxGrid : n;
+}
+
+// Workspace: arrival counters of split units, then their parts' maxima and
+// sums and their outputs (two slots of 256 rows for every CTA).
+constexpr size_t kAttnCounterBytes = 1024;
+static_assert(kAttnCounterBytes >= dsa::kAttnMaxGrid * 4, "counters");
+size_t attention_part_rows() { return (size_t)attention_grid() * 2 * 256; }
+
+// A map over up to four dimensions, innermost first; strides in bytes (of
+// dimensions 1 on).  A dimension of one element may have any stride: it gets
+// one that the encoder takes.
+int make_map(CUtensorMap* m, const char* what, CUtensorMapDataType type, int size, const void* base, int rank,
+             const int64_t* dims, const int64_t* strides, const int* box, bool swizzle) {
+  auto fn = encode_fn();
+  if (!fn) return fail(DSA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  cuuint64_t d[4], st[3];
+  cuuint32_t b[4], e[4];
+  for (int i = 0; i < rank; ++i) {
+    d[i] = (cuuint64_t)dims[i];
+    b[i] = (cuuint32_t)box[i];
+    e[i] = 1;
+    if (i > 0) {
+      if (dims[i] > 1 && strides[i - 1] <= 0)
+        return fail(DSA_ERR_INVALID_ARG, "%s: a stride of 0 over more than one element", what);
+      st[i - 1] = dims[i] > 1 ? (cuuint64_t)strides[i - 1] : (cuuint64_t)((dims[0] * size + 15) / 16 * 16);
+    }
+  }
+  const CUresult r = fn(m, type, (cuuint32_t)rank, const_cast<void*>(base), d, st, b, e, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(DSA_ERR_CUDA, "cuTensorMapEncodeTiled(%s) failed (%d)", what, (int)r);
+  return DSA_OK;
+}
+
+template <int DP, bool BF16>
+int launch_attention(const dsa::AttnParams& p, int grid, cudaStream_t st) {
+  using C = dsa::AttnCfg<DP>;
+  static std::once_flag once;
+  static cudaError_t attr_err = cudaSuccess;
+  std::call_once(once, [] {
+    attr_err = cudaFuncSetAttribute(dsa::paged_attention_kernel<DP, BF16>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  });
+  if (attr_err != cudaSuccess)
+    return fail(DSA_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(attr_err));
+  const CUtensorMapDataType type = BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  CUtensorMap tq, tk, tv;
+  const int64_t qd[3] = {p.D, p.Hq, p.T}, qs[2] = {p.q_head * 2, p.q_token * 2};
+  const int qb[3] = {64, p.group, p.tile_tokens};
+  if (const int rc = make_map(&tq, "q", type, 2, p.q, 3, qd, qs, qb, true)) return rc;
+  const int64_t kd[4] = {p.D, p.Hkv, DSA_PAGE_TOKENS, p.num_pages};
+  const int kb[4] = {64, 1, DSA_PAGE_TOKENS, 1};
+  const char* const names[2] = {"k_cache", "v_cache"};
+  for (int i = 0; i < 2; ++i) {
+    const int64_t ks[3] = {p.head_stride[i], p.token_stride[i], p.page_stride[i]};
+    if (const int rc = make_map(i ? &tv : &tk, names[i], type, 2, p.cache[i], 4, kd, ks, kb, true)) return rc;
+  }
+  dsa::paged_attention_kernel<DP, BF16><<<grid, dsa::kAttnThreads, C::kSmem, st>>>(tq, tk, tv, p);
+  set_last_launches(1);
+  return check_launch("paged_attention_kernel");
+}
+
 template <typename T, bool VEC>
 void launch_norm(const dsa::NormParams& p, cudaStream_t st) {
   const int n8 = (p.N + 7) / 8;
@@ -163,7 +229,9 @@ int dsa_kv_write(const void* k, int64_t k_token_stride, int64_t k_head_stride, c
   return check_launch("kv_write_kernel");
 }
 
-size_t dsa_paged_attention_workspace_bytes(void) { return 256; }
+size_t dsa_paged_attention_workspace_bytes(void) {
+  return kAttnCounterBytes + attention_part_rows() * (128 * sizeof(float) + sizeof(float2));
+}
 
 int dsa_paged_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride, int type, int T,
                         int Hq, const dsa_kv_cache* cache, const int32_t* query_start_loc,
@@ -217,17 +285,26 @@ int dsa_paged_attention(const void* q, int64_t q_token_stride, int64_t q_head_st
   p.sinks = num_sinks;
   p.scale_log2 = (float)((double)softmax_scale * 1.4426950408889634);
   p.status = dev_status;
-  const int64_t grid = ((int64_t)T * Hq + 7) / 8;
-  if (grid > INT32_MAX) return fail(DSA_ERR_INVALID_ARG, "too many rows");
+  p.group = Hq / p.Hkv;
+  p.tile_tokens = 128 / p.group;
+  p.sink_tiles = num_sinks / dsa::kAttnTile + (num_sinks % dsa::kAttnTile != 0);
+  if (sm_count() <= 0) return fail(DSA_ERR_CUDA, "no CUDA device");
+  const int grid = attention_grid();
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  p.counter = reinterpret_cast<uint32_t*>(ws);
+  p.part = reinterpret_cast<float*>(ws + kAttnCounterBytes);
+  p.part_ml = reinterpret_cast<float2*>(p.part + attention_part_rows() * 128);
   const cudaStream_t st = (cudaStream_t)stream;
-  if (cache->type == DSA_TYPE_E4M3)
-    dsa::paged_attention_simple_kernel<true, true><<<(unsigned)grid, 256, 0, st>>>(p);
-  else if (type == DSA_TYPE_BF16)
-    dsa::paged_attention_simple_kernel<true, false><<<(unsigned)grid, 256, 0, st>>>(p);
-  else
-    dsa::paged_attention_simple_kernel<false, false><<<(unsigned)grid, 256, 0, st>>>(p);
-  set_last_launches(1);
-  return check_launch("paged_attention_simple_kernel");
+  if (cache->type == DSA_TYPE_E4M3) {
+    const int64_t blocks = ((int64_t)T * Hq + 7) / 8;
+    if (blocks > INT32_MAX) return fail(DSA_ERR_INVALID_ARG, "too many rows");
+    dsa::paged_attention_simple_kernel<true, true><<<(unsigned)blocks, 256, 0, st>>>(p);
+    set_last_launches(1);
+    return check_launch("paged_attention_simple_kernel");
+  }
+  if (type == DSA_TYPE_BF16)
+    return p.D > 64 ? launch_attention<128, true>(p, grid, st) : launch_attention<64, true>(p, grid, st);
+  return p.D > 64 ? launch_attention<128, false>(p, grid, st) : launch_attention<64, false>(p, grid, st);
 }
 
 int dsa_add_rms_norm(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
