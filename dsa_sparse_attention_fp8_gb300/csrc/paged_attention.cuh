@@ -10,7 +10,9 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
+#include <cstddef>
 #include <cstdint>
+#include <type_traits>
 
 #include "common.cuh"
 #include "ptx.cuh"
@@ -116,11 +118,15 @@ __global__ void __launch_bounds__(256) paged_attention_simple_kernel(const __gri
 // The tensor-core kernel
 // ---------------------------------------------------------------------------
 constexpr int kAttnTile = 128;        // keys per tile (two pages)
-constexpr int kAttnThreads = 384;     // 8 softmax warps, TMA, MMA, 2 housekeeping
-constexpr int kAttnTmaWarp = 8;
-constexpr int kAttnMmaWarp = 9;
+constexpr int kAttnSplit = 2;         // softmax warps that share 32 rows, each with a part of the keys
+constexpr int kAttnSoftmaxWarps = 8 * kAttnSplit;
+constexpr int kAttnTmaWarp = kAttnSoftmaxWarps;
+constexpr int kAttnMmaWarp = kAttnSoftmaxWarps + 1;   // and the next: one for each stream
+constexpr int kAttnWalkWarp = kAttnSoftmaxWarps + 3;
+constexpr int kAttnThreads = (kAttnSoftmaxWarps + 4) * 32;
 constexpr int kAttnMaxGrid = 160;
 constexpr float kAttnRescaleLog2 = 8.0f;  // rescale the output when the max grows by more than 2^8
+constexpr int64_t kAttnMaxShare = 1 << 23;  // cost of a CTA's work, in 32 bits
 constexpr int kAttnUnitCharge = 1;    // a unit's set-up, in key tiles
 
 // A unit of work: up to two query tiles (2 * tile_tokens tokens) of one
@@ -165,33 +171,32 @@ __device__ __forceinline__ int attn_units(const AttnParams& p, int q) {
 }
 
 // Where a CTA is in the work: all units' costs laid end to end, requests
-// outermost, then key heads, then units; the CTA owns [x0, x1).
+// outermost, then key heads, then units, and cut into equal shares.  Places
+// are relative to the CTA's share [0, len).
 struct AttnWalk {
   int r, head, u, nu;
   int row0, q, seq;
-  int64_t s;     // cost before this unit
-  int64_t x0, x1, share;
+  int s;         // cost before this unit (negative: it began in an earlier share)
+  int len, share;
   AttnUnit unit;
   int j0, j1;    // this CTA's key tiles of the unit
 
   __device__ __forceinline__ void enter(const AttnParams& p) {
     unit = attn_unit(p, q, seq, u);
     // tile j lies at s + (charge + j) * weight
-    const int64_t w = unit.weight;
-    j0 = (int)max((int64_t)0, (x0 - s + w - 1) / w - kAttnUnitCharge);
-    if (x0 <= s) j0 = 0;
-    j1 = (int)min((int64_t)unit.n, (x1 - s + w - 1) / w - kAttnUnitCharge);
+    j0 = s >= 0 ? 0 : max(0, (unit.weight - 1 - s) / unit.weight - kAttnUnitCharge);
+    j1 = min(unit.n, (len - s + unit.weight - 1) / unit.weight - kAttnUnitCharge);
   }
-  __device__ __forceinline__ bool inside(const AttnParams& p) const { return r < p.R && s < x1; }
+  __device__ __forceinline__ bool inside() const { return s < len; }
   __device__ __forceinline__ void next(const AttnParams& p) {
-    s += (int64_t)(unit.n + kAttnUnitCharge) * unit.weight;
-    if (s >= x1) return;
+    s += (unit.n + kAttnUnitCharge) * unit.weight;
+    if (s >= len) return;
     if (++u == nu) {
       u = 0;
       if (++head == p.Hkv) {
         head = 0;
         do {
-          if (++r >= p.R) return;
+          ++r;  // there is one with rows: the share goes on
           attn_request(p, r, &row0, &q, &seq);
         } while (q == 0);
         nu = attn_units(p, q);
@@ -200,11 +205,9 @@ struct AttnWalk {
     enter(p);
   }
   // The CTAs that own the unit's first and last key tile.
-  __device__ __forceinline__ int first_cta() const {
-    return (int)((s + (int64_t)kAttnUnitCharge * unit.weight) / share);
-  }
-  __device__ __forceinline__ int last_cta() const {
-    return (int)((s + (int64_t)(kAttnUnitCharge + unit.n - 1) * unit.weight) / share);
+  __device__ __forceinline__ int cta_of(int j) const {
+    const int at = s + (kAttnUnitCharge + j) * unit.weight;
+    return (int)blockIdx.x + (at >= 0 ? at / share : -((share - 1 - at) / share));
   }
 };
 
@@ -216,17 +219,46 @@ struct AttnCfg {
   static constexpr int kSmem = (2 + kStages) * kTileBytes + 3072;
 };
 
+// One unit's part of a CTA's share, as the walking warp hands it to the others.
+struct AttnItem {
+  int n;          // key tiles (0: the end)
+  int ntok;       // tokens of the unit
+  int two;        // two query tiles (a stream each), or one (shared)
+  int p0;         // position of the first token
+  int lo[2], hi[2];  // positions of each stream's first and last token
+  int from[2], step; // a stream's first key tile of the part, and how many on its next is
+  int ns, skip;   // key tile i of the part is i + j0 while that is below ns, else i + j0 + skip
+  int j0;
+  int token, head, r, seq;
+  int c0, c1;     // the CTAs of the unit's first and last key tile
+  int slot;       // where this CTA's part goes, if the unit is split: 1 if it begins here
+  int begins;     // whether it begins in c0's share
+  int q0;         // query tiles loaded before
+};
+constexpr int kAttnItems = 4;
+
 struct AttnSmem {
-  uint64_t q_full[2], q_empty[2], kv_full[8], kv_empty[8], s_full[2], p_full[2], o_full[2], drain;
+  uint64_t q_full[2], q_empty[2], kv_full[8], kv_empty[8], s_full[2], p_full[2], o_full[2], turn[2];
+  uint64_t item_full[kAttnItems], item_empty[kAttnItems], drain[2];
+  AttnItem item[kAttnItems];
   uint32_t tmem;
   int32_t abort, last;
-  int32_t begin_r, begin_head, begin_u;
-  int64_t begin_s, total;
+  int32_t begin_r, begin_head, begin_u, begin_s;
   int64_t warp_cost[kAttnThreads / 32];
   uint8_t bad[16];       // per key tile of the ring: bit i = page i is bad
-  float2 ml[2][128];     // the two streams' maxima and sums
+  float swap[2][2][128]; // a value of each row, between the warps that share it: [stream][half]
 };
 static_assert(sizeof(AttnSmem) <= 3072, "shared memory");
+
+// The order in which an item's K and V tiles are loaded, as places in the
+// ring: K0 V0 K1 V1 ... where the streams share the tiles, and K0 K1 V0 K2 V1
+// K3 ... where they alternate (each stream's next K ahead of its V).
+__device__ __forceinline__ uint32_t attn_k_place(int step, int j) {
+  return step == 1 || j == 0 ? 2 * j : 2 * j - 1;
+}
+__device__ __forceinline__ uint32_t attn_v_place(int step, int j, int n) {
+  return step == 1 || j + 1 == n ? 2 * j + 1 : 2 * j + 2;
+}
 
 // tensor-memory columns of stream x
 __device__ __forceinline__ uint32_t attn_col_s(int x) { return (uint32_t)x * 128; }
@@ -245,8 +277,7 @@ __device__ __forceinline__ uint32_t attn_pack(float lo, float hi) {
 // Finds where this CTA's share of the work begins: every CTA sums the
 // requests' costs itself (a thread per request, a warp together for requests
 // of several units).  Called by all threads; the result is in shared memory.
-__device__ __forceinline__ void attn_locate(const AttnParams& p, AttnSmem* sm, int64_t* x0, int64_t* x1,
-                                            int64_t* share) {
+__device__ __forceinline__ void attn_locate(const AttnParams& p, AttnSmem* sm, int* len, int* share_out) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int per = (p.R + kAttnThreads - 1) / kAttnThreads;
   const int r0 = threadIdx.x * per;
@@ -298,16 +329,21 @@ __device__ __forceinline__ void attn_locate(const AttnParams& p, AttnSmem* sm, i
     total += sm->warp_cost[w];
   }
   // shares of at least 4 single tiles: a split costs a unit's set-up and a merge
-  *share = max((total + gridDim.x - 1) / (int64_t)gridDim.x, (int64_t)4);
-  *x0 = (int64_t)blockIdx.x * *share;
-  *x1 = min(*x0 + *share, total);
-  const bool mine = *x0 < total && before <= *x0 && *x0 < before + sum;
+  int64_t share = max((total + gridDim.x - 1) / (int64_t)gridDim.x, (int64_t)4);
+  if (share > kAttnMaxShare) {  // hours of work: no real batch
+    if (threadIdx.x == 0 && blockIdx.x == 0) raise_status(p.status, kStatusBadMetadata);
+    share = kAttnMaxShare;
+  }
+  const int64_t x0 = (int64_t)blockIdx.x * share;
+  *share_out = (int)share;
+  *len = (int)max(min(share, total - x0), (int64_t)0);
+  const bool mine = x0 < total && before <= x0 && x0 < before + sum;
   if (__any_sync(0xffffffffu, mine)) {
     int found = -1;
     int64_t at = before, cost_found = 0;
     for (int i = 0; i < per; ++i) {
       const int64_t c = per == 1 ? c_last : cost(r0 + i, &bad) * p.Hkv;
-      if (mine && found < 0 && *x0 < at + c) {
+      if (mine && found < 0 && x0 < at + c) {
         found = r0 + i;
         cost_found = c;
       }
@@ -317,7 +353,7 @@ __device__ __forceinline__ void attn_locate(const AttnParams& p, AttnSmem* sm, i
     const int r = __shfl_sync(0xffffffffu, found, src);
     const int64_t begin = __shfl_sync(0xffffffffu, at, src);
     const int64_t per_head = __shfl_sync(0xffffffffu, cost_found, src) / p.Hkv;
-    const int head = (int)((*x0 - begin) / per_head);
+    const int head = (int)((x0 - begin) / per_head);
     int64_t s = begin + head * per_head;
     int row0, q, seq;
     attn_request(p, r, &row0, &q, &seq);
@@ -334,13 +370,13 @@ __device__ __forceinline__ void attn_locate(const AttnParams& p, AttnSmem* sm, i
         const int64_t y = __shfl_up_sync(0xffffffffu, end, o);
         if (lane >= o) end += y;
       }
-      const uint32_t past = __ballot_sync(0xffffffffu, c > 0 && *x0 < s + end);
+      const uint32_t past = __ballot_sync(0xffffffffu, c > 0 && x0 < s + end);
       if (past) {
         if (lane == __ffs(past) - 1) {
           sm->begin_r = r;
           sm->begin_head = head;
           sm->begin_u = u0 + lane;
-          sm->begin_s = s + end - c;
+          sm->begin_s = (int)(s + end - c - x0);
         }
         break;
       }
@@ -349,18 +385,92 @@ __device__ __forceinline__ void attn_locate(const AttnParams& p, AttnSmem* sm, i
   }
 }
 
+// Which of 32 keys a row sees, as bits: key i of them lies i - `back` tokens
+// after the row's own, and `first` is the first one's position.
+__device__ __forceinline__ uint32_t attn_seen(const AttnParams& p, int back, int first, bool gone) {
+  auto below = [](int n) -> uint32_t { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; };  // bits [0, n)
+  uint32_t seen = p.window > 0 ? ~below(back - p.window + 1) | below(p.sinks - first) : 0xFFFFFFFFu;
+  if (back < 32) seen &= below(back + 1);
+  return gone ? 0u : seen;
+}
+
+// Joins the parts of a split unit, in CTA order: a warp per row, a lane per
+// DP / 32 elements.  Part k lies in slot 1 of the CTA in whose share the unit
+// begins, in slot 0 of the others.
+template <int DP, bool BF16>
+__device__ __noinline__ void attn_join(const AttnParams& p, const AttnItem& item, int warp, int lane) {
+  const int parts = item.c1 - item.c0 + 1;
+  const int all = item.ntok * p.group;            // rows of both tiles
+  const int rows0 = p.tile_tokens * p.group;      // rows of the first tile
+  for (int i = warp; i < all; i += kAttnSoftmaxWarps) {
+    const int pr = item.two && i >= rows0 ? 128 + i - rows0 : i;
+    auto at = [&](int k) -> int64_t {
+      return ((int64_t)(item.c0 + k) * 2 + (k == 0 && item.begins ? 1 : 0)) * 256 + pr;
+    };
+    float top = -INFINITY;
+    for (int k = lane; k < parts; k += 32) top = fmaxf(top, __ldcg(p.part_ml + at(k)).x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    float sum = 0.f, acc[DP / 32];
+#pragma unroll
+    for (int c = 0; c < DP / 32; ++c) acc[c] = 0.f;
+    for (int k0 = 0; k0 < parts; k0 += 32) {
+      float f = 0.f;
+      if (k0 + lane < parts) {
+        const float2 v = __ldcg(p.part_ml + at(k0 + lane));
+        f = v.x == -INFINITY ? 0.f : ex2(v.x - top);
+        sum += v.y * f;
+      }
+      const int most = min(32, parts - k0);
+#pragma unroll 4
+      for (int k = 0; k < most; ++k) {
+        const float fk = __shfl_sync(0xffffffffu, f, k);
+        const float* src = p.part + at(k0 + k) * DP + lane * (DP / 32);
+        if (lane * (DP / 32) < p.D) {
+          if (DP == 128) {
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
+            acc[0] += v.x * fk;
+            acc[1] += v.y * fk;
+            acc[2 % (DP / 32)] += v.z * fk;
+            acc[3 % (DP / 32)] += v.w * fk;
+          } else {
+            const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
+            acc[0] += v.x * fk;
+            acc[1] += v.y * fk;
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const float r = sum > 0.f ? 1.0f / sum : 0.f;
+    const int64_t t = item.token + i / p.group;
+    const int h = item.head * p.group + i % p.group;
+    uint16_t* orow = p.out + t * p.out_token + (int64_t)h * p.out_head + lane * (DP / 32);
+    if (lane * (DP / 32) < p.D) {
+#pragma unroll
+      for (int c = 0; c < DP / 32; c += 2)
+        *reinterpret_cast<uint32_t*>(orow + c) = attn_pack<BF16>(acc[c] * r, acc[c + 1] * r);
+    }
+    if (lane == 0 && p.lse)
+      p.lse[t * p.Hq + h] = sum > 0.f ? (top + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+  }
+}
+
 // Two streams of 128 query rows run side by side, each with its own score and
 // output tiles in tensor memory (S, which its probabilities overwrite, and O:
-// 2 x 256 columns, all of it) and its own four softmax warps, so that the
-// tensor core works on one stream while the other's softmax runs.  A unit of
-// two query tiles gives each stream one tile and both read the same K and V
+// 2 x 256 columns, all of it) and its own softmax warps, so that the tensor
+// core works on one stream while the other's softmax runs.  A unit of two
+// query tiles gives each stream one tile and both read the same K and V
 // tiles.  A unit of one query tile (decode; the end of a prompt) gives both
 // streams that tile and alternate key tiles: the two halves are joined at the
 // end, in tensor memory.
-//   warps 0-3, 4-7   softmax of stream 0, 1: thread = row;
-//   warp 8           TMA: query tiles, K and V tiles through the block table;
-//   warp 9           MMA: S = Q K^T, O += P V (P from tensor memory);
-//   warps 10-11      rows that belong to no valid request: zeros.
+//   warps 0-15  softmax, eight for each stream: a thread has 64 keys of a row;
+//   then        TMA: query tiles, K and V tiles through the block table, and
+//               zeros in the rows that belong to no valid request;
+//               two MMA, one for each stream: S = Q K^T, O += P V (P from
+//               tensor memory);
+//               walking: the CTA's share of the work, unit by unit.
 template <int DP, bool BF16>
 __global__ void __launch_bounds__(kAttnThreads, 1)
     paged_attention_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
@@ -375,16 +485,22 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&sm->q_full[i]), 1);
-      mbar_init(smem_u32(&sm->q_empty[i]), 1);
+      mbar_init(smem_u32(&sm->q_empty[i]), 2);  // an arrival from each stream
       mbar_init(smem_u32(&sm->s_full[i]), 1);
-      mbar_init(smem_u32(&sm->p_full[i]), 4);
+      mbar_init(smem_u32(&sm->p_full[i]), 4 * kAttnSplit);
       mbar_init(smem_u32(&sm->o_full[i]), 1);
+      mbar_init(smem_u32(&sm->turn[i]), 1);
     }
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(smem_u32(&sm->kv_full[i]), 1);
-      mbar_init(smem_u32(&sm->kv_empty[i]), 1);
+      mbar_init(smem_u32(&sm->kv_empty[i]), 2);
     }
-    mbar_init(smem_u32(&sm->drain), 1);
+    for (int i = 0; i < kAttnItems; ++i) {
+      mbar_init(smem_u32(&sm->item_full[i]), 1);
+      mbar_init(smem_u32(&sm->item_empty[i]), kAttnSoftmaxWarps + 3);
+    }
+    mbar_init(smem_u32(&sm->drain[0]), 1);
+    mbar_init(smem_u32(&sm->drain[1]), 1);
     sm->abort = 0;
     fence_barrier_init();
   }
@@ -397,15 +513,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     tma_prefetch_desc(&tk);
     tma_prefetch_desc(&tv);
   }
-  AttnWalk w;
-  attn_locate(p, sm, &w.x0, &w.x1, &w.share);
+  int len, share;
+  attn_locate(p, sm, &len, &share);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm->tmem;
   volatile int* abort_flag = &sm->abort;
   bool ok = true;
-  // warp-uniform waits; after one gave up the role walks on without working
+  // warp-uniform waits; after one gave up the role ends (the softmax warps,
+  // which meet at barriers, go on to the items' end without waiting)
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (ok) {
       ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, abort_flag));
@@ -413,156 +530,182 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     }
     return ok;
   };
-  if (w.x0 < w.x1) {
-    w.r = sm->begin_r;
-    w.head = sm->begin_head;
-    w.u = sm->begin_u;
-    w.s = sm->begin_s;
-    attn_request(p, w.r, &w.row0, &w.q, &w.seq);
-    w.nu = attn_units(p, w.q);
-    w.enter(p);
-  } else {
-    w.r = p.R;
-  }
+  // a field of the item at `at`: read where it is needed, not kept in registers
+#define ATTN_AT(base, field) ((int)lds_u32((base) + (uint32_t)offsetof(AttnItem, field)))
+#define ATTN_ITEM(field) ATTN_AT(at, field)
 
-  if (warp < 8) {
+  if (warp < kAttnSoftmaxWarps) {
     // ================================================================ softmax
-    regs_grow<216>();
-    const int x = warp >> 2;                  // stream
-    const int row = threadIdx.x & 127;        // row of its tile
-    const int wg = warp & 3;
-    const uint32_t lanes = tmem + ((uint32_t)(wg * 32) << 16);
-    uint32_t n_s = 0, n_o[2] = {0, 0}, tile0 = 0;  // phases so far; key tiles before this unit
-    for (; w.inside(p); w.next(p)) {
-      const int n = w.j1 - w.j0;
-      if (n <= 0) continue;
-      const bool two = w.unit.ntok > p.tile_tokens;
-      const int tok0 = two ? x * p.tile_tokens : 0;  // this stream's first token in the unit
-      const int ntok = two ? (x ? w.unit.ntok - p.tile_tokens : p.tile_tokens) : w.unit.ntok;
-      const int rows = ntok * p.group;
-      const bool live = wg * 32 < rows;       // some row of this warp is real
-      const int tok = min(row / p.group, ntok - 1);
-      const int pos = w.unit.p0 + tok0 + tok;
-      const int pos_lo = w.unit.p0 + tok0, pos_hi = pos_lo + ntok - 1;
+    constexpr int kKeys = 128 / kAttnSplit;             // keys of a tile to a thread
+    const int x = warp / (4 * kAttnSplit), half = (warp >> 2) % kAttnSplit;  // stream; part of the keys
+    const uint32_t pair = 2 + x * 4 + (warp & 3);       // named barrier of the warps that share the rows
+    const int row = (warp & 3) * 32 + lane;             // row of its tile
+    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    uint32_t n_s = 0, n_o = 0, tile0 = 0;  // score and output tiles so far; key tiles before this item
+    for (uint32_t it = 0;; ++it) {
+      const uint32_t at = smem_u32(&sm->item[it % kAttnItems]);
+      if (!mbar_wait(smem_u32(&sm->item_full[it % kAttnItems]), (it / kAttnItems) & 1, nullptr)) break;
+      const int n = ATTN_ITEM(n);
+      if (n == 0) break;
       float m = -INFINITY, l = 0.f;
-      int done = 0;
-      for (int j = two ? 0 : x; j < n; j += two ? 1 : 2) {
-        wait(&sm->s_full[x], n_s & 1);
-        ++n_s;
-        if (live && ok) {
-          tc_fence_after();
-          uint32_t s[128];
+      {
+        const uint32_t mine = at + 4 * x;
+        const int lo = ATTN_AT(mine, lo), hi = ATTN_AT(mine, hi), step = ATTN_ITEM(step);
+        const bool live = (warp & 3) * 32 < (hi - lo + 1) * p.group;  // some row of this warp is real
+        const int pos = min(lo + row / p.group, hi);
+        const int ns = ATTN_ITEM(ns), skip = ATTN_ITEM(skip), j0 = ATTN_ITEM(j0);
+        for (int j = ATTN_AT(mine, from); j < n; j += step) {
+          const int s0 = (j0 + j + (j0 + j < ns ? 0 : skip)) * kAttnTile;
+          const bool inner = s0 + kAttnTile - 1 <= lo && (p.window == 0 || s0 > hi - p.window || s0 + kAttnTile - 1 < p.sinks);
+          wait(&sm->s_full[x], n_s & 1);
+          ++n_s;
+          if (live) {  // (also after a wait gave up: the warps of a pair meet at barriers)
+            tc_fence_after();
+            const uint32_t base = lanes + attn_col_s(x) + half * kKeys;
+            const uint32_t bad = sm->bad[(tile0 + j) & 15];
+            // Loops over 32 keys that are not unrolled: code that is run once
+            // a tile costs more in instruction fetches than in its work (all
+            // of a row unrolled: 1,500 cycles a tile, against 540 for its
+            // arithmetic in a loop).
+            if (!(inner && bad == 0)) {
+              // -inf over the scores that the row does not see
+#pragma unroll 1
+              for (int c = 0; c < kKeys; c += 32) {
+                uint32_t v[32];
+                tmem_ld<32>(base + c, v);
+                const int k0 = half * kKeys + c;
+                const uint32_t seen = attn_seen(p, pos - s0 - k0, s0 + k0, bad >> (k0 / 64) & 1u);
+                tmem_ld_wait32(v);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld<32>(lanes + attn_col_s(x) + 32 * c, s + 32 * c);
-          const int jj = w.j0 + j;
-          const int s0 = (jj < w.unit.ns ? jj : w.unit.lo + jj - w.unit.ns) * kAttnTile;
-          const uint32_t bad = sm->bad[(tile0 + j) & 15];
-          const bool whole = s0 + kAttnTile - 1 <= pos_lo && bad == 0 &&
-                             (p.window == 0 || s0 > pos_hi - p.window || s0 + kAttnTile - 1 < p.sinks);
-          tmem_ld_wait();
-          if (!whole) {
-            const int hi = pos - s0, lo = p.window > 0 ? hi - p.window : -1, sk = p.sinks - s0;
-#pragma unroll
-            for (int c = 0; c < 128; ++c) {
-              const bool seen = c <= hi && (c > lo || c < sk) && !((bad >> (c / 64)) & 1u);
-              if (!seen) s[c] = 0xFF800000u;  // -inf
+                for (int i = 0; i < 32; ++i) v[i] = seen & (1u << i) ? v[i] : 0xFF800000u;
+                tmem_st<32>(base + c, v);
+              }
+              tmem_st_wait();
             }
-          }
-          float mx[8];
+            float top = -INFINITY;
+#pragma unroll 1
+            for (int c = 0; c < kKeys; c += 32) {
+              uint32_t v[32];
+              float mx[4];
+              tmem_ld<32>(base + c, v);
+              tmem_ld_wait32(v);
 #pragma unroll
-          for (int c = 0; c < 8; ++c) mx[c] = __uint_as_float(s[c]);
+              for (int i = 0; i < 4; ++i) mx[i] = max3(__uint_as_float(v[i]), __uint_as_float(v[i + 4]), __uint_as_float(v[i + 8]));
 #pragma unroll
-          for (int c = 8; c < 128; ++c) mx[c & 7] = fmaxf(mx[c & 7], __uint_as_float(s[c]));
-          const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
-                                  fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * p.scale_log2;
-          const bool grow = top > m + kAttnRescaleLog2;
-          const float m_new = grow ? top : m;
-          if (__any_sync(0xffffffffu, grow && done > 0)) {
-            // the scores' arrival says that the stream's previous product is done
-            const float a = grow && m != -INFINITY ? ex2(m - m_new) : 1.0f;
-            for (int c = 0; c < DP; c += 32) {
-              uint32_t o[32];
-              tmem_ld<32>(lanes + attn_col_o(x) + c, o);
-              tmem_ld_wait();
+              for (int i = 12; i < 32; i += 8)
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
-              tmem_st<32>(lanes + attn_col_o(x) + c, o);
+                for (int k = 0; k < 4; ++k)
+                  mx[k] = i + 4 + k < 32 ? max3(mx[k], __uint_as_float(v[i + k]), __uint_as_float(v[(i + 4 + k) & 31]))
+                                         : fmaxf(mx[k], __uint_as_float(v[i + k]));
+              top = max3(top, max3(mx[0], mx[1], mx[2]), mx[3]);
             }
-            l *= a;
-          }
-          m = m_new;
-          const float shift = m == -INFINITY ? 0.f : -m;
-          const uint64_t mul = pack2(p.scale_log2, p.scale_log2), sub = pack2(shift, shift);
-          uint64_t sum[4] = {0, 0, 0, 0};
+            top *= p.scale_log2;
+            bool grow = top > m + kAttnRescaleLog2;
+            if (kAttnSplit == 2 ? named_bar_any(pair, 64, grow) : __any_sync(0xffffffffu, grow)) {
+              if (kAttnSplit == 2) {
+                sm->swap[x][half][row] = top;
+                named_bar_sync(pair, 64);
+                top = fmaxf(top, sm->swap[x][half ^ 1][row]);
+                grow = top > m + kAttnRescaleLog2;
+              }
+              if (__any_sync(0xffffffffu, m != -INFINITY)) {  // (else there is no output yet, or zeros)
+                // the scores' arrival says that the stream's previous product is done
+                const float a = grow && m != -INFINITY ? ex2(m - top) : 1.0f;
+                constexpr int kCols = DP / kAttnSplit;
+#pragma unroll 1
+                for (int c = half * kCols; c < (half + 1) * kCols; c += 32) {
+                  uint32_t o[32];
+                  tmem_ld<32>(lanes + attn_col_o(x) + c, o);
+                  tmem_ld_wait32(o);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t pr[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float2 z = unpack2(fma2(pack2(__uint_as_float(s[32 * c + 2 * i]),
-                                                  __uint_as_float(s[32 * c + 2 * i + 1])), mul, sub));
-              const float e0 = ex2(z.x), e1 = ex2(z.y);
-              sum[i & 3] = add2(sum[i & 3], pack2(e0, e1));
-              pr[i] = attn_pack<BF16>(e0, e1);
+                  for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
+                  tmem_st<32>(lanes + attn_col_o(x) + c, o);
+                }
+                l *= a;
+              }
+              if (grow) m = top;
             }
-            tmem_st<16>(lanes + attn_col_s(x) + 16 * c, pr);
+            const float shift = m == -INFINITY ? 0.f : -m;
+            const uint64_t mul = pack2(p.scale_log2, p.scale_log2), sub = pack2(shift, shift);
+            uint64_t sum[2] = {0, 0};
+#pragma unroll 1
+            for (int c = 0; c < kKeys; c += 32) {
+              uint32_t v[32], pr[16];
+              tmem_ld<32>(base + c, v);
+              tmem_ld_wait32(v);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const float2 z = unpack2(fma2(pack2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), mul, sub));
+                const float e0 = ex2(z.x), e1 = ex2(z.y);
+                sum[i & 1] = add2(sum[i & 1], pack2(e0, e1));
+                pr[i] = attn_pack<BF16>(e0, e1);
+              }
+              // over scores that this thread has read
+              tmem_st<16>(base + (c & 64) + (c & 32) / 2, pr);
+            }
+            const float2 t = unpack2(add2(sum[0], sum[1]));
+            l += t.x + t.y;
+            tmem_st_wait();
+            tc_fence_before();
           }
-          const float2 t = unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
-          l += t.x + t.y;
-          tmem_st_wait();
-          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sm->p_full[x]));
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sm->p_full[x]));
-        ++done;
       }
       tile0 += n;
 
       // ---- the unit's end: out = O / l, or the part of a split unit
-      const int c0 = w.first_cta(), c1 = w.last_cta();
-      const bool split = c0 != c1;
-      // which streams have an output, and its factors
-      float f0 = 1.f, f1 = 0.f;
-      const bool has0 = two ? x == 0 : true, has1 = two ? x == 1 : n > 1;
-      if (has0 || !two) wait(&sm->o_full[0], n_o[0] & 1);
-      if (has1) wait(&sm->o_full[1], n_o[1] & 1);
-      ++n_o[0];
-      if (two || n > 1) ++n_o[1];
-      tc_fence_after();
-      int col0 = 0, cols = DP;
-      if (!two) {
-        // both streams' warps share the rows: each takes half of the columns
-        sm->ml[x][row] = make_float2(m, l);
-        named_bar_sync(1, 256);
-        const float2 a = sm->ml[0][row], b = sm->ml[1][row];
-        m = fmaxf(a.x, b.x);
-        f0 = a.x == -INFINITY ? 0.f : ex2(a.x - m);
-        f1 = b.x == -INFINITY ? 0.f : ex2(b.x - m);
-        l = a.y * f0 + b.y * f1;
-        col0 = x * (DP / 2);
-        cols = DP / 2;
-      } else {
-        f0 = f1 = 1.f;
+      const bool two = ATTN_ITEM(two) != 0;
+      const int first = two && x ? p.tile_tokens : 0;  // this stream's first token in the unit
+      const int rows = (two ? min(p.tile_tokens, ATTN_ITEM(ntok) - first) : ATTN_ITEM(ntok)) * p.group;
+      const bool live = (warp & 3) * 32 < rows;
+      const bool split = ATTN_ITEM(c0) != ATTN_ITEM(c1);
+      if (two || x < n) {  // this stream had a tile
+        wait(&sm->o_full[x], n_o & 1);
+        ++n_o;
       }
-      const bool row_ok = row < rows;
-      const int token = w.row0 + w.u * 2 * p.tile_tokens + tok0 + tok;
-      const int head = w.head * p.group + row % p.group;
-      const float inv = split ? 1.0f : (l > 0.f ? 1.0f / l : 0.f);
-      const int slot = (int)blockIdx.x * 2 + (w.s >= w.x0 ? 1 : 0);
-      const int prow = two ? x * 128 + row : row;
+      tc_fence_after();
+      // which streams have an output, and its factors; where they share the
+      // rows, all of their warps split the columns
+      float f0 = 1.f, f1 = 1.f;
+      const bool has0 = two ? x == 0 : true, has1 = two ? x == 1 : n > 1;
+      const int cols = two ? DP / kAttnSplit : DP / (2 * kAttnSplit);
+      const int col0 = (two ? half : x * kAttnSplit + half) * cols;
+      if (two) {
+        if (live && kAttnSplit == 2) {
+          sm->swap[x][half][row] = l;
+          named_bar_sync(pair, 64);
+          l += sm->swap[x][half ^ 1][row];
+        }
+      } else {
+        tc_fence_before();
+        sm->swap[x][0][row] = m;  // (both halves have the same)
+        named_bar_sync(1, kAttnSoftmaxWarps * 32);
+        const float a = sm->swap[0][0][row], b = sm->swap[1][0][row], mine = m;
+        m = fmaxf(a, b);
+        f0 = a == -INFINITY ? 0.f : ex2(a - m);
+        f1 = b == -INFINITY ? 0.f : ex2(b - m);
+        named_bar_sync(1, kAttnSoftmaxWarps * 32);
+        sm->swap[x][half][row] = mine == -INFINITY ? 0.f : l * (x ? f1 : f0);
+        named_bar_sync(1, kAttnSoftmaxWarps * 32);
+        l = sm->swap[0][0][row] + sm->swap[1][0][row];
+        if (kAttnSplit == 2) l += sm->swap[0][1][row] + sm->swap[1][1][row];
+        tc_fence_after();  // the other stream's output is there: its warps came here after it
+      }
       if (live && ok) {
+        const int prow = two ? x * 128 + row : row;
+        const int64_t part = ((int64_t)blockIdx.x * 2 + ATTN_ITEM(slot)) * 256 + prow;
+        const int64_t token = ATTN_ITEM(token) + first + row / p.group;
+        const int head = ATTN_ITEM(head) * p.group + row % p.group;
+        const float inv = split ? 1.0f : (l > 0.f ? 1.0f / l : 0.f);
         f0 *= inv;
         f1 *= inv;
-        uint16_t* orow = p.out + (int64_t)token * p.out_token + (int64_t)head * p.out_head;
-        float* srow = p.part + ((int64_t)slot * 256 + prow) * DP;
-#pragma unroll
-        for (int c = 0; c < DP; c += 16) {
-          if (c >= cols) break;
-          const int at = col0 + c;
+#pragma unroll 1
+        for (int c = col0; c < col0 + cols; c += 16) {
           uint32_t a[16], b[16];
           float o[16];
-          if (has0) tmem_ld<16>(lanes + attn_col_o(0) + at, a);
-          if (has1) tmem_ld<16>(lanes + attn_col_o(1) + at, b);
+          if (has0) tmem_ld<16>(lanes + attn_col_o(0) + c, a);
+          if (has1) tmem_ld<16>(lanes + attn_col_o(1) + c, b);
           tmem_ld_wait();
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
@@ -570,107 +713,65 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             if (has0) o[i] = __uint_as_float(a[i]) * f0;
             if (has1) o[i] += __uint_as_float(b[i]) * f1;
           }
-          if (row_ok && at < p.D) {
+          if (row < rows && c < p.D) {
             if (split) {
+              float* dst = p.part + part * DP + c;
 #pragma unroll
               for (int i = 0; i < 16; i += 4)
-                __stcg(reinterpret_cast<float4*>(srow + at + i), make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]));
+                __stcg(reinterpret_cast<float4*>(dst + i), make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]));
             } else {
+              uint4* dst = reinterpret_cast<uint4*>(p.out + token * p.out_token + (int64_t)head * p.out_head + c);
               uint32_t v[8];
 #pragma unroll
               for (int i = 0; i < 8; ++i) v[i] = attn_pack<BF16>(o[2 * i], o[2 * i + 1]);
-              reinterpret_cast<uint4*>(orow + at)[0] = make_uint4(v[0], v[1], v[2], v[3]);
-              reinterpret_cast<uint4*>(orow + at)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+              dst[0] = make_uint4(v[0], v[1], v[2], v[3]);
+              dst[1] = make_uint4(v[4], v[5], v[6], v[7]);
             }
           }
         }
-        if (row_ok && col0 == 0) {
+        if (row < rows && col0 == 0) {
           if (split)
-            __stcg(p.part_ml + (int64_t)slot * 256 + prow, make_float2(m, l));
+            __stcg(p.part_ml + part, make_float2(m, l));
           else if (p.lse)
-            p.lse[(int64_t)token * p.Hq + head] =
-                l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+            p.lse[token * p.Hq + head] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
         }
       }
       tc_fence_before();
       if (split) {
         // the unit's last CTA to arrive joins the parts, in CTA order
         __threadfence();
-        named_bar_sync(1, 256);
+        named_bar_sync(1, kAttnSoftmaxWarps * 32);
         if (threadIdx.x == 0) {
-          const uint32_t parts = (uint32_t)(c1 - c0 + 1);
-          const bool last = atomicAdd(p.counter + c0, 1u) == parts - 1;
+          const int c0 = ATTN_ITEM(c0);
+          const bool last = atomicAdd(p.counter + c0, 1u) == (uint32_t)(ATTN_ITEM(c1) - c0);
           if (last) p.counter[c0] = 0;
           sm->last = last;
         }
-        named_bar_sync(1, 256);
-        if (sm->last) {
+        named_bar_sync(1, kAttnSoftmaxWarps * 32);
+        if (*(volatile int*)&sm->last) {
           __threadfence();
-          const int parts = c1 - c0 + 1;
-          const int all = w.unit.ntok * p.group;            // rows of both tiles
-          const int rows0 = p.tile_tokens * p.group;        // rows of the first tile
-          for (int i = warp; i < all; i += 8) {
-            const int pr = two && i >= rows0 ? 128 + i - rows0 : i;
-            // part k lies in slot 1 of the CTA where the unit begins, in slot 0 of the others
-            auto at = [&](int k) -> int64_t {
-              return ((int64_t)(c0 + k) * 2 + (k == 0 && w.s >= (int64_t)c0 * w.share ? 1 : 0)) * 256 + pr;
-            };
-            float top = -INFINITY;
-            for (int k = lane; k < parts; k += 32) top = fmaxf(top, __ldcg(p.part_ml + at(k)).x);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            float sum = 0.f, acc[DP / 32];
-#pragma unroll
-            for (int c = 0; c < DP / 32; ++c) acc[c] = 0.f;
-            for (int k0 = 0; k0 < parts; k0 += 32) {
-              float f = 0.f;
-              if (k0 + lane < parts) {
-                const float2 v = __ldcg(p.part_ml + at(k0 + lane));
-                f = v.x == -INFINITY ? 0.f : ex2(v.x - top);
-                sum += v.y * f;
-              }
-              const int most = min(32, parts - k0);
-#pragma unroll 4
-              for (int k = 0; k < most; ++k) {
-                const float fk = __shfl_sync(0xffffffffu, f, k);
-                const float* src = p.part + at(k0 + k) * DP + lane * (DP / 32);
-                if (lane * (DP / 32) < p.D) {
-                  if (DP == 128) {
-                    const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
-                    acc[0] += v.x * fk;
-                    acc[1] += v.y * fk;
-                    acc[2 % (DP / 32)] += v.z * fk;
-                    acc[3 % (DP / 32)] += v.w * fk;
-                  } else {
-                    const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
-                    acc[0] += v.x * fk;
-                    acc[1] += v.y * fk;
-                  }
-                }
-              }
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            const float r = sum > 0.f ? 1.0f / sum : 0.f;
-            const int64_t t = w.row0 + w.u * 2 * p.tile_tokens + i / p.group;
-            const int h = w.head * p.group + i % p.group;
-            uint16_t* orow = p.out + t * p.out_token + (int64_t)h * p.out_head + lane * (DP / 32);
-            if (lane * (DP / 32) < p.D) {
-#pragma unroll
-              for (int c = 0; c < DP / 32; c += 2)
-                *reinterpret_cast<uint32_t*>(orow + c) = attn_pack<BF16>(acc[c] * r, acc[c + 1] * r);
-            }
-            if (lane == 0 && p.lse)
-              p.lse[t * p.Hq + h] = sum > 0.f ? (top + log2f(sum)) * 0.69314718055994531f : -INFINITY;
-          }
+          attn_join<DP, BF16>(p, *(const AttnItem*)&sm->item[it % kAttnItems], warp, lane);
         }
       }
       // the other stream's warps may still read this one's output
-      if (!two) named_bar_sync(1, 256);
+      if (!two) named_bar_sync(1, kAttnSoftmaxWarps * 32);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sm->item_empty[it % kAttnItems]));
     }
     if (!ok) raise_status(p.status, kStatusTimeout);
   } else {
-    regs_shrink<72>();
+    // every item is taken, also after a wait gave up: the softmax warps go on
+    auto each_item = [&](auto& serve) {
+      for (uint32_t it = 0;; ++it) {
+        const uint32_t at = smem_u32(&sm->item[it % kAttnItems]);
+        if (!mbar_wait(smem_u32(&sm->item_full[it % kAttnItems]), (it / kAttnItems) & 1, nullptr)) break;
+        const int n = ATTN_ITEM(n);
+        if (n == 0) break;
+        if (ok) serve(at, n);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm->item_empty[it % kAttnItems]));
+      }
+    };
     if (warp == kAttnTmaWarp) {
       // ================================================================ TMA
       uint32_t n_kv = 0, n_q = 0, tile0 = 0;
@@ -704,21 +805,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         __syncwarp();
         ++n_q;
       };
-      for (; w.inside(p) && ok; w.next(p)) {
-        const int n = w.j1 - w.j0;
-        if (n <= 0) continue;
-        const bool two = w.unit.ntok > p.tile_tokens;
-        const int token = w.row0 + w.u * 2 * p.tile_tokens;
-        const int p1 = w.unit.p0 + w.unit.ntok - 1;
-        const int first = p.window > 0 ? max(0, w.unit.p0 - p.window + 1) : 0;
-        const int32_t* bt = p.block_table + (int64_t)w.r * p.max_blocks;
-        auto tile_of = [&](int jj) { return jj < w.unit.ns ? jj : w.unit.lo + jj - w.unit.ns; };
+      auto serve = [&](uint32_t at, int n) {
+        const bool two = ATTN_ITEM(two) != 0;
+        const int token = ATTN_ITEM(token), head = ATTN_ITEM(head);
+        const int p0 = ATTN_ITEM(p0), p1 = p0 + ATTN_ITEM(ntok) - 1;
+        const int j0 = ATTN_ITEM(j0), ns = ATTN_ITEM(ns), skip = ATTN_ITEM(skip);
+        const int first = p.window > 0 ? max(0, p0 - p.window + 1) : 0;
+        const int32_t* bt = p.block_table + (int64_t)ATTN_ITEM(r) * p.max_blocks;
         // page ids of 16 tiles, a pair of lanes each: the pool's end (zeros)
         // for pages that no row sees and for bad ones
         auto ids = [&](int j) -> int {
-          const int jj = w.j0 + j + (lane >> 1);
-          if (j + (lane >> 1) >= n) return 0;
-          const int b = tile_of(jj) * 2 + (lane & 1);
+          const int i = j + (lane >> 1), jj = j0 + i;
+          if (i >= n) return 0;
+          const int b = (jj < ns ? jj : jj + skip) * 2 + (lane & 1);
           const int64_t t0 = (int64_t)b * kPageTokens;
           if (t0 > p1 || !(t0 + kPageTokens > first || t0 < p.sinks)) return (int)p.num_pages;
           const int id = __ldg(bt + b);
@@ -729,186 +828,47 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           return id;
         };
         int here = ids(0), ahead = ids(16);
-        int pg[2][2] = {{0, 0}, {0, 0}};  // the newest key tile's pages, and those of the one before
+        int a0 = 0, a1 = 0, b0 = 0, b1 = 0;  // the newest key tile's pages, and those of the one before
         auto load_k = [&](int j) {
           if (j > 0 && (j & 15) == 0) {
             here = ahead;
             ahead = ids(j + 16);
           }
-          pg[1][0] = pg[0][0];
-          pg[1][1] = pg[0][1];
-          int a = __shfl_sync(0xffffffffu, here, (j & 15) * 2);
-          int b = __shfl_sync(0xffffffffu, here, (j & 15) * 2 + 1);
-          if (lane == 0) sm->bad[(tile0 + j) & 15] = (uint8_t)((a < 0 ? 1 : 0) | (b < 0 ? 2 : 0));
+          b0 = a0;
+          b1 = a1;
+          a0 = __shfl_sync(0xffffffffu, here, (j & 15) * 2);
+          a1 = __shfl_sync(0xffffffffu, here, (j & 15) * 2 + 1);
+          if (lane == 0) sm->bad[(tile0 + j) & 15] = (uint8_t)((a0 < 0 ? 1 : 0) | (a1 < 0 ? 2 : 0));
           __syncwarp();
-          pg[0][0] = a < 0 ? (int)p.num_pages : a;
-          pg[0][1] = b < 0 ? (int)p.num_pages : b;
-          load(&tk, w.head, pg[0][0], pg[0][1]);
+          if (a0 < 0) a0 = (int)p.num_pages;
+          if (a1 < 0) a1 = (int)p.num_pages;
+          load(&tk, head, a0, a1);
         };
         load_k(0);
-        load_q(w.head, token);
+        load_q(head, token);
         if (two) {
-          load_q(w.head, token + p.tile_tokens);
-          load(&tv, w.head, pg[0][0], pg[0][1]);
+          load_q(head, token + p.tile_tokens);
+          load(&tv, head, a0, a1);
           for (int j = 1; j < n && ok; ++j) {
             load_k(j);
-            load(&tv, w.head, pg[0][0], pg[0][1]);
+            load(&tv, head, a0, a1);
           }
         } else {
           if (n > 1) load_k(1);
           for (int j = 0; j < n && ok; ++j) {
-            const int i = j + 1 < n ? 1 : 0;
-            load(&tv, w.head, pg[i][0], pg[i][1]);
+            if (j + 1 < n)
+              load(&tv, head, b0, b1);
+            else
+              load(&tv, head, a0, a1);
             if (j + 2 < n) load_k(j + 2);
           }
         }
         tile0 += n;
-      }
-      // every copy has landed before the CTA leaves
-      for (uint32_t i = n_kv > C::kStages ? n_kv - C::kStages : 0; i < n_kv; ++i)
-        mbar_wait(smem_u32(&sm->kv_full[i % C::kStages]), (i / C::kStages) & 1, nullptr);
-      for (uint32_t i = n_q > 2 ? n_q - 2 : 0; i < n_q; ++i)
-        mbar_wait(smem_u32(&sm->q_full[i & 1]), (i >> 1) & 1, nullptr);
-    } else if (warp == kAttnMmaWarp) {
-      // ================================================================ MMA
-      const uint32_t id_qk = idesc_16_f32(BF16, 128, 128, false);
-      const uint32_t id_pv = idesc_16_f32(BF16, 128, (uint32_t)p.D, true);
-      const int ksteps = p.D / 16;
-      uint32_t n_kv = 0, n_q = 0, n_p[2] = {0, 0};
-      auto qk = [&](int x, uint32_t q_slot, uint32_t st) {
-        if (lane == 0) {
-          const uint64_t a = sw128_desc(q_s + q_slot * C::kTileBytes), b = sw128_desc(kv_s + st * C::kTileBytes);
-#pragma unroll
-          for (int k = 0; k < DP / 16; ++k)
-            if (k < ksteps) {
-              const uint64_t off = (uint64_t)((k >> 2) * 16384 + (k & 3) * 32) >> 4;
-              umma_f16(tmem + attn_col_s(x), a + off, b + off, id_qk, k > 0);
-            }
-          umma_commit(smem_u32(&sm->s_full[x]));
-        }
       };
-      auto pv = [&](int x, uint32_t st, bool accumulate) {
-        if (lane == 0) {
-          const uint64_t b = sw128_desc_mn(kv_s + st * C::kTileBytes, 16384, 1024);
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            umma_f16_ta(tmem + attn_col_o(x), tmem + attn_col_s(x) + 8 * k, b + (uint64_t)(k * 2048 >> 4), id_pv,
-                        accumulate || k > 0);
-        }
-      };
-      auto commit = [&](uint64_t* bar) {
-        if (lane == 0) umma_commit(smem_u32(bar));
-      };
-      auto kv_wait = [&](uint32_t i) { return wait(&sm->kv_full[i % C::kStages], (i / C::kStages) & 1); };
-      for (; w.inside(p) && ok; w.next(p)) {
-        const int n = w.j1 - w.j0;
-        if (n <= 0) continue;
-        const bool two = w.unit.ntok > p.tile_tokens;
-        // values past the request's end, in its last page, may be anything: 0 * NaN would spoil the sum
-        auto clean = [&](int j, uint32_t st) {
-          const int jj = w.j0 + j;
-          const int s0 = (jj < w.unit.ns ? jj : w.unit.lo + jj - w.unit.ns) * kAttnTile;
-          const int from = w.seq - s0;
-          if (from >= kAttnTile || from <= 0 || from % kPageTokens == 0) return;
-          const int to = from < kPageTokens ? kPageTokens : kAttnTile;
-          const uint32_t base = kv_s + st * C::kTileBytes;
-          for (int i = lane; i < (to - from) * 8; i += 32)
-#pragma unroll
-            for (int h = 0; h < C::kHalves; ++h) sts_v4(base + h * 16384 + from * 128 + i * 16, make_uint4(0, 0, 0, 0));
-          fence_proxy_async_smem();
-          __syncwarp();
-        };
-        if (two) {
-          const uint32_t qa = n_q & 1, qb = qa ^ 1;
-          if (!wait(&sm->q_full[qa], (n_q >> 1) & 1)) break;
-          ++n_q;
-          if (!kv_wait(n_kv)) break;
-          tc_fence_after();
-          qk(0, qa, n_kv % C::kStages);
-          if (n == 1) commit(&sm->q_empty[qa]);
-          if (!wait(&sm->q_full[qb], (n_q >> 1) & 1)) break;
-          ++n_q;
-          qk(1, qb, n_kv % C::kStages);
-          if (n == 1) commit(&sm->q_empty[qb]);
-          commit(&sm->kv_empty[n_kv % C::kStages]);
-          ++n_kv;
-          for (int j = 0; j < n; ++j) {
-            const uint32_t v = n_kv % C::kStages, k = (n_kv + 1) % C::kStages;
-            if (!kv_wait(n_kv)) break;
-            clean(j, v);
-            if (!wait(&sm->p_full[0], n_p[0] & 1)) break;
-            ++n_p[0];
-            tc_fence_after();
-            pv(0, v, j > 0);
-            if (j + 1 < n) {
-              if (!kv_wait(n_kv + 1)) break;
-              qk(0, qa, k);
-              if (j + 2 == n) commit(&sm->q_empty[qa]);
-            } else {
-              commit(&sm->o_full[0]);
-            }
-            if (!wait(&sm->p_full[1], n_p[1] & 1)) break;
-            ++n_p[1];
-            tc_fence_after();
-            pv(1, v, j > 0);
-            commit(&sm->kv_empty[v]);
-            ++n_kv;
-            if (j + 1 < n) {
-              qk(1, qb, k);
-              if (j + 2 == n) commit(&sm->q_empty[qb]);
-              commit(&sm->kv_empty[k]);
-              ++n_kv;
-            } else {
-              commit(&sm->o_full[1]);
-            }
-          }
-        } else {
-          const uint32_t qa = n_q & 1;
-          if (!wait(&sm->q_full[qa], (n_q >> 1) & 1)) break;
-          ++n_q;
-          for (int j = 0; j < min(2, n); ++j) {
-            if (!kv_wait(n_kv)) break;
-            tc_fence_after();
-            qk(j, qa, n_kv % C::kStages);
-            if (j + 1 == n) commit(&sm->q_empty[qa]);
-            commit(&sm->kv_empty[n_kv % C::kStages]);
-            ++n_kv;
-          }
-          for (int j = 0; j < n && ok; ++j) {
-            const int x = j & 1;
-            const uint32_t v = n_kv % C::kStages;
-            if (!kv_wait(n_kv)) break;
-            clean(j, v);
-            if (!wait(&sm->p_full[x], n_p[x] & 1)) break;
-            ++n_p[x];
-            tc_fence_after();
-            pv(x, v, j > 1);
-            commit(&sm->kv_empty[v]);
-            ++n_kv;
-            if (j + 2 < n) {
-              if (!kv_wait(n_kv)) break;
-              tc_fence_after();
-              qk(x, qa, n_kv % C::kStages);
-              if (j + 3 == n) commit(&sm->q_empty[qa]);
-              commit(&sm->kv_empty[n_kv % C::kStages]);
-              ++n_kv;
-            } else {
-              commit(&sm->o_full[x]);
-            }
-          }
-        }
-      }
-      // every product issued has completed before tensor memory is released
-      commit(&sm->drain);
-      if (!mbar_wait(smem_u32(&sm->drain), 0, nullptr)) ok = false;
-      if (!ok) {
-        sm->abort = 1;
-        raise_status(p.status, kStatusTimeout);
-      }
-    } else {
-      // ================================================================ rows of no request
+      each_item(serve);
+      // rows that belong to no valid request
       const int64_t lo = (int64_t)blockIdx.x * p.T / gridDim.x, hi = ((int64_t)blockIdx.x + 1) * p.T / gridDim.x;
-      for (int64_t t0 = lo + (warp - 10) * 32; t0 < hi; t0 += 64) {
+      for (int64_t t0 = lo; t0 < hi; t0 += 32) {
         const int t = (int)t0 + lane;
         bool none = false;
         if (t < hi) {
@@ -927,8 +887,208 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             for (int i = lane; i < p.Hq; i += 32) p.lse[row * p.Hq + i] = -INFINITY;
         }
       }
+      // every copy has landed before the CTA leaves
+      for (uint32_t i = n_kv > C::kStages ? n_kv - C::kStages : 0; i < n_kv; ++i)
+        mbar_wait(smem_u32(&sm->kv_full[i % C::kStages]), (i / C::kStages) & 1, nullptr);
+      for (uint32_t i = n_q > 2 ? n_q - 2 : 0; i < n_q; ++i)
+        mbar_wait(smem_u32(&sm->q_full[i & 1]), (i >> 1) & 1, nullptr);
+    } else if (warp < kAttnWalkWarp) {
+      // ================================================================ MMA
+      // A warp for each stream: products run in the order they are issued and
+      // hardly ahead of the issuing thread (a pause of 100 cycles in it costs
+      // the tensor core 150, a commit 115), so one stream's waits have to fall
+      // into the other's products.
+      const int x = warp - kAttnMmaWarp;
+      const uint32_t id_qk = idesc_16_f32(BF16, 128, 128, false);
+      const uint32_t id_pv = idesc_16_f32(BF16, 128, (uint32_t)p.D, true);
+      const uint32_t ksteps = (uint32_t)p.D / 16;
+      uint32_t n_p = 0, kv0 = 0;  // probabilities so far; the ring's place before this item
+      // Every place of the rings is waited for, in order, and given back: when
+      // the products that read it are done, or at once where the tile is the
+      // other stream's.  (A wait on a barrier that may
+      // be two phases on, or not yet at the phase before, would be mistaken.)
+      uint32_t kv_seen = 0, q_seen = 0;
+      auto kv_wait = [&](uint32_t place, int step, int n) {
+        while (kv_seen <= place) {
+          const uint32_t st = kv_seen % C::kStages;
+          if (!wait(&sm->kv_full[st], (kv_seen / C::kStages) & 1)) return false;
+          if (step == 2) {
+            const int i = (int)(kv_seen - kv0);
+            const int j = i == 2 * n - 1 ? n - 1 : i & 1 ? (i + 1) / 2 : max(i / 2 - 1, 0);
+            if ((j & 1) != x && lane == 0) mbar_arrive(smem_u32(&sm->kv_empty[st]));
+          }
+          ++kv_seen;
+        }
+        return true;
+      };
+      auto q_wait = [&](uint32_t place, uint32_t own) {
+        while (q_seen <= place) {
+          if (!wait(&sm->q_full[q_seen & 1], (q_seen >> 1) & 1)) return false;
+          if (q_seen != own && lane == 0) mbar_arrive(smem_u32(&sm->q_empty[q_seen & 1]));
+          ++q_seen;
+        }
+        return true;
+      };
+      auto commit = [&](uint64_t* bar) {
+        if (lane == 0) umma_commit(smem_u32(bar));
+      };
+      // The streams take turns, a turn being a tile's P V and the next one's
+      // Q K^T: left alone, the two warps' products interleave, both end
+      // together and the tensor core idles while both softmaxes run.
+      uint32_t turns = 0;
+      auto take_turn = [&]() {
+        const uint32_t i = turns++;
+        if (x == 0 && i == 0) return true;
+        return wait(&sm->turn[x], (i + x + 1) & 1);
+      };
+      auto pass_turn = [&]() {
+        if (lane == 0) mbar_arrive(smem_u32(&sm->turn[x ^ 1]));
+      };
+      auto serve = [&](uint32_t at, int n) {
+        const int step = ATTN_ITEM(step), from = ATTN_AT(at + 4 * x, from);
+        const uint32_t q0 = ATTN_ITEM(q0), q = q0 + (step == 1 ? x : 0);
+        const uint32_t own = from < n ? q : 0xFFFFFFFFu;
+        // the key tile that holds the request's end inside a page: values
+        // after it may be anything, and 0 * NaN would spoil the sum
+        int tail = -1, end;
+        {
+          const int last = ATTN_ITEM(j0) + n - 1;
+          end = ATTN_ITEM(seq) - (last < ATTN_ITEM(ns) ? last : last + ATTN_ITEM(skip)) * kAttnTile;
+          if (end < kAttnTile && end % kPageTokens != 0) tail = n - 1;
+        }
+        auto qk = [&](uint32_t place) {
+          if (lane == 0)
+            umma_f16_k128(tmem + attn_col_s(x), sw128_desc(q_s + (q & 1) * C::kTileBytes),
+                          sw128_desc(kv_s + place % C::kStages * C::kTileBytes), id_qk, ksteps);
+        };
+        auto release = [&](uint32_t place) { commit(&sm->kv_empty[place % C::kStages]); };
+        if (from < n) {
+          if (!q_wait(q, own)) return;
+          const uint32_t k = kv0 + attn_k_place(step, from);
+          if (!kv_wait(k, step, n)) return;
+          tc_fence_after();
+          qk(k);
+          commit(&sm->s_full[x]);
+          release(k);
+          if (from + step >= n) commit(&sm->q_empty[q & 1]);
+        }
+#pragma unroll 1
+        for (int j = from; j - from < n; j += step) {  // (the last round of an odd n: no tile for stream 1)
+          if (j >= n) {
+            if (!take_turn()) return;
+            pass_turn();
+            break;
+          }
+          const bool more = j + step < n;
+          const uint32_t v = kv0 + attn_v_place(step, j, n), k = kv0 + attn_k_place(step, j + step);
+          const uint32_t v_s = kv_s + v % C::kStages * C::kTileBytes;
+          if (!kv_wait(v, step, n)) return;
+          if (j == tail) {
+            // (in shared tiles each stream's warp writes the same zeros)
+            const int to = end < kPageTokens ? kPageTokens : kAttnTile;
+#pragma unroll 1
+            for (int i = lane; i < (to - end) * 8; i += 32)
+#pragma unroll
+              for (int h = 0; h < C::kHalves; ++h) sts_v4(v_s + h * 16384 + end * 128 + i * 16, make_uint4(0, 0, 0, 0));
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+          if (more && !kv_wait(k, step, n)) return;
+          if (!wait(&sm->p_full[x], n_p & 1)) return;
+          ++n_p;
+          if (!take_turn()) return;
+          tc_fence_after();
+          if (lane == 0)
+            umma_f16_ta_k128(tmem + attn_col_o(x), tmem + attn_col_s(x), sw128_desc_mn(v_s, 16384, 1024), id_pv,
+                             j > from);
+          if (more) {
+            qk(k);
+            pass_turn();
+            commit(&sm->s_full[x]);
+            release(k);
+            if (j + 2 * step >= n) commit(&sm->q_empty[q & 1]);
+          } else {
+            pass_turn();
+            commit(&sm->o_full[x]);
+          }
+          release(v);
+        }
+        if (q_wait(q0 + (step == 1 ? 1 : 0), own)) kv_wait(kv0 + 2 * n - 1, step, n);
+      };
+      auto served = [&](uint32_t at, int n) {
+        serve(at, n);
+        kv0 += 2 * n;
+      };
+      each_item(served);
+      // every product issued has completed before tensor memory is released
+      commit(&sm->drain[x]);
+      if (!mbar_wait(smem_u32(&sm->drain[x]), 0, nullptr)) ok = false;
+      if (!ok) {
+        sm->abort = 1;
+        raise_status(p.status, kStatusTimeout);
+      }
+    } else if (warp == kAttnWalkWarp) {
+      // ================================================================ walking
+      AttnWalk w;
+      w.len = len;
+      w.share = share;
+      w.s = 0;
+      if (len > 0) {
+        w.r = sm->begin_r;
+        w.head = sm->begin_head;
+        w.u = sm->begin_u;
+        w.s = sm->begin_s;
+        attn_request(p, w.r, &w.row0, &w.q, &w.seq);
+        w.nu = attn_units(p, w.q);
+        w.enter(p);
+      }
+      uint32_t it = 0;
+      int q0 = 0;
+      auto hand = [&](int n) {
+        const uint32_t st = it % kAttnItems, round = it / kAttnItems;
+        if (round > 0) mbar_wait(smem_u32(&sm->item_empty[st]), (round - 1) & 1, nullptr);
+        if (lane == 0) {
+          AttnItem* i = &sm->item[st];
+          i->n = n;
+          if (n > 0) {
+            i->ntok = w.unit.ntok;
+            i->two = w.unit.ntok > p.tile_tokens;
+            i->p0 = w.unit.p0;
+            const int last = w.unit.p0 + w.unit.ntok - 1;
+            const bool both = w.unit.ntok > p.tile_tokens;
+            i->lo[0] = w.unit.p0;
+            i->hi[0] = both ? w.unit.p0 + p.tile_tokens - 1 : last;
+            i->lo[1] = both ? w.unit.p0 + p.tile_tokens : w.unit.p0;
+            i->hi[1] = last;
+            i->from[0] = 0;
+            i->from[1] = both ? 0 : 1;
+            i->step = both ? 1 : 2;
+            i->ns = w.unit.ns;
+            i->skip = w.unit.lo - w.unit.ns;
+            i->j0 = w.j0;
+            i->token = w.row0 + w.u * 2 * p.tile_tokens;
+            i->head = w.head;
+            i->r = w.r;
+            i->seq = w.seq;
+            i->c0 = w.cta_of(0);
+            i->c1 = w.cta_of(w.unit.n - 1);
+            i->slot = w.s >= 0;
+            i->begins = w.s >= (i->c0 - (int)blockIdx.x) * share;
+            i->q0 = q0;
+            q0 += both ? 2 : 1;
+          }
+          mbar_arrive(smem_u32(&sm->item_full[st]));
+        }
+        __syncwarp();
+        ++it;
+      };
+      for (; w.inside(); w.next(p))
+        if (w.j1 > w.j0) hand(w.j1 - w.j0);
+      hand(0);
     }
   }
+#undef ATTN_ITEM
+#undef ATTN_AT
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

@@ -274,15 +274,61 @@ __device__ __forceinline__ void umma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, ui
       : "memory");
 }
 
-// D[tmem] (+)= A[smem] * B[smem], kind::f16 (A and B of one 16-bit type), one
-// CTA.  Issued by one thread.
-__device__ __forceinline__ void umma_f16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
-                                         uint32_t idesc, uint32_t accumulate) {
+// D[tmem] = A[smem] * B[smem]^T over `steps` (1 to 8) K steps of 16, kind::f16
+// (A and B of one 16-bit type), one CTA: both operands K-major in the 128-byte
+// swizzle layout, K elements 64 to 127 in a second block 16 KB further on.
+// Issued by one thread, as one block of assembly: the descriptors of all
+// steps, computed ahead by the compiler, would not fit in registers.
+__device__ __forceinline__ void umma_f16_k128(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                              uint32_t idesc, uint32_t steps) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred on, all;\n\t.reg .b64 a, b;\n\t"
+      "setp.eq.u32 all, 0, 0;\n\t"
+      "setp.ne.u32 on, 0, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, on;\n\t"
+      "setp.gt.u32 on, %4, 1;\n\tadd.s64 a, %1, 2;\n\tadd.s64 b, %2, 2;\n\t"
+      "@on tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, all;\n\t"
+      "setp.gt.u32 on, %4, 2;\n\tadd.s64 a, %1, 4;\n\tadd.s64 b, %2, 4;\n\t"
+      "@on tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, all;\n\t"
+      "setp.gt.u32 on, %4, 3;\n\tadd.s64 a, %1, 6;\n\tadd.s64 b, %2, 6;\n\t"
+      "@on tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, all;\n\t"
+      "setp.gt.u32 on, %4, 4;\n\tadd.s64 a, %1, 1024;\n\tadd.s64 b, %2, 1024;\n\t"
+      "@on tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, all;\n\t"
+      "setp.gt.u32 on, %4, 5;\n\tadd.s64 a, %1, 1026;\n\tadd.s64 b, %2, 1026;\n\t"
+      "@on tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, all;\n\t"
+      "setp.gt.u32 on, %4, 6;\n\tadd.s64 a, %1, 1028;\n\tadd.s64 b, %2, 1028;\n\t"
+      "@on tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, all;\n\t"
+      "setp.gt.u32 on, %4, 7;\n\tadd.s64 a, %1, 1030;\n\tadd.s64 b, %2, 1030;\n\t"
+      "@on tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, all;\n\t"
+      "}" ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(steps)
+      : "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem] over 8 K steps of 16 (A's first 64 elements in
+// columns 0 to 31, the others in 64 to 95), B MN-major in the 128-byte swizzle
+// layout.
+__device__ __forceinline__ void umma_f16_ta_k128(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                                 uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred acc, all;\n\t.reg .b64 b;\n\t.reg .b32 a;\n\t"
+      "setp.eq.u32 all, 0, 0;\n\t"
+      "setp.ne.u32 acc, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, acc;\n\t"
+      "add.s32 a, %1, 8;\n\tadd.s64 b, %2, 128;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, all;\n\t"
+      "add.s32 a, %1, 16;\n\tadd.s64 b, %2, 256;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, all;\n\t"
+      "add.s32 a, %1, 24;\n\tadd.s64 b, %2, 384;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, all;\n\t"
+      "add.s32 a, %1, 64;\n\tadd.s64 b, %2, 512;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, all;\n\t"
+      "add.s32 a, %1, 72;\n\tadd.s64 b, %2, 640;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, all;\n\t"
+      "add.s32 a, %1, 80;\n\tadd.s64 b, %2, 768;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, all;\n\t"
+      "add.s32 a, %1, 88;\n\tadd.s64 b, %2, 896;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, all;\n\t"
+      "}" ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 
@@ -409,6 +455,17 @@ __device__ __forceinline__ void tmem_ld_wait() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
+// The same for the registers of one load: their uses cannot be moved ahead of
+// the wait, whatever other loads are in flight.
+__device__ __forceinline__ void tmem_ld_wait16(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
+}
+__device__ __forceinline__ void tmem_ld_wait32(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
+}
+
 // A read-only global load issued where it stands: the compiler may neither
 // move it nor re-issue it at the value's use (it may do both with __ldg), so a
 // value loaded ahead of time stays loaded ahead of time.
@@ -455,6 +512,12 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // Packed pairs of FP32 (one instruction for two, each rounded as usual).
 __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
   uint64_t v;
@@ -485,6 +548,18 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
 // Named barrier among `nthreads` threads (multiple of 32).
 __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
+}
+
+// The same, with the OR of the threads' predicates.
+__device__ __forceinline__ bool named_bar_any(uint32_t id, uint32_t nthreads, bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\tbar.red.or.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(nthreads), "r"((uint32_t)pred)
+      : "memory");
+  return r != 0;
 }
 
 __device__ __forceinline__ uint32_t lane_id() { return threadIdx.x & 31u; }
