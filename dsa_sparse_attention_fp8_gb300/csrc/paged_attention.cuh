@@ -45,87 +45,17 @@ struct AttnParams {
   uint32_t* counter;           // [grid] ... and the parts that have arrived
 };
 
-template <bool BF16>
-__device__ __forceinline__ float widen1(uint16_t v) {
-  return BF16 ? __uint_as_float((uint32_t)v << 16) : __half2float(__ushort_as_half(v));
-}
-
-// One warp per (row, head), lane l owning elements l, l + 32, ...: a plain
-// online softmax over the row's keys.
-template <bool BF16, bool FP8>
-__global__ void __launch_bounds__(256) paged_attention_simple_kernel(const __grid_constant__ AttnParams p) {
-  const int64_t warp = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  const int lane = threadIdx.x & 31;
-  if (warp >= (int64_t)p.T * p.Hq) return;
-  const int t = (int)(warp / p.Hq), hq = (int)(warp % p.Hq), h = hq / (p.Hq / p.Hkv);
-  const int r = find_request(p.start, p.R, t);
-  const int s0 = __ldg(p.start + r), s1 = __ldg(p.start + r + 1), seq = __ldg(p.seq_lens + r);
-  float acc[4] = {0.f, 0.f, 0.f, 0.f}, q[4] = {0.f, 0.f, 0.f, 0.f};
-  float m = -INFINITY, l = 0.f;
-  const bool mine = t >= s0 && t < s1;  // rows past the last request belong to none
-  const bool ok = mine && s0 >= 0 && s1 <= p.T && seq >= s1 - s0 && (int64_t)seq <= (int64_t)p.max_blocks * kPageTokens;
-  if (mine && !ok && lane == 0) raise_status(p.status, kStatusBadMetadata);
-  if (ok) {
-    const int pos = seq - (s1 - s0) + (t - s0);
-    for (int i = 0; i < 4; ++i)
-      if (lane + 32 * i < p.D) q[i] = widen1<BF16>(p.q[t * p.q_token + hq * p.q_head + lane + 32 * i]);
-    const int far = p.window > 0 && pos >= p.window ? pos - p.window + 1 : 0;
-    for (int s = 0; s <= pos; ++s) {
-      if (s < far && s >= p.sinks) { s = far - 1; continue; }
-      const int64_t page = __ldg(p.block_table + (int64_t)r * p.max_blocks + s / kPageTokens);
-      if (page < 0 || page >= p.num_pages) {
-        if (lane == 0) raise_status(p.status, kStatusBadPage);
-        continue;
-      }
-      const int off = s % kPageTokens;
-      const uint8_t* row[2];
-      float sc[2] = {1.f, 1.f};
-      for (int w = 0; w < 2; ++w) {
-        row[w] = p.cache[w] + page * p.page_stride[w] + off * p.token_stride[w] + h * p.head_stride[w];
-        if (FP8) sc[w] = __ldg(p.scale[w] + page * p.scale_page[w] + h * p.scale_head[w] + off);
-      }
-      auto at = [&](int w, int j) -> float {
-        if (FP8) {
-          const __half_raw x = __nv_cvt_fp8_to_halfraw(row[w][j], __NV_E4M3);
-          return __half2float(*reinterpret_cast<const __half*>(&x)) * sc[w];
-        }
-        return widen1<BF16>(reinterpret_cast<const uint16_t*>(row[w])[j]);
-      };
-      float z = 0.f;
-      for (int i = 0; i < 4; ++i)
-        if (lane + 32 * i < p.D) z += q[i] * at(0, lane + 32 * i);
-      for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-      z *= p.scale_log2;
-      const float mn = fmaxf(m, z), a = m == -INFINITY ? 0.f : exp2f(m - mn);
-      const float e = mn == -INFINITY ? 0.f : exp2f(z - mn);
-      l = l * a + e;
-      for (int i = 0; i < 4; ++i)
-        if (lane + 32 * i < p.D) acc[i] = acc[i] * a + e * at(1, lane + 32 * i);
-      m = mn;
-    }
-  }
-  for (int i = 0; i < 4; ++i)
-    if (lane + 32 * i < p.D) {
-      const float o = l > 0.f ? acc[i] / l : 0.f;
-      p.out[t * p.out_token + hq * p.out_head + lane + 32 * i] =
-          BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(o)) : __half_as_ushort(__float2half_rn(o));
-    }
-  if (p.lse && lane == 0)
-    p.lse[(int64_t)t * p.Hq + hq] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
-}
-
-// ---------------------------------------------------------------------------
-// The tensor-core kernel
-// ---------------------------------------------------------------------------
 constexpr int kAttnTile = 128;        // keys per tile (two pages)
-constexpr int kAttnSplit = 2;         // softmax warps that share 32 rows, each with a part of the keys
-constexpr int kAttnSoftmaxWarps = 8 * kAttnSplit;
-constexpr int kAttnTmaWarp = kAttnSoftmaxWarps;
-constexpr int kAttnMmaWarp = kAttnSoftmaxWarps + 1;   // and the next: one for each stream
-constexpr int kAttnWalkWarp = kAttnSoftmaxWarps + 3;
-constexpr int kAttnThreads = (kAttnSoftmaxWarps + 4) * 32;
+constexpr int kAttnSoftmaxWarps = 8;
+constexpr int kAttnTmaWarp = 8;
+constexpr int kAttnMmaWarp = 9;       // and 10: one for each stream
+constexpr int kAttnWalkWarp = 11;
+constexpr int kAttnConvertWarp = 12;  // to 15, with an E4M3 cache
 constexpr int kAttnMaxGrid = 160;
-constexpr float kAttnRescaleLog2 = 8.0f;  // rescale the output when the max grows by more than 2^8
+// A row's probabilities are 2^(score - m) with m the maximum of the tiles up to
+// its last rescale; a tile whose probabilities add up to more than this
+// gets a new m (FP16 holds 65,504).
+constexpr float kAttnMostSum = 16384.0f;
 constexpr int64_t kAttnMaxShare = 1 << 23;  // cost of a CTA's work, in 32 bits
 constexpr int kAttnUnitCharge = 1;    // a unit's set-up, in key tiles
 
@@ -211,12 +141,25 @@ struct AttnWalk {
   }
 };
 
-template <int DP>
+template <int DP, bool FP8>
 struct AttnCfg {
   static constexpr int kHalves = DP / 64;
   static constexpr int kTileBytes = kHalves * 128 * 128;  // 128 rows of 64 elements, a half after the other
-  static constexpr int kStages = DP == 128 ? 5 : 8;
-  static constexpr int kSmem = (2 + kStages) * kTileBytes + 3072;
+  static constexpr int kRawBytes = 128 * DP;              // 128 rows of E4M3 codes
+  // Tiles of K and V in flight.  An E4M3 cache has a ring of raw tiles ahead
+  // of that of converted ones.
+  static constexpr int kStages = FP8 ? (DP == 128 ? 3 : 6) : (DP == 128 ? 5 : 8);
+  static constexpr int kRawStages = FP8 ? (DP == 128 ? 3 : 8) : 0;
+  static constexpr int kScaleTiles = FP8 ? 8 : 0;         // key tiles whose scales are held: 128 of K, 128 of V
+  static constexpr int kThreads = FP8 ? 512 : 384;
+  static constexpr int kQ = 0, kKv = 2 * kTileBytes, kRaw = kKv + kStages * kTileBytes;
+  static constexpr int kScale = kRaw + kRawStages * kRawBytes, kMisc = kScale + kScaleTiles * 1024;
+  static constexpr int kSmem = kMisc + 3072;
+  // Registers a thread.  16-bit caches: 168 (65,536 / 384, in eights).  E4M3
+  // caches: 128 at launch, the softmax warps taking some of the others'.
+  static constexpr int kSoftmaxRegs = 176, kIssueRegs = 72, kConvertRegs = 88;
+  static_assert(2 * kSoftmaxRegs + kIssueRegs + kConvertRegs <= 4 * 128, "the block's registers");
+  static_assert(kSmem <= 232448, "shared memory");
 };
 
 // One unit's part of a CTA's share, as the walking warp hands it to the others.
@@ -239,14 +182,16 @@ constexpr int kAttnItems = 4;
 
 struct AttnSmem {
   uint64_t q_full[2], q_empty[2], kv_full[8], kv_empty[8], s_full[2], p_full[2], o_full[2], turn[2];
+  uint64_t raw_full[8], raw_empty[8], scale_empty[8];
   uint64_t item_full[kAttnItems], item_empty[kAttnItems], drain[2];
   AttnItem item[kAttnItems];
   uint32_t tmem;
   int32_t abort, last;
   int32_t begin_r, begin_head, begin_u, begin_s;
-  int64_t warp_cost[kAttnThreads / 32];
+  int64_t warp_cost[16];
   uint8_t bad[16];       // per key tile of the ring: bit i = page i is bad
-  float swap[2][2][128]; // a value of each row, between the warps that share it: [stream][half]
+  uint16_t held[8];      // per raw key tile: tokens that its two pages hold (a byte each)
+  float swap[2][128];    // a value of each row, between the two streams
 };
 static_assert(sizeof(AttnSmem) <= 3072, "shared memory");
 
@@ -279,7 +224,7 @@ __device__ __forceinline__ uint32_t attn_pack(float lo, float hi) {
 // of several units).  Called by all threads; the result is in shared memory.
 __device__ __forceinline__ void attn_locate(const AttnParams& p, AttnSmem* sm, int* len, int* share_out) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int per = (p.R + kAttnThreads - 1) / kAttnThreads;
+  const int threads = (int)blockDim.x, per = (p.R + threads - 1) / threads;
   const int r0 = threadIdx.x * per;
   // cost of one key head of request r; lanes of a warp call it together
   auto cost = [&](int r, bool* bad) -> int64_t {
@@ -324,7 +269,7 @@ __device__ __forceinline__ void attn_locate(const AttnParams& p, AttnSmem* sm, i
   if (lane == 31) sm->warp_cost[warp] = inc;
   __syncthreads();
   int64_t before = inc - sum, total = 0;
-  for (int w = 0; w < kAttnThreads / 32; ++w) {
+  for (int w = 0; w < threads / 32; ++w) {
     if (w < warp) before += sm->warp_cost[w];
     total += sm->warp_cost[w];
   }
@@ -383,6 +328,16 @@ __device__ __forceinline__ void attn_locate(const AttnParams& p, AttnSmem* sm, i
       s += __shfl_sync(0xffffffffu, end, 31);
     }
   }
+}
+
+// Four E4M3 codes as BF16, exactly: exponent and mantissa moved to their places
+// (a value 2^-120 as large, subnormals included), times 2^120.  The NaN codes
+// become +-480: what no row sees may be anything, but has to be finite.
+__device__ __forceinline__ void e4m3_to_bf16(uint32_t codes, uint32_t* lo, uint32_t* hi) {
+  const uint32_t a = __byte_perm(codes, 0u, 0x1404), b = __byte_perm(codes, 0u, 0x3424);  // a code in each upper byte
+  const uint32_t x = (a & 0x80008000u) | ((a & 0x7F007F00u) >> 4), y = (b & 0x80008000u) | ((b & 0x7F007F00u) >> 4);
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(*lo) : "r"(x), "r"(0x7B807B80u));
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(*hi) : "r"(y), "r"(0x7B807B80u));
 }
 
 // Which of 32 keys a row sees, as bits: key i of them lies i - `back` tokens
@@ -471,15 +426,15 @@ __device__ __noinline__ void attn_join(const AttnParams& p, const AttnItem& item
 //               two MMA, one for each stream: S = Q K^T, O += P V (P from
 //               tensor memory);
 //               walking: the CTA's share of the work, unit by unit.
-template <int DP, bool BF16>
-__global__ void __launch_bounds__(kAttnThreads, 1)
+template <int DP, bool BF16, bool FP8>
+__global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
     paged_attention_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                            const __grid_constant__ CUtensorMap tv, const __grid_constant__ AttnParams p) {
-  using C = AttnCfg<DP>;
+  using C = AttnCfg<DP, FP8>;
   extern __shared__ __align__(1024) unsigned char attn_smem[];
-  const uint32_t q_s = smem_u32(attn_smem);
-  const uint32_t kv_s = q_s + 2 * C::kTileBytes;
-  AttnSmem* sm = reinterpret_cast<AttnSmem*>(attn_smem + (2 + C::kStages) * C::kTileBytes);
+  const uint32_t q_s = smem_u32(attn_smem) + C::kQ, kv_s = smem_u32(attn_smem) + C::kKv;
+  const uint32_t raw_s = smem_u32(attn_smem) + C::kRaw, scale_s = smem_u32(attn_smem) + C::kScale;
+  AttnSmem* sm = reinterpret_cast<AttnSmem*>(attn_smem + C::kMisc);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -487,17 +442,22 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       mbar_init(smem_u32(&sm->q_full[i]), 1);
       mbar_init(smem_u32(&sm->q_empty[i]), 2);  // an arrival from each stream
       mbar_init(smem_u32(&sm->s_full[i]), 1);
-      mbar_init(smem_u32(&sm->p_full[i]), 4 * kAttnSplit);
+      mbar_init(smem_u32(&sm->p_full[i]), 4);
       mbar_init(smem_u32(&sm->o_full[i]), 1);
       mbar_init(smem_u32(&sm->turn[i]), 1);
     }
     for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(smem_u32(&sm->kv_full[i]), 1);
+      mbar_init(smem_u32(&sm->kv_full[i]), FP8 ? 4 : 1);
       mbar_init(smem_u32(&sm->kv_empty[i]), 2);
     }
+    for (int i = 0; i < C::kRawStages; ++i) {
+      mbar_init(smem_u32(&sm->raw_full[i]), 1);
+      mbar_init(smem_u32(&sm->raw_empty[i]), 4);
+    }
+    for (int i = 0; i < C::kScaleTiles; ++i) mbar_init(smem_u32(&sm->scale_empty[i]), 2);
     for (int i = 0; i < kAttnItems; ++i) {
       mbar_init(smem_u32(&sm->item_full[i]), 1);
-      mbar_init(smem_u32(&sm->item_empty[i]), kAttnSoftmaxWarps + 3);
+      mbar_init(smem_u32(&sm->item_empty[i]), kAttnSoftmaxWarps + 3 + (FP8 ? 4 : 0));
     }
     mbar_init(smem_u32(&sm->drain[0]), 1);
     mbar_init(smem_u32(&sm->drain[1]), 1);
@@ -536,9 +496,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 
   if (warp < kAttnSoftmaxWarps) {
     // ================================================================ softmax
-    constexpr int kKeys = 128 / kAttnSplit;             // keys of a tile to a thread
-    const int x = warp / (4 * kAttnSplit), half = (warp >> 2) % kAttnSplit;  // stream; part of the keys
-    const uint32_t pair = 2 + x * 4 + (warp & 3);       // named barrier of the warps that share the rows
+    if (FP8) regs_grow<C::kSoftmaxRegs>();
+    const int x = warp >> 2;                            // stream
     const int row = (warp & 3) * 32 + lane;             // row of its tile
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     uint32_t n_s = 0, n_o = 0, tile0 = 0;  // score and output tiles so far; key tiles before this item
@@ -559,22 +518,18 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           const bool inner = s0 + kAttnTile - 1 <= lo && (p.window == 0 || s0 > hi - p.window || s0 + kAttnTile - 1 < p.sinks);
           wait(&sm->s_full[x], n_s & 1);
           ++n_s;
-          if (live) {  // (also after a wait gave up: the warps of a pair meet at barriers)
+          if (live) {
             tc_fence_after();
-            const uint32_t base = lanes + attn_col_s(x) + half * kKeys;
+            const uint32_t base = lanes + attn_col_s(x);
             const uint32_t bad = sm->bad[(tile0 + j) & 15];
-            // Loops over 32 keys that are not unrolled: code that is run once
-            // a tile costs more in instruction fetches than in its work (all
-            // of a row unrolled: 1,500 cycles a tile, against 540 for its
-            // arithmetic in a loop).
+            const uint32_t scales = scale_s + ((tile0 + j) & 7) * 1024;  // E4M3 caches: this tile's
             if (!(inner && bad == 0)) {
               // -inf over the scores that the row does not see
 #pragma unroll 1
-              for (int c = 0; c < kKeys; c += 32) {
+              for (int c = 0; c < kAttnTile; c += 32) {
                 uint32_t v[32];
                 tmem_ld<32>(base + c, v);
-                const int k0 = half * kKeys + c;
-                const uint32_t seen = attn_seen(p, pos - s0 - k0, s0 + k0, bad >> (k0 / 64) & 1u);
+                const uint32_t seen = attn_seen(p, pos - s0 - c, s0 + c, bad >> (c / 64) & 1u);
                 tmem_ld_wait32(v);
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[i] = seen & (1u << i) ? v[i] : 0xFF800000u;
@@ -582,38 +537,75 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               }
               tmem_st_wait();
             }
-            float top = -INFINITY;
-#pragma unroll 1
-            for (int c = 0; c < kKeys; c += 32) {
-              uint32_t v[32];
-              float mx[4];
-              tmem_ld<32>(base + c, v);
-              tmem_ld_wait32(v);
+            // One pass with the maximum that the row has: the probabilities
+            // stay in registers until their sum says that it will do.  If not
+            // (on each row's first tile, and few after it) the row gets the
+            // right one first: the scores are still there.
+            uint32_t pr[64];
+            float sum;
+            bool ready = !__any_sync(0xffffffffu, m == -INFINITY);
+            for (int pass = 0;; ++pass) {
+              if (ready) {
+                const float shift = m == -INFINITY ? 0.f : -m;
+                const uint64_t mul = pack2(p.scale_log2, p.scale_log2), sub = pack2(shift, shift);
+                uint64_t sums[2] = {0, 0};
 #pragma unroll
-              for (int i = 0; i < 4; ++i) mx[i] = max3(__uint_as_float(v[i]), __uint_as_float(v[i + 4]), __uint_as_float(v[i + 8]));
+                for (int c = 0; c < kAttnTile; c += 32) {
+                  uint32_t v[32];
+                  tmem_ld<32>(base + c, v);
+                  tmem_ld_wait32(v);
 #pragma unroll
-              for (int i = 12; i < 32; i += 8)
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  mx[k] = i + 4 + k < 32 ? max3(mx[k], __uint_as_float(v[i + k]), __uint_as_float(v[(i + 4 + k) & 31]))
-                                         : fmaxf(mx[k], __uint_as_float(v[i + k]));
-              top = max3(top, max3(mx[0], mx[1], mx[2]), mx[3]);
-            }
-            top *= p.scale_log2;
-            bool grow = top > m + kAttnRescaleLog2;
-            if (kAttnSplit == 2 ? named_bar_any(pair, 64, grow) : __any_sync(0xffffffffu, grow)) {
-              if (kAttnSplit == 2) {
-                sm->swap[x][half][row] = top;
-                named_bar_sync(pair, 64);
-                top = fmaxf(top, sm->swap[x][half ^ 1][row]);
-                grow = top > m + kAttnRescaleLog2;
+                  for (int i = 0; i < 16; i += 2) {
+                    uint64_t ks0 = mul, ks1 = mul, e0, e1;
+                    if (FP8) lds_2x64(scales + 4 * (c + 2 * i), &ks0, &ks1);
+                    const float2 z0 = unpack2(fma2(pack2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), ks0, sub));
+                    const float2 z1 = unpack2(fma2(pack2(__uint_as_float(v[2 * i + 2]), __uint_as_float(v[2 * i + 3])), ks1, sub));
+                    e0 = pack2(ex2(z0.x), ex2(z0.y));
+                    e1 = pack2(ex2(z1.x), ex2(z1.y));
+                    sums[0] = add2(sums[0], e0);
+                    sums[1] = add2(sums[1], e1);
+                    if (FP8) {
+                      uint64_t vs0, vs1;
+                      lds_2x64(scales + 512 + 4 * (c + 2 * i), &vs0, &vs1);
+                      e0 = mul2(e0, vs0);
+                      e1 = mul2(e1, vs1);
+                    }
+                    const float2 p0 = unpack2(e0), p1 = unpack2(e1);
+                    pr[c / 2 + i] = attn_pack<BF16>(p0.x, p0.y);
+                    pr[c / 2 + i + 1] = attn_pack<BF16>(p1.x, p1.y);
+                  }
+                }
+                const float2 t = unpack2(add2(sums[0], sums[1]));
+                sum = t.x + t.y;
+                if (!__any_sync(0xffffffffu, pass == 0 && !(sum <= kAttnMostSum))) break;
               }
+              ready = true;
+              float top = -INFINITY;
+#pragma unroll 1
+              for (int c = 0; c < kAttnTile; c += 32) {
+                uint32_t v[32];
+                tmem_ld<32>(base + c, v);
+                tmem_ld_wait32(v);
+#pragma unroll
+                for (int i = 0; i < 32; i += 4) {
+                  float a = __uint_as_float(v[i]), b = __uint_as_float(v[i + 1]);
+                  float d = __uint_as_float(v[i + 2]), g = __uint_as_float(v[i + 3]);
+                  if (FP8) {
+                    uint64_t ks0, ks1;
+                    lds_2x64(scales + 4 * (c + i), &ks0, &ks1);
+                    const float2 z0 = unpack2(mul2(pack2(a, b), ks0)), z1 = unpack2(mul2(pack2(d, g), ks1));
+                    a = z0.x, b = z0.y, d = z1.x, g = z1.y;
+                  }
+                  top = max3(max3(top, a, b), d, g);
+                }
+              }
+              if (!FP8) top *= p.scale_log2;
+              const bool grow = top > m;
               if (__any_sync(0xffffffffu, m != -INFINITY)) {  // (else there is no output yet, or zeros)
                 // the scores' arrival says that the stream's previous product is done
                 const float a = grow && m != -INFINITY ? ex2(m - top) : 1.0f;
-                constexpr int kCols = DP / kAttnSplit;
 #pragma unroll 1
-                for (int c = half * kCols; c < (half + 1) * kCols; c += 32) {
+                for (int c = 0; c < DP; c += 32) {
                   uint32_t o[32];
                   tmem_ld<32>(lanes + attn_col_o(x) + c, o);
                   tmem_ld_wait32(o);
@@ -625,26 +617,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               }
               if (grow) m = top;
             }
-            const float shift = m == -INFINITY ? 0.f : -m;
-            const uint64_t mul = pack2(p.scale_log2, p.scale_log2), sub = pack2(shift, shift);
-            uint64_t sum[2] = {0, 0};
-#pragma unroll 1
-            for (int c = 0; c < kKeys; c += 32) {
-              uint32_t v[32], pr[16];
-              tmem_ld<32>(base + c, v);
-              tmem_ld_wait32(v);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const float2 z = unpack2(fma2(pack2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), mul, sub));
-                const float e0 = ex2(z.x), e1 = ex2(z.y);
-                sum[i & 1] = add2(sum[i & 1], pack2(e0, e1));
-                pr[i] = attn_pack<BF16>(e0, e1);
-              }
-              // over scores that this thread has read
-              tmem_st<16>(base + (c & 64) + (c & 32) / 2, pr);
-            }
-            const float2 t = unpack2(add2(sum[0], sum[1]));
-            l += t.x + t.y;
+            l += sum;
+            // over scores that this thread has read: those of 64 keys in the
+            // first 32 of their columns
+            tmem_st<32>(base, pr);
+            tmem_st<32>(base + 64, pr + 32);
             tmem_st_wait();
             tc_fence_before();
           }
@@ -669,27 +646,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       // rows, all of their warps split the columns
       float f0 = 1.f, f1 = 1.f;
       const bool has0 = two ? x == 0 : true, has1 = two ? x == 1 : n > 1;
-      const int cols = two ? DP / kAttnSplit : DP / (2 * kAttnSplit);
-      const int col0 = (two ? half : x * kAttnSplit + half) * cols;
-      if (two) {
-        if (live && kAttnSplit == 2) {
-          sm->swap[x][half][row] = l;
-          named_bar_sync(pair, 64);
-          l += sm->swap[x][half ^ 1][row];
-        }
-      } else {
+      const int cols = two ? DP : DP / 2, col0 = two ? 0 : x * (DP / 2);
+      if (!two) {
         tc_fence_before();
-        sm->swap[x][0][row] = m;  // (both halves have the same)
+        sm->swap[x][row] = m;
         named_bar_sync(1, kAttnSoftmaxWarps * 32);
-        const float a = sm->swap[0][0][row], b = sm->swap[1][0][row], mine = m;
+        const float a = sm->swap[0][row], b = sm->swap[1][row], mine = m;
         m = fmaxf(a, b);
         f0 = a == -INFINITY ? 0.f : ex2(a - m);
         f1 = b == -INFINITY ? 0.f : ex2(b - m);
         named_bar_sync(1, kAttnSoftmaxWarps * 32);
-        sm->swap[x][half][row] = mine == -INFINITY ? 0.f : l * (x ? f1 : f0);
+        sm->swap[x][row] = mine == -INFINITY ? 0.f : l * (x ? f1 : f0);
         named_bar_sync(1, kAttnSoftmaxWarps * 32);
-        l = sm->swap[0][0][row] + sm->swap[1][0][row];
-        if (kAttnSplit == 2) l += sm->swap[0][1][row] + sm->swap[1][1][row];
+        l = sm->swap[0][row] + sm->swap[1][row];
         tc_fence_after();  // the other stream's output is there: its warps came here after it
       }
       if (live && ok) {
@@ -760,6 +729,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     }
     if (!ok) raise_status(p.status, kStatusTimeout);
   } else {
+    if (FP8) {
+      if (warp < kAttnConvertWarp)
+        regs_shrink<C::kIssueRegs>();
+      else
+        regs_shrink<C::kConvertRegs>();
+    }
     // every item is taken, also after a wait gave up: the softmax warps go on
     auto each_item = [&](auto& serve) {
       for (uint32_t it = 0;; ++it) {
@@ -775,17 +750,44 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     if (warp == kAttnTmaWarp) {
       // ================================================================ TMA
       uint32_t n_kv = 0, n_q = 0, tile0 = 0;
-      auto load = [&](const CUtensorMap* map, int head, int page0, int page1) {
-        const uint32_t st = n_kv % C::kStages, round = n_kv / C::kStages;
-        if (round > 0) wait(&sm->kv_empty[st], (round - 1) & 1);
-        if (!ok) return;
-        if (lane == 0) {
-          const uint32_t bar = smem_u32(&sm->kv_full[st]), dst = kv_s + st * C::kTileBytes;
-          mbar_arrive_expect_tx(bar, C::kTileBytes);
+      // One tile of K (is_k) or V from its two pages.  With an E4M3 cache it
+      // goes to the raw ring, and a K tile brings the scales of both.
+      auto load = [&](const CUtensorMap* map, bool is_k, int head, int page0, int page1, int tile, int held) {
+        if (!FP8) {
+          const uint32_t st = n_kv % C::kStages, round = n_kv / C::kStages;
+          if (round > 0) wait(&sm->kv_empty[st], (round - 1) & 1);
+          if (!ok) return;
+          if (lane == 0) {
+            const uint32_t bar = smem_u32(&sm->kv_full[st]), dst = kv_s + st * C::kTileBytes;
+            mbar_arrive_expect_tx(bar, C::kTileBytes);
 #pragma unroll
-          for (int h = 0; h < C::kHalves; ++h) {
-            tma_load_4d(dst + h * 16384, map, h * 64, head, 0, page0, bar);
-            tma_load_4d(dst + h * 16384 + 8192, map, h * 64, head, 0, page1, bar);
+            for (int h = 0; h < C::kHalves; ++h) {
+              tma_load_4d(dst + h * 16384, map, h * 64, head, 0, page0, bar);
+              tma_load_4d(dst + h * 16384 + 8192, map, h * 64, head, 0, page1, bar);
+            }
+          }
+        } else {
+          constexpr uint32_t kRing = FP8 ? C::kRawStages : 1;
+          const uint32_t st = n_kv % kRing, round = n_kv / kRing;
+          if (round > 0) wait(&sm->raw_empty[st], (round - 1) & 1);
+          if (is_k && tile >= 8) wait(&sm->scale_empty[tile & 7], (tile / 8 - 1) & 1);
+          if (!ok) return;
+          if (lane == 0) {
+            const uint32_t bar = smem_u32(&sm->raw_full[st]), dst = raw_s + st * C::kRawBytes;
+            const int h0 = held & 255, h1 = held >> 8;
+            sm->held[st] = (uint16_t)held;
+            mbar_arrive_expect_tx(bar, C::kRawBytes + (is_k ? ((h0 > 0) + (h1 > 0)) * 512 : 0));
+            tma_load_4d(dst, map, 0, head, 0, page0, bar);
+            tma_load_4d(dst + 64 * DP, map, 0, head, 0, page1, bar);
+            if (is_k) {
+#pragma unroll
+              for (int w = 0; w < 2; ++w) {
+                const uint32_t to = scale_s + (tile & 7) * 1024 + w * 512;
+                const float* from = p.scale[w] + (int64_t)head * p.scale_head[w];
+                if (h0 > 0) bulk_load(to, from + page0 * p.scale_page[w], 256, bar);
+                if (h1 > 0) bulk_load(to + 256, from + page1 * p.scale_page[w], 256, bar);
+              }
+            }
           }
         }
         __syncwarp();
@@ -842,24 +844,32 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           __syncwarp();
           if (a0 < 0) a0 = (int)p.num_pages;
           if (a1 < 0) a1 = (int)p.num_pages;
-          load(&tk, head, a0, a1);
+          // tokens that the pages hold (0: not seen, or bad)
+          int held = 0;
+          if (FP8) {
+            const int jj = j0 + j, first_token = (jj < ns ? jj : jj + skip) * kAttnTile;
+            const int left = ATTN_ITEM(seq) - first_token;
+            if (a0 < (int)p.num_pages) held = min(left, kPageTokens);
+            if (a1 < (int)p.num_pages) held |= min(left - kPageTokens, kPageTokens) << 8;
+          }
+          load(&tk, true, head, a0, a1, (int)(tile0 + j), held);
         };
         load_k(0);
         load_q(head, token);
         if (two) {
           load_q(head, token + p.tile_tokens);
-          load(&tv, head, a0, a1);
+          load(&tv, false, head, a0, a1, 0, 0);
           for (int j = 1; j < n && ok; ++j) {
             load_k(j);
-            load(&tv, head, a0, a1);
+            load(&tv, false, head, a0, a1, 0, 0);
           }
         } else {
           if (n > 1) load_k(1);
           for (int j = 0; j < n && ok; ++j) {
             if (j + 1 < n)
-              load(&tv, head, b0, b1);
+              load(&tv, false, head, b0, b1, 0, 0);
             else
-              load(&tv, head, a0, a1);
+              load(&tv, false, head, a0, a1, 0, 0);
             if (j + 2 < n) load_k(j + 2);
           }
         }
@@ -888,8 +898,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
       }
       // every copy has landed before the CTA leaves
-      for (uint32_t i = n_kv > C::kStages ? n_kv - C::kStages : 0; i < n_kv; ++i)
-        mbar_wait(smem_u32(&sm->kv_full[i % C::kStages]), (i / C::kStages) & 1, nullptr);
+      constexpr uint32_t kRing = FP8 ? C::kRawStages : C::kStages;
+      uint64_t* full = FP8 ? sm->raw_full : sm->kv_full;
+      for (uint32_t i = n_kv > kRing ? n_kv - kRing : 0; i < n_kv; ++i)
+        mbar_wait(smem_u32(&full[i % kRing]), (i / kRing) & 1, nullptr);
       for (uint32_t i = n_q > 2 ? n_q - 2 : 0; i < n_q; ++i)
         mbar_wait(smem_u32(&sm->q_full[i & 1]), (i >> 1) & 1, nullptr);
     } else if (warp < kAttnWalkWarp) {
@@ -954,12 +966,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         {
           const int last = ATTN_ITEM(j0) + n - 1;
           end = ATTN_ITEM(seq) - (last < ATTN_ITEM(ns) ? last : last + ATTN_ITEM(skip)) * kAttnTile;
-          if (end < kAttnTile && end % kPageTokens != 0) tail = n - 1;
+          if (!FP8 && end < kAttnTile && end % kPageTokens != 0) tail = n - 1;
         }
-        auto qk = [&](uint32_t place) {
+        auto qk = [&](uint32_t place, int h) {  // 64 of the dimensions
           if (lane == 0)
-            umma_f16_k128(tmem + attn_col_s(x), sw128_desc(q_s + (q & 1) * C::kTileBytes),
-                          sw128_desc(kv_s + place % C::kStages * C::kTileBytes), id_qk, ksteps);
+            umma_f16_k64(tmem + attn_col_s(x), sw128_desc(q_s + (q & 1) * C::kTileBytes + h * 16384),
+                         sw128_desc(kv_s + place % C::kStages * C::kTileBytes + h * 16384), id_qk, h > 0, ksteps - 4 * h);
         };
         auto release = [&](uint32_t place) { commit(&sm->kv_empty[place % C::kStages]); };
         if (from < n) {
@@ -967,7 +979,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           const uint32_t k = kv0 + attn_k_place(step, from);
           if (!kv_wait(k, step, n)) return;
           tc_fence_after();
-          qk(k);
+          for (int h = 0; h < C::kHalves; ++h) qk(k, h);
           commit(&sm->s_full[x]);
           release(k);
           if (from + step >= n) commit(&sm->q_empty[q & 1]);
@@ -993,17 +1005,26 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             fence_proxy_async_smem();
             __syncwarp();
           }
-          if (more && !kv_wait(k, step, n)) return;
+          if (!FP8 && more && !kv_wait(k, step, n)) return;
           if (!wait(&sm->p_full[x], n_p & 1)) return;
           ++n_p;
+          if (FP8 && lane == 0) {  // the tile's scales have been used
+            const uint32_t bar = smem_u32(&sm->scale_empty[(kv0 / 2 + j) & 7]);
+            mbar_arrive(bar);
+            if (step == 2) mbar_arrive(bar);
+          }
           if (!take_turn()) return;
           tc_fence_after();
           if (lane == 0)
             umma_f16_ta_k128(tmem + attn_col_o(x), tmem + attn_col_s(x), sw128_desc_mn(v_s, 16384, 1024), id_pv,
                              j > from);
           if (more) {
-            qk(k);
+            // (the shorter ring of converted tiles has K after this stream's V)
+            if (FP8 && !kv_wait(k, step, n)) return;
+            // the turn passes a few products early: the other warp wakes up meanwhile
+            if (C::kHalves == 2) qk(k, 0);
             pass_turn();
+            qk(k, C::kHalves - 1);
             commit(&sm->s_full[x]);
             release(k);
             if (j + 2 * step >= n) commit(&sm->q_empty[q & 1]);
@@ -1027,6 +1048,56 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         sm->abort = 1;
         raise_status(p.status, kStatusTimeout);
       }
+    } else if (FP8 && warp >= kAttnConvertWarp) {
+      // ================================================================ converting
+      // E4M3 codes to BF16 (exactly), row by row into the 128-byte-swizzled
+      // layout that both products read.
+      const int tid = threadIdx.x - kAttnConvertWarp * 32;
+      constexpr uint32_t kRing = FP8 ? C::kRawStages : 1;
+      uint32_t n_kv = 0, tile0 = 0;
+      auto serve = [&](uint32_t at, int n) {
+        const int step = ATTN_ITEM(step);
+#pragma unroll 1
+        for (int i = 0; i < 2 * n; ++i, ++n_kv) {
+          const uint32_t rst = n_kv % kRing, st = n_kv % C::kStages;
+          if (!wait(&sm->raw_full[rst], (n_kv / kRing) & 1)) return;
+          const bool is_k = step == 1 ? (i & 1) == 0 : i == 0 || ((i & 1) && i != 2 * n - 1);
+          if (is_k) {
+            // scales: the softmax's own factor goes into those of K; tokens
+            // that their page does not hold get harmless ones
+            const int j = step == 1 || i == 0 ? i / 2 : (i + 1) / 2;
+            const uint32_t mine = scale_s + ((tile0 + j) & 7) * 1024 + tid * 4;
+            const int held = sm->held[rst] >> (tid & 64 ? 8 : 0) & 255;
+            const bool good = (tid & 63) < held;
+            sts_u32(mine, good ? __float_as_uint(fmaxf(__uint_as_float(lds_u32(mine)) * p.scale_log2, 1e-37f))
+                               : __float_as_uint(1.0f));
+            if (!good) sts_u32(mine + 512, 0u);
+          }
+          if (n_kv >= C::kStages && !wait(&sm->kv_empty[st], (n_kv / C::kStages - 1) & 1)) return;
+          const uint32_t src = raw_s + rst * C::kRawBytes, dst = kv_s + st * C::kTileBytes;
+#pragma unroll 2
+          for (int u = tid; u < C::kRawBytes / 16; u += 128) {
+            const int row = u / (DP / 16), cc = u % (DP / 16);  // 16 codes: 32 bytes of a row's half cc / 4
+            const uint4 v = lds_v4(src + u * 16);
+            uint4 lo, hi;
+            e4m3_to_bf16(v.x, &lo.x, &lo.y);
+            e4m3_to_bf16(v.y, &lo.z, &lo.w);
+            e4m3_to_bf16(v.z, &hi.x, &hi.y);
+            e4m3_to_bf16(v.w, &hi.z, &hi.w);
+            const uint32_t to = dst + (cc / 4) * 16384 + row * 128, unit = 2 * (cc & 3);
+            sts_v4(to + ((unit ^ (row & 7)) << 4), lo);
+            sts_v4(to + (((unit + 1) ^ (row & 7)) << 4), hi);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(smem_u32(&sm->kv_full[st]));
+            mbar_arrive(smem_u32(&sm->raw_empty[rst]));
+          }
+        }
+        tile0 += n;
+      };
+      each_item(serve);
     } else if (warp == kAttnWalkWarp) {
       // ================================================================ walking
       AttnWalk w;

@@ -37,6 +37,9 @@ __device__ __forceinline__ uint4 lds_v4(uint32_t a) {
                : "r"(a));
   return v;
 }
+__device__ __forceinline__ void lds_2x64(uint32_t a, uint64_t* x, uint64_t* y) {
+  asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(*x), "=l"(*y) : "r"(a));
+}
 __device__ __forceinline__ void sts_v4(uint32_t a, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z),
                "r"(v.w)
@@ -274,33 +277,24 @@ __device__ __forceinline__ void umma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, ui
       : "memory");
 }
 
-// D[tmem] = A[smem] * B[smem]^T over `steps` (1 to 8) K steps of 16, kind::f16
-// (A and B of one 16-bit type), one CTA: both operands K-major in the 128-byte
-// swizzle layout, K elements 64 to 127 in a second block 16 KB further on.
-// Issued by one thread, as one block of assembly: the descriptors of all
-// steps, computed ahead by the compiler, would not fit in registers.
-__device__ __forceinline__ void umma_f16_k128(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
-                                              uint32_t idesc, uint32_t steps) {
+// D[tmem] (+)= A[smem] * B[smem]^T over the first `steps` (at most 4) K steps of
+// 16, kind::f16 (A and B of one 16-bit type), one CTA: both operands K-major
+// in the 128-byte swizzle layout.  Issued by one thread, as one block of
+// assembly: the descriptors of all steps, computed ahead by the compiler,
+// would take registers.
+__device__ __forceinline__ void umma_f16_k64(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                             uint32_t idesc, uint32_t accumulate, uint32_t steps) {
   asm volatile(
-      "{\n\t.reg .pred on, all;\n\t.reg .b64 a, b;\n\t"
-      "setp.eq.u32 all, 0, 0;\n\t"
-      "setp.ne.u32 on, 0, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, on;\n\t"
-      "setp.gt.u32 on, %4, 1;\n\tadd.s64 a, %1, 2;\n\tadd.s64 b, %2, 2;\n\t"
+      "{\n\t.reg .pred on, acc, all;\n\t.reg .b64 a, b;\n\t"
+      "setp.eq.u32 all, 0, 0;\n\tsetp.ne.u32 acc, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, acc;\n\t"
+      "setp.gt.u32 on, %5, 1;\n\tadd.s64 a, %1, 2;\n\tadd.s64 b, %2, 2;\n\t"
       "@on tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, all;\n\t"
-      "setp.gt.u32 on, %4, 2;\n\tadd.s64 a, %1, 4;\n\tadd.s64 b, %2, 4;\n\t"
+      "setp.gt.u32 on, %5, 2;\n\tadd.s64 a, %1, 4;\n\tadd.s64 b, %2, 4;\n\t"
       "@on tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, all;\n\t"
-      "setp.gt.u32 on, %4, 3;\n\tadd.s64 a, %1, 6;\n\tadd.s64 b, %2, 6;\n\t"
+      "setp.gt.u32 on, %5, 3;\n\tadd.s64 a, %1, 6;\n\tadd.s64 b, %2, 6;\n\t"
       "@on tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, all;\n\t"
-      "setp.gt.u32 on, %4, 4;\n\tadd.s64 a, %1, 1024;\n\tadd.s64 b, %2, 1024;\n\t"
-      "@on tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, all;\n\t"
-      "setp.gt.u32 on, %4, 5;\n\tadd.s64 a, %1, 1026;\n\tadd.s64 b, %2, 1026;\n\t"
-      "@on tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, all;\n\t"
-      "setp.gt.u32 on, %4, 6;\n\tadd.s64 a, %1, 1028;\n\tadd.s64 b, %2, 1028;\n\t"
-      "@on tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, all;\n\t"
-      "setp.gt.u32 on, %4, 7;\n\tadd.s64 a, %1, 1030;\n\tadd.s64 b, %2, 1030;\n\t"
-      "@on tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, all;\n\t"
-      "}" ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(steps)
+      "}" ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(steps)
       : "memory");
 }
 
@@ -370,6 +364,13 @@ __device__ __forceinline__ uint32_t idesc_16_f32(bool bf16, uint32_t M, uint32_t
 template <int N>
 __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t* r);
 
+template <>
+__device__ __forceinline__ void tmem_st<8>(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      : "memory");
+}
 template <>
 __device__ __forceinline__ void tmem_st<16>(uint32_t taddr, const uint32_t* r) {
   asm volatile(

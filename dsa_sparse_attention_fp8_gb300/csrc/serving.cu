@@ -110,30 +110,34 @@ int make_map(CUtensorMap* m, const char* what, CUtensorMapDataType type, int siz
   return DSA_OK;
 }
 
-template <int DP, bool BF16>
+template <int DP, bool BF16, bool FP8>
 int launch_attention(const dsa::AttnParams& p, int grid, cudaStream_t st) {
-  using C = dsa::AttnCfg<DP>;
+  using C = dsa::AttnCfg<DP, FP8>;
   static std::once_flag once;
   static cudaError_t attr_err = cudaSuccess;
   std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(dsa::paged_attention_kernel<DP, BF16>,
+    attr_err = cudaFuncSetAttribute(dsa::paged_attention_kernel<DP, BF16, FP8>,
                                     cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   });
   if (attr_err != cudaSuccess)
     return fail(DSA_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(attr_err));
   const CUtensorMapDataType type = BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  CUtensorMap tq, tk, tv;
+  CUtensorMap tq, tkv[2];
   const int64_t qd[3] = {p.D, p.Hq, p.T}, qs[2] = {p.q_head * 2, p.q_token * 2};
   const int qb[3] = {64, p.group, p.tile_tokens};
   if (const int rc = make_map(&tq, "q", type, 2, p.q, 3, qd, qs, qb, true)) return rc;
+  // a 16-bit page comes in two boxes of 64 dimensions (128-byte rows), an
+  // E4M3 page in one
   const int64_t kd[4] = {p.D, p.Hkv, DSA_PAGE_TOKENS, p.num_pages};
-  const int kb[4] = {64, 1, DSA_PAGE_TOKENS, 1};
+  const int kb[4] = {FP8 ? DP : 64, 1, DSA_PAGE_TOKENS, 1};
   const char* const names[2] = {"k_cache", "v_cache"};
   for (int i = 0; i < 2; ++i) {
     const int64_t ks[3] = {p.head_stride[i], p.token_stride[i], p.page_stride[i]};
-    if (const int rc = make_map(i ? &tv : &tk, names[i], type, 2, p.cache[i], 4, kd, ks, kb, true)) return rc;
+    if (const int rc = make_map(&tkv[i], names[i], FP8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : type, FP8 ? 1 : 2, p.cache[i],
+                                4, kd, ks, kb, !FP8))
+      return rc;
   }
-  dsa::paged_attention_kernel<DP, BF16><<<grid, dsa::kAttnThreads, C::kSmem, st>>>(tq, tk, tv, p);
+  dsa::paged_attention_kernel<DP, BF16, FP8><<<grid, C::kThreads, C::kSmem, st>>>(tq, tkv[0], tkv[1], p);
   set_last_launches(1);
   return check_launch("paged_attention_kernel");
 }
@@ -295,16 +299,12 @@ int dsa_paged_attention(const void* q, int64_t q_token_stride, int64_t q_head_st
   p.part = reinterpret_cast<float*>(ws + kAttnCounterBytes);
   p.part_ml = reinterpret_cast<float2*>(p.part + attention_part_rows() * 128);
   const cudaStream_t st = (cudaStream_t)stream;
-  if (cache->type == DSA_TYPE_E4M3) {
-    const int64_t blocks = ((int64_t)T * Hq + 7) / 8;
-    if (blocks > INT32_MAX) return fail(DSA_ERR_INVALID_ARG, "too many rows");
-    dsa::paged_attention_simple_kernel<true, true><<<(unsigned)blocks, 256, 0, st>>>(p);
-    set_last_launches(1);
-    return check_launch("paged_attention_simple_kernel");
-  }
+  const bool wide = p.D > 64;
+  if (cache->type == DSA_TYPE_E4M3)
+    return wide ? launch_attention<128, true, true>(p, grid, st) : launch_attention<64, true, true>(p, grid, st);
   if (type == DSA_TYPE_BF16)
-    return p.D > 64 ? launch_attention<128, true>(p, grid, st) : launch_attention<64, true>(p, grid, st);
-  return p.D > 64 ? launch_attention<128, false>(p, grid, st) : launch_attention<64, false>(p, grid, st);
+    return wide ? launch_attention<128, true, false>(p, grid, st) : launch_attention<64, true, false>(p, grid, st);
+  return wide ? launch_attention<128, false, false>(p, grid, st) : launch_attention<64, false, false>(p, grid, st);
 }
 
 int dsa_add_rms_norm(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
