@@ -144,22 +144,25 @@ struct AttnWalk {
 template <int DP, bool FP8>
 struct AttnCfg {
   static constexpr int kHalves = DP / 64;
-  static constexpr int kTileBytes = kHalves * 128 * 128;  // 128 rows of 64 elements, a half after the other
-  static constexpr int kRawBytes = 128 * DP;              // 128 rows of E4M3 codes
-  // Tiles of K and V in flight.  An E4M3 cache has a ring of raw tiles ahead
-  // of that of converted ones.
-  static constexpr int kStages = FP8 ? (DP == 128 ? 3 : 6) : (DP == 128 ? 5 : 8);
-  static constexpr int kRawStages = FP8 ? (DP == 128 ? 3 : 8) : 0;
-  static constexpr int kScaleTiles = FP8 ? 8 : 0;         // key tiles whose scales are held: 128 of K, 128 of V
+  static constexpr int kTileBytes = kHalves * 128 * 128;  // 128 rows of 64 16-bit elements, a half after the other
+  static constexpr int kRawBytes = 128 * 128;             // 128 rows of 128 E4M3 codes
+  // Tiles in flight.  16-bit caches: one ring of K and V tiles.  E4M3 caches: a
+  // ring of K tiles as they are, one of V tiles as they are and one of V tiles
+  // as BF16, and the scales of kScaleTiles key tiles (128 of K, 128 of V).
+  static constexpr int kStages = DP == 128 ? 5 : 8;
+  static constexpr int kKStages = 3, kVRawStages = 2, kVStages = 2, kScaleTiles = 8;
   static constexpr int kThreads = FP8 ? 512 : 384;
-  static constexpr int kQ = 0, kKv = 2 * kTileBytes, kRaw = kKv + kStages * kTileBytes;
-  static constexpr int kScale = kRaw + kRawStages * kRawBytes, kMisc = kScale + kScaleTiles * 1024;
+  static constexpr int kQ = 0, kKv = 2 * kTileBytes;
+  static constexpr int kV = kKv + kKStages * kRawBytes, kVRaw = kV + kVStages * kTileBytes;
+  static constexpr int kScale = kVRaw + kVRawStages * kRawBytes;  // then the query rows' factors, 128 for each slot
+  static constexpr int kMisc = FP8 ? kScale + (kScaleTiles + 1) * 1024 : kKv + kStages * kTileBytes;
   static constexpr int kSmem = kMisc + 3072;
   // Registers a thread.  16-bit caches: 168 (65,536 / 384, in eights).  E4M3
   // caches: 128 at launch, the softmax warps taking some of the others'.
   static constexpr int kSoftmaxRegs = 176, kIssueRegs = 72, kConvertRegs = 88;
   static_assert(2 * kSoftmaxRegs + kIssueRegs + kConvertRegs <= 4 * 128, "the block's registers");
   static_assert(kSmem <= 232448, "shared memory");
+  static_assert(!FP8 || DP == 128, "E4M3 rows are 128 bytes, whatever the head's size");
 };
 
 // One unit's part of a CTA's share, as the walking warp hands it to the others.
@@ -182,7 +185,7 @@ constexpr int kAttnItems = 4;
 
 struct AttnSmem {
   uint64_t q_full[2], q_empty[2], kv_full[8], kv_empty[8], s_full[2], p_full[2], o_full[2], turn[2];
-  uint64_t raw_full[8], raw_empty[8], scale_empty[8];
+  uint64_t raw_full[2], raw_empty[2], q_ready[2], scale_empty[8];
   uint64_t item_full[kAttnItems], item_empty[kAttnItems], drain[2];
   AttnItem item[kAttnItems];
   uint32_t tmem;
@@ -190,7 +193,6 @@ struct AttnSmem {
   int32_t begin_r, begin_head, begin_u, begin_s;
   int64_t warp_cost[16];
   uint8_t bad[16];       // per key tile of the ring: bit i = page i is bad
-  uint16_t held[8];      // per raw key tile: tokens that its two pages hold (a byte each)
   float swap[2][128];    // a value of each row, between the two streams
 };
 static_assert(sizeof(AttnSmem) <= 3072, "shared memory");
@@ -433,28 +435,30 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
   using C = AttnCfg<DP, FP8>;
   extern __shared__ __align__(1024) unsigned char attn_smem[];
   const uint32_t q_s = smem_u32(attn_smem) + C::kQ, kv_s = smem_u32(attn_smem) + C::kKv;
-  const uint32_t raw_s = smem_u32(attn_smem) + C::kRaw, scale_s = smem_u32(attn_smem) + C::kScale;
+  const uint32_t scale_s = smem_u32(attn_smem) + C::kScale, factor_s = scale_s + C::kScaleTiles * 1024;
   AttnSmem* sm = reinterpret_cast<AttnSmem*>(attn_smem + C::kMisc);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&sm->q_full[i]), 1);
-      mbar_init(smem_u32(&sm->q_empty[i]), 2);  // an arrival from each stream
+      mbar_init(smem_u32(&sm->q_empty[i]), 2 + (FP8 ? kAttnSoftmaxWarps : 0));  // an arrival from each stream
       mbar_init(smem_u32(&sm->s_full[i]), 1);
       mbar_init(smem_u32(&sm->p_full[i]), 4);
       mbar_init(smem_u32(&sm->o_full[i]), 1);
       mbar_init(smem_u32(&sm->turn[i]), 1);
     }
-    for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(smem_u32(&sm->kv_full[i]), FP8 ? 4 : 1);
+    // (E4M3 caches: K's ring, then that of V as BF16, which four warps fill)
+    for (int i = 0; i < 8; ++i) {
+      mbar_init(smem_u32(&sm->kv_full[i]), FP8 && i >= C::kKStages ? 4 : 1);
       mbar_init(smem_u32(&sm->kv_empty[i]), 2);
+      mbar_init(smem_u32(&sm->scale_empty[i]), 2);
     }
-    for (int i = 0; i < C::kRawStages; ++i) {
+    for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&sm->raw_full[i]), 1);
       mbar_init(smem_u32(&sm->raw_empty[i]), 4);
+      mbar_init(smem_u32(&sm->q_ready[i]), 4);
     }
-    for (int i = 0; i < C::kScaleTiles; ++i) mbar_init(smem_u32(&sm->scale_empty[i]), 2);
     for (int i = 0; i < kAttnItems; ++i) {
       mbar_init(smem_u32(&sm->item_full[i]), 1);
       mbar_init(smem_u32(&sm->item_empty[i]), kAttnSoftmaxWarps + 3 + (FP8 ? 4 : 0));
@@ -472,6 +476,10 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
     tma_prefetch_desc(&tq);
     tma_prefetch_desc(&tk);
     tma_prefetch_desc(&tv);
+  }
+  if (FP8) {  // scales of pages that are never loaded have to be numbers
+    for (int i = threadIdx.x; i < C::kScaleTiles * 256; i += C::kThreads) sts_u32(scale_s + 4 * i, __float_as_uint(1.0f));
+    fence_proxy_async_smem();
   }
   int len, share;
   attn_locate(p, sm, &len, &share);
@@ -500,6 +508,15 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
     const int x = warp >> 2;                            // stream
     const int row = (warp & 3) * 32 + lane;             // row of its tile
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    // E4M3 caches: a query tile's slot is free once its rows' factors are read, too
+    auto factor_read = [&](uint32_t at) {
+      __syncwarp();
+      if (lane == 0) {
+        const uint32_t q0 = ATTN_ITEM(q0);
+        mbar_arrive(smem_u32(&sm->q_empty[q0 & 1]));
+        if (ATTN_ITEM(two)) mbar_arrive(smem_u32(&sm->q_empty[~q0 & 1]));
+      }
+    };
     uint32_t n_s = 0, n_o = 0, tile0 = 0;  // score and output tiles so far; key tiles before this item
     for (uint32_t it = 0;; ++it) {
       const uint32_t at = smem_u32(&sm->item[it % kAttnItems]);
@@ -512,17 +529,33 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
         const int lo = ATTN_AT(mine, lo), hi = ATTN_AT(mine, hi), step = ATTN_ITEM(step);
         const bool live = (warp & 3) * 32 < (hi - lo + 1) * p.group;  // some row of this warp is real
         const int pos = min(lo + row / p.group, hi);
-        const int ns = ATTN_ITEM(ns), skip = ATTN_ITEM(skip), j0 = ATTN_ITEM(j0);
+        const int ns = ATTN_ITEM(ns), skip = ATTN_ITEM(skip), j0 = ATTN_ITEM(j0), seq = ATTN_ITEM(seq);
+        float factor = p.scale_log2;  // of the row's scores
         for (int j = ATTN_AT(mine, from); j < n; j += step) {
           const int s0 = (j0 + j + (j0 + j < ns ? 0 : skip)) * kAttnTile;
           const bool inner = s0 + kAttnTile - 1 <= lo && (p.window == 0 || s0 > hi - p.window || s0 + kAttnTile - 1 < p.sinks);
           wait(&sm->s_full[x], n_s & 1);
           ++n_s;
+          if (FP8 && j == ATTN_AT(mine, from)) {
+            const uint32_t q = ATTN_ITEM(q0) + (step == 1 ? x : 0);
+            factor = p.scale_log2 * __uint_as_float(lds_u32(factor_s + ((q & 1) * 128 + row) * 4));
+            factor_read(at);
+          }
           if (live) {
             tc_fence_after();
             const uint32_t base = lanes + attn_col_s(x);
             const uint32_t bad = sm->bad[(tile0 + j) & 15];
-            const uint32_t scales = scale_s + ((tile0 + j) & 7) * 1024;  // E4M3 caches: this tile's
+            // E4M3 caches: this tile's scales; those past the request's end may
+            // be anything (each warp puts numbers there before it reads them)
+            const uint32_t scales = scale_s + ((tile0 + j) & 7) * 1024;
+            if (FP8 && s0 + kAttnTile > seq) {
+              for (int i = max(seq - s0, 0) + lane; i < kAttnTile; i += 32) {
+                sts_u32(scales + 4 * i, __float_as_uint(1.0f));
+                sts_u32(scales + 512 + 4 * i, 0u);
+              }
+              fence_proxy_async_smem();
+              __syncwarp();
+            }
             if (!(inner && bad == 0)) {
               // -inf over the scores that the row does not see
 #pragma unroll 1
@@ -547,7 +580,7 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
             for (int pass = 0;; ++pass) {
               if (ready) {
                 const float shift = m == -INFINITY ? 0.f : -m;
-                const uint64_t mul = pack2(p.scale_log2, p.scale_log2), sub = pack2(shift, shift);
+                const uint64_t mul = pack2(factor, factor), sub = pack2(shift, shift);
                 uint64_t sums[2] = {0, 0};
 #pragma unroll
                 for (int c = 0; c < kAttnTile; c += 32) {
@@ -557,7 +590,11 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
 #pragma unroll
                   for (int i = 0; i < 16; i += 2) {
                     uint64_t ks0 = mul, ks1 = mul, e0, e1;
-                    if (FP8) lds_2x64(scales + 4 * (c + 2 * i), &ks0, &ks1);
+                    if (FP8) {
+                      lds_2x64(scales + 4 * (c + 2 * i), &ks0, &ks1);
+                      ks0 = mul2(ks0, mul);
+                      ks1 = mul2(ks1, mul);
+                    }
                     const float2 z0 = unpack2(fma2(pack2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), ks0, sub));
                     const float2 z1 = unpack2(fma2(pack2(__uint_as_float(v[2 * i + 2]), __uint_as_float(v[2 * i + 3])), ks1, sub));
                     e0 = pack2(ex2(z0.x), ex2(z0.y));
@@ -599,7 +636,7 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
                   top = max3(max3(top, a, b), d, g);
                 }
               }
-              if (!FP8) top *= p.scale_log2;
+              top *= factor;
               const bool grow = top > m;
               if (__any_sync(0xffffffffu, m != -INFINITY)) {  // (else there is no output yet, or zeros)
                 // the scores' arrival says that the stream's previous product is done
@@ -631,6 +668,7 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
       }
       tile0 += n;
 
+      if (FP8 && ATTN_AT(at + 4 * x, from) >= n) factor_read(at);
       // ---- the unit's end: out = O / l, or the part of a split unit
       const bool two = ATTN_ITEM(two) != 0;
       const int first = two && x ? p.tile_tokens : 0;  // this stream's first token in the unit
@@ -750,48 +788,60 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
     if (warp == kAttnTmaWarp) {
       // ================================================================ TMA
       uint32_t n_kv = 0, n_q = 0, tile0 = 0;
-      // One tile of K (is_k) or V from its two pages.  With an E4M3 cache it
-      // goes to the raw ring, and a K tile brings the scales of both.
-      auto load = [&](const CUtensorMap* map, bool is_k, int head, int page0, int page1, int tile, int held) {
-        if (!FP8) {
-          const uint32_t st = n_kv % C::kStages, round = n_kv / C::kStages;
-          if (round > 0) wait(&sm->kv_empty[st], (round - 1) & 1);
-          if (!ok) return;
-          if (lane == 0) {
-            const uint32_t bar = smem_u32(&sm->kv_full[st]), dst = kv_s + st * C::kTileBytes;
-            mbar_arrive_expect_tx(bar, C::kTileBytes);
+      // One tile of K or V from its two pages.  With
+      // an E4M3 cache K's tile brings the scales of both.
+      auto load = [&](const CUtensorMap* map, int head, int page0, int page1) {
+        const uint32_t st = n_kv % C::kStages, round = n_kv / C::kStages;
+        if (round > 0) wait(&sm->kv_empty[st], (round - 1) & 1);
+        if (!ok) return;
+        if (lane == 0) {
+          const uint32_t bar = smem_u32(&sm->kv_full[st]), dst = kv_s + st * C::kTileBytes;
+          mbar_arrive_expect_tx(bar, C::kTileBytes);
 #pragma unroll
-            for (int h = 0; h < C::kHalves; ++h) {
-              tma_load_4d(dst + h * 16384, map, h * 64, head, 0, page0, bar);
-              tma_load_4d(dst + h * 16384 + 8192, map, h * 64, head, 0, page1, bar);
-            }
-          }
-        } else {
-          constexpr uint32_t kRing = FP8 ? C::kRawStages : 1;
-          const uint32_t st = n_kv % kRing, round = n_kv / kRing;
-          if (round > 0) wait(&sm->raw_empty[st], (round - 1) & 1);
-          if (is_k && tile >= 8) wait(&sm->scale_empty[tile & 7], (tile / 8 - 1) & 1);
-          if (!ok) return;
-          if (lane == 0) {
-            const uint32_t bar = smem_u32(&sm->raw_full[st]), dst = raw_s + st * C::kRawBytes;
-            const int h0 = held & 255, h1 = held >> 8;
-            sm->held[st] = (uint16_t)held;
-            mbar_arrive_expect_tx(bar, C::kRawBytes + (is_k ? ((h0 > 0) + (h1 > 0)) * 512 : 0));
-            tma_load_4d(dst, map, 0, head, 0, page0, bar);
-            tma_load_4d(dst + 64 * DP, map, 0, head, 0, page1, bar);
-            if (is_k) {
-#pragma unroll
-              for (int w = 0; w < 2; ++w) {
-                const uint32_t to = scale_s + (tile & 7) * 1024 + w * 512;
-                const float* from = p.scale[w] + (int64_t)head * p.scale_head[w];
-                if (h0 > 0) bulk_load(to, from + page0 * p.scale_page[w], 256, bar);
-                if (h1 > 0) bulk_load(to + 256, from + page1 * p.scale_page[w], 256, bar);
-              }
-            }
+          for (int h = 0; h < C::kHalves; ++h) {
+            tma_load_4d(dst + h * 16384, map, h * 64, head, 0, page0, bar);
+            tma_load_4d(dst + h * 16384 + 8192, map, h * 64, head, 0, page1, bar);
           }
         }
         __syncwarp();
         ++n_kv;
+      };
+      uint32_t n_k = 0, n_v = 0;  // E4M3 caches: tiles of each
+      auto load8 = [&](bool is_k, int head, int page0, int page1) {
+        const uint32_t t = is_k ? n_k++ : n_v++;
+        const uint32_t ring = is_k ? C::kKStages : C::kVRawStages, st = t % ring, round = t / ring;
+        uint64_t* empty = is_k ? sm->kv_empty : sm->raw_empty;
+        if (round > 0) wait(&empty[st], (round - 1) & 1);
+        if (is_k && t >= 8) wait(&sm->scale_empty[t & 7], (t / 8 - 1) & 1);
+        if (!ok) {
+          if (is_k) --n_k; else --n_v;
+          return;
+        }
+        if (lane == 0) {
+          const uint32_t bar = smem_u32(is_k ? &sm->kv_full[st] : &sm->raw_full[st]);
+          const uint32_t dst = smem_u32(attn_smem) + (is_k ? C::kKv : C::kVRaw) + st * C::kRawBytes;
+          const int none = (int)p.num_pages;
+          const uint32_t held = is_k ? (page0 < none) + (page1 < none) : 0;
+          mbar_arrive_expect_tx(bar, C::kRawBytes + held * 512);
+          tma_load_4d(dst, is_k ? &tk : &tv, 0, head, 0, page0, bar);
+          tma_load_4d(dst + 8192, is_k ? &tk : &tv, 0, head, 0, page1, bar);
+          if (is_k) {
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              const uint32_t to = scale_s + (t & 7) * 1024 + w * 512;
+              const float* from = p.scale[w] + (int64_t)head * p.scale_head[w];
+              if (page0 < none) bulk_load(to, from + page0 * p.scale_page[w], 256, bar);
+              if (page1 < none) bulk_load(to + 256, from + page1 * p.scale_page[w], 256, bar);
+            }
+          }
+        }
+        __syncwarp();
+      };
+      auto load_v = [&](int head, int page0, int page1) {
+        if (FP8)
+          load8(false, head, page0, page1);
+        else
+          load(&tv, head, page0, page1);
       };
       auto load_q = [&](int head, int token) {
         const uint32_t st = n_q & 1, round = n_q >> 1;
@@ -844,32 +894,27 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
           __syncwarp();
           if (a0 < 0) a0 = (int)p.num_pages;
           if (a1 < 0) a1 = (int)p.num_pages;
-          // tokens that the pages hold (0: not seen, or bad)
-          int held = 0;
-          if (FP8) {
-            const int jj = j0 + j, first_token = (jj < ns ? jj : jj + skip) * kAttnTile;
-            const int left = ATTN_ITEM(seq) - first_token;
-            if (a0 < (int)p.num_pages) held = min(left, kPageTokens);
-            if (a1 < (int)p.num_pages) held |= min(left - kPageTokens, kPageTokens) << 8;
-          }
-          load(&tk, true, head, a0, a1, (int)(tile0 + j), held);
+          if (FP8)
+            load8(true, head, a0, a1);
+          else
+            load(&tk, head, a0, a1);
         };
         load_k(0);
         load_q(head, token);
         if (two) {
           load_q(head, token + p.tile_tokens);
-          load(&tv, false, head, a0, a1, 0, 0);
+          load_v(head, a0, a1);
           for (int j = 1; j < n && ok; ++j) {
             load_k(j);
-            load(&tv, false, head, a0, a1, 0, 0);
+            load_v(head, a0, a1);
           }
         } else {
           if (n > 1) load_k(1);
           for (int j = 0; j < n && ok; ++j) {
             if (j + 1 < n)
-              load(&tv, false, head, b0, b1, 0, 0);
+              load_v(head, b0, b1);
             else
-              load(&tv, false, head, a0, a1, 0, 0);
+              load_v(head, a0, a1);
             if (j + 2 < n) load_k(j + 2);
           }
         }
@@ -898,12 +943,16 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
         }
       }
       // every copy has landed before the CTA leaves
-      constexpr uint32_t kRing = FP8 ? C::kRawStages : C::kStages;
-      uint64_t* full = FP8 ? sm->raw_full : sm->kv_full;
-      for (uint32_t i = n_kv > kRing ? n_kv - kRing : 0; i < n_kv; ++i)
-        mbar_wait(smem_u32(&full[i % kRing]), (i / kRing) & 1, nullptr);
-      for (uint32_t i = n_q > 2 ? n_q - 2 : 0; i < n_q; ++i)
-        mbar_wait(smem_u32(&sm->q_full[i & 1]), (i >> 1) & 1, nullptr);
+      auto landed = [&](uint64_t* full, uint32_t n, uint32_t ring) {
+        for (uint32_t i = n > ring ? n - ring : 0; i < n; ++i) mbar_wait(smem_u32(&full[i % ring]), (i / ring) & 1, nullptr);
+      };
+      if (FP8) {
+        landed(sm->kv_full, n_k, C::kKStages);
+        landed(sm->raw_full, n_v, C::kVRawStages);
+      } else {
+        landed(sm->kv_full, n_kv, C::kStages);
+      }
+      landed(sm->q_full, n_q, 2);
     } else if (warp < kAttnWalkWarp) {
       // ================================================================ MMA
       // A warp for each stream: products run in the order they are issued and
@@ -911,9 +960,9 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
       // the tensor core 150, a commit 115), so one stream's waits have to fall
       // into the other's products.
       const int x = warp - kAttnMmaWarp;
-      const uint32_t id_qk = idesc_16_f32(BF16, 128, 128, false);
+      const uint32_t id_qk = FP8 ? idesc_e4m3_f32(128, 128) : idesc_16_f32(BF16, 128, 128, false);
       const uint32_t id_pv = idesc_16_f32(BF16, 128, (uint32_t)p.D, true);
-      const uint32_t ksteps = (uint32_t)p.D / 16;
+      const uint32_t ksteps = FP8 ? (uint32_t)(p.D + 31) / 32 : (uint32_t)p.D / 16;
       uint32_t n_p = 0, kv0 = 0;  // probabilities so far; the ring's place before this item
       // Every place of the rings is waited for, in order, and given back: when
       // the products that read it are done, or at once where the tile is the
@@ -933,9 +982,22 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
         }
         return true;
       };
+      // E4M3 caches: K's and V's rings have a place for each key tile
+      uint32_t t_seen[2] = {0, 0};
+      auto tile_wait = [&](int v, uint32_t tile, int step) {
+        uint32_t& seen = t_seen[v];
+        while (seen <= tile) {
+          const uint32_t st = v ? C::kKStages + seen % C::kVStages : seen % C::kKStages;
+          if (!wait(&sm->kv_full[st], (seen / (v ? C::kVStages : C::kKStages)) & 1)) return false;
+          if (step == 2 && (int)((seen - kv0 / 2) & 1) != x && lane == 0) mbar_arrive(smem_u32(&sm->kv_empty[st]));
+          ++seen;
+        }
+        return true;
+      };
       auto q_wait = [&](uint32_t place, uint32_t own) {
+        uint64_t* full = FP8 ? sm->q_ready : sm->q_full;
         while (q_seen <= place) {
-          if (!wait(&sm->q_full[q_seen & 1], (q_seen >> 1) & 1)) return false;
+          if (!wait(&full[q_seen & 1], (q_seen >> 1) & 1)) return false;
           if (q_seen != own && lane == 0) mbar_arrive(smem_u32(&sm->q_empty[q_seen & 1]));
           ++q_seen;
         }
@@ -968,20 +1030,34 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
           end = ATTN_ITEM(seq) - (last < ATTN_ITEM(ns) ? last : last + ATTN_ITEM(skip)) * kAttnTile;
           if (!FP8 && end < kAttnTile && end % kPageTokens != 0) tail = n - 1;
         }
-        auto qk = [&](uint32_t place, int h) {  // 64 of the dimensions
-          if (lane == 0)
-            umma_f16_k64(tmem + attn_col_s(x), sw128_desc(q_s + (q & 1) * C::kTileBytes + h * 16384),
-                         sw128_desc(kv_s + place % C::kStages * C::kTileBytes + h * 16384), id_qk, h > 0, ksteps - 4 * h);
+        const uint32_t tile0 = kv0 / 2;
+        // half of Q K^T: 64 of the dimensions, or (E4M3) one of the queries' two terms
+        auto qk = [&](int j, int h) {
+          const uint32_t q_tile = q_s + (q & 1) * C::kTileBytes + h * 16384;
+          if (lane != 0) return;
+          if (FP8)
+            umma_f8_k128(tmem + attn_col_s(x), sw128_desc(q_tile),
+                         sw128_desc(kv_s + (tile0 + j) % C::kKStages * C::kRawBytes), id_qk, h > 0, ksteps);
+          else
+            umma_f16_k64(tmem + attn_col_s(x), sw128_desc(q_tile),
+                         sw128_desc(kv_s + (kv0 + attn_k_place(step, j)) % C::kStages * C::kTileBytes + h * 16384), id_qk,
+                         h > 0, ksteps - 4 * h);
         };
-        auto release = [&](uint32_t place) { commit(&sm->kv_empty[place % C::kStages]); };
+        auto k_wait = [&](int j) { return FP8 ? tile_wait(0, tile0 + j, step) : kv_wait(kv0 + attn_k_place(step, j), step, n); };
+        auto v_wait = [&](int j) { return FP8 ? tile_wait(1, tile0 + j, step) : kv_wait(kv0 + attn_v_place(step, j, n), step, n); };
+        auto k_release = [&](int j) {
+          commit(&sm->kv_empty[FP8 ? (tile0 + j) % C::kKStages : (kv0 + attn_k_place(step, j)) % C::kStages]);
+        };
+        auto v_release = [&](int j) {
+          commit(&sm->kv_empty[FP8 ? C::kKStages + (tile0 + j) % C::kVStages : (kv0 + attn_v_place(step, j, n)) % C::kStages]);
+        };
         if (from < n) {
           if (!q_wait(q, own)) return;
-          const uint32_t k = kv0 + attn_k_place(step, from);
-          if (!kv_wait(k, step, n)) return;
+          if (!k_wait(from)) return;
           tc_fence_after();
-          for (int h = 0; h < C::kHalves; ++h) qk(k, h);
+          for (int h = 0; h < C::kHalves; ++h) qk(from, h);
           commit(&sm->s_full[x]);
-          release(k);
+          k_release(from);
           if (from + step >= n) commit(&sm->q_empty[q & 1]);
         }
 #pragma unroll 1
@@ -992,9 +1068,9 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
             break;
           }
           const bool more = j + step < n;
-          const uint32_t v = kv0 + attn_v_place(step, j, n), k = kv0 + attn_k_place(step, j + step);
-          const uint32_t v_s = kv_s + v % C::kStages * C::kTileBytes;
-          if (!kv_wait(v, step, n)) return;
+          const uint32_t v_s = FP8 ? smem_u32(attn_smem) + C::kV + (tile0 + j) % C::kVStages * C::kTileBytes
+                                   : kv_s + (kv0 + attn_v_place(step, j, n)) % C::kStages * C::kTileBytes;
+          if (!v_wait(j)) return;
           if (j == tail) {
             // (in shared tiles each stream's warp writes the same zeros)
             const int to = end < kPageTokens ? kPageTokens : kAttnTile;
@@ -1005,11 +1081,11 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
             fence_proxy_async_smem();
             __syncwarp();
           }
-          if (!FP8 && more && !kv_wait(k, step, n)) return;
+          if (more && !k_wait(j + step)) return;
           if (!wait(&sm->p_full[x], n_p & 1)) return;
           ++n_p;
           if (FP8 && lane == 0) {  // the tile's scales have been used
-            const uint32_t bar = smem_u32(&sm->scale_empty[(kv0 / 2 + j) & 7]);
+            const uint32_t bar = smem_u32(&sm->scale_empty[(tile0 + j) & 7]);
             mbar_arrive(bar);
             if (step == 2) mbar_arrive(bar);
           }
@@ -1019,22 +1095,24 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
             umma_f16_ta_k128(tmem + attn_col_o(x), tmem + attn_col_s(x), sw128_desc_mn(v_s, 16384, 1024), id_pv,
                              j > from);
           if (more) {
-            // (the shorter ring of converted tiles has K after this stream's V)
-            if (FP8 && !kv_wait(k, step, n)) return;
             // the turn passes a few products early: the other warp wakes up meanwhile
-            if (C::kHalves == 2) qk(k, 0);
+            if (C::kHalves == 2) qk(j + step, 0);
             pass_turn();
-            qk(k, C::kHalves - 1);
+            qk(j + step, C::kHalves - 1);
             commit(&sm->s_full[x]);
-            release(k);
+            k_release(j + step);
             if (j + 2 * step >= n) commit(&sm->q_empty[q & 1]);
           } else {
             pass_turn();
             commit(&sm->o_full[x]);
           }
-          release(v);
+          v_release(j);
         }
-        if (q_wait(q0 + (step == 1 ? 1 : 0), own)) kv_wait(kv0 + 2 * n - 1, step, n);
+        if (!q_wait(q0 + (step == 1 ? 1 : 0), own)) return;
+        if (!FP8)
+          kv_wait(kv0 + 2 * n - 1, step, n);
+        else if (tile_wait(0, tile0 + n - 1, step))
+          tile_wait(1, tile0 + n - 1, step);
       };
       auto served = [&](uint32_t at, int n) {
         serve(at, n);
@@ -1050,48 +1128,83 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
       }
     } else if (FP8 && warp >= kAttnConvertWarp) {
       // ================================================================ converting
-      // E4M3 codes to BF16 (exactly), row by row into the 128-byte-swizzled
-      // layout that both products read.
-      const int tid = threadIdx.x - kAttnConvertWarp * 32;
-      constexpr uint32_t kRing = FP8 ? C::kRawStages : 1;
-      uint32_t n_kv = 0, tile0 = 0;
-      auto serve = [&](uint32_t at, int n) {
-        const int step = ATTN_ITEM(step);
-#pragma unroll 1
-        for (int i = 0; i < 2 * n; ++i, ++n_kv) {
-          const uint32_t rst = n_kv % kRing, st = n_kv % C::kStages;
-          if (!wait(&sm->raw_full[rst], (n_kv / kRing) & 1)) return;
-          const bool is_k = step == 1 ? (i & 1) == 0 : i == 0 || ((i & 1) && i != 2 * n - 1);
-          if (is_k) {
-            // scales: the softmax's own factor goes into those of K; tokens
-            // that their page does not hold get harmless ones
-            const int j = step == 1 || i == 0 ? i / 2 : (i + 1) / 2;
-            const uint32_t mine = scale_s + ((tile0 + j) & 7) * 1024 + tid * 4;
-            const int held = sm->held[rst] >> (tid & 64 ? 8 : 0) & 255;
-            const bool good = (tid & 63) < held;
-            sts_u32(mine, good ? __float_as_uint(fmaxf(__uint_as_float(lds_u32(mine)) * p.scale_log2, 1e-37f))
-                               : __float_as_uint(1.0f));
-            if (!good) sts_u32(mine + 512, 0u);
-          }
-          if (n_kv >= C::kStages && !wait(&sm->kv_empty[st], (n_kv / C::kStages - 1) & 1)) return;
-          const uint32_t src = raw_s + rst * C::kRawBytes, dst = kv_s + st * C::kTileBytes;
+      const int cw = warp - kAttnConvertWarp, tid = cw * 32 + lane;
+      uint32_t tile0 = 0;
+      // A query tile in place: each row, scaled by a power of two to a maximum
+      // in [128, 256), as the sum of two E4M3 terms (8 significant bits as two
+      // times 4: exact but for elements under 2^-9 of the row's maximum, which
+      // are off by 2^-18 of it at most).  So Q K^T needs no conversion of K:
+      // two products with its codes cost what one in 16 bits does.
+      auto split_q = [&](uint32_t place, int rows) {
+        if (!wait(&sm->q_full[place & 1], (place >> 1) & 1)) return false;
+        const uint32_t tile = q_s + (place & 1) * C::kTileBytes;
 #pragma unroll 2
-          for (int u = tid; u < C::kRawBytes / 16; u += 128) {
-            const int row = u / (DP / 16), cc = u % (DP / 16);  // 16 codes: 32 bytes of a row's half cc / 4
-            const uint4 v = lds_v4(src + u * 16);
-            uint4 lo, hi;
-            e4m3_to_bf16(v.x, &lo.x, &lo.y);
-            e4m3_to_bf16(v.y, &lo.z, &lo.w);
-            e4m3_to_bf16(v.z, &hi.x, &hi.y);
-            e4m3_to_bf16(v.w, &hi.z, &hi.w);
-            const uint32_t to = dst + (cc / 4) * 16384 + row * 128, unit = 2 * (cc & 3);
-            sts_v4(to + ((unit ^ (row & 7)) << 4), lo);
-            sts_v4(to + (((unit + 1) ^ (row & 7)) << 4), hi);
+        for (int r = cw; r < rows; r += 4) {
+          // a lane's 4 elements
+          const uint2 w = lds_v2(tile + (lane / 16) * 16384 + r * 128 + (((lane % 16 / 2) ^ (r & 7)) << 4) + 8 * (lane & 1));
+          float f[4] = {__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
+                        __uint_as_float(w.y & 0xFFFF0000u)};
+          float top = fmaxf(fmaxf(fabsf(f[0]), fabsf(f[1])), fmaxf(fabsf(f[2]), fabsf(f[3])));
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          const uint32_t e = min(max(__float_as_uint(top) >> 23, 8u), 254u);
+          const float up = __uint_as_float((261u - e) << 23);  // 2^(7 - exponent)
+          uint32_t c1 = 0, c2 = 0;
+#pragma unroll
+          for (int i = 0; i < 4; i += 2) {
+            const float2 v = make_float2(f[i] * up, f[i + 1] * up);
+            const uint32_t a = __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
+            const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)a, __NV_E4M3);
+            const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&h));
+            const uint32_t b = __nv_cvt_float2_to_fp8x2(make_float2(v.x - g.x, v.y - g.y), __NV_SATFINITE, __NV_E4M3);
+            c1 |= (a & 0xFFFFu) << (8 * i);
+            c2 |= (b & 0xFFFFu) << (8 * i);
+          }
+          __syncwarp();  // the whole row has been read
+          const uint32_t to = tile + r * 128 + (((lane / 4) ^ (r & 7)) << 4) + 4 * (lane & 3);
+          sts_u32(to, c1);
+          sts_u32(to + 16384, c2);
+          if (lane == 0) sts_u32(factor_s + ((place & 1) * 128 + r) * 4, (e - 7u) << 23);  // 2^(exponent - 7)
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm->q_ready[place & 1]));
+        return true;
+      };
+      const int units = p.D / 16;  // of a row
+      auto serve = [&](uint32_t at, int n) {
+        const int ntok = ATTN_ITEM(ntok);
+        const uint32_t q0 = ATTN_ITEM(q0);
+        if (!split_q(q0, min(ntok, p.tile_tokens) * p.group)) return;
+        if (ATTN_ITEM(two) && !split_q(q0 + 1, (ntok - p.tile_tokens) * p.group)) return;
+        // V's codes to BF16 (exactly), into the layout that its product reads
+#pragma unroll 1
+        for (uint32_t t = tile0; t < tile0 + n; ++t) {
+          const uint32_t rst = t % C::kVRawStages, st = t % C::kVStages;
+          if (!wait(&sm->raw_full[rst], (t / C::kVRawStages) & 1)) return;
+          if (t >= C::kVStages && !wait(&sm->kv_empty[C::kKStages + st], (t / C::kVStages - 1) & 1)) return;
+          const uint32_t src = smem_u32(attn_smem) + C::kVRaw + rst * C::kRawBytes;
+          const uint32_t dst = smem_u32(attn_smem) + C::kV + st * C::kTileBytes;
+          const int cc = tid & 7;  // 16 codes: 32 bytes of a row's half cc / 4
+          const uint32_t unit = 2 * (cc & 3);
+          if (cc < units) {
+#pragma unroll 4
+            for (int row = tid >> 3; row < 128; row += 16) {
+              const uint4 v = lds_v4(src + row * 128 + cc * 16);
+              uint4 lo, hi;
+              e4m3_to_bf16(v.x, &lo.x, &lo.y);
+              e4m3_to_bf16(v.y, &lo.z, &lo.w);
+              e4m3_to_bf16(v.z, &hi.x, &hi.y);
+              e4m3_to_bf16(v.w, &hi.z, &hi.w);
+              const uint32_t to = dst + (cc / 4) * 16384 + row * 128;
+              sts_v4(to + ((unit ^ (row & 7)) << 4), lo);
+              sts_v4(to + (((unit + 1) ^ (row & 7)) << 4), hi);
+            }
           }
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            mbar_arrive(smem_u32(&sm->kv_full[st]));
+            mbar_arrive(smem_u32(&sm->kv_full[C::kKStages + st]));
             mbar_arrive(smem_u32(&sm->raw_empty[rst]));
           }
         }

@@ -298,6 +298,23 @@ __device__ __forceinline__ void umma_f16_k64(uint32_t d_tmem, uint64_t adesc, ui
       : "memory");
 }
 
+// The same for 8-bit operands (kind::f8f6f4), K steps of 32.
+__device__ __forceinline__ void umma_f8_k128(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                             uint32_t idesc, uint32_t accumulate, uint32_t steps) {
+  asm volatile(
+      "{\n\t.reg .pred on, acc, all;\n\t.reg .b64 a, b;\n\t"
+      "setp.eq.u32 all, 0, 0;\n\tsetp.ne.u32 acc, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, acc;\n\t"
+      "setp.gt.u32 on, %5, 1;\n\tadd.s64 a, %1, 2;\n\tadd.s64 b, %2, 2;\n\t"
+      "@on tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, all;\n\t"
+      "setp.gt.u32 on, %5, 2;\n\tadd.s64 a, %1, 4;\n\tadd.s64 b, %2, 4;\n\t"
+      "@on tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, all;\n\t"
+      "setp.gt.u32 on, %5, 3;\n\tadd.s64 a, %1, 6;\n\tadd.s64 b, %2, 6;\n\t"
+      "@on tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, all;\n\t"
+      "}" ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(steps)
+      : "memory");
+}
+
 // D[tmem] (+)= A[tmem] * B[smem] over 8 K steps of 16 (A's first 64 elements in
 // columns 0 to 31, the others in 64 to 95), B MN-major in the 128-byte swizzle
 // layout.

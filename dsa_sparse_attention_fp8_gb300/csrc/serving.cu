@@ -126,15 +126,15 @@ int launch_attention(const dsa::AttnParams& p, int grid, cudaStream_t st) {
   const int64_t qd[3] = {p.D, p.Hq, p.T}, qs[2] = {p.q_head * 2, p.q_token * 2};
   const int qb[3] = {64, p.group, p.tile_tokens};
   if (const int rc = make_map(&tq, "q", type, 2, p.q, 3, qd, qs, qb, true)) return rc;
-  // a 16-bit page comes in two boxes of 64 dimensions (128-byte rows), an
-  // E4M3 page in one
+  // boxes are 128 bytes wide: 64 16-bit dimensions, 128 E4M3 codes (zeros past
+  // the head's); V's codes are converted from plain rows
   const int64_t kd[4] = {p.D, p.Hkv, DSA_PAGE_TOKENS, p.num_pages};
-  const int kb[4] = {FP8 ? DP : 64, 1, DSA_PAGE_TOKENS, 1};
+  const int kb[4] = {FP8 ? 128 : 64, 1, DSA_PAGE_TOKENS, 1};
   const char* const names[2] = {"k_cache", "v_cache"};
   for (int i = 0; i < 2; ++i) {
     const int64_t ks[3] = {p.head_stride[i], p.token_stride[i], p.page_stride[i]};
     if (const int rc = make_map(&tkv[i], names[i], FP8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : type, FP8 ? 1 : 2, p.cache[i],
-                                4, kd, ks, kb, !FP8))
+                                4, kd, ks, kb, !FP8 || i == 0))
       return rc;
   }
   dsa::paged_attention_kernel<DP, BF16, FP8><<<grid, C::kThreads, C::kSmem, st>>>(tq, tkv[0], tkv[1], p);
@@ -301,7 +301,7 @@ int dsa_paged_attention(const void* q, int64_t q_token_stride, int64_t q_head_st
   const cudaStream_t st = (cudaStream_t)stream;
   const bool wide = p.D > 64;
   if (cache->type == DSA_TYPE_E4M3)
-    return wide ? launch_attention<128, true, true>(p, grid, st) : launch_attention<64, true, true>(p, grid, st);
+    return launch_attention<128, true, true>(p, grid, st);
   if (type == DSA_TYPE_BF16)
     return wide ? launch_attention<128, true, false>(p, grid, st) : launch_attention<64, true, false>(p, grid, st);
   return wide ? launch_attention<128, false, false>(p, grid, st) : launch_attention<64, false, false>(p, grid, st);
