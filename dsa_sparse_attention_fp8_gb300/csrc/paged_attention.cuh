@@ -211,16 +211,6 @@ __device__ __forceinline__ uint32_t attn_v_place(int step, int j, int n) {
 __device__ __forceinline__ uint32_t attn_col_s(int x) { return (uint32_t)x * 128; }
 __device__ __forceinline__ uint32_t attn_col_o(int x) { return 256u + (uint32_t)x * 128; }
 
-template <bool BF16>
-__device__ __forceinline__ uint32_t attn_pack(float lo, float hi) {
-  if (BF16) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
-  }
-  const __half2 v = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-
 // Finds where this CTA's share of the work begins: every CTA sums the
 // requests' costs itself (a thread per request, a warp together for requests
 // of several units).  Called by all threads; the result is in shared memory.
@@ -332,14 +322,24 @@ __device__ __forceinline__ void attn_locate(const AttnParams& p, AttnSmem* sm, i
   }
 }
 
-// Four E4M3 codes as BF16, exactly: exponent and mantissa moved to their places
-// (a value 2^-120 as large, subnormals included), times 2^120.  The NaN codes
-// become +-480: what no row sees may be anything, but has to be finite.
+template <bool BF16>
+__device__ __forceinline__ uint32_t attn_pack(float lo, float hi) {
+  if (BF16) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Four E4M3 codes as BF16, exactly (through FP16, which holds them all).
 __device__ __forceinline__ void e4m3_to_bf16(uint32_t codes, uint32_t* lo, uint32_t* hi) {
-  const uint32_t a = __byte_perm(codes, 0u, 0x1404), b = __byte_perm(codes, 0u, 0x3424);  // a code in each upper byte
-  const uint32_t x = (a & 0x80008000u) | ((a & 0x7F007F00u) >> 4), y = (b & 0x80008000u) | ((b & 0x7F007F00u) >> 4);
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(*lo) : "r"(x), "r"(0x7B807B80u));
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(*hi) : "r"(y), "r"(0x7B807B80u));
+  const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(codes & 0xFFFFu), __NV_E4M3);
+  const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(codes >> 16), __NV_E4M3);
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&a));
+  const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&b));
+  *lo = attn_pack<true>(f.x, f.y);
+  *hi = attn_pack<true>(g.x, g.y);
 }
 
 // Which of 32 keys a row sees, as bits: key i of them lies i - `back` tokens
@@ -548,6 +548,7 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
             // E4M3 caches: this tile's scales; those past the request's end may
             // be anything (each warp puts numbers there before it reads them)
             const uint32_t scales = scale_s + ((tile0 + j) & 7) * 1024;
+            const ulonglong2* k_scale = reinterpret_cast<const ulonglong2*>(attn_smem + C::kScale + ((tile0 + j) & 7) * 1024);
             if (FP8 && s0 + kAttnTile > seq) {
               for (int i = max(seq - s0, 0) + lane; i < kAttnTile; i += 32) {
                 sts_u32(scales + 4 * i, __float_as_uint(1.0f));
@@ -585,31 +586,35 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
 #pragma unroll
                 for (int c = 0; c < kAttnTile; c += 32) {
                   uint32_t v[32];
+                  ulonglong2 ks[8];  // scales of 4 keys each
                   tmem_ld<32>(base + c, v);
+                  if (FP8) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) ks[i] = k_scale[c / 4 + i];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                      ks[i].x = mul2(ks[i].x, mul);
+                      ks[i].y = mul2(ks[i].y, mul);
+                    }
+                  }
                   tmem_ld_wait32(v);
 #pragma unroll
-                  for (int i = 0; i < 16; i += 2) {
-                    uint64_t ks0 = mul, ks1 = mul, e0, e1;
-                    if (FP8) {
-                      lds_2x64(scales + 4 * (c + 2 * i), &ks0, &ks1);
-                      ks0 = mul2(ks0, mul);
-                      ks1 = mul2(ks1, mul);
-                    }
-                    const float2 z0 = unpack2(fma2(pack2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), ks0, sub));
-                    const float2 z1 = unpack2(fma2(pack2(__uint_as_float(v[2 * i + 2]), __uint_as_float(v[2 * i + 3])), ks1, sub));
-                    e0 = pack2(ex2(z0.x), ex2(z0.y));
-                    e1 = pack2(ex2(z1.x), ex2(z1.y));
+                  for (int i = 0; i < 32; i += 4) {
+                    const float2 z0 = unpack2(fma2(pack2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])),
+                                                   FP8 ? ks[i / 4].x : mul, sub));
+                    const float2 z1 = unpack2(fma2(pack2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3])),
+                                                   FP8 ? ks[i / 4].y : mul, sub));
+                    uint64_t e0 = pack2(ex2(z0.x), ex2(z0.y)), e1 = pack2(ex2(z1.x), ex2(z1.y));
                     sums[0] = add2(sums[0], e0);
                     sums[1] = add2(sums[1], e1);
                     if (FP8) {
-                      uint64_t vs0, vs1;
-                      lds_2x64(scales + 512 + 4 * (c + 2 * i), &vs0, &vs1);
-                      e0 = mul2(e0, vs0);
-                      e1 = mul2(e1, vs1);
+                      const ulonglong2 vs = k_scale[32 + (c + i) / 4];  // V's
+                      e0 = mul2(e0, vs.x);
+                      e1 = mul2(e1, vs.y);
                     }
                     const float2 p0 = unpack2(e0), p1 = unpack2(e1);
-                    pr[c / 2 + i] = attn_pack<BF16>(p0.x, p0.y);
-                    pr[c / 2 + i + 1] = attn_pack<BF16>(p1.x, p1.y);
+                    pr[(c + i) / 2] = attn_pack<BF16>(p0.x, p0.y);
+                    pr[(c + i) / 2 + 1] = attn_pack<BF16>(p1.x, p1.y);
                   }
                 }
                 const float2 t = unpack2(add2(sums[0], sums[1]));
@@ -628,9 +633,8 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
                   float a = __uint_as_float(v[i]), b = __uint_as_float(v[i + 1]);
                   float d = __uint_as_float(v[i + 2]), g = __uint_as_float(v[i + 3]);
                   if (FP8) {
-                    uint64_t ks0, ks1;
-                    lds_2x64(scales + 4 * (c + i), &ks0, &ks1);
-                    const float2 z0 = unpack2(mul2(pack2(a, b), ks0)), z1 = unpack2(mul2(pack2(d, g), ks1));
+                    const ulonglong2 ks = k_scale[(c + i) / 4];
+                    const float2 z0 = unpack2(mul2(pack2(a, b), ks.x)), z1 = unpack2(mul2(pack2(d, g), ks.y));
                     a = z0.x, b = z0.y, d = z1.x, g = z1.y;
                   }
                   top = max3(max3(top, a, b), d, g);
@@ -1185,13 +1189,16 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
           if (t >= C::kVStages && !wait(&sm->kv_empty[C::kKStages + st], (t / C::kVStages - 1) & 1)) return;
           const uint32_t src = smem_u32(attn_smem) + C::kVRaw + rst * C::kRawBytes;
           const uint32_t dst = smem_u32(attn_smem) + C::kV + st * C::kTileBytes;
+          // rows past the request's end may be anything, NaN too: zeros
+          const int jj = ATTN_ITEM(j0) + (int)(t - tile0);
+          const int end = ATTN_ITEM(seq) - (jj < ATTN_ITEM(ns) ? jj : jj + ATTN_ITEM(skip)) * kAttnTile;
           const int cc = tid & 7;  // 16 codes: 32 bytes of a row's half cc / 4
           const uint32_t unit = 2 * (cc & 3);
           if (cc < units) {
 #pragma unroll 4
             for (int row = tid >> 3; row < 128; row += 16) {
-              const uint4 v = lds_v4(src + row * 128 + cc * 16);
-              uint4 lo, hi;
+              uint4 v = lds_v4(src + row * 128 + cc * 16), lo, hi;
+              if (row >= end) v = make_uint4(0, 0, 0, 0);
               e4m3_to_bf16(v.x, &lo.x, &lo.y);
               e4m3_to_bf16(v.y, &lo.z, &lo.w);
               e4m3_to_bf16(v.z, &hi.x, &hi.y);

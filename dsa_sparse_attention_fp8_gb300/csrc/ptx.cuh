@@ -37,9 +37,6 @@ __device__ __forceinline__ uint4 lds_v4(uint32_t a) {
                : "r"(a));
   return v;
 }
-__device__ __forceinline__ void lds_2x64(uint32_t a, uint64_t* x, uint64_t* y) {
-  asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(*x), "=l"(*y) : "r"(a));
-}
 __device__ __forceinline__ void sts_v4(uint32_t a, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z),
                "r"(v.w)
