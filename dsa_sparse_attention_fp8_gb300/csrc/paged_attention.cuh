@@ -56,6 +56,7 @@ constexpr int kAttnMaxGrid = 160;
 // its last rescale; a tile whose probabilities add up to more than this
 // gets a new m (FP16 holds 65,504).
 constexpr float kAttnMostSum = 16384.0f;
+constexpr float kAttnRescaleLog2 = 8.0f;  // (with E4M3 caches: when the maximum grows by more than 2^8)
 constexpr int64_t kAttnMaxShare = 1 << 23;  // cost of a CTA's work, in 32 bits
 constexpr int kAttnUnitCharge = 1;    // a unit's set-up, in key tiles
 
@@ -571,57 +572,8 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
               }
               tmem_st_wait();
             }
-            // One pass with the maximum that the row has: the probabilities
-            // stay in registers until their sum says that it will do.  If not
-            // (on each row's first tile, and few after it) the row gets the
-            // right one first: the scores are still there.
-            uint32_t pr[64];
-            float sum;
-            bool ready = !__any_sync(0xffffffffu, m == -INFINITY);
-            for (int pass = 0;; ++pass) {
-              if (ready) {
-                const float shift = m == -INFINITY ? 0.f : -m;
-                const uint64_t mul = pack2(factor, factor), sub = pack2(shift, shift);
-                uint64_t sums[2] = {0, 0};
-#pragma unroll
-                for (int c = 0; c < kAttnTile; c += 32) {
-                  uint32_t v[32];
-                  ulonglong2 ks[8];  // scales of 4 keys each
-                  tmem_ld<32>(base + c, v);
-                  if (FP8) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) ks[i] = k_scale[c / 4 + i];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                      ks[i].x = mul2(ks[i].x, mul);
-                      ks[i].y = mul2(ks[i].y, mul);
-                    }
-                  }
-                  tmem_ld_wait32(v);
-#pragma unroll
-                  for (int i = 0; i < 32; i += 4) {
-                    const float2 z0 = unpack2(fma2(pack2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])),
-                                                   FP8 ? ks[i / 4].x : mul, sub));
-                    const float2 z1 = unpack2(fma2(pack2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3])),
-                                                   FP8 ? ks[i / 4].y : mul, sub));
-                    uint64_t e0 = pack2(ex2(z0.x), ex2(z0.y)), e1 = pack2(ex2(z1.x), ex2(z1.y));
-                    sums[0] = add2(sums[0], e0);
-                    sums[1] = add2(sums[1], e1);
-                    if (FP8) {
-                      const ulonglong2 vs = k_scale[32 + (c + i) / 4];  // V's
-                      e0 = mul2(e0, vs.x);
-                      e1 = mul2(e1, vs.y);
-                    }
-                    const float2 p0 = unpack2(e0), p1 = unpack2(e1);
-                    pr[(c + i) / 2] = attn_pack<BF16>(p0.x, p0.y);
-                    pr[(c + i) / 2 + 1] = attn_pack<BF16>(p1.x, p1.y);
-                  }
-                }
-                const float2 t = unpack2(add2(sums[0], sums[1]));
-                sum = t.x + t.y;
-                if (!__any_sync(0xffffffffu, pass == 0 && !(sum <= kAttnMostSum))) break;
-              }
-              ready = true;
+            // the scores' maximum
+            auto maximum = [&]() {
               float top = -INFINITY;
 #pragma unroll 1
               for (int c = 0; c < kAttnTile; c += 32) {
@@ -640,8 +592,11 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
                   top = max3(max3(top, a, b), d, g);
                 }
               }
-              top *= factor;
-              const bool grow = top > m;
+              return top * factor;
+            };
+            // the row's maximum becomes `top` where that is larger and `wanted`
+            auto raise = [&](float top, bool wanted) {
+              const bool grow = wanted && top > m;
               if (__any_sync(0xffffffffu, m != -INFINITY)) {  // (else there is no output yet, or zeros)
                 // the scores' arrival says that the stream's previous product is done
                 const float a = grow && m != -INFINITY ? ex2(m - top) : 1.0f;
@@ -657,12 +612,79 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
                 l *= a;
               }
               if (grow) m = top;
+            };
+            // probabilities of the 32 keys at c: packed, and added to sums
+            uint64_t sums[2];
+            auto probabilities = [&](int c, uint32_t* pr) {
+              const float shift = m == -INFINITY ? 0.f : -m;
+              const uint64_t mul = pack2(factor, factor), sub = pack2(shift, shift);
+              uint32_t v[32];
+              tmem_ld<32>(base + c, v);
+              tmem_ld_wait32(v);
+#pragma unroll
+              for (int i = 0; i < 32; i += 4) {
+                ulonglong2 ks = make_ulonglong2(mul, mul);
+                if (FP8) {
+                  ks = k_scale[(c + i) / 4];
+                  ks.x = mul2(ks.x, mul);
+                  ks.y = mul2(ks.y, mul);
+                }
+                const float2 z0 = unpack2(fma2(pack2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), ks.x, sub));
+                const float2 z1 = unpack2(fma2(pack2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3])), ks.y, sub));
+                uint64_t e0 = pack2(ex2(z0.x), ex2(z0.y)), e1 = pack2(ex2(z1.x), ex2(z1.y));
+                sums[0] = add2(sums[0], e0);
+                sums[1] = add2(sums[1], e1);
+                if (FP8) {
+                  const ulonglong2 vs = k_scale[32 + (c + i) / 4];  // V's
+                  e0 = mul2(e0, vs.x);
+                  e1 = mul2(e1, vs.y);
+                }
+                const float2 p0 = unpack2(e0), p1 = unpack2(e1);
+                pr[i / 2] = attn_pack<BF16>(p0.x, p0.y);
+                pr[i / 2 + 1] = attn_pack<BF16>(p1.x, p1.y);
+              }
+            };
+            // Probabilities go over scores that this thread has read: those of
+            // 64 keys in the first 32 of their columns.
+            float sum;
+            if constexpr (FP8) {
+              // the maximum first, then loops that are not unrolled: with the
+              // scales' arithmetic the other form's code (below) is fetched
+              // more slowly than it runs (4,400 cycles a tile)
+              const float top = maximum();
+              if (__any_sync(0xffffffffu, top > m + kAttnRescaleLog2)) raise(top, top > m + kAttnRescaleLog2);
+              sums[0] = sums[1] = 0;
+#pragma unroll 1
+              for (int c = 0; c < kAttnTile; c += 32) {
+                uint32_t pr[16];
+                probabilities(c, pr);
+                tmem_st<16>(base + (c & 64) + (c & 32) / 2, pr);
+              }
+              const float2 t = unpack2(add2(sums[0], sums[1]));
+              sum = t.x + t.y;
+            } else {
+              // One pass with the maximum that the row has: the probabilities
+              // stay in registers until their sum says that it will do.  If
+              // not (on each row's first tile, and few after it) the row gets
+              // the right one first: the scores are still there.
+              uint32_t pr[64];
+              bool ready = !__any_sync(0xffffffffu, m == -INFINITY);
+              for (int pass = 0;; ++pass) {
+                if (ready) {
+                  sums[0] = sums[1] = 0;
+#pragma unroll
+                  for (int c = 0; c < kAttnTile; c += 32) probabilities(c, pr + c / 2);
+                  const float2 t = unpack2(add2(sums[0], sums[1]));
+                  sum = t.x + t.y;
+                  if (!__any_sync(0xffffffffu, pass == 0 && !(sum <= kAttnMostSum))) break;
+                }
+                raise(maximum(), true);
+                ready = true;
+              }
+              tmem_st<32>(base, pr);
+              tmem_st<32>(base + 64, pr + 32);
             }
             l += sum;
-            // over scores that this thread has read: those of 64 keys in the
-            // first 32 of their columns
-            tmem_st<32>(base, pr);
-            tmem_st<32>(base + 64, pr + 32);
             tmem_st_wait();
             tc_fence_before();
           }
@@ -798,15 +820,12 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
         const uint32_t st = n_kv % C::kStages, round = n_kv / C::kStages;
         if (round > 0) wait(&sm->kv_empty[st], (round - 1) & 1);
         if (!ok) return;
-        if (lane == 0) {
-          const uint32_t bar = smem_u32(&sm->kv_full[st]), dst = kv_s + st * C::kTileBytes;
-          mbar_arrive_expect_tx(bar, C::kTileBytes);
-#pragma unroll
-          for (int h = 0; h < C::kHalves; ++h) {
-            tma_load_4d(dst + h * 16384, map, h * 64, head, 0, page0, bar);
-            tma_load_4d(dst + h * 16384 + 8192, map, h * 64, head, 0, page1, bar);
-          }
-        }
+        // (a copy costs its issuing thread some 150 cycles: a lane for each)
+        const uint32_t bar = smem_u32(&sm->kv_full[st]), dst = kv_s + st * C::kTileBytes;
+        if (lane == 0) mbar_arrive_expect_tx(bar, C::kTileBytes);
+        __syncwarp();
+        if (lane < 2 * C::kHalves)
+          tma_load_4d(dst + lane * 8192, map, (lane >> 1) * 64, head, 0, lane & 1 ? page1 : page0, bar);
         __syncwarp();
         ++n_kv;
       };
@@ -821,23 +840,17 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
           if (is_k) --n_k; else --n_v;
           return;
         }
-        if (lane == 0) {
-          const uint32_t bar = smem_u32(is_k ? &sm->kv_full[st] : &sm->raw_full[st]);
-          const uint32_t dst = smem_u32(attn_smem) + (is_k ? C::kKv : C::kVRaw) + st * C::kRawBytes;
-          const int none = (int)p.num_pages;
-          const uint32_t held = is_k ? (page0 < none) + (page1 < none) : 0;
-          mbar_arrive_expect_tx(bar, C::kRawBytes + held * 512);
-          tma_load_4d(dst, is_k ? &tk : &tv, 0, head, 0, page0, bar);
-          tma_load_4d(dst + 8192, is_k ? &tk : &tv, 0, head, 0, page1, bar);
-          if (is_k) {
-#pragma unroll
-            for (int w = 0; w < 2; ++w) {
-              const uint32_t to = scale_s + (t & 7) * 1024 + w * 512;
-              const float* from = p.scale[w] + (int64_t)head * p.scale_head[w];
-              if (page0 < none) bulk_load(to, from + page0 * p.scale_page[w], 256, bar);
-              if (page1 < none) bulk_load(to + 256, from + page1 * p.scale_page[w], 256, bar);
-            }
-          }
+        const uint32_t bar = smem_u32(is_k ? &sm->kv_full[st] : &sm->raw_full[st]);
+        const uint32_t dst = smem_u32(attn_smem) + (is_k ? C::kKv : C::kVRaw) + st * C::kRawBytes;
+        const int none = (int)p.num_pages, page = lane & 1 ? page1 : page0;
+        const uint32_t held = is_k ? (page0 < none) + (page1 < none) : 0;
+        if (lane == 0) mbar_arrive_expect_tx(bar, C::kRawBytes + held * 512);
+        __syncwarp();
+        if (lane < 2) tma_load_4d(dst + lane * 8192, is_k ? &tk : &tv, 0, head, 0, page, bar);
+        if (is_k && lane < 4 && page < none) {
+          const int w = lane >> 1;
+          bulk_load(scale_s + (t & 7) * 1024 + w * 512 + (lane & 1) * 256,
+                    p.scale[w] + (int64_t)head * p.scale_head[w] + page * p.scale_page[w], 256, bar);
         }
         __syncwarp();
       };
@@ -1195,17 +1208,24 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
           const int cc = tid & 7;  // 16 codes: 32 bytes of a row's half cc / 4
           const uint32_t unit = 2 * (cc & 3);
           if (cc < units) {
-#pragma unroll 4
-            for (int row = tid >> 3; row < 128; row += 16) {
-              uint4 v = lds_v4(src + row * 128 + cc * 16), lo, hi;
-              if (row >= end) v = make_uint4(0, 0, 0, 0);
-              e4m3_to_bf16(v.x, &lo.x, &lo.y);
-              e4m3_to_bf16(v.y, &lo.z, &lo.w);
-              e4m3_to_bf16(v.z, &hi.x, &hi.y);
-              e4m3_to_bf16(v.w, &hi.z, &hi.w);
-              const uint32_t to = dst + (cc / 4) * 16384 + row * 128;
-              sts_v4(to + ((unit ^ (row & 7)) << 4), lo);
-              sts_v4(to + (((unit + 1) ^ (row & 7)) << 4), hi);
+#pragma unroll 1
+            for (int r0 = tid >> 3; r0 < 128; r0 += 64) {
+              uint4 v[4];  // loaded ahead of the stores
+#pragma unroll
+              for (int i = 0; i < 4; ++i) v[i] = lds_v4(src + (r0 + 16 * i) * 128 + cc * 16);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int row = r0 + 16 * i;
+                uint4 lo, hi;
+                if (row >= end) v[i] = make_uint4(0, 0, 0, 0);
+                e4m3_to_bf16(v[i].x, &lo.x, &lo.y);
+                e4m3_to_bf16(v[i].y, &lo.z, &lo.w);
+                e4m3_to_bf16(v[i].z, &hi.x, &hi.y);
+                e4m3_to_bf16(v[i].w, &hi.z, &hi.w);
+                const uint32_t to = dst + (cc / 4) * 16384 + row * 128;
+                sts_v4(to + ((unit ^ (row & 7)) << 4), lo);
+                sts_v4(to + (((unit + 1) ^ (row & 7)) << 4), hi);
+              }
             }
           }
           fence_proxy_async_smem();
