@@ -60,20 +60,33 @@ constexpr float kAttnRescaleLog2 = 8.0f;  // (with E4M3 caches: when the maximum
 constexpr int64_t kAttnMaxShare = 1 << 23;  // cost of a CTA's work, in 32 bits
 constexpr int kAttnUnitCharge = 1;    // a unit's set-up, in key tiles
 
-// A unit of work: up to two query tiles (2 * tile_tokens tokens) of one
-// request and key head, over the key tiles that any of its rows sees: the
-// first `ns` tiles (sinks), then those from `lo` on.
+// A unit of work: the query rows of one request that two streams of 128 rows
+// take at a time, over the key tiles that any of its rows sees: the first `ns`
+// tiles (sinks), then those from `lo` on.
+enum AttnKind : int {
+  kOneTile = 0,   // one query tile of one key head: the streams take turns at the key tiles
+  kTwoTiles = 1,  // two query tiles of one key head: a stream each, the same key tiles
+  kTwoHeads = 2,  // a query tile each of two neighbouring key heads: a stream each, its head's key tiles
+};
 struct AttnUnit {
+  int kind;
   int ntok;      // tokens
   int p0;        // position of the first
   int lo, ns, n; // first window tile, sink tiles before it, tiles in all
-  int weight;    // cost of a key tile
+  __device__ __forceinline__ int weight() const { return kind == kOneTile ? 1 : 2; }  // cost of a key tile
+  __device__ __forceinline__ int cost() const;
 };
 
-__device__ __forceinline__ AttnUnit attn_unit(const AttnParams& p, int q, int seq, int u) {
+// Requests of at most one query tile take their key heads in pairs: a page's
+// rows of two neighbouring heads lie next to each other, and DRAM gives twice
+// the bytes of an E4M3 row for the same effort.
+__device__ __forceinline__ bool attn_pairs(const AttnParams& p, int q) { return q <= p.tile_tokens && p.Hkv > 1; }
+
+__device__ __forceinline__ AttnUnit attn_unit(const AttnParams& p, int q, int seq, int u, int head) {
   AttnUnit x;
   const int t0 = u * 2 * p.tile_tokens;
   x.ntok = min(2 * p.tile_tokens, q - t0);
+  x.kind = x.ntok > p.tile_tokens ? kTwoTiles : attn_pairs(p, q) && head + 1 < p.Hkv ? kTwoHeads : kOneTile;
   x.p0 = seq - q + t0;
   x.lo = 0;
   x.ns = 0;
@@ -82,7 +95,6 @@ __device__ __forceinline__ AttnUnit attn_unit(const AttnParams& p, int q, int se
     x.ns = min(p.sink_tiles, x.lo);
   }
   x.n = x.ns + (x.p0 + x.ntok - 1) / kAttnTile + 1 - x.lo;
-  x.weight = x.ntok > p.tile_tokens ? 2 : 1;
   return x;
 }
 
@@ -96,6 +108,8 @@ __device__ __forceinline__ bool attn_request(const AttnParams& p, int r, int* ro
   *q = ok ? s1 - s0 : 0;
   return ok;
 }
+
+__device__ __forceinline__ int AttnUnit::cost() const { return (n + kAttnUnitCharge) * weight(); }
 
 __device__ __forceinline__ int attn_units(const AttnParams& p, int q) {
   return (q + 2 * p.tile_tokens - 1) / (2 * p.tile_tokens);
@@ -113,18 +127,20 @@ struct AttnWalk {
   int j0, j1;    // this CTA's key tiles of the unit
 
   __device__ __forceinline__ void enter(const AttnParams& p) {
-    unit = attn_unit(p, q, seq, u);
+    unit = attn_unit(p, q, seq, u, head);
     // tile j lies at s + (charge + j) * weight
-    j0 = s >= 0 ? 0 : max(0, (unit.weight - 1 - s) / unit.weight - kAttnUnitCharge);
-    j1 = min(unit.n, (len - s + unit.weight - 1) / unit.weight - kAttnUnitCharge);
+    const int w = unit.weight();
+    j0 = s >= 0 ? 0 : max(0, (w - 1 - s) / w - kAttnUnitCharge);
+    j1 = min(unit.n, (len - s + w - 1) / w - kAttnUnitCharge);
   }
   __device__ __forceinline__ bool inside() const { return s < len; }
   __device__ __forceinline__ void next(const AttnParams& p) {
-    s += (unit.n + kAttnUnitCharge) * unit.weight;
+    s += unit.cost();
     if (s >= len) return;
     if (++u == nu) {
       u = 0;
-      if (++head == p.Hkv) {
+      head += unit.kind == kTwoHeads ? 2 : 1;
+      if (head == p.Hkv) {
         head = 0;
         do {
           ++r;  // there is one with rows: the share goes on
@@ -137,7 +153,7 @@ struct AttnWalk {
   }
   // The CTAs that own the unit's first and last key tile.
   __device__ __forceinline__ int cta_of(int j) const {
-    const int at = s + (kAttnUnitCharge + j) * unit.weight;
+    const int at = s + (kAttnUnitCharge + j) * unit.weight();
     return (int)blockIdx.x + (at >= 0 ? at / share : -((share - 1 - at) / share));
   }
 };
@@ -168,13 +184,13 @@ struct AttnCfg {
 
 // One unit's part of a CTA's share, as the walking warp hands it to the others.
 struct AttnItem {
-  int n;          // key tiles (0: the end)
+  int n;          // tiles of K (0: the end); of two heads, those of both in turn
   int ntok;       // tokens of the unit
-  int two;        // two query tiles (a stream each), or one (shared)
+  int kind;       // AttnKind
   int p0;         // position of the first token
   int lo[2], hi[2];  // positions of each stream's first and last token
   int from[2], step; // a stream's first key tile of the part, and how many on its next is
-  int ns, skip;   // key tile i of the part is i + j0 while that is below ns, else i + j0 + skip
+  int ns, skip;   // the request's key tile j0 + i is the part's i-th while that is below ns, else it is j0 + i + skip
   int j0;
   int token, head, r, seq;
   int c0, c1;     // the CTAs of the unit's first and last key tile
@@ -219,15 +235,15 @@ __device__ __forceinline__ void attn_locate(const AttnParams& p, AttnSmem* sm, i
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int threads = (int)blockDim.x, per = (p.R + threads - 1) / threads;
   const int r0 = threadIdx.x * per;
-  // cost of one key head of request r; lanes of a warp call it together
+  // cost of request r; lanes of a warp call it together
   auto cost = [&](int r, bool* bad) -> int64_t {
     int row0 = 0, q = 0, seq = 0;
     if (r < p.R && !attn_request(p, r, &row0, &q, &seq)) *bad = true;
     const int nu = attn_units(p, q);
     int64_t c = 0;
     if (nu == 1) {
-      const AttnUnit x = attn_unit(p, q, seq, 0);
-      c = (int64_t)(x.n + kAttnUnitCharge) * x.weight;
+      c = (int64_t)attn_unit(p, q, seq, 0, p.Hkv - 1).cost() * p.Hkv;
+      if (attn_pairs(p, q)) c = (int64_t)attn_unit(p, q, seq, 0, 0).cost() * (p.Hkv / 2) + c / p.Hkv * (p.Hkv & 1);
     }
     uint32_t many = __ballot_sync(0xffffffffu, nu > 1);
     while (many) {
@@ -236,20 +252,17 @@ __device__ __forceinline__ void attn_locate(const AttnParams& p, AttnSmem* sm, i
       const int q_s = __shfl_sync(0xffffffffu, q, src), seq_s = __shfl_sync(0xffffffffu, seq, src);
       const int nu_s = __shfl_sync(0xffffffffu, nu, src);
       int64_t sum = 0;
-      for (int u = lane; u < nu_s; u += 32) {
-        const AttnUnit x = attn_unit(p, q_s, seq_s, u);
-        sum += (int64_t)(x.n + kAttnUnitCharge) * x.weight;
-      }
+      for (int u = lane; u < nu_s; u += 32) sum += attn_unit(p, q_s, seq_s, u, 0).cost();
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      if (lane == src) c = sum;
+      if (lane == src) c = sum * p.Hkv;
     }
     return c;
   };
   bool bad = false;
   int64_t sum = 0, c_last = 0;
   for (int i = 0; i < per; ++i) {
-    c_last = cost(r0 + i, &bad) * p.Hkv;
+    c_last = cost(r0 + i, &bad);
     sum += c_last;
   }
   if (bad && blockIdx.x == 0) raise_status(p.status, kStatusBadMetadata);
@@ -280,7 +293,7 @@ __device__ __forceinline__ void attn_locate(const AttnParams& p, AttnSmem* sm, i
     int found = -1;
     int64_t at = before, cost_found = 0;
     for (int i = 0; i < per; ++i) {
-      const int64_t c = per == 1 ? c_last : cost(r0 + i, &bad) * p.Hkv;
+      const int64_t c = per == 1 ? c_last : cost(r0 + i, &bad);
       if (mine && found < 0 && x0 < at + c) {
         found = r0 + i;
         cost_found = c;
@@ -290,17 +303,18 @@ __device__ __forceinline__ void attn_locate(const AttnParams& p, AttnSmem* sm, i
     const int src = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
     const int r = __shfl_sync(0xffffffffu, found, src);
     const int64_t begin = __shfl_sync(0xffffffffu, at, src);
-    const int64_t per_head = __shfl_sync(0xffffffffu, cost_found, src) / p.Hkv;
-    const int head = (int)((x0 - begin) / per_head);
-    int64_t s = begin + head * per_head;
+    const int64_t all = __shfl_sync(0xffffffffu, cost_found, src);
     int row0, q, seq;
     attn_request(p, r, &row0, &q, &seq);
+    const bool pairs = attn_pairs(p, q);
+    const int64_t per_head = pairs ? attn_unit(p, q, seq, 0, 0).cost() : all / p.Hkv;
+    const int at_head = (int)((x0 - begin) / per_head), head = at_head * (pairs ? 2 : 1);
+    int64_t s = begin + at_head * per_head;
     const int nu = attn_units(p, q);
     for (int u0 = 0; u0 < nu; u0 += 32) {
       int64_t c = 0;
       if (u0 + lane < nu) {
-        const AttnUnit x = attn_unit(p, q, seq, u0 + lane);
-        c = (int64_t)(x.n + kAttnUnitCharge) * x.weight;
+        c = attn_unit(p, q, seq, u0 + lane, head).cost();
       }
       int64_t end = c;
 #pragma unroll
@@ -358,10 +372,11 @@ __device__ __forceinline__ uint32_t attn_seen(const AttnParams& p, int back, int
 template <int DP, bool BF16>
 __device__ __noinline__ void attn_join(const AttnParams& p, const AttnItem& item, int warp, int lane) {
   const int parts = item.c1 - item.c0 + 1;
-  const int all = item.ntok * p.group;            // rows of both tiles
-  const int rows0 = p.tile_tokens * p.group;      // rows of the first tile
+  const int rows0 = min(item.ntok, p.tile_tokens) * p.group;  // rows of the first tile
+  const int all = item.kind == kTwoHeads ? 2 * rows0 : item.ntok * p.group;
   for (int i = warp; i < all; i += kAttnSoftmaxWarps) {
-    const int pr = item.two && i >= rows0 ? 128 + i - rows0 : i;
+    const bool second = i >= rows0;
+    const int pr = second ? 128 + i - rows0 : i;
     auto at = [&](int k) -> int64_t {
       return ((int64_t)(item.c0 + k) * 2 + (k == 0 && item.begins ? 1 : 0)) * 256 + pr;
     };
@@ -402,8 +417,10 @@ __device__ __noinline__ void attn_join(const AttnParams& p, const AttnItem& item
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     const float r = sum > 0.f ? 1.0f / sum : 0.f;
-    const int64_t t = item.token + i / p.group;
-    const int h = item.head * p.group + i % p.group;
+    const bool other_head = item.kind == kTwoHeads && second;
+    const int k = other_head ? i - rows0 : i;
+    const int64_t t = item.token + k / p.group;
+    const int h = (item.head + other_head) * p.group + k % p.group;
     uint16_t* orow = p.out + t * p.out_token + (int64_t)h * p.out_head + lane * (DP / 32);
     if (lane * (DP / 32) < p.D) {
 #pragma unroll
@@ -515,7 +532,7 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
       if (lane == 0) {
         const uint32_t q0 = ATTN_ITEM(q0);
         mbar_arrive(smem_u32(&sm->q_empty[q0 & 1]));
-        if (ATTN_ITEM(two)) mbar_arrive(smem_u32(&sm->q_empty[~q0 & 1]));
+        if (ATTN_ITEM(kind) != kOneTile) mbar_arrive(smem_u32(&sm->q_empty[~q0 & 1]));
       }
     };
     uint32_t n_s = 0, n_o = 0, tile0 = 0;  // score and output tiles so far; key tiles before this item
@@ -531,14 +548,15 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
         const bool live = (warp & 3) * 32 < (hi - lo + 1) * p.group;  // some row of this warp is real
         const int pos = min(lo + row / p.group, hi);
         const int ns = ATTN_ITEM(ns), skip = ATTN_ITEM(skip), j0 = ATTN_ITEM(j0), seq = ATTN_ITEM(seq);
+        const int heads = ATTN_ITEM(kind) == kTwoHeads;
         float factor = p.scale_log2;  // of the row's scores
         for (int j = ATTN_AT(mine, from); j < n; j += step) {
-          const int s0 = (j0 + j + (j0 + j < ns ? 0 : skip)) * kAttnTile;
+          const int jj = j0 + (j >> heads), s0 = (jj + (jj < ns ? 0 : skip)) * kAttnTile;
           const bool inner = s0 + kAttnTile - 1 <= lo && (p.window == 0 || s0 > hi - p.window || s0 + kAttnTile - 1 < p.sinks);
           wait(&sm->s_full[x], n_s & 1);
           ++n_s;
           if (FP8 && j == ATTN_AT(mine, from)) {
-            const uint32_t q = ATTN_ITEM(q0) + (step == 1 ? x : 0);
+            const uint32_t q = ATTN_ITEM(q0) + (ATTN_ITEM(kind) != kOneTile ? x : 0);
             factor = p.scale_log2 * __uint_as_float(lds_u32(factor_s + ((q & 1) * 128 + row) * 4));
             factor_read(at);
           }
@@ -696,9 +714,10 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
 
       if (FP8 && ATTN_AT(at + 4 * x, from) >= n) factor_read(at);
       // ---- the unit's end: out = O / l, or the part of a split unit
-      const bool two = ATTN_ITEM(two) != 0;
-      const int first = two && x ? p.tile_tokens : 0;  // this stream's first token in the unit
-      const int rows = (two ? min(p.tile_tokens, ATTN_ITEM(ntok) - first) : ATTN_ITEM(ntok)) * p.group;
+      const int kind = ATTN_ITEM(kind);
+      const bool two = kind != kOneTile;  // each stream has rows of its own
+      const int first = kind == kTwoTiles && x ? p.tile_tokens : 0;  // this stream's first token in the unit
+      const int rows = min(p.tile_tokens, ATTN_ITEM(ntok) - first) * p.group;
       const bool live = (warp & 3) * 32 < rows;
       const bool split = ATTN_ITEM(c0) != ATTN_ITEM(c1);
       if (two || x < n) {  // this stream had a tile
@@ -729,7 +748,7 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
         const int prow = two ? x * 128 + row : row;
         const int64_t part = ((int64_t)blockIdx.x * 2 + ATTN_ITEM(slot)) * 256 + prow;
         const int64_t token = ATTN_ITEM(token) + first + row / p.group;
-        const int head = ATTN_ITEM(head) * p.group + row % p.group;
+        const int head = (ATTN_ITEM(head) + (kind == kTwoHeads ? x : 0)) * p.group + row % p.group;
         const float inv = split ? 1.0f : (l > 0.f ? 1.0f / l : 0.f);
         f0 *= inv;
         f1 *= inv;
@@ -875,17 +894,18 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
         ++n_q;
       };
       auto serve = [&](uint32_t at, int n) {
-        const bool two = ATTN_ITEM(two) != 0;
+        const int kind = ATTN_ITEM(kind), heads = kind == kTwoHeads;
         const int token = ATTN_ITEM(token), head = ATTN_ITEM(head);
         const int p0 = ATTN_ITEM(p0), p1 = p0 + ATTN_ITEM(ntok) - 1;
         const int j0 = ATTN_ITEM(j0), ns = ATTN_ITEM(ns), skip = ATTN_ITEM(skip);
         const int first = p.window > 0 ? max(0, p0 - p.window + 1) : 0;
         const int32_t* bt = p.block_table + (int64_t)ATTN_ITEM(r) * p.max_blocks;
-        // page ids of 16 tiles, a pair of lanes each: the pool's end (zeros)
-        // for pages that no row sees and for bad ones
+        // page ids of 16 key tiles, a pair of lanes each: the pool's end (zeros)
+        // for pages that no row sees, -1 for bad ones
+        const int keys = n >> heads;
         auto ids = [&](int j) -> int {
           const int i = j + (lane >> 1), jj = j0 + i;
-          if (i >= n) return 0;
+          if (i >= keys) return 0;
           const int b = (jj < ns ? jj : jj + skip) * 2 + (lane & 1);
           const int64_t t0 = (int64_t)b * kPageTokens;
           if (t0 > p1 || !(t0 + kPageTokens > first || t0 < p.sinks)) return (int)p.num_pages;
@@ -897,28 +917,30 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
           return id;
         };
         int here = ids(0), ahead = ids(16);
-        int a0 = 0, a1 = 0, b0 = 0, b1 = 0;  // the newest key tile's pages, and those of the one before
+        int a0 = 0, a1 = 0, b0 = 0, b1 = 0;  // the newest K tile's pages, and those of the one before
         auto load_k = [&](int j) {
-          if (j > 0 && (j & 15) == 0) {
+          const int i = j >> heads;
+          if (i > 0 && (i & 15) == 0 && (heads == 0 || (j & 1) == 0)) {
             here = ahead;
-            ahead = ids(j + 16);
+            ahead = ids(i + 16);
           }
           b0 = a0;
           b1 = a1;
-          a0 = __shfl_sync(0xffffffffu, here, (j & 15) * 2);
-          a1 = __shfl_sync(0xffffffffu, here, (j & 15) * 2 + 1);
+          a0 = __shfl_sync(0xffffffffu, here, (i & 15) * 2);
+          a1 = __shfl_sync(0xffffffffu, here, (i & 15) * 2 + 1);
           if (lane == 0) sm->bad[(tile0 + j) & 15] = (uint8_t)((a0 < 0 ? 1 : 0) | (a1 < 0 ? 2 : 0));
           __syncwarp();
           if (a0 < 0) a0 = (int)p.num_pages;
           if (a1 < 0) a1 = (int)p.num_pages;
+          const int h = head + (j & heads);
           if (FP8)
-            load8(true, head, a0, a1);
+            load8(true, h, a0, a1);
           else
-            load(&tk, head, a0, a1);
+            load(&tk, h, a0, a1);
         };
         load_k(0);
         load_q(head, token);
-        if (two) {
+        if (kind == kTwoTiles) {
           load_q(head, token + p.tile_tokens);
           load_v(head, a0, a1);
           for (int j = 1; j < n && ok; ++j) {
@@ -927,11 +949,13 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
           }
         } else {
           if (n > 1) load_k(1);
+          if (heads) load_q(head + 1, token);
           for (int j = 0; j < n && ok; ++j) {
+            const int h = head + (j & heads);
             if (j + 1 < n)
-              load_v(head, b0, b1);
+              load_v(h, b0, b1);
             else
-              load_v(head, a0, a1);
+              load_v(h, a0, a1);
             if (j + 2 < n) load_k(j + 2);
           }
         }
@@ -1037,15 +1061,16 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
       };
       auto serve = [&](uint32_t at, int n) {
         const int step = ATTN_ITEM(step), from = ATTN_AT(at + 4 * x, from);
-        const uint32_t q0 = ATTN_ITEM(q0), q = q0 + (step == 1 ? x : 0);
+        const int kind = ATTN_ITEM(kind), heads = kind == kTwoHeads;
+        const uint32_t q0 = ATTN_ITEM(q0), q = q0 + (kind != kOneTile ? x : 0);
         const uint32_t own = from < n ? q : 0xFFFFFFFFu;
         // the key tile that holds the request's end inside a page: values
         // after it may be anything, and 0 * NaN would spoil the sum
-        int tail = -1, end;
+        int tail = n, end;
         {
-          const int last = ATTN_ITEM(j0) + n - 1;
+          const int last = ATTN_ITEM(j0) + (n >> heads) - 1;
           end = ATTN_ITEM(seq) - (last < ATTN_ITEM(ns) ? last : last + ATTN_ITEM(skip)) * kAttnTile;
-          if (!FP8 && end < kAttnTile && end % kPageTokens != 0) tail = n - 1;
+          if (!FP8 && end < kAttnTile && end % kPageTokens != 0) tail = n - 1 - heads;
         }
         const uint32_t tile0 = kv0 / 2;
         // half of Q K^T: 64 of the dimensions, or (E4M3) one of the queries' two terms
@@ -1088,7 +1113,7 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
           const uint32_t v_s = FP8 ? smem_u32(attn_smem) + C::kV + (tile0 + j) % C::kVStages * C::kTileBytes
                                    : kv_s + (kv0 + attn_v_place(step, j, n)) % C::kStages * C::kTileBytes;
           if (!v_wait(j)) return;
-          if (j == tail) {
+          if (j >= tail) {
             // (in shared tiles each stream's warp writes the same zeros)
             const int to = end < kPageTokens ? kPageTokens : kAttnTile;
 #pragma unroll 1
@@ -1125,7 +1150,7 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
           }
           v_release(j);
         }
-        if (!q_wait(q0 + (step == 1 ? 1 : 0), own)) return;
+        if (!q_wait(q0 + (kind != kOneTile ? 1 : 0), own)) return;
         if (!FP8)
           kv_wait(kv0 + 2 * n - 1, step, n);
         else if (tile_wait(0, tile0 + n - 1, step))
@@ -1192,8 +1217,9 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
       auto serve = [&](uint32_t at, int n) {
         const int ntok = ATTN_ITEM(ntok);
         const uint32_t q0 = ATTN_ITEM(q0);
-        if (!split_q(q0, min(ntok, p.tile_tokens) * p.group)) return;
-        if (ATTN_ITEM(two) && !split_q(q0 + 1, (ntok - p.tile_tokens) * p.group)) return;
+        const int kind = ATTN_ITEM(kind), rows = min(ntok, p.tile_tokens) * p.group;
+        if (!split_q(q0, rows)) return;
+        if (kind != kOneTile && !split_q(q0 + 1, kind == kTwoHeads ? rows : (ntok - p.tile_tokens) * p.group)) return;
         // V's codes to BF16 (exactly), into the layout that its product reads
 #pragma unroll 1
         for (uint32_t t = tile0; t < tile0 + n; ++t) {
@@ -1203,7 +1229,7 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
           const uint32_t src = smem_u32(attn_smem) + C::kVRaw + rst * C::kRawBytes;
           const uint32_t dst = smem_u32(attn_smem) + C::kV + st * C::kTileBytes;
           // rows past the request's end may be anything, NaN too: zeros
-          const int jj = ATTN_ITEM(j0) + (int)(t - tile0);
+          const int jj = ATTN_ITEM(j0) + ((int)(t - tile0) >> (kind == kTwoHeads));
           const int end = ATTN_ITEM(seq) - (jj < ATTN_ITEM(ns) ? jj : jj + ATTN_ITEM(skip)) * kAttnTile;
           const int cc = tid & 7;  // 16 codes: 32 bytes of a row's half cc / 4
           const uint32_t unit = 2 * (cc & 3);
@@ -1263,17 +1289,17 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
           i->n = n;
           if (n > 0) {
             i->ntok = w.unit.ntok;
-            i->two = w.unit.ntok > p.tile_tokens;
+            i->kind = w.unit.kind;
             i->p0 = w.unit.p0;
             const int last = w.unit.p0 + w.unit.ntok - 1;
-            const bool both = w.unit.ntok > p.tile_tokens;
+            const bool tiles = w.unit.kind == kTwoTiles;
             i->lo[0] = w.unit.p0;
-            i->hi[0] = both ? w.unit.p0 + p.tile_tokens - 1 : last;
-            i->lo[1] = both ? w.unit.p0 + p.tile_tokens : w.unit.p0;
+            i->hi[0] = tiles ? w.unit.p0 + p.tile_tokens - 1 : last;
+            i->lo[1] = tiles ? w.unit.p0 + p.tile_tokens : w.unit.p0;
             i->hi[1] = last;
             i->from[0] = 0;
-            i->from[1] = both ? 0 : 1;
-            i->step = both ? 1 : 2;
+            i->from[1] = tiles ? 0 : 1;
+            i->step = tiles ? 1 : 2;
             i->ns = w.unit.ns;
             i->skip = w.unit.lo - w.unit.ns;
             i->j0 = w.j0;
@@ -1286,7 +1312,7 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
             i->slot = w.s >= 0;
             i->begins = w.s >= (i->c0 - (int)blockIdx.x) * share;
             i->q0 = q0;
-            q0 += both ? 2 : 1;
+            q0 += w.unit.kind != kOneTile ? 2 : 1;
           }
           mbar_arrive(smem_u32(&sm->item_full[st]));
         }
@@ -1294,7 +1320,7 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
         ++it;
       };
       for (; w.inside(); w.next(p))
-        if (w.j1 > w.j0) hand(w.j1 - w.j0);
+        if (w.j1 > w.j0) hand((w.j1 - w.j0) << (w.unit.kind == kTwoHeads));
       hand(0);
     }
   }

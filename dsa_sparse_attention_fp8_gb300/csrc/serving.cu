@@ -89,7 +89,6 @@ size_t attention_part_rows() { return (size_t)attention_grid() * 2 * 256; }
 // one that the encoder takes.
 int make_map(CUtensorMap* m, const char* what, CUtensorMapDataType type, int size, const void* base, int rank,
              const int64_t* dims, const int64_t* strides, const int* box, bool swizzle) {
-  // (a larger promotion would fetch the next head of an E4M3 cache along)
   auto fn = encode_fn();
   if (!fn) return fail(DSA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
   cuuint64_t d[4], st[3];
@@ -106,8 +105,7 @@ int make_map(CUtensorMap* m, const char* what, CUtensorMapDataType type, int siz
   }
   const CUresult r = fn(m, type, (cuuint32_t)rank, const_cast<void*>(base), d, st, b, e, CU_TENSOR_MAP_INTERLEAVE_NONE,
                         swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-                        size == 1 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(DSA_ERR_CUDA, "cuTensorMapEncodeTiled(%s) failed (%d)", what, (int)r);
   return DSA_OK;
 }
