@@ -39,6 +39,7 @@ struct AttnParams {
   int32_t* status;
   int group;                   // Hq / Hkv
   int tile_tokens;             // tokens of a 128-row query tile: 128 / group
+  int tile_tokens32;           // tokens of 32 rows: 32 / group
   int sink_tiles;              // ceil(sinks / 128)
   float* part;                 // [grid][2][256][DP] split units' outputs ...
   float2* part_ml;             // [grid][2][256] ... their maxima and sums ...
@@ -47,9 +48,11 @@ struct AttnParams {
 
 constexpr int kAttnTile = 128;        // keys per tile (two pages)
 constexpr int kAttnSoftmaxWarps = 8;
-constexpr int kAttnTmaWarp = 8;
+// (A single token's rows are all in one warp of each stream, warps 0 and 5: the
+// scheduler of warps 0, 4, 8 ... has to spare the others' work.)
+constexpr int kAttnWalkWarp = 8;
 constexpr int kAttnMmaWarp = 9;       // and 10: one for each stream
-constexpr int kAttnWalkWarp = 11;
+constexpr int kAttnTmaWarp = 11;
 constexpr int kAttnConvertWarp = 12;  // to 15, with an E4M3 cache
 constexpr int kAttnMaxGrid = 160;
 // A row's probabilities are 2^(score - m) with m the maximum of the tiles up to
@@ -73,7 +76,7 @@ struct AttnUnit {
   int ntok;      // tokens
   int p0;        // position of the first
   int lo, ns, n; // first window tile, sink tiles before it, tiles in all
-  __device__ __forceinline__ int weight() const { return kind == kOneTile ? 1 : 2; }  // cost of a key tile
+  __device__ __forceinline__ int lg_weight() const { return kind != kOneTile; }  // cost of a key tile: 1 or 2
   __device__ __forceinline__ int cost() const;
 };
 
@@ -109,7 +112,7 @@ __device__ __forceinline__ bool attn_request(const AttnParams& p, int r, int* ro
   return ok;
 }
 
-__device__ __forceinline__ int AttnUnit::cost() const { return (n + kAttnUnitCharge) * weight(); }
+__device__ __forceinline__ int AttnUnit::cost() const { return (n + kAttnUnitCharge) << lg_weight(); }
 
 __device__ __forceinline__ int attn_units(const AttnParams& p, int q) {
   return (q + 2 * p.tile_tokens - 1) / (2 * p.tile_tokens);
@@ -129,9 +132,9 @@ struct AttnWalk {
   __device__ __forceinline__ void enter(const AttnParams& p) {
     unit = attn_unit(p, q, seq, u, head);
     // tile j lies at s + (charge + j) * weight
-    const int w = unit.weight();
-    j0 = s >= 0 ? 0 : max(0, (w - 1 - s) / w - kAttnUnitCharge);
-    j1 = min(unit.n, (len - s + w - 1) / w - kAttnUnitCharge);
+    const int lg = unit.lg_weight();
+    j0 = s >= 0 ? 0 : max(0, ((lg - s) >> lg) - kAttnUnitCharge);
+    j1 = min(unit.n, ((len - s + lg) >> lg) - kAttnUnitCharge);
   }
   __device__ __forceinline__ bool inside() const { return s < len; }
   __device__ __forceinline__ void next(const AttnParams& p) {
@@ -153,7 +156,7 @@ struct AttnWalk {
   }
   // The CTAs that own the unit's first and last key tile.
   __device__ __forceinline__ int cta_of(int j) const {
-    const int at = s + (kAttnUnitCharge + j) * unit.weight();
+    const int at = s + ((kAttnUnitCharge + j) << unit.lg_weight());
     return (int)blockIdx.x + (at >= 0 ? at / share : -((share - 1 - at) / share));
   }
 };
@@ -189,6 +192,7 @@ struct AttnItem {
   int kind;       // AttnKind
   int p0;         // position of the first token
   int lo[2], hi[2];  // positions of each stream's first and last token
+  int shift;         // rows of its tile that stream 1 leaves free before its own
   int from[2], step; // a stream's first key tile of the part, and how many on its next is
   int ns, skip;   // the request's key tile j0 + i is the part's i-th while that is below ns, else it is j0 + i + skip
   int j0;
@@ -228,6 +232,26 @@ __device__ __forceinline__ uint32_t attn_v_place(int step, int j, int n) {
 __device__ __forceinline__ uint32_t attn_col_s(int x) { return (uint32_t)x * 128; }
 __device__ __forceinline__ uint32_t attn_col_o(int x) { return 256u + (uint32_t)x * 128; }
 
+// A bounded wait as small as it can be: the kernel has some thirty, and its
+// code has to stay in the instruction caches.
+__device__ __forceinline__ bool attn_wait(uint32_t bar, uint32_t parity, const volatile int* abort_flag) {
+#pragma unroll 1
+  for (uint32_t i = 0; i < kWaitLimit; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 255u) == 255u && abort_flag && *abort_flag) return false;
+  }
+  return false;
+}
+
+// a / b for 0 <= a < 2^52, 0 < b: by way of FP64, whose quotient is off by one at
+// most (the compiler's division of 64-bit integers is a hundred instructions).
+__device__ __forceinline__ int64_t attn_divide(int64_t a, int64_t b) {
+  int64_t q = (int64_t)((double)a / (double)b);
+  if (q * b > a) --q;
+  if ((q + 1) * b <= a) ++q;
+  return q;
+}
+
 // Finds where this CTA's share of the work begins: every CTA sums the
 // requests' costs itself (a thread per request, a warp together for requests
 // of several units).  Called by all threads; the result is in shared memory.
@@ -259,47 +283,55 @@ __device__ __forceinline__ void attn_locate(const AttnParams& p, AttnSmem* sm, i
     }
     return c;
   };
-  bool bad = false;
-  int64_t sum = 0, c_last = 0;
-  for (int i = 0; i < per; ++i) {
-    c_last = cost(r0 + i, &bad);
-    sum += c_last;
-  }
-  if (bad && blockIdx.x == 0) raise_status(p.status, kStatusBadMetadata);
-  int64_t inc = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += y;
-  }
-  if (lane == 31) sm->warp_cost[warp] = inc;
-  __syncthreads();
-  int64_t before = inc - sum, total = 0;
-  for (int w = 0; w < threads / 32; ++w) {
-    if (w < warp) before += sm->warp_cost[w];
-    total += sm->warp_cost[w];
-  }
-  // shares of at least 4 single tiles: a split costs a unit's set-up and a merge
-  int64_t share = max((total + gridDim.x - 1) / (int64_t)gridDim.x, (int64_t)4);
-  if (share > kAttnMaxShare) {  // hours of work: no real batch
-    if (threadIdx.x == 0 && blockIdx.x == 0) raise_status(p.status, kStatusBadMetadata);
-    share = kAttnMaxShare;
-  }
-  const int64_t x0 = (int64_t)blockIdx.x * share;
-  *share_out = (int)share;
-  *len = (int)max(min(share, total - x0), (int64_t)0);
-  const bool mine = x0 < total && before <= x0 && x0 < before + sum;
-  if (__any_sync(0xffffffffu, mine)) {
-    int found = -1;
-    int64_t at = before, cost_found = 0;
+  // the sum first, then, in the warp of the share's first request, its place
+  bool bad = false, mine = false;
+  int64_t sum = 0, before = 0, total = 0, share = 0, x0 = 0, at = 0, cost_found = 0;
+  int found = -1;
+#pragma unroll 1
+  for (int phase = 0; phase < 2; ++phase) {
+#pragma unroll 1
     for (int i = 0; i < per; ++i) {
-      const int64_t c = per == 1 ? c_last : cost(r0 + i, &bad);
-      if (mine && found < 0 && x0 < at + c) {
-        found = r0 + i;
-        cost_found = c;
+      const int64_t c = cost(r0 + i, &bad);
+      if (phase == 0) {
+        sum += c;
+      } else {
+        if (mine && found < 0 && x0 < at + c) {
+          found = r0 + i;
+          cost_found = c;
+        }
+        if (found < 0) at += c;
       }
-      if (found < 0) at += c;
     }
+    if (phase == 1) break;
+    if (bad && blockIdx.x == 0) raise_status(p.status, kStatusBadMetadata);
+    int64_t inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    if (lane == 31) sm->warp_cost[warp] = inc;
+    __syncthreads();
+    before = inc - sum;
+#pragma unroll 1
+    for (int w = 0; w < threads / 32; ++w) {
+      if (w < warp) before += sm->warp_cost[w];
+      total += sm->warp_cost[w];
+    }
+    // shares of at least 4 single tiles: a split costs a unit's set-up and a merge
+    share = max(attn_divide(total + gridDim.x - 1, gridDim.x), (int64_t)4);
+    if (share > kAttnMaxShare) {  // hours of work: no real batch
+      if (threadIdx.x == 0 && blockIdx.x == 0) raise_status(p.status, kStatusBadMetadata);
+      share = kAttnMaxShare;
+    }
+    x0 = (int64_t)blockIdx.x * share;
+    *share_out = (int)share;
+    *len = (int)max(min(share, total - x0), (int64_t)0);
+    mine = x0 < total && before <= x0 && x0 < before + sum;
+    at = before;
+    if (!__any_sync(0xffffffffu, mine)) break;
+  }
+  if (__any_sync(0xffffffffu, mine)) {
     const int src = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
     const int r = __shfl_sync(0xffffffffu, found, src);
     const int64_t begin = __shfl_sync(0xffffffffu, at, src);
@@ -307,8 +339,8 @@ __device__ __forceinline__ void attn_locate(const AttnParams& p, AttnSmem* sm, i
     int row0, q, seq;
     attn_request(p, r, &row0, &q, &seq);
     const bool pairs = attn_pairs(p, q);
-    const int64_t per_head = pairs ? attn_unit(p, q, seq, 0, 0).cost() : all / p.Hkv;
-    const int at_head = (int)((x0 - begin) / per_head), head = at_head * (pairs ? 2 : 1);
+    const int64_t per_head = pairs ? attn_unit(p, q, seq, 0, 0).cost() : attn_divide(all, p.Hkv);
+    const int at_head = (int)attn_divide(x0 - begin, per_head), head = at_head * (pairs ? 2 : 1);
     int64_t s = begin + at_head * per_head;
     const int nu = attn_units(p, q);
     for (int u0 = 0; u0 < nu; u0 += 32) {
@@ -448,7 +480,8 @@ __device__ __noinline__ void attn_join(const AttnParams& p, const AttnItem& item
 //               walking: the CTA's share of the work, unit by unit.
 template <int DP, bool BF16, bool FP8>
 __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
-    paged_attention_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+    paged_attention_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tq32,
+                           const __grid_constant__ CUtensorMap tk,
                            const __grid_constant__ CUtensorMap tv, const __grid_constant__ AttnParams p) {
   using C = AttnCfg<DP, FP8>;
   extern __shared__ __align__(1024) unsigned char attn_smem[];
@@ -492,6 +525,7 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
   }
   if (warp == kAttnTmaWarp && lane == 0) {
     tma_prefetch_desc(&tq);
+    tma_prefetch_desc(&tq32);
     tma_prefetch_desc(&tk);
     tma_prefetch_desc(&tv);
   }
@@ -511,7 +545,7 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
   // which meet at barriers, go on to the items' end without waiting)
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (ok) {
-      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, abort_flag));
+      ok = __all_sync(0xffffffffu, attn_wait(smem_u32(bar), parity, abort_flag));
       if (!ok) *abort_flag = 1;
     }
     return ok;
@@ -524,7 +558,7 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
     // ================================================================ softmax
     if (FP8) regs_grow<C::kSoftmaxRegs>();
     const int x = warp >> 2;                            // stream
-    const int row = (warp & 3) * 32 + lane;             // row of its tile
+    const int tile_row = (warp & 3) * 32 + lane;        // row of its tile
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     // E4M3 caches: a query tile's slot is free once its rows' factors are read, too
     auto factor_read = [&](uint32_t at) {
@@ -538,15 +572,17 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
     uint32_t n_s = 0, n_o = 0, tile0 = 0;  // score and output tiles so far; key tiles before this item
     for (uint32_t it = 0;; ++it) {
       const uint32_t at = smem_u32(&sm->item[it % kAttnItems]);
-      if (!mbar_wait(smem_u32(&sm->item_full[it % kAttnItems]), (it / kAttnItems) & 1, nullptr)) break;
+      if (!attn_wait(smem_u32(&sm->item_full[it % kAttnItems]), (it / kAttnItems) & 1, nullptr)) break;
       const int n = ATTN_ITEM(n);
       if (n == 0) break;
       float m = -INFINITY, l = 0.f;
       {
         const uint32_t mine = at + 4 * x;
         const int lo = ATTN_AT(mine, lo), hi = ATTN_AT(mine, hi), step = ATTN_ITEM(step);
-        const bool live = (warp & 3) * 32 < (hi - lo + 1) * p.group;  // some row of this warp is real
-        const int pos = min(lo + row / p.group, hi);
+        const int shift = x ? ATTN_ITEM(shift) : 0, row = tile_row - shift;
+        // some row of this warp is real
+        const bool live = tile_row - lane < (hi - lo + 1) * p.group + shift && tile_row - lane >= shift;
+        const int pos = min(lo + max(row, 0) / p.group, hi);
         const int ns = ATTN_ITEM(ns), skip = ATTN_ITEM(skip), j0 = ATTN_ITEM(j0), seq = ATTN_ITEM(seq);
         const int heads = ATTN_ITEM(kind) == kTwoHeads;
         float factor = p.scale_log2;  // of the row's scores
@@ -557,7 +593,7 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
           ++n_s;
           if (FP8 && j == ATTN_AT(mine, from)) {
             const uint32_t q = ATTN_ITEM(q0) + (ATTN_ITEM(kind) != kOneTile ? x : 0);
-            factor = p.scale_log2 * __uint_as_float(lds_u32(factor_s + ((q & 1) * 128 + row) * 4));
+            factor = p.scale_log2 * __uint_as_float(lds_u32(factor_s + ((q & 1) * 128 + tile_row) * 4));
             factor_read(at);
           }
           if (live) {
@@ -718,7 +754,8 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
       const bool two = kind != kOneTile;  // each stream has rows of its own
       const int first = kind == kTwoTiles && x ? p.tile_tokens : 0;  // this stream's first token in the unit
       const int rows = min(p.tile_tokens, ATTN_ITEM(ntok) - first) * p.group;
-      const bool live = (warp & 3) * 32 < rows;
+      const int shift = x ? ATTN_ITEM(shift) : 0, row = tile_row - shift;
+      const bool live = tile_row - lane < rows + shift && tile_row - lane >= shift;
       const bool split = ATTN_ITEM(c0) != ATTN_ITEM(c1);
       if (two || x < n) {  // this stream had a tile
         wait(&sm->o_full[x], n_o & 1);
@@ -765,7 +802,7 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
             if (has0) o[i] = __uint_as_float(a[i]) * f0;
             if (has1) o[i] += __uint_as_float(b[i]) * f1;
           }
-          if (row < rows && c < p.D) {
+          if (row >= 0 && row < rows && c < p.D) {
             if (split) {
               float* dst = p.part + part * DP + c;
 #pragma unroll
@@ -781,7 +818,7 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
             }
           }
         }
-        if (row < rows && col0 == 0) {
+        if (row >= 0 && row < rows && col0 == 0) {
           if (split)
             __stcg(p.part_ml + part, make_float2(m, l));
           else if (p.lse)
@@ -822,7 +859,7 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
     auto each_item = [&](auto& serve) {
       for (uint32_t it = 0;; ++it) {
         const uint32_t at = smem_u32(&sm->item[it % kAttnItems]);
-        if (!mbar_wait(smem_u32(&sm->item_full[it % kAttnItems]), (it / kAttnItems) & 1, nullptr)) break;
+        if (!attn_wait(smem_u32(&sm->item_full[it % kAttnItems]), (it / kAttnItems) & 1, nullptr)) break;
         const int n = ATTN_ITEM(n);
         if (n == 0) break;
         if (ok) serve(at, n);
@@ -873,23 +910,16 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
         }
         __syncwarp();
       };
-      auto load_v = [&](int head, int page0, int page1) {
-        if (FP8)
-          load8(false, head, page0, page1);
-        else
-          load(&tv, head, page0, page1);
-      };
-      auto load_q = [&](int head, int token) {
+      // a query tile, or its first 32 rows' worth of tokens (`shift` rows down)
+      auto load_q = [&](int head, int token, bool few, int shift) {
         const uint32_t st = n_q & 1, round = n_q >> 1;
         if (round > 0) wait(&sm->q_empty[st], (round - 1) & 1);
         if (!ok) return;
-        if (lane == 0) {
-          const uint32_t bar = smem_u32(&sm->q_full[st]), dst = q_s + st * C::kTileBytes;
-          mbar_arrive_expect_tx(bar, (uint32_t)(C::kHalves * p.tile_tokens * p.group * 128));
-#pragma unroll
-          for (int h = 0; h < C::kHalves; ++h)
-            tma_load_3d(dst + h * 16384, &tq, h * 64, head * p.group, token, bar);
-        }
+        const uint32_t bar = smem_u32(&sm->q_full[st]), dst = q_s + st * C::kTileBytes + shift * 128;
+        const int tokens = few ? p.tile_tokens32 : p.tile_tokens;
+        if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(C::kHalves * tokens * p.group * 128));
+        __syncwarp();
+        if (lane < C::kHalves) tma_load_3d(dst + lane * 16384, few ? &tq32 : &tq, lane * 64, head * p.group, token, bar);
         __syncwarp();
         ++n_q;
       };
@@ -918,46 +948,40 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
         };
         int here = ids(0), ahead = ids(16);
         int a0 = 0, a1 = 0, b0 = 0, b1 = 0;  // the newest K tile's pages, and those of the one before
-        auto load_k = [&](int j) {
-          const int i = j >> heads;
-          if (i > 0 && (i & 15) == 0 && (heads == 0 || (j & 1) == 0)) {
-            here = ahead;
-            ahead = ids(i + 16);
+        // tiles in the order in which they are used (attn_k_place, attn_v_place),
+        // the query tiles after the first two
+#pragma unroll 1
+        for (int i = 0; i < 2 * n && ok; ++i) {
+          bool is_k = (i & 1) == 0;
+          int j = i >> 1;
+          if (kind != kTwoTiles) {
+            is_k = i == 0 || ((i & 1) && i != 2 * n - 1);
+            j = is_k ? (i + 1) >> 1 : i == 2 * n - 1 ? n - 1 : (i >> 1) - 1;
           }
-          b0 = a0;
-          b1 = a1;
-          a0 = __shfl_sync(0xffffffffu, here, (i & 15) * 2);
-          a1 = __shfl_sync(0xffffffffu, here, (i & 15) * 2 + 1);
-          if (lane == 0) sm->bad[(tile0 + j) & 15] = (uint8_t)((a0 < 0 ? 1 : 0) | (a1 < 0 ? 2 : 0));
-          __syncwarp();
-          if (a0 < 0) a0 = (int)p.num_pages;
-          if (a1 < 0) a1 = (int)p.num_pages;
-          const int h = head + (j & heads);
+          if (is_k) {
+            const int key = j >> heads;
+            if (key > 0 && (key & 15) == 0 && (j & heads) == 0) {
+              here = ahead;
+              ahead = ids(key + 16);
+            }
+            b0 = a0;
+            b1 = a1;
+            a0 = __shfl_sync(0xffffffffu, here, (key & 15) * 2);
+            a1 = __shfl_sync(0xffffffffu, here, (key & 15) * 2 + 1);
+            if (lane == 0) sm->bad[(tile0 + j) & 15] = (uint8_t)((a0 < 0 ? 1 : 0) | (a1 < 0 ? 2 : 0));
+            __syncwarp();
+            if (a0 < 0) a0 = (int)p.num_pages;
+            if (a1 < 0) a1 = (int)p.num_pages;
+          }
+          const bool older = !is_k && kind != kTwoTiles && j + 1 < n;  // V's pages are not the newest K's
+          const int h = head + (j & heads), page0 = older ? b0 : a0, page1 = older ? b1 : a1;
           if (FP8)
-            load8(true, h, a0, a1);
+            load8(is_k, h, page0, page1);
           else
-            load(&tk, h, a0, a1);
-        };
-        load_k(0);
-        load_q(head, token);
-        if (kind == kTwoTiles) {
-          load_q(head, token + p.tile_tokens);
-          load_v(head, a0, a1);
-          for (int j = 1; j < n && ok; ++j) {
-            load_k(j);
-            load_v(head, a0, a1);
-          }
-        } else {
-          if (n > 1) load_k(1);
-          if (heads) load_q(head + 1, token);
-          for (int j = 0; j < n && ok; ++j) {
-            const int h = head + (j & heads);
-            if (j + 1 < n)
-              load_v(h, b0, b1);
-            else
-              load_v(h, a0, a1);
-            if (j + 2 < n) load_k(j + 2);
-          }
+            load(is_k ? &tk : &tv, h, page0, page1);
+          if (i < (kind != kOneTile ? 2 : 1))
+            load_q(head + (i & heads), token + (kind == kTwoTiles && i ? p.tile_tokens : 0),
+                   ATTN_ITEM(ntok) <= p.tile_tokens32, i ? ATTN_ITEM(shift) : 0);
         }
         tile0 += n;
       };
@@ -985,7 +1009,7 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
       }
       // every copy has landed before the CTA leaves
       auto landed = [&](uint64_t* full, uint32_t n, uint32_t ring) {
-        for (uint32_t i = n > ring ? n - ring : 0; i < n; ++i) mbar_wait(smem_u32(&full[i % ring]), (i / ring) & 1, nullptr);
+        for (uint32_t i = n > ring ? n - ring : 0; i < n; ++i) attn_wait(smem_u32(&full[i % ring]), (i / ring) & 1, nullptr);
       };
       if (FP8) {
         landed(sm->kv_full, n_k, C::kKStages);
@@ -994,7 +1018,7 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
         landed(sm->kv_full, n_kv, C::kStages);
       }
       landed(sm->q_full, n_q, 2);
-    } else if (warp < kAttnWalkWarp) {
+    } else if (warp < kAttnTmaWarp && warp >= kAttnMmaWarp) {
       // ================================================================ MMA
       // A warp for each stream: products run in the order they are issued and
       // hardly ahead of the issuing thread (a pause of 100 cycles in it costs
@@ -1093,62 +1117,57 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
         auto v_release = [&](int j) {
           commit(&sm->kv_empty[FP8 ? C::kKStages + (tile0 + j) % C::kVStages : (kv0 + attn_v_place(step, j, n)) % C::kStages]);
         };
-        if (from < n) {
-          if (!q_wait(q, own)) return;
-          if (!k_wait(from)) return;
-          tc_fence_after();
-          for (int h = 0; h < C::kHalves; ++h) qk(from, h);
-          commit(&sm->s_full[x]);
-          k_release(from);
-          if (from + step >= n) commit(&sm->q_empty[q & 1]);
-        }
+        // Round by round: the P V of tile j and the Q K^T of the next; before the
+        // first a Q K^T alone, and in the last of an odd n nothing for stream 1.
+        bool first = true;
 #pragma unroll 1
-        for (int j = from; j - from < n; j += step) {  // (the last round of an odd n: no tile for stream 1)
-          if (j >= n) {
-            if (!take_turn()) return;
-            pass_turn();
-            break;
-          }
-          const bool more = j + step < n;
+        for (int j = from - step; j - from < n; j += step, first = false) {
+          const bool more = j + step < n, tile = !first && j < n;
+          if (first && !q_wait(q, own)) return;  // (no tile for this stream: the places are taken below)
           const uint32_t v_s = FP8 ? smem_u32(attn_smem) + C::kV + (tile0 + j) % C::kVStages * C::kTileBytes
                                    : kv_s + (kv0 + attn_v_place(step, j, n)) % C::kStages * C::kTileBytes;
-          if (!v_wait(j)) return;
-          if (j >= tail) {
-            // (in shared tiles each stream's warp writes the same zeros)
-            const int to = end < kPageTokens ? kPageTokens : kAttnTile;
+          if (tile) {
+            if (!v_wait(j)) return;
+            if (j >= tail) {
+              // (in shared tiles each stream's warp writes the same zeros)
+              const int to = end < kPageTokens ? kPageTokens : kAttnTile;
 #pragma unroll 1
-            for (int i = lane; i < (to - end) * 8; i += 32)
+              for (int i = lane; i < (to - end) * 8; i += 32)
 #pragma unroll
-              for (int h = 0; h < C::kHalves; ++h) sts_v4(v_s + h * 16384 + end * 128 + i * 16, make_uint4(0, 0, 0, 0));
-            fence_proxy_async_smem();
-            __syncwarp();
+                for (int h = 0; h < C::kHalves; ++h) sts_v4(v_s + h * 16384 + end * 128 + i * 16, make_uint4(0, 0, 0, 0));
+              fence_proxy_async_smem();
+              __syncwarp();
+            }
           }
           if (more && !k_wait(j + step)) return;
-          if (!wait(&sm->p_full[x], n_p & 1)) return;
-          ++n_p;
-          if (FP8 && lane == 0) {  // the tile's scales have been used
-            const uint32_t bar = smem_u32(&sm->scale_empty[(tile0 + j) & 7]);
-            mbar_arrive(bar);
-            if (step == 2) mbar_arrive(bar);
+          if (tile) {
+            if (!wait(&sm->p_full[x], n_p & 1)) return;
+            ++n_p;
+            if (FP8 && lane == 0) {  // the tile's scales have been used
+              const uint32_t bar = smem_u32(&sm->scale_empty[(tile0 + j) & 7]);
+              mbar_arrive(bar);
+              if (step == 2) mbar_arrive(bar);
+            }
           }
-          if (!take_turn()) return;
+          if (!first && !take_turn()) return;
           tc_fence_after();
-          if (lane == 0)
+          if (tile && lane == 0)
             umma_f16_ta_k128(tmem + attn_col_o(x), tmem + attn_col_s(x), sw128_desc_mn(v_s, 16384, 1024), id_pv,
                              j > from);
+          // the turn passes a few products early: the other warp wakes up meanwhile
+#pragma unroll
+          for (int h = 0; h < C::kHalves; ++h) {
+            if (h == C::kHalves - 1 && !first) pass_turn();
+            if (more) qk(j + step, h);
+          }
           if (more) {
-            // the turn passes a few products early: the other warp wakes up meanwhile
-            if (C::kHalves == 2) qk(j + step, 0);
-            pass_turn();
-            qk(j + step, C::kHalves - 1);
             commit(&sm->s_full[x]);
             k_release(j + step);
             if (j + 2 * step >= n) commit(&sm->q_empty[q & 1]);
-          } else {
-            pass_turn();
+          } else if (tile) {
             commit(&sm->o_full[x]);
           }
-          v_release(j);
+          if (tile) v_release(j);
         }
         if (!q_wait(q0 + (kind != kOneTile ? 1 : 0), own)) return;
         if (!FP8)
@@ -1163,7 +1182,7 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
       each_item(served);
       // every product issued has completed before tensor memory is released
       commit(&sm->drain[x]);
-      if (!mbar_wait(smem_u32(&sm->drain[x]), 0, nullptr)) ok = false;
+      if (!attn_wait(smem_u32(&sm->drain[x]), 0, nullptr)) ok = false;
       if (!ok) {
         sm->abort = 1;
         raise_status(p.status, kStatusTimeout);
@@ -1177,11 +1196,11 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
       // times 4: exact but for elements under 2^-9 of the row's maximum, which
       // are off by 2^-18 of it at most).  So Q K^T needs no conversion of K:
       // two products with its codes cost what one in 16 bits does.
-      auto split_q = [&](uint32_t place, int rows) {
+      auto split_q = [&](uint32_t place, int first, int rows) {
         if (!wait(&sm->q_full[place & 1], (place >> 1) & 1)) return false;
         const uint32_t tile = q_s + (place & 1) * C::kTileBytes;
 #pragma unroll 2
-        for (int r = cw; r < rows; r += 4) {
+        for (int r = first + cw; r < first + rows; r += 4) {
           // a lane's 4 elements
           const uint2 w = lds_v2(tile + (lane / 16) * 16384 + r * 128 + (((lane % 16 / 2) ^ (r & 7)) << 4) + 8 * (lane & 1));
           float f[4] = {__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
@@ -1218,8 +1237,8 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
         const int ntok = ATTN_ITEM(ntok);
         const uint32_t q0 = ATTN_ITEM(q0);
         const int kind = ATTN_ITEM(kind), rows = min(ntok, p.tile_tokens) * p.group;
-        if (!split_q(q0, rows)) return;
-        if (kind != kOneTile && !split_q(q0 + 1, kind == kTwoHeads ? rows : (ntok - p.tile_tokens) * p.group)) return;
+        if (!split_q(q0, 0, rows)) return;
+        if (kind != kOneTile && !split_q(q0 + 1, ATTN_ITEM(shift), kind == kTwoHeads ? rows : (ntok - p.tile_tokens) * p.group)) return;
         // V's codes to BF16 (exactly), into the layout that its product reads
 #pragma unroll 1
         for (uint32_t t = tile0; t < tile0 + n; ++t) {
@@ -1283,7 +1302,7 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
       int q0 = 0;
       auto hand = [&](int n) {
         const uint32_t st = it % kAttnItems, round = it / kAttnItems;
-        if (round > 0) mbar_wait(smem_u32(&sm->item_empty[st]), (round - 1) & 1, nullptr);
+        if (round > 0) attn_wait(smem_u32(&sm->item_empty[st]), (round - 1) & 1, nullptr);
         if (lane == 0) {
           AttnItem* i = &sm->item[st];
           i->n = n;
@@ -1297,6 +1316,7 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
             i->hi[0] = tiles ? w.unit.p0 + p.tile_tokens - 1 : last;
             i->lo[1] = tiles ? w.unit.p0 + p.tile_tokens : w.unit.p0;
             i->hi[1] = last;
+            i->shift = w.unit.kind == kTwoHeads && w.unit.ntok * p.group <= 32 ? 32 : 0;
             i->from[0] = 0;
             i->from[1] = tiles ? 0 : 1;
             i->step = tiles ? 1 : 2;

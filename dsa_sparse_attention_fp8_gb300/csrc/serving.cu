@@ -122,10 +122,12 @@ int launch_attention(const dsa::AttnParams& p, int grid, cudaStream_t st) {
   if (attr_err != cudaSuccess)
     return fail(DSA_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(attr_err));
   const CUtensorMapDataType type = BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  CUtensorMap tq, tkv[2];
+  CUtensorMap tq, tq32, tkv[2];
   const int64_t qd[3] = {p.D, p.Hq, p.T}, qs[2] = {p.q_head * 2, p.q_token * 2};
   const int qb[3] = {64, p.group, p.tile_tokens};
   if (const int rc = make_map(&tq, "q", type, 2, p.q, 3, qd, qs, qb, true)) return rc;
+  const int qb32[3] = {64, p.group, std::max(1, p.tile_tokens32)};
+  if (const int rc = make_map(&tq32, "q", type, 2, p.q, 3, qd, qs, qb32, true)) return rc;
   // boxes are 128 bytes wide: 64 16-bit dimensions, 128 E4M3 codes (zeros past
   // the head's); V's codes are converted from plain rows
   const int64_t kd[4] = {p.D, p.Hkv, DSA_PAGE_TOKENS, p.num_pages};
@@ -137,7 +139,7 @@ int launch_attention(const dsa::AttnParams& p, int grid, cudaStream_t st) {
                                 4, kd, ks, kb, !FP8 || i == 0))
       return rc;
   }
-  dsa::paged_attention_kernel<DP, BF16, FP8><<<grid, C::kThreads, C::kSmem, st>>>(tq, tkv[0], tkv[1], p);
+  dsa::paged_attention_kernel<DP, BF16, FP8><<<grid, C::kThreads, C::kSmem, st>>>(tq, tq32, tkv[0], tkv[1], p);
   set_last_launches(1);
   return check_launch("paged_attention_kernel");
 }
@@ -291,6 +293,7 @@ int dsa_paged_attention(const void* q, int64_t q_token_stride, int64_t q_head_st
   p.status = dev_status;
   p.group = Hq / p.Hkv;
   p.tile_tokens = 128 / p.group;
+  p.tile_tokens32 = 32 / p.group;
   p.sink_tiles = num_sinks / dsa::kAttnTile + (num_sinks % dsa::kAttnTile != 0);
   if (sm_count() <= 0) return fail(DSA_ERR_CUDA, "no CUDA device");
   const int grid = attention_grid();
