@@ -398,6 +398,52 @@ __device__ __forceinline__ uint32_t attn_seen(const AttnParams& p, int back, int
   return gone ? 0u : seen;
 }
 
+// The pages of an item's key tiles, looked up by a warp 16 tiles ahead, a pair
+// of lanes for each tile.
+struct AttnPages {
+  const int32_t* bt;
+  int j0, ns, skip, keys, first, last;  // first window position, last position that some row sees
+  int here, ahead;
+
+  // the id of this lane's page for tile key + lane / 2: the pool's end (zeros)
+  // for a page that no row sees, -1 for a bad one
+  __device__ __forceinline__ int look(const AttnParams& p, int key) const {
+    const int lane = lane_id(), i = key + (lane >> 1), jj = j0 + i;
+    if (i >= keys) return 0;
+    const int b = (jj < ns ? jj : jj + skip) * 2 + (lane & 1);
+    const int64_t t0 = (int64_t)b * kPageTokens;
+    if (t0 > last || !(t0 + kPageTokens > first || t0 < p.sinks)) return (int)p.num_pages;
+    const int id = __ldg(bt + b);
+    if (id < 0 || id >= p.num_pages) {
+      raise_status(p.status, kStatusBadPage);
+      return -1;
+    }
+    return id;
+  }
+  __device__ __forceinline__ void begin(const AttnParams& p, uint32_t at, int n) {
+    auto field = [&](size_t offset) { return (int)lds_u32(at + (uint32_t)offset); };
+    const int p0 = field(offsetof(AttnItem, p0));
+    bt = p.block_table + (int64_t)field(offsetof(AttnItem, r)) * p.max_blocks;
+    j0 = field(offsetof(AttnItem, j0));
+    ns = field(offsetof(AttnItem, ns));
+    skip = field(offsetof(AttnItem, skip));
+    keys = n >> (field(offsetof(AttnItem, kind)) == kTwoHeads);
+    first = p.window > 0 ? max(0, p0 - p.window + 1) : 0;
+    last = p0 + field(offsetof(AttnItem, ntok)) - 1;
+    here = look(p, 0);
+    ahead = look(p, 16);
+  }
+  // both pages of key tile `key`, asked for in order (several times if need be)
+  __device__ __forceinline__ void get(const AttnParams& p, int key, bool again, int* a, int* b) {
+    if (key > 0 && (key & 15) == 0 && !again) {
+      here = ahead;
+      ahead = look(p, key + 16);
+    }
+    *a = __shfl_sync(0xffffffffu, here, (key & 15) * 2);
+    *b = __shfl_sync(0xffffffffu, here, (key & 15) * 2 + 1);
+  }
+};
+
 // Joins the parts of a split unit, in CTA order: a warp per row, a lane per
 // DP / 32 elements.  Part k lies in slot 1 of the CTA in whose share the unit
 // begins, in slot 0 of the others.
@@ -867,6 +913,31 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
         if (lane == 0) mbar_arrive(smem_u32(&sm->item_empty[it % kAttnItems]));
       }
     };
+    // E4M3 caches: the next tile of K, with the scales of both, or of V
+    uint32_t n_t = 0;  // tiles so far
+    auto load8 = [&](bool is_k, int head, int page0, int page1) {
+      const uint32_t t = n_t, ring = is_k ? C::kKStages : C::kVRawStages, st = t % ring, round = t / ring;
+      if (round > 0) wait(is_k ? &sm->kv_empty[st] : &sm->raw_empty[st], (round - 1) & 1);
+      if (is_k && t >= 8) wait(&sm->scale_empty[t & 7], (t / 8 - 1) & 1);
+      if (!ok) return;
+      const uint32_t bar = smem_u32(is_k ? &sm->kv_full[st] : &sm->raw_full[st]);
+      const uint32_t dst = smem_u32(attn_smem) + (is_k ? C::kKv : C::kVRaw) + st * C::kRawBytes;
+      const int none = (int)p.num_pages, page = lane & 1 ? page1 : page0;
+      const uint32_t held = is_k ? (page0 < none) + (page1 < none) : 0;
+      if (lane == 0) mbar_arrive_expect_tx(bar, C::kRawBytes + held * 512);
+      __syncwarp();
+      if (lane < 2) tma_load_4d(dst + lane * 8192, is_k ? &tk : &tv, 0, head, 0, page, bar);
+      if (is_k && lane < 4 && page < none) {
+        const int w = lane >> 1;
+        bulk_load(scale_s + (t & 7) * 1024 + w * 512 + (lane & 1) * 256,
+                  p.scale[w] + (int64_t)head * p.scale_head[w] + page * p.scale_page[w], 256, bar);
+      }
+      __syncwarp();
+      ++n_t;
+    };
+    auto landed = [&](uint64_t* full, uint32_t n, uint32_t ring) {
+      for (uint32_t i = n > ring ? n - ring : 0; i < n; ++i) attn_wait(smem_u32(&full[i % ring]), (i / ring) & 1, nullptr);
+    };
     if (warp == kAttnTmaWarp) {
       // ================================================================ TMA
       uint32_t n_kv = 0, n_q = 0, tile0 = 0;
@@ -885,31 +956,6 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
         __syncwarp();
         ++n_kv;
       };
-      uint32_t n_k = 0, n_v = 0;  // E4M3 caches: tiles of each
-      auto load8 = [&](bool is_k, int head, int page0, int page1) {
-        const uint32_t t = is_k ? n_k++ : n_v++;
-        const uint32_t ring = is_k ? C::kKStages : C::kVRawStages, st = t % ring, round = t / ring;
-        uint64_t* empty = is_k ? sm->kv_empty : sm->raw_empty;
-        if (round > 0) wait(&empty[st], (round - 1) & 1);
-        if (is_k && t >= 8) wait(&sm->scale_empty[t & 7], (t / 8 - 1) & 1);
-        if (!ok) {
-          if (is_k) --n_k; else --n_v;
-          return;
-        }
-        const uint32_t bar = smem_u32(is_k ? &sm->kv_full[st] : &sm->raw_full[st]);
-        const uint32_t dst = smem_u32(attn_smem) + (is_k ? C::kKv : C::kVRaw) + st * C::kRawBytes;
-        const int none = (int)p.num_pages, page = lane & 1 ? page1 : page0;
-        const uint32_t held = is_k ? (page0 < none) + (page1 < none) : 0;
-        if (lane == 0) mbar_arrive_expect_tx(bar, C::kRawBytes + held * 512);
-        __syncwarp();
-        if (lane < 2) tma_load_4d(dst + lane * 8192, is_k ? &tk : &tv, 0, head, 0, page, bar);
-        if (is_k && lane < 4 && page < none) {
-          const int w = lane >> 1;
-          bulk_load(scale_s + (t & 7) * 1024 + w * 512 + (lane & 1) * 256,
-                    p.scale[w] + (int64_t)head * p.scale_head[w] + page * p.scale_page[w], 256, bar);
-        }
-        __syncwarp();
-      };
       // a query tile, or its first 32 rows' worth of tokens (`shift` rows down)
       auto load_q = [&](int head, int token, bool few, int shift) {
         const uint32_t st = n_q & 1, round = n_q >> 1;
@@ -926,48 +972,24 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
       auto serve = [&](uint32_t at, int n) {
         const int kind = ATTN_ITEM(kind), heads = kind == kTwoHeads;
         const int token = ATTN_ITEM(token), head = ATTN_ITEM(head);
-        const int p0 = ATTN_ITEM(p0), p1 = p0 + ATTN_ITEM(ntok) - 1;
-        const int j0 = ATTN_ITEM(j0), ns = ATTN_ITEM(ns), skip = ATTN_ITEM(skip);
-        const int first = p.window > 0 ? max(0, p0 - p.window + 1) : 0;
-        const int32_t* bt = p.block_table + (int64_t)ATTN_ITEM(r) * p.max_blocks;
-        // page ids of 16 key tiles, a pair of lanes each: the pool's end (zeros)
-        // for pages that no row sees, -1 for bad ones
-        const int keys = n >> heads;
-        auto ids = [&](int j) -> int {
-          const int i = j + (lane >> 1), jj = j0 + i;
-          if (i >= keys) return 0;
-          const int b = (jj < ns ? jj : jj + skip) * 2 + (lane & 1);
-          const int64_t t0 = (int64_t)b * kPageTokens;
-          if (t0 > p1 || !(t0 + kPageTokens > first || t0 < p.sinks)) return (int)p.num_pages;
-          const int id = __ldg(bt + b);
-          if (id < 0 || id >= p.num_pages) {
-            raise_status(p.status, kStatusBadPage);
-            return -1;
-          }
-          return id;
-        };
-        int here = ids(0), ahead = ids(16);
+        AttnPages pages;
+        pages.begin(p, at, n);
         int a0 = 0, a1 = 0, b0 = 0, b1 = 0;  // the newest K tile's pages, and those of the one before
-        // tiles in the order in which they are used (attn_k_place, attn_v_place),
-        // the query tiles after the first two
+        // tiles in the order in which they are used (attn_k_place, attn_v_place;
+        // with E4M3 caches K's alone), the query tiles after the first two
+        const int places = FP8 ? n : 2 * n;
 #pragma unroll 1
-        for (int i = 0; i < 2 * n && ok; ++i) {
-          bool is_k = (i & 1) == 0;
-          int j = i >> 1;
-          if (kind != kTwoTiles) {
+        for (int i = 0; i < places && ok; ++i) {
+          bool is_k = FP8 || (i & 1) == 0;
+          int j = FP8 ? i : i >> 1;
+          if (!FP8 && kind != kTwoTiles) {
             is_k = i == 0 || ((i & 1) && i != 2 * n - 1);
             j = is_k ? (i + 1) >> 1 : i == 2 * n - 1 ? n - 1 : (i >> 1) - 1;
           }
           if (is_k) {
-            const int key = j >> heads;
-            if (key > 0 && (key & 15) == 0 && (j & heads) == 0) {
-              here = ahead;
-              ahead = ids(key + 16);
-            }
             b0 = a0;
             b1 = a1;
-            a0 = __shfl_sync(0xffffffffu, here, (key & 15) * 2);
-            a1 = __shfl_sync(0xffffffffu, here, (key & 15) * 2 + 1);
+            pages.get(p, j >> heads, j & heads, &a0, &a1);
             if (lane == 0) sm->bad[(tile0 + j) & 15] = (uint8_t)((a0 < 0 ? 1 : 0) | (a1 < 0 ? 2 : 0));
             __syncwarp();
             if (a0 < 0) a0 = (int)p.num_pages;
@@ -976,12 +998,13 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
           const bool older = !is_k && kind != kTwoTiles && j + 1 < n;  // V's pages are not the newest K's
           const int h = head + (j & heads), page0 = older ? b0 : a0, page1 = older ? b1 : a1;
           if (FP8)
-            load8(is_k, h, page0, page1);
+            load8(true, h, page0, page1);
           else
             load(is_k ? &tk : &tv, h, page0, page1);
-          if (i < (kind != kOneTile ? 2 : 1))
-            load_q(head + (i & heads), token + (kind == kTwoTiles && i ? p.tile_tokens : 0),
-                   ATTN_ITEM(ntok) <= p.tile_tokens32, i ? ATTN_ITEM(shift) : 0);
+          const int queries = kind != kOneTile ? 2 : 1;
+          for (int k = i; k < queries && (k == i || i + 1 == places); ++k)
+            load_q(head + (k & heads), token + (kind == kTwoTiles && k ? p.tile_tokens : 0),
+                   ATTN_ITEM(ntok) <= p.tile_tokens32, k ? ATTN_ITEM(shift) : 0);
         }
         tile0 += n;
       };
@@ -1008,15 +1031,10 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
         }
       }
       // every copy has landed before the CTA leaves
-      auto landed = [&](uint64_t* full, uint32_t n, uint32_t ring) {
-        for (uint32_t i = n > ring ? n - ring : 0; i < n; ++i) attn_wait(smem_u32(&full[i % ring]), (i / ring) & 1, nullptr);
-      };
-      if (FP8) {
-        landed(sm->kv_full, n_k, C::kKStages);
-        landed(sm->raw_full, n_v, C::kVRawStages);
-      } else {
+      if (FP8)
+        landed(sm->kv_full, n_t, C::kKStages);
+      else
         landed(sm->kv_full, n_kv, C::kStages);
-      }
       landed(sm->q_full, n_q, 2);
     } else if (warp < kAttnTmaWarp && warp >= kAttnMmaWarp) {
       // ================================================================ MMA
@@ -1339,9 +1357,30 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
         __syncwarp();
         ++it;
       };
-      for (; w.inside(); w.next(p))
-        if (w.j1 > w.j0) hand((w.j1 - w.j0) << (w.unit.kind == kTwoHeads));
+      // With E4M3 caches this warp loads V as well, an item behind the walk (one
+      // warp with both loads is what the kernel waits for: each copy costs it
+      // some 150 cycles).
+      auto load_v = [&](uint32_t item) {
+        const uint32_t at = smem_u32(&sm->item[item % kAttnItems]);
+        const int n = ATTN_ITEM(n), heads = ATTN_ITEM(kind) == kTwoHeads, head = ATTN_ITEM(head);
+        if (!ok) return;
+        AttnPages pages;
+        pages.begin(p, at, n);
+#pragma unroll 1
+        for (int j = 0; j < n && ok; ++j) {
+          int a, b;
+          pages.get(p, j >> heads, j & heads, &a, &b);
+          load8(false, head + (j & heads), a < 0 ? (int)p.num_pages : a, b < 0 ? (int)p.num_pages : b);
+        }
+      };
+      for (; w.inside(); w.next(p)) {
+        if (w.j1 <= w.j0) continue;
+        hand((w.j1 - w.j0) << (w.unit.kind == kTwoHeads));
+        if (FP8 && it > 1) load_v(it - 2);
+      }
       hand(0);
+      if (FP8 && it > 1) load_v(it - 2);
+      if (FP8) landed(sm->raw_full, n_t, C::kVRawStages);
     }
   }
 #undef ATTN_ITEM
