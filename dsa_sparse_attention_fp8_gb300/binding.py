@@ -9,6 +9,7 @@ shapes and contiguity, then passes raw pointers and the current CUDA stream.
 from __future__ import annotations
 
 import ctypes
+import struct
 from pathlib import Path
 from typing import Optional, Sequence
 
@@ -164,12 +165,12 @@ def _declare(lib: ctypes.CDLL) -> None:
     lib.dsa_block_tables_build.argtypes = [_P, _P, _I, _P, _I, _P, _I, _I, _P, _P, _P, _P, _P, _P]
     lib.dsa_kv_write.restype = _I
     lib.dsa_kv_write.argtypes = [
-        _P, _I64, _I64, _P, _I64, _I64, _I, _I, _P, ctypes.POINTER(KvCache), _P, _P]
+        _P, _I64, _I64, _P, _I64, _I64, _I, _I, _P, _P, _P, _P]
     lib.dsa_paged_attention_workspace_bytes.restype = _SZ
     lib.dsa_paged_attention_workspace_bytes.argtypes = []
     lib.dsa_paged_attention.restype = _I
     lib.dsa_paged_attention.argtypes = [
-        _P, _I64, _I64, _I, _I, _I, ctypes.POINTER(KvCache), _P, _P, _I, _P, _I, _F, _I, _I, _P,
+        _P, _I64, _I64, _I, _I, _I, _P, _P, _P, _I, _P, _I, _F, _I, _I, _P,
         _I64, _I64, _P, _P, _SZ, _P, _P]
     lib.dsa_add_rms_norm.restype = _I
     lib.dsa_add_rms_norm.argtypes = [
@@ -612,16 +613,52 @@ def sparse_mla_attention(q: torch.Tensor, kv_cache: torch.Tensor, query_start_lo
 
 
 # ------------------------------------------- tables, K/V cache, attention, norm
+# These calls are made for every layer and step, some with a few microseconds of
+# GPU work: their checks take the short way where everything is as it should be.
 TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 TYPE_E4M3 = 3
 NORM_GROUP = 128
+_KV_CACHE = struct.Struct("@4P11q3i")   # KvCache's fields
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _same_device(*tensors: Optional[torch.Tensor]) -> None:
-    dev = tensors[0].device
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors lie on {dev} and {t.device}")
+def _stream_of(stream, device: int) -> int:
+    """The stream to launch on: the device's current one unless given."""
+    return _raw_stream(device) if stream is None else stream.cuda_stream
+
+
+def _device_of(t: torch.Tensor, name: str) -> int:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    device = t.get_device()
+    if device < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return device
+
+
+def _full(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, device: int) -> int:
+    """The address of a contiguous tensor of this dtype and shape on `device`."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.get_device() == device and t.is_contiguous()):
+        _need(t, name, dtype, shape)
+        raise ValueError(f"{name} lies on cuda:{t.get_device()}, expected cuda:{device}")
+    return t.data_ptr()
+
+
+def _rows(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, device: int) -> tuple:
+    """The strides of a tensor of this dtype and shape on `device` whose last
+    dimension is contiguous."""
+    strides = t.stride()
+    if not (t.dtype is dtype and t.shape == shape and t.get_device() == device
+            and (strides[-1] == 1 or shape[-1] == 1)):
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+        if _device_of(t, name) != device:
+            raise ValueError(f"{name} lies on cuda:{t.get_device()}, expected cuda:{device}")
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    return strides
 
 
 def _type_of(t: torch.Tensor, name: str, most: int = 1) -> int:
@@ -629,19 +666,16 @@ def _type_of(t: torch.Tensor, name: str, most: int = 1) -> int:
     if kind is None or kind > most:
         wanted = ", ".join(str(d) for d, k in TYPES.items() if k <= most)
         raise TypeError(f"{name} must be one of {wanted}, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
     return kind
 
 
-def _need_like(t: torch.Tensor, name: str, like: torch.Tensor, shape) -> None:
-    """`t` has like's dtype, this shape and a contiguous last dimension."""
-    if t.dtype != like.dtype:
-        raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
-        raise ValueError(f"the last dimension of {name} must be contiguous")
+def _status(status: Optional[torch.Tensor], device: int) -> Optional[int]:
+    if status is None:
+        return None
+    _need(status, "status", torch.int32)
+    if status.get_device() != device:
+        raise ValueError(f"status lies on cuda:{status.get_device()}, expected cuda:{device}")
+    return status.data_ptr()
 
 
 def build_block_tables(query_lens: torch.Tensor, seq_lens: torch.Tensor, free_pages: torch.Tensor,
@@ -653,53 +687,43 @@ def build_block_tables(query_lens: torch.Tensor, seq_lens: torch.Tensor, free_pa
     (dsa_block_tables_build): block_table [R, max_blocks] gains the new pages
     (taken from free_pages in request order), and query_start_loc [R+1],
     positions [T], slot_mapping [T] and pages_used [1] are written."""
+    dev = _device_of(query_lens, "query_lens")
     R, T = query_lens.shape[0], positions.shape[0]
-    _need(query_lens, "query_lens", torch.int32, (R,))
-    _need(seq_lens, "seq_lens", torch.int32, (R,))
-    _need(free_pages, "free_pages", torch.int32, (None,))
-    _need(block_table, "block_table", torch.int32, (R, None))
-    _need(query_start_loc, "query_start_loc", torch.int32, (R + 1,))
-    _need(positions, "positions", torch.int32, (T,))
-    _need(slot_mapping, "slot_mapping", torch.int64, (T,))
-    _need(pages_used, "pages_used", torch.int32, (1,))
-    if status is not None:
-        _need(status, "status", torch.int32)
-    _same_device(query_lens, seq_lens, free_pages, block_table, query_start_loc, positions,
-                 slot_mapping, pages_used, status)
-    _check(load().dsa_block_tables_build(
-        _ptr(query_lens), _ptr(seq_lens), R, _ptr(free_pages), free_pages.shape[0],
-        _ptr(block_table), block_table.shape[1], T, _ptr(query_start_loc), _ptr(positions),
-        _ptr(slot_mapping), _ptr(pages_used), _ptr(status), _stream(stream)))
+    num_free, max_blocks = free_pages.shape[0], block_table.shape[-1]
+    i32 = torch.int32
+    rc = load().dsa_block_tables_build(
+        _full(query_lens, "query_lens", i32, (R,), dev), _full(seq_lens, "seq_lens", i32, (R,), dev), R,
+        _full(free_pages, "free_pages", i32, (num_free,), dev), num_free,
+        _full(block_table, "block_table", i32, (R, max_blocks), dev), max_blocks, T,
+        _full(query_start_loc, "query_start_loc", i32, (R + 1,), dev),
+        _full(positions, "positions", i32, (T,), dev),
+        _full(slot_mapping, "slot_mapping", torch.int64, (T,), dev),
+        _full(pages_used, "pages_used", i32, (1,), dev), _status(status, dev), _stream_of(stream, dev))
+    if rc:
+        _check(rc)
 
 
-def _kv_cache(k_cache, v_cache, k_scale, v_scale, like, heads, dim) -> KvCache:
-    """The C description of a paged K/V cache after checking its tensors."""
-    pages = k_cache.shape[0]
-    shape = (pages, PAGE_TOKENS, heads, dim)
-    if k_cache.dtype == torch.uint8:
+def _kv_cache(k_cache, v_cache, k_scale, v_scale, like, heads, dim, device) -> bytes:
+    """The C description (KvCache) of a paged K/V cache after checking its tensors."""
+    pages, dtype = k_cache.shape[0], k_cache.dtype
+    if dtype is torch.uint8:
         if k_scale is None or v_scale is None:
             raise ValueError("a uint8 (E4M3) cache needs k_scale and v_scale")
-        kind = TYPE_E4M3
-        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-            if t.dtype != torch.float32:
-                raise TypeError(f"{name} must be torch.float32, got {t.dtype}")
-            _need_like(t, name, t, (pages, heads, PAGE_TOKENS))
-        sk, sv = k_scale.stride(), v_scale.stride()
-        scales = (k_scale.data_ptr(), v_scale.data_ptr())
+        kind, shape = TYPE_E4M3, (pages, heads, PAGE_TOKENS)
+        sk = _rows(k_scale, "k_scale", torch.float32, shape, device)
+        sv = _rows(v_scale, "v_scale", torch.float32, shape, device)
+        ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
     else:
         if k_scale is not None or v_scale is not None:
             raise ValueError("scales go with a uint8 (E4M3) cache")
-        kind = TYPES.get(k_cache.dtype)
-        if k_cache.dtype != like.dtype:
-            raise TypeError(f"k_cache must be {like.dtype} or torch.uint8, got {k_cache.dtype}")
-        sk = sv = (0, 0)
-        scales = (None, None)
-    _need_like(k_cache, "k_cache", k_cache, shape)
-    _need_like(v_cache, "v_cache", k_cache, shape)
-    _same_device(like, k_cache, v_cache, k_scale, v_scale)
-    a, b = k_cache.stride(), v_cache.stride()
-    return KvCache(k_cache.data_ptr(), v_cache.data_ptr(), *scales, a[0], a[1], a[2], b[0], b[1],
-                   b[2], sk[0], sk[1], sv[0], sv[1], pages, heads, dim, kind)
+        if dtype is not like.dtype:
+            raise TypeError(f"k_cache must be {like.dtype} or torch.uint8, got {dtype}")
+        kind, sk, sv, ks, vs = TYPES[dtype], (0, 0), (0, 0), 0, 0
+    shape = (pages, PAGE_TOKENS, heads, dim)
+    a = _rows(k_cache, "k_cache", dtype, shape, device)
+    b = _rows(v_cache, "v_cache", dtype, shape, device)
+    return _KV_CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, a[0], a[1], a[2], b[0],
+                          b[1], b[2], sk[0], sk[1], sv[0], sv[1], pages, heads, dim, kind)
 
 
 def kv_write(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor, k_cache: torch.Tensor,
@@ -711,17 +735,17 @@ def kv_write(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor, k_cac
     copied into caches of the same type, or quantised into uint8 (E4M3) caches
     with scales [num_pages, Hkv, 64]."""
     kind = _type_of(k, "k")
-    T, heads, dim = k.shape
-    _need_like(k, "k", k, (T, heads, dim))
-    _need_like(v, "v", k, (T, heads, dim))
-    _need(slot_mapping, "slot_mapping", torch.int64, (T,))
-    cache = _kv_cache(k_cache, v_cache, k_scale, v_scale, k, heads, dim)
-    if status is not None:
-        _need(status, "status", torch.int32)
-    _same_device(k, v, slot_mapping, status)
-    _check(load().dsa_kv_write(
-        k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1), kind, T,
-        slot_mapping.data_ptr(), ctypes.byref(cache), _ptr(status), _stream(stream)))
+    dev = _device_of(k, "k")
+    T, heads, dim = shape = tuple(k.shape)
+    a = _rows(k, "k", k.dtype, shape, dev)
+    b = _rows(v, "v", k.dtype, shape, dev)
+    cache = _kv_cache(k_cache, v_cache, k_scale, v_scale, k, heads, dim, dev)
+    rc = load().dsa_kv_write(
+        k.data_ptr(), a[0], a[1], v.data_ptr(), b[0], b[1], kind, T,
+        _full(slot_mapping, "slot_mapping", torch.int64, (T,), dev), cache, _status(status, dev),
+        _stream_of(stream, dev))
+    if rc:
+        _check(rc)
 
 
 def attention_workspace_bytes() -> int:
@@ -745,29 +769,27 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     `window` tokens and the first `num_sinks` (dsa_paged_attention).  Returns
     (out [T, Hq, D] like q, lse [T, Hq] FP32)."""
     kind = _type_of(q, "q")
-    T, Hq, dim = q.shape
-    R = seq_lens.shape[0]
-    _need_like(q, "q", q, (T, Hq, dim))
-    cache = _kv_cache(k_cache, v_cache, k_scale, v_scale, q, k_cache.shape[2], dim)
-    _need(query_start_loc, "query_start_loc", torch.int32, (R + 1,))
-    _need(seq_lens, "seq_lens", torch.int32, (R,))
-    _need(block_table, "block_table", torch.int32, (R, None))
-    _need(workspace, "workspace", torch.uint8)
+    dev = _device_of(q, "q")
+    T, Hq, dim = shape = tuple(q.shape)
+    a = _rows(q, "q", q.dtype, shape, dev)
+    cache = _kv_cache(k_cache, v_cache, k_scale, v_scale, q, k_cache.shape[2], dim, dev)
     if out is None:
-        out = torch.empty((T, Hq, dim), dtype=q.dtype, device=q.device)
+        out = torch.empty(shape, dtype=q.dtype, device=q.device)
     if lse is None:
         lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
-    _need_like(out, "out", q, (T, Hq, dim))
-    _need(lse, "lse", torch.float32, (T, Hq))
-    if status is not None:
-        _need(status, "status", torch.int32)
-    _same_device(q, query_start_loc, seq_lens, block_table, workspace, out, lse, status)
-    _check(load().dsa_paged_attention(
-        q.data_ptr(), q.stride(0), q.stride(1), kind, T, Hq, ctypes.byref(cache),
-        query_start_loc.data_ptr(), seq_lens.data_ptr(), R, block_table.data_ptr(),
-        block_table.shape[1], softmax_scale, window, num_sinks, out.data_ptr(), out.stride(0),
-        out.stride(1), lse.data_ptr(), workspace.data_ptr(), workspace.numel(), _ptr(status),
-        _stream(stream)))
+    b = _rows(out, "out", q.dtype, shape, dev)
+    R, max_blocks, n_ws = seq_lens.shape[0], block_table.shape[-1], workspace.shape[0]
+    i32 = torch.int32
+    rc = load().dsa_paged_attention(
+        q.data_ptr(), a[0], a[1], kind, T, Hq, cache,
+        _full(query_start_loc, "query_start_loc", i32, (R + 1,), dev),
+        _full(seq_lens, "seq_lens", i32, (R,), dev), R,
+        _full(block_table, "block_table", i32, (R, max_blocks), dev), max_blocks, softmax_scale,
+        window, num_sinks, out.data_ptr(), b[0], b[1], _full(lse, "lse", torch.float32, (T, Hq), dev),
+        _full(workspace, "workspace", torch.uint8, (n_ws,), dev), n_ws, _status(status, dev),
+        _stream_of(stream, dev))
+    if rc:
+        _check(rc)
     return out, lse
 
 
@@ -781,19 +803,21 @@ def add_rms_norm(x: torch.Tensor, residual: Optional[torch.Tensor], weight: torc
     residual, residual_out, out [T, N] may have any row stride; residual_out
     may be x or residual."""
     kind = _type_of(x, "x", most=2)
-    T, N = x.shape
-    strides = []
-    for t, name in ((x, "x"), (residual, "residual"), (residual_out, "residual_out"), (out, "out")):
-        if t is not None:
-            _need_like(t, name, x, (T, N))
-        strides.append(N if t is None or T == 1 else t.stride(0))
-    _need_like(weight, "weight", x, (N,))
-    if codes is not None:
-        _need(codes, "codes", torch.uint8, (T, N))
-    if scales is not None:
-        _need(scales, "scales", torch.float32, (T, -(-N // NORM_GROUP)))
-    _same_device(x, residual, weight, residual_out, out, codes, scales)
-    _check(load().dsa_add_rms_norm(
-        x.data_ptr(), strides[0], _ptr(residual), strides[1], weight.data_ptr(), kind, T, N, eps,
-        _ptr(residual_out), strides[2], _ptr(out), strides[3], _ptr(codes), _ptr(scales),
-        _stream(stream)))
+    dev, dtype = _device_of(x, "x"), x.dtype
+    T, N = shape = tuple(x.shape)
+
+    def row(t, name):  # address and row stride
+        if t is None:
+            return None, N
+        strides = _rows(t, name, dtype, shape, dev)
+        return t.data_ptr(), strides[0] if T > 1 else N
+
+    args = [*row(x, "x"), *row(residual, "residual")]
+    args += [_full(weight, "weight", dtype, (N,), dev), kind, T, N, eps]
+    args += [*row(residual_out, "residual_out"), *row(out, "out")]
+    args.append(None if codes is None else _full(codes, "codes", torch.uint8, (T, N), dev))
+    args.append(None if scales is None else
+                _full(scales, "scales", torch.float32, (T, -(-N // NORM_GROUP)), dev))
+    rc = load().dsa_add_rms_norm(*args, _stream_of(stream, dev))
+    if rc:
+        _check(rc)

@@ -19,6 +19,7 @@ struct KvWriteParams {
   int64_t src_token[2], src_head[2];
   const int64_t* slots;         // [T]
   int T, heads, dim;
+  int tokens;                   // of a CTA
   uint8_t* cache[2];            // [num_pages, 64, Hkv, D], byte strides below
   int64_t page_stride[2], token_stride[2], head_stride[2];
   float* scale[2];              // [num_pages, Hkv, 64], element strides below (E4M3 caches)
@@ -36,67 +37,69 @@ __device__ __forceinline__ float2 widen2(uint32_t w) {
 // A row is one head of one token's key or value.  16 lanes own a row, 8
 // elements (16 bytes) each, so a warp reads two rows of up to 256 bytes with
 // one instruction, and a row's maximum takes four shuffles.  kRows rows per
-// lane are in flight at once.
+// lane are in flight at once; a CTA has the rows of `tokens` tokens.
 constexpr int kKvThreads = 256;
+constexpr int kKvRows = 4;
 
-template <bool BF16, bool FP8, int kRows>
+template <bool BF16, bool FP8>
 __global__ void __launch_bounds__(kKvThreads) kv_write_kernel(const __grid_constant__ KvWriteParams p) {
+  constexpr int kRows = kKvRows;
   const int lane = threadIdx.x & 15;
-  const int64_t rows = 2 * (int64_t)p.T * p.heads;
-  const int64_t first = ((int64_t)blockIdx.x * (kKvThreads / 16) + (threadIdx.x >> 4)) * kRows;
-  uint4 x[kRows];
-  int64_t slot[kRows];
-  int which[kRows], head[kRows];
+  const int64_t t0 = (int64_t)blockIdx.x * p.tokens;
+  const int rows = (int)min((int64_t)p.tokens, p.T - t0) * 2 * p.heads;  // (token, k or v, head)
+  for (int first = threadIdx.x >> 4; first - (int)(threadIdx.x >> 4) < rows; first += kKvThreads / 16 * kRows) {
+    uint4 x[kRows];
+    int64_t slot[kRows];
+    int which[kRows], head[kRows];
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    const int64_t row = first + i;  // (token, k or v, head)
-    x[i] = make_uint4(0, 0, 0, 0);
-    slot[i] = -1;
-    which[i] = head[i] = 0;
-    if (row < rows) {
-      const int64_t t = row / (2 * p.heads);
-      const int rest = (int)(row - t * (2 * p.heads));
-      which[i] = rest >= p.heads;
-      head[i] = rest - which[i] * p.heads;
-      slot[i] = __ldg(p.slots + t);
-      if (lane * 8 < p.dim)
-        x[i] = __ldg(reinterpret_cast<const uint4*>(p.src[which[i]] + t * p.src_token[which[i]] +
-                                                    head[i] * p.src_head[which[i]] + lane * 8));
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    const int w = which[i];
-    const int64_t page = slot[i] / kPageTokens;
-    const int off = (int)(slot[i] % kPageTokens);
-    const bool live = slot[i] >= 0 && page < p.num_pages;
-    if (slot[i] >= 0 && !live && lane == 0) raise_status(p.status, kStatusBadPage);
-    uint8_t* dst = p.cache[w] + page * p.page_stride[w] + off * p.token_stride[w] + head[i] * p.head_stride[w];
-    if (!FP8) {
-      if (live && lane * 8 < p.dim) *reinterpret_cast<uint4*>(dst + lane * 16) = x[i];
-      continue;
-    }
-    const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-    float2 f[4];
-    float amax = 0.f;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      f[j] = widen2<BF16>(u[j]);
-      amax = fmaxf(amax, fmaxf(fabsf(f[j].x), fabsf(f[j].y)));
+    for (int i = 0; i < kRows; ++i) {
+      const int row = first + i * (kKvThreads / 16);
+      x[i] = make_uint4(0, 0, 0, 0);
+      slot[i] = -1;
+      which[i] = head[i] = 0;
+      if (row < rows) {
+        const int t = row / (2 * p.heads), rest = row - t * (2 * p.heads);
+        which[i] = rest >= p.heads;
+        head[i] = rest - which[i] * p.heads;
+        slot[i] = __ldg(p.slots + t0 + t);
+        if (lane * 8 < p.dim)
+          x[i] = __ldg(reinterpret_cast<const uint4*>(p.src[which[i]] + (t0 + t) * p.src_token[which[i]] +
+                                                      head[i] * p.src_head[which[i]] + lane * 8));
+      }
     }
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    const float s = amax == 0.f ? 1.0f : __fdiv_rn(amax, 448.0f);
-    uint32_t c[4];
+    for (int i = 0; i < kRows; ++i) {
+      const int w = which[i];
+      const int64_t page = slot[i] >> 6;  // (64 tokens)
+      const int off = (int)(slot[i] & 63);
+      const bool live = slot[i] >= 0 && page < p.num_pages;
+      if (slot[i] >= 0 && !live && lane == 0) raise_status(p.status, kStatusBadPage);
+      uint8_t* dst = p.cache[w] + page * p.page_stride[w] + off * p.token_stride[w] + head[i] * p.head_stride[w];
+      if (!FP8) {
+        if (live && lane * 8 < p.dim) *reinterpret_cast<uint4*>(dst + lane * 16) = x[i];
+        continue;
+      }
+      const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+      float f[8];
+      float amax = 0.f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      c[j] = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(f[j].x, s), __fdiv_rn(f[j].y, s)), __NV_SATFINITE,
-                                      __NV_E4M3);
-    if (live) {
-      if (lane * 8 < p.dim)
-        *reinterpret_cast<uint2*>(dst + lane * 8) =
-            make_uint2((c[0] & 0xFFFFu) | (c[1] << 16), (c[2] & 0xFFFFu) | (c[3] << 16));
-      if (lane == 0) p.scale[w][page * p.scale_page[w] + head[i] * p.scale_head[w] + off] = s;
+      for (int j = 0; j < 4; ++j) {
+        const float2 w2 = widen2<BF16>(u[j]);
+        f[2 * j] = w2.x;
+        f[2 * j + 1] = w2.y;
+        amax = fmaxf(amax, fmaxf(fabsf(w2.x), fabsf(w2.y)));
+      }
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      const float s = amax == 0.f ? 1.0f : __fdiv_rn(amax, 448.0f);
+      uint32_t c[4];
+      quantize8(f, s, c);
+      if (live) {
+        if (lane * 8 < p.dim)
+          *reinterpret_cast<uint2*>(dst + lane * 8) =
+              make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+        if (lane == 0) p.scale[w][page * p.scale_page[w] + head[i] * p.scale_head[w] + off] = s;
+      }
     }
   }
 }

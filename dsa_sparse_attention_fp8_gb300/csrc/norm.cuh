@@ -51,25 +51,31 @@ __device__ __forceinline__ __half from_f32(float v) { return __float2half_rn(v);
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32(float v) { return __float2bfloat16_rn(v); }
 
-// 16-byte accesses where every row starts on a 16-byte boundary and is a
-// multiple of 8 elements long; single elements otherwise.
+// 8 elements of a row as they lie in memory.  16-byte accesses where every row
+// starts on a 16-byte boundary and is a multiple of 8 elements long; single
+// elements otherwise.
+template <typename T>
+union Norm8 {
+  uint4 u[sizeof(T) / 2];
+  T e[8];
+};
 template <typename T, bool VEC>
-__device__ __forceinline__ void load8(const T* row, int at, int n, float* f) {
+__device__ __forceinline__ Norm8<T> load8(const T* row, int at, int n) {
+  Norm8<T> v;
   if (VEC) {
-    union { uint4 u[sizeof(T) / 2]; T e[8]; } v;
 #pragma unroll
-    for (int j = 0; j < (int)sizeof(T) / 2; ++j) v.u[j] = __ldg(reinterpret_cast<const uint4*>(row + at) + j);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = to_f32(v.e[j]);
+    for (int j = 0; j < (int)sizeof(T) / 2; ++j)
+      v.u[j] = at < n ? __ldg(reinterpret_cast<const uint4*>(row + at) + j) : make_uint4(0, 0, 0, 0);
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = at + j < n ? to_f32(row[at + j]) : 0.f;
+    for (int j = 0; j < 8; ++j) v.e[j] = at + j < n ? row[at + j] : from_f32<T>(0.f);
   }
+  return v;
 }
 template <typename T, bool VEC>
 __device__ __forceinline__ void store8(T* row, int at, int n, const float* f) {
   if (VEC) {
-    union { uint4 u[sizeof(T) / 2]; T e[8]; } v;
+    Norm8<T> v;
 #pragma unroll
     for (int j = 0; j < 8; ++j) v.e[j] = from_f32<T>(f[j]);
 #pragma unroll
@@ -81,42 +87,39 @@ __device__ __forceinline__ void store8(T* row, int at, int n, const float* f) {
   }
 }
 
-// One CTA per row; thread i owns elements [8 i, 8 i + 8) and every
-// 8 * blockDim further on, VPT times, in registers from the load to the
-// store, so the row is read once.  The 16 lanes of half a warp share a
-// 128-element group.
+// A CTA per row; thread i owns elements [8 i, 8 i + 8) and every 8 * blockDim
+// further on, VPT times, in registers from the load to the store, so a row is
+// read once.  The 16 lanes of half a warp share a 128-element group.
 template <typename T, bool VEC, int VPT>
-__global__ void add_rms_norm_kernel(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) add_rms_norm_kernel(const __grid_constant__ NormParams p) {
   __shared__ float warp_sum[32];
-  const int row = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, step = blockDim.x * 8, row = blockIdx.x;
   const T* x = static_cast<const T*>(p.x) + (int64_t)row * p.x_stride;
   const T* res = p.residual ? static_cast<const T*>(p.residual) + (int64_t)row * p.residual_stride : nullptr;
-  const T* weight = static_cast<const T*>(p.weight);
-  float h[VPT][8];
+  Norm8<T> v[VPT], rv[VPT];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int at = threadIdx.x * 8 + i * step;
+    v[i] = load8<T, VEC>(x, at, p.N);
+    if (res) rv[i] = load8<T, VEC>(res, at, p.N);
+  }
   float sq = 0.f;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int at = (threadIdx.x + i * blockDim.x) * 8;
+    const int at = threadIdx.x * 8 + i * step;
+    float h[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) h[i][j] = 0.f;
-    if (at < p.N) {
-      load8<T, VEC>(x, at, p.N, h[i]);
-      if (res) {
-        float r[8];
-        load8<T, VEC>(res, at, p.N, r);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) h[i][j] = to_f32(from_f32<T>(h[i][j] + r[j]));
-      }
+    for (int j = 0; j < 8; ++j) {
+      if (res) v[i].e[j] = from_f32<T>(to_f32(v[i].e[j]) + to_f32(rv[i].e[j]));
+      h[j] = to_f32(v[i].e[j]);
+      sq += h[j] * h[j];
     }
+    if (p.sum && at < p.N) store8<T, VEC>(static_cast<T*>(p.sum) + (int64_t)row * p.sum_stride, at, p.N, h);
   }
+  // (the weights' loads fall into the sum's)
+  Norm8<T> wv[VPT];
 #pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int at = (threadIdx.x + i * blockDim.x) * 8;
-    if (p.sum && at < p.N)
-      store8<T, VEC>(static_cast<T*>(p.sum) + (int64_t)row * p.sum_stride, at, p.N, h[i]);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) sq += h[i][j] * h[i][j];
-  }
+  for (int i = 0; i < VPT; ++i) wv[i] = load8<T, VEC>(static_cast<const T*>(p.weight), threadIdx.x * 8 + i * step, p.N);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
   if (lane == 0) warp_sum[warp] = sq;
@@ -127,15 +130,12 @@ __global__ void add_rms_norm_kernel(const __grid_constant__ NormParams p) {
   const float rstd = 1.0f / sqrtf(total / (float)p.N + p.eps);
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int at = (threadIdx.x + i * blockDim.x) * 8;
-    float y[8], w[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = 0.f;
-    if (at < p.N) load8<T, VEC>(weight, at, p.N, w);
+    const int at = threadIdx.x * 8 + i * step;
+    float y[8];
     float amax = 0.f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      y[j] = h[i][j] * rstd * w[j];
+      y[j] = to_f32(v[i].e[j]) * rstd * to_f32(wv[i].e[j]);
       amax = fmaxf(amax, fabsf(y[j]));
     }
     if (p.out && at < p.N)
@@ -145,10 +145,7 @@ __global__ void add_rms_norm_kernel(const __grid_constant__ NormParams p) {
     for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     const float s = amax == 0.f ? 1.0f : __fdiv_rn(amax, 448.0f);
     uint32_t c[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      c[j] = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(y[2 * j], s), __fdiv_rn(y[2 * j + 1], s)),
-                                      __NV_SATFINITE, __NV_E4M3) & 0xFFFFu;
+    quantize8(y, s, c);
     if (at < p.N) {
       uint8_t* dst = p.codes + (int64_t)row * p.N + at;
       if (VEC) {
@@ -158,8 +155,7 @@ __global__ void add_rms_norm_kernel(const __grid_constant__ NormParams p) {
         for (int j = 0; j < 8; ++j)
           if (at + j < p.N) dst[j] = (uint8_t)(c[j >> 1] >> (8 * (j & 1)));
       }
-      if ((lane & 15) == 0)
-        p.scales[(int64_t)row * ((p.N + kNormGroup - 1) / kNormGroup) + at / kNormGroup] = s;
+      if ((lane & 15) == 0) p.scales[(int64_t)row * ((p.N + kNormGroup - 1) / kNormGroup) + at / kNormGroup] = s;
     }
   }
 }

@@ -144,11 +144,14 @@ int launch_attention(const dsa::AttnParams& p, int grid, cudaStream_t st) {
   return check_launch("paged_attention_kernel");
 }
 
+constexpr int kNormOne = 1024;
+// A thread's share of a row: one piece of 8 elements up to 1,024 threads, then
+// as few as keep the block at 512.
 template <typename T, bool VEC>
 void launch_norm(const dsa::NormParams& p, cudaStream_t st) {
   const int n8 = (p.N + 7) / 8;
   auto block = [&](int vpt) { return std::max(32, ((n8 + vpt - 1) / vpt + 31) / 32 * 32); };
-  if (block(1) <= 256)
+  if (block(1) <= kNormOne)
     dsa::add_rms_norm_kernel<T, VEC, 1><<<p.T, block(1), 0, st>>>(p);
   else if (block(2) <= 512)
     dsa::add_rms_norm_kernel<T, VEC, 2><<<p.T, block(2), 0, st>>>(p);
@@ -219,18 +222,17 @@ int dsa_kv_write(const void* k, int64_t k_token_stride, int64_t k_head_stride, c
   p.dim = cache->head_dim;
   set_cache(&p, cache);
   p.status = dev_status;
-  constexpr int kRows = 2;
-  const int64_t rows = 2 * (int64_t)T * p.heads, per = (int64_t)dsa::kKvThreads / 16 * kRows;
-  const int64_t grid = (rows + per - 1) / per;
-  if (grid > INT32_MAX) return fail(DSA_ERR_INVALID_ARG, "too many rows");
+  // a CTA's tokens: as many as make one pass of its lanes, at least one
+  p.tokens = std::max(1, dsa::kKvThreads / 16 * dsa::kKvRows / (2 * p.heads));
+  const int64_t grid = ((int64_t)T + p.tokens - 1) / p.tokens;
   const cudaStream_t st = (cudaStream_t)stream;
   const bool fp8 = cache->type == DSA_TYPE_E4M3;
   if (type == DSA_TYPE_BF16 && fp8)
-    dsa::kv_write_kernel<true, true, kRows><<<(unsigned)grid, dsa::kKvThreads, 0, st>>>(p);
+    dsa::kv_write_kernel<true, true><<<(unsigned)grid, dsa::kKvThreads, 0, st>>>(p);
   else if (fp8)
-    dsa::kv_write_kernel<false, true, kRows><<<(unsigned)grid, dsa::kKvThreads, 0, st>>>(p);
+    dsa::kv_write_kernel<false, true><<<(unsigned)grid, dsa::kKvThreads, 0, st>>>(p);
   else
-    dsa::kv_write_kernel<true, false, kRows><<<(unsigned)grid, dsa::kKvThreads, 0, st>>>(p);
+    dsa::kv_write_kernel<true, false><<<(unsigned)grid, dsa::kKvThreads, 0, st>>>(p);
   set_last_launches(1);
   return check_launch("kv_write_kernel");
 }

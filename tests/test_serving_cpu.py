@@ -110,8 +110,22 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
     with pytest.raises(ValueError, match="CUDA"):
         B.add_rms_norm(x[0], None, x[0, 0], 1e-6, out=x[0])
     with pytest.raises(ValueError, match="scales go"):
-        B._kv_cache(x, x, x.float(), x.float(), x, 4, 64)
+        B._kv_cache(x, x, x.float(), x.float(), x, 4, 64, 0)
     with pytest.raises(ValueError, match="needs k_scale"):
-        B._kv_cache(x.view(torch.uint8), x.view(torch.uint8), None, None, x, 4, 128)
+        B._kv_cache(x.view(torch.uint8), x.view(torch.uint8), None, None, x, 4, 128, 0)
     with pytest.raises(ValueError, match="shape"):
-        B._kv_cache(x, x, None, None, x, 4, 64)          # 4 tokens to a page
+        B._kv_cache(x, x, None, None, x, 4, 64, 0)          # 4 tokens to a page
+    y = torch.zeros(2, 64, 4, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="CUDA"):
+        B._kv_cache(y, y, None, None, x, 4, 64, 0)
+    with pytest.raises(TypeError, match="k_cache must be"):
+        B._kv_cache(y.half(), y, None, None, x, 4, 64, 0)
+
+
+def test_the_cache_description_matches_the_c_struct(lib):
+    """The packed bytes that the binding hands over are the fields of dsa_kv_cache."""
+    from dsa_sparse_attention_fp8_gb300 import binding as B
+    values = list(range(1, 19))
+    got = B.KvCache.from_buffer_copy(B._KV_CACHE.pack(*values).ljust(ctypes.sizeof(B.KvCache), b"\0"))
+    assert [getattr(got, n) for n, _ in B.KvCache._fields_] == values
+    assert B._KV_CACHE.size <= ctypes.sizeof(B.KvCache) <= B._KV_CACHE.size + 4
