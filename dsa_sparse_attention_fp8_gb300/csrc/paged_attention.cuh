@@ -48,8 +48,6 @@ struct AttnParams {
 
 constexpr int kAttnTile = 128;        // keys per tile (two pages)
 constexpr int kAttnSoftmaxWarps = 8;
-// (A single token's rows are all in one warp of each stream, warps 0 and 5: the
-// scheduler of warps 0, 4, 8 ... has to spare the others' work.)
 constexpr int kAttnWalkWarp = 8;
 constexpr int kAttnMmaWarp = 9;       // and 10: one for each stream
 constexpr int kAttnTmaWarp = 11;
@@ -192,7 +190,7 @@ struct AttnItem {
   int kind;       // AttnKind
   int p0;         // position of the first token
   int lo[2], hi[2];  // positions of each stream's first and last token
-  int shift;         // rows of its tile that stream 1 leaves free before its own
+  int few;           // at most 32 rows to a stream: each of its warps has them all, and 32 of a tile's keys
   int from[2], step; // a stream's first key tile of the part, and how many on its next is
   int ns, skip;   // the request's key tile j0 + i is the part's i-th while that is below ns, else it is j0 + i + skip
   int j0;
@@ -444,19 +442,22 @@ struct AttnPages {
   }
 };
 
-// Joins the parts of a split unit, in CTA order: a warp per row, a lane per
-// DP / 32 elements.  Part k lies in slot 1 of the CTA in whose share the unit
-// begins, in slot 0 of the others.
+// Joins the parts of a unit, in order: a warp per row, a lane per DP / 32
+// elements.  A CTA's parts lie in its slot 1 if the unit begins in its share,
+// else in slot 0; of few rows there is one from each warp of the streams that
+// had the row.
 template <int DP, bool BF16>
 __device__ __noinline__ void attn_join(const AttnParams& p, const AttnItem& item, int warp, int lane) {
-  const int parts = item.c1 - item.c0 + 1;
+  const int lg = item.few ? (item.kind == kOneTile ? 3 : 2) : 0;  // parts of a CTA: 8, 4 or 1
+  const int parts = (item.c1 - item.c0 + 1) << lg;
   const int rows0 = min(item.ntok, p.tile_tokens) * p.group;  // rows of the first tile
   const int all = item.kind == kTwoHeads ? 2 * rows0 : item.ntok * p.group;
   for (int i = warp; i < all; i += kAttnSoftmaxWarps) {
     const bool second = i >= rows0;
     const int pr = second ? 128 + i - rows0 : i;
     auto at = [&](int k) -> int64_t {
-      return ((int64_t)(item.c0 + k) * 2 + (k == 0 && item.begins ? 1 : 0)) * 256 + pr;
+      const int cta = k >> lg, sub = k & ((1 << lg) - 1);
+      return ((int64_t)(item.c0 + cta) * 2 + (cta == 0 && item.begins ? 1 : 0)) * 256 + pr + sub * 32;
     };
     float top = -INFINITY;
     for (int k = lane; k < parts; k += 32) top = fmaxf(top, __ldcg(p.part_ml + at(k)).x);
@@ -625,10 +626,11 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
       {
         const uint32_t mine = at + 4 * x;
         const int lo = ATTN_AT(mine, lo), hi = ATTN_AT(mine, hi), step = ATTN_ITEM(step);
-        const int shift = x ? ATTN_ITEM(shift) : 0, row = tile_row - shift;
-        // some row of this warp is real
-        const bool live = tile_row - lane < (hi - lo + 1) * p.group + shift && tile_row - lane >= shift;
-        const int pos = min(lo + max(row, 0) / p.group, hi);
+        const bool few = FP8 && ATTN_ITEM(few);
+        const int row = few ? lane : tile_row;
+        const int from_key = few ? tile_row - lane : 0, to_key = few ? from_key + 32 : kAttnTile;  // this warp's keys
+        const bool live = row - lane < (hi - lo + 1) * p.group;  // some row of this warp is real
+        const int pos = min(lo + row / p.group, hi);
         const int ns = ATTN_ITEM(ns), skip = ATTN_ITEM(skip), j0 = ATTN_ITEM(j0), seq = ATTN_ITEM(seq);
         const int heads = ATTN_ITEM(kind) == kTwoHeads;
         float factor = p.scale_log2;  // of the row's scores
@@ -639,7 +641,7 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
           ++n_s;
           if (FP8 && j == ATTN_AT(mine, from)) {
             const uint32_t q = ATTN_ITEM(q0) + (ATTN_ITEM(kind) != kOneTile ? x : 0);
-            factor = p.scale_log2 * __uint_as_float(lds_u32(factor_s + ((q & 1) * 128 + tile_row) * 4));
+            factor = p.scale_log2 * __uint_as_float(lds_u32(factor_s + ((q & 1) * 128 + row) * 4));
             factor_read(at);
           }
           if (live) {
@@ -661,7 +663,7 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
             if (!(inner && bad == 0)) {
               // -inf over the scores that the row does not see
 #pragma unroll 1
-              for (int c = 0; c < kAttnTile; c += 32) {
+              for (int c = from_key; c < to_key; c += 32) {
                 uint32_t v[32];
                 tmem_ld<32>(base + c, v);
                 const uint32_t seen = attn_seen(p, pos - s0 - c, s0 + c, bad >> (c / 64) & 1u);
@@ -676,7 +678,7 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
             auto maximum = [&]() {
               float top = -INFINITY;
 #pragma unroll 1
-              for (int c = 0; c < kAttnTile; c += 32) {
+              for (int c = from_key; c < to_key; c += 32) {
                 uint32_t v[32];
                 tmem_ld<32>(base + c, v);
                 tmem_ld_wait32(v);
@@ -755,10 +757,20 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
               if (__any_sync(0xffffffffu, top > m + kAttnRescaleLog2)) raise(top, top > m + kAttnRescaleLog2);
               sums[0] = sums[1] = 0;
 #pragma unroll 1
-              for (int c = 0; c < kAttnTile; c += 32) {
+              for (int c = from_key; c < to_key; c += 32) {
                 uint32_t pr[16];
                 probabilities(c, pr);
                 tmem_st<16>(base + (c & 64) + (c & 32) / 2, pr);
+              }
+              if (few) {
+                // zeros for the other warps' keys: this warp's output rows are
+                // those of its own keys
+                uint32_t zero[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) zero[i] = 0;
+#pragma unroll 1
+                for (int c = 0; c < kAttnTile; c += 32)
+                  if (c != from_key) tmem_st<16>(base + (c & 64) + (c & 32) / 2, zero);
               }
               const float2 t = unpack2(add2(sums[0], sums[1]));
               sum = t.x + t.y;
@@ -800,8 +812,9 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
       const bool two = kind != kOneTile;  // each stream has rows of its own
       const int first = kind == kTwoTiles && x ? p.tile_tokens : 0;  // this stream's first token in the unit
       const int rows = min(p.tile_tokens, ATTN_ITEM(ntok) - first) * p.group;
-      const int shift = x ? ATTN_ITEM(shift) : 0, row = tile_row - shift;
-      const bool live = tile_row - lane < rows + shift && tile_row - lane >= shift;
+      const bool few = FP8 && ATTN_ITEM(few);
+      const int row = few ? lane : tile_row;
+      const bool live = row - lane < rows;
       const bool split = ATTN_ITEM(c0) != ATTN_ITEM(c1);
       if (two || x < n) {  // this stream had a tile
         wait(&sm->o_full[x], n_o & 1);
@@ -811,9 +824,10 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
       // which streams have an output, and its factors; where they share the
       // rows, all of their warps split the columns
       float f0 = 1.f, f1 = 1.f;
-      const bool has0 = two ? x == 0 : true, has1 = two ? x == 1 : n > 1;
-      const int cols = two ? DP : DP / 2, col0 = two ? 0 : x * (DP / 2);
-      if (!two) {
+      // (of few rows each warp has parts of its own, joined as a split unit's are)
+      const bool has0 = two || few ? x == 0 : true, has1 = two || few ? x == 1 && (two || n > 1) : n > 1;
+      const int cols = two || few ? DP : DP / 2, col0 = two || few ? 0 : x * (DP / 2);
+      if (!two && !few) {
         tc_fence_before();
         sm->swap[x][row] = m;
         named_bar_sync(1, kAttnSoftmaxWarps * 32);
@@ -828,11 +842,12 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
         tc_fence_after();  // the other stream's output is there: its warps came here after it
       }
       if (live && ok) {
-        const int prow = two ? x * 128 + row : row;
+        const int prow = few ? x * 128 + tile_row : two ? x * 128 + row : row;
         const int64_t part = ((int64_t)blockIdx.x * 2 + ATTN_ITEM(slot)) * 256 + prow;
         const int64_t token = ATTN_ITEM(token) + first + row / p.group;
         const int head = (ATTN_ITEM(head) + (kind == kTwoHeads ? x : 0)) * p.group + row % p.group;
-        const float inv = split ? 1.0f : (l > 0.f ? 1.0f / l : 0.f);
+        const bool parts = split || few;
+        const float inv = parts ? 1.0f : (l > 0.f ? 1.0f / l : 0.f);
         f0 *= inv;
         f1 *= inv;
 #pragma unroll 1
@@ -848,8 +863,8 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
             if (has0) o[i] = __uint_as_float(a[i]) * f0;
             if (has1) o[i] += __uint_as_float(b[i]) * f1;
           }
-          if (row >= 0 && row < rows && c < p.D) {
-            if (split) {
+          if (row < rows && c < p.D) {
+            if (parts) {
               float* dst = p.part + part * DP + c;
 #pragma unroll
               for (int i = 0; i < 16; i += 4)
@@ -864,32 +879,36 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
             }
           }
         }
-        if (row >= 0 && row < rows && col0 == 0) {
-          if (split)
+        if (row < rows && col0 == 0) {
+          if (parts)
             __stcg(p.part_ml + part, make_float2(m, l));
           else if (p.lse)
             p.lse[token * p.Hq + head] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
         }
       }
       tc_fence_before();
-      if (split) {
+      if (split || few) {
         // the unit's last CTA to arrive joins the parts, in CTA order
-        __threadfence();
+        if (split) __threadfence();
         named_bar_sync(1, kAttnSoftmaxWarps * 32);
-        if (threadIdx.x == 0) {
-          const int c0 = ATTN_ITEM(c0);
-          const bool last = atomicAdd(p.counter + c0, 1u) == (uint32_t)(ATTN_ITEM(c1) - c0);
-          if (last) p.counter[c0] = 0;
-          sm->last = last;
+        bool last = true;
+        if (split) {
+          if (threadIdx.x == 0) {
+            const int c0 = ATTN_ITEM(c0);
+            const bool all = atomicAdd(p.counter + c0, 1u) == (uint32_t)(ATTN_ITEM(c1) - c0);
+            if (all) p.counter[c0] = 0;
+            sm->last = all;
+          }
+          named_bar_sync(1, kAttnSoftmaxWarps * 32);
+          last = *(volatile int*)&sm->last != 0;
+          if (last) __threadfence();
         }
-        named_bar_sync(1, kAttnSoftmaxWarps * 32);
-        if (*(volatile int*)&sm->last) {
-          __threadfence();
-          attn_join<DP, BF16>(p, *(const AttnItem*)&sm->item[it % kAttnItems], warp, lane);
-        }
+        if (last) attn_join<DP, BF16>(p, *(const AttnItem*)&sm->item[it % kAttnItems], warp, lane);
+        // (the parts' places are free for the next unit's)
+        if (few && !split) named_bar_sync(1, kAttnSoftmaxWarps * 32);
       }
       // the other stream's warps may still read this one's output
-      if (!two) named_bar_sync(1, kAttnSoftmaxWarps * 32);
+      if (!two && !few) named_bar_sync(1, kAttnSoftmaxWarps * 32);
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sm->item_empty[it % kAttnItems]));
     }
@@ -956,12 +975,12 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
         __syncwarp();
         ++n_kv;
       };
-      // a query tile, or its first 32 rows' worth of tokens (`shift` rows down)
-      auto load_q = [&](int head, int token, bool few, int shift) {
+      // a query tile; of few rows, a box of them
+      auto load_q = [&](int head, int token, bool few) {
         const uint32_t st = n_q & 1, round = n_q >> 1;
         if (round > 0) wait(&sm->q_empty[st], (round - 1) & 1);
         if (!ok) return;
-        const uint32_t bar = smem_u32(&sm->q_full[st]), dst = q_s + st * C::kTileBytes + shift * 128;
+        const uint32_t bar = smem_u32(&sm->q_full[st]), dst = q_s + st * C::kTileBytes;
         const int tokens = few ? p.tile_tokens32 : p.tile_tokens;
         if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(C::kHalves * tokens * p.group * 128));
         __syncwarp();
@@ -1004,7 +1023,7 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
           const int queries = kind != kOneTile ? 2 : 1;
           for (int k = i; k < queries && (k == i || i + 1 == places); ++k)
             load_q(head + (k & heads), token + (kind == kTwoTiles && k ? p.tile_tokens : 0),
-                   ATTN_ITEM(ntok) <= p.tile_tokens32, k ? ATTN_ITEM(shift) : 0);
+                   ATTN_ITEM(ntok) <= p.tile_tokens32);
         }
         tile0 += n;
       };
@@ -1214,11 +1233,11 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
       // times 4: exact but for elements under 2^-9 of the row's maximum, which
       // are off by 2^-18 of it at most).  So Q K^T needs no conversion of K:
       // two products with its codes cost what one in 16 bits does.
-      auto split_q = [&](uint32_t place, int first, int rows) {
+      auto split_q = [&](uint32_t place, int rows, int copies) {
         if (!wait(&sm->q_full[place & 1], (place >> 1) & 1)) return false;
         const uint32_t tile = q_s + (place & 1) * C::kTileBytes;
 #pragma unroll 2
-        for (int r = first + cw; r < first + rows; r += 4) {
+        for (int r = cw; r < rows; r += 4) {
           // a lane's 4 elements
           const uint2 w = lds_v2(tile + (lane / 16) * 16384 + r * 128 + (((lane % 16 / 2) ^ (r & 7)) << 4) + 8 * (lane & 1));
           float f[4] = {__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
@@ -1241,8 +1260,10 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
           }
           __syncwarp();  // the whole row has been read
           const uint32_t to = tile + r * 128 + (((lane / 4) ^ (r & 7)) << 4) + 4 * (lane & 3);
-          sts_u32(to, c1);
-          sts_u32(to + 16384, c2);
+          for (int k = 0; k < copies; ++k) {  // of few rows, one for each 32 rows of the tile
+            sts_u32(to + k * 4096, c1);
+            sts_u32(to + k * 4096 + 16384, c2);
+          }
           if (lane == 0) sts_u32(factor_s + ((place & 1) * 128 + r) * 4, (e - 7u) << 23);  // 2^(exponent - 7)
         }
         fence_proxy_async_smem();
@@ -1255,8 +1276,9 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
         const int ntok = ATTN_ITEM(ntok);
         const uint32_t q0 = ATTN_ITEM(q0);
         const int kind = ATTN_ITEM(kind), rows = min(ntok, p.tile_tokens) * p.group;
-        if (!split_q(q0, 0, rows)) return;
-        if (kind != kOneTile && !split_q(q0 + 1, ATTN_ITEM(shift), kind == kTwoHeads ? rows : (ntok - p.tile_tokens) * p.group)) return;
+        const int copies = ATTN_ITEM(few) ? 4 : 1;
+        if (!split_q(q0, rows, copies)) return;
+        if (kind != kOneTile && !split_q(q0 + 1, kind == kTwoHeads ? rows : (ntok - p.tile_tokens) * p.group, copies)) return;
         // V's codes to BF16 (exactly), into the layout that its product reads
 #pragma unroll 1
         for (uint32_t t = tile0; t < tile0 + n; ++t) {
@@ -1334,7 +1356,10 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
             i->hi[0] = tiles ? w.unit.p0 + p.tile_tokens - 1 : last;
             i->lo[1] = tiles ? w.unit.p0 + p.tile_tokens : w.unit.p0;
             i->hi[1] = last;
-            i->shift = w.unit.kind == kTwoHeads && w.unit.ntok * p.group <= 32 ? 32 : 0;
+            // (16-bit caches: the joins cost more than the shorter tiles give, 28.8
+            // instead of 20.6 us for one request of 1,024 tokens, 218 instead of
+            // 201 us for 64; E4M3: 473 instead of 559 us for four of 231,000)
+            i->few = FP8 && w.unit.ntok <= p.tile_tokens32;
             i->from[0] = 0;
             i->from[1] = tiles ? 0 : 1;
             i->step = tiles ? 1 : 2;
