@@ -530,3 +530,35 @@ def test_tables_write_attention_together(B, ws):
         b.c, b.T, b.q, b.scale = Case(q_lens, seq, heads=heads, kv=h, d=d), T, q, d ** -0.5
         b.kv = [[x.double().cpu(), y.double().cpu()] for x, y in zip(ks, vs)]
         b.check(out, lse)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_the_example_attends_over_what_it_wrote(B, fp8):
+    """The example's steps: attention of the last step equals attention over the kept keys and values."""
+    import importlib.util
+
+    from conftest import ROOT
+    spec = importlib.util.spec_from_file_location("serve_step", ROOT / "examples" / "serve_step.py")
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    layer = ex.WindowLayer(requests=3, width=384, heads=8, kv_heads=2, dim=64, window=100, sinks=3, fp8_cache=fp8)
+    torch.manual_seed(2)
+    kept, lens = [[[], []] for _ in range(3)], [0, 0, 0]
+    for new in ([150, 1, 70], [1, 1, 1], [3, 1, 1]):
+        lens = [a + b for a, b in zip(lens, new)]
+        T = sum(new)
+        out, qkv, positions = layer.step(torch.randn(T, 384, device="cuda").to(BF), torch.randn(T, 384, device="cuda").to(BF),
+                                         ints(new), ints(lens))
+        assert positions.tolist() == [p for n, c in zip(new, lens) for p in range(c - n, c)]
+        for r, rows in enumerate(qkv.split(new)):
+            for i, part in enumerate((rows[:, 8:10], rows[:, 10:])):
+                if fp8:
+                    codes, sc = quantised(part)
+                    part = codes.view(torch.float8_e4m3fn).double() * sc.double()[..., None]
+                kept[r][i].append(part.double().cpu())
+    assert int(layer.status) == 0
+    b = Batch.__new__(Batch)
+    b.c, b.T, b.q, b.scale = Case([3, 1, 1], lens, heads=8, kv=2, d=64, window=100, sinks=3), T, qkv[:, :8], 64 ** -0.5
+    b.kv = [[torch.cat(k), torch.cat(v)] for k, v in kept]
+    o, ob, _, _ = b.reference()
+    assert ((out.double().cpu() - o).abs() <= ob).all()
