@@ -215,6 +215,10 @@ struct AttnSmem {
   float swap[2][128];    // a value of each row, between the two streams
 };
 static_assert(sizeof(AttnSmem) <= 3072, "shared memory");
+static_assert(AttnCfg<128, false>::kStages <= 8 && AttnCfg<64, false>::kStages <= 8 &&
+                  AttnCfg<128, true>::kKStages + AttnCfg<128, true>::kVStages <= 8 &&
+                  AttnCfg<128, true>::kVRawStages <= 2 && AttnCfg<128, true>::kScaleTiles <= 8,
+              "a barrier for each place of a ring");
 
 // The order in which an item's K and V tiles are loaded, as places in the
 // ring: K0 V0 K1 V1 ... where the streams share the tiles, and K0 K1 V0 K2 V1
