@@ -21,6 +21,10 @@ using namespace dsa_host;
 
 int element_bytes(int type) { return type == DSA_TYPE_FP32 ? 4 : type == DSA_TYPE_E4M3 ? 1 : 2; }
 
+// Whether a stride over n elements is neither negative nor off a multiple of
+// `unit` (one element may have any stride: nothing is ever a stride away).
+bool stride_ok(int64_t stride, int64_t n, int unit) { return n <= 1 || (stride >= 0 && stride % unit == 0); }
+
 // A K/V cache as the kernels need it: 16-byte aligned heads, at most 128
 // elements each.
 int check_cache(const dsa_kv_cache* c, int type) {
@@ -35,18 +39,20 @@ int check_cache(const dsa_kv_cache* c, int type) {
   if (c->num_pages < 1 || c->num_pages > INT32_MAX / DSA_PAGE_TOKENS)
     return fail(DSA_ERR_INVALID_ARG, "num_pages=%lld outside [1, %d]", (long long)c->num_pages,
                 INT32_MAX / DSA_PAGE_TOKENS);
-  const int size = element_bytes(c->type);
-  const int64_t strides[6] = {c->k_page_stride, c->k_token_stride, c->k_head_stride,
-                              c->v_page_stride, c->v_token_stride, c->v_head_stride};
-  for (int64_t s : strides)
-    if (s < 0 || s * size % 16) return fail(DSA_ERR_INVALID_ARG, "cache strides must be multiples of 16 bytes");
+  const int unit = 16 / element_bytes(c->type);
+  const int64_t pages = c->num_pages, heads = c->num_kv_heads;
+  if (!stride_ok(c->k_page_stride, pages, unit) || !stride_ok(c->v_page_stride, pages, unit) ||
+      !stride_ok(c->k_token_stride, DSA_PAGE_TOKENS, unit) || !stride_ok(c->v_token_stride, DSA_PAGE_TOKENS, unit) ||
+      !stride_ok(c->k_head_stride, heads, unit) || !stride_ok(c->v_head_stride, heads, unit))
+    return fail(DSA_ERR_INVALID_ARG, "cache strides must be multiples of 16 bytes");
   if (!c->k || !c->v) return fail(DSA_ERR_INVALID_ARG, "null cache pointer");
   if (!aligned(c->k, 16) || !aligned(c->v, 16))
     return fail(DSA_ERR_INVALID_ARG, "the caches must be 16-byte aligned");
   if (c->type == DSA_TYPE_E4M3) {
     if (!c->k_scale || !c->v_scale) return fail(DSA_ERR_INVALID_ARG, "an E4M3 cache needs k_scale and v_scale");
-    if (!aligned(c->k_scale, 16) || !aligned(c->v_scale, 16) || c->k_scale_page_stride % 4 ||
-        c->k_scale_head_stride % 4 || c->v_scale_page_stride % 4 || c->v_scale_head_stride % 4)
+    if (!aligned(c->k_scale, 16) || !aligned(c->v_scale, 16) || !stride_ok(c->k_scale_page_stride, pages, 4) ||
+        !stride_ok(c->v_scale_page_stride, pages, 4) || !stride_ok(c->k_scale_head_stride, heads, 4) ||
+        !stride_ok(c->v_scale_head_stride, heads, 4))
       return fail(DSA_ERR_INVALID_ARG, "scales must be 16-byte aligned, strides multiples of 4 elements");
   }
   return DSA_OK;
@@ -206,8 +212,9 @@ int dsa_kv_write(const void* k, int64_t k_token_stride, int64_t k_head_stride, c
   if (const int rc = check_cache(cache, type)) return rc;
   if (T == 0) return DSA_OK;
   if (!k || !v || !slot_mapping) return fail(DSA_ERR_INVALID_ARG, "null pointer");
-  if (!aligned(k, 16) || !aligned(v, 16) || k_token_stride % 8 || k_head_stride % 8 || v_token_stride % 8 ||
-      v_head_stride % 8)
+  const int heads = cache->num_kv_heads;
+  if (!aligned(k, 16) || !aligned(v, 16) || !stride_ok(k_token_stride, T, 8) || !stride_ok(v_token_stride, T, 8) ||
+      !stride_ok(k_head_stride, heads, 8) || !stride_ok(v_head_stride, heads, 8))
     return fail(DSA_ERR_INVALID_ARG, "k and v must be 16-byte aligned, strides multiples of 8 elements");
   dsa::KvWriteParams p{};
   p.src[0] = static_cast<const uint16_t*>(k);
@@ -264,8 +271,8 @@ int dsa_paged_attention(const void* q, int64_t q_token_stride, int64_t q_head_st
   if (T == 0) return DSA_OK;
   if (!q || !query_start_loc || !seq_lens || !block_table || !out || !workspace)
     return fail(DSA_ERR_INVALID_ARG, "null pointer");
-  if (!aligned(q, 16) || !aligned(out, 16) || q_token_stride % 8 || q_head_stride % 8 || out_token_stride % 8 ||
-      out_head_stride % 8)
+  if (!aligned(q, 16) || !aligned(out, 16) || !stride_ok(q_token_stride, T, 8) || !stride_ok(q_head_stride, Hq, 8) ||
+      !stride_ok(out_token_stride, T, 8) || !stride_ok(out_head_stride, Hq, 8))
     return fail(DSA_ERR_INVALID_ARG, "q and out must be 16-byte aligned, strides multiples of 8 elements");
   if (!aligned(workspace, 256)) return fail(DSA_ERR_INVALID_ARG, "workspace is not 256-byte aligned");
   const size_t need = dsa_paged_attention_workspace_bytes();

@@ -461,7 +461,8 @@ int dsa_block_tables_build(const int32_t* query_lens, const int32_t* seq_lens, i
  * one pool, all fit), the last dimension contiguous.  E4M3 caches have one
  * FP32 scale per (token, head): k_scale and v_scale [num_pages,
  * num_kv_heads, 64], the last dimension contiguous; value = code * scale.
- * Strides are in elements.  head_dim: a multiple of 16 in [16, 128].
+ * Strides are in elements, not negative; a dimension of one element may have
+ * any.  head_dim: a multiple of 16 in [16, 128].
  */
 typedef struct {
   void* k;
@@ -517,7 +518,10 @@ int dsa_kv_write(const void* k, int64_t k_token_stride, int64_t k_head_stride, c
  * > 64*max_blocks: DSA_STATUS_BAD_METADATA; a table entry outside the pool
  * under a token that is seen: DSA_STATUS_BAD_PAGE, its tokens are skipped.
  * Computation: tensor-core products with FP32 accumulation, FP32 softmax
- * statistics, probabilities rounded to 16 bits.
+ * statistics, probabilities rounded to 16 bits.  Over an E4M3 cache a query
+ * row enters as the sum of two E4M3 terms over a scale of its own (within
+ * 2^-8 of each element, as BF16 itself is, or 2^-18 of the row's largest) and
+ * V's codes times a probability times the token's scale as BF16.
  * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE_TOO_SMALL, CUDA.
  */
 size_t dsa_paged_attention_workspace_bytes(void);

@@ -454,6 +454,36 @@ def test_attention_in_a_graph_reads_new_lengths(B, ws):
         short.check(out, lse)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_dimensions_of_one_with_odd_strides(B, ws, fp8):
+    """One key head, one page, one row, one query head, each with a stride that would be refused over more."""
+    torch.manual_seed(8)
+    d, n = 64, 40
+
+    def odd(t, dim):  # the same view with an odd stride at a dimension of one element
+        assert t.shape[dim] == 1
+        return t.as_strided(t.shape, [3 if i == dim else s for i, s in enumerate(t.stride())])
+    k, v = torch.randn(n, 1, d, device="cuda").to(BF), torch.randn(n, 1, d, device="cuda").to(BF)
+    kc, vc = (odd(odd(torch.zeros(1, 64, 1, d, dtype=torch.uint8 if fp8 else BF, device="cuda"), 0), 2) for _ in "kv")
+    ks, vs = (odd(torch.zeros(1, 64, 1, device="cuda").transpose(1, 2), 1) for _ in "kv") if fp8 else (None, None)
+    status = ints([0])
+    B.kv_write(odd(k, 1), odd(v, 1), torch.arange(n, device="cuda"), kc, vc, ks, vs, status=status)
+    q = odd(odd(torch.randn(1, 1, d, device="cuda").to(BF), 0), 1)
+    out, lse = B.paged_attention(q, kc, vc, ints([0, 1]), ints([n]), ints([[0]]), d ** -0.5, ws, k_scale=ks, v_scale=vs,
+                                 status=status)
+    torch.cuda.synchronize()
+    assert status.item() == 0
+    b = Batch.__new__(Batch)
+    b.c, b.T, b.q, b.scale = Case([1], [n], heads=1, kv=1, d=d, fp8=fp8), 1, q.contiguous(), d ** -0.5
+    b.kv = [[]]
+    for x in (k, v):
+        if fp8:
+            c, s = quantised(x)
+            x = c.view(torch.float8_e4m3fn).double() * s.double()[..., None]
+        b.kv[0].append(x.double().cpu())
+    b.check(out, lse)
+
+
 # ------------------------------------------------------------------ norm
 @pytest.mark.parametrize("dtype", [BF, HF, torch.float32])
 @pytest.mark.parametrize("T,N", [(1, 1), (3, 7), (2, 128), (5, 129), (2, 1000), (3, 2048), (2, 2560), (4, 7168),

@@ -46,6 +46,18 @@ def test_bad_caches_are_refused(lib, change, code):
     assert attention(lib, c) == code and lib.dsa_last_error()
 
 
+def test_a_dimension_of_one_may_have_any_stride(lib):
+    """Nothing is ever a stride away (a transposed [pages, 64, 1] scale counts as contiguous with a head stride of 1)."""
+    one = dict(num_kv_heads=1, num_pages=1, type=3, k_scale=0x1000, v_scale=0x1000, k_page_stride=7, v_page_stride=-3,
+               k_head_stride=1, v_head_stride=5, k_scale_page_stride=3, v_scale_page_stride=-1, k_scale_head_stride=1,
+               v_scale_head_stride=2)
+    c = cache(**one)
+    assert write(lib, c, T=0) == 0 and attention(lib, c, T=0) == 0
+    for name, size in (("num_kv_heads", 8), ("num_pages", 16)):
+        assert write(lib, cache(**{**one, name: size}), T=0) == -1
+    assert write(lib, cache(type=3, k_scale=0x1000, v_scale=0x1000, k_scale_page_stride=-4), T=0) == -1
+
+
 def test_attention_refusals(lib):
     c = cache()
     assert attention(lib, None) == -1
