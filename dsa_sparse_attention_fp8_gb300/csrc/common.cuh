@@ -5,6 +5,8 @@
 #include <cuda_fp8.h>
 #include <cstdint>
 
+#include "ptx.cuh"
+
 namespace dsa {
 
 constexpr int kPageTokens = 64;
@@ -29,27 +31,30 @@ __device__ __forceinline__ int find_request(const int32_t* __restrict__ qsl, int
 }
 
 // E4M3 codes of 8 values over a common scale, E4M3(x / s) with IEEE FP32
-// division, nearest even, saturating; two codes to a word's lower half.  The
-// quotient is taken as x * (1 / s), at most 2 units in the last place off,
-// which changes no code unless it lies that near to a border between two
-// codes: in the normal range those are the values whose lower 20 bits are
-// 0x80000.  There, and in E4M3's subnormal range, the division is done.
-__device__ __forceinline__ void quantize8(const float* x, float s, uint32_t* codes) {
+// division, nearest even, saturating; four codes to a word.  The quotient lies
+// between x * (1 / s) a little too small and a little too large (1 / s, the
+// factor, the product and the division are each off by 2^-24 at most, the
+// factors are 2^-21 apart from 1): where both round to the same code, that is
+// the quotient's, and only where they do not, some 1 in 10^5 values, is the
+// division done.  (Below 1e-30 the reciprocal of s may overflow.)
+__device__ __forceinline__ uint2 quantize8(const float* x, float s) {
   const float inv = __fdiv_rn(1.0f, s);
-  float q[8];
-  bool near = s < 1e-30f;
+  const uint64_t lo = pack2(inv * (1.0f - 0x1p-21f), inv * (1.0f - 0x1p-21f));
+  const uint64_t hi = pack2(inv * (1.0f + 0x1p-21f), inv * (1.0f + 0x1p-21f));
+  uint32_t c[4], differ = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    q[i] = x[i] * inv;
-    near |= ((__float_as_uint(q[i]) - 0x7FFFCu) & 0xFFFFFu) <= 8u || fabsf(q[i]) < 0.015625f;
+  for (int i = 0; i < 4; ++i) {
+    const uint64_t v = pack2(x[2 * i], x[2 * i + 1]);
+    c[i] = __nv_cvt_float2_to_fp8x2(unpack2(mul2(v, lo)), __NV_SATFINITE, __NV_E4M3);
+    differ |= c[i] ^ __nv_cvt_float2_to_fp8x2(unpack2(mul2(v, hi)), __NV_SATFINITE, __NV_E4M3);
   }
-  if (near) {
+  if (differ || s < 1e-30f) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(x[i], s);
+    for (int i = 0; i < 4; ++i)
+      c[i] = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(x[2 * i], s), __fdiv_rn(x[2 * i + 1], s)), __NV_SATFINITE,
+                                      __NV_E4M3);
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    codes[i] = __nv_cvt_float2_to_fp8x2(make_float2(q[2 * i], q[2 * i + 1]), __NV_SATFINITE, __NV_E4M3) & 0xFFFFu;
+  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
 }  // namespace dsa

@@ -92,12 +92,10 @@ __global__ void __launch_bounds__(kKvThreads) kv_write_kernel(const __grid_const
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
       const float s = amax == 0.f ? 1.0f : __fdiv_rn(amax, 448.0f);
-      uint32_t c[4];
-      quantize8(f, s, c);
+      const uint2 c = quantize8(f, s);
       if (live) {
         if (lane * 8 < p.dim)
-          *reinterpret_cast<uint2*>(dst + lane * 8) =
-              make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+          *reinterpret_cast<uint2*>(dst + lane * 8) = c;
         if (lane == 0) p.scale[w][page * p.scale_page[w] + head[i] * p.scale_head[w] + off] = s;
       }
     }

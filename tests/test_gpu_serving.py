@@ -195,6 +195,34 @@ def test_kv_write(B, T, h, d, dtype, fp8, layout):
         assert torch.equal(got, w)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_kv_write_codes_near_borders(B, dtype):
+    """Codes are those of the IEEE quotient, ties and subnormal codes included: rows over every exponent below their
+    maximum, with maxima that make the quotients exact, and with ones that do not."""
+    torch.manual_seed(5)
+    T, h, d = 600, 2, 128
+    x = torch.randint(0, 1 << 15, (T, 2 * h, d)).short()
+    top = 0x4000 + torch.randint(0, 200, (T, 2 * h)).short()
+    top[::2] = torch.tensor(448.0, dtype=dtype).view(torch.int16)      # s = 1: many quotients are ties
+    x = torch.minimum(x, top[..., None])                               # (positive bit patterns order like their values)
+    # near the maximum too, where codes are coarse
+    x[:, :, ::3] = torch.maximum(top[..., None] - x[:, :, ::3] % 2000, torch.tensor(0, dtype=torch.int16))
+    x[:, :, 0] = top
+    x = x.contiguous().view(dtype) * (1 - 2 * torch.randint(0, 2, (T, 2 * h, d))).to(dtype)
+    x = x.cuda()
+    pages = T // 64 + 1
+    kc, vc = (torch.zeros(pages, 64, h, d, dtype=torch.uint8, device="cuda") for _ in "kv")
+    ks, vs = (torch.zeros(pages, h, 64, device="cuda") for _ in "kv")
+    status = ints([0])
+    B.kv_write(x[:, :h], x[:, h:], torch.arange(T, device="cuda"), kc, vc, ks, vs, status=status)
+    torch.cuda.synchronize()
+    assert status.item() == 0
+    for cache, scale, rows in ((kc, ks, x[:, :h]), (vc, vs, x[:, h:])):
+        codes, want = quantised(rows)
+        assert torch.equal(scale.transpose(1, 2).reshape(-1, h)[:T], want)
+        assert torch.equal(cache.view(-1, h, d)[:T], codes)
+
+
 # ------------------------------------------------------------------ attention
 @dataclasses.dataclass
 class Case:
@@ -529,6 +557,12 @@ def test_norm(B, T, N, dtype):
     y3 = torch.empty(T, N, dtype=dtype, device="cuda")
     B.add_rms_norm(h, None, wd, 1e-6, out=y3)
     assert torch.equal(y3, y)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("T,N", [(1300, 1024), (1217, 1033), (1400, 7168)])
+def test_norm_of_many_rows(B, T, N, dtype):
+    test_norm(B, T, N, dtype)
 
 
 def test_tables_write_attention_together(B, ws):
