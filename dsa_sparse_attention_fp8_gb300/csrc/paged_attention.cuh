@@ -43,7 +43,7 @@ struct AttnParams {
   int sink_tiles;              // ceil(sinks / 128)
   float* part;                 // [grid][2][256][DP] split units' outputs ...
   float2* part_ml;             // [grid][2][256] ... their maxima and sums ...
-  uint32_t* counter;           // [grid] ... and the parts that have arrived
+  uint32_t* counter;           // [3][kAttnMaxGrid] ... and the parts that have arrived (see below)
 };
 
 constexpr int kAttnTile = 128;        // keys per tile (two pages)
@@ -60,6 +60,18 @@ constexpr float kAttnMostSum = 16384.0f;
 constexpr float kAttnRescaleLog2 = 8.0f;  // (with E4M3 caches: when the maximum grows by more than 2^8)
 constexpr int64_t kAttnMaxShare = 1 << 23;  // cost of a CTA's work, in 32 bits
 constexpr int kAttnUnitCharge = 1;    // a unit's set-up, in key tiles
+// Parts of a unit split over more CTAs than this are joined in groups first,
+// by one CTA of each group (one request of 100,000 tokens over one key head,
+// bf16: of 128 query heads 96 us, 362 if one CTA joins all parts; of 8 26 and
+// 41; four requests of 20,000 over four key heads, 10 parts each: 54).  A
+// unit's count
+// of arrivals is at its first CTA, that of its first group kAttnMaxGrid further
+// on, those of the other groups at the group's first CTA another kAttnMaxGrid
+// further on (two units share a CTA only as the last one of the one and the
+// first of the other).
+constexpr int kAttnUngrouped = 24;
+constexpr int kAttnGroup = 12;
+static_assert(kAttnUngrouped <= 32 && kAttnGroup <= 32 && (kAttnMaxGrid + kAttnGroup - 1) / kAttnGroup <= 32, "parts of a join");
 
 // A unit of work: the query rows of one request that two streams of 128 rows
 // take at a time, over the key tiles that any of its rows sees: the first `ns`
@@ -446,59 +458,90 @@ struct AttnPages {
   }
 };
 
-// Joins the parts of a unit, in order: a warp per row, a lane per DP / 32
-// elements.  A CTA's parts lie in its slot 1 if the unit begins in its share,
-// else in slot 0; of few rows there is one from each warp of the streams that
-// had the row.
-template <int DP, bool BF16>
-__device__ __noinline__ void attn_join(const AttnParams& p, const AttnItem& item, int warp, int lane) {
-  const int lg = item.few ? (item.kind == kOneTile ? 3 : 2) : 0;  // parts of a CTA: 8, 4 or 1
-  const int parts = (item.c1 - item.c0 + 1) << lg;
+// Joins parts of a unit, in order: a warp per row, a lane per DP / 32 elements.
+// Of few rows each warp of the streams that had a row has a part of its own.
+//   kJoinWarps  those of this CTA's warps
+//   kJoinGroup  of a unit split over many CTAs: those of this CTA's group
+//   kJoinUnit   the unit's: those of its CTAs' warps, of its CTAs, or of their
+//               groups, whichever come to at most kAttnUngrouped
+// into the output, or (where that is not all of the unit) into the first one's
+// place.  A CTA's parts lie in its slot 1 if the unit begins in its share, else
+// in slot 0.  Bound by the latency of its loads, of which a lane has W under
+// way; there are at most 32 parts.
+enum AttnJoin : int { kJoinWarps, kJoinGroup, kJoinUnit };
+// log2 of a CTA's parts
+__device__ __forceinline__ int attn_lg_parts(int few, int kind) { return few ? (kind == kOneTile ? 3 : 2) : 0; }
+template <int DP, bool BF16, int W>
+__device__ __noinline__ void attn_join(const AttnParams& p, const AttnItem& item, int what, int warp, int lane) {
+  const int ctas = item.c1 - item.c0 + 1, mine = (int)blockIdx.x - item.c0;
+  const int lg_all = attn_lg_parts(item.few, item.kind);
+  const int lg = what == kJoinWarps || (what == kJoinUnit && ctas << lg_all <= kAttnUngrouped) ? lg_all : 0;
+  const int step = what == kJoinUnit && ctas > kAttnUngrouped ? kAttnGroup : 1;
+  const int first = what == kJoinWarps ? mine : what == kJoinGroup ? mine / kAttnGroup * kAttnGroup : 0;
+  const int parts = (what == kJoinWarps   ? 1
+                     : what == kJoinGroup ? min(kAttnGroup, ctas - first)
+                                          : (ctas + step - 1) / step) << lg;
+  const bool into_part = what == kJoinGroup || (what == kJoinWarps && ctas > 1);
   const int rows0 = min(item.ntok, p.tile_tokens) * p.group;  // rows of the first tile
   const int all = item.kind == kTwoHeads ? 2 * rows0 : item.ntok * p.group;
   for (int i = warp; i < all; i += kAttnSoftmaxWarps) {
     const bool second = i >= rows0;
     const int pr = second ? 128 + i - rows0 : i;
     auto at = [&](int k) -> int64_t {
-      const int cta = k >> lg, sub = k & ((1 << lg) - 1);
-      return ((int64_t)(item.c0 + cta) * 2 + (cta == 0 && item.begins ? 1 : 0)) * 256 + pr + sub * 32;
+      const int cta = first + (k >> lg) * step;
+      return ((int64_t)(item.c0 + cta) * 2 + (cta == 0 && item.begins ? 1 : 0)) * 256 + pr +
+             (k & ((1 << lg) - 1)) * 32;
     };
-    float top = -INFINITY;
-    for (int k = lane; k < parts; k += 32) top = fmaxf(top, __ldcg(p.part_ml + at(k)).x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    float sum = 0.f, acc[DP / 32];
+    const float2 ml = lane < parts ? __ldcg(p.part_ml + at(lane)) : make_float2(-INFINITY, 0.f);
+    float top = ml.x, f = 0.f, acc[DP / 32];
 #pragma unroll
     for (int c = 0; c < DP / 32; ++c) acc[c] = 0.f;
-    for (int k0 = 0; k0 < parts; k0 += 32) {
-      float f = 0.f;
-      if (k0 + lane < parts) {
-        const float2 v = __ldcg(p.part_ml + at(k0 + lane));
-        f = v.x == -INFINITY ? 0.f : ex2(v.x - top);
-        sum += v.y * f;
-      }
-      const int most = min(32, parts - k0);
-#pragma unroll 4
-      for (int k = 0; k < most; ++k) {
-        const float fk = __shfl_sync(0xffffffffu, f, k);
-        const float* src = p.part + at(k0 + k) * DP + lane * (DP / 32);
-        if (lane * (DP / 32) < p.D) {
-          if (DP == 128) {
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
-            acc[0] += v.x * fk;
-            acc[1] += v.y * fk;
-            acc[2 % (DP / 32)] += v.z * fk;
-            acc[3 % (DP / 32)] += v.w * fk;
+    for (int k0 = 0; k0 < parts; k0 += W) {
+      float v[W][DP / 32];
+#pragma unroll
+      for (int k = 0; k < W; ++k) {
+#pragma unroll
+        for (int c = 0; c < DP / 32; ++c) v[k][c] = 0.f;
+        if (k0 + k < parts && lane * (DP / 32) < p.D) {
+          const float* src = p.part + at(k0 + k) * DP + lane * (DP / 32);
+          if constexpr (DP == 128) {
+            const float4 w = __ldcg(reinterpret_cast<const float4*>(src));
+            v[k][0] = w.x;
+            v[k][1] = w.y;
+            v[k][2] = w.z;
+            v[k][3] = w.w;
           } else {
-            const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
-            acc[0] += v.x * fk;
-            acc[1] += v.y * fk;
+            const float2 w = __ldcg(reinterpret_cast<const float2*>(src));
+            v[k][0] = w.x;
+            v[k][1] = w.y;
           }
         }
       }
+      if (k0 == 0) {  // (while the loads above are under way)
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        f = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
+      }
+#pragma unroll
+      for (int k = 0; k < W; ++k) {
+        const float fk = __shfl_sync(0xffffffffu, f, k0 + k);
+#pragma unroll
+        for (int c = 0; c < DP / 32; ++c) acc[c] += v[k][c] * fk;
+      }
     }
+    float sum = ml.y * f;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (into_part) {
+      const int64_t part = at(0);
+      if (lane * (DP / 32) < p.D) {
+#pragma unroll
+        for (int c = 0; c < DP / 32; c += 2)
+          __stcg(reinterpret_cast<float2*>(p.part + part * DP + lane * (DP / 32) + c), make_float2(acc[c], acc[c + 1]));
+      }
+      if (lane == 0) __stcg(p.part_ml + part, make_float2(top, sum));
+      continue;
+    }
     const float r = sum > 0.f ? 1.0f / sum : 0.f;
     const bool other_head = item.kind == kTwoHeads && second;
     const int k = other_head ? i - rows0 : i;
@@ -891,25 +934,34 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
         }
       }
       tc_fence_before();
-      if (split || few) {
-        // the unit's last CTA to arrive joins the parts, in CTA order
-        if (split) __threadfence();
+      const int c0 = ATTN_ITEM(c0), ctas = ATTN_ITEM(c1) - c0 + 1;
+      if (few && (!split || ctas << attn_lg_parts(1, kind) > kAttnUngrouped)) {
         named_bar_sync(1, kAttnSoftmaxWarps * 32);
-        bool last = true;
-        if (split) {
+        attn_join<DP, BF16, 4>(p, *(const AttnItem*)&sm->item[it % kAttnItems], kJoinWarps, warp, lane);
+        // (the parts' places are free for the next unit's)
+        if (!split) named_bar_sync(1, kAttnSoftmaxWarps * 32);
+      }
+      if (split) {
+        // the last CTA of a group to arrive, then the last of a unit, joins the
+        // parts, in CTA order
+        for (int what = ctas > kAttnUngrouped ? kJoinGroup : kJoinUnit; what <= kJoinUnit; ++what) {
+          __threadfence();
+          named_bar_sync(1, kAttnSoftmaxWarps * 32);
           if (threadIdx.x == 0) {
-            const int c0 = ATTN_ITEM(c0);
-            const bool all = atomicAdd(p.counter + c0, 1u) == (uint32_t)(ATTN_ITEM(c1) - c0);
-            if (all) p.counter[c0] = 0;
+            const int first = ((int)blockIdx.x - c0) / kAttnGroup * kAttnGroup;
+            uint32_t* const count = p.counter + c0 + (what == kJoinUnit ? 0 : kAttnMaxGrid + (first ? kAttnMaxGrid + first : 0));
+            const int most = what == kJoinGroup       ? min(kAttnGroup, ctas - first)
+                             : ctas > kAttnUngrouped ? (ctas + kAttnGroup - 1) / kAttnGroup
+                                                     : ctas;
+            const bool all = atomicAdd(count, 1u) == (uint32_t)(most - 1);
+            if (all) *count = 0;
             sm->last = all;
           }
           named_bar_sync(1, kAttnSoftmaxWarps * 32);
-          last = *(volatile int*)&sm->last != 0;
-          if (last) __threadfence();
+          if (!*(volatile int*)&sm->last) break;
+          __threadfence();
+          attn_join<DP, BF16, 12>(p, *(const AttnItem*)&sm->item[it % kAttnItems], what, warp, lane);
         }
-        if (last) attn_join<DP, BF16>(p, *(const AttnItem*)&sm->item[it % kAttnItems], warp, lane);
-        // (the parts' places are free for the next unit's)
-        if (few && !split) named_bar_sync(1, kAttnSoftmaxWarps * 32);
       }
       // the other stream's warps may still read this one's output
       if (!two && !few) named_bar_sync(1, kAttnSoftmaxWarps * 32);

@@ -86,8 +86,8 @@ int attention_grid() {
 
 // Workspace: arrival counters of split units, then their parts' maxima and
 // sums and their outputs (two slots of 256 rows for every CTA).
-constexpr size_t kAttnCounterBytes = 1024;
-static_assert(kAttnCounterBytes >= dsa::kAttnMaxGrid * 4, "counters");
+constexpr size_t kAttnCounterBytes = 2048;
+static_assert(kAttnCounterBytes >= 3 * dsa::kAttnMaxGrid * 4, "counters");
 size_t attention_part_rows() { return (size_t)attention_grid() * 2 * 256; }
 
 // A map over up to four dimensions, innermost first; strides in bytes (of

@@ -462,6 +462,21 @@ def test_attention_without_optional_outputs_and_on_a_stream(B, ws):
     assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("heads,d,q,seq", [(4, 128, [1, 2], [30011, 20500]), (128, 64, [1, 0, 1], [16001, 9, 33000]),
+                                           (48, 128, [5], [25003])])
+def test_units_split_over_many_ctas(B, ws, heads, d, q, seq, fp8):
+    """One key head and few requests: each unit is most of the grid's work, its parts joined in groups; again and again
+    the same bits, so every call leaves the counts of arrivals at zero."""
+    b = Batch(Case(q, seq, heads=heads, kv=1, d=d, fp8=fp8))
+    out, lse, status = b.run(B, ws)
+    assert status == 0
+    b.check(out, lse)
+    for _ in range(3):
+        again = b.run(B, ws)
+        assert torch.equal(again[0], out) and torch.equal(again[1], lse)
+
+
 def test_attention_in_a_graph_reads_new_lengths(B, ws):
     c = Case([1, 1, 1], [500, 64, 1000])
     b = Batch(c)
