@@ -41,7 +41,7 @@ struct AttnParams {
   int tile_tokens;             // tokens of a 128-row query tile: 128 / group
   int tile_tokens32;           // tokens of 32 rows: 32 / group
   int sink_tiles;              // ceil(sinks / 128)
-  float* part;                 // [grid][2][256][DP] split units' outputs ...
+  float* part;                 // [grid][2][DP / 4][256][4] split units' outputs ...
   float2* part_ml;             // [grid][2][256] ... their maxima and sums ...
   uint32_t* counter;           // [3][kAttnMaxGrid] ... and the parts that have arrived (see below)
 };
@@ -272,7 +272,11 @@ __device__ __forceinline__ int64_t attn_divide(int64_t a, int64_t b) {
 __device__ __forceinline__ void attn_locate(const AttnParams& p, AttnSmem* sm, int* len, int* share_out) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int threads = (int)blockDim.x, per = (p.R + threads - 1) / threads;
-  const int r0 = threadIdx.x * per;
+  // (one request a thread: neighbours in different warps, which have to sum the
+  // requests of several units one after the other)
+  const int r0 = per > 1 ? threadIdx.x * per : lane * (threads / 32) + warp;
+  extern __shared__ __align__(1024) unsigned char attn_smem[];
+  int64_t* const costs = reinterpret_cast<int64_t*>(attn_smem);  // (before anything else is there)
   // cost of request r; lanes of a warp call it together
   auto cost = [&](int r, bool* bad) -> int64_t {
     int row0 = 0, q = 0, seq = 0;
@@ -317,6 +321,12 @@ __device__ __forceinline__ void attn_locate(const AttnParams& p, AttnSmem* sm, i
       }
     }
     if (phase == 1) break;
+    if (per == 1) {
+      costs[r0] = sum;
+      __syncthreads();
+      sum = costs[threadIdx.x];
+      fence_proxy_async_smem();  // (a query tile is loaded there)
+    }
     if (bad && blockIdx.x == 0) raise_status(p.status, kStatusBadMetadata);
     int64_t inc = sum;
 #pragma unroll
@@ -343,7 +353,11 @@ __device__ __forceinline__ void attn_locate(const AttnParams& p, AttnSmem* sm, i
     *len = (int)max(min(share, total - x0), (int64_t)0);
     mine = x0 < total && before <= x0 && x0 < before + sum;
     at = before;
-    if (!__any_sync(0xffffffffu, mine)) break;
+    if (per == 1) {
+      found = threadIdx.x;
+      cost_found = sum;
+    }
+    if (per == 1 || !__any_sync(0xffffffffu, mine)) break;
   }
   if (__any_sync(0xffffffffu, mine)) {
     const int src = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
@@ -458,21 +472,30 @@ struct AttnPages {
   }
 };
 
-// Joins parts of a unit, in order: a warp per row, a lane per DP / 32 elements.
-// Of few rows each warp of the streams that had a row has a part of its own.
+// Four columns of a row's output in a CTA's slot (four of all rows next to each
+// other, so that threads with a row each write and read them together).
+template <int DP>
+__device__ __forceinline__ float4* attn_part(const AttnParams& p, int slot, int row, int c4) {
+  return reinterpret_cast<float4*>(p.part) + (uint32_t)(slot * (DP / 4) + c4) * 256 + row;
+}
+
+// Joins parts of a unit, in order.  Of few rows each warp of the streams that
+// had a row has a part of its own.
 //   kJoinWarps  those of this CTA's warps
 //   kJoinGroup  of a unit split over many CTAs: those of this CTA's group
 //   kJoinUnit   the unit's: those of its CTAs' warps, of its CTAs, or of their
 //               groups, whichever come to at most kAttnUngrouped
 // into the output, or (where that is not all of the unit) into the first one's
 // place.  A CTA's parts lie in its slot 1 if the unit begins in its share, else
-// in slot 0.  Bound by the latency of its loads, of which a lane has W under
-// way; there are at most 32 parts.
+// in slot 0.  A thread has a row, and every so many-th four columns of it: with
+// few rows several threads share one.  Bound by the latency of its loads (a
+// thread has N of a part under way, or one of four parts), and by that of its
+// own code: it runs a few times in a call, so its loops stay small.
 enum AttnJoin : int { kJoinWarps, kJoinGroup, kJoinUnit };
 // log2 of a CTA's parts
 __device__ __forceinline__ int attn_lg_parts(int few, int kind) { return few ? (kind == kOneTile ? 3 : 2) : 0; }
-template <int DP, bool BF16, int W>
-__device__ __noinline__ void attn_join(const AttnParams& p, const AttnItem& item, int what, int warp, int lane) {
+template <int DP, bool BF16, int N>
+__device__ __noinline__ void attn_join_rows(const AttnParams& p, const AttnItem& item, int what, int all, int lg_pad) {
   const int ctas = item.c1 - item.c0 + 1, mine = (int)blockIdx.x - item.c0;
   const int lg_all = attn_lg_parts(item.few, item.kind);
   const int lg = what == kJoinWarps || (what == kJoinUnit && ctas << lg_all <= kAttnUngrouped) ? lg_all : 0;
@@ -483,79 +506,81 @@ __device__ __noinline__ void attn_join(const AttnParams& p, const AttnItem& item
                                           : (ctas + step - 1) / step) << lg;
   const bool into_part = what == kJoinGroup || (what == kJoinWarps && ctas > 1);
   const int rows0 = min(item.ntok, p.tile_tokens) * p.group;  // rows of the first tile
-  const int all = item.kind == kTwoHeads ? 2 * rows0 : item.ntok * p.group;
-  for (int i = warp; i < all; i += kAttnSoftmaxWarps) {
-    const bool second = i >= rows0;
-    const int pr = second ? 128 + i - rows0 : i;
-    auto at = [&](int k) -> int64_t {
-      const int cta = first + (k >> lg) * step;
-      return ((int64_t)(item.c0 + cta) * 2 + (cta == 0 && item.begins ? 1 : 0)) * 256 + pr +
-             (k & ((1 << lg) - 1)) * 32;
-    };
-    const float2 ml = lane < parts ? __ldcg(p.part_ml + at(lane)) : make_float2(-INFINITY, 0.f);
-    float top = ml.x, f = 0.f, acc[DP / 32];
+  const int i = threadIdx.x & ((1 << lg_pad) - 1), c0 = threadIdx.x >> lg_pad, per = kAttnSoftmaxWarps * 32 >> lg_pad;
+  const int row = i >= rows0 ? 128 + i - rows0 : i;
+  // a part's place among the maxima and sums, [slot][256]; its outputs' is
+  // [slot][DP / 4][256]
+  auto place = [&](int k) -> uint32_t {
+    const int cta = first + (k >> lg) * step;
+    return (uint32_t)((item.c0 + cta) * 2 + (cta == 0 && item.begins ? 1 : 0)) * 256 + row + (k & ((1 << lg) - 1)) * 32;
+  };
+  auto outputs = [&](uint32_t at) {
+    return reinterpret_cast<float4*>(p.part) + (at & ~255u) * (DP / 4) + (at & 255u);
+  };
+  float top = -INFINITY, sum = 0.f;
+  if (i < all) {
+    const bool other_head = item.kind == kTwoHeads && i >= rows0;
+    const int q = other_head ? i - rows0 : i;
+    const int64_t t = item.token + q / p.group;
+    const int h = (item.head + other_head) * p.group + q % p.group;
+    uint16_t* const out = p.out + t * p.out_token + (int64_t)h * p.out_head;
+#pragma unroll 1
+    for (int c = c0; c < p.D / 4; c += N * per) {
+      float4 acc[N];
 #pragma unroll
-    for (int c = 0; c < DP / 32; ++c) acc[c] = 0.f;
-    for (int k0 = 0; k0 < parts; k0 += W) {
-      float v[W][DP / 32];
+      for (int n = 0; n < N; ++n) acc[n] = make_float4(0.f, 0.f, 0.f, 0.f);
+      top = -INFINITY;
+      sum = 0.f;
+#pragma unroll(N == 1 ? 4 : 1)
+      for (int k = 0; k < parts; ++k) {
+        const uint32_t at = place(k);
+        const float2 ml = __ldcg(p.part_ml + at);
+        const float4* src = outputs(at) + c * 256;
+        float4 v[N];
 #pragma unroll
-      for (int k = 0; k < W; ++k) {
+        for (int n = 0; n < N; ++n)
+          v[n] = c + n * per < p.D / 4 ? __ldcg(src + n * per * 256) : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float t = fmaxf(top, ml.x);
+        const float a = t == -INFINITY ? 0.f : ex2(top - t), b = t == -INFINITY ? 0.f : ex2(ml.x - t);
+        top = t;
+        sum = sum * a + ml.y * b;
 #pragma unroll
-        for (int c = 0; c < DP / 32; ++c) v[k][c] = 0.f;
-        if (k0 + k < parts && lane * (DP / 32) < p.D) {
-          const float* src = p.part + at(k0 + k) * DP + lane * (DP / 32);
-          if constexpr (DP == 128) {
-            const float4 w = __ldcg(reinterpret_cast<const float4*>(src));
-            v[k][0] = w.x;
-            v[k][1] = w.y;
-            v[k][2] = w.z;
-            v[k][3] = w.w;
-          } else {
-            const float2 w = __ldcg(reinterpret_cast<const float2*>(src));
-            v[k][0] = w.x;
-            v[k][1] = w.y;
-          }
+        for (int n = 0; n < N; ++n) {
+          acc[n].x = acc[n].x * a + v[n].x * b;
+          acc[n].y = acc[n].y * a + v[n].y * b;
+          acc[n].z = acc[n].z * a + v[n].z * b;
+          acc[n].w = acc[n].w * a + v[n].w * b;
         }
       }
-      if (k0 == 0) {  // (while the loads above are under way)
+      const float r = into_part ? 1.0f : sum > 0.f ? 1.0f / sum : 0.f;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        f = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
-      }
-#pragma unroll
-      for (int k = 0; k < W; ++k) {
-        const float fk = __shfl_sync(0xffffffffu, f, k0 + k);
-#pragma unroll
-        for (int c = 0; c < DP / 32; ++c) acc[c] += v[k][c] * fk;
+      for (int n = 0; n < N; ++n) {
+        const int at = c + n * per;
+        if (at >= p.D / 4) break;
+        if (into_part)
+          __stcg(outputs(place(0)) + at * 256, acc[n]);
+        else
+          *reinterpret_cast<uint2*>(out + at * 4) = make_uint2(attn_pack<BF16>(acc[n].x * r, acc[n].y * r),
+                                                               attn_pack<BF16>(acc[n].z * r, acc[n].w * r));
       }
     }
-    float sum = ml.y * f;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (into_part) {
-      const int64_t part = at(0);
-      if (lane * (DP / 32) < p.D) {
-#pragma unroll
-        for (int c = 0; c < DP / 32; c += 2)
-          __stcg(reinterpret_cast<float2*>(p.part + part * DP + lane * (DP / 32) + c), make_float2(acc[c], acc[c + 1]));
-      }
-      if (lane == 0) __stcg(p.part_ml + part, make_float2(top, sum));
-      continue;
-    }
-    const float r = sum > 0.f ? 1.0f / sum : 0.f;
-    const bool other_head = item.kind == kTwoHeads && second;
-    const int k = other_head ? i - rows0 : i;
-    const int64_t t = item.token + k / p.group;
-    const int h = (item.head + other_head) * p.group + k % p.group;
-    uint16_t* orow = p.out + t * p.out_token + (int64_t)h * p.out_head + lane * (DP / 32);
-    if (lane * (DP / 32) < p.D) {
-#pragma unroll
-      for (int c = 0; c < DP / 32; c += 2)
-        *reinterpret_cast<uint32_t*>(orow + c) = attn_pack<BF16>(acc[c] * r, acc[c + 1] * r);
-    }
-    if (lane == 0 && p.lse)
+    if (!into_part && c0 == 0 && p.lse)
       p.lse[t * p.Hq + h] = sum > 0.f ? (top + log2f(sum)) * 0.69314718055994531f : -INFINITY;
   }
+  if (into_part) {  // (once no thread of the row reads the first part's any more)
+    named_bar_sync(1, kAttnSoftmaxWarps * 32);
+    if (i < all && c0 == 0) __stcg(p.part_ml + place(0), make_float2(top, sum));
+  }
+}
+template <int DP, bool BF16>
+__device__ __forceinline__ void attn_join(const AttnParams& p, const AttnItem& item, int what) {
+  const int rows0 = min(item.ntok, p.tile_tokens) * p.group;
+  const int all = item.kind == kTwoHeads ? 2 * rows0 : item.ntok * p.group;
+  const int lg_pad = 32 - __clz(all - 1);
+  if (lg_pad <= 4)
+    attn_join_rows<DP, BF16, 1>(p, item, what, all, lg_pad);
+  else
+    attn_join_rows<DP, BF16, 8>(p, item, what, all, lg_pad);
 }
 
 // Two streams of 128 query rows run side by side, each with its own score and
@@ -890,7 +915,7 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
       }
       if (live && ok) {
         const int prow = few ? x * 128 + tile_row : two ? x * 128 + row : row;
-        const int64_t part = ((int64_t)blockIdx.x * 2 + ATTN_ITEM(slot)) * 256 + prow;
+        const int slot = (int)blockIdx.x * 2 + ATTN_ITEM(slot);
         const int64_t token = ATTN_ITEM(token) + first + row / p.group;
         const int head = (ATTN_ITEM(head) + (kind == kTwoHeads ? x : 0)) * p.group + row % p.group;
         const bool parts = split || few;
@@ -912,10 +937,9 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
           }
           if (row < rows && c < p.D) {
             if (parts) {
-              float* dst = p.part + part * DP + c;
 #pragma unroll
               for (int i = 0; i < 16; i += 4)
-                __stcg(reinterpret_cast<float4*>(dst + i), make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]));
+                __stcg(attn_part<DP>(p, slot, prow, (c + i) / 4), make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]));
             } else {
               uint4* dst = reinterpret_cast<uint4*>(p.out + token * p.out_token + (int64_t)head * p.out_head + c);
               uint32_t v[8];
@@ -928,7 +952,7 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
         }
         if (row < rows && col0 == 0) {
           if (parts)
-            __stcg(p.part_ml + part, make_float2(m, l));
+            __stcg(p.part_ml + slot * 256 + prow, make_float2(m, l));
           else if (p.lse)
             p.lse[token * p.Hq + head] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
         }
@@ -937,7 +961,7 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
       const int c0 = ATTN_ITEM(c0), ctas = ATTN_ITEM(c1) - c0 + 1;
       if (few && (!split || ctas << attn_lg_parts(1, kind) > kAttnUngrouped)) {
         named_bar_sync(1, kAttnSoftmaxWarps * 32);
-        attn_join<DP, BF16, 4>(p, *(const AttnItem*)&sm->item[it % kAttnItems], kJoinWarps, warp, lane);
+        attn_join<DP, BF16>(p, *(const AttnItem*)&sm->item[it % kAttnItems], kJoinWarps);
         // (the parts' places are free for the next unit's)
         if (!split) named_bar_sync(1, kAttnSoftmaxWarps * 32);
       }
@@ -960,7 +984,7 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
           named_bar_sync(1, kAttnSoftmaxWarps * 32);
           if (!*(volatile int*)&sm->last) break;
           __threadfence();
-          attn_join<DP, BF16, 12>(p, *(const AttnItem*)&sm->item[it % kAttnItems], what, warp, lane);
+          attn_join<DP, BF16>(p, *(const AttnItem*)&sm->item[it % kAttnItems], what);
         }
       }
       // the other stream's warps may still read this one's output
