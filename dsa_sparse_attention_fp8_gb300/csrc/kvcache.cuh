@@ -37,7 +37,11 @@ __device__ __forceinline__ float2 widen2(uint32_t w) {
 // A row is one head of one token's key or value.  16 lanes own a row, 8
 // elements (16 bytes) each, so a warp reads two rows of up to 256 bytes with
 // one instruction, and a row's maximum takes four shuffles.  kRows rows per
-// lane are in flight at once; a CTA has the rows of `tokens` tokens.
+// lane are in flight at once; a CTA has the rows of `tokens` tokens.  8192
+// tokens of 8 + 8 heads of 128 bf16 elements into an E4M3 cache, 51 MB read and
+// written, take 24.7 us (2.1 TB/s; from L2, where the rows of a step are, and
+// bound by its scattered writes of 128 bytes and of a scale's 4), 64 tokens 4 to
+// 5 us, a launch.
 constexpr int kKvThreads = 256;
 constexpr int kKvRows = 4;
 

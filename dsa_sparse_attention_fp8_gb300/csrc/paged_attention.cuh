@@ -59,19 +59,19 @@ constexpr int kAttnMaxGrid = 160;
 constexpr float kAttnMostSum = 16384.0f;
 constexpr float kAttnRescaleLog2 = 8.0f;  // (with E4M3 caches: when the maximum grows by more than 2^8)
 constexpr int64_t kAttnMaxShare = 1 << 23;  // cost of a CTA's work, in 32 bits
-constexpr int kAttnUnitCharge = 1;    // a unit's set-up, in key tiles
+constexpr int kAttnUnitCharge = 1;    // a unit's set-up, in key tiles (2 and 3 change no measured batch by 2 %)
 // Parts of a unit split over more CTAs than this are joined in groups first,
-// by one CTA of each group (one request of 100,000 tokens over one key head,
-// bf16: of 128 query heads 96 us, 362 if one CTA joins all parts; of 8 26 and
-// 41; four requests of 20,000 over four key heads, 10 parts each: 54).  A
-// unit's count
-// of arrivals is at its first CTA, that of its first group kAttnMaxGrid further
-// on, those of the other groups at the group's first CTA another kAttnMaxGrid
-// further on (two units share a CTA only as the last one of the one and the
-// first of the other).
+// by one CTA of each group: one request of 100,000 tokens over one key head,
+// 131 parts, bf16: of 128 query heads 59 us, 196 if one CTA joins them all; of
+// 8 query heads 27 and 39.  Up to two groups' worth the second round of
+// arrivals costs what it saves (four requests of 20,000 tokens over four key
+// heads, 10 parts each: 50 us either way); groups of 6 give 67 and 28.
+// A unit's count of arrivals is at its first CTA, that of its first group
+// kAttnMaxGrid further on, those of the other groups at the group's first CTA
+// another kAttnMaxGrid further on (two units share a CTA only as the last one
+// of the one and the first of the other).
 constexpr int kAttnUngrouped = 24;
 constexpr int kAttnGroup = 12;
-static_assert(kAttnUngrouped <= 32 && kAttnGroup <= 32 && (kAttnMaxGrid + kAttnGroup - 1) / kAttnGroup <= 32, "parts of a join");
 
 // A unit of work: the query rows of one request that two streams of 128 rows
 // take at a time, over the key tiles that any of its rows sees: the first `ns`
@@ -583,20 +583,50 @@ __device__ __forceinline__ void attn_join(const AttnParams& p, const AttnItem& i
     attn_join_rows<DP, BF16, 8>(p, item, what, all, lg_pad);
 }
 
+// One CTA to an SM, each with an equal share of the work (AttnWalk): whatever
+// the batch, all SMs end together, and a unit that lies across a share's end is
+// joined by the last of its CTAs to arrive.
+//
 // Two streams of 128 query rows run side by side, each with its own score and
 // output tiles in tensor memory (S, which its probabilities overwrite, and O:
 // 2 x 256 columns, all of it) and its own softmax warps, so that the tensor
-// core works on one stream while the other's softmax runs.  A unit of two
-// query tiles gives each stream one tile and both read the same K and V
-// tiles.  A unit of one query tile (decode; the end of a prompt) gives both
-// streams that tile and alternate key tiles: the two halves are joined at the
-// end, in tensor memory.
-//   warps 0-15  softmax, eight for each stream: a thread has 64 keys of a row;
-//   then        TMA: query tiles, K and V tiles through the block table, and
+// core works on one stream while the other's softmax runs.  Rows are the query
+// heads of a key head, for as many tokens as fit: a page is read once for all
+// of them.  A unit of two query tiles gives each stream one tile, and both read
+// the same K and V tiles; one of two key heads gives each stream one head; one
+// of a single query tile gives both streams that tile and alternate key tiles:
+// the two halves are joined at the end, in tensor memory.
+//   warps 0-7   softmax, four for each stream, a thread to a row: the tile's
+//               probabilities are taken over the maximum so far in one pass
+//               over S, and only where a row's sum shows that this maximum was
+//               far too low is the tile taken again over its own (the output
+//               so far is scaled then, and only then); the row's sum and
+//               maximum in FP32;
+//   warp 8      walking: the CTA's share of the work, unit by unit, handed to
+//               the others through a ring of four items; V of an E4M3 cache;
+//   warps 9, 10 MMA, one for each stream in strict turns: S = Q K^T, O += P V
+//               (P from tensor memory);
+//   warp 11     TMA: query tiles, K and V tiles through the block table, and
 //               zeros in the rows that belong to no valid request;
-//               two MMA, one for each stream: S = Q K^T, O += P V (P from
-//               tensor memory);
-//               walking: the CTA's share of the work, unit by unit.
+//   warps 12-15 E4M3 caches: queries into two E4M3 terms, V's codes to BF16.
+// E4M3 caches: K's codes go to the tensor core as they are, with each query row
+// as two E4M3 terms over a power of two (two 8-bit products cost what one of 16
+// bits does; converting K as well took 896 us instead of 790 for four requests
+// of 231,000 tokens); a key's scale is applied to its scores and its value's to
+// its probabilities.  Few rows (at most 32): each of a stream's warps has all
+// of them and 32 of a tile's keys (559 -> 475 us); 16-bit caches, whose softmax
+// keeps the tile's probabilities in registers, lose by it (202 -> 218 us for 64
+// requests of 1K to 8K).
+//
+// What bounds it, measured: prefill (8192 tokens after 16,384, 32 heads of 128)
+// 1882 us, 1460 TFLOP/s: the tensor core is busy for 77 % of what a library
+// product reaches, the rest is the streams' first and last tiles and their
+// turns; batched decode of 64 requests (1K to 8K, 16 bits) 202 us, 6.1 TB/s, by
+// HBM; long decode over an E4M3 cache (4 x 231,000) 474 us, 4.3 TB/s: by the
+// chain of scores, softmax, probabilities and output of each stream, 2.5 us for
+// a key tile, of which only two run side by side; one request of 1024 tokens
+// 21 us, launch, set-up and the latency of each step, the kernel's own code
+// (115 KB, 155 KB with conversions) among them: hence rolled loops.
 template <int DP, bool BF16, bool FP8>
 __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
     paged_attention_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tq32,
@@ -928,7 +958,8 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
           float o[16];
           if (has0) tmem_ld<16>(lanes + attn_col_o(0) + c, a);
           if (has1) tmem_ld<16>(lanes + attn_col_o(1) + c, b);
-          tmem_ld_wait();
+          if (has0) tmem_ld_wait16(a);
+          if (has1) tmem_ld_wait16(b);
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             o[i] = 0.f;
