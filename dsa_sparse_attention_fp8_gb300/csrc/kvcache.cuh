@@ -20,6 +20,7 @@ struct KvWriteParams {
   const int64_t* slots;         // [T]
   int T, heads, dim;
   int tokens;                   // of a CTA
+  uint32_t per_token;           // ceil(2^16 / rows of a token): row * this >> 16 is the row's token, for rows < 64
   uint8_t* cache[2];            // [num_pages, 64, Hkv, D], byte strides below
   int64_t page_stride[2], token_stride[2], head_stride[2];
   float* scale[2];              // [num_pages, Hkv, 64], element strides below (E4M3 caches)
@@ -62,7 +63,7 @@ __global__ void __launch_bounds__(kKvThreads) kv_write_kernel(const __grid_const
       slot[i] = -1;
       which[i] = head[i] = 0;
       if (row < rows) {
-        const int t = row / (2 * p.heads), rest = row - t * (2 * p.heads);
+        const int t = (int)((uint32_t)row * p.per_token >> 16), rest = row - t * (2 * p.heads);
         which[i] = rest >= p.heads;
         head[i] = rest - which[i] * p.heads;
         slot[i] = __ldg(p.slots + t0 + t);

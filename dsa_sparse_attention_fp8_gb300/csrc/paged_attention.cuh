@@ -257,9 +257,12 @@ __device__ __forceinline__ bool attn_wait(uint32_t bar, uint32_t parity, const v
   return false;
 }
 
-// a / b for 0 <= a < 2^52, 0 < b: by way of FP64, whose quotient is off by one at
-// most (the compiler's division of 64-bit integers is a hundred instructions).
+// a / b for 0 <= a < 2^52, 0 < b: in 32 bits where both fit (any batch but one
+// of days of work), else by way of FP64, whose quotient is off by one at most
+// (the compiler's division of 64-bit integers is a hundred instructions, and
+// this card's FP64 has long latencies).
 __device__ __forceinline__ int64_t attn_divide(int64_t a, int64_t b) {
+  if ((uint64_t)(a | b) >> 32 == 0) return (uint32_t)a / (uint32_t)b;
   int64_t q = (int64_t)((double)a / (double)b);
   if (q * b > a) --q;
   if ((q + 1) * b <= a) ++q;

@@ -237,6 +237,7 @@ int dsa_kv_write(const void* k, int64_t k_token_stride, int64_t k_head_stride, c
   p.status = dev_status;
   // a CTA's tokens: as many as make one pass of its lanes, at least one
   p.tokens = std::max(1, dsa::kKvThreads / 16 * dsa::kKvRows / (2 * p.heads));
+  p.per_token = p.tokens > 1 ? (65536 + 2 * p.heads - 1) / (2 * p.heads) : 0;  // (one token: rows of any number)
   const int64_t grid = ((int64_t)T + p.tokens - 1) / p.tokens;
   const cudaStream_t st = (cudaStream_t)stream;
   const bool fp8 = cache->type == DSA_TYPE_E4M3;

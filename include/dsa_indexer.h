@@ -519,9 +519,9 @@ int dsa_kv_write(const void* k, int64_t k_token_stride, int64_t k_head_stride, c
  * under a token that is seen: DSA_STATUS_BAD_PAGE, its tokens are skipped.
  * Computation: tensor-core products with FP32 accumulation, FP32 softmax
  * statistics, probabilities rounded to 16 bits.  Over an E4M3 cache a query
- * row enters as the sum of two E4M3 terms over a scale of its own (within
- * 2^-8 of each element, as BF16 itself is, or 2^-18 of the row's largest) and
- * V's codes times a probability times the token's scale as BF16.
+ * row enters as two E4M3 terms over a power of two of its own (exactly, but
+ * for elements below 2^-9 of the row's largest, which are off by 2^-18 of that
+ * at most), and V's scale is in the probability that is rounded.
  * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE_TOO_SMALL, CUDA.
  */
 size_t dsa_paged_attention_workspace_bytes(void);
