@@ -98,7 +98,7 @@ __device__ __forceinline__ void round2(Norm8<T>& v, int i, float2 f) {
 // further on, VPT times, in registers from the load to the store, so a row is
 // read once; the 16 lanes of half a warp share a 128-element group.  Arithmetic
 // is in pairs (packed FP32).  Bound by HBM where rows are many: 8192 rows of
-// 7168 bf16 elements, 411 MB read and written, in 75.4 us (5.5 TB/s; with one
+// 7168 bf16 elements, 411 MB read and written, in 74.2 us (5.6 TB/s; with one
 // value at a time and VPT = 1, 50 instructions an element, 107 us; with a
 // persistent grid that copies two rows ahead into shared memory 85).  Of 64
 // rows, 6 us: launch and the latencies of two loads, a barrier and a store.

@@ -527,6 +527,13 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// 1 / x to within a unit in the last place; subnormal x and results are zeros.
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));

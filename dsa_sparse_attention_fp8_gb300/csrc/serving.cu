@@ -236,17 +236,16 @@ int dsa_kv_write(const void* k, int64_t k_token_stride, int64_t k_head_stride, c
   set_cache(&p, cache);
   p.status = dev_status;
   // a CTA's tokens: as many as make one pass of its lanes, at least one
-  p.tokens = std::max(1, dsa::kKvThreads / 16 * dsa::kKvRows / (2 * p.heads));
-  p.per_token = p.tokens > 1 ? (65536 + 2 * p.heads - 1) / (2 * p.heads) : 0;  // (one token: rows of any number)
-  const int64_t grid = ((int64_t)T + p.tokens - 1) / p.tokens;
+  p.tokens = std::max(1, dsa::kKvThreads / 16 / heads);
+  p.per_token = p.tokens > 1 ? (65536 + heads - 1) / heads : 0;
+  const unsigned grid = (unsigned)(((int64_t)T + p.tokens - 1) / p.tokens);
   const cudaStream_t st = (cudaStream_t)stream;
-  const bool fp8 = cache->type == DSA_TYPE_E4M3;
-  if (type == DSA_TYPE_BF16 && fp8)
-    dsa::kv_write_kernel<true, true><<<(unsigned)grid, dsa::kKvThreads, 0, st>>>(p);
-  else if (fp8)
-    dsa::kv_write_kernel<false, true><<<(unsigned)grid, dsa::kKvThreads, 0, st>>>(p);
+  if (cache->type != DSA_TYPE_E4M3)
+    dsa::kv_write_kernel<true, false><<<grid, dsa::kKvThreads, 0, st>>>(p);
+  else if (type == DSA_TYPE_BF16)
+    dsa::kv_write_kernel<true, true><<<grid, dsa::kKvThreads, 0, st>>>(p);
   else
-    dsa::kv_write_kernel<true, false><<<(unsigned)grid, dsa::kKvThreads, 0, st>>>(p);
+    dsa::kv_write_kernel<false, true><<<grid, dsa::kKvThreads, 0, st>>>(p);
   set_last_launches(1);
   return check_launch("kv_write_kernel");
 }
