@@ -628,7 +628,7 @@ __device__ __forceinline__ void attn_join(const AttnParams& p, const AttnItem& i
 // HBM; long decode over an E4M3 cache (4 x 231,000) 474 us, 4.3 TB/s: by the
 // chain of scores, softmax, probabilities and output of each stream, 2.5 us for
 // a key tile, of which only two run side by side; one request of 1024 tokens
-// 21 us, launch, set-up and the latency of each step, the kernel's own code
+// 19 us, launch, set-up and the latency of each step, the kernel's own code
 // (115 KB, 155 KB with conversions) among them: hence rolled loops.
 template <int DP, bool BF16, bool FP8>
 __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
@@ -735,6 +735,7 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
         const int row = few ? lane : tile_row;
         const int from_key = few ? tile_row - lane : 0, to_key = few ? from_key + 32 : kAttnTile;  // this warp's keys
         const bool live = row - lane < (hi - lo + 1) * p.group;  // some row of this warp is real
+        const bool real = row < (hi - lo + 1) * p.group;  // (the others hold whatever was there: they decide nothing)
         const int pos = min(lo + row / p.group, hi);
         const int ns = ATTN_ITEM(ns), skip = ATTN_ITEM(skip), j0 = ATTN_ITEM(j0), seq = ATTN_ITEM(seq);
         const int heads = ATTN_ITEM(kind) == kTwoHeads;
@@ -859,7 +860,8 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
               // scales' arithmetic the other form's code (below) is fetched
               // more slowly than it runs (4,400 cycles a tile)
               const float top = maximum();
-              if (__any_sync(0xffffffffu, top > m + kAttnRescaleLog2)) raise(top, top > m + kAttnRescaleLog2);
+              const bool low = real && top > m + kAttnRescaleLog2;
+              if (__any_sync(0xffffffffu, low)) raise(top, low);
               sums[0] = sums[1] = 0;
 #pragma unroll 1
               for (int c = from_key; c < to_key; c += 32) {
@@ -885,18 +887,21 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
               // not (on each row's first tile, and few after it) the row gets
               // the right one first: the scores are still there.
               uint32_t pr[64];
-              bool ready = !__any_sync(0xffffffffu, m == -INFINITY);
-              for (int pass = 0;; ++pass) {
-                if (ready) {
+              // Each row by itself, so that its result depends on no other row.
+              bool low = real && m == -INFINITY, raised = false;
+              for (;;) {
+                if (!__any_sync(0xffffffffu, low)) {
                   sums[0] = sums[1] = 0;
 #pragma unroll
                   for (int c = 0; c < kAttnTile; c += 32) probabilities(c, pr + c / 2);
                   const float2 t = unpack2(add2(sums[0], sums[1]));
                   sum = t.x + t.y;
-                  if (!__any_sync(0xffffffffu, pass == 0 && !(sum <= kAttnMostSum))) break;
+                  low = real && !raised && !(sum <= kAttnMostSum);
+                  if (!__any_sync(0xffffffffu, low)) break;
                 }
-                raise(maximum(), true);
-                ready = true;
+                raise(maximum(), low);
+                raised |= low;
+                low = false;
               }
               tmem_st<32>(base, pr);
               tmem_st<32>(base + 64, pr + 32);

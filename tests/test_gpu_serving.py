@@ -477,6 +477,22 @@ def test_units_split_over_many_ctas(B, ws, heads, d, q, seq, fp8):
         assert torch.equal(again[0], out) and torch.equal(again[1], lse)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("group", [3, 5, 7])
+def test_results_do_not_depend_on_what_ran_before(B, ws, group, fp8):
+    """Head groups that leave rows of a query tile over: the bits are the same whatever other calls left there."""
+    b = Batch(Case([40, 1, 3, 100], [300, 200, 77, 500], heads=4 * group, kv=4, fp8=fp8))
+    other = Batch(Case([256, 1], [900, 700], heads=32, kv=4, spread=30.0, fp8=fp8), seed=1)
+    out, lse, status = b.run(B, ws)
+    assert status == 0
+    b.check(out, lse)
+    for scale in (1.0, 30.0, 300.0):
+        other.scale = scale
+        other.run(B, ws)
+        again = b.run(B, ws)
+        assert torch.equal(again[0], out) and torch.equal(again[1], lse)
+
+
 def test_attention_in_a_graph_reads_new_lengths(B, ws):
     c = Case([1, 1, 1], [500, 64, 1000])
     b = Batch(c)
