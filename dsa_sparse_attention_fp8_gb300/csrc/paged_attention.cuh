@@ -171,6 +171,7 @@ struct AttnWalk {
   }
 };
 
+constexpr int kAttnMiscBytes = 3 * 1024;  // of AttnSmem
 template <int DP, bool FP8>
 struct AttnCfg {
   static constexpr int kHalves = DP / 64;
@@ -186,7 +187,7 @@ struct AttnCfg {
   static constexpr int kV = kKv + kKStages * kRawBytes, kVRaw = kV + kVStages * kTileBytes;
   static constexpr int kScale = kVRaw + kVRawStages * kRawBytes;  // then the query rows' factors, 128 for each slot
   static constexpr int kMisc = FP8 ? kScale + (kScaleTiles + 1) * 1024 : kKv + kStages * kTileBytes;
-  static constexpr int kSmem = kMisc + 3072;
+  static constexpr int kSmem = kMisc + kAttnMiscBytes;
   // Registers a thread.  16-bit caches: 168 (65,536 / 384, in eights).  E4M3
   // caches: 128 at launch, the softmax warps taking some of the others'.
   static constexpr int kSoftmaxRegs = 176, kIssueRegs = 72, kConvertRegs = 88;
@@ -226,7 +227,7 @@ struct AttnSmem {
   uint8_t bad[16];       // per key tile of the ring: bit i = page i is bad
   float swap[2][128];    // a value of each row, between the two streams
 };
-static_assert(sizeof(AttnSmem) <= 3072, "shared memory");
+static_assert(sizeof(AttnSmem) <= kAttnMiscBytes, "shared memory");
 static_assert(AttnCfg<128, false>::kStages <= 8 && AttnCfg<64, false>::kStages <= 8 &&
                   AttnCfg<128, true>::kKStages + AttnCfg<128, true>::kVStages <= 8 &&
                   AttnCfg<128, true>::kVRawStages <= 2 && AttnCfg<128, true>::kScaleTiles <= 8,
