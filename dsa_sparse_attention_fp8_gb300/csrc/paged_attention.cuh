@@ -626,7 +626,7 @@ __device__ __forceinline__ void attn_join(const AttnParams& p, const AttnItem& i
 // 1882 us, 1460 TFLOP/s: the tensor core is busy for 77 % of what a library
 // product reaches, the rest is the streams' first and last tiles and their
 // turns; batched decode of 64 requests (1K to 8K, 16 bits) 202 us, 6.1 TB/s, by
-// HBM; long decode over an E4M3 cache (4 x 231,000) 474 us, 4.3 TB/s: by the
+// HBM; long decode over an E4M3 cache (4 x 231,000) 469 us, 4.3 TB/s: by the
 // chain of scores, softmax, probabilities and output of each stream, 2.5 us for
 // a key tile, of which only two run side by side; one request of 1024 tokens
 // 19 us, launch, set-up and the latency of each step, the kernel's own code
@@ -746,6 +746,12 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
           const bool inner = s0 + kAttnTile - 1 <= lo && (p.window == 0 || s0 > hi - p.window || s0 + kAttnTile - 1 < p.sinks);
           wait(&sm->s_full[x], n_s & 1);
           ++n_s;
+          // The scores' arrival says that K's tile is done with, too: the fourth
+          // warp, which with few rows is not the slowest, gives it back instead of
+          // a commit (475 -> 468 us for four requests of 231,000; 16-bit caches,
+          // whose softmax is the longer part, lose by it: 1885 -> 1976 us for 8192
+          // tokens after 16,384).
+          if (FP8 && lane == 0 && (warp & 3) == 3) mbar_arrive(smem_u32(&sm->kv_empty[(tile0 + j) % C::kKStages]));
           if (FP8 && j == ATTN_AT(mine, from)) {
             const uint32_t q = ATTN_ITEM(q0) + (ATTN_ITEM(kind) != kOneTile ? x : 0);
             factor = p.scale_log2 * __uint_as_float(lds_u32(factor_s + ((q & 1) * 128 + row) * 4));
@@ -1268,9 +1274,6 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
         };
         auto k_wait = [&](int j) { return FP8 ? tile_wait(0, tile0 + j, step) : kv_wait(kv0 + attn_k_place(step, j), step, n); };
         auto v_wait = [&](int j) { return FP8 ? tile_wait(1, tile0 + j, step) : kv_wait(kv0 + attn_v_place(step, j, n), step, n); };
-        auto k_release = [&](int j) {
-          commit(&sm->kv_empty[FP8 ? (tile0 + j) % C::kKStages : (kv0 + attn_k_place(step, j)) % C::kStages]);
-        };
         auto v_release = [&](int j) {
           commit(&sm->kv_empty[FP8 ? C::kKStages + (tile0 + j) % C::kVStages : (kv0 + attn_v_place(step, j, n)) % C::kStages]);
         };
@@ -1319,7 +1322,7 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
           }
           if (more) {
             commit(&sm->s_full[x]);
-            k_release(j + step);
+            if (!FP8) commit(&sm->kv_empty[(kv0 + attn_k_place(step, j + step)) % C::kStages]);
             if (j + 2 * step >= n) commit(&sm->q_empty[q & 1]);
           } else if (tile) {
             commit(&sm->o_full[x]);
