@@ -430,6 +430,15 @@ __device__ __forceinline__ uint32_t attn_seen(const AttnParams& p, int back, int
   return gone ? 0u : seen;
 }
 
+// Keys of the tile at position s0 that lie between the first tokens and the
+// window of a unit's first row, at position p0: [from, to), as places in the
+// tile.  No row of the unit sees them, so they may hold anything; whole pages
+// of them are never loaded.
+__device__ __forceinline__ void attn_hidden(const AttnParams& p, int p0, int s0, int* from, int* to) {
+  *from = min(max(p.sinks - s0, 0), kAttnTile);
+  *to = p.window > 0 ? min(max(max(p0 - p.window + 1, 0) - s0, 0), kAttnTile) : 0;
+}
+
 // The pages of an item's key tiles, looked up by a warp 16 tiles ahead, a pair
 // of lanes for each tile.
 struct AttnPages {
@@ -1251,14 +1260,18 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
         const int kind = ATTN_ITEM(kind), heads = kind == kTwoHeads;
         const uint32_t q0 = ATTN_ITEM(q0), q = q0 + (kind != kOneTile ? x : 0);
         const uint32_t own = from < n ? q : 0xFFFFFFFFu;
-        // the key tile that holds the request's end inside a page: values
-        // after it may be anything, and 0 * NaN would spoil the sum
+        // Values that no row sees may be anything, and 0 * NaN would spoil the
+        // sum.  The key tile that holds the request's end inside a page ...
+        const int j0 = ATTN_ITEM(j0), ns = ATTN_ITEM(ns), skip = ATTN_ITEM(skip);
         int tail = n, end;
         {
-          const int last = ATTN_ITEM(j0) + (n >> heads) - 1;
-          end = ATTN_ITEM(seq) - (last < ATTN_ITEM(ns) ? last : last + ATTN_ITEM(skip)) * kAttnTile;
+          const int last = j0 + (n >> heads) - 1;
+          end = ATTN_ITEM(seq) - (last < ns ? last : last + skip) * kAttnTile;
           if (!FP8 && end < kAttnTile && end % kPageTokens != 0) tail = n - 1 - heads;
         }
+        // ... and, with a window, the last tile of the first tokens and the
+        // window's first one (the item's key tiles `edge` and `edge` + 1)
+        const int edge = p.window > 0 ? ns - 1 - j0 : n;
         const uint32_t tile0 = kv0 / 2;
         // half of Q K^T: 64 of the dimensions, or (E4M3) one of the queries' two terms
         auto qk = [&](int j, int h) {
@@ -1288,13 +1301,22 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
                                    : kv_s + (kv0 + attn_v_place(step, j, n)) % C::kStages * C::kTileBytes;
           if (tile) {
             if (!v_wait(j)) return;
-            if (j >= tail) {
+            const bool at_edge = !FP8 && (uint32_t)((j >> heads) - edge) < 2u;
+            if (j >= tail || at_edge) {
               // (in shared tiles each stream's warp writes the same zeros)
-              const int to = end < kPageTokens ? kPageTokens : kAttnTile;
+              auto zeros = [&](int from, int to) {
 #pragma unroll 1
-              for (int i = lane; i < (to - end) * 8; i += 32)
+                for (int i = from * 8 + lane; i < to * 8; i += 32)
 #pragma unroll
-                for (int h = 0; h < C::kHalves; ++h) sts_v4(v_s + h * 16384 + end * 128 + i * 16, make_uint4(0, 0, 0, 0));
+                  for (int h = 0; h < C::kHalves; ++h) sts_v4(v_s + h * 16384 + i * 16, make_uint4(0, 0, 0, 0));
+              };
+              if (j >= tail) zeros(end, end < kPageTokens ? kPageTokens : kAttnTile);
+              if (at_edge) {
+                const int jj = j0 + (j >> heads);
+                int from, to;
+                attn_hidden(p, ATTN_ITEM(p0), (jj < ns ? jj : jj + skip) * kAttnTile, &from, &to);
+                zeros(from, to);
+              }
               fence_proxy_async_smem();
               __syncwarp();
             }
@@ -1410,9 +1432,13 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
           if (t >= C::kVStages && !wait(&sm->kv_empty[C::kKStages + st], (t / C::kVStages - 1) & 1)) return;
           const uint32_t src = smem_u32(attn_smem) + C::kVRaw + rst * C::kRawBytes;
           const uint32_t dst = smem_u32(attn_smem) + C::kV + st * C::kTileBytes;
-          // rows past the request's end may be anything, NaN too: zeros
+          // rows that no row sees (past the request's end, between the first
+          // tokens and the window) may be anything, NaN too: zeros
           const int jj = ATTN_ITEM(j0) + ((int)(t - tile0) >> (kind == kTwoHeads));
-          const int end = ATTN_ITEM(seq) - (jj < ATTN_ITEM(ns) ? jj : jj + ATTN_ITEM(skip)) * kAttnTile;
+          const int s0 = (jj < ATTN_ITEM(ns) ? jj : jj + ATTN_ITEM(skip)) * kAttnTile;
+          const int end = ATTN_ITEM(seq) - s0;
+          int from, to;
+          attn_hidden(p, ATTN_ITEM(p0), s0, &from, &to);
           const int cc = tid & 7;  // 16 codes: 32 bytes of a row's half cc / 4
           const uint32_t unit = 2 * (cc & 3);
           if (cc < units) {
@@ -1425,7 +1451,7 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
               for (int i = 0; i < 4; ++i) {
                 const int row = r0 + 16 * i;
                 uint4 lo, hi;
-                if (row >= end) v[i] = make_uint4(0, 0, 0, 0);
+                if (row >= end || (row >= from && row < to)) v[i] = make_uint4(0, 0, 0, 0);
                 e4m3_to_bf16(v[i].x, &lo.x, &lo.y);
                 e4m3_to_bf16(v[i].y, &lo.z, &lo.w);
                 e4m3_to_bf16(v[i].z, &hi.x, &hi.y);

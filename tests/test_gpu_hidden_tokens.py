@@ -1,0 +1,74 @@
+"""Attention over caches whose hidden tokens hold anything (GPU).
+
+A token that no row of its request sees may share a page with tokens that are seen: those before the window's first
+position, those after the first `sinks` tokens.  Neither its key, its value nor (E4M3 caches) its scales may reach a
+result.  Bars as in test_gpu_serving.py.
+"""
+
+import math
+
+import pytest
+import torch
+
+from test_gpu_serving import B, BF, HF, NAN_CODE, Batch, Case, ws  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+WINDOWS = {
+    "decode": Case([1] * 5, [1000, 130, 257, 700, 64], window=100, sinks=5),
+    "prompt": Case([200, 1, 3], [700, 1000, 130], heads=16, window=100, sinks=5),
+    "window 1": Case([70, 1], [300, 200], window=1),
+    "sinks end inside a page": Case([64, 1], [512, 640], window=128, sinks=3),
+    "sinks past a tile": Case([111, 1], [640, 641], heads=9, kv=3, d=96, window=77, sinks=130),
+    "one tile": Case([1, 2, 20], [120, 125, 90], window=30, sinks=5),
+    "dim 64": Case([150, 1], [300, 200], d=64, window=50, sinks=3),
+    "group of 128": Case([3, 1], [500, 300], heads=128, kv=1, window=90, sinks=70),
+    "split": Case([1, 2], [20000, 9000], heads=8, kv=1, window=7001, sinks=200),
+}
+
+
+def spoil(b, put):
+    """Calls put(page, places) for the tokens of each seen page that no row of their request sees."""
+    c, n = b.c, 0
+    for r, (a, s) in enumerate(zip(c.q, c.seq)):
+        far = max(0, s - a - c.window + 1)
+        for block, page in enumerate(b.table[r].tolist()):
+            if page >= 0:
+                p = torch.arange(64 * block, min(64 * block + 64, s))
+                at = (p[(p < far) & (p >= c.sinks)] % 64).cuda()
+                n += len(at)
+                put(page, at)
+    assert n > 0
+
+
+def case(name, **kw):
+    return Case(**{**WINDOWS[name].__dict__, **kw})
+
+
+def check(B, ws, b):  # noqa: F811
+    out, lse, status = b.run(B, ws)
+    assert status == 0
+    b.check(out, lse)
+
+
+@pytest.mark.parametrize("name", WINDOWS)
+@pytest.mark.parametrize("dtype,value", [(BF, math.nan), (BF, math.inf), (HF, math.nan), (HF, -math.inf)])
+def test_hidden_keys_and_values(B, ws, name, dtype, value):  # noqa: F811
+    b = Batch(case(name, dtype=dtype))
+
+    def put(page, at):
+        b.kc[page, at] = value
+        b.vc[page, at] = value
+    spoil(b, put)
+    check(B, ws, b)
+
+
+@pytest.mark.parametrize("name", WINDOWS)
+def test_hidden_codes(B, ws, name):  # noqa: F811
+    b = Batch(case(name, fp8=True))
+
+    def put(page, at):
+        b.kc[page, at] = NAN_CODE
+        b.vc[page, at] = NAN_CODE
+    spoil(b, put)
+    check(B, ws, b)
