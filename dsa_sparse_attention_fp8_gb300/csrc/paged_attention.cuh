@@ -186,7 +186,8 @@ struct AttnCfg {
   static constexpr int kQ = 0, kKv = 2 * kTileBytes;
   static constexpr int kV = kKv + kKStages * kRawBytes, kVRaw = kV + kVStages * kTileBytes;
   static constexpr int kScale = kVRaw + kVRawStages * kRawBytes;  // then the query rows' factors, 128 for each slot
-  static constexpr int kMisc = FP8 ? kScale + (kScaleTiles + 1) * 1024 : kKv + kStages * kTileBytes;
+  static constexpr int kOnes = kScale + (kScaleTiles + 1) * 1024;  // 128 scales of 1
+  static constexpr int kMisc = FP8 ? kOnes + 512 : kKv + kStages * kTileBytes;
   static constexpr int kSmem = kMisc + kAttnMiscBytes;
   // Registers a thread.  16-bit caches: 168 (65,536 / 384, in eights).  E4M3
   // caches: 128 at launch, the softmax warps taking some of the others'.
@@ -437,6 +438,35 @@ __device__ __forceinline__ uint32_t attn_seen(const AttnParams& p, int back, int
 __device__ __forceinline__ void attn_hidden(const AttnParams& p, int p0, int s0, int* from, int* to) {
   *from = min(max(p.sinks - s0, 0), kAttnTile);
   *to = p.window > 0 ? min(max(max(p0 - p.window + 1, 0) - s0, 0), kAttnTile) : 0;
+}
+
+// E4M3 caches: a row's scores at `base` times their keys' scales, then -inf over
+// those that the row, at `pos`, does not see.  In that order: the scale of a
+// hidden key may be anything, and that of a key which other rows see 0 or
+// negative.  What follows takes scales of 1 for such a tile.  Few tiles come
+// here, and code that stands among the softmax loops costs every tile (inlined
+// with 32 scores at a time 486 us for the long decode, so 470).
+__device__ __noinline__ void attn_scale_and_mask(const AttnParams& p, uint32_t base, const ulonglong2* k_scale,
+                                                 int from_key, int to_key, int pos, int s0, uint32_t bad) {
+#pragma unroll 1
+  for (int c = from_key; c < to_key; c += 16) {
+    uint32_t v[16];
+    tmem_ld<16>(base + c, v);
+    const uint32_t seen = attn_seen(p, pos - s0 - c, s0 + c, bad >> (c / 64) & 1u);
+    tmem_ld_wait16(v);
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      const ulonglong2 ks = k_scale[(c + i) / 4];
+      const float2 z0 = unpack2(mul2(pack2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), ks.x));
+      const float2 z1 = unpack2(mul2(pack2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3])), ks.y));
+      v[i] = seen >> i & 1u ? __float_as_uint(z0.x) : 0xFF800000u;
+      v[i + 1] = seen >> (i + 1) & 1u ? __float_as_uint(z0.y) : 0xFF800000u;
+      v[i + 2] = seen >> (i + 2) & 1u ? __float_as_uint(z1.x) : 0xFF800000u;
+      v[i + 3] = seen >> (i + 3) & 1u ? __float_as_uint(z1.y) : 0xFF800000u;
+    }
+    tmem_st<16>(base + c, v);
+  }
+  tmem_st_wait();
 }
 
 // The pages of an item's key tiles, looked up by a warp 16 tiles ahead, a pair
@@ -693,6 +723,7 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
   }
   if (FP8) {  // scales of pages that are never loaded have to be numbers
     for (int i = threadIdx.x; i < C::kScaleTiles * 256; i += C::kThreads) sts_u32(scale_s + 4 * i, __float_as_uint(1.0f));
+    if (threadIdx.x < 128) sts_u32(smem_u32(attn_smem) + C::kOnes + 4 * threadIdx.x, __float_as_uint(1.0f));
     fence_proxy_async_smem();
   }
   int len, share;
@@ -763,7 +794,8 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
           if (FP8 && lane == 0 && (warp & 3) == 3) mbar_arrive(smem_u32(&sm->kv_empty[(tile0 + j) % C::kKStages]));
           if (FP8 && j == ATTN_AT(mine, from)) {
             const uint32_t q = ATTN_ITEM(q0) + (ATTN_ITEM(kind) != kOneTile ? x : 0);
-            factor = p.scale_log2 * __uint_as_float(lds_u32(factor_s + ((q & 1) * 128 + row) * 4));
+            // (not 0, however small the row's elements: it multiplies -inf)
+            factor = fmaxf(p.scale_log2 * __uint_as_float(lds_u32(factor_s + ((q & 1) * 128 + row) * 4)), 0x1p-126f);
             factor_read(at);
           }
           if (live) {
@@ -774,27 +806,30 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
             // be anything (each warp puts numbers there before it reads them)
             const uint32_t scales = scale_s + ((tile0 + j) & 7) * 1024;
             const ulonglong2* k_scale = reinterpret_cast<const ulonglong2*>(attn_smem + C::kScale + ((tile0 + j) & 7) * 1024);
+            const ulonglong2* const v_scale = k_scale + 32;
             if (FP8 && s0 + kAttnTile > seq) {
-              for (int i = max(seq - s0, 0) + lane; i < kAttnTile; i += 32) {
-                sts_u32(scales + 4 * i, __float_as_uint(1.0f));
-                sts_u32(scales + 512 + 4 * i, 0u);
-              }
+              for (int i = max(seq - s0, 0) + lane; i < kAttnTile; i += 32) sts_u32(scales + 512 + 4 * i, 0u);
               fence_proxy_async_smem();
               __syncwarp();
             }
             if (!(inner && bad == 0)) {
               // -inf over the scores that the row does not see
+              if constexpr (FP8) {
+                attn_scale_and_mask(p, base, k_scale, from_key, to_key, pos, s0, bad);
+                k_scale = reinterpret_cast<const ulonglong2*>(attn_smem + C::kOnes);
+              } else {
 #pragma unroll 1
-              for (int c = from_key; c < to_key; c += 32) {
-                uint32_t v[32];
-                tmem_ld<32>(base + c, v);
-                const uint32_t seen = attn_seen(p, pos - s0 - c, s0 + c, bad >> (c / 64) & 1u);
-                tmem_ld_wait32(v);
+                for (int c = from_key; c < to_key; c += 32) {
+                  uint32_t v[32];
+                  tmem_ld<32>(base + c, v);
+                  const uint32_t seen = attn_seen(p, pos - s0 - c, s0 + c, bad >> (c / 64) & 1u);
+                  tmem_ld_wait32(v);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = seen & (1u << i) ? v[i] : 0xFF800000u;
-                tmem_st<32>(base + c, v);
+                  for (int i = 0; i < 32; ++i) v[i] = seen & (1u << i) ? v[i] : 0xFF800000u;
+                  tmem_st<32>(base + c, v);
+                }
+                tmem_st_wait();
               }
-              tmem_st_wait();
             }
             // the scores' maximum
             auto maximum = [&]() {
@@ -859,7 +894,7 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
                 sums[0] = add2(sums[0], e0);
                 sums[1] = add2(sums[1], e1);
                 if (FP8) {
-                  const ulonglong2 vs = k_scale[32 + (c + i) / 4];  // V's
+                  const ulonglong2 vs = v_scale[(c + i) / 4];
                   e0 = mul2(e0, vs.x);
                   e1 = mul2(e1, vs.y);
                 }

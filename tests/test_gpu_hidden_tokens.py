@@ -72,3 +72,48 @@ def test_hidden_codes(B, ws, name):  # noqa: F811
         b.vc[page, at] = NAN_CODE
     spoil(b, put)
     check(B, ws, b)
+
+
+# ------------------------------------------------------------------ scales of keys
+@pytest.mark.parametrize("name", WINDOWS)
+@pytest.mark.parametrize("value", [0.0, math.nan, -1.0, math.inf, -math.inf])
+def test_hidden_scales_of_keys(B, ws, name, value):  # noqa: F811
+    b = Batch(case(name, fp8=True))
+    spoil(b, lambda page, at: b.ks[page].index_fill_(1, at, value))
+    check(B, ws, b)
+
+
+def rescale(b, factors):
+    """Multiplies the scales of the keys of request r at position p by factors(p), and the exact keys alike."""
+    for r, s in enumerate(b.c.seq):
+        p = torch.arange(s)
+        f = factors(p)
+        for block in range(-(-s // 64)):
+            i = p[64 * block:64 * block + 64]
+            b.ks[int(b.table[r, block]), :, : len(i)] *= f[i].cuda()
+        b.kv[r][0] *= f.double()[:, None, None]
+
+
+CHUNKS = [Case([130, 1, 77], [400, 300, 77], heads=16, fp8=True), Case([300], [900], heads=8, kv=1, d=64, fp8=True),
+          Case([200, 1], [700, 300], window=100, sinks=5, fp8=True)]
+
+
+@pytest.mark.parametrize("c", CHUNKS)
+def test_scales_of_keys_of_zero_and_below(B, ws, c):  # noqa: F811
+    """Finite scales of tokens that some rows see and others do not: a key of scale 0 is a key of zeros."""
+    b = Batch(Case(**{**c.__dict__, "window": 0, "sinks": 0}))
+    b.c = c
+    rescale(b, lambda p: torch.where(p % 7 == 3, 0.0, torch.where(p % 7 == 5, -1.0, 1.0)))
+    check(B, ws, b)
+
+
+@pytest.mark.parametrize("c", CHUNKS)
+@pytest.mark.parametrize("small", [1.0, 2.0 ** -30])
+def test_query_rows_of_zeros(B, ws, c, small):  # noqa: F811
+    """Rows of zeros, and rows of the smallest numbers, weigh all the tokens they see alike, whatever the scales."""
+    b = Batch(Case(**{**c.__dict__, "window": 0, "sinks": 0}))
+    b.c = c
+    b.q[::3] = 0
+    b.q[1::3] = 2.0 ** -133
+    rescale(b, lambda p: torch.full(p.shape, small))
+    check(B, ws, b)
