@@ -469,6 +469,22 @@ __device__ __noinline__ void attn_scale_and_mask(const AttnParams& p, uint32_t b
   tmem_st_wait();
 }
 
+// Zeros over the scales of the values of a tile that no row of the item at `at`
+// sees: between the first tokens and the window, past the unit's end, in bad
+// pages.  They may be anything (those of pages that are not loaded are what
+// another tile left there), and 0 * NaN would spoil the probabilities.  A warp
+// does it together before it reads them; all that do write the same.
+__device__ __noinline__ void attn_hide_scales(const AttnParams& p, uint32_t at, uint32_t scales, int s0, uint32_t bad) {
+  const int p0 = (int)lds_u32(at + (uint32_t)offsetof(AttnItem, p0));
+  const int end = p0 + (int)lds_u32(at + (uint32_t)offsetof(AttnItem, ntok)) - s0;
+  int from, to;
+  attn_hidden(p, p0, s0, &from, &to);
+  for (int i = lane_id(); i < kAttnTile; i += 32)
+    if (i >= end || (i >= from && i < to) || (bad >> (i / kPageTokens) & 1u)) sts_u32(scales + 4 * i, 0u);
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
 // The pages of an item's key tiles, looked up by a warp 16 tiles ahead, a pair
 // of lanes for each tile.
 struct AttnPages {
@@ -721,11 +737,7 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
     tma_prefetch_desc(&tk);
     tma_prefetch_desc(&tv);
   }
-  if (FP8) {  // scales of pages that are never loaded have to be numbers
-    for (int i = threadIdx.x; i < C::kScaleTiles * 256; i += C::kThreads) sts_u32(scale_s + 4 * i, __float_as_uint(1.0f));
-    if (threadIdx.x < 128) sts_u32(smem_u32(attn_smem) + C::kOnes + 4 * threadIdx.x, __float_as_uint(1.0f));
-    fence_proxy_async_smem();
-  }
+  if (FP8 && threadIdx.x < 128) sts_u32(smem_u32(attn_smem) + C::kOnes + 4 * threadIdx.x, __float_as_uint(1.0f));
   int len, share;
   attn_locate(p, sm, &len, &share);
   tc_fence_before();
@@ -778,7 +790,7 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
         const bool live = row - lane < (hi - lo + 1) * p.group;  // some row of this warp is real
         const bool real = row < (hi - lo + 1) * p.group;  // (the others hold whatever was there: they decide nothing)
         const int pos = min(lo + row / p.group, hi);
-        const int ns = ATTN_ITEM(ns), skip = ATTN_ITEM(skip), j0 = ATTN_ITEM(j0), seq = ATTN_ITEM(seq);
+        const int ns = ATTN_ITEM(ns), skip = ATTN_ITEM(skip), j0 = ATTN_ITEM(j0);
         const int heads = ATTN_ITEM(kind) == kTwoHeads;
         float factor = p.scale_log2;  // of the row's scores
         for (int j = ATTN_AT(mine, from); j < n; j += step) {
@@ -802,19 +814,13 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
             tc_fence_after();
             const uint32_t base = lanes + attn_col_s(x);
             const uint32_t bad = sm->bad[(tile0 + j) & 15];
-            // E4M3 caches: this tile's scales; those past the request's end may
-            // be anything (each warp puts numbers there before it reads them)
-            const uint32_t scales = scale_s + ((tile0 + j) & 7) * 1024;
+            // E4M3 caches: this tile's scales
             const ulonglong2* k_scale = reinterpret_cast<const ulonglong2*>(attn_smem + C::kScale + ((tile0 + j) & 7) * 1024);
             const ulonglong2* const v_scale = k_scale + 32;
-            if (FP8 && s0 + kAttnTile > seq) {
-              for (int i = max(seq - s0, 0) + lane; i < kAttnTile; i += 32) sts_u32(scales + 512 + 4 * i, 0u);
-              fence_proxy_async_smem();
-              __syncwarp();
-            }
             if (!(inner && bad == 0)) {
               // -inf over the scores that the row does not see
               if constexpr (FP8) {
+                attn_hide_scales(p, at, scale_s + ((tile0 + j) & 7) * 1024 + 512, s0, bad);
                 attn_scale_and_mask(p, base, k_scale, from_key, to_key, pos, s0, bad);
                 k_scale = reinterpret_cast<const ulonglong2*>(attn_smem + C::kOnes);
               } else {

@@ -117,3 +117,37 @@ def test_query_rows_of_zeros(B, ws, c, small):  # noqa: F811
     b.q[1::3] = 2.0 ** -133
     rescale(b, lambda p: torch.full(p.shape, small))
     check(B, ws, b)
+
+
+# ------------------------------------------------------------------ scales of values
+@pytest.mark.parametrize("name", WINDOWS)
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+def test_hidden_scales_of_values(B, ws, name, value):  # noqa: F811
+    b = Batch(case(name, fp8=True))
+
+    def put(page, at):
+        b.ks[page].index_fill_(1, at, value)
+        b.vs[page].index_fill_(1, at, value)
+    spoil(b, put)
+    check(B, ws, b)
+
+
+@pytest.mark.parametrize("window,sinks", [(100, 5), (0, 0)])
+def test_scales_of_pages_that_are_not_loaded(B, ws, window, sinks):  # noqa: F811
+    """A prompt's first rows see one page of a tile only, and bad pages are skipped: neither page brings scales.  What an
+    earlier tile of another request left in their place (hidden tokens' NaN) decides nothing."""
+    n = 60
+    b = Batch(Case([1, 300] * n, [1000, 300] * n, heads=16, window=100, sinks=5, fp8=True))
+
+    def put(page, at):
+        b.ks[page].index_fill_(1, at, math.nan)
+        b.vs[page].index_fill_(1, at, math.nan)
+    spoil(b, put)
+    hidden = []
+    if not window:                # bad pages instead: blocks inside the prompts' windows
+        for r in range(1, 2 * n, 4):
+            b.table[r, 3] = -1
+            hidden.append((r, 3))
+    out, lse, status = b.run(B, ws)
+    assert status == (1 if hidden else 0)
+    b.check(out, lse, hidden_pages=hidden)
