@@ -36,7 +36,9 @@ struct NormParams {
 
 // 8 elements of a row as they lie in memory, and as four pairs in FP32.
 // 16-byte accesses where every row starts on a 16-byte boundary and is a
-// multiple of 8 elements long; single elements otherwise.
+// multiple of 8 elements long; single elements otherwise.  Ordinary loads: the
+// sum may be written over x or the residual, and what a kernel writes it may
+// not read by way of the read-only path.
 template <typename T>
 union Norm8 {
   uint4 u[sizeof(T) / 2];
@@ -51,7 +53,7 @@ __device__ __forceinline__ Norm8<T> load8(const T* row, int at, int n) {
   if (VEC) {
 #pragma unroll
     for (int j = 0; j < (int)sizeof(T) / 2; ++j)
-      if (at < n) v.u[j] = __ldg(reinterpret_cast<const uint4*>(row + at) + j);
+      if (at < n) v.u[j] = reinterpret_cast<const uint4*>(row + at)[j];
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)

@@ -1,0 +1,23 @@
+"""Outputs that a call allocates belong to the stream that writes them (GPU)."""
+
+import pytest
+import torch
+
+from test_gpu_serving import B, Batch, Case, ws  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def test_attention_outputs_come_from_the_launch_stream(B, ws):  # noqa: F811
+    """Memory that the current stream's queued work may still use is not handed to a launch on another stream."""
+    b = Batch(Case([1, 3], [70, 200], heads=32, kv=4))
+    want = b.run(B, ws)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    freed = [torch.empty(b.T, 32, 128, dtype=torch.bfloat16, device="cuda"), torch.empty(b.T, 32, device="cuda")]
+    at = [t.data_ptr() for t in freed]
+    del freed                                # as after a step whose work is still queued
+    out, lse = B.paged_attention(b.q, b.kc, b.vc, b.start, b.seq, b.table, b.scale, ws, stream=side)
+    side.synchronize()
+    assert out.data_ptr() not in at and lse.data_ptr() not in at
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
