@@ -211,6 +211,15 @@ def _stream(stream) -> Optional[int]:
     return stream.cuda_stream
 
 
+def _empty(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
+    """Memory for a call's output, of the stream it is launched on: taken for the current one
+    it could still be in use there by work that was queued before."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _need(t: torch.Tensor, name: str, dtype: torch.dtype, shape=None) -> None:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -271,9 +280,9 @@ def quantize_fp8_blocks(x: torch.Tensor, codes: Optional[torch.Tensor] = None,
         raise ValueError("last dimension must be 128")
     nb = x.numel() // HEAD_DIM
     if codes is None:
-        codes = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
+        codes = _empty(x.shape, torch.uint8, x.device, stream)
     if scales is None:
-        scales = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        scales = _empty(x.shape[:-1], torch.float32, x.device, stream)
     _need(codes, "codes", torch.uint8)
     _need(scales, "scales", torch.float32)
     _check(load().dsa_quantize_fp8_blocks(_ptr(x), nb, _ptr(codes), _ptr(scales), _stream(stream)))
@@ -597,9 +606,9 @@ def sparse_mla_attention(q: torch.Tensor, kv_cache: torch.Tensor, query_start_lo
     if topk_indices.shape[0] < T:
         raise ValueError("topk_indices has fewer rows than q")
     if out is None:
-        out = torch.empty((T, Hq, MLA_LATENT), dtype=torch.bfloat16, device=q.device)
+        out = _empty((T, Hq, MLA_LATENT), torch.bfloat16, q.device, stream)
     if lse is None:
-        lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+        lse = _empty((T, Hq), torch.float32, q.device, stream)
     _need(out, "out", torch.bfloat16, (T, Hq, MLA_LATENT))
     _need(lse, "lse", torch.float32, (T, Hq))
     if status is not None:
@@ -767,16 +776,17 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     """Attention of the step's query rows (q [T, Hq, D], BF16 or FP16) over the
     paged K/V cache [num_pages, 64, Hkv, D], causal; window > 0 keeps the last
     `window` tokens and the first `num_sinks` (dsa_paged_attention).  Returns
-    (out [T, Hq, D] like q, lse [T, Hq] FP32)."""
+    (out [T, Hq, D] like q, lse [T, Hq] FP32); where they are not given, their
+    memory belongs to the stream of the launch."""
     kind = _type_of(q, "q")
     dev = _device_of(q, "q")
     T, Hq, dim = shape = tuple(q.shape)
     a = _rows(q, "q", q.dtype, shape, dev)
     cache = _kv_cache(k_cache, v_cache, k_scale, v_scale, q, k_cache.shape[2], dim, dev)
     if out is None:
-        out = torch.empty(shape, dtype=q.dtype, device=q.device)
+        out = _empty(shape, q.dtype, q.device, stream)
     if lse is None:
-        lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+        lse = _empty((T, Hq), torch.float32, q.device, stream)
     b = _rows(out, "out", q.dtype, shape, dev)
     R, max_blocks, n_ws = seq_lens.shape[0], block_table.shape[-1], workspace.shape[0]
     i32 = torch.int32
