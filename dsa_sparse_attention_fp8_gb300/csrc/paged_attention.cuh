@@ -54,9 +54,17 @@ constexpr int kAttnTmaWarp = 11;
 constexpr int kAttnConvertWarp = 12;  // to 15, with an E4M3 cache
 constexpr int kAttnMaxGrid = 160;
 // A row's probabilities are 2^(score - m) with m the maximum of the tiles up to
-// its last rescale; a tile whose probabilities add up to more than this
-// gets a new m (FP16 holds 65,504).
-constexpr float kAttnMostSum = 16384.0f;
+// its last rescale, or a little less; a tile whose probabilities add up to more
+// than attn_most_sum gets a new m.  FP16 holds 65,504 at most and loses what is
+// below 2^-25: there m lies 6 under the maximum, so that the largest probability
+// is 2^6 at least and what is lost or off by rounding below the normal numbers
+// comes to 2^-31 of the row's sum for each key, 2^-11 (a rounding of the output)
+// for a million of them.  Of a flat tile's 128 probabilities of 2^6 the sum is an
+// eighth of the most.
+template <bool BF16>
+__device__ constexpr float attn_most_sum() { return BF16 ? 16384.0f : 65504.0f; }
+template <bool BF16>
+__device__ constexpr float attn_lift() { return BF16 ? 0.0f : 6.0f; }
 constexpr float kAttnRescaleLog2 = 8.0f;  // (with E4M3 caches: when the maximum grows by more than 2^8)
 constexpr int64_t kAttnMaxShare = 1 << 23;  // cost of a CTA's work, in 32 bits
 constexpr int kAttnUnitCharge = 1;    // a unit's set-up, in key tiles (2 and 3 change no measured batch by 2 %)
@@ -859,8 +867,10 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
               }
               return top * factor;
             };
-            // the row's maximum becomes `top` where that is larger and `wanted`
-            auto raise = [&](float top, bool wanted) {
+            // the row's m becomes that of the maximum `highest` where that is
+            // larger and `wanted`
+            auto raise = [&](float highest, bool wanted) {
+              const float top = highest - attn_lift<BF16>();
               const bool grow = wanted && top > m;
               if (__any_sync(0xffffffffu, m != -INFINITY)) {  // (else there is no output yet, or zeros)
                 // the scores' arrival says that the stream's previous product is done
@@ -953,7 +963,7 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
                   for (int c = 0; c < kAttnTile; c += 32) probabilities(c, pr + c / 2);
                   const float2 t = unpack2(add2(sums[0], sums[1]));
                   sum = t.x + t.y;
-                  low = real && !raised && !(sum <= kAttnMostSum);
+                  low = real && !raised && !(sum <= attn_most_sum<BF16>());
                   if (!__any_sync(0xffffffffu, low)) break;
                 }
                 raise(maximum(), low);

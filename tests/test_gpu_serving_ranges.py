@@ -29,3 +29,29 @@ def test_norm_over_its_inputs(B, T, N, dtype):  # noqa: F811
     for got in (run(over_x, res, over_x), run(x, over_res, over_res)):
         for a, b in zip(got, want):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("at", [0, 31, 5000, 59999])
+@pytest.mark.parametrize("gap", [10.0, 14.0, 17.0])
+def test_many_small_probabilities_in_fp16(B, ws, at, gap):  # noqa: F811
+    """One key of a long context far above the others, which weigh little each and something together (requests enough
+    that few are split: a part without that key has a maximum of its own).
+
+    A row's probabilities are rounded over a maximum that leaves its largest one at 2^6 at least, so each is off by
+    half a step of itself (2^-11) or by 2^-25 of 2^6 where it falls below FP16's normal numbers: 2^-31 of the row's
+    sum for each key.  The output is rounded once; sums of 60,000 terms in FP32."""
+    n, d, heads, requests = 60000, 64, 4, 304
+    pages = -(-n // 64)
+    kc, vc = torch.zeros(pages, 64, 1, d, dtype=HF, device="cuda"), torch.ones(pages, 64, 1, d, dtype=HF, device="cuda")
+    kc[at // 64, at % 64, 0, 0], vc[at // 64, at % 64] = gap, 0
+    q = torch.zeros(requests, heads, d, dtype=HF, device="cuda")
+    q[..., 0] = 1
+    table = torch.arange(pages, device="cuda").int().repeat(requests, 1)       # all read the same pages
+    out, lse = B.paged_attention(q, kc, vc, torch.arange(requests + 1, device="cuda").int(), ints([n] * requests), table,
+                                 1.0, ws)
+    torch.cuda.synchronize()
+    rest = (n - 1) * math.exp(-gap)
+    want = rest / (1 + rest)
+    bar = (2 * 2.0 ** -11 + 2.0 ** -18 + n * 2.0 ** -23) * want + 2.0 ** -31 * n + 2.0 ** -25
+    assert ((out.double() - want).abs() <= bar).all(), f"{want} became {out.min().item()} to {out.max().item()}"
+    assert ((lse.double() - (gap + math.log1p(rest))).abs() <= n * 2.0 ** -23 + 2.0 ** -18 + 2.0 ** -22 * gap).all()
