@@ -2,8 +2,9 @@
 // over a row:
 //   h = round(x + r)            (to the stored type; h = x without a residual)
 //   y = h * rsqrt(mean(h^2) + eps) * w
-//   codes = E4M3(y / s), s = amax / 448 over each 128 elements of y (the rule
-//   of the indexer cache), and / or y rounded to the stored type.
+//   codes = E4M3(y / s), s = amax / 448 over each 128 elements of y, 1 where
+//   that is 0 (the rule of the indexer cache), and / or y rounded to the stored
+//   type.
 // The norm is that of the stored sum, so that whoever reads the residual
 // stream back gets the same row.  Sums are held in FP32.
 #pragma once
@@ -163,7 +164,9 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) add_rms_norm_kernel(con
     if (!p.codes) continue;
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    const float s = amax == 0.f ? 1.0f : __fdiv_rn(amax, 448.0f);
+    // 1 for a group of zeros, and for one of FP32's smallest numbers, whose
+    // scale would be 0 (and 0 / 0 no code)
+    const float step = __fdiv_rn(amax, 448.0f), s = step == 0.f ? 1.0f : step;
     const uint2 c = quantize8(y, s);
     if (at < p.N) {
       uint8_t* dst = p.codes + (int64_t)row * p.N + at;

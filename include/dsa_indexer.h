@@ -538,8 +538,9 @@ int dsa_paged_attention(const void* q, int64_t q_token_stride, int64_t q_head_st
  *   h = round(x + residual) to `type` (h = x where residual is NULL)
  *   y = h * weight / sqrt(mean(h^2) + eps)          (FP32)
  *   residual_out = h; out = y rounded to `type`; codes, scales = y quantised
- *   per 128 elements with the rule of the indexer cache (a last group of
- *   fewer elements has its own scale).
+ *   per 128 elements with the rule of the indexer cache (s = 1 also where
+ *   amax/448 underflows to 0; a last group of fewer elements has its own
+ *   scale).
  * x, residual, residual_out, out: [T, N] of `type` (BF16, FP16, FP32), row
  * strides in elements, >= N; weight [N] of `type`; codes [T, N] and scales
  * [T, ceil(N/128)] contiguous.  residual, residual_out, out may each be NULL,

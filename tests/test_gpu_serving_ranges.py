@@ -55,3 +55,19 @@ def test_many_small_probabilities_in_fp16(B, ws, at, gap):  # noqa: F811
     bar = (2 * 2.0 ** -11 + 2.0 ** -18 + n * 2.0 ** -23) * want + 2.0 ** -31 * n + 2.0 ** -25
     assert ((out.double() - want).abs() <= bar).all(), f"{want} became {out.min().item()} to {out.max().item()}"
     assert ((lse.double() - (gap + math.log1p(rest))).abs() <= n * 2.0 ** -23 + 2.0 ** -18 + 2.0 ** -22 * gap).all()
+
+
+def test_norm_of_the_smallest_numbers(B):  # noqa: F811
+    """A group whose scale would underflow is a group of zeros: finite codes and scales."""
+    x = torch.ones(2, 256, device="cuda")
+    x[:, ::2] = 0
+    w = torch.full((256,), 1e-43, device="cuda")
+    w[128:] = 1.0
+    codes, scales = torch.empty(2, 256, dtype=torch.uint8, device="cuda"), torch.empty(2, 2, device="cuda")
+    B.add_rms_norm(x, None, w, 1e-6, codes=codes, scales=scales)
+    torch.cuda.synchronize()
+    value = codes.view(torch.float8_e4m3fn).double().cpu() * scales.double().cpu().repeat_interleave(128, 1)
+    want = x.double().cpu() * math.sqrt(2) * w.double().cpu()
+    assert (scales > 0).all() and torch.isfinite(scales).all()
+    # half a code's step of the group's largest (2^-4), or an FP32 number below the normal ones
+    assert ((value - want).abs() <= want.abs() * (2.0 ** -4 + 2.0 ** -18) + 3e-43).all()
