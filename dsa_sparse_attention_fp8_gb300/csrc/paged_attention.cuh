@@ -66,7 +66,10 @@ __device__ constexpr float attn_most_sum() { return BF16 ? 16384.0f : 65504.0f; 
 template <bool BF16>
 __device__ constexpr float attn_lift() { return BF16 ? 0.0f : 6.0f; }
 constexpr float kAttnRescaleLog2 = 8.0f;  // (with E4M3 caches: when the maximum grows by more than 2^8)
-constexpr int64_t kAttnMaxShare = 1 << 23;  // cost of a CTA's work, in 32 bits
+// The most that a CTA's work may cost: places in it are 32 bits, and a unit of
+// 2^25 may begin before it or end after it.  At some 0.3 us a key tile and stream
+// that is minutes (2.8e7 for a prompt of a million tokens under 128 heads).
+constexpr int64_t kAttnMaxShare = 1 << 30;
 constexpr int kAttnUnitCharge = 1;    // a unit's set-up, in key tiles (2 and 3 change no measured batch by 2 %)
 // Parts of a unit split over more CTAs than this are joined in groups first,
 // by one CTA of each group: one request of 100,000 tokens over one key head,
@@ -357,7 +360,7 @@ __device__ __forceinline__ void attn_locate(const AttnParams& p, AttnSmem* sm, i
     }
     // shares of at least 4 single tiles: a split costs a unit's set-up and a merge
     share = max(attn_divide(total + gridDim.x - 1, gridDim.x), (int64_t)4);
-    if (share > kAttnMaxShare) {  // hours of work: no real batch
+    if (share > kAttnMaxShare) {
       if (threadIdx.x == 0 && blockIdx.x == 0) raise_status(p.status, kStatusBadMetadata);
       share = kAttnMaxShare;
     }

@@ -11,3 +11,16 @@ def test_the_norm_reads_by_ordinary_loads():
     """The kernel may write its sum over x or the residual: no read of it by way of the read-only path."""
     text = (PACKAGE / "csrc" / "norm.cuh").read_text()
     assert not re.search(r"__ldg|ld\.global\.nc|__restrict__", text)
+
+
+def test_a_prompt_of_a_million_tokens_is_within_the_share():
+    """The cost that the attention kernel gives a prompt of 2^20 tokens, 128 heads over 8 key heads, on 152 SMs, and
+    that of four such prompts, are within a CTA's share; a share, and a unit before or after it, are within 32 bits."""
+    text = (PACKAGE / "csrc" / "paged_attention.cuh").read_text()
+    most = 1 << int(re.search(r"kAttnMaxShare = 1 << (\d+)", text).group(1))
+    tokens, group, kv_heads, sms = 1 << 20, 16, 8, 152
+    unit = 2 * (128 // group)                       # tokens of two query tiles
+    cost = sum(2 * (1 + -(-end // 128)) for end in range(unit, tokens + 1, unit)) * kv_heads
+    assert 4 * cost // sms <= most
+    longest = 2 * (1 + (1 << 31) // 128)            # a unit over all the positions there are
+    assert most + 2 * longest < 1 << 31
