@@ -53,6 +53,13 @@ int sm_count() {
   return n;
 }
 
+int allow_smem(PerDevice& done, const void* kernel, int bytes) {
+  const cudaError_t e =
+      done.once([&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes); });
+  if (e != cudaSuccess) return fail(DSA_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+  return DSA_OK;
+}
+
 // ---------------------------------------------------------------- tensor maps
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
@@ -226,14 +233,8 @@ bool score_shape(int T, int R, int H, int k, ScoreShape* s) {
 template <int H>
 int launch_score_h(const CUtensorMap& tk, const CUtensorMap& ts, const CUtensorMap& tq,
                    const dsa::ScoreParams& p, size_t smem, int grid, cudaStream_t st) {
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(dsa::score_topk_kernel<H>,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemLimit);
-  });
-  if (attr_err != cudaSuccess)
-    return fail(DSA_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(attr_err));
+  static PerDevice allowed;
+  if (const int rc = allow_smem(allowed, (const void*)dsa::score_topk_kernel<H>, (int)kSmemLimit)) return rc;
   // programmatic stream serialisation: the kernel's prologue (TMEM
   // allocation, barrier set-up) overlaps the preceding plan or cache-write
   // kernel; it waits for that kernel's results before reading them
@@ -438,14 +439,8 @@ int launch_rows_topk(const Batch& b, const ScoreShape& s, int* launches) {
   const int grid = grid_ctas();
   const dsa::WsLayout L = dsa::ws_layout(b.T, b.R, s.G, b.k, grid, score_stride_in(b, s.G, grid));
   if (L.score_stride <= 0) return DSA_OK;
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(dsa::rows_topk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    (int)dsa::rows_topk_smem(dsa::kScoreRowMax));
-  });
-  if (attr_err != cudaSuccess)
-    return fail(DSA_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(attr_err));
+  static PerDevice allowed;
+  if (const int rc = allow_smem(allowed, (const void*)dsa::rows_topk_kernel, (int)dsa::rows_topk_smem(dsa::kScoreRowMax))) return rc;
   unsigned char* ws = static_cast<unsigned char*>(b.ws);
   dsa::RowsTopkParams rp;
   rp.score_rows = reinterpret_cast<const uint32_t*>(ws + L.score_rows);
@@ -980,15 +975,8 @@ int dsa_sparse_mla_attention(const void* q, int T, int Hq, const uint8_t* kv_cac
   if (!aligned(q, 16) || !aligned(kv_cache, 16) || !aligned(out, 16))
     return fail(DSA_ERR_INVALID_ARG, "q, kv_cache and out must be 16-byte aligned");
   if ((int64_t)T * 4 > INT32_MAX) return fail(DSA_ERR_INVALID_ARG, "too many rows");
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(dsa::sparse_mla_kernel,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    (int)dsa::kMlaSmemBytes);
-  });
-  if (attr_err != cudaSuccess)
-    return fail(DSA_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(attr_err));
+  static PerDevice allowed;
+  if (const int rc = allow_smem(allowed, (const void*)dsa::sparse_mla_kernel, (int)dsa::kMlaSmemBytes)) return rc;
   dsa::MlaParams p;
   p.q = static_cast<const uint16_t*>(q);
   p.cache = kv_cache;

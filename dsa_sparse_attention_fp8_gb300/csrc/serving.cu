@@ -6,7 +6,6 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <mutex>
 
 #include "dsa_indexer.h"
 #include "host.h"
@@ -119,14 +118,8 @@ int make_map(CUtensorMap* m, const char* what, CUtensorMapDataType type, int siz
 template <int DP, bool BF16, bool FP8>
 int launch_attention(const dsa::AttnParams& p, int grid, cudaStream_t st) {
   using C = dsa::AttnCfg<DP, FP8>;
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(dsa::paged_attention_kernel<DP, BF16, FP8>,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-  });
-  if (attr_err != cudaSuccess)
-    return fail(DSA_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(attr_err));
+  static PerDevice allowed;
+  if (const int rc = allow_smem(allowed, (const void*)dsa::paged_attention_kernel<DP, BF16, FP8>, C::kSmem)) return rc;
   const CUtensorMapDataType type = BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   CUtensorMap tq, tq32, tkv[2];
   const int64_t qd[3] = {p.D, p.Hq, p.T}, qs[2] = {p.q_head * 2, p.q_token * 2};
@@ -192,14 +185,9 @@ int dsa_block_tables_build(const int32_t* query_lens, const int32_t* seq_lens, i
   if (!query_lens || !seq_lens || (num_free && !free_pages) || !block_table || !query_start_loc ||
       (T && (!positions || !slot_mapping)) || !pages_used)
     return fail(DSA_ERR_INVALID_ARG, "null pointer");
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
   constexpr int kMost = 2 * (dsa::kTablesMaxRequests + 1) * 4;
-  std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(dsa::block_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
-  });
-  if (attr_err != cudaSuccess)
-    return fail(DSA_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(attr_err));
+  static PerDevice allowed;
+  if (const int rc = allow_smem(allowed, (const void*)dsa::block_tables_kernel, kMost)) return rc;
   const dsa::TablesParams p{query_lens, seq_lens, R, free_pages, num_free, block_table, max_blocks, T,
                             query_start_loc, positions, slot_mapping, pages_used, dev_status};
   const int64_t most = std::max<int64_t>(1, ((int64_t)T + dsa::kTablesThreads - 1) / dsa::kTablesThreads);

@@ -1,6 +1,8 @@
 """What the serving operators promise that shows without a GPU: in their sources, their host code and their arguments."""
 
 import re
+import subprocess
+from pathlib import Path
 
 from conftest import ROOT
 
@@ -24,3 +26,34 @@ def test_a_prompt_of_a_million_tokens_is_within_the_share():
     assert 4 * cost // sms <= most
     longest = 2 * (1 + (1 << 31) // 128)            # a unit over all the positions there are
     assert most + 2 * longest < 1 << 31
+
+
+def test_attributes_are_set_for_each_device(tmp_path):
+    """Host code under a runtime of its own: once a device, again where it failed."""
+    source = tmp_path / "per_device.cpp"
+    source.write_text(r'''
+#include "host.h"
+static int current = 0;
+extern "C" cudaError_t CUDARTAPI cudaGetDevice(int* d) { *d = current; return current < 0 ? cudaErrorInvalidDevice : cudaSuccess; }
+static dsa_host::PerDevice done;
+int main() {
+  int calls = 0;
+  auto call = [&](int dev, cudaError_t answer) { current = dev; return done.once([&] { ++calls; return answer; }); };
+  if (call(0, cudaSuccess) != cudaSuccess || call(0, cudaSuccess) != cudaSuccess || calls != 1) return 1;
+  if (call(1, cudaErrorInvalidValue) != cudaErrorInvalidValue || calls != 2) return 2;
+  if (call(1, cudaSuccess) != cudaSuccess || call(1, cudaSuccess) != cudaSuccess || calls != 3) return 3;
+  if (call(0, cudaSuccess) != cudaSuccess || calls != 3) return 4;
+  if (call(200, cudaSuccess) != cudaSuccess || call(200, cudaSuccess) != cudaSuccess || calls != 5) return 5;
+  if (call(-1, cudaSuccess) == cudaSuccess || calls != 5) return 6;
+  return 0;
+}
+''')
+    from dsa_sparse_attention_fp8_gb300 import _build
+    toolkit = Path(_build._nvcc()).resolve().parents[1] / "include"
+    program = tmp_path / "per_device"
+    subprocess.run(["g++", "-std=c++17", "-I", str(PACKAGE / "csrc"), "-I", str(toolkit), str(source), "-o", str(program)],
+                   check=True)
+    assert subprocess.run([str(program)]).returncode == 0
+    for name in ("serving.cu", "dsa_indexer.cu"):
+        text = (PACKAGE / "csrc" / name).read_text()
+        assert not re.search(r"call_once\(once, \[\] \{\s*attr_err", text)
