@@ -220,6 +220,14 @@ def _empty(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+_current_device = torch._C._cuda_getDevice
+
+
+def _refuse_device(device: int, name: str) -> None:
+    raise ValueError(f"{name} lies on cuda:{device}, but cuda:{_current_device()} is the current device, which a call "
+                     f"launches on: make it within torch.cuda.device({device})")
+
+
 def _need(t: torch.Tensor, name: str, dtype: torch.dtype, shape=None) -> None:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -227,6 +235,8 @@ def _need(t: torch.Tensor, name: str, dtype: torch.dtype, shape=None) -> None:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != _current_device():
+        _refuse_device(t.get_device(), name)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if shape is not None:
@@ -633,7 +643,11 @@ _raw_stream = torch._C._cuda_getCurrentRawStream
 
 def _stream_of(stream, device: int) -> int:
     """The stream to launch on: the device's current one unless given."""
-    return _raw_stream(device) if stream is None else stream.cuda_stream
+    if stream is None:
+        return _raw_stream(device)
+    if stream.device_index != device:
+        raise ValueError(f"the stream is one of cuda:{stream.device_index}, the tensors lie on cuda:{device}")
+    return stream.cuda_stream
 
 
 def _device_of(t: torch.Tensor, name: str) -> int:
@@ -645,12 +659,20 @@ def _device_of(t: torch.Tensor, name: str) -> int:
     return device
 
 
+def _launch_device(t: torch.Tensor, name: str) -> int:
+    """The device of a call's tensors, which has to be the current one."""
+    device = _device_of(t, name)
+    if device != _current_device():
+        _refuse_device(device, name)
+    return device
+
+
 def _full(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, device: int) -> int:
-    """The address of a contiguous tensor of this dtype and shape on `device`."""
+    """The address of a contiguous tensor of this dtype and shape on `device`, the current one."""
     if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
             and t.get_device() == device and t.is_contiguous()):
         _need(t, name, dtype, shape)
-        raise ValueError(f"{name} lies on cuda:{t.get_device()}, expected cuda:{device}")
+        raise ValueError(f"{name} is not as it should be: {dtype} {shape} on cuda:{device}")
     return t.data_ptr()
 
 
@@ -682,8 +704,6 @@ def _status(status: Optional[torch.Tensor], device: int) -> Optional[int]:
     if status is None:
         return None
     _need(status, "status", torch.int32)
-    if status.get_device() != device:
-        raise ValueError(f"status lies on cuda:{status.get_device()}, expected cuda:{device}")
     return status.data_ptr()
 
 
@@ -696,7 +716,7 @@ def build_block_tables(query_lens: torch.Tensor, seq_lens: torch.Tensor, free_pa
     (dsa_block_tables_build): block_table [R, max_blocks] gains the new pages
     (taken from free_pages in request order), and query_start_loc [R+1],
     positions [T], slot_mapping [T] and pages_used [1] are written."""
-    dev = _device_of(query_lens, "query_lens")
+    dev = _launch_device(query_lens, "query_lens")
     R, T = query_lens.shape[0], positions.shape[0]
     num_free, max_blocks = free_pages.shape[0], block_table.shape[-1]
     i32 = torch.int32
@@ -744,7 +764,7 @@ def kv_write(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor, k_cac
     copied into caches of the same type, or quantised into uint8 (E4M3) caches
     with scales [num_pages, Hkv, 64]."""
     kind = _type_of(k, "k")
-    dev = _device_of(k, "k")
+    dev = _launch_device(k, "k")
     T, heads, dim = shape = tuple(k.shape)
     a = _rows(k, "k", k.dtype, shape, dev)
     b = _rows(v, "v", k.dtype, shape, dev)
@@ -779,7 +799,7 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     (out [T, Hq, D] like q, lse [T, Hq] FP32); where they are not given, their
     memory belongs to the stream of the launch."""
     kind = _type_of(q, "q")
-    dev = _device_of(q, "q")
+    dev = _launch_device(q, "q")
     T, Hq, dim = shape = tuple(q.shape)
     a = _rows(q, "q", q.dtype, shape, dev)
     cache = _kv_cache(k_cache, v_cache, k_scale, v_scale, q, k_cache.shape[2], dim, dev)
@@ -813,7 +833,7 @@ def add_rms_norm(x: torch.Tensor, residual: Optional[torch.Tensor], weight: torc
     residual, residual_out, out [T, N] may have any row stride; residual_out
     may be x or residual."""
     kind = _type_of(x, "x", most=2)
-    dev, dtype = _device_of(x, "x"), x.dtype
+    dev, dtype = _launch_device(x, "x"), x.dtype
     T, N = shape = tuple(x.shape)
 
     def row(t, name):  # address and row stride

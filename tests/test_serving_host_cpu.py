@@ -4,6 +4,9 @@ import re
 import subprocess
 from pathlib import Path
 
+import pytest
+import torch
+
 from conftest import ROOT
 
 PACKAGE = ROOT / "dsa_sparse_attention_fp8_gb300"
@@ -57,3 +60,41 @@ int main() {
     for name in ("serving.cu", "dsa_indexer.cu"):
         text = (PACKAGE / "csrc" / name).read_text()
         assert not re.search(r"call_once\(once, \[\] \{\s*attr_err", text)
+
+
+class On(torch.Tensor):
+    """A host tensor that says it lies on cuda:1."""
+
+    def get_device(self):
+        return 1
+
+    is_cuda = True
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    """A call launches on the current device: with tensors of another one it is refused before it reaches the library."""
+    from dsa_sparse_attention_fp8_gb300 import binding as B
+    monkeypatch.setattr(B, "_current_device", lambda: 0)
+    monkeypatch.setattr(B, "load", lambda: pytest.fail("the call went on"))
+
+    def t(*shape, dtype=torch.int32):
+        return torch.zeros(*shape, dtype=dtype).as_subclass(On)
+    bf = torch.bfloat16
+    rows, cache = t(2, 4, 64, dtype=bf), t(1, 64, 4, 64, dtype=bf)
+    calls = [lambda: B.build_block_tables(t(1), t(1), t(1), t(1, 1), t(2), t(2), t(2, dtype=torch.int64), t(1)),
+             lambda: B.kv_write(rows, rows, t(2, dtype=torch.int64), cache, cache),
+             lambda: B.paged_attention(rows, cache, cache, t(2), t(1), t(1, 1), 1.0, t(8, dtype=torch.uint8)),
+             lambda: B.add_rms_norm(rows[0], None, t(64, dtype=bf), 1e-6, out=rows[0]),
+             lambda: B.quantize_fp8_blocks(t(2, 128, dtype=torch.float32))]
+    for call in calls:
+        with pytest.raises(ValueError, match="cuda:1.*cuda:0 is the current device"):
+            call()
+
+
+def test_a_stream_of_another_device_is_refused():
+    from types import SimpleNamespace
+
+    from dsa_sparse_attention_fp8_gb300 import binding as B
+    assert B._stream_of(SimpleNamespace(cuda_stream=7, device_index=1), 1) == 7
+    with pytest.raises(ValueError, match="stream is one of cuda:0"):
+        B._stream_of(SimpleNamespace(cuda_stream=7, device_index=0), 1)
