@@ -651,17 +651,12 @@ def _stream_of(stream, device: int) -> int:
 
 
 def _device_of(t: torch.Tensor, name: str) -> int:
+    """The device of a call's tensors, which has to be the current one."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     device = t.get_device()
     if device < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    return device
-
-
-def _launch_device(t: torch.Tensor, name: str) -> int:
-    """The device of a call's tensors, which has to be the current one."""
-    device = _device_of(t, name)
     if device != _current_device():
         _refuse_device(device, name)
     return device
@@ -686,8 +681,7 @@ def _rows(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, device: 
             raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
         if t.shape != shape:
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
-        if _device_of(t, name) != device:
-            raise ValueError(f"{name} lies on cuda:{t.get_device()}, expected cuda:{device}")
+        _device_of(t, name)
         raise ValueError(f"the last dimension of {name} must be contiguous")
     return strides
 
@@ -716,7 +710,7 @@ def build_block_tables(query_lens: torch.Tensor, seq_lens: torch.Tensor, free_pa
     (dsa_block_tables_build): block_table [R, max_blocks] gains the new pages
     (taken from free_pages in request order), and query_start_loc [R+1],
     positions [T], slot_mapping [T] and pages_used [1] are written."""
-    dev = _launch_device(query_lens, "query_lens")
+    dev = _device_of(query_lens, "query_lens")
     R, T = query_lens.shape[0], positions.shape[0]
     num_free, max_blocks = free_pages.shape[0], block_table.shape[-1]
     i32 = torch.int32
@@ -764,7 +758,7 @@ def kv_write(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor, k_cac
     copied into caches of the same type, or quantised into uint8 (E4M3) caches
     with scales [num_pages, Hkv, 64]."""
     kind = _type_of(k, "k")
-    dev = _launch_device(k, "k")
+    dev = _device_of(k, "k")
     T, heads, dim = shape = tuple(k.shape)
     a = _rows(k, "k", k.dtype, shape, dev)
     b = _rows(v, "v", k.dtype, shape, dev)
@@ -799,7 +793,7 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     (out [T, Hq, D] like q, lse [T, Hq] FP32); where they are not given, their
     memory belongs to the stream of the launch."""
     kind = _type_of(q, "q")
-    dev = _launch_device(q, "q")
+    dev = _device_of(q, "q")
     T, Hq, dim = shape = tuple(q.shape)
     a = _rows(q, "q", q.dtype, shape, dev)
     cache = _kv_cache(k_cache, v_cache, k_scale, v_scale, q, k_cache.shape[2], dim, dev)
@@ -833,7 +827,7 @@ def add_rms_norm(x: torch.Tensor, residual: Optional[torch.Tensor], weight: torc
     residual, residual_out, out [T, N] may have any row stride; residual_out
     may be x or residual."""
     kind = _type_of(x, "x", most=2)
-    dev, dtype = _launch_device(x, "x"), x.dtype
+    dev, dtype = _device_of(x, "x"), x.dtype
     T, N = shape = tuple(x.shape)
 
     def row(t, name):  # address and row stride
