@@ -24,9 +24,13 @@ int element_bytes(int type) { return type == DSA_TYPE_FP32 ? 4 : type == DSA_TYP
 // `unit` (one element may have any stride: nothing is ever a stride away).
 bool stride_ok(int64_t stride, int64_t n, int unit) { return n <= 1 || (stride >= 0 && stride % unit == 0); }
 
+// Whether a stride over n elements keeps them apart, as what is written, or read
+// by way of a tensor map, has to be.
+bool apart(int64_t stride, int64_t n) { return n <= 1 || stride != 0; }
+
 // A K/V cache as the kernels need it: 16-byte aligned heads, at most 128
 // elements each.
-int check_cache(const dsa_kv_cache* c, int type) {
+int check_cache(const dsa_kv_cache* c, int type, bool written) {
   if (!c) return fail(DSA_ERR_INVALID_ARG, "null cache");
   if (type != DSA_TYPE_BF16 && type != DSA_TYPE_FP16)
     return fail(DSA_ERR_UNSUPPORTED, "type=%d: BF16 or FP16 is wanted", type);
@@ -44,6 +48,10 @@ int check_cache(const dsa_kv_cache* c, int type) {
       !stride_ok(c->k_token_stride, DSA_PAGE_TOKENS, unit) || !stride_ok(c->v_token_stride, DSA_PAGE_TOKENS, unit) ||
       !stride_ok(c->k_head_stride, heads, unit) || !stride_ok(c->v_head_stride, heads, unit))
     return fail(DSA_ERR_INVALID_ARG, "cache strides must be multiples of 16 bytes");
+  if (!apart(c->k_page_stride, pages) || !apart(c->v_page_stride, pages) ||
+      !apart(c->k_token_stride, DSA_PAGE_TOKENS) || !apart(c->v_token_stride, DSA_PAGE_TOKENS) ||
+      !apart(c->k_head_stride, heads) || !apart(c->v_head_stride, heads))
+    return fail(DSA_ERR_INVALID_ARG, "a cache stride of 0 over more than one element");
   if (!c->k || !c->v) return fail(DSA_ERR_INVALID_ARG, "null cache pointer");
   if (!aligned(c->k, 16) || !aligned(c->v, 16))
     return fail(DSA_ERR_INVALID_ARG, "the caches must be 16-byte aligned");
@@ -53,6 +61,9 @@ int check_cache(const dsa_kv_cache* c, int type) {
         !stride_ok(c->v_scale_page_stride, pages, 4) || !stride_ok(c->k_scale_head_stride, heads, 4) ||
         !stride_ok(c->v_scale_head_stride, heads, 4))
       return fail(DSA_ERR_INVALID_ARG, "scales must be 16-byte aligned, strides multiples of 4 elements");
+    if (written && (!apart(c->k_scale_page_stride, pages) || !apart(c->v_scale_page_stride, pages) ||
+                    !apart(c->k_scale_head_stride, heads) || !apart(c->v_scale_head_stride, heads)))
+      return fail(DSA_ERR_INVALID_ARG, "a stride of 0 over more than one element of scales that are written");
   }
   return DSA_OK;
 }
@@ -102,11 +113,7 @@ int make_map(CUtensorMap* m, const char* what, CUtensorMapDataType type, int siz
     d[i] = (cuuint64_t)dims[i];
     b[i] = (cuuint32_t)box[i];
     e[i] = 1;
-    if (i > 0) {
-      if (dims[i] > 1 && strides[i - 1] <= 0)
-        return fail(DSA_ERR_INVALID_ARG, "%s: a stride of 0 over more than one element", what);
-      st[i - 1] = dims[i] > 1 ? (cuuint64_t)strides[i - 1] : (cuuint64_t)((dims[0] * size + 15) / 16 * 16);
-    }
+    if (i > 0) st[i - 1] = dims[i] > 1 ? (cuuint64_t)strides[i - 1] : (cuuint64_t)((dims[0] * size + 15) / 16 * 16);
   }
   const CUresult r = fn(m, type, (cuuint32_t)rank, const_cast<void*>(base), d, st, b, e, CU_TENSOR_MAP_INTERLEAVE_NONE,
                         swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
@@ -203,7 +210,7 @@ int dsa_kv_write(const void* k, int64_t k_token_stride, int64_t k_head_stride, c
                  dsa_stream_t stream) {
   set_last_launches(0);
   if (T < 0) return fail(DSA_ERR_INVALID_ARG, "T=%d < 0", T);
-  if (const int rc = check_cache(cache, type)) return rc;
+  if (const int rc = check_cache(cache, type, true)) return rc;
   if (T == 0) return DSA_OK;
   if (!k || !v || !slot_mapping) return fail(DSA_ERR_INVALID_ARG, "null pointer");
   const int heads = cache->num_kv_heads;
@@ -252,7 +259,7 @@ int dsa_paged_attention(const void* q, int64_t q_token_stride, int64_t q_head_st
   set_last_launches(0);
   if (T < 0) return fail(DSA_ERR_INVALID_ARG, "T=%d < 0", T);
   if (R < 1) return fail(DSA_ERR_INVALID_ARG, "R=%d < 1", R);
-  if (const int rc = check_cache(cache, type)) return rc;
+  if (const int rc = check_cache(cache, type, false)) return rc;
   if (cache->type == DSA_TYPE_E4M3 && type != DSA_TYPE_BF16)
     return fail(DSA_ERR_UNSUPPORTED, "an E4M3 cache takes BF16 queries");
   if (Hq < 1 || Hq % cache->num_kv_heads || Hq / cache->num_kv_heads > 128)
@@ -268,6 +275,9 @@ int dsa_paged_attention(const void* q, int64_t q_token_stride, int64_t q_head_st
   if (!aligned(q, 16) || !aligned(out, 16) || !stride_ok(q_token_stride, T, 8) || !stride_ok(q_head_stride, Hq, 8) ||
       !stride_ok(out_token_stride, T, 8) || !stride_ok(out_head_stride, Hq, 8))
     return fail(DSA_ERR_INVALID_ARG, "q and out must be 16-byte aligned, strides multiples of 8 elements");
+  if (!apart(q_token_stride, T) || !apart(q_head_stride, Hq) || !apart(out_token_stride, T) ||
+      !apart(out_head_stride, Hq))
+    return fail(DSA_ERR_INVALID_ARG, "a stride of 0 over more than one element of q or out");
   if (!aligned(workspace, 256)) return fail(DSA_ERR_INVALID_ARG, "workspace is not 256-byte aligned");
   const size_t need = dsa_paged_attention_workspace_bytes();
   if (workspace_bytes < need)

@@ -461,8 +461,9 @@ int dsa_block_tables_build(const int32_t* query_lens, const int32_t* seq_lens, i
  * one pool, all fit), the last dimension contiguous.  E4M3 caches have one
  * FP32 scale per (token, head): k_scale and v_scale [num_pages,
  * num_kv_heads, 64], the last dimension contiguous; value = code * scale.
- * Strides are in elements, not negative; a dimension of one element may have
- * any.  head_dim: a multiple of 16 in [16, 128].
+ * Strides are in elements, positive (of scales that are only read also 0); a
+ * dimension of one element may have any.  head_dim: a multiple of 16 in
+ * [16, 128].
  */
 typedef struct {
   void* k;
@@ -507,7 +508,8 @@ int dsa_kv_write(const void* k, int64_t k_token_stride, int64_t k_head_stride, c
  *   q   [T, Hq, head_dim] BF16 or FP16, strides in elements (multiples of 8),
  *       16-byte aligned; Hq a multiple of num_kv_heads, at most 128 times it.
  *       The cache has q's type, or is E4M3 with BF16 queries.
- *   out as q; lse [T, Hq] FP32 or NULL.
+ *   out as q; lse [T, Hq] FP32 or NULL.  Strides of q and out are positive (a
+ *   dimension of one element may have any).
  *   workspace: dsa_paged_attention_workspace_bytes() bytes, 256-byte aligned,
  *       zeroed once before its first use; every call leaves it ready for the
  *       next.  Calls that share one must not overlap on the GPU.

@@ -98,3 +98,30 @@ def test_a_stream_of_another_device_is_refused():
     assert B._stream_of(SimpleNamespace(cuda_stream=7, device_index=1), 1) == 7
     with pytest.raises(ValueError, match="stream is one of cuda:0"):
         B._stream_of(SimpleNamespace(cuda_stream=7, device_index=0), 1)
+
+
+def test_strides_of_zero_are_refused(lib):
+    """Rows that would be written over one another, and what a tensor map does not read."""
+    import ctypes
+
+    from test_serving_cpu import FAKE, P, attention, cache, write
+    e4m3 = dict(type=3, k_scale=0x1000, v_scale=0x1000)
+    for name in ("k_page_stride", "k_token_stride", "k_head_stride", "v_page_stride", "v_token_stride", "v_head_stride"):
+        for kind in ({}, e4m3):
+            c = cache(**kind, **{name: 0})
+            assert write(lib, c) == -1 and b"stride of 0" in lib.dsa_last_error(), name
+            assert attention(lib, c, ws_bytes=0) == -1 and b"stride of 0" in lib.dsa_last_error(), name
+    for name in ("k_scale_page_stride", "k_scale_head_stride", "v_scale_page_stride", "v_scale_head_stride"):
+        c = cache(**e4m3, **{name: 0})
+        assert write(lib, c) == -1 and b"written" in lib.dsa_last_error(), name
+        assert attention(lib, c, ws_bytes=0) == -3              # one scale for all heads or pages may be read
+    c = cache()
+
+    def call(q=(8192, 128), out=(8192, 128), T=4, Hq=64, c=c):
+        return lib.dsa_paged_attention(FAKE, *q, 0, T, Hq, ctypes.byref(c), FAKE, FAKE, 1, FAKE, 4, 0.1, 0, 0, FAKE, *out,
+                                       None, P(0x1000), 0, None, None)
+    assert call() == -3                                         # (no workspace: everything before it is as it should be)
+    for bad in (dict(q=(0, 128)), dict(q=(8192, 0)), dict(out=(0, 128)), dict(out=(8192, 0))):
+        assert call(**bad) == -1 and b"stride of 0" in lib.dsa_last_error()
+    one = cache(num_kv_heads=1, k_head_stride=0, v_head_stride=0)
+    assert call(q=(0, 0), out=(0, 0), T=1, Hq=1, c=one) == -3
