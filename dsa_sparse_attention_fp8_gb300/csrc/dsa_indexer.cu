@@ -77,6 +77,22 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 
 void set_last_launches(int n) { g_last_launches = n; }
 
+// Tuning overrides read from the environment: DSA_MIN_SPLIT (keys, the
+// smallest per-CTA share of key tiles worth a piece of its own, default 1024),
+// DSA_STAGE_KEYS (128 or 256, the decode layout's keys per pipeline stage,
+// default 256), DSA_GROUP_ROWS (cap on query rows per group), DSA_PDL (0
+// turns off programmatic dependent launch of the scoring kernel) and
+// DSA_WAIT_LIMIT (iterations a scoring-kernel wait on another role may take,
+// default and maximum kWaitLimit; 0 makes every such wait give up at once, and
+// the attention kernel's loading warp, to exercise the timeout path: the call
+// then reports DSA_STATUS_TIMEOUT).
+int env_int(const char* name, int dflt, int lo, int hi) {
+  const char* v = getenv(name);
+  if (!v || !*v) return dflt;
+  const int x = atoi(v);
+  return x < lo ? lo : (x > hi ? hi : x);
+}
+
 }  // namespace dsa_host
 
 namespace {
@@ -111,21 +127,6 @@ int make_rows128_map(CUtensorMap* m, const void* base, uint64_t rows, uint32_t b
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(DSA_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
   return DSA_OK;
-}
-
-// Tuning overrides read from the environment: DSA_MIN_SPLIT (keys, the
-// smallest per-CTA share of key tiles worth a piece of its own, default 1024),
-// DSA_STAGE_KEYS (128 or 256, the decode layout's keys per pipeline stage,
-// default 256), DSA_GROUP_ROWS (cap on query rows per group), DSA_PDL (0
-// turns off programmatic dependent launch of the scoring kernel) and
-// DSA_WAIT_LIMIT (iterations a scoring-kernel wait on another role may take,
-// default and maximum kWaitLimit; 0 makes every such wait give up at once, to
-// exercise the timeout path: the call then reports DSA_STATUS_TIMEOUT).
-int env_int(const char* name, int dflt, int lo, int hi) {
-  const char* v = getenv(name);
-  if (!v || !*v) return dflt;
-  const int x = atoi(v);
-  return x < lo ? lo : (x > hi ? hi : x);
 }
 
 // ---------------------------------------------------------------- launch shape

@@ -42,6 +42,8 @@ class PerDevice {
 // Allows `kernel` that many bytes of dynamic shared memory; `done` is the kernel's own.
 int allow_smem(PerDevice& done, const void* kernel, int bytes);
 
+// An integer from the environment, within [lo, hi]; `dflt` where it is not set.
+int env_int(const char* name, int dflt, int lo, int hi);
 // The driver's cuTensorMapEncodeTiled, or null.
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn();
 // The value dsa_last_launch_count() reports.

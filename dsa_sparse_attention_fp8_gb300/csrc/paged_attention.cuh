@@ -37,6 +37,7 @@ struct AttnParams {
   int window, sinks;
   float scale_log2;            // softmax scale * log2(e)
   int32_t* status;
+  bool give_up;                // for tests: the loading warp gives up at once
   int group;                   // Hq / Hkv
   int tile_tokens;             // tokens of a 128-row query tile: 128 / group
   int tile_tokens32;           // tokens of 32 rows: 32 / group
@@ -260,15 +261,23 @@ __device__ __forceinline__ uint32_t attn_col_s(int x) { return (uint32_t)x * 128
 __device__ __forceinline__ uint32_t attn_col_o(int x) { return 256u + (uint32_t)x * 128; }
 
 // A bounded wait as small as it can be: the kernel has some thirty, and its
-// code has to stay in the instruction caches.
-__device__ __forceinline__ bool attn_wait(uint32_t bar, uint32_t parity, const volatile int* abort_flag) {
+// code has to stay in the instruction caches (a limit that is no constant made
+// the long decode 494 us of 466).
+__device__ __forceinline__ bool attn_wait(uint32_t bar, uint32_t parity, const volatile int* abort_flag,
+                                          uint32_t limit = kWaitLimit) {
 #pragma unroll 1
-  for (uint32_t i = 0; i < kWaitLimit; ++i) {
+  for (uint32_t i = 0; i < limit; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
     if ((i & 255u) == 255u && abort_flag && *abort_flag) return false;
   }
   return false;
 }
+// Once a role's wait has given up all others' follow, so an item in work is
+// done with, one way or the other, long before the walking warp's wait for its
+// place runs out; and that warp hands out an item, or ends, long before the
+// waits for an item do.  (These have to agree: the softmax warps meet at
+// barriers.)
+constexpr uint32_t kAttnWalkLimit = 16 * kWaitLimit, kAttnItemLimit = 64 * kWaitLimit;
 
 // a / b for 0 <= a < 2^52, 0 < b: in 32 bits where both fit (any batch but one
 // of days of work), else by way of FP64, whose quotient is off by one at most
@@ -758,7 +767,8 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
   volatile int* abort_flag = &sm->abort;
   bool ok = true;
   // warp-uniform waits; after one gave up the role ends (the softmax warps,
-  // which meet at barriers, go on to the items' end without waiting)
+  // which meet at barriers, go on to the items' end without waiting) and gives
+  // no place of a ring back
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (ok) {
       ok = __all_sync(0xffffffffu, attn_wait(smem_u32(bar), parity, abort_flag));
@@ -779,7 +789,7 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
     // E4M3 caches: a query tile's slot is free once its rows' factors are read, too
     auto factor_read = [&](uint32_t at) {
       __syncwarp();
-      if (lane == 0) {
+      if (lane == 0 && ok) {
         const uint32_t q0 = ATTN_ITEM(q0);
         mbar_arrive(smem_u32(&sm->q_empty[q0 & 1]));
         if (ATTN_ITEM(kind) != kOneTile) mbar_arrive(smem_u32(&sm->q_empty[~q0 & 1]));
@@ -788,7 +798,7 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
     uint32_t n_s = 0, n_o = 0, tile0 = 0;  // score and output tiles so far; key tiles before this item
     for (uint32_t it = 0;; ++it) {
       const uint32_t at = smem_u32(&sm->item[it % kAttnItems]);
-      if (!attn_wait(smem_u32(&sm->item_full[it % kAttnItems]), (it / kAttnItems) & 1, nullptr)) break;
+      if (!attn_wait(smem_u32(&sm->item_full[it % kAttnItems]), (it / kAttnItems) & 1, nullptr, kAttnItemLimit)) break;
       const int n = ATTN_ITEM(n);
       if (n == 0) break;
       float m = -INFINITY, l = 0.f;
@@ -814,7 +824,7 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
           // a commit (475 -> 468 us for four requests of 231,000; 16-bit caches,
           // whose softmax is the longer part, lose by it: 1885 -> 1976 us for 8192
           // tokens after 16,384).
-          if (FP8 && lane == 0 && (warp & 3) == 3) mbar_arrive(smem_u32(&sm->kv_empty[(tile0 + j) % C::kKStages]));
+          if (FP8 && ok && lane == 0 && (warp & 3) == 3) mbar_arrive(smem_u32(&sm->kv_empty[(tile0 + j) % C::kKStages]));
           if (FP8 && j == ATTN_AT(mine, from)) {
             const uint32_t q = ATTN_ITEM(q0) + (ATTN_ITEM(kind) != kOneTile ? x : 0);
             // (not 0, however small the row's elements: it multiplies -inf)
@@ -1113,7 +1123,7 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
     auto each_item = [&](auto& serve) {
       for (uint32_t it = 0;; ++it) {
         const uint32_t at = smem_u32(&sm->item[it % kAttnItems]);
-        if (!attn_wait(smem_u32(&sm->item_full[it % kAttnItems]), (it / kAttnItems) & 1, nullptr)) break;
+        if (!attn_wait(smem_u32(&sm->item_full[it % kAttnItems]), (it / kAttnItems) & 1, nullptr, kAttnItemLimit)) break;
         const int n = ATTN_ITEM(n);
         if (n == 0) break;
         if (ok) serve(at, n);
@@ -1149,6 +1159,10 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
     if (warp == kAttnTmaWarp) {
       // ================================================================ TMA
       uint32_t n_kv = 0, n_q = 0, tile0 = 0;
+      if (p.give_up) {  // as if its first wait had: nothing is loaded, and all the others' waits end by that
+        ok = false;
+        *abort_flag = 1;
+      }
       // One tile of K or V from its two pages.  With
       // an E4M3 cache K's tile brings the scales of both.
       auto load = [&](const CUtensorMap* map, int head, int page0, int page1) {
@@ -1543,9 +1557,16 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
       }
       uint32_t it = 0;
       int q0 = 0;
+      // false where no place got free in time: what lies there may be in use, so
+      // nothing is put over it, and the walk is over
       auto hand = [&](int n) {
         const uint32_t st = it % kAttnItems, round = it / kAttnItems;
-        if (round > 0) attn_wait(smem_u32(&sm->item_empty[st]), (round - 1) & 1, nullptr);
+        if (round > 0 && !__all_sync(0xffffffffu, attn_wait(smem_u32(&sm->item_empty[st]), (round - 1) & 1, nullptr,
+                                                            kAttnWalkLimit))) {
+          *abort_flag = 1;
+          if (lane == 0) raise_status(p.status, kStatusTimeout);
+          return false;
+        }
         if (lane == 0) {
           AttnItem* i = &sm->item[st];
           i->n = n;
@@ -1584,6 +1605,7 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
         }
         __syncwarp();
         ++it;
+        return true;
       };
       // With E4M3 caches this warp loads V as well, an item behind the walk (one
       // warp with both loads is what the kernel waits for: each copy costs it
@@ -1601,13 +1623,14 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
           load8(false, head + (j & heads), a < 0 ? (int)p.num_pages : a, b < 0 ? (int)p.num_pages : b);
         }
       };
-      for (; w.inside(); w.next(p)) {
+      bool handed = true;
+      for (; handed && w.inside(); w.next(p)) {
         if (w.j1 <= w.j0) continue;
-        hand((w.j1 - w.j0) << (w.unit.kind == kTwoHeads));
-        if (FP8 && it > 1) load_v(it - 2);
+        handed = hand((w.j1 - w.j0) << (w.unit.kind == kTwoHeads));
+        if (FP8 && handed && it > 1) load_v(it - 2);
       }
-      hand(0);
-      if (FP8 && it > 1) load_v(it - 2);
+      if (handed) handed = hand(0);
+      if (FP8 && handed && it > 1) load_v(it - 2);
       if (FP8) landed(sm->raw_full, n_t, C::kVRawStages);
     }
   }

@@ -304,6 +304,7 @@ int dsa_paged_attention(const void* q, int64_t q_token_stride, int64_t q_head_st
   p.sinks = num_sinks;
   p.scale_log2 = (float)((double)softmax_scale * 1.4426950408889634);
   p.status = dev_status;
+  p.give_up = env_int("DSA_WAIT_LIMIT", (int)dsa::kWaitLimit, 0, (int)dsa::kWaitLimit) == 0;
   p.group = Hq / p.Hkv;
   p.tile_tokens = 128 / p.group;
   p.tile_tokens32 = 32 / p.group;

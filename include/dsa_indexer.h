@@ -512,7 +512,8 @@ int dsa_kv_write(const void* k, int64_t k_token_stride, int64_t k_head_stride, c
  *   dimension of one element may have any).
  *   workspace: dsa_paged_attention_workspace_bytes() bytes, 256-byte aligned,
  *       zeroed once before its first use; every call leaves it ready for the
- *       next.  Calls that share one must not overlap on the GPU.
+ *       next, but one that sets DSA_STATUS_TIMEOUT: zero it again after that.
+ *       Calls that share one must not overlap on the GPU.
  * Requests may bring any number of new tokens (none, one, thousands).  Cache
  * contents that no row of the request sees may hold anything; keys and
  * values that some row sees must be finite.
