@@ -1444,7 +1444,8 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
       // A query tile in place: each row, scaled by a power of two to a maximum
       // in [128, 256), as the sum of two E4M3 terms (8 significant bits as two
       // times 4: exact but for elements under 2^-9 of the row's maximum, which
-      // are off by 2^-18 of it at most).  So Q K^T needs no conversion of K:
+      // are off by half of E4M3's smallest step, 2^-10, and so by 2^-17 of it at
+      // most).  So Q K^T needs no conversion of K:
       // two products with its codes cost what one in 16 bits does.
       auto split_q = [&](uint32_t place, int rows, int copies) {
         if (!wait(&sm->q_full[place & 1], (place >> 1) & 1)) return false;

@@ -523,7 +523,7 @@ int dsa_kv_write(const void* k, int64_t k_token_stride, int64_t k_head_stride, c
  * Computation: tensor-core products with FP32 accumulation, FP32 softmax
  * statistics, probabilities rounded to 16 bits.  Over an E4M3 cache a query
  * row enters as two E4M3 terms over a power of two of its own (exactly, but
- * for elements below 2^-9 of the row's largest, which are off by 2^-18 of that
+ * for elements below 2^-9 of the row's largest, which are off by 2^-17 of that
  * at most), and V's scale is in the probability that is rounded.
  * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE_TOO_SMALL, CUDA.
  */

@@ -125,3 +125,21 @@ def test_strides_of_zero_are_refused(lib):
         assert call(**bad) == -1 and b"stride of 0" in lib.dsa_last_error()
     one = cache(num_kv_heads=1, k_head_stride=0, v_head_stride=0)
     assert call(q=(0, 0), out=(0, 0), T=1, Hq=1, c=one) == -3
+
+
+def test_queries_as_two_e4m3_terms_are_as_near_as_stated():
+    """Over an E4M3 cache a row, times a power of two that brings its maximum to [128, 256), is a sum of two E4M3 terms:
+    exactly down to 2^-9 of the maximum, and below that as near as the header and the kernel say."""
+    stated = [int(re.search(r"by 2\^-(\d+) of (?:it|that)[\s*/]*at[\s*/]*most", path.read_text()).group(1))
+              for path in (ROOT / "include" / "dsa_indexer.h", PACKAGE / "csrc" / "paged_attention.cuh")]
+    x = torch.arange(0x3000, 0x4380).to(torch.int16).view(torch.bfloat16).float()      # BF16 numbers from 2^-31 to 256
+    first = x.to(torch.float8_e4m3fn).float()
+    off = (first + (x - first).to(torch.float8_e4m3fn).float() - x).abs()
+    assert x.max() < 256
+    worst = 0.0
+    for top in (128.0, 255.0):                          # the row's maximum
+        row = x <= top
+        assert (off[row & (x >= top * 2.0 ** -9)] == 0).all()
+        worst = max(worst, (off[row].max() / top).item())
+    assert all(worst <= 2.0 ** -n for n in stated), (worst, stated)
+    assert worst > 2.0 ** -18
