@@ -261,7 +261,7 @@ int dsa_paged_attention(const void* q, int64_t q_token_stride, int64_t q_head_st
   if (R < 1) return fail(DSA_ERR_INVALID_ARG, "R=%d < 1", R);
   if (const int rc = check_cache(cache, type, false)) return rc;
   if (cache->type == DSA_TYPE_E4M3 && type != DSA_TYPE_BF16)
-    return fail(DSA_ERR_UNSUPPORTED, "an E4M3 cache takes BF16 queries");
+    return fail(DSA_ERR_UNSUPPORTED, "an E4M3 cache takes BF16 queries: FP16's 11 significant bits do not fit their two E4M3 terms");
   if (Hq < 1 || Hq % cache->num_kv_heads || Hq / cache->num_kv_heads > 128)
     return fail(DSA_ERR_UNSUPPORTED, "Hq=%d: a multiple of num_kv_heads=%d, at most 128 query heads to a key head",
                 Hq, cache->num_kv_heads);

@@ -486,7 +486,8 @@ typedef struct {
  * (s = amax/448, s = 1 for an all-zero head, codes E4M3(x/s) RNE,
  * saturating).  slot_mapping [T]: page*64 + offset; negative slots write
  * nothing, slots past the pool set DSA_STATUS_BAD_PAGE and write nothing.
- * Two tokens with one slot leave either's row.
+ * Two tokens must not share a slot: its bytes and scales may then be a
+ * mixture of both rows.
  * Errors: INVALID_ARG, UNSUPPORTED, CUDA.
  */
 int dsa_kv_write(const void* k, int64_t k_token_stride, int64_t k_head_stride, const void* v,
@@ -507,7 +508,10 @@ int dsa_kv_write(const void* k, int64_t k_token_stride, int64_t k_head_stride, c
  * out = 0, lse = -inf.
  *   q   [T, Hq, head_dim] BF16 or FP16, strides in elements (multiples of 8),
  *       16-byte aligned; Hq a multiple of num_kv_heads, at most 128 times it.
- *       The cache has q's type, or is E4M3 with BF16 queries.
+ *       The cache has q's type, or is E4M3 with BF16 queries (FP16's 11
+ *       significant bits are more than the two E4M3 terms of a query hold:
+ *       round them to BF16 first; FP16 keys and values can be written to
+ *       either cache).
  *   out as q; lse [T, Hq] FP32 or NULL.  Strides of q and out are positive (a
  *   dimension of one element may have any).
  *   workspace: dsa_paged_attention_workspace_bytes() bytes, 256-byte aligned,

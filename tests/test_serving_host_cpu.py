@@ -143,3 +143,14 @@ def test_queries_as_two_e4m3_terms_are_as_near_as_stated():
         worst = max(worst, (off[row].max() / top).item())
     assert all(worst <= 2.0 ** -n for n in stated), (worst, stated)
     assert worst > 2.0 ** -18
+
+
+def test_fp16_queries_over_an_e4m3_cache_are_refused_with_the_reason(lib):
+    from test_serving_cpu import attention, cache, write
+    c = cache(type=3, k_scale=0x1000, v_scale=0x1000)
+    assert attention(lib, c, type=1) == -2 and b"significant bits" in lib.dsa_last_error()
+    assert attention(lib, c, type=0, ws_bytes=0) == -3 and write(lib, c, type=1, T=0) == 0
+    x = torch.arange(0x5800, 0x5C00).to(torch.int16).view(torch.float16).float()      # the FP16 numbers from 128 to 256
+    first = x.to(torch.float8_e4m3fn).float()
+    off = (first + (x - first).to(torch.float8_e4m3fn).float() - x).abs() / x
+    assert off.max() > 2.0 ** -10                                                      # their rounding is 2^-11
