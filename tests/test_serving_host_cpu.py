@@ -154,3 +154,12 @@ def test_fp16_queries_over_an_e4m3_cache_are_refused_with_the_reason(lib):
     first = x.to(torch.float8_e4m3fn).float()
     off = (first + (x - first).to(torch.float8_e4m3fn).float() - x).abs() / x
     assert off.max() > 2.0 ** -10                                                      # their rounding is 2^-11
+
+
+def test_the_library_is_rebuilt_when_any_of_its_sources_changes():
+    from dsa_sparse_attention_fp8_gb300 import _build
+    included = set()
+    for path in (PACKAGE / "csrc").iterdir():
+        included |= set(re.findall(r'#include "([^"]+)"', path.read_text()))
+    known = {path.name for path in _build._sources()}
+    assert included <= known and "host.h" in known
