@@ -48,7 +48,7 @@ METRIC = "DSA indexer score+top-k query-key pairs/s; % of HBM / FP8 roofline"
 UNIT = "pairs/s"
 BYTES_PER_PAIR = 132 + 4 / 64          # FP8 key + FP32 scale + its share of a block-table entry
 L2_FLUSH_BYTES = 256 << 20             # larger than the 129 MB L2
-KERNEL_SOURCES = ["score_topk.cuh", "ptx.cuh", "plan.cuh", "kwrite.cuh"]
+KERNEL_SOURCES = ["score_topk.cuh", "ptx.cuh", "plan.cuh", "kwrite.cuh", "common.cuh"]
 
 
 def parse():

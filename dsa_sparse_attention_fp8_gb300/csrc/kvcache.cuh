@@ -11,6 +11,7 @@
 #include <cstdint>
 
 #include "common.cuh"
+#include "quantize.cuh"
 
 namespace dsa {
 

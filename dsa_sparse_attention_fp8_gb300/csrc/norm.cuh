@@ -16,6 +16,7 @@
 #include <type_traits>
 
 #include "common.cuh"
+#include "quantize.cuh"
 
 namespace dsa {
 

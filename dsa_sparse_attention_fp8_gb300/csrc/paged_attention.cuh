@@ -15,7 +15,7 @@
 #include <type_traits>
 
 #include "common.cuh"
-#include "ptx.cuh"
+#include "ptx_serving.cuh"
 
 namespace dsa {
 

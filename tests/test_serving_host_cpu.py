@@ -163,3 +163,11 @@ def test_the_library_is_rebuilt_when_any_of_its_sources_changes():
         included |= set(re.findall(r'#include "([^"]+)"', path.read_text()))
     known = {path.name for path in _build._sources()}
     assert included <= known and "host.h" in known
+
+
+def test_the_scoring_kernels_counters_are_of_its_present_sources():
+    """Additions for other kernels go where they leave the committed counters, and the bench's traffic figure, valid."""
+    import bench
+    assert bench.profiled_traffic("long_context_decode") and bench.profiled_traffic("batched_decode")
+    included = re.findall(r'#include "(\w+\.cuh)"', "".join((PACKAGE / "csrc" / n).read_text() for n in bench.KERNEL_SOURCES))
+    assert set(included) <= set(bench.KERNEL_SOURCES)
