@@ -72,6 +72,16 @@ constexpr float kAttnRescaleLog2 = 8.0f;  // (with E4M3 caches: when the maximum
 // that is minutes (2.8e7 for a prompt of a million tokens under 128 heads).
 constexpr int64_t kAttnMaxShare = 1 << 30;
 constexpr int kAttnUnitCharge = 1;    // a unit's set-up, in key tiles (2 and 3 change no measured batch by 2 %)
+// Over E4M3 caches, units of at most 32 rows to a stream and this many key tiles
+// or more give each warp of a stream all rows and a quarter of a tile's keys.
+// That shortens each tile and costs a join of the warps' parts: 464 us instead
+// of 600 for four requests of 231,000 tokens, 171 instead of 204 for 64 in a
+// window of 4096, 96 instead of 106 for 64 of 2,000; 216 and 218 for 256 of
+// 1,000; but 510 instead of 481 for 1,000 requests of 300, 23.6 instead of 21.5
+// for one of 1,024 (split).  16-bit caches, whose softmax keeps the tile's
+// probabilities in registers, lose by it (28.8 instead of 20.6 us for one
+// request of 1,024 tokens, 218 instead of 201 for 64 of 1,000 to 8,000).
+constexpr int kAttnFewTiles = 8;
 // Parts of a unit split over more CTAs than this are joined in groups first,
 // by one CTA of each group: one request of 100,000 tokens over one key head,
 // 131 parts, bf16: of 128 query heads 59 us, 196 if one CTA joins them all; of
@@ -216,7 +226,7 @@ struct AttnItem {
   int kind;       // AttnKind
   int p0;         // position of the first token
   int lo[2], hi[2];  // positions of each stream's first and last token
-  int few;           // at most 32 rows to a stream: each of its warps has them all, and 32 of a tile's keys
+  int few;           // each warp of a stream has all of its rows (at most 32), and 32 of a tile's keys
   int from[2], step; // a stream's first key tile of the part, and how many on its next is
   int ns, skip;   // the request's key tile j0 + i is the part's i-th while that is below ns, else it is j0 + i + skip
   int j0;
@@ -692,10 +702,7 @@ __device__ __forceinline__ void attn_join(const AttnParams& p, const AttnItem& i
 // as two E4M3 terms over a power of two (two 8-bit products cost what one of 16
 // bits does; converting K as well took 896 us instead of 790 for four requests
 // of 231,000 tokens); a key's scale is applied to its scores and its value's to
-// its probabilities.  Few rows (at most 32): each of a stream's warps has all
-// of them and 32 of a tile's keys (559 -> 475 us); 16-bit caches, whose softmax
-// keeps the tile's probabilities in registers, lose by it (202 -> 218 us for 64
-// requests of 1K to 8K).
+// its probabilities.  Few rows over many tiles: kAttnFewTiles.
 //
 // What bounds it, measured: prefill (8192 tokens after 16,384, 32 heads of 128)
 // 1882 us, 1460 TFLOP/s: the tensor core is busy for 77 % of what a library
@@ -1581,10 +1588,8 @@ __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)
             i->hi[0] = tiles ? w.unit.p0 + p.tile_tokens - 1 : last;
             i->lo[1] = tiles ? w.unit.p0 + p.tile_tokens : w.unit.p0;
             i->hi[1] = last;
-            // (16-bit caches: the joins cost more than the shorter tiles give, 28.8
-            // instead of 20.6 us for one request of 1,024 tokens, 218 instead of
-            // 201 us for 64; E4M3: 473 instead of 559 us for four of 231,000)
-            i->few = FP8 && w.unit.ntok <= p.tile_tokens32;
+            // (a rule on the unit, so that its CTAs agree)
+            i->few = FP8 && w.unit.ntok <= p.tile_tokens32 && w.unit.n >= kAttnFewTiles;
             i->from[0] = 0;
             i->from[1] = tiles ? 0 : 1;
             i->step = tiles ? 1 : 2;
