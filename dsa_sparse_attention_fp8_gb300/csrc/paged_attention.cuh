@@ -705,13 +705,16 @@ __device__ __forceinline__ void attn_join(const AttnParams& p, const AttnItem& i
 // its probabilities.  Few rows over many tiles: kAttnFewTiles.
 //
 // What bounds it, measured: prefill (8192 tokens after 16,384, 32 heads of 128)
-// 1882 us, 1460 TFLOP/s: the tensor core is busy for 77 % of what a library
+// 1883 us, 1460 TFLOP/s: the tensor core is busy for 77 % of what a library
 // product reaches, the rest is the streams' first and last tiles and their
-// turns; batched decode of 64 requests (1K to 8K, 16 bits) 202 us, 6.1 TB/s, by
-// HBM; long decode over an E4M3 cache (4 x 231,000) 469 us, 4.3 TB/s: by the
-// chain of scores, softmax, probabilities and output of each stream, 2.5 us for
-// a key tile, of which only two run side by side; one request of 1024 tokens
-// 19 us, launch, set-up and the latency of each step, the kernel's own code
+// turns; batched decode of 64 requests (1K to 8K, 16 bits) 197 to 202 us, 6.1
+// TB/s, by HBM; long decode over an E4M3 cache (4 x 231,000) 463 us, 4.4 TB/s: by
+// the chain of scores, softmax, probabilities and output of each stream, 2.5 us
+// for a key tile, of which two run side by side; prompts over an E4M3 cache (8192
+// tokens 1010 us) by the softmax, which reads a tile's scores twice and applies
+// the scales each time; short prompts (16 of up to 300 tokens 57 us, one of 2000
+// 71) by units that shares cut and that are joined; one request of 1024 tokens
+// 20 us, launch, set-up and the latency of each step, the kernel's own code
 // (115 KB, 155 KB with conversions) among them: hence rolled loops.
 template <int DP, bool BF16, bool FP8>
 __global__ void __launch_bounds__((AttnCfg<DP, FP8>::kThreads), 1)

@@ -72,8 +72,10 @@ __device__ __forceinline__ int tables_find(const int32_t* a, int n, int x) {
 // request from 8 bytes that L2 holds; no second launch and no hand-over
 // between CTAs), keeps both exclusive sums in shared memory and then serves a
 // share of the tokens and of the new table entries, each found by a binary
-// search in shared memory.  Bound by latency: 64 requests of one token 6.1 us,
-// 2048 requests with 70,000 tokens 8.4 us (0.9 MB).
+// search in shared memory.  Bound by latency: the lengths are read three times,
+// one global latency after the other (for the sums, the exclusive sums and a
+// token's request): 64 requests of one token 6.2 us, of which a launch is 2.7;
+// 2048 requests with 75,000 tokens 8.4 us (0.9 MB).
 __global__ void __launch_bounds__(kTablesThreads) block_tables_kernel(const __grid_constant__ TablesParams p) {
   extern __shared__ int32_t tables_smem[];
   int32_t* start = tables_smem;           // [R + 1]
