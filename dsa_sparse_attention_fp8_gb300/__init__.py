@@ -12,11 +12,15 @@ from .binding import (  # noqa: F401
     add_rms_norm,
     alloc_attention_workspace,
     build_block_tables,
+    combine_experts,
+    fp8_matmul,
+    grouped_matmul,
     kv_write,
     layer_is_full,
     layer_stack_run,
     paged_attention,
     quantize_fp8_blocks,
+    route_experts,
     score_topk,
     workspace_bytes,
     alloc_workspace,

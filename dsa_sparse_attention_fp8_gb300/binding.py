@@ -61,6 +61,10 @@ EXPORTS = (
     "dsa_paged_attention_workspace_bytes",
     "dsa_paged_attention",
     "dsa_add_rms_norm",
+    "dsa_fp8_matmul",
+    "dsa_grouped_matmul",
+    "dsa_route_experts",
+    "dsa_combine_experts",
 )
 
 
@@ -175,6 +179,18 @@ def _declare(lib: ctypes.CDLL) -> None:
     lib.dsa_add_rms_norm.restype = _I
     lib.dsa_add_rms_norm.argtypes = [
         _P, _I64, _P, _I64, _P, _I, _I, _I, _F, _P, _I64, _P, _I64, _P, _P, _P]
+    lib.dsa_fp8_matmul.restype = _I
+    lib.dsa_fp8_matmul.argtypes = [
+        _P, _I64, _P, _I, _P, _I64, _P, _I, _I, _I, _P, _I64, _I, _P, _P, _P, _P]
+    lib.dsa_grouped_matmul.restype = _I
+    lib.dsa_grouped_matmul.argtypes = [
+        _P, _I64, _P, _I, _I, _P, _I, _P, _I64, _I64, _P, _I, _I, _P, _I, _I, _P, _I64, _I, _P, _P, _P, _P]
+    lib.dsa_route_experts.restype = _I
+    lib.dsa_route_experts.argtypes = [
+        _P, _I64, _I, _P, _I, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P, _P, _P, _P, _P]
+    lib.dsa_combine_experts.restype = _I
+    lib.dsa_combine_experts.argtypes = [
+        _P, _I64, _I, _I, _P, _P, _I, _I, _I, _P, _I64, _P, _I64, _P, _P]
     lib.dsa_layer_stack_run_bf16.restype = _I
     lib.dsa_layer_stack_run_bf16.argtypes = [
         _I, ctypes.c_char_p, _I, _I, ctypes.POINTER(LayerIOBf16), _I, _I, _P, _P, _I, _P, _I,
@@ -845,3 +861,162 @@ def add_rms_norm(x: torch.Tensor, residual: Optional[torch.Tensor], weight: torc
     rc = load().dsa_add_rms_norm(*args, _stream_of(stream, dev))
     if rc:
         _check(rc)
+
+
+# ------------------------------------------- products, router, weighted sum
+SCORINGS = {"sigmoid": 0, "softmax": 1}
+
+
+def _blocks(n: int) -> int:
+    """128-element groups of n elements."""
+    return -(-n // NORM_GROUP)
+
+
+def _matmul_out(M, N, gated, x, dtype, out, out_codes, out_scales, device, stream):
+    """The outputs of a product, checked: what it returns, and the entry point's arguments for them."""
+    if gated and N % 2:
+        raise ValueError(f"gated weights have two halves: {N} rows are odd")
+    width = N // 2 if gated else N
+    if out_codes is not None or out_scales is not None:
+        if out is not None:
+            raise ValueError("either out or out_codes and out_scales")
+        if out_codes is None or out_scales is None:
+            raise ValueError("out_codes and out_scales are given together")
+        return (out_codes, out_scales), (
+            None, width, 0, _full(out_codes, "out_codes", torch.uint8, (M, width), device),
+            _full(out_scales, "out_scales", torch.float32, (M, _blocks(width)), device))
+    if out is None:
+        out = _empty((M, width), dtype, x.device, stream)
+    kind = _type_of(out, "out", most=2)
+    strides = _rows(out, "out", out.dtype, (M, width), device)
+    return out, (out.data_ptr(), strides[0] if M > 1 else width, kind, None, None)
+
+
+def fp8_matmul(codes: torch.Tensor, scales: torch.Tensor, w_codes: torch.Tensor,
+               w_scales: torch.Tensor, gated: bool = False, out: Optional[torch.Tensor] = None,
+               out_codes: Optional[torch.Tensor] = None, out_scales: Optional[torch.Tensor] = None,
+               out_dtype: torch.dtype = torch.bfloat16, status: Optional[torch.Tensor] = None,
+               stream=None):
+    """Product of 8-bit rows (codes [T, K] uint8 E4M3, scales [T, ceil(K/128)], as add_rms_norm
+    writes them) and weights (w_codes [N, K], w_scales [ceil(N/128), ceil(K/128)])
+    (dsa_fp8_matmul).  gated: silu of the first half times the second, N/2 wide; with out_codes
+    [T, N/2] uint8 and out_scales [T, ceil(N/256)] the result is quantised for the next product.
+    Returns out [T, N or N/2] (allocated as out_dtype, of the stream of the launch, where it is
+    not given), or (out_codes, out_scales)."""
+    dev = _device_of(codes, "codes")
+    T, K = shape = tuple(codes.shape)
+    N = w_codes.shape[0]
+    a = _rows(codes, "codes", torch.uint8, shape, dev)
+    b = _rows(w_codes, "w_codes", torch.uint8, (N, K), dev)
+    got, args = _matmul_out(T, N, gated, codes, out_dtype, out, out_codes, out_scales, dev, stream)
+    rc = load().dsa_fp8_matmul(
+        codes.data_ptr(), a[0], _full(scales, "scales", torch.float32, (T, _blocks(K)), dev), T,
+        w_codes.data_ptr(), b[0],
+        _full(w_scales, "w_scales", torch.float32, (_blocks(N), _blocks(K)), dev), N, K, gated, *args,
+        _status(status, dev), _stream_of(stream, dev))
+    if rc:
+        _check(rc)
+    return got
+
+
+def grouped_matmul(x: torch.Tensor, weight: torch.Tensor, group_starts: torch.Tensor,
+                   x_scales: Optional[torch.Tensor] = None,
+                   w_scales: Optional[torch.Tensor] = None, rows: Optional[torch.Tensor] = None,
+                   gated: bool = False, out: Optional[torch.Tensor] = None,
+                   out_codes: Optional[torch.Tensor] = None,
+                   out_scales: Optional[torch.Tensor] = None,
+                   out_dtype: Optional[torch.dtype] = None, status: Optional[torch.Tensor] = None,
+                   stream=None):
+    """Products grouped by expert (dsa_grouped_matmul): rows group_starts[e] to group_starts[e+1]
+    times weight[e] of weight [E, N, K].  Row i is x[rows[i]] (rows [M] int32, as route_experts
+    makes them), or x[i] without rows.  x [S, K] and weight are uint8 (E4M3) with x_scales [S,
+    ceil(K/128)] and w_scales [E, ceil(N/128), ceil(K/128)], or both BF16 or FP16.  gated, the
+    outputs [M, ..] and what is returned: as fp8_matmul; out_dtype is x's own unless given (BF16
+    of 8-bit rows).  Rows in no group are left as they were."""
+    dev = _device_of(x, "x")
+    S, K = shape = tuple(x.shape)
+    E, N = weight.shape[0], weight.shape[1]
+    if x.dtype is torch.uint8:
+        if x_scales is None or w_scales is None:
+            raise ValueError("uint8 (E4M3) rows and weights need x_scales and w_scales")
+        kind = TYPE_E4M3
+        xs = _full(x_scales, "x_scales", torch.float32, (S, _blocks(K)), dev)
+        ws = _full(w_scales, "w_scales", torch.float32, (E, _blocks(N), _blocks(K)), dev)
+        dtype = torch.bfloat16
+    else:
+        kind, xs, ws, dtype = _type_of(x, "x"), None, None, x.dtype
+        if x_scales is not None or w_scales is not None:
+            raise ValueError("scales go with uint8 (E4M3) rows and weights")
+    a = _rows(x, "x", x.dtype, shape, dev)
+    b = _rows(weight, "weight", x.dtype, (E, N, K), dev)
+    M, index = S, None
+    if rows is not None:
+        M = rows.shape[0]
+        index = _full(rows, "rows", torch.int32, (M,), dev)
+    got, args = _matmul_out(M, N, gated, x, out_dtype or dtype, out, out_codes, out_scales, dev, stream)
+    rc = load().dsa_grouped_matmul(
+        x.data_ptr(), a[0], xs, kind, S, index, M, weight.data_ptr(), b[1], b[0], ws, N, K,
+        _full(group_starts, "group_starts", torch.int32, (E + 1,), dev), E, gated, *args,
+        _status(status, dev), _stream_of(stream, dev))
+    if rc:
+        _check(rc)
+    return got
+
+
+def route_experts(logits: torch.Tensor, top_k: int, expert_ids: torch.Tensor,
+                  weights: torch.Tensor, group_starts: torch.Tensor, rows: torch.Tensor,
+                  places: torch.Tensor, scoring: str = "sigmoid",
+                  bias: Optional[torch.Tensor] = None, num_groups: int = 1, top_groups: int = 1,
+                  normalize: bool = True, scale: float = 1.0,
+                  num_tokens: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Each token's top_k experts by logits [T, E] and the groups that they make
+    (dsa_route_experts): expert_ids, weights (FP32) and places [T, top_k], group_starts [E+1]
+    and rows [T * top_k] are written (int32).  scoring is "sigmoid" or "softmax"; bias [E] FP32
+    counts in the choice alone; num_groups > 1 chooses within the best top_groups runs of
+    experts; num_tokens [1] int32 (query_start_loc[-1:]) leaves padding rows out."""
+    dev = _device_of(logits, "logits")
+    kind = _type_of(logits, "logits", most=2)
+    T, E = shape = tuple(logits.shape)
+    if scoring not in SCORINGS:
+        raise ValueError(f"scoring must be one of {', '.join(SCORINGS)}, got {scoring!r}")
+    a = _rows(logits, "logits", logits.dtype, shape, dev)
+    i32, pairs = torch.int32, (T, top_k)
+    rc = load().dsa_route_experts(
+        logits.data_ptr(), a[0] if T > 1 else E, kind,
+        None if bias is None else _full(bias, "bias", torch.float32, (E,), dev), T, E, top_k,
+        SCORINGS[scoring], num_groups, top_groups, normalize, scale,
+        None if num_tokens is None else _full(num_tokens, "num_tokens", i32, (1,), dev),
+        _full(expert_ids, "expert_ids", i32, pairs, dev), _full(weights, "weights", torch.float32, pairs, dev),
+        _full(group_starts, "group_starts", i32, (E + 1,), dev), _full(rows, "rows", i32, (T * top_k,), dev),
+        _full(places, "places", i32, pairs, dev), _stream_of(stream, dev))
+    if rc:
+        _check(rc)
+
+
+def combine_experts(y: torch.Tensor, places: torch.Tensor, weights: torch.Tensor,
+                    add: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                    status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """out[t] = add[t] + sum_j weights[t, j] * y[places[t, j]] (dsa_combine_experts): the experts'
+    rows y [M, N] back to their tokens, places and weights [T, top_k] as route_experts writes
+    them.  add and out [T, N] of y's type with any row stride; add may be out.  Returns out."""
+    dev = _device_of(y, "y")
+    kind, dtype = _type_of(y, "y", most=2), y.dtype
+    M, N = tuple(y.shape)
+    T, top_k = pairs = tuple(places.shape)
+    a = _rows(y, "y", dtype, (M, N), dev)
+    if out is None:
+        out = _empty((T, N), dtype, y.device, stream)
+
+    def row(t, name):  # address and row stride
+        if t is None:
+            return None, N
+        strides = _rows(t, name, dtype, (T, N), dev)
+        return t.data_ptr(), strides[0] if T > 1 else N
+
+    rc = load().dsa_combine_experts(
+        y.data_ptr(), a[0] if M > 1 else N, kind, M, _full(places, "places", torch.int32, pairs, dev),
+        _full(weights, "weights", torch.float32, pairs, dev), T, top_k, N, *row(add, "add"), *row(out, "out"),
+        _status(status, dev), _stream_of(stream, dev))
+    if rc:
+        _check(rc)
+    return out

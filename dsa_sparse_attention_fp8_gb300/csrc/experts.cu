@@ -1,0 +1,189 @@
+// C ABI of the operators behind the norm's 8-bit rows: the block-scaled product, the products grouped by expert, the router
+// and the weighted sum of the experts' rows.  See include/dsa_indexer.h for the contract of every entry point.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "combine.cuh"
+#include "dsa_indexer.h"
+#include "host.h"
+#include "host_tensors.h"
+#include "matmul.cuh"
+#include "route.cuh"
+
+namespace {
+
+using namespace dsa_host;
+
+bool is_float(int type) { return type == DSA_TYPE_BF16 || type == DSA_TYPE_FP16 || type == DSA_TYPE_FP32; }
+
+// The checks that both products share, and their launch.  p has the sizes, strides and pointers.
+int run_matmul(dsa::MatmulParams p, int64_t groups, cudaStream_t st) {
+  if (p.M < 0 || p.x_rows < 0) return fail(DSA_ERR_INVALID_ARG, "a negative number of rows");
+  if (p.N < 1 || p.K < 1) return fail(DSA_ERR_INVALID_ARG, "N=%d, K=%d: both must be positive", p.N, p.K);
+  if (p.gated && p.N % 2) return fail(DSA_ERR_INVALID_ARG, "gated weights have two halves: N=%d is odd", p.N);
+  p.width = p.gated ? p.N / 2 : p.N;
+  const bool fp8 = p.x_type == DSA_TYPE_E4M3;
+  if (fp8 && p.gated && p.width % 64)
+    return fail(DSA_ERR_UNSUPPORTED, "gated E4M3 weights: N/2=%d is no multiple of 64", p.width);
+  if ((p.out || !p.codes) && !is_float(p.out_type)) return fail(DSA_ERR_UNSUPPORTED, "out_type=%d: BF16, FP16 or FP32 is wanted", p.out_type);
+  if (p.out && p.M > 1 && p.out_stride < p.width) return fail(DSA_ERR_INVALID_ARG, "out's row stride is shorter than a row");
+  const int size = element_bytes(p.x_type), unit = 16 / size;
+  if (!stride_ok(p.x_stride, p.x_rows, unit) || !stride_ok(p.w_stride, p.N, unit) || !stride_ok(p.w_group, groups, unit))
+    return fail(DSA_ERR_INVALID_ARG, "strides of rows and weights must be multiples of 16 bytes");
+  if (!apart(p.x_stride, p.x_rows) || !apart(p.w_stride, p.N) || !apart(p.w_group, groups))
+    return fail(DSA_ERR_INVALID_ARG, "a stride of 0 over more than one row");
+  if (p.M == 0) return DSA_OK;
+  if ((p.out != nullptr) == (p.codes != nullptr) || (p.codes != nullptr) != (p.scales != nullptr))
+    return fail(DSA_ERR_INVALID_ARG, "either out or out_codes and out_scales");
+  if (p.codes && !p.gated) return fail(DSA_ERR_UNSUPPORTED, "8-bit results are those of gated products");
+  if (!p.x || !p.w) return fail(DSA_ERR_INVALID_ARG, "null pointer");
+  if (fp8 && (!p.x_scales || !p.w_scales)) return fail(DSA_ERR_INVALID_ARG, "E4M3 rows and weights need their scales");
+  if (!aligned(p.x, 16) || !aligned(p.w, 16)) return fail(DSA_ERR_INVALID_ARG, "rows and weights must be 16-byte aligned");
+  if (p.out && !aligned(p.out, element_bytes(p.out_type))) return fail(DSA_ERR_INVALID_ARG, "out is not aligned to its elements");
+  p.kb = (p.K + dsa::kMatmulBlock - 1) / dsa::kMatmulBlock;
+  p.nb = (p.N + dsa::kMatmulBlock - 1) / dsa::kMatmulBlock;
+  if (!fp8) p.x_scales = p.w_scales = nullptr;
+  const dim3 grid((unsigned)((p.M + dsa::kSimpleRows - 1) / dsa::kSimpleRows + (p.starts ? p.E : 0)), (p.width + 127) / 128);
+  dsa::matmul_kernel<<<grid, 128, 0, st>>>(p);
+  set_last_launches(1);
+  return check_launch("matmul_kernel");
+}
+
+template <int V>
+void launch_choose(const dsa::RouteParams& p, int type, cudaStream_t st) {
+  const unsigned grid = (unsigned)(((int64_t)p.T * 32 + dsa::kRouteThreads - 1) / dsa::kRouteThreads);
+  if (type == DSA_TYPE_BF16) dsa::route_choose_kernel<V, __nv_bfloat16><<<grid, dsa::kRouteThreads, 0, st>>>(p);
+  else if (type == DSA_TYPE_FP16) dsa::route_choose_kernel<V, __half><<<grid, dsa::kRouteThreads, 0, st>>>(p);
+  else dsa::route_choose_kernel<V, float><<<grid, dsa::kRouteThreads, 0, st>>>(p);
+}
+
+template <typename T>
+void launch_combine(const dsa::CombineParams& p, bool vec, cudaStream_t st) {
+  const int block = std::min(256, (p.N / 8 + 31) / 32 * 32 + 32);
+  if (vec) dsa::combine_kernel<T, true><<<p.T, block, 0, st>>>(p);
+  else dsa::combine_kernel<T, false><<<p.T, block, 0, st>>>(p);
+}
+
+}  // namespace
+
+extern "C" {
+
+int dsa_fp8_matmul(const uint8_t* codes, int64_t stride, const float* scales, int T,
+                   const uint8_t* w_codes, int64_t w_stride, const float* w_scales, int N, int K,
+                   int gated, void* out, int64_t out_stride, int out_type, uint8_t* out_codes,
+                   float* out_scales, int32_t* dev_status, dsa_stream_t stream) {
+  set_last_launches(0);
+  dsa::MatmulParams p{};
+  p.x = codes, p.x_scales = scales, p.w = w_codes, p.w_scales = w_scales;
+  p.out = out, p.codes = out_codes, p.scales = out_scales, p.status = dev_status;
+  p.x_stride = stride, p.w_stride = w_stride, p.out_stride = out_stride;
+  p.x_rows = T, p.M = T, p.N = N, p.K = K, p.E = 1;
+  p.x_type = DSA_TYPE_E4M3, p.out_type = out_type, p.gated = gated != 0;
+  return run_matmul(p, 1, (cudaStream_t)stream);
+}
+
+int dsa_grouped_matmul(const void* x, int64_t x_stride, const float* x_scales, int x_type, int x_rows,
+                       const int32_t* rows, int M, const void* weight, int64_t w_row_stride,
+                       int64_t w_group_stride, const float* w_scales, int N, int K,
+                       const int32_t* group_starts, int E, int gated, void* out, int64_t out_stride,
+                       int out_type, uint8_t* out_codes, float* out_scales, int32_t* dev_status,
+                       dsa_stream_t stream) {
+  set_last_launches(0);
+  if (x_type != DSA_TYPE_E4M3 && x_type != DSA_TYPE_BF16 && x_type != DSA_TYPE_FP16)
+    return fail(DSA_ERR_UNSUPPORTED, "x_type=%d: BF16, FP16 or E4M3 is wanted", x_type);
+  if (E < 1) return fail(DSA_ERR_INVALID_ARG, "E=%d < 1", E);
+  if (E > dsa::kMatmulMaxGroups) return fail(DSA_ERR_UNSUPPORTED, "E=%d > %d", E, dsa::kMatmulMaxGroups);
+  if (!rows && M != x_rows) return fail(DSA_ERR_INVALID_ARG, "without rows, M=%d must be x_rows=%d", M, x_rows);
+  if (M > 0 && x_rows < 1) return fail(DSA_ERR_INVALID_ARG, "x_rows=%d < 1", x_rows);
+  if (M > 0 && !group_starts) return fail(DSA_ERR_INVALID_ARG, "null pointer");
+  dsa::MatmulParams p{};
+  p.x = x, p.x_scales = x_scales, p.rows = rows, p.w = weight, p.w_scales = w_scales, p.starts = group_starts;
+  p.out = out, p.codes = out_codes, p.scales = out_scales, p.status = dev_status;
+  p.x_stride = x_stride, p.w_stride = w_row_stride, p.w_group = w_group_stride, p.out_stride = out_stride;
+  p.x_rows = x_rows, p.M = M, p.N = N, p.K = K, p.E = E;
+  p.x_type = x_type, p.out_type = out_type, p.gated = gated != 0;
+  return run_matmul(p, E, (cudaStream_t)stream);
+}
+
+int dsa_route_experts(const void* logits, int64_t stride, int type, const float* bias, int T, int E,
+                      int top_k, int scoring, int num_groups, int top_groups, int normalize,
+                      float scale, const int32_t* num_tokens, int32_t* expert_ids, float* weights,
+                      int32_t* group_starts, int32_t* rows, int32_t* places, dsa_stream_t stream) {
+  set_last_launches(0);
+  if (T < 0) return fail(DSA_ERR_INVALID_ARG, "T=%d < 0", T);
+  if (E < 1) return fail(DSA_ERR_INVALID_ARG, "E=%d < 1", E);
+  if (E > dsa::kRouteMaxExperts) return fail(DSA_ERR_UNSUPPORTED, "E=%d > %d", E, dsa::kRouteMaxExperts);
+  if (!is_float(type)) return fail(DSA_ERR_UNSUPPORTED, "type=%d: BF16, FP16 or FP32 is wanted", type);
+  if (top_k < 1) return fail(DSA_ERR_INVALID_ARG, "top_k=%d < 1", top_k);
+  if (top_k > dsa::kRouteMaxTop) return fail(DSA_ERR_UNSUPPORTED, "top_k=%d > %d", top_k, dsa::kRouteMaxTop);
+  if (scoring != DSA_SCORE_SIGMOID && scoring != DSA_SCORE_SOFTMAX)
+    return fail(DSA_ERR_INVALID_ARG, "scoring=%d is neither DSA_SCORE_SIGMOID nor DSA_SCORE_SOFTMAX", scoring);
+  if (num_groups < 1 || E % num_groups) return fail(DSA_ERR_INVALID_ARG, "num_groups=%d does not divide E=%d", num_groups, E);
+  if (num_groups > dsa::kRouteMaxRuns)
+    return fail(DSA_ERR_UNSUPPORTED, "num_groups=%d > %d", num_groups, dsa::kRouteMaxRuns);
+  if (top_groups < 1 || top_groups > num_groups)
+    return fail(DSA_ERR_INVALID_ARG, "top_groups=%d outside [1, %d]", top_groups, num_groups);
+  if (top_k > top_groups * (E / num_groups))
+    return fail(DSA_ERR_INVALID_ARG, "top_k=%d of %d experts in the chosen groups", top_k, top_groups * (E / num_groups));
+  if (!(scale == scale) || scale - scale != 0.0f) return fail(DSA_ERR_INVALID_ARG, "scale must be finite");
+  if ((int64_t)T * top_k > INT32_MAX) return fail(DSA_ERR_UNSUPPORTED, "T=%d times top_k=%d exceeds 2^31", T, top_k);
+  if (T > 1 && stride < E) return fail(DSA_ERR_INVALID_ARG, "the row stride is shorter than E");
+  if (!group_starts) return fail(DSA_ERR_INVALID_ARG, "null pointer");
+  if (T && (!logits || !expert_ids || !weights || !rows || !places)) return fail(DSA_ERR_INVALID_ARG, "null pointer");
+  dsa::RouteParams p{};
+  p.logits = logits, p.bias = bias, p.num_tokens = num_tokens;
+  p.ids = expert_ids, p.weights = weights, p.starts = group_starts, p.rows = rows, p.places = places;
+  p.stride = stride, p.T = T, p.E = E, p.top_k = top_k;
+  p.num_groups = num_groups, p.top_groups = top_groups, p.per = E / num_groups;
+  p.scale = scale, p.softmax = scoring == DSA_SCORE_SOFTMAX, p.normalize = normalize != 0;
+  const cudaStream_t st = (cudaStream_t)stream;
+  const int smem = (dsa::kPlaceThreads / 32 + 1) * E * 4;
+  static PerDevice allowed;
+  if (const int rc = allow_smem(allowed, (const void*)dsa::route_place_kernel, (dsa::kPlaceThreads / 32 + 1) * dsa::kRouteMaxExperts * 4))
+    return rc;
+  if (T) {
+    if (E <= 32) launch_choose<1>(p, type, st);
+    else if (E <= 64) launch_choose<2>(p, type, st);
+    else if (E <= 128) launch_choose<4>(p, type, st);
+    else if (E <= 256) launch_choose<8>(p, type, st);
+    else launch_choose<16>(p, type, st);
+    if (const int rc = check_launch("route_choose_kernel")) return rc;
+  }
+  dsa::route_place_kernel<<<1, dsa::kPlaceThreads, smem, st>>>(p);
+  set_last_launches(T ? 2 : 1);
+  return check_launch("route_place_kernel");
+}
+
+int dsa_combine_experts(const void* y, int64_t y_stride, int type, int M, const int32_t* places,
+                        const float* weights, int T, int top_k, int N, const void* add,
+                        int64_t add_stride, void* out, int64_t out_stride, int32_t* dev_status,
+                        dsa_stream_t stream) {
+  set_last_launches(0);
+  if (T < 0 || M < 0) return fail(DSA_ERR_INVALID_ARG, "a negative number of rows");
+  if (N < 1) return fail(DSA_ERR_INVALID_ARG, "N=%d < 1", N);
+  if (top_k < 1) return fail(DSA_ERR_INVALID_ARG, "top_k=%d < 1", top_k);
+  if (top_k > dsa::kCombineMaxTop) return fail(DSA_ERR_UNSUPPORTED, "top_k=%d > %d", top_k, dsa::kCombineMaxTop);
+  if (!is_float(type)) return fail(DSA_ERR_UNSUPPORTED, "type=%d: BF16, FP16 or FP32 is wanted", type);
+  if ((M > 1 && y_stride < N) || (T > 1 && ((add && add_stride < N) || out_stride < N)))
+    return fail(DSA_ERR_INVALID_ARG, "a row stride is shorter than N");
+  if (T == 0) return DSA_OK;
+  if ((M && !y) || !places || !weights || !out) return fail(DSA_ERR_INVALID_ARG, "null pointer");
+  const int size = element_bytes(type);
+  if (!aligned(y, size) || !aligned(add, size) || !aligned(out, size))
+    return fail(DSA_ERR_INVALID_ARG, "rows are not aligned to their elements");
+  const dsa::CombineParams p{y, places, weights, add, out, dev_status, y_stride, add_stride, out_stride, M, T, top_k, N};
+  auto row16 = [&](const void* ptr, int64_t stride, int64_t n) {
+    return !ptr || (aligned(ptr, 16) && (n <= 1 || stride * size % 16 == 0));
+  };
+  const bool vec = N % 8 == 0 && row16(y, y_stride, M) && row16(add, add_stride, T) && row16(out, out_stride, T);
+  const cudaStream_t st = (cudaStream_t)stream;
+  if (type == DSA_TYPE_BF16) launch_combine<__nv_bfloat16>(p, vec, st);
+  else if (type == DSA_TYPE_FP16) launch_combine<__half>(p, vec, st);
+  else launch_combine<float>(p, vec, st);
+  set_last_launches(1);
+  return check_launch("combine_kernel");
+}
+
+}  // extern "C"

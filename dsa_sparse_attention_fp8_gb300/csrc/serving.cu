@@ -9,6 +9,7 @@
 
 #include "dsa_indexer.h"
 #include "host.h"
+#include "host_tensors.h"
 #include "kvcache.cuh"
 #include "norm.cuh"
 #include "paged_attention.cuh"
@@ -17,16 +18,6 @@
 namespace {
 
 using namespace dsa_host;
-
-int element_bytes(int type) { return type == DSA_TYPE_FP32 ? 4 : type == DSA_TYPE_E4M3 ? 1 : 2; }
-
-// Whether a stride over n elements is neither negative nor off a multiple of
-// `unit` (one element may have any stride: nothing is ever a stride away).
-bool stride_ok(int64_t stride, int64_t n, int unit) { return n <= 1 || (stride >= 0 && stride % unit == 0); }
-
-// Whether a stride over n elements keeps them apart, as what is written, or read
-// by way of a tensor map, has to be.
-bool apart(int64_t stride, int64_t n) { return n <= 1 || stride != 0; }
 
 // A K/V cache as the kernels need it: 16-byte aligned heads, at most 128
 // elements each.
@@ -99,28 +90,6 @@ int attention_grid() {
 constexpr size_t kAttnCounterBytes = 2048;
 static_assert(kAttnCounterBytes >= 3 * dsa::kAttnMaxGrid * 4, "counters");
 size_t attention_part_rows() { return (size_t)attention_grid() * 2 * 256; }
-
-// A map over up to four dimensions, innermost first; strides in bytes (of
-// dimensions 1 on).  A dimension of one element may have any stride: it gets
-// one that the encoder takes.
-int make_map(CUtensorMap* m, const char* what, CUtensorMapDataType type, int size, const void* base, int rank,
-             const int64_t* dims, const int64_t* strides, const int* box, bool swizzle) {
-  auto fn = encode_fn();
-  if (!fn) return fail(DSA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
-  cuuint64_t d[4], st[3];
-  cuuint32_t b[4], e[4];
-  for (int i = 0; i < rank; ++i) {
-    d[i] = (cuuint64_t)dims[i];
-    b[i] = (cuuint32_t)box[i];
-    e[i] = 1;
-    if (i > 0) st[i - 1] = dims[i] > 1 ? (cuuint64_t)strides[i - 1] : (cuuint64_t)((dims[0] * size + 15) / 16 * 16);
-  }
-  const CUresult r = fn(m, type, (cuuint32_t)rank, const_cast<void*>(base), d, st, b, e, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return fail(DSA_ERR_CUDA, "cuTensorMapEncodeTiled(%s) failed (%d)", what, (int)r);
-  return DSA_OK;
-}
 
 template <int DP, bool BF16, bool FP8>
 int launch_attention(const dsa::AttnParams& p, int grid, cudaStream_t st) {

@@ -560,6 +560,113 @@ int dsa_add_rms_norm(const void* x, int64_t x_stride, const void* residual, int6
                      float* scales, dsa_stream_t stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * Behind the norm: products of 8-bit rows, products grouped by expert, the
+ * router that makes the groups and the sum that brings the experts' rows back.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * Product of E4M3 rows and weights whose scales belong to blocks of K:
+ *   y[t, n] = sum_b scales[t, b] * w_scales[n / 128, b] *
+ *             sum_{k in [128 b, 128 b + 128)} codes[t, k] * w_codes[n, k]
+ * codes [T, K] and scales [T, ceil(K/128)] are rows as dsa_add_rms_norm writes
+ * them, w_codes [N, K] and w_scales [ceil(N/128), ceil(K/128)] weights with a
+ * scale for each 128 x 128 block.
+ *   gated != 0: the first N/2 weight rows are gates, the others what they
+ *     gate, and a row's result is silu(y[t, i]) * y[t, N/2 + i], N/2 elements
+ *     (silu(g) = g / (1 + exp(-g))).  N/2 is a multiple of 64 here, so that 64
+ *     weight rows lie in one block of scales.
+ *   out [T, N or N/2] of out_type (BF16, FP16, FP32), row stride out_stride, or
+ *   out_codes and out_scales (gated only): the result quantised per 128
+ *     elements with the rule of the indexer cache (s = amax/448, 1 where that
+ *     is 0; codes E4M3(y/s), RNE, saturating), [T, N/2] and [T, ceil(N/256)]
+ *     contiguous.  Exactly one of the two is given.
+ * Row strides are in elements; those of codes and w_codes are multiples of 16,
+ * both 16-byte aligned.  K and N are any sizes from 1.  Outputs must not
+ * overlap inputs.
+ * Computation: tensor-core products with FP32 accumulation over a block of K,
+ * its scales and the sums over blocks in FP32, gate in FP32, one rounding.
+ * Faults: DSA_STATUS_TIMEOUT (an internal wait ran out; results are invalid).
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA.
+ */
+int dsa_fp8_matmul(const uint8_t* codes, int64_t stride, const float* scales, int T,
+                   const uint8_t* w_codes, int64_t w_stride, const float* w_scales, int N, int K,
+                   int gated, void* out, int64_t out_stride, int out_type, uint8_t* out_codes,
+                   float* out_scales, int32_t* dev_status, dsa_stream_t stream);
+
+/*
+ * Products grouped by expert: row i of group e, group_starts[e] <= i <
+ * group_starts[e + 1], is x[rows[i]] (x[i] where rows is NULL) times weight[e].
+ *   x       [x_rows, K] of x_type: E4M3 codes with x_scales [x_rows,
+ *           ceil(K/128)] contiguous, or BF16 / FP16 without.
+ *   weight  [E, N, K] of the same type; w_scales [E, ceil(N/128), ceil(K/128)]
+ *           contiguous (E4M3 only).
+ *   group_starts [E + 1] on the device, rows [M] or NULL (then x_rows = M).
+ *   gated, out [M, ..], out_codes, out_scales: as dsa_fp8_matmul, with BF16
+ *           and FP16 too (any even N).
+ * Row and group strides are in elements, multiples of 16 bytes.  Rows that lie
+ * in no group are left as they were.  Groups may be empty.  E <= 1024.
+ * Faults: a group that is not within [0, M] or ends before it starts is
+ * skipped, an index in rows outside [0, x_rows) gives a row of zeros:
+ * DSA_STATUS_BAD_METADATA.  (Groups that overlap, which only starts that go
+ * back make, leave either's result in the rows they share.)  DSA_STATUS_TIMEOUT
+ * as above.  Errors: INVALID_ARG, UNSUPPORTED, CUDA.
+ */
+int dsa_grouped_matmul(const void* x, int64_t x_stride, const float* x_scales, int x_type, int x_rows,
+                       const int32_t* rows, int M, const void* weight, int64_t w_row_stride,
+                       int64_t w_group_stride, const float* w_scales, int N, int K,
+                       const int32_t* group_starts, int E, int gated, void* out, int64_t out_stride,
+                       int out_type, uint8_t* out_codes, float* out_scales, int32_t* dev_status,
+                       dsa_stream_t stream);
+
+/*
+ * Each token's experts and the groups that they make.
+ *   s[t, e] = sigmoid(logits[t, e]) or softmax over e, v = s + bias (bias [E]
+ *   FP32 or NULL).  With num_groups > 1 the experts are num_groups runs of
+ *   E/num_groups, a run's value is the sum of its best two v (its best where it
+ *   has one), and only the top_groups best runs are chosen from.  A token's
+ *   experts are the top_k of largest v, largest first.  Ties go to the lowest
+ *   index; values are compared as in 64 bits (by the logits themselves where
+ *   there is neither a bias nor a run).
+ *   expert_ids [T, top_k], weights [T, top_k] FP32: scale * s, divided by the
+ *     sum of the chosen s where normalize != 0 (0 where that sum is 0).
+ *   group_starts [E + 1], rows [T * top_k], places [T, top_k]: the choices
+ *     sorted by expert, and by token within an expert: places is where a
+ *     choice went, rows the token of each place, as dsa_grouped_matmul and
+ *     dsa_combine_experts take them.  Entries of rows from group_starts[E] on
+ *     are left as they were.
+ *   num_tokens: NULL, or on the device how many of the T rows are real (a batch
+ *     padded to a fixed T; query_start_loc + R).  The others get expert -1,
+ *     weight 0, place -1, and no place in the groups.
+ * logits [T, E] BF16, FP16 or FP32, row stride in elements.  NaN counts as
+ * -inf, +inf as the largest finite value.  E <= 512, top_k <= 16, num_groups
+ * <= 32 dividing E, top_k <= top_groups * E / num_groups.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA.
+ */
+#define DSA_SCORE_SIGMOID 0
+#define DSA_SCORE_SOFTMAX 1
+int dsa_route_experts(const void* logits, int64_t stride, int type, const float* bias, int T, int E,
+                      int top_k, int scoring, int num_groups, int top_groups, int normalize,
+                      float scale, const int32_t* num_tokens, int32_t* expert_ids, float* weights,
+                      int32_t* group_starts, int32_t* rows, int32_t* places, dsa_stream_t stream);
+
+/*
+ * The experts' rows back to their tokens:
+ *   out[t] = add[t] + sum_j weights[t, j] * y[places[t, j]]
+ * y [M, N], add and out [T, N] of one type (BF16, FP16, FP32), row strides in
+ * elements, >= N; add may be NULL, and may be out itself.  places and weights
+ * [T, top_k] contiguous, top_k <= 16; a negative place contributes nothing.
+ * Sums in FP32, in the order of j, add last; one rounding.
+ * Faults: a place >= M contributes nothing: DSA_STATUS_BAD_METADATA.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA.
+ */
+int dsa_combine_experts(const void* y, int64_t y_stride, int type, int M, const int32_t* places,
+                        const float* weights, int T, int top_k, int N, const void* add,
+                        int64_t add_stride, void* out, int64_t out_stride, int32_t* dev_status,
+                        dsa_stream_t stream);
+
+/*
  * Number of kernel launches the last successful call of each entry point on
  * this thread enqueued (for launch accounting by benchmarks).
  */

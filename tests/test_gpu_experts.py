@@ -1,0 +1,512 @@
+"""The block-scaled product, the products grouped by expert, the router and the experts' sum (GPU), against plain
+implementations in 64 bits.
+
+Bars, worst-case, per element, on the 64-bit values (A = sum_k |x_k w_k| with the scales, u = eps/2 of the output's type):
+  * a product y: sums in FP32, even truncating, of the elements of a block of K (all of K without scales), then of the
+    blocks with their scales' products: |dy| <= (n + blocks + 3) 2^-23 A, n = min(K, 128) or K;
+  * gated: |silu'| <= 1.1 and |silu(g)| <= |g|, so (1.1 dg |u| + |g| du + 1.1 dg du); the gate itself: exponential
+    (4 + 1.2 |g|) 2^-23, quotient 2^-21, of |silu(g) u|;
+  * rounded outputs: u |y| (FP16 also 2^-25: below 2^-14 its steps are 2^-24);
+  * 8-bit outputs: the scale is off by dy_max / 448 and 2^-23 of itself; a code stands for y / scale rounded to 4 bits:
+    2^-4 |y|, or 2^-10 scale where E4M3 is subnormal, and what y and the scale are off by, 2^-4 of that more;
+  * router: whole numbers are exact; weights' exponentials and sums in FP32: 2^-18 + 2^-23 max|l - max l|, relative;
+  * sum: (top_k + 2) 2^-24 sum_j |w_j y_j| and the rounding.
+"""
+
+import pytest
+import torch
+
+from conftest import gpu_available
+
+pytestmark = pytest.mark.gpu
+BF, HALF, F32, U8 = torch.bfloat16, torch.float16, torch.float32, torch.uint8
+E4M3 = torch.float8_e4m3fn
+
+
+@pytest.fixture(scope="module")
+def B(lib):
+    if not gpu_available():
+        pytest.skip("no CUDA device")
+    from dsa_sparse_attention_fp8_gb300 import binding
+    return binding
+
+
+def ints(v, dtype=torch.int32):
+    return torch.tensor(v, dtype=dtype, device="cuda")
+
+
+def wide(scale, n):
+    return scale.double().repeat_interleave(128, -1)[..., :n]
+
+
+def ceil(a, b=128):
+    return -(-a // b)
+
+
+# ------------------------------------------------------------------ products
+class Product:
+    """Operands of a product and its 64-bit result: `counts` rows to each group (dense: one number), weights [E, N, K]."""
+
+    def __init__(self, counts, N, K, kind=U8, gather=False, gated=False, seed=0, pad=0, lead=0):
+        g = torch.Generator(device="cuda").manual_seed(seed + N * 7 + K)
+        rand = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+        self.E, self.N, self.K, self.kind, self.gated = len(counts), N, K, kind, gated
+        self.lead = lead                                   # rows before the first group
+        starts = [lead]
+        for c in counts:
+            starts.append(starts[-1] + c)
+        self.starts_list, self.M = starts, starts[-1] + pad     # and after the last
+        S = max(1, self.M if not gather else max(1, self.M // 2 + 1))
+        self.rows = torch.randint(0, S, (self.M,), generator=g, device="cuda").int() if gather else None
+        unit = 16 if kind is U8 else 8
+        width = ceil(K, unit) * unit + unit                     # rows lie apart
+        x, w = rand(S, width), rand(self.E, N, width) * K ** -0.5
+        if kind is U8:
+            self.x, self.w = (40 * x).clamp(-448, 448).to(E4M3).view(U8), (110 * K ** 0.5 * w).clamp(-448, 448).to(E4M3).view(U8)
+            self.xs = (0.5 + torch.rand(S, ceil(K), generator=g, device="cuda")) / 40
+            self.ws = (0.5 + torch.rand(self.E, ceil(N), ceil(K), generator=g, device="cuda")) / (110 * K ** 0.5)
+        else:
+            self.x, self.w, self.xs, self.ws = x.to(kind), w.to(kind), None, None
+        self.x, self.w = self.x[:, :K], self.w[:, :, :K]
+        self.starts = ints(starts)
+
+    def values(self):
+        if self.kind is not U8:
+            return self.x.double(), self.w.double()
+        w = self.w.view(E4M3).double() * wide(self.ws, self.K).repeat_interleave(128, 1)[:, : self.N]
+        return self.x.view(E4M3).double() * wide(self.xs, self.K), w
+
+    def want(self):
+        """(y, bar) [M, width] in 64 bits; rows in no group are NaN."""
+        x, w = self.values()
+        if self.rows is not None:
+            x = x[self.rows.long()]
+        n = min(self.K, 128) if self.kind is U8 else self.K
+        rel = (n + (ceil(self.K) if self.kind is U8 else 0) + 3) * 2.0 ** -23
+        y = torch.full((self.M, self.N), torch.nan, dtype=torch.float64, device="cuda")
+        bar = y.clone()
+        for e in range(self.E):
+            a, b = self.starts_list[e:e + 2]
+            y[a:b], bar[a:b] = x[a:b] @ w[e].T, rel * (x[a:b].abs() @ w[e].abs().T)
+        if not self.gated:
+            return y, bar
+        (g, u), (dg, du) = y.chunk(2, 1), bar.chunk(2, 1)
+        out = g * torch.sigmoid(g) * u
+        return out, 1.1 * dg * u.abs() + g.abs() * du + 1.1 * dg * du + ((4 + 1.2 * g.abs()) * 2.0 ** -23 + 2.0 ** -21) * out.abs()
+
+    def call(self, B, out=None, codes=None, scales=None, dense=False, **kw):
+        kw.update(out=out, out_codes=codes, out_scales=scales, gated=self.gated)
+        if dense:
+            return B.fp8_matmul(self.x, self.xs, self.w[0], self.ws[0], **kw)
+        return B.grouped_matmul(self.x, self.w, self.starts, self.xs, self.ws, rows=self.rows, **kw)
+
+    def check(self, B, out_type, dense=False):
+        y, bar = self.want()
+        in_group = torch.zeros(self.M, dtype=torch.bool, device="cuda")
+        in_group[self.lead: self.starts_list[-1]] = True
+        width = y.shape[1]
+        status = ints([0])
+        if out_type is U8:
+            codes = torch.full((self.M, width), 77, dtype=U8, device="cuda")
+            scales = torch.full((self.M, ceil(width)), -5.0, device="cuda")
+            got = self.call(B, codes=codes, scales=scales, dense=dense, status=status)
+            assert got[0] is codes and got[1] is scales and status.item() == 0
+            assert (codes[~in_group] == 77).all() and (scales[~in_group] == -5).all()
+            y, bar, codes, scales = y[in_group], bar[in_group], codes[in_group], scales[in_group].double()
+            for b in range(ceil(width)):
+                part = slice(128 * b, 128 * b + 128)
+                most = y[:, part].abs().amax(1)
+                s, ds = scales[:, b], bar[:, part].amax(1) / 448
+                w = torch.where(most == 0, torch.ones_like(most), most / 448)
+                ok = (s - w).abs() <= ds + 2.0 ** -23 * w
+                assert ok.all(), f"scale off by {(s - w).abs().max()}"
+                near = codes[:, part].view(E4M3).double() * s[:, None]
+                d = bar[:, part] + (ds + 2.0 ** -23 * w)[:, None] * (y[:, part].abs() / w[:, None])
+                lim = torch.maximum(2.0 ** -4 * y[:, part].abs(), 2.0 ** -10 * s[:, None]) + (1 + 2.0 ** -4) * d
+                over = (near - y[:, part]).abs() - lim
+                assert (over <= 0).all(), f"codes off by {over.max()} more than the bar"
+            return
+        dtype = out_type
+        box = torch.full((self.M, width + 24), 3.0, dtype=dtype, device="cuda")
+        out = box[:, 8:8 + width]
+        assert self.call(B, out=out, dense=dense, status=status) is out and status.item() == 0
+        assert (box[:, :8] == 3).all() and (box[:, 8 + width:] == 3).all() and (out[~in_group] == 3).all()
+        lim = bar + torch.finfo(dtype).eps / 2 * (y.abs() + bar) + (2.0 ** -25 if dtype is HALF else 0.0)
+        d = ((out.double() - y).abs() - lim)[in_group]
+        assert d.numel() == 0 or d.max() <= 0, f"off by {d.max()} more than the bar of {lim[in_group].max()}"
+
+
+DENSE = [
+    # T, N, K, gated, output
+    (1, 1, 1, False, F32), (1, 1, 16, False, BF), (1, 16, 128, False, BF), (3, 17, 130, False, HALF), (1, 129, 1040, False, BF),
+    (64, 256, 256, False, F32), (127, 255, 127, False, BF), (128, 256, 512, False, HALF), (129, 257, 640, False, BF),
+    (255, 300, 1000, False, F32), (257, 513, 896, False, BF), (600, 577, 1040, False, F32), (33, 2112, 2176, False, BF),
+    (1, 128, 384, True, BF), (1, 128, 16, True, U8), (31, 256, 272, True, U8), (64, 384, 1024, True, HALF), (200, 640, 144, True, U8),
+    (300, 1024, 520, True, U8), (130, 1152, 384, True, F32), (5, 4096, 7168, True, U8), (16, 192 * 2, 7168, True, BF),
+    (1000, 128, 4096, False, BF), (64, 64, 7168, False, BF), (2, 7168, 64, False, F32), (700, 1111, 3000, False, BF),
+]
+
+
+@pytest.mark.parametrize("T,N,K,gated,out", DENSE)
+def test_fp8_matmul(B, T, N, K, gated, out):
+    Product([T], N, K, gated=gated, seed=T).check(B, out, dense=True)
+
+
+GROUPS = [
+    [1], [0, 1, 0], [5, 0, 0, 130, 1, 64], [128, 128], [127, 129, 3], [300, 0, 17, 256, 1, 31, 33], [1] * 70, [0, 0, 0],
+    [2, 0, 1, 4, 3] * 13, [600, 40],
+]
+
+
+@pytest.mark.parametrize("counts", GROUPS)
+@pytest.mark.parametrize("kind,gated,out,N,K,gather", [
+    (U8, False, BF, 200, 272, True), (U8, True, U8, 384, 400, True), (U8, False, F32, 33, 640, False),
+    (BF, False, BF, 129, 200, False), (BF, True, BF, 130, 136, True), (HALF, False, F32, 256, 1032, True),
+    (HALF, True, U8, 300, 64, False), (BF, True, U8, 512, 8, True),
+])
+def test_grouped_matmul(B, counts, kind, gated, out, N, K, gather):
+    Product(counts, N, K, kind, gather, gated, seed=len(counts), pad=3, lead=2 if gather else 0).check(B, out)
+
+
+@pytest.mark.parametrize("kind,gated,out,N,K", [(U8, True, U8, 4096, 1024), (BF, False, BF, 1408, 2048), (U8, False, BF, 2048, 2048)])
+def test_grouped_matmul_of_many_rows(B, kind, gated, out, N, K):
+    Product([700, 0, 1024, 3, 513, 256, 255], N, K, kind, kind is U8, gated).check(B, out)
+
+
+def test_allocated_outputs(B):
+    p = Product([5], 64, 256)
+    for dtype in (BF, HALF, F32):
+        got = B.fp8_matmul(p.x, p.xs, p.w[0], p.ws[0], out_dtype=dtype)
+        assert got.shape == (5, 64) and got.dtype is dtype
+    assert B.fp8_matmul(p.x[:0], p.xs[:0], p.w[0], p.ws[0]).shape == (0, 64)
+    p = Product([5, 2], 64, 256, HALF, gather=True)
+    assert p.call(B).dtype is HALF and p.call(B).shape == (7, 64) and p.call(B, out_dtype=F32).dtype is F32
+
+
+def test_bad_groups_and_rows_are_reported(B):
+    """Groups outside the rows are skipped, an index outside x gives zeros; everything else is as it should be."""
+    p = Product([10, 20, 30, 5], 128, 256, gather=True)
+    y = p.want()[0]
+    p.rows[3], p.rows[33] = -1, p.x.shape[0]
+    p.starts = ints([0, 10, 30, 66, 65])                     # the third ends past the rows, the fourth goes back
+    out, status = torch.full((65, 128), 9.0, device="cuda"), ints([0])
+    p.call(B, out=out, status=status)
+    assert status.item() == 2 and (out[30:] == 9).all() and (out[3] == 0).all()
+    keep = torch.tensor([i for i in range(30) if i != 3], device="cuda")
+    assert ((out[keep].double() - y[keep]).abs() <= 1e-4 * (1 + y[keep].abs())).all()
+    for starts in ([-1, 10, 30, 60, 65], [0, 10, 70, 60, 65]):
+        p.starts, status = ints(starts), ints([0])
+        out.fill_(9.0)
+        p.call(B, out=out, status=status)
+        assert status.item() == 2 and (out[60:].double() - y[60:]).abs().max() < 1e-3
+    p = Product([3, 4], 256, 128, gather=True, gated=True)   # 8 bits: zeros and a scale of 1
+    p.rows[5] = 1 << 30
+    codes, scales, status = torch.full((7, 128), 9, dtype=U8, device="cuda"), torch.zeros(7, 1, device="cuda"), ints([0])
+    p.call(B, codes=codes, scales=scales, status=status)
+    assert status.item() == 2 and (codes[5] == 0).all() and scales[5].item() == 1
+
+
+def test_rows_do_not_leak_into_one_another(B):
+    """NaN in one row, in rows of no group, and in another group's weights stay there."""
+    for kind, nan in ((U8, 0x7F), (BF, float("nan"))):
+        p = Product([5, 0, 40, 3], 200, 264, kind, pad=4, lead=3)
+        y, bar = p.want()
+        p.x[10, 7] = nan
+        p.x[:3], p.x[-4:] = nan, nan
+        p.w[1] = nan
+        p.w[3, 150] = nan
+        out = p.call(B, out_dtype=F32).double()
+        assert out[10].isnan().all() and out[48:51, 150].isnan().all()
+        rest = torch.ones_like(out, dtype=torch.bool)
+        rest[10], rest[:3], rest[-4:], rest[48:51, 150] = False, False, False, False
+        assert ((out - y).abs() <= 2 * bar + 1e-6)[rest].all()
+
+
+def test_results_do_not_change_from_call_to_call(B):
+    for p, dense in ((Product([64], 2112, 7168), True), (Product([7, 0, 300, 40], 512, 2048, BF, True), False)):
+        want = p.call(B, dense=dense, out_dtype=F32)
+        for _ in range(5):
+            assert torch.equal(p.call(B, dense=dense, out_dtype=F32), want)
+
+
+def test_products_in_a_graph_follow_their_inputs(B):
+    """Groups, rows and operands are read when the graph runs; two streams may run products at once."""
+    p, q = Product([3, 50, 0, 9], 256, 384, gather=True), Product([1, 0, 60, 1], 256, 384, gather=True, seed=3)
+    n = 62
+    x, xs, w, ws = (torch.empty_like(a) for a in (p.x.contiguous(), p.xs, p.w.contiguous(), p.ws))
+    starts, rows, out = torch.empty_like(p.starts), torch.empty_like(p.rows), torch.empty(n, 256, device="cuda")
+
+    def load(a):
+        for to, new in ((x, a.x), (xs, a.xs), (w, a.w), (ws, a.ws), (starts, a.starts), (rows, a.rows)):
+            to.copy_(new)
+    load(p)
+    B.grouped_matmul(x, w, starts, xs, ws, rows=rows, out=out)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        B.grouped_matmul(x, w, starts, xs, ws, rows=rows, out=out)
+    for a in (q, p, q):
+        load(a)
+        graph.replay()
+        assert torch.equal(out, a.call(B, out_dtype=F32))
+    want = [a.call(B, out_dtype=F32) for a in (p, q)]
+    streams = [torch.cuda.Stream() for _ in "pq"]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [[a.call(B, out_dtype=F32, stream=s) for a, s in zip((p, q), streams)] for _ in range(20)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, w) for pair in got for g, w in zip(pair, want))
+
+
+def test_weights_beyond_32_bits(B):
+    """The last groups of weights that are longer than 2^32 bytes in all, and outputs beyond 2^31 elements."""
+    E, N, K = 150, 4096, 7168
+    w = torch.zeros(E, N, K, dtype=U8, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    for e in (0, E - 1):
+        w[e] = (100 * torch.randn(N, K, generator=g, device="cuda")).clamp(-448, 448).to(E4M3).view(U8)
+    ws = torch.full((E, N // 128, K // 128), 1e-4, device="cuda")
+    x = (100 * torch.randn(4, K, generator=g, device="cuda")).clamp(-448, 448).to(E4M3).view(U8)
+    xs = torch.full((4, K // 128), 0.01, device="cuda")
+    out = B.grouped_matmul(x, w, ints([0, 2] + [2] * (E - 2) + [4]), xs, ws, out_dtype=F32)
+    for rows, e in ((slice(0, 2), 0), (slice(2, 4), E - 1)):
+        want = (x[rows].view(E4M3).double() @ w[e].view(E4M3).double().T) * 1e-6
+        a = (x[rows].view(E4M3).double().abs() @ w[e].view(E4M3).double().abs().T) * 1e-6
+        assert ((out[rows].double() - want).abs() <= (128 + 56 + 5) * 2.0 ** -23 * a).all()
+    del w, ws
+    M = (1 << 31) // 2048 + 5
+    x = torch.randn(M, 8, generator=g, device="cuda").to(BF)
+    w = torch.randn(2, 2048, 8, generator=g, device="cuda").to(BF)
+    out = B.grouped_matmul(x, w, ints([0, 100, M]))
+    for rows, e in ((slice(0, 100), 0), (slice(M - 300, M), 1)):
+        want = x[rows].double() @ w[e].double().T
+        assert ((out[rows].double() - want).abs() <= 2.0 ** -8 * want.abs() + 1e-4).all()
+
+
+# ------------------------------------------------------------------ router
+def plain_route(logits, k, scoring, bias, runs, top_runs, normalize, scale, real):
+    """The definition, in 64 bits, token by token on the host."""
+    T, E = logits.shape
+    l = logits.double().cpu()
+    l = torch.where(l.isnan(), -torch.inf, l).clamp(max=torch.finfo(F32).max)
+    ids, weights = [], []
+    for t in range(T):
+        if t >= real:
+            ids.append([-1] * k)
+            weights.append([0.0] * k)
+            continue
+        if scoring == "sigmoid":
+            s = torch.sigmoid(l[t])
+        else:
+            s = torch.exp(l[t] - l[t].max()) if l[t].max() > -torch.inf else torch.zeros(E, dtype=torch.float64)
+            s = s / s.sum() if s.sum() > 0 else s
+        v = l[t] if bias is None and runs == 1 else s + (0 if bias is None else bias.double().cpu())
+        v, per = v.tolist(), E // runs
+        order = lambda x, of: sorted(of, key=lambda i: (-x[i], i))  # noqa: E731
+        best = [sum(sorted(v[g * per:(g + 1) * per])[-2:]) for g in range(runs)]
+        kept = order(best, range(runs))[:top_runs]
+        chosen = order(v, [e for e in range(E) if e // per in kept])[:k]
+        w = s[chosen]
+        if normalize:
+            w = w / w.sum() if w.sum() > 0 else w * 0
+        ids.append(chosen)
+        weights.append((w * scale).tolist())
+    flat = [e for row in ids for e in row]
+    order = sorted((i for i, e in enumerate(flat) if e >= 0), key=lambda i: (flat[i], i))
+    places = [-1] * len(flat)
+    for at, i in enumerate(order):
+        places[i] = at
+    starts = [sum(0 <= x < e for x in flat) for e in range(E + 1)]
+    return ids, weights, starts, [i // k for i in order], places
+
+
+def check_route(B, logits, k, scoring="sigmoid", bias=None, runs=1, top_runs=1, normalize=True, scale=1.0, real=None):
+    T, E = logits.shape
+    ids, places = (torch.full((T, k), -9, dtype=torch.int32, device="cuda") for _ in "ip")
+    weights, starts = torch.full((T, k), -9.0, device="cuda"), torch.full((E + 1,), -9, dtype=torch.int32, device="cuda")
+    rows = torch.full((T * k,), -9, dtype=torch.int32, device="cuda")
+    B.route_experts(logits, k, ids, weights, starts, rows, places, scoring=scoring, bias=bias, num_groups=runs, top_groups=top_runs,
+                    normalize=normalize, scale=scale, num_tokens=None if real is None else ints([real]))
+    n = T if real is None else min(max(real, 0), T)
+    w = plain_route(logits, k, scoring, bias, runs, top_runs, normalize, scale, n)
+    assert ids.tolist() == w[0]
+    assert starts.tolist() == w[2] and rows.tolist() == w[3] + [-9] * ((T - n) * k) and places.flatten().tolist() == w[4]
+    want = torch.tensor(w[1], dtype=torch.float64).view(T, k)
+    l = logits.double().cpu().clamp(-1e30, 1e30)
+    l = l[l.abs() < 1e29] if scoring == "softmax" else l[:0]
+    reach = (l.max() - l.min()).item() if l.numel() else 0.0
+    got = weights.double().cpu()
+    assert ((got - want).abs() <= (2.0 ** -18 + 2.0 ** -23 * reach) * want.abs() + 1e-37).all()
+
+
+@pytest.mark.parametrize("scoring", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("T,E,k,runs,top_runs,biased,dtype", [
+    (1, 1, 1, 1, 1, False, F32), (1, 8, 8, 1, 1, False, BF), (3, 33, 2, 1, 1, True, F32), (64, 256, 8, 8, 4, True, F32),
+    (65, 256, 8, 8, 4, True, BF), (130, 60, 6, 4, 3, False, F32), (40, 128, 4, 32, 2, True, HALF), (300, 512, 16, 1, 1, True, F32),
+    (17, 64, 3, 64 // 2, 5, False, BF), (700, 160, 6, 8, 3, True, F32), (9, 7, 7, 7, 7, True, F32),
+])
+def test_route(B, T, E, k, runs, top_runs, biased, dtype, scoring):
+    torch.manual_seed(T + E)
+    logits = (1.5 * torch.randn(T, E + 3, device="cuda")).to(dtype)[:, :E]
+    bias = 0.05 * torch.randn(E, device="cuda") if biased else None
+    check_route(B, logits, k, scoring, bias, runs, top_runs, True, 2.5)
+    check_route(B, logits, k, scoring, bias, runs, top_runs, False, 1.0)
+
+
+def test_route_ties_and_near_ties(B):
+    """Equal values go to the lowest index, and values nearer than FP32 tells are ordered as in 64 bits."""
+    torch.manual_seed(5)
+    coarse = torch.randint(-2, 3, (200, 64), device="cuda").float()
+    for scoring in ("sigmoid", "softmax"):
+        check_route(B, coarse, 6, scoring)
+        check_route(B, coarse, 6, scoring, torch.zeros(64, device="cuda"), 8, 3)
+        check_route(B, coarse, 6, scoring, 0.25 * torch.randint(0, 3, (64,), device="cuda").float(), 4, 2)
+    check_route(B, coarse * 0, 8)
+    check_route(B, -coarse * 0, 8)                                       # zeros of both signs
+    check_route(B, coarse * torch.where(coarse == 0, -1.0, 1.0), 8, "softmax")
+    # steps of one unit in the last place; sigmoids that FP32 rounds to 1
+    near = torch.nextafter(torch.ones(100, 96, device="cuda"), torch.full((100, 96), 2.0, device="cuda"))
+    near = torch.where(torch.rand(100, 96, device="cuda") < 0.5, near, 1.0)
+    for scoring in ("sigmoid", "softmax"):
+        check_route(B, near, 5, scoring, torch.zeros(96, device="cuda"), 6, 2)
+    check_route(B, 17 + 3 * torch.randn(100, 64, device="cuda"), 8, "sigmoid", torch.zeros(64, device="cuda"), 8, 4)
+    check_route(B, 0.01 * torch.randn(500, 256, device="cuda").bfloat16(), 8, "softmax", torch.zeros(256, device="cuda"), 8, 4)
+
+
+def test_route_ends_of_the_range(B):
+    torch.manual_seed(6)
+    inf, nan = float("inf"), float("nan")
+    l = torch.randn(12, 40, device="cuda")
+    l[0], l[1], l[2, 3:], l[3, ::2] = -inf, -200.0 + l[1], -inf, nan
+    l[4, 7], l[5, 7], l[6], l[7] = inf, 1000.0, 500 * l[6], -100 + 10 * l[7]
+    for scoring in ("sigmoid", "softmax"):
+        for bias in (None, 0.1 * torch.randn(40, device="cuda")):
+            for runs, top in ((1, 1), (5, 2)):
+                check_route(B, l, 5, scoring, bias, runs, top)
+    bias = 1e4 * torch.randn(40, device="cuda")
+    check_route(B, l[8:], 5, "sigmoid", bias, 5, 2)
+
+
+@pytest.mark.parametrize("T,real", [(70, 64), (5, 0), (8, -3), (9, 20), (2500, 1999)])
+def test_route_of_a_padded_batch(B, T, real):
+    torch.manual_seed(T)
+    check_route(B, torch.randn(T, 96, device="cuda"), 4, "sigmoid", 0.1 * torch.randn(96, device="cuda"), 8, 4, real=real)
+
+
+def test_route_of_many_tokens(B):
+    torch.manual_seed(1)
+    T, E, k = 20000, 256, 8
+    logits, bias = torch.randn(T, E, device="cuda"), 0.05 * torch.randn(E, device="cuda")
+    ids, places = (torch.empty(T, k, dtype=torch.int32, device="cuda") for _ in "ip")
+    weights, starts, rows = torch.empty(T, k, device="cuda"), torch.empty(E + 1, dtype=torch.int32, device="cuda"), \
+        torch.empty(T * k, dtype=torch.int32, device="cuda")
+    B.route_experts(logits, k, ids, weights, starts, rows, places, bias=bias)
+    v = torch.sigmoid(logits.double()) + bias.double()
+    want = v.sort(dim=1, descending=True, stable=True).indices[:, :k]
+    assert torch.equal(ids.long(), want)
+    flat = want.flatten()
+    order = flat.argsort(stable=True)
+    assert torch.equal(rows.long(), order // k) and torch.equal(places.flatten().long()[order], torch.arange(T * k, device="cuda"))
+    assert torch.equal(starts.long(), torch.searchsorted(flat[order], torch.arange(E + 1, device="cuda")))
+
+
+def test_route_of_nothing(B):
+    starts = torch.full((9,), 5, dtype=torch.int32, device="cuda")
+    none = torch.empty(0, 2, dtype=torch.int32, device="cuda")
+    B.route_experts(torch.empty(0, 8, device="cuda"), 2, none, torch.empty(0, 2, device="cuda"), starts, none.flatten(), none)
+    assert (starts == 0).all()
+
+
+# ------------------------------------------------------------------ sum
+@pytest.mark.parametrize("T,k,N,dtype,add,step", [
+    (1, 1, 1, F32, False, 0), (1, 8, 7168, BF, True, 0), (64, 8, 7168, BF, True, 8), (5, 3, 17, HALF, True, 3), (33, 16, 1032, F32, False, 4),
+    (200, 2, 2056, HALF, False, 8), (7, 6, 129, BF, True, 0), (1000, 4, 512, BF, True, 16),
+])
+def test_combine(B, T, k, N, dtype, add, step):
+    torch.manual_seed(T + N)
+    M = T * k
+    y = torch.randn(M, N + step, device="cuda").to(dtype)[:, :N]
+    shared = torch.randn(T, N + 2 * step, device="cuda").to(dtype)[:, :N] if add else None
+    places = torch.randperm(M, device="cuda").view(T, k).int()
+    weights = torch.rand(T, k, device="cuda")
+    if T > 4:
+        places[1, 0], places[2], places[3, k - 1] = -1, -1, M            # none, a padded row, past the rows
+    ok = (places >= 0) & (places < M)
+    rows = torch.where(ok[..., None], y.double()[places.clamp(0, M - 1).long()], 0.0)
+    want = (rows * weights[..., None].double()).sum(1) + (0 if shared is None else shared.double())
+    size = (rows * weights[..., None].double()).abs().sum(1) + (0 if shared is None else shared.double().abs())
+    status = ints([0])
+    out = torch.full((T, N + step), 5.0, dtype=dtype, device="cuda")[:, :N]
+    assert B.combine_experts(y, places, weights, add=shared, out=out, status=status) is out
+    assert status.item() == (2 if T > 4 else 0)
+    bar = (k + 2) * 2.0 ** -24 * size
+    lim = bar + torch.finfo(dtype).eps / 2 * (want.abs() + bar) + (2.0 ** -25 if dtype is HALF else 0.0)
+    assert ((out.double() - want).abs() <= lim).all()
+    if add:                                                              # in place of the shared rows
+        assert torch.equal(B.combine_experts(y, places, weights, add=shared, out=shared), out)
+    assert torch.equal(B.combine_experts(y, places, weights), B.combine_experts(y, places, weights, add=torch.zeros_like(out)))
+
+
+# ------------------------------------------------------------------ together
+@pytest.mark.parametrize("T,real", [(1, 1), (40, 33), (300, 300)])
+def test_a_layers_experts(B, T, real):
+    """Norm, router, both expert products beside a shared expert's, and the sum, as a layer runs them, in a graph of a
+    padded batch: against 64 bits from the 8-bit rows on."""
+    torch.manual_seed(T)
+    E, k, width, inner = 16, 4, 512, 256
+
+    def weight(*shape):
+        w = torch.randn(*shape, device="cuda")
+        s = 0.9 + 0.2 * torch.rand(*shape[:-2], ceil(shape[-2]), ceil(shape[-1]), device="cuda")
+        return (100 * w).clamp(-448, 448).to(E4M3).view(U8), s * shape[-1] ** -0.5 / 100
+    w1, s1 = weight(E + 1, 2 * inner, width)                              # (the last is the shared expert)
+    w2, s2 = weight(E + 1, width, inner)
+    router, bias = torch.randn(E, width, device="cuda") * width ** -0.5, 0.1 * torch.randn(E, device="cuda")
+    x, norm = torch.randn(T, width, device="cuda").to(BF), torch.ones(width, dtype=BF, device="cuda")
+    num = ints([real])
+    y = torch.empty_like(x)
+    codes, scales = torch.empty(T, width, dtype=U8, device="cuda"), torch.empty(T, width // 128, device="cuda")
+    ids, places = (torch.empty(T, k, dtype=torch.int32, device="cuda") for _ in "ip")
+    weights, starts, rows = torch.empty(T, k, device="cuda"), torch.empty(E + 1, dtype=torch.int32, device="cuda"), \
+        torch.zeros(T * k, dtype=torch.int32, device="cuda")
+    hc, hs = torch.empty(T * k, inner, dtype=U8, device="cuda"), torch.empty(T * k, inner // 128, device="cuda")
+    sc, ss = torch.empty(T, inner, dtype=U8, device="cuda"), torch.empty(T, inner // 128, device="cuda")
+    e_out, shared, out = torch.empty(T * k, width, dtype=BF, device="cuda"), torch.empty_like(x), torch.empty_like(x)
+    status = ints([0])
+
+    def layer():
+        B.add_rms_norm(x, None, norm, 1e-6, out=y, codes=codes, scales=scales)
+        logits = y.float() @ router.T
+        B.route_experts(logits, k, ids, weights, starts, rows, places, bias=bias, num_groups=4, top_groups=2, num_tokens=num)
+        B.grouped_matmul(codes, w1[:E], starts, scales, s1[:E], rows=rows, gated=True, out_codes=hc, out_scales=hs, status=status)
+        B.grouped_matmul(hc, w2[:E], starts, hs, s2[:E], out=e_out, status=status)
+        B.fp8_matmul(codes, scales, w1[E], s1[E], gated=True, out_codes=sc, out_scales=ss, status=status)
+        B.fp8_matmul(sc, ss, w2[E], s2[E], out=shared, status=status)
+        B.combine_experts(e_out, places, weights, add=shared, out=out, status=status)
+
+    layer()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        layer()
+    x.copy_(torch.randn(T, width, device="cuda"))
+    graph.replay()
+    assert status.item() == 0 and starts[-1].item() == real * k
+
+    def mat(c, s):
+        return c.view(E4M3).double() * wide(s, c.shape[-1]).repeat_interleave(128, -2)[..., : c.shape[-2], :]
+    a = codes.view(E4M3).double() * wide(scales, width)
+    v1, v2 = mat(w1, s1), mat(w2, s2)
+
+    def expert(e, r):
+        g, u = (r @ v1[e].T).chunk(2, -1)
+        return g * torch.sigmoid(g) * u
+    want, size = torch.zeros(T, width, dtype=torch.float64, device="cuda"), torch.zeros(T, 1, dtype=torch.float64, device="cuda")
+    for t in range(real):
+        for j in range(k):
+            h = expert(ids[t, j], a[t])
+            want[t] += weights[t, j].double() * (h @ v2[ids[t, j]].T)
+            size[t] += weights[t, j].double() * h.norm()
+    h = expert(E, a)
+    want, size = want + h @ v2[E].T, size + h.norm(dim=1, keepdim=True)
+    # each hidden element is off by 2^-4 of itself at most, and the second product's columns have a length of about 1
+    assert ((out.double() - want).abs() <= 2.0 ** -4 * 1.5 * size + 2.0 ** -7 * want.abs()).all()
+    assert ((out.double() - want).norm() <= 0.04 * want.norm())
