@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "combine.cuh"
 #include "dsa_indexer.h"
@@ -17,6 +18,72 @@ namespace {
 using namespace dsa_host;
 
 bool is_float(int type) { return type == DSA_TYPE_BF16 || type == DSA_TYPE_FP16 || type == DSA_TYPE_FP32; }
+
+// The tensor maps of rows and weights.  Rows come in boxes of `box` rows, or one by one where they are gathered; weights in
+// boxes of `w_box` rows; 128 bytes of K at a time.
+int product_maps(const dsa::MatmulParams& p, int box, int w_box, CUtensorMap* tx, CUtensorMap* tw) {
+  const int size = element_bytes(p.x_type);
+  const CUtensorMapDataType type = size == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                   : p.x_type == DSA_TYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  const int64_t xd[2] = {p.K, p.x_rows}, xs[1] = {p.x_stride * size};
+  const int xb[2] = {128 / size, p.rows ? 1 : box};
+  if (const int rc = make_map(tx, "x", type, size, p.x, 2, xd, xs, xb, true)) return rc;
+  const int64_t wd[3] = {p.K, p.N, p.E}, ws[2] = {p.w_stride * size, p.w_group * size};
+  const int wb[3] = {128 / size, w_box, 1};
+  return make_map(tw, "weight", type, size, p.w, 3, wd, ws, wb, true);
+}
+
+// Clusters of `size` CTAs of a kernel that the current device runs at once, asked for once a device.
+class ClusterCount {
+ public:
+  int get(const void* kernel, int size, int threads, int smem) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    std::atomic<int>* known = dev >= 0 && dev < 64 ? &known_[dev][size] : nullptr;
+    if (known && known->load(std::memory_order_relaxed)) return known->load(std::memory_order_relaxed);
+    cudaLaunchConfig_t c{};
+    cudaLaunchAttribute a[1];
+    a[0].id = cudaLaunchAttributeClusterDimension;
+    a[0].val.clusterDim.x = size, a[0].val.clusterDim.y = 1, a[0].val.clusterDim.z = 1;
+    c.gridDim = dim3(size), c.blockDim = dim3(threads), c.dynamicSmemBytes = smem, c.attrs = a, c.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &c) != cudaSuccess) return 0;
+    if (known) known->store(n, std::memory_order_relaxed);
+    return n;
+  }
+
+ private:
+  std::atomic<int> known_[64][9] = {};
+};
+
+template <bool FP8, bool GATED, int BM>
+int launch_few(const dsa::MatmulParams& p, int64_t groups, cudaStream_t st) {
+  using C = dsa::FewCfg<FP8, GATED, BM>;
+  const auto kernel = dsa::few_rows_kernel<FP8, GATED, BM>;
+  static PerDevice allowed;
+  static ClusterCount resident;
+  if (const int rc = allow_smem(allowed, (const void*)kernel, C::kSmem)) return rc;
+  CUtensorMap tx, tw;
+  if (const int rc = product_maps(p, 32, C::kBox, &tx, &tw)) return rc;
+  const int64_t columns = (p.width + C::kOut - 1) / C::kOut;
+  const int64_t most = std::min<int64_t>(groups, p.M);  // groups with rows
+  const int64_t tiles = (most + (p.M - most) / BM) * columns;
+  const int blocks = (p.K + C::kK - 1) / C::kK;
+  int size = 8;
+  while (size > 1 && (tiles * size > sm_count() || size * 2 > blocks)) size /= 2;
+  const int clusters = resident.get((const void*)kernel, size, dsa::kMatmulThreads, C::kSmem);
+  if (clusters < 1) return fail(DSA_ERR_CUDA, "no cluster of %d CTAs fits the device", size);
+  cudaLaunchConfig_t c{};
+  cudaLaunchAttribute a[1];
+  a[0].id = cudaLaunchAttributeClusterDimension;
+  a[0].val.clusterDim.x = size, a[0].val.clusterDim.y = 1, a[0].val.clusterDim.z = 1;
+  c.gridDim = dim3((unsigned)(std::min<int64_t>(tiles, clusters) * size)), c.blockDim = dim3(dsa::kMatmulThreads);
+  c.dynamicSmemBytes = C::kSmem, c.stream = st, c.attrs = a, c.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&c, kernel, tx, tw, p);
+  if (e != cudaSuccess) return fail(DSA_ERR_CUDA, "few_rows_kernel: %s", cudaGetErrorString(e));
+  set_last_launches(1);
+  return check_launch("few_rows_kernel");
+}
 
 // The checks that both products share, and their launch.  p has the sizes, strides and pointers.
 int run_matmul(dsa::MatmulParams p, int64_t groups, cudaStream_t st) {
@@ -45,10 +112,15 @@ int run_matmul(dsa::MatmulParams p, int64_t groups, cudaStream_t st) {
   p.kb = (p.K + dsa::kMatmulBlock - 1) / dsa::kMatmulBlock;
   p.nb = (p.N + dsa::kMatmulBlock - 1) / dsa::kMatmulBlock;
   if (!fp8) p.x_scales = p.w_scales = nullptr;
-  const dim3 grid((unsigned)((p.M + dsa::kSimpleRows - 1) / dsa::kSimpleRows + (p.starts ? p.E : 0)), (p.width + 127) / 128);
-  dsa::matmul_kernel<<<grid, 128, 0, st>>>(p);
-  set_last_launches(1);
-  return check_launch("matmul_kernel");
+  p.give_up = env_int("DSA_WAIT_LIMIT", (int)dsa::kWaitLimit, 0, (int)dsa::kWaitLimit) == 0;
+  if (sm_count() <= 0) return fail(DSA_ERR_CUDA, "no CUDA device");
+  const bool few = p.M <= 64 * groups;
+  if (fp8) {
+    if (p.gated) return few ? launch_few<true, true, 64>(p, groups, st) : launch_few<true, true, 128>(p, groups, st);
+    return few ? launch_few<true, false, 64>(p, groups, st) : launch_few<true, false, 128>(p, groups, st);
+  }
+  if (p.gated) return few ? launch_few<false, true, 64>(p, groups, st) : launch_few<false, true, 128>(p, groups, st);
+  return few ? launch_few<false, false, 64>(p, groups, st) : launch_few<false, false, 128>(p, groups, st);
 }
 
 template <int V>
