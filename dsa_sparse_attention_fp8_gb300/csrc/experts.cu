@@ -56,8 +56,23 @@ class ClusterCount {
   std::atomic<int> known_[64][9] = {};
 };
 
+template <typename Kernel>
+int launch_clusters(const char* name, Kernel kernel, int clusters, int size, int smem, cudaStream_t st, const CUtensorMap& tx,
+                    const CUtensorMap& tw, const dsa::MatmulParams& p) {
+  cudaLaunchConfig_t c{};
+  cudaLaunchAttribute a[1];
+  a[0].id = cudaLaunchAttributeClusterDimension;
+  a[0].val.clusterDim.x = size, a[0].val.clusterDim.y = 1, a[0].val.clusterDim.z = 1;
+  c.gridDim = dim3((unsigned)(clusters * size)), c.blockDim = dim3(dsa::kMatmulThreads);
+  c.dynamicSmemBytes = smem, c.stream = st, c.attrs = a, c.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&c, kernel, tx, tw, p);
+  if (e != cudaSuccess) return fail(DSA_ERR_CUDA, "%s: %s", name, cudaGetErrorString(e));
+  set_last_launches(1);
+  return check_launch(name);
+}
+
 template <bool FP8, bool GATED, int BM>
-int launch_few(const dsa::MatmulParams& p, int64_t groups, cudaStream_t st) {
+int launch_few(dsa::MatmulParams p, int64_t groups, cudaStream_t st) {
   using C = dsa::FewCfg<FP8, GATED, BM>;
   const auto kernel = dsa::few_rows_kernel<FP8, GATED, BM>;
   static PerDevice allowed;
@@ -67,22 +82,32 @@ int launch_few(const dsa::MatmulParams& p, int64_t groups, cudaStream_t st) {
   if (const int rc = product_maps(p, 32, C::kBox, &tx, &tw)) return rc;
   const int64_t columns = (p.width + C::kOut - 1) / C::kOut;
   const int64_t most = std::min<int64_t>(groups, p.M);  // groups with rows
-  const int64_t tiles = (most + (p.M - most) / BM) * columns;
+  const int64_t tiles = (p.most_tiles = (int)(most + (p.M - most) / BM)) * columns;
   const int blocks = (p.K + C::kK - 1) / C::kK;
   int size = 8;
   while (size > 1 && (tiles * size > sm_count() || size * 2 > blocks)) size /= 2;
+  if (tiles > INT32_MAX / 2) return fail(DSA_ERR_UNSUPPORTED, "%lld tiles of results", (long long)tiles);
   const int clusters = resident.get((const void*)kernel, size, dsa::kMatmulThreads, C::kSmem);
   if (clusters < 1) return fail(DSA_ERR_CUDA, "no cluster of %d CTAs fits the device", size);
-  cudaLaunchConfig_t c{};
-  cudaLaunchAttribute a[1];
-  a[0].id = cudaLaunchAttributeClusterDimension;
-  a[0].val.clusterDim.x = size, a[0].val.clusterDim.y = 1, a[0].val.clusterDim.z = 1;
-  c.gridDim = dim3((unsigned)(std::min<int64_t>(tiles, clusters) * size)), c.blockDim = dim3(dsa::kMatmulThreads);
-  c.dynamicSmemBytes = C::kSmem, c.stream = st, c.attrs = a, c.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&c, kernel, tx, tw, p);
-  if (e != cudaSuccess) return fail(DSA_ERR_CUDA, "few_rows_kernel: %s", cudaGetErrorString(e));
-  set_last_launches(1);
-  return check_launch("few_rows_kernel");
+  return launch_clusters("few_rows_kernel", kernel, (int)std::min<int64_t>(tiles, clusters), size, C::kSmem, st, tx, tw, p);
+}
+
+template <bool FP8, bool GATED>
+int launch_many(dsa::MatmulParams p, int64_t groups, cudaStream_t st) {
+  using C = dsa::ManyCfg<FP8, GATED>;
+  const auto kernel = dsa::many_rows_kernel<FP8, GATED>;
+  static PerDevice allowed;
+  static ClusterCount resident;
+  if (const int rc = allow_smem(allowed, (const void*)kernel, C::kSmem)) return rc;
+  CUtensorMap tx, tw;
+  if (const int rc = product_maps(p, 32, C::kBox, &tx, &tw)) return rc;
+  const int64_t columns = (p.width + C::kOut - 1) / C::kOut;
+  const int64_t most = std::min<int64_t>(groups, p.M);  // groups with rows
+  const int64_t tiles = (p.most_tiles = (int)(most + (p.M - most) / C::BM)) * columns;
+  if (tiles > INT32_MAX / 2) return fail(DSA_ERR_UNSUPPORTED, "%lld tiles of results", (long long)tiles);
+  const int clusters = resident.get((const void*)kernel, 2, dsa::kMatmulThreads, C::kSmem);
+  if (clusters < 1) return fail(DSA_ERR_CUDA, "no pair of CTAs fits the device");
+  return launch_clusters("many_rows_kernel", kernel, (int)std::min<int64_t>(tiles, clusters), 2, C::kSmem, st, tx, tw, p);
 }
 
 // The checks that both products share, and their launch.  p has the sizes, strides and pointers.
@@ -114,13 +139,13 @@ int run_matmul(dsa::MatmulParams p, int64_t groups, cudaStream_t st) {
   if (!fp8) p.x_scales = p.w_scales = nullptr;
   p.give_up = env_int("DSA_WAIT_LIMIT", (int)dsa::kWaitLimit, 0, (int)dsa::kWaitLimit) == 0;
   if (sm_count() <= 0) return fail(DSA_ERR_CUDA, "no CUDA device");
-  const bool few = p.M <= 64 * groups;
+  bool few = p.M <= 64 * groups, some = p.M <= 128 * groups;
   if (fp8) {
-    if (p.gated) return few ? launch_few<true, true, 64>(p, groups, st) : launch_few<true, true, 128>(p, groups, st);
-    return few ? launch_few<true, false, 64>(p, groups, st) : launch_few<true, false, 128>(p, groups, st);
+    if (p.gated) return few ? launch_few<true, true, 64>(p, groups, st) : some ? launch_few<true, true, 128>(p, groups, st) : launch_many<true, true>(p, groups, st);
+    return few ? launch_few<true, false, 64>(p, groups, st) : some ? launch_few<true, false, 128>(p, groups, st) : launch_many<true, false>(p, groups, st);
   }
-  if (p.gated) return few ? launch_few<false, true, 64>(p, groups, st) : launch_few<false, true, 128>(p, groups, st);
-  return few ? launch_few<false, false, 64>(p, groups, st) : launch_few<false, false, 128>(p, groups, st);
+  if (p.gated) return few ? launch_few<false, true, 64>(p, groups, st) : some ? launch_few<false, true, 128>(p, groups, st) : launch_many<false, true>(p, groups, st);
+  return few ? launch_few<false, false, 64>(p, groups, st) : some ? launch_few<false, false, 128>(p, groups, st) : launch_many<false, false>(p, groups, st);
 }
 
 template <int V>

@@ -36,7 +36,7 @@ struct MatmulParams {
   int32_t* status;
   int64_t x_stride, w_stride, w_group, out_stride;  // elements
   int x_rows, M, N, K, E, width, kb, nb;            // width: N, or N / 2 where gated
-  int x_type, out_type;
+  int x_type, out_type, most_tiles;                 // row tiles that there can be
   bool gated, give_up;
 };
 
@@ -68,58 +68,69 @@ __device__ __forceinline__ void load_groups(const MatmulParams& p, const Groups&
     g.end[e] = n;
   }
 }
-// One warp.
+// One warp.  Groups that overlap may have more rows than there are: tiles past `most` are dropped.
 template <int BM>
-__device__ __forceinline__ void count_tiles(int E, const Groups& g) {
+__device__ __forceinline__ void count_tiles(int E, int most, const Groups& g) {
   const int lane = threadIdx.x & 31;
-  int sum = 0;
+  int64_t sum = 0;
   for (int at = 0; at < E; at += 32) {
     const int e = at + lane;
     const int c = e < E ? (int)(((int64_t)g.end[e] - g.begin[e] + BM - 1) / BM) : 0;
-    int up = c;
+    int64_t up = c;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, up, o);
+      const int64_t v = __shfl_up_sync(0xffffffffu, up, o);
       if (lane >= o) up += v;
     }
-    if (e < E) g.first[e] = sum + up - c;
+    if (e < E) g.first[e] = (int)min((int64_t)most, sum + up - c);
     sum += __shfl_sync(0xffffffffu, up, 31);
   }
-  if (lane == 0) g.first[E] = sum;
+  if (lane == 0) g.first[E] = (int)min((int64_t)most, sum);
 }
 
-// Walks the tiles of one CTA or cluster: t, t + step, ...
+// The t-th tile, in kOut columns of the result and BM rows; false past the last.
 template <int BM, int OUT>
-struct Walk {
-  Groups g;
-  int64_t t, step, total;
-  int E, e = 0, columns;
-  __device__ Walk(const MatmulParams& p, const Groups& groups, int64_t from, int64_t by)
-      : g(groups), t(from), step(by), E(p.E), columns((p.width + OUT - 1) / OUT) {
-    total = (int64_t)g.first[E] * columns;
+__device__ __forceinline__ bool find_tile(const MatmulParams& p, const Groups& g, int t, Tile* tile) {
+  const int columns = (p.width + OUT - 1) / OUT;
+  if (t >= g.first[p.E] * columns) return false;
+  int e = 0, hi = p.E - 1;
+  while (e < hi) {
+    const int mid = (e + hi + 1) >> 1;
+    if (g.first[mid] * columns <= t) e = mid; else hi = mid - 1;
   }
-  __device__ bool next(Tile* tile) {
-    if (t >= total) return false;
-    if ((int64_t)g.first[e + 1] * columns <= t) {
-      int lo = e + 1, hi = E - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if ((int64_t)g.first[mid] * columns <= t) lo = mid; else hi = mid - 1;
-      }
-      e = lo;
-    }
-    const int tiles = g.first[e + 1] - g.first[e];
-    const int64_t j = t - (int64_t)g.first[e] * columns;
-    const int column = tiles == 1 ? (int)j : (int)(j / tiles);
-    const int m = (int)(j - (int64_t)column * tiles);
-    tile->e = e;
-    tile->row = g.begin[e] + m * BM;
-    tile->count = min(BM, g.end[e] - tile->row);
-    tile->column = column * OUT;
-    t += step;
-    return true;
+  const int tiles = g.first[e + 1] - g.first[e], j = t - g.first[e] * columns;
+  const int column = j / tiles;
+  tile->e = e;
+  tile->row = g.begin[e] + (j - column * tiles) * BM;
+  tile->count = min(BM, g.end[e] - tile->row);
+  tile->column = column * OUT;
+  return true;
+}
+
+// Adds a block's accumulator, COLS columns of this warp's lanes, to acc: the first half times f, the rest times u.
+template <int COLS>
+__device__ __forceinline__ void add_block(uint32_t from, uint64_t (&acc)[COLS / 2], float f, float u) {
+#pragma unroll
+  for (int c = 0; c < COLS / 64; ++c) {
+    uint32_t d[64];
+    tmem_ld<64>(from + 64 * c, d);
+    tmem_ld_wait();
+    const uint64_t f0 = COLS == 64 || c == 0 ? pack2(f, f) : pack2(u, u);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) fma2_here(acc[32 * c + i], d[2 * i], d[2 * i + 1], f0);
   }
-};
+}
+template <int COLS>
+__device__ __forceinline__ void take_block(uint32_t from, uint64_t (&acc)[COLS / 2]) {
+#pragma unroll
+  for (int c = 0; c < COLS / 32; ++c) {
+    uint32_t d[32];
+    tmem_ld<32>(from + 32 * c, d);
+    tmem_ld_wait32(d);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[16 * c + i] = pack2(__uint_as_float(d[2 * i]), __uint_as_float(d[2 * i + 1]));
+  }
+}
 
 // ---------------------------------------------------------------- results
 __device__ __forceinline__ float gate(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
@@ -131,6 +142,12 @@ __device__ __forceinline__ uint32_t round_pair(float a, float b, bool bf16) {
   }
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ void store_element(void* p, int64_t at, int type, float v) {
+  if (type == 0) static_cast<__nv_bfloat16*>(p)[at] = __float2bfloat16_rn(v);
+  else if (type == 1) static_cast<__half*>(p)[at] = __float2half_rn(v);
+  else static_cast<float*>(p)[at] = v;
 }
 
 // Four neighbouring results of a row to out.
@@ -148,9 +165,7 @@ __device__ __forceinline__ void store4(const MatmulParams& p, int64_t row, int n
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     if (n + i >= p.width) break;
-    if (p.out_type == 2) static_cast<float*>(p.out)[at + i] = y[i];
-    else if (p.out_type == 0) static_cast<__nv_bfloat16*>(p.out)[at + i] = __float2bfloat16_rn(y[i]);
-    else static_cast<__half*>(p.out)[at + i] = __float2half_rn(y[i]);
+    store_element(p.out, at + i, p.out_type, y[i]);
   }
 }
 
@@ -195,7 +210,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
   const auto acc_empty = [&](int b) { return bars + 160 + 8 * b; };
   const uint32_t join_full = bars + 192, join_free = bars + 200;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t S = cluster_size(), rank = cluster_rank();
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) mbar_init(full(s), 1), mbar_init(empty(s), 1);
@@ -213,7 +228,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
     tmem_relinquish();
   }
   __syncthreads();
-  if (warp == 8) count_tiles<BM>(p.E, groups);
+  if (warp == 8) count_tiles<BM>(p.E, p.most_tiles, groups);
   tc_fence_before();
   if (S > 1) cluster_sync(); else __syncthreads();
   tc_fence_after();
@@ -226,7 +241,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
   // this CTA's part of K, in stages
   const int blocks = (p.K + C::kK - 1) / C::kK;
   const int k0 = (int)((int64_t)blocks * rank / S), k1 = (int)((int64_t)blocks * (rank + 1) / S);
-  Walk<BM, C::kOut> walk(p, groups, blockIdx.x / S, gridDim.x / S);
+  const int step = gridDim.x / S;
   Tile tile;
 
   if (warp < 8) {
@@ -238,7 +253,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
     const bool vec_codes = p.codes && (reinterpret_cast<uintptr_t>(p.codes) | (uintptr_t)p.width) % 4 == 0;
     int buffer = 0, turn = 0, joined = 0;
     bool on = true;
-    while (on && walk.next(&tile)) {
+    for (int t = blockIdx.x / S; on && find_tile<BM, C::kOut>(p, groups, t, &tile); t += step) {
       const int row = q * 32 + lane;
       const bool busy = q * 32 < tile.count;  // the warp has rows
       int src = 0;
@@ -257,66 +272,27 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
         const int n0 = GATED ? tile.column + 64 * half : tile.column;
         const float* const ws = p.w_scales + ((int64_t)tile.e * p.nb + n0 / kMatmulBlock) * p.kb;
         const float* const wu = p.w_scales + ((int64_t)tile.e * p.nb + min(p.nb - 1, (p.width + n0) / kMatmulBlock)) * p.kb;
-        // the scales of four blocks are loaded while the four before are summed
-        float s_next[4], g_next[4], u_next[4];
-        const auto ahead = [&](int k) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int at = min(k + j, k1 - 1);
-            s_next[j] = __ldg(xs + at);
-            g_next[j] = __ldg(ws + at);
-            u_next[j] = GATED ? __ldg(wu + at) : 0.f;
-          }
-        };
-        ahead(k0);
-        for (int k = k0; k < k1 && on; k += 4) {
-          float gs[4], us[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) gs[j] = s_next[j] * g_next[j], us[j] = s_next[j] * u_next[j];
-          if (k + 4 < k1) ahead(k + 4);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (k + j >= k1) break;
-            on = __all_sync(~0u, mbar_wait(acc_full(buffer), turn, abort_flag));
-            if (!on) break;
-            tc_fence_after();
-            if (busy) {
-              uint32_t d[2][32];
-              const uint32_t from = lanes + buffer * C::BN;
-              tmem_ld<32>(from, d[0]);
-              tmem_ld_wait32(d[0]);
-#pragma unroll
-              for (int c = 0; c < C::kHalf / 32; ++c) {
-                if (c + 1 < C::kHalf / 32) tmem_ld<32>(from + 32 * (c + 1), d[(c + 1) & 1]);
-                const float f = GATED && c >= 2 ? us[j] : gs[j];
-                const uint64_t f2 = pack2(f, f);
-                const uint32_t* v = d[c & 1];
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                  acc[16 * c + i] = fma2(pack2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), f2, acc[16 * c + i]);
-                if (c + 1 < C::kHalf / 32) tmem_ld_wait32(d[(c + 1) & 1]);
-              }
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(acc_empty(buffer));
-            if (++buffer == C::kBuffers) buffer = 0, turn ^= 1;
-          }
+        // (a block's scales are loaded while the block before is summed)
+        float s_next = ld_ahead(xs + k0), g_next = ld_ahead(ws + k0), u_next = GATED ? ld_ahead(wu + k0) : 0.f;
+        for (int k = k0; k < k1; ++k) {
+          const float f = s_next * g_next, u = GATED ? s_next * u_next : f;
+          const int at = min(k + 1, k1 - 1);
+          s_next = ld_ahead(xs + at), g_next = ld_ahead(ws + at);
+          if (GATED) u_next = ld_ahead(wu + at);
+          on = __all_sync(~0u, mbar_wait(acc_full(buffer), turn, abort_flag));
+          if (!on) break;
+          tc_fence_after();
+          if (busy) add_block<C::kHalf>(lanes + buffer * C::BN, acc, f, u);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(acc_empty(buffer));
+          if (++buffer == C::kBuffers) buffer = 0, turn ^= 1;
         }
       } else {
         on = __all_sync(~0u, mbar_wait(acc_full(buffer), turn, abort_flag));
         if (on) {
           tc_fence_after();
-          if (busy) {
-#pragma unroll
-            for (int c = 0; c < C::kHalf / 32; ++c) {
-              uint32_t d[32];
-              tmem_ld<32>(lanes + buffer * C::BN + 32 * c, d);
-              tmem_ld_wait32(d);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) acc[16 * c + i] = pack2(__uint_as_float(d[2 * i]), __uint_as_float(d[2 * i + 1]));
-            }
-          }
+          if (busy) take_block<C::kHalf>(lanes + buffer * C::BN, acc);
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(acc_empty(buffer));
@@ -398,7 +374,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
       uint32_t used = 0;  // stages that were ever filled
       bool on = !p.give_up;
       if (!on) quit();
-      while (on && walk.next(&tile)) {
+      for (int t = blockIdx.x / S; on && find_tile<BM, C::kOut>(p, groups, t, &tile); t += step) {
         int4 from = make_int4(0, 0, 0, 0);
         const int boxes = p.rows ? (tile.count + 3) / 4 : (tile.count + 31) / 32;
         if (p.rows) {
@@ -447,7 +423,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
         const uint32_t idesc = FP8 ? idesc_e4m3_f32(128, C::BN) : idesc_16_f32(p.x_type == 0, 128, C::BN, false);
         int s = 0, phase = 0, buffer = 0, turn = 0;
         bool on = true;
-        while (on && walk.next(&tile)) {
+        for (int t = blockIdx.x / S; on && find_tile<BM, C::kOut>(p, groups, t, &tile); t += step) {
           for (int k = k0; k < k1; ++k) {
             if (FP8 || k == k0) on = mbar_wait(acc_empty(buffer), turn ^ 1, abort_flag);
             on = on && mbar_wait(full(s), phase, abort_flag);
@@ -479,6 +455,339 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
   if (S > 1) cluster_sync(); else __syncthreads();
   tc_fence_after();
   if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+// ---------------------------------------------------------------- many rows to a group
+// Tiles of 256 rows and 256 weight rows, each shared by a pair of CTAs (cta_group::2): a CTA loads half of the rows and half
+// of the weights, and has half of the rows' sums.
+template <bool FP8, bool GATED>
+struct ManyCfg {
+  static constexpr int BM = 256, BN = 256, kOut = GATED ? 128 : 256;
+  static constexpr int kBox = GATED ? 64 : 128;  // weight rows of a load
+  static constexpr int kK = FP8 ? 128 : 64;      // elements of K in a stage: 128 bytes
+  static constexpr int kStageA = 128 * 128, kStageB = 128 * 128, kStage = kStageA + kStageB;
+  static constexpr int kRow = 80;                // bytes of a row's staged piece, 64, its largest value, and room against bank conflicts
+  static constexpr int kPieces = 8 * 32 * kRow;
+  static constexpr int kTable = (3 * kMatmulMaxGroups + 4) * 4;
+  static constexpr int kRest = kPieces + kTable + 512 + 1024;  // barriers, alignment
+  static constexpr int kStages = (232448 - kRest) / kStage;
+  static constexpr int kSmem = kRest + kStages * kStage;
+  static_assert(kStages >= 6 && kStages <= 8);
+};
+
+// 64 bytes of each of a warp's 32 rows, a row to a lane, out by way of shared memory so that four lanes write a row's
+// piece: `rows` rows at `to`, `stride` bytes apart, of which the first `bytes` are wanted.  16-byte aligned.
+__device__ __forceinline__ void store_piece(uint32_t stage, uint8_t* to, int64_t stride, int rows, int bytes, const uint32_t* v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) sts_v4(stage + lane * 80 + 16 * i, make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+  __syncwarp();
+  const int at = (lane & 3) * 16;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 8 * i + (lane >> 2);
+    const uint4 w = lds_v4(stage + r * 80 + at);
+    if (r < rows && at < bytes) *reinterpret_cast<uint4*>(to + r * stride + at) = w;
+  }
+  __syncwarp();
+}
+
+template <bool FP8, bool GATED>
+__global__ void __launch_bounds__(kMatmulThreads, 1)
+many_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tw, const __grid_constant__ MatmulParams p) {
+  using C = ManyCfg<FP8, GATED>;
+  extern __shared__ uint8_t raw[];
+  const uint32_t stages = (smem_u32(raw) + 1023u) & ~1023u;
+  uint8_t* const base = raw + (stages - smem_u32(raw));
+  const uint32_t pieces = stages + C::kStages * C::kStage;
+  int* const table = reinterpret_cast<int*>(base + C::kStages * C::kStage + C::kPieces);
+  const Groups groups{table, table + kMatmulMaxGroups + 1, table + 2 * kMatmulMaxGroups + 1};
+  const uint32_t bars = pieces + C::kPieces + C::kTable;
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(base + (bars - stages) + 496);
+  const uint32_t tmem_holder = bars + 500;
+  const auto full = [&](int s) { return bars + 8 * s; };    // (the first CTA's are used)
+  const auto empty = [&](int s) { return bars + 64 + 8 * s; };
+  const auto acc_full = [&](int b) { return bars + 128 + 8 * b; };
+  const auto acc_empty = [&](int b) { return bars + 144 + 8 * b; };  // (the first CTA's)
+  const auto both = [&](int q) { return bars + 160 + 8 * q; };       // a row's two warps
+
+  const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) mbar_init(full(s), 1), mbar_init(empty(s), 1);
+    for (int b = 0; b < 2; ++b) mbar_init(acc_full(b), 1), mbar_init(acc_empty(b), 16);
+    for (int q = 0; q < 4; ++q) mbar_init(both(q), 2);
+    *abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&tx);
+    tma_prefetch_desc(&tw);
+  }
+  load_groups<C::BM>(p, groups);
+  if (warp == 9) {
+    tmem_alloc_pair(tmem_holder, 512);
+    tmem_relinquish_pair();
+  }
+  __syncthreads();
+  if (warp == 8) count_tiles<C::BM>(p.E, p.most_tiles, groups);
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = lds_u32(tmem_holder);
+  const auto quit = [&] {
+    *abort_flag = 1;
+    st_cluster_u32(map_to(bars + 496, rank ^ 1), 1);
+    raise_status(p.status, kStatusTimeout);
+  };
+  const int blocks = (p.K + C::kK - 1) / C::kK;
+  const int step = gridDim.x / 2;
+  Tile tile;
+
+  if (warp < 8) {
+    // ------------------------------------------------ sums and results
+    regs_grow<224>();  // (2 x 224 + 56 = 3 x 168)
+    const int half = warp >> 2, q = warp & 3;
+    const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + half * 128;
+    const uint32_t stage = pieces + warp * 32 * C::kRow;
+    const int size = p.out_type == 2 ? 4 : 2;
+    const bool vec = p.out ? (reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)(p.out_stride * size)) % 16 == 0
+                           : (reinterpret_cast<uintptr_t>(p.codes) | (uintptr_t)p.width) % 16 == 0;
+    int buffer = 0, turn = 0, tiles = 0;
+    bool on = true;
+    for (int t = blockIdx.x / 2; on && find_tile<C::BM, C::kOut>(p, groups, t, &tile); t += step) {
+      const int64_t row0 = tile.row + 128 * (int)rank + q * 32;   // the warp's first row
+      const int rows = tile.count - 128 * (int)rank - q * 32;      // and how many it has
+      int src = 0;
+      bool bad = false;
+      if (lane < rows) {
+        src = p.rows ? __ldg(p.rows + row0 + lane) : (int)row0 + lane;
+        bad = src < 0 || src >= p.x_rows;
+        if (bad) src = 0;
+        if (bad && half == 0) raise_status(p.status, kStatusBadMetadata);
+      }
+      uint64_t acc[64];
+#pragma unroll
+      for (int i = 0; i < 64; ++i) acc[i] = 0;
+      if (FP8) {
+        const float* const xs = p.x_scales + (int64_t)src * p.kb;
+        const int n0 = GATED ? tile.column + 64 * half : tile.column + 128 * half;
+        const float* const ws = p.w_scales + ((int64_t)tile.e * p.nb + min(p.nb - 1, n0 / kMatmulBlock)) * p.kb;
+        const float* const wu = p.w_scales + ((int64_t)tile.e * p.nb + min(p.nb - 1, (p.width + n0) / kMatmulBlock)) * p.kb;
+        // (a block's scales are loaded while the block before is summed)
+        float s_next = ld_ahead(xs + 0), g_next = ld_ahead(ws + 0), u_next = GATED ? ld_ahead(wu + 0) : 0.f;
+        for (int k = 0; k < blocks; ++k) {
+          const float f = s_next * g_next, u = GATED ? s_next * u_next : f;
+          const int at = min(k + 1, blocks - 1);
+          s_next = ld_ahead(xs + at), g_next = ld_ahead(ws + at);
+          if (GATED) u_next = ld_ahead(wu + at);
+          on = __all_sync(~0u, mbar_wait(acc_full(buffer), turn, abort_flag));
+          if (!on) break;
+          tc_fence_after();
+          if (rows > 0) add_block<128>(lanes + buffer * 256, acc, f, u);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster_relaxed(map_to(acc_empty(buffer), 0));
+          if (++buffer == 2) buffer = 0, turn ^= 1;
+        }
+      } else {
+        on = __all_sync(~0u, mbar_wait(acc_full(buffer), turn, abort_flag));
+        if (on) {
+          tc_fence_after();
+          if (rows > 0) take_block<128>(lanes + buffer * 256, acc);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster_relaxed(map_to(acc_empty(buffer), 0));
+          if (++buffer == 2) buffer = 0, turn ^= 1;
+        }
+      }
+      if (!on) break;
+      if (bad) {
+#pragma unroll
+        for (int i = 0; i < 64; ++i) acc[i] = 0;
+      }
+      // the results of this lane's row: 128 of them, or gated 64
+      constexpr int kMine = GATED ? 64 : 128;
+      const int n = tile.column + half * kMine;
+      if (GATED) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const float2 g = unpack2(acc[i]), u = unpack2(acc[32 + i]);
+          acc[i] = pack2(gate(g.x, u.x), gate(g.y, u.y));
+        }
+      }
+      if (GATED && p.codes) {
+        float amax = 0.f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const float2 y = unpack2(acc[i]);
+          if (n + 2 * i < p.width) amax = fmaxf(amax, fabsf(y.x));
+          if (n + 2 * i + 1 < p.width) amax = fmaxf(amax, fabsf(y.y));
+        }
+        // the row's other 64 results are another warp's
+        const uint32_t here = lane * C::kRow + 64 + (tiles & 1) * 4;
+        sts_u32(stage + here, __float_as_uint(amax));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(both(q));
+        on = __all_sync(~0u, mbar_wait(both(q), tiles & 1, abort_flag));
+        if (!on) break;
+        amax = fmaxf(amax, __uint_as_float(lds_u32(pieces + (warp ^ 4) * 32 * C::kRow + here)));
+        const float step = __fdiv_rn(amax, 448.0f), s = step == 0.f ? 1.0f : step;
+        uint32_t codes[16];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float y[8];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 v = unpack2(acc[4 * i + j]);
+            y[2 * j] = v.x, y[2 * j + 1] = v.y;
+          }
+          const uint2 c = quantize8(y, s);
+          codes[2 * i] = c.x, codes[2 * i + 1] = c.y;
+        }
+        if (rows > 0 && n < p.width) {
+          uint8_t* const to = p.codes + row0 * p.width + n;
+          if (vec) {
+            store_piece(stage, to, p.width, rows, p.width - n, codes);
+          } else if (lane < rows) {
+#pragma unroll
+            for (int i = 0; i < 64; ++i)
+              if (n + i < p.width) to[(int64_t)lane * p.width + i] = (uint8_t)(codes[i / 4] >> (8 * (i & 3)));
+          }
+          if (half == 0 && lane < rows) p.scales[(row0 + lane) * ((p.width + 127) / 128) + tile.column / 128] = s;
+        }
+      } else if (rows > 0) {
+        // pieces of 64 bytes: 32 results of 16 bits, or 16 of 32
+        const int wanted = min(kMine, p.width - n);
+        uint8_t* const to = static_cast<uint8_t*>(p.out) + (row0 * p.out_stride + n) * size;
+        if (vec && wanted * size % 16 == 0) {
+          if (size == 2) {
+#pragma unroll
+            for (int c = 0; c < kMine / 32; ++c) {
+              uint32_t v[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const float2 y = unpack2(acc[16 * c + i]);
+                v[i] = round_pair(y.x, y.y, p.out_type == 0);
+              }
+              if (32 * c < wanted) store_piece(stage, to + 64 * c, p.out_stride * 2, rows, (wanted - 32 * c) * 2, v);
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < kMine / 16; ++c) {
+              uint32_t v[16];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float2 y = unpack2(acc[8 * c + i]);
+                v[2 * i] = __float_as_uint(y.x), v[2 * i + 1] = __float_as_uint(y.y);
+              }
+              if (16 * c < wanted) store_piece(stage, to + 64 * c, p.out_stride * 4, rows, (wanted - 16 * c) * 4, v);
+            }
+          }
+        } else if (lane < rows) {
+#pragma unroll
+          for (int i = 0; i < kMine / 2; ++i) {
+            const float2 y = unpack2(acc[i]);
+            const int64_t at = (row0 + lane) * p.out_stride + n + 2 * i;
+            if (2 * i < wanted) store_element(p.out, at, p.out_type, y.x);
+            if (2 * i + 1 < wanted) store_element(p.out, at + 1, p.out_type, y.y);
+          }
+        }
+      }
+      ++tiles;
+    }
+    if (!on) quit();
+  } else {
+    regs_shrink<56>();
+    if (warp == 8) {
+      // ------------------------------------------------ loads
+      int s = 0, phase = 0;
+      uint32_t used = 0;  // stages that were ever filled
+      bool on = !p.give_up;
+      for (int t = blockIdx.x / 2; on && find_tile<C::BM, C::kOut>(p, groups, t, &tile); t += step) {
+        const int rows0 = min(128, tile.count), rows1 = max(0, tile.count - 128);
+        const int mine = rank ? rows1 : rows0;
+        const int unit = p.rows ? 4 : 32;
+        const int boxes = (mine + unit - 1) / unit;
+        const uint32_t bytes = 2 * C::kStageB + ((rows0 + unit - 1) / unit + (rows1 + unit - 1) / unit) * unit * 128;
+        const int first = tile.row + 128 * (int)rank;
+        int4 from = make_int4(0, 0, 0, 0);
+        if (p.rows && boxes) {
+          int r[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            r[i] = __ldg(p.rows + first + min(4 * lane + i, mine - 1));
+            if (r[i] < 0 || r[i] >= p.x_rows) r[i] = 0;
+          }
+          from = make_int4(r[0], r[1], r[2], r[3]);
+        }
+        for (int k = 0; k < blocks; ++k) {
+          if (!__all_sync(~0u, mbar_wait(empty(s), phase ^ 1, abort_flag))) {
+            on = false;
+            break;
+          }
+          const uint32_t a = stages + s * C::kStage, b = a + C::kStageA, bar = map_to(full(s), 0);
+          const int x = k * C::kK;
+          if (lane == 0) {
+            if (rank == 0) mbar_arrive_expect_tx(full(s), bytes);
+            if (GATED) {
+              tma_load_3d_pair(b, &tw, x, tile.column + 64 * (int)rank, tile.e, bar);
+              tma_load_3d_pair(b + 8192, &tw, x, p.width + tile.column + 64 * (int)rank, tile.e, bar);
+            } else {
+              tma_load_3d_pair(b, &tw, x, tile.column + 128 * (int)rank, tile.e, bar);
+            }
+          }
+          __syncwarp();
+          if (lane < boxes) {
+            if (p.rows) tma_gather4_pair(a + lane * 512, &tx, x, from, bar);
+            else tma_load_2d_pair(a + lane * 4096, &tx, x, first + 32 * lane, bar);
+          }
+          used |= 1u << s;
+          if (++s == C::kStages) s = 0, phase ^= 1;
+        }
+      }
+      if (!on) {
+        // the copies of both CTAs under way end before either does
+        quit();
+        for (int i = 0; i < C::kStages && rank == 0; ++i)
+          if (used >> i & 1) mbar_wait(full(i), (i < s ? phase : phase ^ 1), nullptr);
+      }
+    } else if (warp == 9 && rank == 0) {
+      // ------------------------------------------------ products of both CTAs
+      if (lane == 0) {
+        const uint32_t idesc = FP8 ? idesc_e4m3_f32(256, 256) : idesc_16_f32(p.x_type == 0, 256, 256, false);
+        int s = 0, phase = 0, buffer = 0, turn = 0;
+        bool on = true;
+        for (int t = blockIdx.x / 2; on && find_tile<C::BM, C::kOut>(p, groups, t, &tile); t += step) {
+          for (int k = 0; k < blocks; ++k) {
+            if (FP8 || k == 0) on = mbar_wait_cluster(acc_empty(buffer), turn ^ 1, abort_flag);
+            on = on && mbar_wait(full(s), phase, abort_flag);
+            if (!on) break;
+            tc_fence_after();
+            const uint32_t a = stages + s * C::kStage, d = tmem + buffer * 256;
+            if (FP8) umma_f8_k128_pair(d, sw128_desc(a), sw128_desc(a + C::kStageA), idesc, 0);
+            else umma_f16_k64_pair(d, sw128_desc(a), sw128_desc(a + C::kStageA), idesc, k > 0);
+            umma_commit_pair(empty(s));
+            if (FP8 || k + 1 == blocks) {
+              umma_commit_pair(acc_full(buffer));
+              if (++buffer == 2) buffer = 0, turn ^= 1;
+            }
+            if (++s == C::kStages) s = 0, phase ^= 1;
+          }
+        }
+        if (!on) {
+          quit();
+          // products under way end before the CTAs do: their last commit is that of the stage before
+          const int last = s == 0 ? C::kStages - 1 : s - 1;
+          mbar_wait(empty(last), s == 0 ? phase ^ 1 : phase, nullptr);
+        }
+      }
+      __syncwarp();
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  if (warp == 9) tmem_dealloc_pair(tmem, 512);
 }
 
 }  // namespace dsa
