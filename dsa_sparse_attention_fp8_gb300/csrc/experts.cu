@@ -19,14 +19,13 @@ using namespace dsa_host;
 
 bool is_float(int type) { return type == DSA_TYPE_BF16 || type == DSA_TYPE_FP16 || type == DSA_TYPE_FP32; }
 
-// The tensor maps of rows and weights.  Rows come in boxes of `box` rows, or one by one where they are gathered; weights in
-// boxes of `w_box` rows; 128 bytes of K at a time.
+// The tensor maps of rows (unless they are gathered) and weights, in boxes of `box` and `w_box` rows and 128 bytes of K.
 int product_maps(const dsa::MatmulParams& p, int box, int w_box, CUtensorMap* tx, CUtensorMap* tw) {
   const int size = element_bytes(p.x_type);
   const CUtensorMapDataType type = size == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                                    : p.x_type == DSA_TYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   const int64_t xd[2] = {p.K, p.x_rows}, xs[1] = {p.x_stride * size};
-  const int xb[2] = {128 / size, p.rows ? 1 : box};
+  const int xb[2] = {128 / size, box};
   if (const int rc = make_map(tx, "x", type, size, p.x, 2, xd, xs, xb, true)) return rc;
   const int64_t wd[3] = {p.K, p.N, p.E}, ws[2] = {p.w_stride * size, p.w_group * size};
   const int wb[3] = {128 / size, w_box, 1};
@@ -114,6 +113,7 @@ int launch_many(dsa::MatmulParams p, int64_t groups, cudaStream_t st) {
 int run_matmul(dsa::MatmulParams p, int64_t groups, cudaStream_t st) {
   if (p.M < 0 || p.x_rows < 0) return fail(DSA_ERR_INVALID_ARG, "a negative number of rows");
   if (p.N < 1 || p.K < 1) return fail(DSA_ERR_INVALID_ARG, "N=%d, K=%d: both must be positive", p.N, p.K);
+  if (p.N > 1 << 28 || p.K > 1 << 28) return fail(DSA_ERR_UNSUPPORTED, "N=%d, K=%d: at most 2^28", p.N, p.K);
   if (p.gated && p.N % 2) return fail(DSA_ERR_INVALID_ARG, "gated weights have two halves: N=%d is odd", p.N);
   p.width = p.gated ? p.N / 2 : p.N;
   const bool fp8 = p.x_type == DSA_TYPE_E4M3;
@@ -126,6 +126,8 @@ int run_matmul(dsa::MatmulParams p, int64_t groups, cudaStream_t st) {
     return fail(DSA_ERR_INVALID_ARG, "strides of rows and weights must be multiples of 16 bytes");
   if (!apart(p.x_stride, p.x_rows) || !apart(p.w_stride, p.N) || !apart(p.w_group, groups))
     return fail(DSA_ERR_INVALID_ARG, "a stride of 0 over more than one row");
+  if (p.rows && p.x_stride * size / 16 > (INT64_C(1) << 32) / std::max(1, p.x_rows))
+    return fail(DSA_ERR_UNSUPPORTED, "gathered rows lie over more than 64 GB");
   if (p.M == 0) return DSA_OK;
   if ((p.out != nullptr) == (p.codes != nullptr) || (p.codes != nullptr) != (p.scales != nullptr))
     return fail(DSA_ERR_INVALID_ARG, "either out or out_codes and out_scales");

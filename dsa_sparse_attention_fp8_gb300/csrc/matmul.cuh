@@ -132,6 +132,52 @@ __device__ __forceinline__ void take_block(uint32_t from, uint64_t (&acc)[COLS /
   }
 }
 
+// ---------------------------------------------------------------- gathered rows
+// Two warps copy a tile's rows x[rows[i]] into the stages, 16 bytes a lane, in the layout that the tensor core reads (and
+// TMA writes): 128-byte rows whose 16-byte pieces change places within eight rows.  Every lane's copies arrive at the
+// stage's barrier by themselves; whoever waits there fences them for the tensor core (a fence in these warps would wait for
+// all their copies, also those of later stages: experts of a chunk took 4773 us by it).  The tensor-copy unit gathers too,
+// four rows an instruction, but at 19 cycles a row (4041 us; 1506 from rows that lie in order).
+constexpr int kGatherLanes = 64;
+template <int STAGES, int STAGE, int BM, int OUT>
+__device__ __forceinline__ bool gather_rows(const MatmulParams& p, const Groups& groups, int t, int step, int offset, int most, int size,
+                                            int k0, int k1, uint32_t stages, int g, const volatile int* abort_flag,
+                                            uint32_t empty, uint32_t landed) {
+  const int lane = threadIdx.x & 31, piece = lane & 7;
+  const uint32_t row_pieces = (uint32_t)(p.x_stride * size / 16);
+  const int end = p.K * size;  // of a row's bytes
+  int s = 0, phase = 0;
+  Tile tile;
+  bool on = true;
+  for (; on && find_tile<BM, OUT>(p, groups, t, &tile); t += step) {
+    const int mine = max(0, min(most, tile.count - offset));
+    // this lane's rows are 8 i + 4 g + lane / 8
+    const int own = 4 * g + (lane >> 3);
+    uint32_t from[16];  // and start these many pieces into x
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int r = 8 * i + own < mine ? __ldg(p.rows + tile.row + offset + 8 * i + own) : 0;
+      from[i] = r < 0 || r >= p.x_rows ? 0 : (uint32_t)r * row_pieces;
+    }
+    const uint8_t* const x = static_cast<const uint8_t*>(p.x) + piece * 16;
+    for (int k = k0; k < k1; ++k) {
+      on = __all_sync(~0u, mbar_wait(empty + 8 * s, phase ^ 1, abort_flag));
+      if (!on) break;
+      const int at = k * 128;
+      const uint32_t bytes = (uint32_t)min(16, max(0, end - at - piece * 16));
+      const uint32_t to = stages + s * STAGE + own * 128 + ((piece ^ own) * 16);
+      const uint8_t* const src = bytes ? x + at : x;
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (8 * i + own < mine) copy16_async(to + i * 1024, src + (uint64_t)from[i] * 16, bytes);
+      copies_arrive(landed + 8 * s);
+      if (++s == STAGES) s = 0, phase ^= 1;
+    }
+  }
+  copies_wait_all();
+  return on;
+}
+
 // ---------------------------------------------------------------- results
 __device__ __forceinline__ float gate(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
 
@@ -213,7 +259,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
   const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t S = cluster_size(), rank = cluster_rank();
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::kStages; ++s) mbar_init(full(s), 1), mbar_init(empty(s), 1);
+    for (int s = 0; s < C::kStages; ++s) mbar_init(full(s), p.rows ? 1 + kGatherLanes : 1), mbar_init(empty(s), 1);
     for (int b = 0; b < C::kBuffers; ++b) mbar_init(acc_full(b), 1), mbar_init(acc_empty(b), 8);
     mbar_init(join_full, 8 * S);
     mbar_init(join_free, 8 * S);
@@ -375,18 +421,8 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
       bool on = !p.give_up;
       if (!on) quit();
       for (int t = blockIdx.x / S; on && find_tile<BM, C::kOut>(p, groups, t, &tile); t += step) {
-        int4 from = make_int4(0, 0, 0, 0);
-        const int boxes = p.rows ? (tile.count + 3) / 4 : (tile.count + 31) / 32;
-        if (p.rows) {
-          int r[4];
-  #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            r[i] = __ldg(p.rows + tile.row + min(4 * lane + i, tile.count - 1));
-            if (r[i] < 0 || r[i] >= p.x_rows) r[i] = 0;
-          }
-          from = make_int4(r[0], r[1], r[2], r[3]);
-        }
-        const uint32_t bytes = C::kStageB + boxes * (p.rows ? 512 : 4096);
+        const int boxes = p.rows ? 0 : (tile.count + 31) / 32;
+        const uint32_t bytes = C::kStageB + boxes * 4096;
         for (int k = k0; k < k1; ++k) {
           if (!__all_sync(~0u, mbar_wait(empty(s), phase ^ 1, abort_flag))) {
             on = false;
@@ -403,10 +439,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
             }
           }
           __syncwarp();
-          if (lane < boxes) {
-            if (p.rows) tma_gather4(a + lane * 512, &tx, x, from, full(s));
-            else tma_load_2d(a + lane * 4096, &tx, x, tile.row + 32 * lane, full(s));
-          }
+          if (lane < boxes) tma_load_2d(a + lane * 4096, &tx, x, tile.row + 32 * lane, full(s));
           used |= 1u << s;
           if (++s == C::kStages) s = 0, phase ^= 1;
         }
@@ -428,6 +461,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
             if (FP8 || k == k0) on = mbar_wait(acc_empty(buffer), turn ^ 1, abort_flag);
             on = on && mbar_wait(full(s), phase, abort_flag);
             if (!on) break;
+            if (p.rows) fence_proxy_async_smem();
             tc_fence_after();
             const uint32_t a = stages + s * C::kStage, d = tmem + buffer * C::BN;
             if (FP8) umma_f8_k128(d, sw128_desc(a), sw128_desc(a + C::kStageA), idesc, 0, 4);
@@ -448,6 +482,13 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
         }
       }
       __syncwarp();
+    } else if (p.rows) {
+      // ------------------------------------------------ gathered rows
+      const int g = warp - 10;
+      if (!gather_rows<C::kStages, C::kStage, BM, C::kOut>(
+              p, groups, blockIdx.x / S, step, 0, BM, FP8 ? 1 : 2, k0, k1, stages,
+              g, abort_flag, bars + 64, bars))
+        quit();
     }
   }
   __syncwarp();
@@ -509,12 +550,13 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__
   const auto empty = [&](int s) { return bars + 64 + 8 * s; };
   const auto acc_full = [&](int b) { return bars + 128 + 8 * b; };
   const auto acc_empty = [&](int b) { return bars + 144 + 8 * b; };  // (the first CTA's)
+  const auto landed = [&](int s) { return bars + 200 + 8 * s; };     // the second CTA's gathered rows
   const auto both = [&](int q) { return bars + 160 + 8 * q; };       // a row's two warps
 
   const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::kStages; ++s) mbar_init(full(s), 1), mbar_init(empty(s), 1);
+    for (int s = 0; s < C::kStages; ++s) mbar_init(full(s), p.rows ? 2 + kGatherLanes : 1), mbar_init(empty(s), 1), mbar_init(landed(s), kGatherLanes);
     for (int b = 0; b < 2; ++b) mbar_init(acc_full(b), 1), mbar_init(acc_empty(b), 16);
     for (int q = 0; q < 4; ++q) mbar_init(both(q), 2);
     *abort_flag = 0;
@@ -544,7 +586,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__
 
   if (warp < 8) {
     // ------------------------------------------------ sums and results
-    regs_grow<224>();  // (2 x 224 + 56 = 3 x 168)
+    regs_grow<216>();  // (2 x 216 + 72 = 3 x 168)
     const int half = warp >> 2, q = warp & 3;
     const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + half * 128;
     const uint32_t stage = pieces + warp * 32 * C::kRow;
@@ -696,29 +738,17 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__
     }
     if (!on) quit();
   } else {
-    regs_shrink<56>();
+    regs_shrink<72>();
     if (warp == 8) {
       // ------------------------------------------------ loads
       int s = 0, phase = 0;
       uint32_t used = 0;  // stages that were ever filled
       bool on = !p.give_up;
       for (int t = blockIdx.x / 2; on && find_tile<C::BM, C::kOut>(p, groups, t, &tile); t += step) {
-        const int rows0 = min(128, tile.count), rows1 = max(0, tile.count - 128);
-        const int mine = rank ? rows1 : rows0;
-        const int unit = p.rows ? 4 : 32;
-        const int boxes = (mine + unit - 1) / unit;
-        const uint32_t bytes = 2 * C::kStageB + ((rows0 + unit - 1) / unit + (rows1 + unit - 1) / unit) * unit * 128;
-        const int first = tile.row + 128 * (int)rank;
-        int4 from = make_int4(0, 0, 0, 0);
-        if (p.rows && boxes) {
-          int r[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            r[i] = __ldg(p.rows + first + min(4 * lane + i, mine - 1));
-            if (r[i] < 0 || r[i] >= p.x_rows) r[i] = 0;
-          }
-          from = make_int4(r[0], r[1], r[2], r[3]);
-        }
+        // boxes of 32 rows of each CTA
+        const int boxes0 = p.rows ? 0 : (min(128, tile.count) + 31) / 32, boxes1 = p.rows ? 0 : (max(0, tile.count - 128) + 31) / 32;
+        const int boxes = rank ? boxes1 : boxes0, first = tile.row + 128 * (int)rank;
+        const uint32_t bytes = 2 * C::kStageB + (boxes0 + boxes1) * 4096;
         for (int k = 0; k < blocks; ++k) {
           if (!__all_sync(~0u, mbar_wait(empty(s), phase ^ 1, abort_flag))) {
             on = false;
@@ -736,10 +766,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__
             }
           }
           __syncwarp();
-          if (lane < boxes) {
-            if (p.rows) tma_gather4_pair(a + lane * 512, &tx, x, from, bar);
-            else tma_load_2d_pair(a + lane * 4096, &tx, x, first + 32 * lane, bar);
-          }
+          if (lane < boxes) tma_load_2d_pair(a + lane * 4096, &tx, x, first + 32 * lane, bar);
           used |= 1u << s;
           if (++s == C::kStages) s = 0, phase ^= 1;
         }
@@ -758,9 +785,10 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__
         bool on = true;
         for (int t = blockIdx.x / 2; on && find_tile<C::BM, C::kOut>(p, groups, t, &tile); t += step) {
           for (int k = 0; k < blocks; ++k) {
-            if (FP8 || k == 0) on = mbar_wait_cluster(acc_empty(buffer), turn ^ 1, abort_flag);
+            if (FP8 || k == 0) on = mbar_wait(acc_empty(buffer), turn ^ 1, abort_flag);
             on = on && mbar_wait(full(s), phase, abort_flag);
             if (!on) break;
+            if (p.rows) fence_proxy_async_smem();
             tc_fence_after();
             const uint32_t a = stages + s * C::kStage, d = tmem + buffer * 256;
             if (FP8) umma_f8_k128_pair(d, sw128_desc(a), sw128_desc(a + C::kStageA), idesc, 0);
@@ -781,6 +809,30 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__
         }
       }
       __syncwarp();
+    } else if (warp == 9 && p.rows) {
+      // ------------------------------------------------ the second CTA's gathered rows, told to the first
+      if (lane == 0) {
+        int s = 0, phase = 0;
+        bool on = true;
+        for (int t = blockIdx.x / 2; on && find_tile<C::BM, C::kOut>(p, groups, t, &tile); t += step) {
+          for (int k = 0; k < blocks; ++k) {
+            on = mbar_wait(landed(s), phase, abort_flag);
+            if (!on) break;
+            fence_proxy_async_smem();
+            mbar_arrive_remote(map_to(full(s), 0));
+            if (++s == C::kStages) s = 0, phase ^= 1;
+          }
+        }
+        if (!on) quit();
+      }
+      __syncwarp();
+    } else if (warp >= 10 && p.rows) {
+      // ------------------------------------------------ gathered rows
+      const int g = warp - 10;
+      if (!gather_rows<C::kStages, C::kStage, C::BM, C::kOut>(
+              p, groups, blockIdx.x / 2, step, 128 * (int)rank, 128, FP8 ? 1 : 2, 0, blocks, stages,
+              g, abort_flag, bars + 64, rank ? bars + 200 : bars))
+        quit();
     }
   }
   __syncwarp();

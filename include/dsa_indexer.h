@@ -583,8 +583,8 @@ int dsa_add_rms_norm(const void* x, int64_t x_stride, const void* residual, int6
  *     is 0; codes E4M3(y/s), RNE, saturating), [T, N/2] and [T, ceil(N/256)]
  *     contiguous.  Exactly one of the two is given.
  * Row strides are in elements; those of codes and w_codes are multiples of 16,
- * both 16-byte aligned.  K and N are any sizes from 1.  Outputs must not
- * overlap inputs.
+ * both 16-byte aligned.  K and N are any sizes from 1 to 2^28.  Outputs must
+ * not overlap inputs.
  * Computation: tensor-core products with FP32 accumulation over a block of K,
  * its scales and the sums over blocks in FP32, gate in FP32, one rounding.
  * Faults: DSA_STATUS_TIMEOUT (an internal wait ran out; results are invalid).
