@@ -150,12 +150,53 @@ int run_matmul(dsa::MatmulParams p, int64_t groups, cudaStream_t st) {
   return few ? launch_few<false, false, 64>(p, groups, st) : some ? launch_few<false, false, 128>(p, groups, st) : launch_many<false, false>(p, groups, st);
 }
 
-template <int V>
-void launch_choose(const dsa::RouteParams& p, int type, cudaStream_t st) {
+// A kernel of the router, as a cluster of `ctas` CTAs or behind a kernel that lets it start early.
+template <typename Kernel>
+int launch_places(const char* name, Kernel kernel, PerDevice& allowed, int threads, int ctas, bool early, const dsa::RouteParams& p,
+                  cudaStream_t st) {
+  if (const int rc = allow_smem(allowed, (const void*)kernel, dsa::counts_bytes(threads / 32, dsa::kRouteMaxExperts))) return rc;
+  if (ctas > 8) {
+    static PerDevice wide;
+    const cudaError_t rc = wide.once([&] { return cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1); });
+    if (rc != cudaSuccess) return fail(DSA_ERR_CUDA, "%s: %s", name, cudaGetErrorString(rc));
+  }
+  cudaLaunchConfig_t c{};
+  cudaLaunchAttribute a[2];
+  a[0].id = cudaLaunchAttributeClusterDimension;
+  a[0].val.clusterDim.x = ctas, a[0].val.clusterDim.y = 1, a[0].val.clusterDim.z = 1;
+  a[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a[1].val.programmaticStreamSerializationAllowed = 1;
+  c.gridDim = dim3(ctas), c.blockDim = dim3(threads), c.dynamicSmemBytes = dsa::counts_bytes(threads / 32, p.E);
+  c.stream = st, c.attrs = a, c.numAttrs = early ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&c, kernel, p);
+  if (e != cudaSuccess) return fail(DSA_ERR_CUDA, "%s: %s", name, cudaGetErrorString(e));
+  return check_launch(name);
+}
+
+template <int V, typename T>
+int launch_route(const dsa::RouteParams& p, cudaStream_t st) {
+  static PerDevice few, many;
+  constexpr int kWarps = dsa::kFewThreads / 32;
+  if (p.T <= kWarps * dsa::kFewCtas) {
+    int ctas = 1;
+    while (ctas * kWarps < p.T) ctas *= 2;
+    if (const int rc = launch_places("route_few_kernel", dsa::route_few_kernel<V, T>, few, dsa::kFewThreads, ctas, false, p, st)) return rc;
+    set_last_launches(1);
+    return DSA_OK;
+  }
   const unsigned grid = (unsigned)(((int64_t)p.T * 32 + dsa::kRouteThreads - 1) / dsa::kRouteThreads);
-  if (type == DSA_TYPE_BF16) dsa::route_choose_kernel<V, __nv_bfloat16><<<grid, dsa::kRouteThreads, 0, st>>>(p);
-  else if (type == DSA_TYPE_FP16) dsa::route_choose_kernel<V, __half><<<grid, dsa::kRouteThreads, 0, st>>>(p);
-  else dsa::route_choose_kernel<V, float><<<grid, dsa::kRouteThreads, 0, st>>>(p);
+  dsa::route_choose_kernel<V, T><<<grid, dsa::kRouteThreads, 0, st>>>(p);
+  if (const int rc = check_launch("route_choose_kernel")) return rc;
+  if (const int rc = launch_places("route_place_kernel", dsa::route_place_kernel, many, dsa::kPlaceThreads, dsa::kPlaceCtas, true, p, st)) return rc;
+  set_last_launches(2);
+  return DSA_OK;
+}
+
+template <int V>
+int launch_route(const dsa::RouteParams& p, int type, cudaStream_t st) {
+  if (type == DSA_TYPE_BF16) return launch_route<V, __nv_bfloat16>(p, st);
+  if (type == DSA_TYPE_FP16) return launch_route<V, __half>(p, st);
+  return launch_route<V, float>(p, st);
 }
 
 template <typename T>
@@ -238,21 +279,16 @@ int dsa_route_experts(const void* logits, int64_t stride, int type, const float*
   p.num_groups = num_groups, p.top_groups = top_groups, p.per = E / num_groups;
   p.scale = scale, p.softmax = scoring == DSA_SCORE_SOFTMAX, p.normalize = normalize != 0;
   const cudaStream_t st = (cudaStream_t)stream;
-  const int smem = (dsa::kPlaceThreads / 32 + 1) * E * 4;
-  static PerDevice allowed;
-  if (const int rc = allow_smem(allowed, (const void*)dsa::route_place_kernel, (dsa::kPlaceThreads / 32 + 1) * dsa::kRouteMaxExperts * 4))
-    return rc;
-  if (T) {
-    if (E <= 32) launch_choose<1>(p, type, st);
-    else if (E <= 64) launch_choose<2>(p, type, st);
-    else if (E <= 128) launch_choose<4>(p, type, st);
-    else if (E <= 256) launch_choose<8>(p, type, st);
-    else launch_choose<16>(p, type, st);
-    if (const int rc = check_launch("route_choose_kernel")) return rc;
-  }
-  dsa::route_place_kernel<<<1, dsa::kPlaceThreads, smem, st>>>(p);
-  set_last_launches(T ? 2 : 1);
-  return check_launch("route_place_kernel");
+  // a run's lanes: as many as there are for each of so many runs
+  p.lanes = 32;
+  while (32 / p.lanes < num_groups) p.lanes /= 2;
+  p.wide = (p.per + p.lanes - 1) / p.lanes;
+  if (p.wide <= 1) return launch_route<1>(p, type, st);
+  if (p.wide <= 2) return launch_route<2>(p, type, st);
+  if (p.wide <= 4) return launch_route<4>(p, type, st);
+  if (p.wide <= 8) return launch_route<8>(p, type, st);
+  if (p.wide <= 16) return launch_route<16>(p, type, st);
+  return launch_route<32>(p, type, st);
 }
 
 int dsa_combine_experts(const void* y, int64_t y_stride, int type, int M, const int32_t* places,
