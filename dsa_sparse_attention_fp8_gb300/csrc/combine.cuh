@@ -5,6 +5,7 @@
 
 #include "common.cuh"
 #include "norm.cuh"
+#include "ptx.cuh"
 
 namespace dsa {
 
@@ -21,42 +22,60 @@ struct CombineParams {
   int M, T, top_k, N;
 };
 
-// A CTA per token.  `add` may be `out` itself: ordinary loads.
+// A thread has 8 elements of a token; blockIdx.y is the slice of the row.  All of a token's rows are asked for before the
+// first is added.  `add` may be `out` itself: ordinary loads.
+constexpr int kCombineThreads = 128;
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ CombineParams p) {
+__global__ void __launch_bounds__(kCombineThreads) combine_kernel(const __grid_constant__ CombineParams p) {
+  constexpr int kAhead = 8;
   const int t = blockIdx.x;
-  const int32_t* places = p.places + (int64_t)t * p.top_k;
-  const float* weights = p.weights + (int64_t)t * p.top_k;
-  for (int at = threadIdx.x * 8; at < p.N; at += blockDim.x * 8) {
+  const int32_t* const places = p.places + (int64_t)t * p.top_k;
+  const float* const weights = p.weights + (int64_t)t * p.top_k;
+  pdl_launch_dependents();
+  pdl_wait();
+  for (int at = (blockIdx.y * kCombineThreads + threadIdx.x) * 8; at < p.N; at += gridDim.y * kCombineThreads * 8) {
     float sum[8] = {};
-    for (int j = 0; j < p.top_k; ++j) {
-      const int place = places[j];
-      if (place >= p.M) {
-        if (at == 0) raise_status(p.status, kStatusBadMetadata);
-        continue;
-      }
-      if (place < 0) continue;
-      const Norm8<T> v = load8<T, VEC>(static_cast<const T*>(p.y) + (int64_t)place * p.y_stride, at, p.N);
-      const float w = weights[j];
+    Norm8<T> own;
+    if (p.add) own = load8<T, VEC>(static_cast<const T*>(p.add) + (int64_t)t * p.add_stride, at, p.N);
+    for (int j0 = 0; j0 < p.top_k; j0 += kAhead) {
+      int place[kAhead];
+      float w[kAhead];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 f = widen(v, i);
-        sum[2 * i] = fmaf(w, f.x, sum[2 * i]);
-        sum[2 * i + 1] = fmaf(w, f.y, sum[2 * i + 1]);
+      for (int j = 0; j < kAhead; ++j) {
+        const bool is = j0 + j < p.top_k;
+        place[j] = is ? places[j0 + j] : -1;
+        w[j] = is ? weights[j0 + j] : 0.f;
       }
-    }
-    if (p.add) {
-      const Norm8<T> v = load8<T, VEC>(static_cast<const T*>(p.add) + (int64_t)t * p.add_stride, at, p.N);
+      Norm8<T> v[kAhead];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 f = widen(v, i);
-        sum[2 * i] += f.x;
-        sum[2 * i + 1] += f.y;
+      for (int j = 0; j < kAhead; ++j) {
+        if (place[j] >= p.M) {
+          if (at == 0) raise_status(p.status, kStatusBadMetadata);
+          place[j] = -1;
+        }
+        if (place[j] >= 0) v[j] = load8<T, VEC>(static_cast<const T*>(p.y) + (int64_t)place[j] * p.y_stride, at, p.N);
+      }
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        if (place[j] < 0) continue;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = widen(v[j], i);
+          sum[2 * i] = fmaf(w[j], f.x, sum[2 * i]);
+          sum[2 * i + 1] = fmaf(w[j], f.y, sum[2 * i + 1]);
+        }
       }
     }
     Norm8<T> out;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) round2(out, i, make_float2(sum[2 * i], sum[2 * i + 1]));
+    for (int i = 0; i < 4; ++i) {
+      float2 f = make_float2(sum[2 * i], sum[2 * i + 1]);
+      if (p.add) {
+        const float2 a = widen(own, i);
+        f.x += a.x, f.y += a.y;
+      }
+      round2(out, i, f);
+    }
     store8<T, VEC>(static_cast<T*>(p.out) + (int64_t)t * p.out_stride, at, p.N, out);
   }
 }

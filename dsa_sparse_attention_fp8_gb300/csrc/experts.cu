@@ -5,6 +5,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "combine.cuh"
 #include "dsa_indexer.h"
@@ -32,6 +33,12 @@ int product_maps(const dsa::MatmulParams& p, int box, int w_box, CUtensorMap* tx
   return make_map(tw, "weight", type, size, p.w, 3, wd, ws, wb, true);
 }
 
+// Tiles of `tile` rows that so many groups of M rows in all can have.
+int64_t row_tiles(int64_t M, int64_t groups, int tile) {
+  const int64_t used = std::min(groups, M);
+  return used + (M - used) / tile;
+}
+
 // Clusters of `size` CTAs of a kernel that the current device runs at once, asked for once a device.
 class ClusterCount {
  public:
@@ -55,40 +62,50 @@ class ClusterCount {
   std::atomic<int> known_[64][9] = {};
 };
 
-template <typename Kernel>
-int launch_clusters(const char* name, Kernel kernel, int clusters, int size, int smem, cudaStream_t st, const CUtensorMap& tx,
-                    const CUtensorMap& tw, const dsa::MatmulParams& p) {
+// Launches a kernel, in clusters of `size` CTAs, that waits for what is before it in the stream by itself: it is set up while
+// the kernel before drains (DSA_PDL=0: not).
+template <typename... P, typename... A>
+int launch(const char* name, void (*kernel)(P...), dim3 grid, int block, int size, int smem, cudaStream_t st, const A&... args) {
   cudaLaunchConfig_t c{};
-  cudaLaunchAttribute a[1];
-  a[0].id = cudaLaunchAttributeClusterDimension;
-  a[0].val.clusterDim.x = size, a[0].val.clusterDim.y = 1, a[0].val.clusterDim.z = 1;
-  c.gridDim = dim3((unsigned)(clusters * size)), c.blockDim = dim3(dsa::kMatmulThreads);
-  c.dynamicSmemBytes = smem, c.stream = st, c.attrs = a, c.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&c, kernel, tx, tw, p);
+  cudaLaunchAttribute a[2];
+  a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a[0].val.programmaticStreamSerializationAllowed = env_int("DSA_PDL", 1, 0, 1);
+  a[1].id = cudaLaunchAttributeClusterDimension;
+  a[1].val.clusterDim.x = size, a[1].val.clusterDim.y = 1, a[1].val.clusterDim.z = 1;
+  c.gridDim = grid, c.blockDim = dim3(block), c.dynamicSmemBytes = smem;
+  c.stream = st, c.attrs = a, c.numAttrs = size > 1 ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&c, kernel, args...);
   if (e != cudaSuccess) return fail(DSA_ERR_CUDA, "%s: %s", name, cudaGetErrorString(e));
-  set_last_launches(1);
   return check_launch(name);
 }
 
-template <bool FP8, bool GATED, int BM>
+template <bool FP8, bool GATED, bool WIDE, int BM>
 int launch_few(dsa::MatmulParams p, int64_t groups, cudaStream_t st) {
-  using C = dsa::FewCfg<FP8, GATED, BM>;
-  const auto kernel = dsa::few_rows_kernel<FP8, GATED, BM>;
+  using C = dsa::FewCfg<FP8, GATED, WIDE, BM>;
+  const auto kernel = dsa::few_rows_kernel<FP8, GATED, WIDE, BM>;
   static PerDevice allowed;
   static ClusterCount resident;
   if (const int rc = allow_smem(allowed, (const void*)kernel, C::kSmem)) return rc;
   CUtensorMap tx, tw;
-  if (const int rc = product_maps(p, 32, C::kBox, &tx, &tw)) return rc;
+  p.box = p.M <= 32 * groups ? 32 : BM;
+  if (const int rc = product_maps(p, p.box, C::kBox, &tx, &tw)) return rc;
   const int64_t columns = (p.width + C::kOut - 1) / C::kOut;
-  const int64_t most = std::min<int64_t>(groups, p.M);  // groups with rows
-  const int64_t tiles = (p.most_tiles = (int)(most + (p.M - most) / BM)) * columns;
-  const int blocks = (p.K + C::kK - 1) / C::kK;
-  int size = 8;
-  while (size > 1 && (tiles * size > sm_count() || size * 2 > blocks)) size /= 2;
+  p.most_tiles = (int)row_tiles(p.M, groups, BM);
+  const int64_t tiles = p.most_tiles * columns;
   if (tiles > INT32_MAX / 2) return fail(DSA_ERR_UNSUPPORTED, "%lld tiles of results", (long long)tiles);
-  const int clusters = resident.get((const void*)kernel, size, dsa::kMatmulThreads, C::kSmem);
-  if (clusters < 1) return fail(DSA_ERR_CUDA, "no cluster of %d CTAs fits the device", size);
-  return launch_clusters("few_rows_kernel", kernel, (int)std::min<int64_t>(tiles, clusters), size, C::kSmem, st, tx, tw, p);
+  // A CTA alone takes 0.28 us for a block of K, whatever it reads from; CTAs that share a tile join its sums in some 0.1 us each.
+  const int blocks = (p.K + C::kK - 1) / C::kK;
+  int size = 1, clusters = 0;
+  double best = 1e30;
+  for (int s = 1; s <= 8 && (s == 1 || (2 * s <= blocks && tiles * s <= sm_count())); ++s) {
+    const int n = resident.get((const void*)kernel, s, dsa::kMatmulThreads, C::kSmem);
+    if (n < 1) continue;
+    const double t = (double)((tiles + n - 1) / n) * ((blocks + s - 1) / s * 0.28 + 0.5 + 0.1 * s);
+    if (t < best) best = t, size = s, clusters = n;
+  }
+  if (clusters < 1) return fail(DSA_ERR_CUDA, "few_rows_kernel does not fit the device");
+  set_last_launches(1);
+  return launch("few_rows_kernel", kernel, (unsigned)(std::min<int64_t>(tiles, clusters) * size), dsa::kMatmulThreads, size, C::kSmem, st, tx, tw, p);
 }
 
 template <bool FP8, bool GATED>
@@ -99,14 +116,14 @@ int launch_many(dsa::MatmulParams p, int64_t groups, cudaStream_t st) {
   static ClusterCount resident;
   if (const int rc = allow_smem(allowed, (const void*)kernel, C::kSmem)) return rc;
   CUtensorMap tx, tw;
-  if (const int rc = product_maps(p, 32, C::kBox, &tx, &tw)) return rc;
-  const int64_t columns = (p.width + C::kOut - 1) / C::kOut;
-  const int64_t most = std::min<int64_t>(groups, p.M);  // groups with rows
-  const int64_t tiles = (p.most_tiles = (int)(most + (p.M - most) / C::BM)) * columns;
+  if (const int rc = product_maps(p, 128, C::kBox, &tx, &tw)) return rc;
+  p.most_tiles = (int)row_tiles(p.M, groups, C::BM);
+  const int64_t tiles = p.most_tiles * (int64_t)((p.width + C::kOut - 1) / C::kOut);
   if (tiles > INT32_MAX / 2) return fail(DSA_ERR_UNSUPPORTED, "%lld tiles of results", (long long)tiles);
   const int clusters = resident.get((const void*)kernel, 2, dsa::kMatmulThreads, C::kSmem);
   if (clusters < 1) return fail(DSA_ERR_CUDA, "no pair of CTAs fits the device");
-  return launch_clusters("many_rows_kernel", kernel, (int)std::min<int64_t>(tiles, clusters), 2, C::kSmem, st, tx, tw, p);
+  set_last_launches(1);
+  return launch("many_rows_kernel", kernel, (unsigned)(std::min<int64_t>(tiles, clusters) * 2), dsa::kMatmulThreads, 2, C::kSmem, st, tx, tw, p);
 }
 
 // The checks that both products share, and their launch.  p has the sizes, strides and pointers.
@@ -141,55 +158,47 @@ int run_matmul(dsa::MatmulParams p, int64_t groups, cudaStream_t st) {
   if (!fp8) p.x_scales = p.w_scales = nullptr;
   p.give_up = env_int("DSA_WAIT_LIMIT", (int)dsa::kWaitLimit, 0, (int)dsa::kWaitLimit) == 0;
   if (sm_count() <= 0) return fail(DSA_ERR_CUDA, "no CUDA device");
-  bool few = p.M <= 64 * groups, some = p.M <= 128 * groups;
-  if (fp8) {
-    if (p.gated) return few ? launch_few<true, true, 64>(p, groups, st) : some ? launch_few<true, true, 128>(p, groups, st) : launch_many<true, true>(p, groups, st);
-    return few ? launch_few<true, false, 64>(p, groups, st) : some ? launch_few<true, false, 128>(p, groups, st) : launch_many<true, false>(p, groups, st);
-  }
-  if (p.gated) return few ? launch_few<false, true, 64>(p, groups, st) : some ? launch_few<false, true, 128>(p, groups, st) : launch_many<false, true>(p, groups, st);
-  return few ? launch_few<false, false, 64>(p, groups, st) : some ? launch_few<false, false, 128>(p, groups, st) : launch_many<false, false>(p, groups, st);
-}
-
-// A kernel of the router, as a cluster of `ctas` CTAs or behind a kernel that lets it start early.
-template <typename Kernel>
-int launch_places(const char* name, Kernel kernel, PerDevice& allowed, int threads, int ctas, bool early, const dsa::RouteParams& p,
-                  cudaStream_t st) {
-  if (const int rc = allow_smem(allowed, (const void*)kernel, dsa::counts_bytes(threads / 32, dsa::kRouteMaxExperts))) return rc;
-  if (ctas > 8) {
-    static PerDevice wide;
-    const cudaError_t rc = wide.once([&] { return cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1); });
-    if (rc != cudaSuccess) return fail(DSA_ERR_CUDA, "%s: %s", name, cudaGetErrorString(rc));
-  }
-  cudaLaunchConfig_t c{};
-  cudaLaunchAttribute a[2];
-  a[0].id = cudaLaunchAttributeClusterDimension;
-  a[0].val.clusterDim.x = ctas, a[0].val.clusterDim.y = 1, a[0].val.clusterDim.z = 1;
-  a[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  a[1].val.programmaticStreamSerializationAllowed = 1;
-  c.gridDim = dim3(ctas), c.blockDim = dim3(threads), c.dynamicSmemBytes = dsa::counts_bytes(threads / 32, p.E);
-  c.stream = st, c.attrs = a, c.numAttrs = early ? 2 : 1;
-  const cudaError_t e = cudaLaunchKernelEx(&c, kernel, p);
-  if (e != cudaSuccess) return fail(DSA_ERR_CUDA, "%s: %s", name, cudaGetErrorString(e));
-  return check_launch(name);
+  // Many rows to a group, or many tiles: pairs of CTAs; else tiles of 64 or 128 rows and as many CTAs as share their K.
+  enum { kFew64, kWide64, kFew128, kMany } way;
+  const int sms = sm_count();
+  const int64_t columns = (p.width + 127) / 128, few = row_tiles(p.M, groups, 64) * columns, some = row_tiles(p.M, groups, 128) * columns;
+  if (p.M <= 64 * groups) way = !p.gated && few > 2 * sms ? kWide64 : kFew64;
+  else if (4 * few <= sms) way = kFew64;
+  else if (2 * some <= sms) way = kFew128;
+  else way = kMany;
+  const auto go = [&](auto is8) {
+    constexpr bool FP8 = decltype(is8)::value;
+    if (p.gated)
+      return way == kMany ? launch_many<FP8, true>(p, groups, st)
+             : way == kFew128 ? launch_few<FP8, true, false, 128>(p, groups, st) : launch_few<FP8, true, false, 64>(p, groups, st);
+    if (way == kMany) return launch_many<FP8, false>(p, groups, st);
+    if (way == kFew128) return launch_few<FP8, false, false, 128>(p, groups, st);
+    return way == kWide64 ? launch_few<FP8, false, true, 64>(p, groups, st) : launch_few<FP8, false, false, 64>(p, groups, st);
+  };
+  return fp8 ? go(std::true_type{}) : go(std::false_type{});
 }
 
 template <int V, typename T>
 int launch_route(const dsa::RouteParams& p, cudaStream_t st) {
-  static PerDevice few, many;
+  static PerDevice few, many, wide;
   constexpr int kWarps = dsa::kFewThreads / 32;
   if (p.T <= kWarps * dsa::kFewCtas) {
     int ctas = 1;
     while (ctas * kWarps < p.T) ctas *= 2;
-    if (const int rc = launch_places("route_few_kernel", dsa::route_few_kernel<V, T>, few, dsa::kFewThreads, ctas, false, p, st)) return rc;
+    const auto kernel = dsa::route_few_kernel<V, T>;
+    if (const int rc = allow_smem(few, (const void*)kernel, dsa::counts_bytes(kWarps, dsa::kRouteMaxExperts))) return rc;
     set_last_launches(1);
-    return DSA_OK;
+    return launch("route_few_kernel", kernel, ctas, dsa::kFewThreads, ctas, dsa::counts_bytes(kWarps, p.E), st, p);
   }
   const unsigned grid = (unsigned)(((int64_t)p.T * 32 + dsa::kRouteThreads - 1) / dsa::kRouteThreads);
-  dsa::route_choose_kernel<V, T><<<grid, dsa::kRouteThreads, 0, st>>>(p);
-  if (const int rc = check_launch("route_choose_kernel")) return rc;
-  if (const int rc = launch_places("route_place_kernel", dsa::route_place_kernel, many, dsa::kPlaceThreads, dsa::kPlaceCtas, true, p, st)) return rc;
+  if (const int rc = launch("route_choose_kernel", dsa::route_choose_kernel<V, T>, grid, dsa::kRouteThreads, 1, 0, st, p)) return rc;
+  const auto kernel = dsa::route_place_kernel;
+  constexpr int kPlaceWarps = dsa::kPlaceThreads / 32;
+  if (const int rc = allow_smem(many, (const void*)kernel, dsa::counts_bytes(kPlaceWarps, dsa::kRouteMaxExperts))) return rc;
+  const cudaError_t e = wide.once([&] { return cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1); });
+  if (e != cudaSuccess) return fail(DSA_ERR_CUDA, "route_place_kernel: %s", cudaGetErrorString(e));
   set_last_launches(2);
-  return DSA_OK;
+  return launch("route_place_kernel", kernel, dsa::kPlaceCtas, dsa::kPlaceThreads, dsa::kPlaceCtas, dsa::counts_bytes(kPlaceWarps, p.E), st, p);
 }
 
 template <int V>
@@ -200,10 +209,10 @@ int launch_route(const dsa::RouteParams& p, int type, cudaStream_t st) {
 }
 
 template <typename T>
-void launch_combine(const dsa::CombineParams& p, bool vec, cudaStream_t st) {
-  const int block = std::min(256, (p.N / 8 + 31) / 32 * 32 + 32);
-  if (vec) dsa::combine_kernel<T, true><<<p.T, block, 0, st>>>(p);
-  else dsa::combine_kernel<T, false><<<p.T, block, 0, st>>>(p);
+int launch_combine(const dsa::CombineParams& p, bool vec, cudaStream_t st) {
+  const unsigned slices = (unsigned)std::min(65535, (p.N + dsa::kCombineThreads * 8 - 1) / (dsa::kCombineThreads * 8));
+  set_last_launches(1);
+  return launch("combine_kernel", vec ? dsa::combine_kernel<T, true> : dsa::combine_kernel<T, false>, dim3(p.T, slices), dsa::kCombineThreads, 1, 0, st, p);
 }
 
 }  // namespace
@@ -314,11 +323,9 @@ int dsa_combine_experts(const void* y, int64_t y_stride, int type, int M, const 
   };
   const bool vec = N % 8 == 0 && row16(y, y_stride, M) && row16(add, add_stride, T) && row16(out, out_stride, T);
   const cudaStream_t st = (cudaStream_t)stream;
-  if (type == DSA_TYPE_BF16) launch_combine<__nv_bfloat16>(p, vec, st);
-  else if (type == DSA_TYPE_FP16) launch_combine<__half>(p, vec, st);
-  else launch_combine<float>(p, vec, st);
-  set_last_launches(1);
-  return check_launch("combine_kernel");
+  if (type == DSA_TYPE_BF16) return launch_combine<__nv_bfloat16>(p, vec, st);
+  if (type == DSA_TYPE_FP16) return launch_combine<__half>(p, vec, st);
+  return launch_combine<float>(p, vec, st);
 }
 
 }  // extern "C"

@@ -36,7 +36,7 @@ struct MatmulParams {
   int32_t* status;
   int64_t x_stride, w_stride, w_group, out_stride;  // elements
   int x_rows, M, N, K, E, width, kb, nb;            // width: N, or N / 2 where gated
-  int x_type, out_type, most_tiles;                 // row tiles that there can be
+  int x_type, out_type, most_tiles, box;            // row tiles that there can be, rows of a load
   bool gated, give_up;
 };
 
@@ -216,17 +216,18 @@ __device__ __forceinline__ void store4(const MatmulParams& p, int64_t row, int n
 }
 
 // ---------------------------------------------------------------- few rows to a group
-// Tiles of BM rows and 128 results.  A cluster's CTAs share a tile's K in equal parts, each part a stream of its own from
+// Tiles of BM rows and 128 results (WIDE: 256).  A cluster's CTAs share a tile's K in equal parts, each part a stream of its own from
 // HBM, and join their sums through each other's shared memory in rank order.
-template <bool FP8, bool GATED, int BM>
+template <bool FP8, bool GATED, bool WIDE, int BM>
 struct FewCfg {
-  static constexpr int kOut = 128;               // results of a tile
-  static constexpr int BN = GATED ? 256 : 128;   // its weight rows: gated 64 gates, their 64 partners, and so again
-  static constexpr int kBox = GATED ? 64 : 128;  // weight rows of a load
-  static constexpr int kHalf = BN / 2;           // columns of an epilogue warpgroup
+  static_assert(!(GATED && WIDE));
+  static constexpr int kOut = WIDE ? 256 : 128;         // results of a tile
+  static constexpr int BN = GATED || WIDE ? 256 : 128;  // its weight rows: gated 64 gates, their 64 partners, and so again
+  static constexpr int kBox = GATED ? 64 : 128;         // weight rows of a load
+  static constexpr int kHalf = BN / 2;                  // columns of an epilogue warpgroup
   static constexpr int kK = FP8 ? 128 : 64;      // elements of K in a stage: 128 bytes
   static constexpr int kStageA = BM * 128, kStageB = BN * 128, kStage = kStageA + kStageB;
-  static constexpr int kRound = GATED ? 32 : 64;     // rows joined at a time
+  static constexpr int kRound = BN == 256 ? 32 : 64;  // rows joined at a time
   static constexpr int kStride = (BN + 4) * 4;       // bytes between their sums; the fifth float from the end tells a bad row
   static constexpr int kJoin = kRound * kStride;
   static constexpr int kTable = (3 * kMatmulMaxGroups + 4) * 4;
@@ -237,10 +238,10 @@ struct FewCfg {
   static_assert(kStages >= 3 && kSmem <= 232448);
 };
 
-template <bool FP8, bool GATED, int BM>
+template <bool FP8, bool GATED, bool WIDE, int BM>
 __global__ void __launch_bounds__(kMatmulThreads, 1)
 few_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tw, const __grid_constant__ MatmulParams p) {
-  using C = FewCfg<FP8, GATED, BM>;
+  using C = FewCfg<FP8, GATED, WIDE, BM>;
   extern __shared__ uint8_t raw[];
   const uint32_t stages = (smem_u32(raw) + 1023u) & ~1023u;
   uint8_t* const base = raw + (stages - smem_u32(raw));
@@ -268,11 +269,13 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
     tma_prefetch_desc(&tx);
     tma_prefetch_desc(&tw);
   }
-  load_groups<BM>(p, groups);
   if (warp == 9) {
     tmem_alloc(tmem_holder, 512);
     tmem_relinquish();
   }
+  pdl_launch_dependents();
+  pdl_wait();
+  load_groups<BM>(p, groups);
   __syncthreads();
   if (warp == 8) count_tiles<BM>(p.E, p.most_tiles, groups);
   tc_fence_before();
@@ -315,8 +318,8 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
       for (int i = 0; i < C::kHalf / 2; ++i) acc[i] = 0;
       if (FP8) {
         const float* const xs = p.x_scales + (int64_t)src * p.kb;
-        const int n0 = GATED ? tile.column + 64 * half : tile.column;
-        const float* const ws = p.w_scales + ((int64_t)tile.e * p.nb + n0 / kMatmulBlock) * p.kb;
+        const int n0 = GATED ? tile.column + 64 * half : WIDE ? tile.column + 128 * half : tile.column;
+        const float* const ws = p.w_scales + ((int64_t)tile.e * p.nb + min(p.nb - 1, n0 / kMatmulBlock)) * p.kb;
         const float* const wu = p.w_scales + ((int64_t)tile.e * p.nb + min(p.nb - 1, (p.width + n0) / kMatmulBlock)) * p.kb;
         // (a block's scales are loaded while the block before is summed)
         float s_next = ld_ahead(xs + k0), g_next = ld_ahead(ws + k0), u_next = GATED ? ld_ahead(wu + k0) : 0.f;
@@ -366,18 +369,8 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
         on = __all_sync(~0u, mbar_wait_cluster(join_full, joined & 1, abort_flag));
         if (!on) break;
         const int rows = min(C::kRound, tile.count - r0);
-        for (int r = (int)rank * 8 + warp; r < rows; r += 8 * S) {
-          const uint32_t at = join + r * C::kStride + 16 * lane;
-          float4 a = make_float4(0.f, 0.f, 0.f, 0.f), u = a;
-          for (uint32_t o = 0; o < S; ++o) {
-            const uint32_t there = S > 1 ? map_to(at, o) : at;
-            const float4 v = ld_cluster_v4(there);
-            a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
-            if (GATED) {
-              const float4 w = ld_cluster_v4(there + 512);
-              u.x += w.x, u.y += w.y, u.z += w.z, u.w += w.w;
-            }
-          }
+        // a row's 128 results, four to a lane, from its sums (upper: those of what they gate, or the next 128 results)
+        const auto finish = [&](int r, float4 a, float4 u) {
           float y[4] = {a.x, a.y, a.z, a.w};
           if (GATED) y[0] = gate(a.x, u.x), y[1] = gate(a.y, u.y), y[2] = gate(a.z, u.z), y[3] = gate(a.w, u.w);
           const int64_t to = (int64_t)tile.row + r0 + r;
@@ -388,7 +381,14 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
             if (no_row || n + i >= p.width) y[i] = 0.f;
           if (p.out) {
             store4(p, to, n, y, vec);
-            continue;
+            if (WIDE) {
+              float z[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (no_row) z[i] = 0.f;
+              store4(p, to, n + 128, z, vec);
+            }
+            return;
           }
           float amax = fmaxf(fmaxf(fabsf(y[0]), fabsf(y[1])), fmaxf(fabsf(y[2]), fabsf(y[3])));
 #pragma unroll
@@ -405,6 +405,43 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
               if (n + i < p.width) dst[i] = (uint8_t)(codes >> (8 * i));
           }
           if (lane == 0) p.scales[to * ((p.width + 127) / 128) + tile.column / 128] = s;
+        };
+        if (S == 1) {
+          // (four rows are read before the first is finished)
+          for (int r = warp; r < rows; r += 32) {
+            float4 a[4], u[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t at = join + min(r + 8 * j, C::kRound - 1) * C::kStride + 16 * lane;
+              const uint4 v = lds_v4(at), w = C::BN == 256 ? lds_v4(at + 512) : make_uint4(0, 0, 0, 0);
+              a[j] = make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
+              u[j] = make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w));
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (r + 8 * j < rows) finish(r + 8 * j, a[j], u[j]);
+          }
+        } else {
+          for (int r = (int)rank * 8 + warp; r < rows; r += 8 * S) {
+            const uint32_t at = join + r * C::kStride + 16 * lane;
+            float4 part[8], upper[8];  // (all parts are asked for before the first is added)
+#pragma unroll
+            for (uint32_t o = 0; o < 8; ++o) {
+              part[o] = upper[o] = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (o < S) {
+                const uint32_t there = map_to(at, o);
+                part[o] = ld_cluster_v4(there);
+                if (C::BN == 256) upper[o] = ld_cluster_v4(there + 512);
+              }
+            }
+            float4 a = part[0], u = upper[0];
+#pragma unroll
+            for (uint32_t o = 1; o < 8; ++o) {
+              a.x += part[o].x, a.y += part[o].y, a.z += part[o].z, a.w += part[o].w;
+              u.x += upper[o].x, u.y += upper[o].y, u.z += upper[o].z, u.w += upper[o].w;
+            }
+            finish(r, a, u);
+          }
         }
         __syncwarp();
         if (lane < S) mbar_arrive_cluster(map_to(join_free, lane));
@@ -421,8 +458,8 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
       bool on = !p.give_up;
       if (!on) quit();
       for (int t = blockIdx.x / S; on && find_tile<BM, C::kOut>(p, groups, t, &tile); t += step) {
-        const int boxes = p.rows ? 0 : (tile.count + 31) / 32;
-        const uint32_t bytes = C::kStageB + boxes * 4096;
+        const int boxes = p.rows ? 0 : (tile.count + p.box - 1) / p.box;
+        const uint32_t bytes = C::kStageB + boxes * p.box * 128;
         for (int k = k0; k < k1; ++k) {
           if (!__all_sync(~0u, mbar_wait(empty(s), phase ^ 1, abort_flag))) {
             on = false;
@@ -430,16 +467,16 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
           }
           const uint32_t a = stages + s * C::kStage, b = a + C::kStageA;
           const int x = k * C::kK;
-          if (lane == 0) {
+          if (elect_one()) {
             mbar_arrive_expect_tx(full(s), bytes);
-  #pragma unroll
+#pragma unroll
             for (int i = 0; i < C::BN / C::kBox; ++i) {
-              const int n = GATED ? tile.column + 64 * (i >> 1) + (i & 1) * p.width : tile.column;
+              const int n = GATED ? tile.column + 64 * (i >> 1) + (i & 1) * p.width : tile.column + 128 * i;
               tma_load_3d(b + i * C::kBox * 128, &tw, x, n, tile.e, full(s));
             }
+            for (int i = 0; i < boxes; ++i) tma_load_2d(a + i * p.box * 128, &tx, x, tile.row + p.box * i, full(s));
           }
           __syncwarp();
-          if (lane < boxes) tma_load_2d(a + lane * 4096, &tx, x, tile.row + 32 * lane, full(s));
           used |= 1u << s;
           if (++s == C::kStages) s = 0, phase ^= 1;
         }
@@ -452,36 +489,36 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
       }
     } else if (warp == 9) {
       // ------------------------------------------------ products
-      if (lane == 0) {
-        const uint32_t idesc = FP8 ? idesc_e4m3_f32(128, C::BN) : idesc_16_f32(p.x_type == 0, 128, C::BN, false);
-        int s = 0, phase = 0, buffer = 0, turn = 0;
-        bool on = true;
-        for (int t = blockIdx.x / S; on && find_tile<BM, C::kOut>(p, groups, t, &tile); t += step) {
-          for (int k = k0; k < k1; ++k) {
-            if (FP8 || k == k0) on = mbar_wait(acc_empty(buffer), turn ^ 1, abort_flag);
-            on = on && mbar_wait(full(s), phase, abort_flag);
-            if (!on) break;
-            if (p.rows) fence_proxy_async_smem();
-            tc_fence_after();
-            const uint32_t a = stages + s * C::kStage, d = tmem + buffer * C::BN;
-            if (FP8) umma_f8_k128(d, sw128_desc(a), sw128_desc(a + C::kStageA), idesc, 0, 4);
-            else umma_f16_k64(d, sw128_desc(a), sw128_desc(a + C::kStageA), idesc, k > k0, 4);
+      const uint32_t idesc = FP8 ? idesc_e4m3_f32(128, C::BN) : idesc_16_f32(p.x_type == 0, 128, C::BN, false);
+      int s = 0, phase = 0, buffer = 0, turn = 0;
+      bool on = true;
+      for (int t = blockIdx.x / S; on && find_tile<BM, C::kOut>(p, groups, t, &tile); t += step) {
+        for (int k = k0; k < k1; ++k) {
+          if (FP8 || k == k0) on = __all_sync(~0u, mbar_wait(acc_empty(buffer), turn ^ 1, abort_flag));
+          on = on && __all_sync(~0u, mbar_wait(full(s), phase, abort_flag));
+          if (!on) break;
+          if (p.rows) fence_proxy_async_smem();
+          tc_fence_after();
+          const uint32_t a = stages + s * C::kStage, d = tmem + buffer * C::BN;
+          if (elect_one()) {
+            if (FP8) umma_f8_k128_all(d, sw128_desc(a), sw128_desc(a + C::kStageA), idesc, 0);
+            else umma_f16_k64_all(d, sw128_desc(a), sw128_desc(a + C::kStageA), idesc, k > k0);
             umma_commit(empty(s));
-            if (FP8 || k + 1 == k1) {
-              umma_commit(acc_full(buffer));
-              if (++buffer == C::kBuffers) buffer = 0, turn ^= 1;
-            }
-            if (++s == C::kStages) s = 0, phase ^= 1;
+            if (FP8 || k + 1 == k1) umma_commit(acc_full(buffer));
           }
-        }
-        if (!on) {
-          quit();
-          // products under way end before the CTA does: their last commit is that of the stage before
-          const int last = s == 0 ? C::kStages - 1 : s - 1;
-          mbar_wait(empty(last), s == 0 ? phase ^ 1 : phase, nullptr);
+          __syncwarp();
+          if (FP8 || k + 1 == k1) {
+            if (++buffer == C::kBuffers) buffer = 0, turn ^= 1;
+          }
+          if (++s == C::kStages) s = 0, phase ^= 1;
         }
       }
-      __syncwarp();
+      if (!on) {
+        quit();
+        // products under way end before the CTA does: their last commit is that of the stage before
+        const int last = s == 0 ? C::kStages - 1 : s - 1;
+        mbar_wait(empty(last), s == 0 ? phase ^ 1 : phase, nullptr);
+      }
     } else if (p.rows) {
       // ------------------------------------------------ gathered rows
       const int g = warp - 10;
@@ -516,19 +553,39 @@ struct ManyCfg {
   static_assert(kStages >= 6 && kStages <= 8);
 };
 
-// 64 bytes of each of a warp's 32 rows, a row to a lane, out by way of shared memory so that four lanes write a row's
-// piece: `rows` rows at `to`, `stride` bytes apart, of which the first `bytes` are wanted.  16-byte aligned.
+// 64 bytes of each of a warp's 32 rows, a row to a lane, out by way of shared memory so that neighbouring lanes write a row's
+// piece: `rows` rows at `to`, `stride` bytes apart, of which the first `bytes` are wanted.  VEC: both multiples of 16, four
+// lanes a row; otherwise elements of SIZE bytes.
+template <bool VEC, int SIZE>
 __device__ __forceinline__ void store_piece(uint32_t stage, uint8_t* to, int64_t stride, int rows, int bytes, const uint32_t* v) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int i = 0; i < 4; ++i) sts_v4(stage + lane * 80 + 16 * i, make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
   __syncwarp();
-  const int at = (lane & 3) * 16;
+  if constexpr (VEC) {
+    const int at = (lane & 3) * 16;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = 8 * i + (lane >> 2);
-    const uint4 w = lds_v4(stage + r * 80 + at);
-    if (r < rows && at < bytes) *reinterpret_cast<uint4*>(to + r * stride + at) = w;
+    for (int i = 0; i < 4; ++i) {
+      const int r = 8 * i + (lane >> 2);
+      const uint4 w = lds_v4(stage + r * 80 + at);
+      if (r < rows && at < bytes) *reinterpret_cast<uint4*>(to + r * stride + at) = w;
+    }
+  } else {
+    const int at = (lane & 15) * 4;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int r = 2 * i + (lane >> 4);
+      const uint32_t w = lds_u32(stage + r * 80 + at);
+      if (r >= rows) continue;
+      uint8_t* const dst = to + r * stride + at;
+#pragma unroll
+      for (int j = 0; j < 4 / SIZE; ++j) {
+        if (at + j * SIZE >= bytes) break;
+        if constexpr (SIZE == 4) *reinterpret_cast<uint32_t*>(dst) = w;
+        else if constexpr (SIZE == 2) *reinterpret_cast<uint16_t*>(dst + 2 * j) = (uint16_t)(w >> (16 * j));
+        else dst[j] = (uint8_t)(w >> (8 * j));
+      }
+    }
   }
   __syncwarp();
 }
@@ -564,11 +621,13 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__
     tma_prefetch_desc(&tx);
     tma_prefetch_desc(&tw);
   }
-  load_groups<C::BM>(p, groups);
   if (warp == 9) {
     tmem_alloc_pair(tmem_holder, 512);
     tmem_relinquish_pair();
   }
+  pdl_launch_dependents();
+  pdl_wait();
+  load_groups<C::BM>(p, groups);
   __syncthreads();
   if (warp == 8) count_tiles<C::BM>(p.E, p.most_tiles, groups);
   tc_fence_before();
@@ -687,50 +746,40 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__
         }
         if (rows > 0 && n < p.width) {
           uint8_t* const to = p.codes + row0 * p.width + n;
-          if (vec) {
-            store_piece(stage, to, p.width, rows, p.width - n, codes);
-          } else if (lane < rows) {
-#pragma unroll
-            for (int i = 0; i < 64; ++i)
-              if (n + i < p.width) to[(int64_t)lane * p.width + i] = (uint8_t)(codes[i / 4] >> (8 * (i & 3)));
-          }
+          if (vec) store_piece<true, 1>(stage, to, p.width, rows, p.width - n, codes);
+          else store_piece<false, 1>(stage, to, p.width, rows, p.width - n, codes);
           if (half == 0 && lane < rows) p.scales[(row0 + lane) * ((p.width + 127) / 128) + tile.column / 128] = s;
         }
       } else if (rows > 0) {
         // pieces of 64 bytes: 32 results of 16 bits, or 16 of 32
         const int wanted = min(kMine, p.width - n);
         uint8_t* const to = static_cast<uint8_t*>(p.out) + (row0 * p.out_stride + n) * size;
-        if (vec && wanted * size % 16 == 0) {
-          if (size == 2) {
+        const bool whole = vec && wanted * size % 16 == 0;
+        if (size == 2) {
 #pragma unroll
-            for (int c = 0; c < kMine / 32; ++c) {
-              uint32_t v[16];
+          for (int c = 0; c < kMine / 32; ++c) {
+            uint32_t v[16];
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const float2 y = unpack2(acc[16 * c + i]);
-                v[i] = round_pair(y.x, y.y, p.out_type == 0);
-              }
-              if (32 * c < wanted) store_piece(stage, to + 64 * c, p.out_stride * 2, rows, (wanted - 32 * c) * 2, v);
+            for (int i = 0; i < 16; ++i) {
+              const float2 y = unpack2(acc[16 * c + i]);
+              v[i] = round_pair(y.x, y.y, p.out_type == 0);
             }
-          } else {
-#pragma unroll
-            for (int c = 0; c < kMine / 16; ++c) {
-              uint32_t v[16];
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float2 y = unpack2(acc[8 * c + i]);
-                v[2 * i] = __float_as_uint(y.x), v[2 * i + 1] = __float_as_uint(y.y);
-              }
-              if (16 * c < wanted) store_piece(stage, to + 64 * c, p.out_stride * 4, rows, (wanted - 16 * c) * 4, v);
-            }
+            if (32 * c >= wanted) continue;
+            if (whole) store_piece<true, 2>(stage, to + 64 * c, p.out_stride * 2, rows, (wanted - 32 * c) * 2, v);
+            else store_piece<false, 2>(stage, to + 64 * c, p.out_stride * 2, rows, (wanted - 32 * c) * 2, v);
           }
-        } else if (lane < rows) {
+        } else {
 #pragma unroll
-          for (int i = 0; i < kMine / 2; ++i) {
-            const float2 y = unpack2(acc[i]);
-            const int64_t at = (row0 + lane) * p.out_stride + n + 2 * i;
-            if (2 * i < wanted) store_element(p.out, at, p.out_type, y.x);
-            if (2 * i + 1 < wanted) store_element(p.out, at + 1, p.out_type, y.y);
+          for (int c = 0; c < kMine / 16; ++c) {
+            uint32_t v[16];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float2 y = unpack2(acc[8 * c + i]);
+              v[2 * i] = __float_as_uint(y.x), v[2 * i + 1] = __float_as_uint(y.y);
+            }
+            if (16 * c >= wanted) continue;
+            if (whole) store_piece<true, 4>(stage, to + 64 * c, p.out_stride * 4, rows, (wanted - 16 * c) * 4, v);
+            else store_piece<false, 4>(stage, to + 64 * c, p.out_stride * 4, rows, (wanted - 16 * c) * 4, v);
           }
         }
       }
@@ -745,10 +794,9 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__
       uint32_t used = 0;  // stages that were ever filled
       bool on = !p.give_up;
       for (int t = blockIdx.x / 2; on && find_tile<C::BM, C::kOut>(p, groups, t, &tile); t += step) {
-        // boxes of 32 rows of each CTA
-        const int boxes0 = p.rows ? 0 : (min(128, tile.count) + 31) / 32, boxes1 = p.rows ? 0 : (max(0, tile.count - 128) + 31) / 32;
-        const int boxes = rank ? boxes1 : boxes0, first = tile.row + 128 * (int)rank;
-        const uint32_t bytes = 2 * C::kStageB + (boxes0 + boxes1) * 4096;
+        // a box of 128 rows for each CTA that has some
+        const bool second = tile.count > 128, boxed = !p.rows && (rank == 0 || second);
+        const uint32_t bytes = 2 * C::kStageB + (p.rows ? 0 : second ? 2 : 1) * C::kStageA;
         for (int k = 0; k < blocks; ++k) {
           if (!__all_sync(~0u, mbar_wait(empty(s), phase ^ 1, abort_flag))) {
             on = false;
@@ -756,7 +804,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__
           }
           const uint32_t a = stages + s * C::kStage, b = a + C::kStageA, bar = map_to(full(s), 0);
           const int x = k * C::kK;
-          if (lane == 0) {
+          if (elect_one()) {
             if (rank == 0) mbar_arrive_expect_tx(full(s), bytes);
             if (GATED) {
               tma_load_3d_pair(b, &tw, x, tile.column + 64 * (int)rank, tile.e, bar);
@@ -764,9 +812,9 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__
             } else {
               tma_load_3d_pair(b, &tw, x, tile.column + 128 * (int)rank, tile.e, bar);
             }
+            if (boxed) tma_load_2d_pair(a, &tx, x, tile.row + 128 * (int)rank, bar);
           }
           __syncwarp();
-          if (lane < boxes) tma_load_2d_pair(a + lane * 4096, &tx, x, first + 32 * lane, bar);
           used |= 1u << s;
           if (++s == C::kStages) s = 0, phase ^= 1;
         }
@@ -779,36 +827,36 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__
       }
     } else if (warp == 9 && rank == 0) {
       // ------------------------------------------------ products of both CTAs
-      if (lane == 0) {
-        const uint32_t idesc = FP8 ? idesc_e4m3_f32(256, 256) : idesc_16_f32(p.x_type == 0, 256, 256, false);
-        int s = 0, phase = 0, buffer = 0, turn = 0;
-        bool on = true;
-        for (int t = blockIdx.x / 2; on && find_tile<C::BM, C::kOut>(p, groups, t, &tile); t += step) {
-          for (int k = 0; k < blocks; ++k) {
-            if (FP8 || k == 0) on = mbar_wait(acc_empty(buffer), turn ^ 1, abort_flag);
-            on = on && mbar_wait(full(s), phase, abort_flag);
-            if (!on) break;
-            if (p.rows) fence_proxy_async_smem();
-            tc_fence_after();
-            const uint32_t a = stages + s * C::kStage, d = tmem + buffer * 256;
+      const uint32_t idesc = FP8 ? idesc_e4m3_f32(256, 256) : idesc_16_f32(p.x_type == 0, 256, 256, false);
+      int s = 0, phase = 0, buffer = 0, turn = 0;
+      bool on = true;
+      for (int t = blockIdx.x / 2; on && find_tile<C::BM, C::kOut>(p, groups, t, &tile); t += step) {
+        for (int k = 0; k < blocks; ++k) {
+          if (FP8 || k == 0) on = __all_sync(~0u, mbar_wait(acc_empty(buffer), turn ^ 1, abort_flag));
+          on = on && __all_sync(~0u, mbar_wait(full(s), phase, abort_flag));
+          if (!on) break;
+          if (p.rows) fence_proxy_async_smem();
+          tc_fence_after();
+          const uint32_t a = stages + s * C::kStage, d = tmem + buffer * 256;
+          if (elect_one()) {
             if (FP8) umma_f8_k128_pair(d, sw128_desc(a), sw128_desc(a + C::kStageA), idesc, 0);
             else umma_f16_k64_pair(d, sw128_desc(a), sw128_desc(a + C::kStageA), idesc, k > 0);
             umma_commit_pair(empty(s));
-            if (FP8 || k + 1 == blocks) {
-              umma_commit_pair(acc_full(buffer));
-              if (++buffer == 2) buffer = 0, turn ^= 1;
-            }
-            if (++s == C::kStages) s = 0, phase ^= 1;
+            if (FP8 || k + 1 == blocks) umma_commit_pair(acc_full(buffer));
           }
-        }
-        if (!on) {
-          quit();
-          // products under way end before the CTAs do: their last commit is that of the stage before
-          const int last = s == 0 ? C::kStages - 1 : s - 1;
-          mbar_wait(empty(last), s == 0 ? phase ^ 1 : phase, nullptr);
+          __syncwarp();
+          if (FP8 || k + 1 == blocks) {
+            if (++buffer == 2) buffer = 0, turn ^= 1;
+          }
+          if (++s == C::kStages) s = 0, phase ^= 1;
         }
       }
-      __syncwarp();
+      if (!on) {
+        quit();
+        // products under way end before the CTAs do: their last commit is that of the stage before
+        const int last = s == 0 ? C::kStages - 1 : s - 1;
+        mbar_wait(empty(last), s == 0 ? phase ^ 1 : phase, nullptr);
+      }
     } else if (warp == 9 && p.rows) {
       // ------------------------------------------------ the second CTA's gathered rows, told to the first
       if (lane == 0) {

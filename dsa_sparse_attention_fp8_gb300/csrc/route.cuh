@@ -446,6 +446,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_choose_kernel(const __gri
   const int t = (int)((blockIdx.x * (unsigned)kRouteThreads + threadIdx.x) >> 5);
   __shared__ alignas(8) int list[kRouteThreads / 32][64];
   pdl_launch_dependents();
+  pdl_wait();
   if (t < p.T) choose_token<V, T>(p, t, real_tokens(p), threadIdx.x & 31, list[threadIdx.x >> 5]);
 }
 
@@ -524,6 +525,7 @@ __global__ void __launch_bounds__(kPlaceThreads) route_place_kernel(const __grid
   int* const mine = c.warp + warp * p.E;
   for (int i = lane; i < p.E; i += 32) mine[i] = 0;
   __syncwarp();
+  pdl_launch_dependents();
   pdl_wait();
   // a lane's choice among the warp's tokens, several tokens loaded at a time
   constexpr int kAhead = 16;
@@ -572,6 +574,8 @@ __global__ void __launch_bounds__(kFewThreads) route_few_kernel(const __grid_con
   int* const mine = c.warp + warp * p.E;
   for (int i = lane; i < p.E; i += 32) mine[i] = 0;
   __syncwarp();
+  pdl_launch_dependents();
+  pdl_wait();
   const int warps = (int)ctas * W, each = (p.T + warps - 1) / warps;
   const int first = ((int)rank * W + warp) * each, last = min(p.T, first + each);
   const int real = real_tokens(p);
