@@ -79,10 +79,10 @@ int launch(const char* name, void (*kernel)(P...), dim3 grid, int block, int siz
   return check_launch(name);
 }
 
-template <bool FP8, bool GATED, bool WIDE, int BM>
+template <bool FP8, bool GATED, bool WIDE, int BM, int ROUND = GATED || WIDE ? 32 : 64>
 int launch_few(dsa::MatmulParams p, int64_t groups, cudaStream_t st) {
-  using C = dsa::FewCfg<FP8, GATED, WIDE, BM>;
-  const auto kernel = dsa::few_rows_kernel<FP8, GATED, WIDE, BM>;
+  using C = dsa::FewCfg<FP8, GATED, WIDE, BM, ROUND>;
+  const auto kernel = dsa::few_rows_kernel<FP8, GATED, WIDE, BM, ROUND>;
   static PerDevice allowed;
   static ClusterCount resident;
   if (const int rc = allow_smem(allowed, (const void*)kernel, C::kSmem)) return rc;
@@ -170,7 +170,8 @@ int run_matmul(dsa::MatmulParams p, int64_t groups, cudaStream_t st) {
     constexpr bool FP8 = decltype(is8)::value;
     if (p.gated)
       return way == kMany ? launch_many<FP8, true>(p, groups, st)
-             : way == kFew128 ? launch_few<FP8, true, false, 128>(p, groups, st) : launch_few<FP8, true, false, 64>(p, groups, st);
+             : way == kFew128 ? launch_few<FP8, true, false, 128>(p, groups, st)
+             : 2 * few <= sms ? launch_few<FP8, true, false, 64, 64>(p, groups, st) : launch_few<FP8, true, false, 64>(p, groups, st);
     if (way == kMany) return launch_many<FP8, false>(p, groups, st);
     if (way == kFew128) return launch_few<FP8, false, false, 128>(p, groups, st);
     return way == kWide64 ? launch_few<FP8, false, true, 64>(p, groups, st) : launch_few<FP8, false, false, 64>(p, groups, st);

@@ -218,7 +218,7 @@ __device__ __forceinline__ void store4(const MatmulParams& p, int64_t row, int n
 // ---------------------------------------------------------------- few rows to a group
 // Tiles of BM rows and 128 results (WIDE: 256).  A cluster's CTAs share a tile's K in equal parts, each part a stream of its own from
 // HBM, and join their sums through each other's shared memory in rank order.
-template <bool FP8, bool GATED, bool WIDE, int BM>
+template <bool FP8, bool GATED, bool WIDE, int BM, int ROUND>
 struct FewCfg {
   static_assert(!(GATED && WIDE));
   static constexpr int kOut = WIDE ? 256 : 128;         // results of a tile
@@ -227,7 +227,7 @@ struct FewCfg {
   static constexpr int kHalf = BN / 2;                  // columns of an epilogue warpgroup
   static constexpr int kK = FP8 ? 128 : 64;      // elements of K in a stage: 128 bytes
   static constexpr int kStageA = BM * 128, kStageB = BN * 128, kStage = kStageA + kStageB;
-  static constexpr int kRound = BN == 256 ? 32 : 64;  // rows joined at a time
+  static constexpr int kRound = ROUND;                // rows joined at a time
   static constexpr int kStride = (BN + 4) * 4;       // bytes between their sums; the fifth float from the end tells a bad row
   static constexpr int kJoin = kRound * kStride;
   static constexpr int kTable = (3 * kMatmulMaxGroups + 4) * 4;
@@ -238,10 +238,10 @@ struct FewCfg {
   static_assert(kStages >= 3 && kSmem <= 232448);
 };
 
-template <bool FP8, bool GATED, bool WIDE, int BM>
+template <bool FP8, bool GATED, bool WIDE, int BM, int ROUND>
 __global__ void __launch_bounds__(kMatmulThreads, 1)
 few_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tw, const __grid_constant__ MatmulParams p) {
-  using C = FewCfg<FP8, GATED, WIDE, BM>;
+  using C = FewCfg<FP8, GATED, WIDE, BM, ROUND>;
   extern __shared__ uint8_t raw[];
   const uint32_t stages = (smem_u32(raw) + 1023u) & ~1023u;
   uint8_t* const base = raw + (stages - smem_u32(raw));
@@ -444,7 +444,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
           }
         }
         __syncwarp();
-        if (lane < S) mbar_arrive_cluster(map_to(join_free, lane));
+        if (lane < S) mbar_arrive_remote(map_to(join_free, lane));
         ++joined;
       }
     }
