@@ -79,51 +79,111 @@ int launch(const char* name, void (*kernel)(P...), dim3 grid, int block, int siz
   return check_launch(name);
 }
 
-template <bool FP8, bool GATED, bool WIDE, int BM, int ROUND = GATED || WIDE ? 32 : 64>
-int launch_few(dsa::MatmulParams p, int64_t groups, cudaStream_t st) {
-  using C = dsa::FewCfg<FP8, GATED, WIDE, BM, ROUND>;
-  const auto kernel = dsa::few_rows_kernel<FP8, GATED, WIDE, BM, ROUND>;
-  static PerDevice allowed;
-  static ClusterCount resident;
-  if (const int rc = allow_smem(allowed, (const void*)kernel, C::kSmem)) return rc;
-  CUtensorMap tx, tw;
-  p.box = p.M <= 32 * groups ? 32 : BM;
-  if (const int rc = product_maps(p, p.box, C::kBox, &tx, &tw)) return rc;
-  const int64_t columns = (p.width + C::kOut - 1) / C::kOut;
-  p.most_tiles = (int)row_tiles(p.M, groups, BM);
-  const int64_t tiles = p.most_tiles * columns;
-  if (tiles > INT32_MAX / 2) return fail(DSA_ERR_UNSUPPORTED, "%lld tiles of results", (long long)tiles);
-  // A CTA alone takes 0.28 us for a block of K, whatever it reads from; CTAs that share a tile join its sums in some 0.1 us each.
-  const int blocks = (p.K + C::kK - 1) / C::kK;
-  int size = 1, clusters = 0;
-  double best = 1e30;
-  for (int s = 1; s <= 8 && (s == 1 || (2 * s <= blocks && tiles * s <= sm_count())); ++s) {
-    const int n = resident.get((const void*)kernel, s, dsa::kMatmulThreads, C::kSmem);
-    if (n < 1) continue;
-    const double t = (double)((tiles + n - 1) / n) * ((blocks + s - 1) / s * 0.28 + 0.5 + 0.1 * s);
-    if (t < best) best = t, size = s, clusters = n;
-  }
-  if (clusters < 1) return fail(DSA_ERR_CUDA, "few_rows_kernel does not fit the device");
-  set_last_launches(1);
-  return launch("few_rows_kernel", kernel, (unsigned)(std::min<int64_t>(tiles, clusters) * size), dsa::kMatmulThreads, size, C::kSmem, st, tx, tw, p);
-}
+// How a product's tiles go to CTAs: clusters of `size`, so many of them, and about how long it takes in microseconds.
+struct Plan {
+  double us;
+  int size, clusters;
+};
 
+// Tiles of BM rows, a tile's K shared by a cluster.
+template <bool FP8, bool GATED, bool WIDE, int BM, int ROUND = GATED || WIDE ? 32 : 64>
+struct Few {
+  using C = dsa::FewCfg<FP8, GATED, WIDE, BM, ROUND>;
+  static constexpr auto kKernel = dsa::few_rows_kernel<FP8, GATED, WIDE, BM, ROUND>;
+  static inline PerDevice allowed;
+  static inline ClusterCount resident;
+
+  // A CTA alone takes as long for a block of K wherever it lies, bound by what one SM draws from L2 (measured of one tile of
+  // 7168 elements of K, in L2: 22 us by one CTA, 7.5 by eight).  CTAs that share a tile join their sums, round by round.
+  static constexpr double kBlock = (C::kStageA + C::kStageB) / 110e3 + 0.06, kRoundUs = C::BN == 256 ? 1.8 : 0.8;
+
+  static int plan(const dsa::MatmulParams& p, int64_t groups, Plan* best) {
+    *best = {1e30, 0, 0};
+    if (const int rc = allow_smem(allowed, (const void*)kKernel, C::kSmem)) return rc;
+    const int64_t tiles = row_tiles(p.M, groups, BM) * ((p.width + C::kOut - 1) / C::kOut);
+    const int blocks = (p.K + C::kK - 1) / C::kK, rounds = (std::min(BM, p.M) + ROUND - 1) / ROUND;
+    for (int s = 1; s <= 8 && (s == 1 || (2 * s <= blocks && tiles * s <= sm_count())); ++s) {
+      const int n = resident.get((const void*)kKernel, s, dsa::kMatmulThreads, C::kSmem);
+      if (n < 1) continue;
+      const double us = (double)((tiles + n - 1) / n) * ((blocks + s - 1) / s * kBlock + (s == 1 ? 0.5 : 0.4 + 0.1 * s + rounds * kRoundUs));
+      if (us < best->us) *best = {us, s, n};
+    }
+    return best->clusters ? DSA_OK : fail(DSA_ERR_CUDA, "few_rows_kernel does not fit the device");
+  }
+
+  static int run(dsa::MatmulParams p, int64_t groups, cudaStream_t st) {
+    Plan plan;
+    if (const int rc = Few::plan(p, groups, &plan)) return rc;
+    CUtensorMap tx, tw;
+    p.box = p.M <= 32 * groups ? 32 : BM;
+    if (const int rc = product_maps(p, p.box, C::kBox, &tx, &tw)) return rc;
+    const int64_t rows = row_tiles(p.M, groups, BM), tiles = rows * ((p.width + C::kOut - 1) / C::kOut);
+    if (tiles > INT32_MAX / 2) return fail(DSA_ERR_UNSUPPORTED, "%lld tiles of results", (long long)tiles);
+    p.most_tiles = (int)rows;
+    set_last_launches(1);
+    return launch("few_rows_kernel", kKernel, (unsigned)(std::min<int64_t>(tiles, plan.clusters) * plan.size), dsa::kMatmulThreads, plan.size,
+                  C::kSmem, st, tx, tw, p);
+  }
+};
+
+// Tiles of 256 rows by pairs of CTAs.
 template <bool FP8, bool GATED>
-int launch_many(dsa::MatmulParams p, int64_t groups, cudaStream_t st) {
+struct Many {
   using C = dsa::ManyCfg<FP8, GATED>;
-  const auto kernel = dsa::many_rows_kernel<FP8, GATED>;
-  static PerDevice allowed;
-  static ClusterCount resident;
-  if (const int rc = allow_smem(allowed, (const void*)kernel, C::kSmem)) return rc;
-  CUtensorMap tx, tw;
-  if (const int rc = product_maps(p, 128, C::kBox, &tx, &tw)) return rc;
-  p.most_tiles = (int)row_tiles(p.M, groups, C::BM);
-  const int64_t tiles = p.most_tiles * (int64_t)((p.width + C::kOut - 1) / C::kOut);
-  if (tiles > INT32_MAX / 2) return fail(DSA_ERR_UNSUPPORTED, "%lld tiles of results", (long long)tiles);
-  const int clusters = resident.get((const void*)kernel, 2, dsa::kMatmulThreads, C::kSmem);
-  if (clusters < 1) return fail(DSA_ERR_CUDA, "no pair of CTAs fits the device");
-  set_last_launches(1);
-  return launch("many_rows_kernel", kernel, (unsigned)(std::min<int64_t>(tiles, clusters) * 2), dsa::kMatmulThreads, 2, C::kSmem, st, tx, tw, p);
+  static constexpr auto kKernel = dsa::many_rows_kernel<FP8, GATED>;
+  static inline PerDevice allowed;
+  static inline ClusterCount resident;
+
+  static int plan(const dsa::MatmulParams& p, int64_t groups, Plan* best) {
+    if (const int rc = allow_smem(allowed, (const void*)kKernel, C::kSmem)) return rc;
+    const int n = resident.get((const void*)kKernel, 2, dsa::kMatmulThreads, C::kSmem);
+    if (n < 1) return fail(DSA_ERR_CUDA, "no pair of CTAs fits the device");
+    const int64_t tiles = row_tiles(p.M, groups, C::BM) * ((p.width + C::kOut - 1) / C::kOut);
+    // (8192 rows, K = N = 7168: twelve tiles of 56 blocks to a pair in 300 us)
+    *best = {(double)((tiles + n - 1) / n) * ((p.K + C::kK - 1) / C::kK * 0.43 + 1.0), 2, n};
+    return DSA_OK;
+  }
+
+  static int run(dsa::MatmulParams p, int64_t groups, cudaStream_t st) {
+    Plan plan;
+    if (const int rc = Many::plan(p, groups, &plan)) return rc;
+    CUtensorMap tx, tw;
+    if (const int rc = product_maps(p, 128, C::kBox, &tx, &tw)) return rc;
+    const int64_t rows = row_tiles(p.M, groups, C::BM), tiles = rows * ((p.width + C::kOut - 1) / C::kOut);
+    if (tiles > INT32_MAX / 2) return fail(DSA_ERR_UNSUPPORTED, "%lld tiles of results", (long long)tiles);
+    p.most_tiles = (int)rows;
+    set_last_launches(1);
+    return launch("many_rows_kernel", kKernel, (unsigned)(std::min<int64_t>(tiles, plan.clusters) * 2), dsa::kMatmulThreads, 2, C::kSmem, st, tx, tw, p);
+  }
+};
+
+// The variant for a product's sizes.
+template <bool FP8, bool GATED>
+int run_variant(const dsa::MatmulParams& p, int64_t groups, cudaStream_t st) {
+  using Few64 = Few<FP8, GATED, false, 64>;
+  using Joined64 = Few<FP8, GATED, false, 64, 64>;  // (a gated tile joined in one round, for which it has a stage less)
+  using Wide64 = Few<FP8, false, !GATED, 64>;
+  using Few128 = Few<FP8, GATED, false, 128>;
+  using Pairs = Many<FP8, GATED>;
+  const int64_t tiles = row_tiles(p.M, groups, 64) * ((p.width + 127) / 128);
+  if (groups > 1 && tiles > 2 * sm_count()) {
+    // Bound by the weights' way from HBM.  Tiles fit the rows of a group; 256 weight rows to a tile, so that rows are read less
+    // often (64 groups, K 2048, N 7168, us with 128 / 256 weight rows and by pairs, of 16 rows to a group 199 / 165 / 183, of 32 203 / 170 / 186;
+    // tiles of 128 rows and pairs, of 48 189 / 193, of 96 243 / 206; gated, K 7168, N 4096, tiles of 64 and 128 rows and
+    // pairs, of 32 300 / 304 / 352, of 48 343 / 320 / 374, of 96 486 / 386 / 392, of 128 545 / 491 / 379).
+    if (p.M <= 32 * groups) {
+      if constexpr (GATED) return Few64::run(p, groups, st);
+      else return Wide64::run(p, groups, st);
+    }
+    return p.M <= (GATED ? 96 : 48) * groups ? Few128::run(p, groups, st) : Pairs::run(p, groups, st);
+  }
+  // Few tiles: as the CTAs that share their K take.
+  Plan few, some, many;
+  if (const int rc = Joined64::plan(p, groups, &few)) return rc;
+  if (const int rc = Few128::plan(p, groups, &some)) return rc;
+  if (const int rc = Pairs::plan(p, groups, &many)) return rc;
+  if (many.us < few.us && many.us < some.us) return Pairs::run(p, groups, st);
+  return some.us < few.us ? Few128::run(p, groups, st) : Joined64::run(p, groups, st);
 }
 
 // The checks that both products share, and their launch.  p has the sizes, strides and pointers.
@@ -158,25 +218,8 @@ int run_matmul(dsa::MatmulParams p, int64_t groups, cudaStream_t st) {
   if (!fp8) p.x_scales = p.w_scales = nullptr;
   p.give_up = env_int("DSA_WAIT_LIMIT", (int)dsa::kWaitLimit, 0, (int)dsa::kWaitLimit) == 0;
   if (sm_count() <= 0) return fail(DSA_ERR_CUDA, "no CUDA device");
-  // Many rows to a group, or many tiles: pairs of CTAs; else tiles of 64 or 128 rows and as many CTAs as share their K.
-  enum { kFew64, kWide64, kFew128, kMany } way;
-  const int sms = sm_count();
-  const int64_t columns = (p.width + 127) / 128, few = row_tiles(p.M, groups, 64) * columns, some = row_tiles(p.M, groups, 128) * columns;
-  if (p.M <= 64 * groups) way = !p.gated && few > 2 * sms ? kWide64 : kFew64;
-  else if (4 * few <= sms) way = kFew64;
-  else if (2 * some <= sms) way = kFew128;
-  else way = kMany;
-  const auto go = [&](auto is8) {
-    constexpr bool FP8 = decltype(is8)::value;
-    if (p.gated)
-      return way == kMany ? launch_many<FP8, true>(p, groups, st)
-             : way == kFew128 ? launch_few<FP8, true, false, 128>(p, groups, st)
-             : 2 * few <= sms ? launch_few<FP8, true, false, 64, 64>(p, groups, st) : launch_few<FP8, true, false, 64>(p, groups, st);
-    if (way == kMany) return launch_many<FP8, false>(p, groups, st);
-    if (way == kFew128) return launch_few<FP8, false, false, 128>(p, groups, st);
-    return way == kWide64 ? launch_few<FP8, false, true, 64>(p, groups, st) : launch_few<FP8, false, false, 64>(p, groups, st);
-  };
-  return fp8 ? go(std::true_type{}) : go(std::false_type{});
+  if (fp8) return p.gated ? run_variant<true, true>(p, groups, st) : run_variant<true, false>(p, groups, st);
+  return p.gated ? run_variant<false, true>(p, groups, st) : run_variant<false, false>(p, groups, st);
 }
 
 template <int V, typename T>
