@@ -655,6 +655,7 @@ TYPE_E4M3 = 3
 NORM_GROUP = 128
 _KV_CACHE = struct.Struct("@4P11q3i")   # KvCache's fields
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_Tensor = torch.Tensor
 
 
 def _stream_of(stream, device: int) -> int:
@@ -680,7 +681,7 @@ def _device_of(t: torch.Tensor, name: str) -> int:
 
 def _full(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, device: int) -> int:
     """The address of a contiguous tensor of this dtype and shape on `device`, the current one."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+    if not (isinstance(t, _Tensor) and t.dtype is dtype and t.shape == shape
             and t.get_device() == device and t.is_contiguous()):
         _need(t, name, dtype, shape)
         raise ValueError(f"{name} is not as it should be: {dtype} {shape} on cuda:{device}")
@@ -867,29 +868,25 @@ def add_rms_norm(x: torch.Tensor, residual: Optional[torch.Tensor], weight: torc
 SCORINGS = {"sigmoid": 0, "softmax": 1}
 
 
-def _blocks(n: int) -> int:
-    """128-element groups of n elements."""
-    return -(-n // NORM_GROUP)
-
-
 def _matmul_out(M, N, gated, x, dtype, out, out_codes, out_scales, device, stream):
     """The outputs of a product, checked: what it returns, and the entry point's arguments for them."""
-    if gated and N % 2:
-        raise ValueError(f"gated weights have two halves: {N} rows are odd")
-    width = N // 2 if gated else N
+    if gated:
+        if N % 2:
+            raise ValueError(f"gated weights have two halves: {N} rows are odd")
+        N //= 2
     if out_codes is not None or out_scales is not None:
         if out is not None:
             raise ValueError("either out or out_codes and out_scales")
         if out_codes is None or out_scales is None:
             raise ValueError("out_codes and out_scales are given together")
         return (out_codes, out_scales), (
-            None, width, 0, _full(out_codes, "out_codes", torch.uint8, (M, width), device),
-            _full(out_scales, "out_scales", torch.float32, (M, _blocks(width)), device))
+            None, N, 0, _full(out_codes, "out_codes", torch.uint8, (M, N), device),
+            _full(out_scales, "out_scales", torch.float32, (M, (N + 127) // 128), device))
     if out is None:
-        out = _empty((M, width), dtype, x.device, stream)
+        out = _empty((M, N), dtype, x.device, stream)
     kind = _type_of(out, "out", most=2)
-    strides = _rows(out, "out", out.dtype, (M, width), device)
-    return out, (out.data_ptr(), strides[0] if M > 1 else width, kind, None, None)
+    strides = _rows(out, "out", out.dtype, (M, N), device)
+    return out, (out.data_ptr(), strides[0] if M > 1 else N, kind, None, None)
 
 
 def fp8_matmul(codes: torch.Tensor, scales: torch.Tensor, w_codes: torch.Tensor,
@@ -904,16 +901,16 @@ def fp8_matmul(codes: torch.Tensor, scales: torch.Tensor, w_codes: torch.Tensor,
     Returns out [T, N or N/2] (allocated as out_dtype, of the stream of the launch, where it is
     not given), or (out_codes, out_scales)."""
     dev = _device_of(codes, "codes")
-    T, K = shape = tuple(codes.shape)
-    N = w_codes.shape[0]
-    a = _rows(codes, "codes", torch.uint8, shape, dev)
-    b = _rows(w_codes, "w_codes", torch.uint8, (N, K), dev)
-    got, args = _matmul_out(T, N, gated, codes, out_dtype, out, out_codes, out_scales, dev, stream)
+    T, K = shape = codes.shape
+    N, kb = w_codes.shape[0], (K + 127) // 128
+    f32, u8 = torch.float32, torch.uint8
+    a = _rows(codes, "codes", u8, shape, dev)
+    b = _rows(w_codes, "w_codes", u8, (N, K), dev)
+    got, (o, o_stride, o_type, o_codes, o_scales) = _matmul_out(T, N, gated, codes, out_dtype, out, out_codes, out_scales, dev, stream)
     rc = load().dsa_fp8_matmul(
-        codes.data_ptr(), a[0], _full(scales, "scales", torch.float32, (T, _blocks(K)), dev), T,
-        w_codes.data_ptr(), b[0],
-        _full(w_scales, "w_scales", torch.float32, (_blocks(N), _blocks(K)), dev), N, K, gated, *args,
-        _status(status, dev), _stream_of(stream, dev))
+        codes.data_ptr(), a[0], _full(scales, "scales", f32, (T, kb), dev), T, w_codes.data_ptr(), b[0],
+        _full(w_scales, "w_scales", f32, ((N + 127) // 128, kb), dev), N, K, gated, o, o_stride, o_type,
+        o_codes, o_scales, None if status is None else _status(status, dev), _stream_of(stream, dev))
     if rc:
         _check(rc)
     return got
@@ -934,30 +931,33 @@ def grouped_matmul(x: torch.Tensor, weight: torch.Tensor, group_starts: torch.Te
     outputs [M, ..] and what is returned: as fp8_matmul; out_dtype is x's own unless given (BF16
     of 8-bit rows).  Rows in no group are left as they were."""
     dev = _device_of(x, "x")
-    S, K = shape = tuple(x.shape)
-    E, N = weight.shape[0], weight.shape[1]
-    if x.dtype is torch.uint8:
+    S, K = shape = x.shape
+    if weight.dim() != 3:
+        raise ValueError(f"weight has shape {tuple(weight.shape)}, expected (groups, rows, {K})")
+    E, N = weight.shape[:2]
+    own = x.dtype
+    if own is torch.uint8:
         if x_scales is None or w_scales is None:
             raise ValueError("uint8 (E4M3) rows and weights need x_scales and w_scales")
-        kind = TYPE_E4M3
-        xs = _full(x_scales, "x_scales", torch.float32, (S, _blocks(K)), dev)
-        ws = _full(w_scales, "w_scales", torch.float32, (E, _blocks(N), _blocks(K)), dev)
-        dtype = torch.bfloat16
+        kind, kb, f32 = TYPE_E4M3, (K + 127) // 128, torch.float32
+        xs = _full(x_scales, "x_scales", f32, (S, kb), dev)
+        ws = _full(w_scales, "w_scales", f32, (E, (N + 127) // 128, kb), dev)
     else:
-        kind, xs, ws, dtype = _type_of(x, "x"), None, None, x.dtype
+        kind, xs, ws = _type_of(x, "x"), None, None
         if x_scales is not None or w_scales is not None:
             raise ValueError("scales go with uint8 (E4M3) rows and weights")
-    a = _rows(x, "x", x.dtype, shape, dev)
-    b = _rows(weight, "weight", x.dtype, (E, N, K), dev)
+    a = _rows(x, "x", own, shape, dev)
+    b = _rows(weight, "weight", own, (E, N, K), dev)
     M, index = S, None
     if rows is not None:
         M = rows.shape[0]
         index = _full(rows, "rows", torch.int32, (M,), dev)
-    got, args = _matmul_out(M, N, gated, x, out_dtype or dtype, out, out_codes, out_scales, dev, stream)
+    got, (o, o_stride, o_type, o_codes, o_scales) = _matmul_out(
+        M, N, gated, x, out_dtype or (torch.bfloat16 if xs else own), out, out_codes, out_scales, dev, stream)
     rc = load().dsa_grouped_matmul(
         x.data_ptr(), a[0], xs, kind, S, index, M, weight.data_ptr(), b[1], b[0], ws, N, K,
-        _full(group_starts, "group_starts", torch.int32, (E + 1,), dev), E, gated, *args,
-        _status(status, dev), _stream_of(stream, dev))
+        _full(group_starts, "group_starts", torch.int32, (E + 1,), dev), E, gated, o, o_stride, o_type,
+        o_codes, o_scales, None if status is None else _status(status, dev), _stream_of(stream, dev))
     if rc:
         _check(rc)
     return got
@@ -976,7 +976,7 @@ def route_experts(logits: torch.Tensor, top_k: int, expert_ids: torch.Tensor,
     experts; num_tokens [1] int32 (query_start_loc[-1:]) leaves padding rows out."""
     dev = _device_of(logits, "logits")
     kind = _type_of(logits, "logits", most=2)
-    T, E = shape = tuple(logits.shape)
+    T, E = shape = logits.shape
     if scoring not in SCORINGS:
         raise ValueError(f"scoring must be one of {', '.join(SCORINGS)}, got {scoring!r}")
     a = _rows(logits, "logits", logits.dtype, shape, dev)
@@ -1001,22 +1001,18 @@ def combine_experts(y: torch.Tensor, places: torch.Tensor, weights: torch.Tensor
     them.  add and out [T, N] of y's type with any row stride; add may be out.  Returns out."""
     dev = _device_of(y, "y")
     kind, dtype = _type_of(y, "y", most=2), y.dtype
-    M, N = tuple(y.shape)
-    T, top_k = pairs = tuple(places.shape)
-    a = _rows(y, "y", dtype, (M, N), dev)
+    M, N = shape = y.shape
+    T, top_k = pairs = places.shape
+    a = _rows(y, "y", dtype, shape, dev)
     if out is None:
         out = _empty((T, N), dtype, y.device, stream)
-
-    def row(t, name):  # address and row stride
-        if t is None:
-            return None, N
-        strides = _rows(t, name, dtype, (T, N), dev)
-        return t.data_ptr(), strides[0] if T > 1 else N
-
+    b = _rows(out, "out", dtype, (T, N), dev)
+    c = b if add is None else _rows(add, "add", dtype, (T, N), dev)
     rc = load().dsa_combine_experts(
         y.data_ptr(), a[0] if M > 1 else N, kind, M, _full(places, "places", torch.int32, pairs, dev),
-        _full(weights, "weights", torch.float32, pairs, dev), T, top_k, N, *row(add, "add"), *row(out, "out"),
-        _status(status, dev), _stream_of(stream, dev))
+        _full(weights, "weights", torch.float32, pairs, dev), T, top_k, N,
+        None if add is None else add.data_ptr(), c[0] if T > 1 else N, out.data_ptr(), b[0] if T > 1 else N,
+        None if status is None else _status(status, dev), _stream_of(stream, dev))
     if rc:
         _check(rc)
     return out

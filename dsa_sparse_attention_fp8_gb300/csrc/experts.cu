@@ -5,6 +5,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <mutex>
 #include <type_traits>
 
 #include "combine.cuh"
@@ -39,27 +40,50 @@ int64_t row_tiles(int64_t M, int64_t groups, int tile) {
   return used + (M - used) / tile;
 }
 
-// Clusters of `size` CTAs of a kernel that the current device runs at once, asked for once a device.
-class ClusterCount {
+// The current device: its number and SMs.
+struct Device {
+  int id = -1, sms = 0;
+  Device() {
+    if (cudaGetDevice(&id) == cudaSuccess) sms = sm_count();
+  }
+};
+
+// What a kernel needs once a device: its shared memory allowed, and how many clusters of 1 to 8 CTAs run at once.
+class Ready {
  public:
-  int get(const void* kernel, int size, int threads, int smem) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-    std::atomic<int>* known = dev >= 0 && dev < 64 ? &known_[dev][size] : nullptr;
-    if (known && known->load(std::memory_order_relaxed)) return known->load(std::memory_order_relaxed);
-    cudaLaunchConfig_t c{};
-    cudaLaunchAttribute a[1];
-    a[0].id = cudaLaunchAttributeClusterDimension;
-    a[0].val.clusterDim.x = size, a[0].val.clusterDim.y = 1, a[0].val.clusterDim.z = 1;
-    c.gridDim = dim3(size), c.blockDim = dim3(threads), c.dynamicSmemBytes = smem, c.attrs = a, c.numAttrs = 1;
-    int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, kernel, &c) != cudaSuccess) return 0;
-    if (known) known->store(n, std::memory_order_relaxed);
-    return n;
+  // The counts by size, or null with the error recorded.
+  const int* on(const Device& d, const void* kernel, int threads, int smem) {
+    if (d.id < 0 || d.id >= kDevices) return fail(DSA_ERR_CUDA, "no CUDA device, or more than %d", kDevices), nullptr;
+    Slot& s = slot_[d.id];
+    if (s.done.load(std::memory_order_acquire)) return s.clusters;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return fail(DSA_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e)), nullptr;
+    int found[9] = {};
+    for (int size = 1; size <= 8; ++size) {
+      cudaLaunchConfig_t c{};
+      cudaLaunchAttribute a[1];
+      a[0].id = cudaLaunchAttributeClusterDimension;
+      a[0].val.clusterDim.x = size, a[0].val.clusterDim.y = 1, a[0].val.clusterDim.z = 1;
+      c.gridDim = dim3(size), c.blockDim = dim3(threads), c.dynamicSmemBytes = smem, c.attrs = a, c.numAttrs = 1;
+      if (cudaOccupancyMaxActiveClusters(&found[size], kernel, &c) != cudaSuccess) found[size] = 0, cudaGetLastError();
+    }
+    if (found[1] < 1 || found[2] < 1) return fail(DSA_ERR_CUDA, "the products' kernels do not fit the device"), nullptr;
+    const std::lock_guard<std::mutex> hold(lock_);
+    if (!s.done.load(std::memory_order_relaxed)) {
+      std::copy(found, found + 9, s.clusters);
+      s.done.store(true, std::memory_order_release);
+    }
+    return s.clusters;
   }
 
  private:
-  std::atomic<int> known_[64][9] = {};
+  static constexpr int kDevices = 64;
+  struct Slot {
+    std::atomic<bool> done{false};
+    int clusters[9] = {};
+  };
+  Slot slot_[kDevices];
+  std::mutex lock_;
 };
 
 // Launches a kernel, in clusters of `size` CTAs, that waits for what is before it in the stream by itself: it is set up while
@@ -90,30 +114,33 @@ template <bool FP8, bool GATED, bool WIDE, int BM, int ROUND = GATED || WIDE ? 3
 struct Few {
   using C = dsa::FewCfg<FP8, GATED, WIDE, BM, ROUND>;
   static constexpr auto kKernel = dsa::few_rows_kernel<FP8, GATED, WIDE, BM, ROUND>;
-  static inline PerDevice allowed;
-  static inline ClusterCount resident;
+  static inline Ready ready;
 
   // A CTA alone takes as long for a block of K wherever it lies, bound by what one SM draws from L2 (measured of one tile of
   // 7168 elements of K, in L2: 22 us by one CTA, 7.5 by eight).  CTAs that share a tile join their sums, round by round.
   static constexpr double kBlock = (C::kStageA + C::kStageB) / 110e3 + 0.06, kRoundUs = C::BN == 256 ? 1.8 : 0.8;
 
-  static int plan(const dsa::MatmulParams& p, int64_t groups, Plan* best) {
+  static int plan(const dsa::MatmulParams& p, int64_t groups, const Device& d, Plan* best) {
     *best = {1e30, 0, 0};
-    if (const int rc = allow_smem(allowed, (const void*)kKernel, C::kSmem)) return rc;
+    const int* const clusters = ready.on(d, (const void*)kKernel, dsa::kMatmulThreads, C::kSmem);
+    if (!clusters) return DSA_ERR_CUDA;
     const int64_t tiles = row_tiles(p.M, groups, BM) * ((p.width + C::kOut - 1) / C::kOut);
     const int blocks = (p.K + C::kK - 1) / C::kK, rounds = (std::min(BM, p.M) + ROUND - 1) / ROUND;
-    for (int s = 1; s <= 8 && (s == 1 || (2 * s <= blocks && tiles * s <= sm_count())); ++s) {
-      const int n = resident.get((const void*)kKernel, s, dsa::kMatmulThreads, C::kSmem);
+    for (int s = 1; s <= 8 && (s == 1 || (2 * s <= blocks && tiles * s <= d.sms)); ++s) {
+      const int n = clusters[s];
       if (n < 1) continue;
       const double us = (double)((tiles + n - 1) / n) * ((blocks + s - 1) / s * kBlock + (s == 1 ? 0.5 : 0.4 + 0.1 * s + rounds * kRoundUs));
       if (us < best->us) *best = {us, s, n};
     }
-    return best->clusters ? DSA_OK : fail(DSA_ERR_CUDA, "few_rows_kernel does not fit the device");
+    return DSA_OK;
   }
 
-  static int run(dsa::MatmulParams p, int64_t groups, cudaStream_t st) {
+  static int run(dsa::MatmulParams p, int64_t groups, const Device& d, cudaStream_t st) {
     Plan plan;
-    if (const int rc = Few::plan(p, groups, &plan)) return rc;
+    if (const int rc = Few::plan(p, groups, d, &plan)) return rc;
+    return run(p, groups, plan, st);
+  }
+  static int run(dsa::MatmulParams p, int64_t groups, Plan plan, cudaStream_t st) {
     CUtensorMap tx, tw;
     p.box = p.M <= 32 * groups ? 32 : BM;
     if (const int rc = product_maps(p, p.box, C::kBox, &tx, &tw)) return rc;
@@ -131,22 +158,24 @@ template <bool FP8, bool GATED>
 struct Many {
   using C = dsa::ManyCfg<FP8, GATED>;
   static constexpr auto kKernel = dsa::many_rows_kernel<FP8, GATED>;
-  static inline PerDevice allowed;
-  static inline ClusterCount resident;
+  static inline Ready ready;
 
-  static int plan(const dsa::MatmulParams& p, int64_t groups, Plan* best) {
-    if (const int rc = allow_smem(allowed, (const void*)kKernel, C::kSmem)) return rc;
-    const int n = resident.get((const void*)kKernel, 2, dsa::kMatmulThreads, C::kSmem);
-    if (n < 1) return fail(DSA_ERR_CUDA, "no pair of CTAs fits the device");
+  static int plan(const dsa::MatmulParams& p, int64_t groups, const Device& d, Plan* best) {
+    const int* const clusters = ready.on(d, (const void*)kKernel, dsa::kMatmulThreads, C::kSmem);
+    if (!clusters) return DSA_ERR_CUDA;
+    const int n = clusters[2];
     const int64_t tiles = row_tiles(p.M, groups, C::BM) * ((p.width + C::kOut - 1) / C::kOut);
     // (8192 rows, K = N = 7168: twelve tiles of 56 blocks to a pair in 300 us)
     *best = {(double)((tiles + n - 1) / n) * ((p.K + C::kK - 1) / C::kK * 0.43 + 1.0), 2, n};
     return DSA_OK;
   }
 
-  static int run(dsa::MatmulParams p, int64_t groups, cudaStream_t st) {
+  static int run(dsa::MatmulParams p, int64_t groups, const Device& d, cudaStream_t st) {
     Plan plan;
-    if (const int rc = Many::plan(p, groups, &plan)) return rc;
+    if (const int rc = Many::plan(p, groups, d, &plan)) return rc;
+    return run(p, groups, plan, st);
+  }
+  static int run(dsa::MatmulParams p, int64_t groups, const Plan& plan, cudaStream_t st) {
     CUtensorMap tx, tw;
     if (const int rc = product_maps(p, 128, C::kBox, &tx, &tw)) return rc;
     const int64_t rows = row_tiles(p.M, groups, C::BM), tiles = rows * ((p.width + C::kOut - 1) / C::kOut);
@@ -165,25 +194,27 @@ int run_variant(const dsa::MatmulParams& p, int64_t groups, cudaStream_t st) {
   using Wide64 = Few<FP8, false, !GATED, 64>;
   using Few128 = Few<FP8, GATED, false, 128>;
   using Pairs = Many<FP8, GATED>;
+  const Device d;
+  if (d.sms <= 0) return fail(DSA_ERR_CUDA, "no CUDA device");
   const int64_t tiles = row_tiles(p.M, groups, 64) * ((p.width + 127) / 128);
-  if (groups > 1 && tiles > 2 * sm_count()) {
+  if (groups > 1 && tiles > 2 * d.sms) {
     // Bound by the weights' way from HBM.  Tiles fit the rows of a group; 256 weight rows to a tile, so that rows are read less
     // often (64 groups, K 2048, N 7168, us with 128 / 256 weight rows and by pairs, of 16 rows to a group 199 / 165 / 183, of 32 203 / 170 / 186;
     // tiles of 128 rows and pairs, of 48 189 / 193, of 96 243 / 206; gated, K 7168, N 4096, tiles of 64 and 128 rows and
     // pairs, of 32 300 / 304 / 352, of 48 343 / 320 / 374, of 96 486 / 386 / 392, of 128 545 / 491 / 379).
     if (p.M <= 32 * groups) {
-      if constexpr (GATED) return Few64::run(p, groups, st);
-      else return Wide64::run(p, groups, st);
+      if constexpr (GATED) return Few64::run(p, groups, d, st);
+      else return Wide64::run(p, groups, d, st);
     }
-    return p.M <= (GATED ? 96 : 48) * groups ? Few128::run(p, groups, st) : Pairs::run(p, groups, st);
+    return p.M <= (GATED ? 96 : 48) * groups ? Few128::run(p, groups, d, st) : Pairs::run(p, groups, d, st);
   }
   // Few tiles: as the CTAs that share their K take.
   Plan few, some, many;
-  if (const int rc = Joined64::plan(p, groups, &few)) return rc;
-  if (const int rc = Few128::plan(p, groups, &some)) return rc;
-  if (const int rc = Pairs::plan(p, groups, &many)) return rc;
-  if (many.us < few.us && many.us < some.us) return Pairs::run(p, groups, st);
-  return some.us < few.us ? Few128::run(p, groups, st) : Joined64::run(p, groups, st);
+  if (const int rc = Joined64::plan(p, groups, d, &few)) return rc;
+  if (const int rc = Few128::plan(p, groups, d, &some)) return rc;
+  if (const int rc = Pairs::plan(p, groups, d, &many)) return rc;
+  if (many.us < few.us && many.us < some.us) return Pairs::run(p, groups, many, st);
+  return some.us < few.us ? Few128::run(p, groups, some, st) : Joined64::run(p, groups, few, st);
 }
 
 // The checks that both products share, and their launch.  p has the sizes, strides and pointers.
@@ -217,7 +248,6 @@ int run_matmul(dsa::MatmulParams p, int64_t groups, cudaStream_t st) {
   p.nb = (p.N + dsa::kMatmulBlock - 1) / dsa::kMatmulBlock;
   if (!fp8) p.x_scales = p.w_scales = nullptr;
   p.give_up = env_int("DSA_WAIT_LIMIT", (int)dsa::kWaitLimit, 0, (int)dsa::kWaitLimit) == 0;
-  if (sm_count() <= 0) return fail(DSA_ERR_CUDA, "no CUDA device");
   if (fp8) return p.gated ? run_variant<true, true>(p, groups, st) : run_variant<true, false>(p, groups, st);
   return p.gated ? run_variant<false, true>(p, groups, st) : run_variant<false, false>(p, groups, st);
 }
