@@ -302,27 +302,45 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
     const bool vec_codes = p.codes && (reinterpret_cast<uintptr_t>(p.codes) | (uintptr_t)p.width) % 4 == 0;
     int buffer = 0, turn = 0, joined = 0;
     bool on = true;
-    for (int t = blockIdx.x / S; on && find_tile<BM, C::kOut>(p, groups, t, &tile); t += step) {
+    // A tile's rows and first scales are asked for a tile ahead: where it is and this lane's row of x before the products of the
+    // tile before are summed, the scales before its results are written (experts of a batch of 64, 290 us without it, 279.5).
+    Tile ahead;
+    const auto row_of = [&](const Tile& of) {
       const int row = q * 32 + lane;
+      return row >= of.count ? 0 : p.rows ? ld_ahead(p.rows + of.row + row) : of.row + row;
+    };
+    const auto scales_of = [&](const Tile& of, int src, const float** xs, const float** ws, const float** wu) {
+      const int n0 = GATED ? of.column + 64 * half : WIDE ? of.column + 128 * half : of.column;
+      *xs = p.x_scales + (int64_t)(src < 0 || src >= p.x_rows ? 0 : src) * p.kb;
+      *ws = p.w_scales + ((int64_t)of.e * p.nb + min(p.nb - 1, n0 / kMatmulBlock)) * p.kb;
+      *wu = p.w_scales + ((int64_t)of.e * p.nb + min(p.nb - 1, (p.width + n0) / kMatmulBlock)) * p.kb;
+    };
+    float s_next = 0.f, g_next = 0.f, u_next = 0.f;
+    const auto first_scales = [&](const Tile& of, int src) {
+      const float *xs, *ws, *wu;
+      scales_of(of, src, &xs, &ws, &wu);
+      s_next = ld_ahead(xs + k0), g_next = ld_ahead(ws + k0), u_next = GATED ? ld_ahead(wu + k0) : 0.f;
+    };
+    int t = blockIdx.x / S;
+    bool more = find_tile<BM, C::kOut>(p, groups, t, &ahead);
+    int src_ahead = more ? row_of(ahead) : 0;
+    if (FP8 && more) first_scales(ahead, src_ahead);
+    while (on && more) {
+      tile = ahead;
+      const int row = q * 32 + lane, src = src_ahead;
+      t += step;
+      more = find_tile<BM, C::kOut>(p, groups, t, &ahead);
+      if (more) src_ahead = row_of(ahead);
       const bool busy = q * 32 < tile.count;  // the warp has rows
-      int src = 0;
-      bool bad = false;
-      if (row < tile.count) {
-        src = p.rows ? __ldg(p.rows + tile.row + row) : tile.row + row;
-        bad = src < 0 || src >= p.x_rows;
-        if (bad) src = 0;
-        if (bad && half == 0 && rank == 0) raise_status(p.status, kStatusBadMetadata);
-      }
+      const bool bad = row < tile.count && (src < 0 || src >= p.x_rows);
+      if (bad && half == 0 && rank == 0) raise_status(p.status, kStatusBadMetadata);
       uint64_t acc[C::kHalf / 2];
 #pragma unroll
       for (int i = 0; i < C::kHalf / 2; ++i) acc[i] = 0;
       if (FP8) {
-        const float* const xs = p.x_scales + (int64_t)src * p.kb;
-        const int n0 = GATED ? tile.column + 64 * half : WIDE ? tile.column + 128 * half : tile.column;
-        const float* const ws = p.w_scales + ((int64_t)tile.e * p.nb + min(p.nb - 1, n0 / kMatmulBlock)) * p.kb;
-        const float* const wu = p.w_scales + ((int64_t)tile.e * p.nb + min(p.nb - 1, (p.width + n0) / kMatmulBlock)) * p.kb;
+        const float *xs, *ws, *wu;
+        scales_of(tile, src, &xs, &ws, &wu);
         // (a block's scales are loaded while the block before is summed)
-        float s_next = ld_ahead(xs + k0), g_next = ld_ahead(ws + k0), u_next = GATED ? ld_ahead(wu + k0) : 0.f;
         for (int k = k0; k < k1; ++k) {
           const float f = s_next * g_next, u = GATED ? s_next * u_next : f;
           const int at = min(k + 1, k1 - 1);
@@ -349,6 +367,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
         }
       }
       if (!on) break;
+      if (FP8 && more) first_scales(ahead, src_ahead);
 
       // rounds of kRound rows: every CTA lays its sums out, then each warp of the cluster takes rows
       for (int r0 = 0; r0 < tile.count && on; r0 += C::kRound) {
