@@ -173,6 +173,51 @@ def test_grouped_matmul_of_many_rows(B, kind, gated, out, N, K):
     Product([700, 0, 1024, 3, 513, 256, 255], N, K, kind, kind is U8, gated).check(B, out)
 
 
+MANY_GROUPS = [[2, 0, 1, 4, 3] * 13, [40, 0, 37, 70, 1] * 8, [90] * 40, [200, 3] * 20]    # by what rows to a group decide
+
+
+@pytest.mark.parametrize("counts", MANY_GROUPS)
+@pytest.mark.parametrize("kind,gated,out,N,K", [(U8, True, U8, 2048, 272), (U8, False, BF, 1101, 400), (HALF, True, HALF, 1800, 72),
+                                                (BF, False, F32, 1024, 200)])
+def test_grouped_matmul_of_many_groups(B, counts, kind, gated, out, N, K):
+    Product(counts, N, K, kind, kind is U8, gated, pad=2).check(B, out)
+
+
+@pytest.mark.parametrize("T", [1, 17, 64, 65, 128, 200, 300])
+@pytest.mark.parametrize("N,K,gated", [(256, 5000, False), (640, 2048, True), (1000, 1500, False)])
+def test_fp8_matmul_with_a_tiles_k_shared(B, T, N, K, gated):
+    """As many CTAs to a tile as fit, whose parts of K are not alike."""
+    Product([T], N, K, gated=gated, seed=T).check(B, U8 if gated else F32, dense=True)
+
+
+def test_a_call_right_behind_another_sees_its_results(B):
+    """Kernels are set up while the one before drains: a chain of products, each of the rows that the one before wrote."""
+    torch.manual_seed(3)
+    n = 512
+    w = (100 * torch.randn(2 * n, n, device="cuda")).clamp(-448, 448).to(E4M3).view(U8)
+    ws = torch.full((8, 4), n ** -0.5 / 100, device="cuda")
+    fixed = torch.full((700, 4), 0.01, device="cuda")                # (of every step's rows, so that they keep their size)
+    codes = [torch.zeros(700, n, dtype=U8, device="cuda") for _ in range(9)]
+    scales = [torch.ones(700, 4, device="cuda") for _ in range(9)]
+    codes[0].copy_((100 * torch.randn(700, n, device="cuda")).clamp(-448, 448).to(E4M3).view(U8))
+    rows = {1: 1, 2: 64, 3: 700, 4: 200, 5: 700, 6: 3, 7: 128, 8: 700}
+
+    def chain(wait):
+        for i in range(1, 9):
+            t = rows[i]
+            B.fp8_matmul(codes[i - 1][:t], fixed[:t], w, ws, gated=True, out_codes=codes[i][:t], out_scales=scales[i][:t])
+            if wait:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return [c.clone() for c in codes + scales]
+    want = chain(True)
+    assert all(x.isfinite().all() for x in want[9:]) and want[8].float().abs().sum() > 0
+    for _ in range(20):
+        for i in range(1, 9):
+            codes[i].zero_(), scales[i].fill_(1)
+        assert all(torch.equal(a, b) for a, b in zip(chain(False), want))
+
+
 def test_allocated_outputs(B):
     p = Product([5], 64, 256)
     for dtype in (BF, HALF, F32):
@@ -446,7 +491,35 @@ def test_combine(B, T, k, N, dtype, add, step):
     assert torch.equal(B.combine_experts(y, places, weights), B.combine_experts(y, places, weights, add=torch.zeros_like(out)))
 
 
+def test_outputs_come_from_the_launch_stream(B):
+    """Memory that the current stream's queued work may still use is not handed to a launch on another stream."""
+    p = Product([40], 512, 256)
+    y, places, weights = torch.randn(80, 512, device="cuda").to(BF), torch.arange(80, device="cuda").view(40, 2).int(), torch.rand(40, 2, device="cuda")
+    calls = [lambda **kw: p.call(B, dense=True, **kw), lambda **kw: p.call(B, **kw), lambda **kw: B.combine_experts(y, places, weights, **kw)]
+    for call in calls:
+        want = call()
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        freed = torch.empty_like(want)
+        at = freed.data_ptr()
+        del freed
+        got = call(stream=side)
+        side.synchronize()
+        assert got.data_ptr() != at and torch.equal(got, want)
+
+
 # ------------------------------------------------------------------ together
+def test_the_example_runs(B, capsys):
+    import importlib.util
+
+    from conftest import ROOT
+    spec = importlib.util.spec_from_file_location("expert_layer", ROOT / "examples" / "expert_layer.py")
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    layer = ex.main(steps=3, width=512, inner=256, experts=16, top_k=4, tokens=40)
+    assert int(layer.status) == 0 and capsys.readouterr().out.count("step") == 3
+
+
 @pytest.mark.parametrize("T,real", [(1, 1), (40, 33), (300, 300)])
 def test_a_layers_experts(B, T, real):
     """Norm, router, both expert products beside a shared expert's, and the sum, as a layer runs them, in a graph of a
