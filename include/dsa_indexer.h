@@ -655,8 +655,9 @@ int dsa_route_experts(const void* logits, int64_t stride, int type, const float*
  * The experts' rows back to their tokens:
  *   out[t] = add[t] + sum_j weights[t, j] * y[places[t, j]]
  * y [M, N], add and out [T, N] of one type (BF16, FP16, FP32), row strides in
- * elements, >= N; add may be NULL, and may be out itself.  places and weights
- * [T, top_k] contiguous, top_k <= 16; a negative place contributes nothing.
+ * elements, >= N; add may be NULL, and may be out itself; y must not overlap
+ * out.  places and weights [T, top_k] contiguous, top_k <= 16; a negative
+ * place contributes nothing.
  * Sums in FP32, in the order of j, add last; one rounding.
  * Faults: a place >= M contributes nothing: DSA_STATUS_BAD_METADATA.
  * Errors: INVALID_ARG, UNSUPPORTED, CUDA.
