@@ -953,7 +953,7 @@ def grouped_matmul(x: torch.Tensor, weight: torch.Tensor, group_starts: torch.Te
         M = rows.shape[0]
         index = _full(rows, "rows", torch.int32, (M,), dev)
     got, (o, o_stride, o_type, o_codes, o_scales) = _matmul_out(
-        M, N, gated, x, out_dtype or (torch.bfloat16 if xs else own), out, out_codes, out_scales, dev, stream)
+        M, N, gated, x, out_dtype or (torch.bfloat16 if kind == TYPE_E4M3 else own), out, out_codes, out_scales, dev, stream)
     rc = load().dsa_grouped_matmul(
         x.data_ptr(), a[0], xs, kind, S, index, M, weight.data_ptr(), b[1], b[0], ws, N, K,
         _full(group_starts, "group_starts", torch.int32, (E + 1,), dev), E, gated, o, o_stride, o_type,

@@ -221,6 +221,7 @@ int run_variant(const dsa::MatmulParams& p, int64_t groups, cudaStream_t st) {
 int run_matmul(dsa::MatmulParams p, int64_t groups, cudaStream_t st) {
   if (p.M < 0 || p.x_rows < 0) return fail(DSA_ERR_INVALID_ARG, "a negative number of rows");
   if (p.N < 1 || p.K < 1) return fail(DSA_ERR_INVALID_ARG, "N=%d, K=%d: both must be positive", p.N, p.K);
+  if (p.M > 1 << 30 || p.x_rows > 1 << 30) return fail(DSA_ERR_UNSUPPORTED, "%d rows of %d: at most 2^30", p.M, p.x_rows);
   if (p.N > 1 << 28 || p.K > 1 << 28) return fail(DSA_ERR_UNSUPPORTED, "N=%d, K=%d: at most 2^28", p.N, p.K);
   if (p.gated && p.N % 2) return fail(DSA_ERR_INVALID_ARG, "gated weights have two halves: N=%d is odd", p.N);
   p.width = p.gated ? p.N / 2 : p.N;
@@ -351,7 +352,7 @@ int dsa_route_experts(const void* logits, int64_t stride, int type, const float*
   if (top_k > top_groups * (E / num_groups))
     return fail(DSA_ERR_INVALID_ARG, "top_k=%d of %d experts in the chosen groups", top_k, top_groups * (E / num_groups));
   if (!(scale == scale) || scale - scale != 0.0f) return fail(DSA_ERR_INVALID_ARG, "scale must be finite");
-  if ((int64_t)T * top_k > INT32_MAX) return fail(DSA_ERR_UNSUPPORTED, "T=%d times top_k=%d exceeds 2^31", T, top_k);
+  if ((int64_t)T * top_k > 1 << 30) return fail(DSA_ERR_UNSUPPORTED, "T=%d times top_k=%d: at most 2^30", T, top_k);
   if (T > 1 && stride < E) return fail(DSA_ERR_INVALID_ARG, "the row stride is shorter than E");
   if (!group_starts) return fail(DSA_ERR_INVALID_ARG, "null pointer");
   if (T && (!logits || !expert_ids || !weights || !rows || !places)) return fail(DSA_ERR_INVALID_ARG, "null pointer");
@@ -381,6 +382,7 @@ int dsa_combine_experts(const void* y, int64_t y_stride, int type, int M, const 
   set_last_launches(0);
   if (T < 0 || M < 0) return fail(DSA_ERR_INVALID_ARG, "a negative number of rows");
   if (N < 1) return fail(DSA_ERR_INVALID_ARG, "N=%d < 1", N);
+  if (N > 1 << 28) return fail(DSA_ERR_UNSUPPORTED, "N=%d: at most 2^28", N);
   if (top_k < 1) return fail(DSA_ERR_INVALID_ARG, "top_k=%d < 1", top_k);
   if (top_k > dsa::kCombineMaxTop) return fail(DSA_ERR_UNSUPPORTED, "top_k=%d > %d", top_k, dsa::kCombineMaxTop);
   if (!is_float(type)) return fail(DSA_ERR_UNSUPPORTED, "type=%d: BF16, FP16 or FP32 is wanted", type);

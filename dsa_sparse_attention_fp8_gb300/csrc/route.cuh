@@ -446,7 +446,7 @@ __device__ __forceinline__ int real_tokens(const RouteParams& p) { return p.num_
 
 template <int V, typename T>
 __global__ void __launch_bounds__(kRouteThreads) route_choose_kernel(const __grid_constant__ RouteParams p) {
-  const int t = (int)((blockIdx.x * (unsigned)kRouteThreads + threadIdx.x) >> 5);
+  const int t = (int)(blockIdx.x * (kRouteThreads / 32) + (threadIdx.x >> 5));
   __shared__ alignas(8) int list[kRouteThreads / 32][64];
   pdl_launch_dependents();
   pdl_wait();

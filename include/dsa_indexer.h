@@ -583,8 +583,8 @@ int dsa_add_rms_norm(const void* x, int64_t x_stride, const void* residual, int6
  *     is 0; codes E4M3(y/s), RNE, saturating), [T, N/2] and [T, ceil(N/256)]
  *     contiguous.  Exactly one of the two is given.
  * Row strides are in elements; those of codes and w_codes are multiples of 16,
- * both 16-byte aligned.  K and N are any sizes from 1 to 2^28.  Outputs must
- * not overlap inputs.
+ * both 16-byte aligned.  K and N are any sizes from 1 to 2^28, T at most 2^30.
+ * Outputs must not overlap inputs.
  * Computation: tensor-core products with FP32 accumulation over a block of K,
  * its scales and the sums over blocks in FP32, gate in FP32, one rounding.
  * Faults: DSA_STATUS_TIMEOUT (an internal wait ran out; results are invalid).
@@ -606,7 +606,8 @@ int dsa_fp8_matmul(const uint8_t* codes, int64_t stride, const float* scales, in
  *   gated, out [M, ..], out_codes, out_scales: as dsa_fp8_matmul, with BF16
  *           and FP16 too (any even N).
  * Row and group strides are in elements, multiples of 16 bytes.  Rows that lie
- * in no group are left as they were.  Groups may be empty.  E <= 1024.
+ * in no group are left as they were.  Groups may be empty.  E <= 1024, M and
+ * x_rows <= 2^30; gathered x spans at most 64 GB.
  * Faults: a group that is not within [0, M] or ends before it starts is
  * skipped, an index in rows outside [0, x_rows) gives a row of zeros:
  * DSA_STATUS_BAD_METADATA.  (Groups that overlap, which only starts that go
@@ -641,7 +642,7 @@ int dsa_grouped_matmul(const void* x, int64_t x_stride, const float* x_scales, i
  *     weight 0, place -1, and no place in the groups.
  * logits [T, E] BF16, FP16 or FP32, row stride in elements.  NaN counts as
  * -inf, +inf as the largest finite value.  E <= 512, top_k <= 16, num_groups
- * <= 32 dividing E, top_k <= top_groups * E / num_groups.
+ * <= 32 dividing E, top_k <= top_groups * E / num_groups, T * top_k <= 2^30.
  * Errors: INVALID_ARG, UNSUPPORTED, CUDA.
  */
 #define DSA_SCORE_SIGMOID 0

@@ -38,6 +38,7 @@ def test_products_refuse(lib, change, code):
 
 def test_dense_product_refusals(lib):
     assert fp8(lib, T=-1) == -1 and fp8(lib, w_stride=250) == -1 and fp8(lib, w_stride=0) == -1
+    assert fp8(lib, T=(1 << 30) + 1) == -2 and fp8(lib, N=(1 << 28) + 1) == -2 and fp8(lib, K=(1 << 28) + 1) == -2
     assert fp8(lib, T=0, x=None, w=None) == 0 and lib.dsa_last_launch_count() == 0
 
 
@@ -48,6 +49,7 @@ def test_grouped_product_refusals(lib):
     assert grouped(lib, S=0, rows=FAKE) == -1 and grouped(lib, starts=None) == -1
     assert grouped(lib, w_row=0) == -1 and grouped(lib, w_group=0) == -1 and grouped(lib, w_group=8) == -1
     assert grouped(lib, type=0, w_row=260) == -1 and grouped(lib, type=0, stride=260) == -1   # multiples of 8 elements
+    assert grouped(lib, S=1 << 20, stride=1 << 20, rows=FAKE) == -2 and b"64 GB" in lib.dsa_last_error()
     assert grouped(lib, M=0, S=0, x=None) == 0 and grouped(lib, M=0, rows=FAKE, starts=None) == 0
 
 
@@ -61,7 +63,7 @@ def route(lib, logits=FAKE, stride=256, type=2, T=4, E=256, k=8, scoring=0, grou
     (dict(T=-1), -1), (dict(E=0), -1), (dict(E=513), -2), (dict(type=3), -2), (dict(k=0), -1), (dict(k=17), -2),
     (dict(scoring=2), -1), (dict(groups=0), -1), (dict(groups=7), -1), (dict(groups=64, top_groups=64), -2),
     (dict(top_groups=0), -1), (dict(top_groups=9), -1), (dict(groups=128, E=512), -2), (dict(groups=32, top_groups=1, k=9), -1),
-    (dict(scale=float("nan")), -1), (dict(scale=float("inf")), -1), (dict(T=1 << 28, k=8), -2), (dict(stride=255), -1),
+    (dict(scale=float("nan")), -1), (dict(scale=float("inf")), -1), (dict(T=1 << 27, k=9), -2), (dict(stride=255), -1),
     (dict(logits=None), -1), (dict(ids=None), -1), (dict(starts=None), -1),
 ])
 def test_router_refuses(lib, change, code):
@@ -74,7 +76,7 @@ def combine(lib, y=FAKE, stride=64, type=0, M=8, places=FAKE, T=4, k=2, N=64, ad
 
 @pytest.mark.parametrize("change,code", [
     (dict(T=-1), -1), (dict(M=-1), -1), (dict(N=0), -1), (dict(k=0), -1), (dict(k=17), -2), (dict(type=3), -2),
-    (dict(stride=63), -1), (dict(out_stride=63), -1), (dict(add=FAKE, add_stride=63), -1), (dict(y=None), -1),
+    (dict(N=(1 << 28) + 1, stride=1 << 29, out_stride=1 << 29), -2), (dict(stride=63), -1), (dict(out_stride=63), -1), (dict(add=FAKE, add_stride=63), -1), (dict(y=None), -1),
     (dict(places=None), -1), (dict(out=None), -1), (dict(y=P(0x1001)), -1), (dict(out=P(0x1001)), -1),
 ])
 def test_combine_refuses(lib, change, code):

@@ -224,6 +224,8 @@ def test_allocated_outputs(B):
         got = B.fp8_matmul(p.x, p.xs, p.w[0], p.ws[0], out_dtype=dtype)
         assert got.shape == (5, 64) and got.dtype is dtype
     assert B.fp8_matmul(p.x[:0], p.xs[:0], p.w[0], p.ws[0]).shape == (0, 64)
+    none = B.grouped_matmul(p.x[:0], p.w, ints([0, 0]), p.xs[:0], p.ws)
+    assert none.shape == (0, 64) and none.dtype is BF
     p = Product([5, 2], 64, 256, HALF, gather=True)
     assert p.call(B).dtype is HALF and p.call(B).shape == (7, 64) and p.call(B, out_dtype=F32).dtype is F32
 
@@ -489,6 +491,37 @@ def test_combine(B, T, k, N, dtype, add, step):
     if add:                                                              # in place of the shared rows
         assert torch.equal(B.combine_experts(y, places, weights, add=shared, out=shared), out)
     assert torch.equal(B.combine_experts(y, places, weights), B.combine_experts(y, places, weights, add=torch.zeros_like(out)))
+
+
+def test_first_calls_may_be_captured(B):
+    """What a kernel needs once a device is done within a capture too (a process of its own, in which nothing ran before)."""
+    import subprocess
+    import sys
+
+    from conftest import ROOT
+    script = """
+import torch
+from dsa_sparse_attention_fp8_gb300 import binding as B
+u8, i32 = torch.uint8, torch.int32
+for T in (3, 700):
+    x, xs = torch.full((T, 256), 0x38, dtype=u8, device="cuda"), torch.ones(T, 2, device="cuda")
+    w, ws = torch.full((4, 512, 256), 0x38, dtype=u8, device="cuda"), torch.ones(4, 4, 2, device="cuda")
+    logits = torch.randn(T, 4, device="cuda")
+    ids, places, rows = (torch.zeros(*s, dtype=i32, device="cuda") for s in ((T, 2), (T, 2), (2 * T,)))
+    weights, starts, out = torch.zeros(T, 2, device="cuda"), torch.zeros(5, dtype=i32, device="cuda"), torch.zeros(T, 512, device="cuda")
+    y = torch.zeros(2 * T, 512, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        B.route_experts(logits, 2, ids, weights, starts, rows, places)
+        B.grouped_matmul(x, w, starts, xs, ws, rows=rows, out=y)
+        B.fp8_matmul(x, xs, w[0], ws[0], out=out)
+        B.combine_experts(y, places, weights, add=out, out=out)
+    graph.replay()
+    assert (out - 512.0).abs().max() < 1e-3, out
+print("done")
+"""
+    done = subprocess.run([sys.executable, "-c", script], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0 and "done" in done.stdout, done.stderr[-2000:]
 
 
 def test_outputs_come_from_the_launch_stream(B):
