@@ -319,7 +319,7 @@ int dsa_grouped_matmul(const void* x, int64_t x_stride, const float* x_scales, i
     return fail(DSA_ERR_UNSUPPORTED, "x_type=%d: BF16, FP16 or E4M3 is wanted", x_type);
   if (E < 1) return fail(DSA_ERR_INVALID_ARG, "E=%d < 1", E);
   if (E > dsa::kMatmulMaxGroups) return fail(DSA_ERR_UNSUPPORTED, "E=%d > %d", E, dsa::kMatmulMaxGroups);
-  if (!rows && M != x_rows) return fail(DSA_ERR_INVALID_ARG, "without rows, M=%d must be x_rows=%d", M, x_rows);
+  if (!rows && M > 0 && M != x_rows) return fail(DSA_ERR_INVALID_ARG, "without rows, M=%d must be x_rows=%d", M, x_rows);
   if (M > 0 && x_rows < 1) return fail(DSA_ERR_INVALID_ARG, "x_rows=%d < 1", x_rows);
   if (M > 0 && !group_starts) return fail(DSA_ERR_INVALID_ARG, "null pointer");
   dsa::MatmulParams p{};

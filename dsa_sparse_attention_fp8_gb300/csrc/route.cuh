@@ -71,13 +71,6 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 __device__ __forceinline__ double key_value(uint64_t k) {
   return __longlong_as_double((k >> 63) ? k ^ (1ull << 63) : ~k);
 }
-template <typename F>
-struct KeyOf;
-template <>
-struct KeyOf<float> { using type = uint32_t; };
-template <>
-struct KeyOf<double> { using type = uint64_t; };
-
 __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return max(a, b); }
 __device__ __forceinline__ uint64_t larger(uint64_t a, uint64_t b) { return a > b ? a : b; }
 __device__ __forceinline__ uint32_t smaller(uint32_t a, uint32_t b) { return min(a, b); }
@@ -400,7 +393,7 @@ __device__ __forceinline__ int choose_token(const RouteParams& p, int t, int rea
   } else {
     chosen = choose<V, T>(p, l, own, row, lane, list);
   }
-  // weights: in FP32, but for rows all of whose scores are next to nothing
+  // weights
   const bool mine = lane < p.top_k;
   const float lc = load_logit<T>(p.logits, row + chosen);
   float top = 0.f, score;
@@ -424,7 +417,8 @@ __device__ __forceinline__ int choose_token(const RouteParams& p, int t, int rea
     float all = score;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-    if (all < 1e-30f) {
+    // scores near FP32's smallest numbers have no 24 bits: then in 64
+    if (__any_sync(0xffffffffu, mine && lc != -INFINITY && (p.softmax ? lc - top : lc) < -80.0f)) {
       double d = 0;
       if (mine && lc != -INFINITY) d = p.softmax ? exp((double)lc - (double)top) : 1.0 / (1.0 + exp(-(double)lc));
       double each = d;
@@ -432,7 +426,7 @@ __device__ __forceinline__ int choose_token(const RouteParams& p, int t, int rea
       for (int o = 16; o > 0; o >>= 1) each += __shfl_xor_sync(0xffffffffu, each, o);
       score = each > 0 ? (float)(d / each) : 0.f;
     } else {
-      score = __fdividef(score, all);
+      score = all > 0.0f ? __fdividef(score, all) : 0.f;
     }
   }
   if (mine) {

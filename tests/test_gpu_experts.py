@@ -226,6 +226,8 @@ def test_allocated_outputs(B):
     assert B.fp8_matmul(p.x[:0], p.xs[:0], p.w[0], p.ws[0]).shape == (0, 64)
     none = B.grouped_matmul(p.x[:0], p.w, ints([0, 0]), p.xs[:0], p.ws)
     assert none.shape == (0, 64) and none.dtype is BF
+    none = B.grouped_matmul(p.x, p.w, ints([0, 0]), p.xs, p.ws, rows=ints([]))        # an empty index of rows that are there
+    assert none.shape == (0, 64)
     p = Product([5, 2], 64, 256, HALF, gather=True)
     assert p.call(B).dtype is HALF and p.call(B).shape == (7, 64) and p.call(B, out_dtype=F32).dtype is F32
 
@@ -431,6 +433,15 @@ def test_route_ends_of_the_range(B):
                 check_route(B, l, 5, scoring, bias, runs, top)
     bias = 1e4 * torch.randn(40, device="cuda")
     check_route(B, l[8:], 5, "sigmoid", bias, 5, 2)
+
+
+def test_route_weights_of_scores_far_apart(B):
+    """A normalised weight is as exact where its score is a subnormal number in FP32, or none."""
+    l = -11.0 * torch.arange(40, device="cuda").float()[None] - torch.tensor([[0.0], [30.0], [90.0], [300.0]], device="cuda")
+    for scoring in ("sigmoid", "softmax"):
+        for bias in (None, -torch.sigmoid(l[0]), 0.1 * torch.arange(40, device="cuda").float()):
+            check_route(B, l, 12, scoring, bias)
+            check_route(B, l, 12, scoring, bias, 8, 5, True, 3.0)
 
 
 @pytest.mark.parametrize("T,real", [(70, 64), (5, 0), (8, -3), (9, 20), (2500, 1999)])
