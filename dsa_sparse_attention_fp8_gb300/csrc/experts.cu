@@ -199,9 +199,10 @@ int run_variant(const dsa::MatmulParams& p, int64_t groups, cudaStream_t st) {
   const int64_t tiles = row_tiles(p.M, groups, 64) * ((p.width + 127) / 128);
   if (groups > 1 && tiles > 2 * d.sms) {
     // Bound by the weights' way from HBM.  Tiles fit the rows of a group; 256 weight rows to a tile, so that rows are read less
-    // often (64 groups, K 2048, N 7168, us with 128 / 256 weight rows and by pairs, of 16 rows to a group 199 / 165 / 183, of 32 203 / 170 / 186;
-    // tiles of 128 rows and pairs, of 48 189 / 193, of 96 243 / 206; gated, K 7168, N 4096, tiles of 64 and 128 rows and
-    // pairs, of 32 300 / 304 / 352, of 48 343 / 320 / 374, of 96 486 / 386 / 392, of 128 545 / 491 / 379).
+    // often.  Of 64 groups, in us: K 2048, N 7168, tiles of 128 and of 256 weight rows and by pairs, of 16 rows to a group 199,
+    // 165, 183, of 32 203, 170, 186; tiles of 128 rows and by pairs, of 48 189, 193, of 96 243, 206.  Gated, K 7168, N 4096,
+    // tiles of 64 and of 128 rows and by pairs, of 32 300, 304, 352, of 48 343, 320, 374, of 96 486, 386, 392, of 128 545,
+    // 491, 379.
     if (p.M <= 32 * groups) {
       if constexpr (GATED) return Few64::run(p, groups, d, st);
       else return Wide64::run(p, groups, d, st);
