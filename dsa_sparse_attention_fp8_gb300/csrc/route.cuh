@@ -464,11 +464,13 @@ __device__ __forceinline__ Counts counts_of(int* smem, int E) {
 }
 inline int counts_bytes(int warps, int E) { return ((warps + kPlaceCtas + 1) * E + warps) * 4; }
 
-// From every warp's counts to the places' bases.  All threads.
+// From every warp's counts to the places' bases.  All threads, which have arrived at the cluster's barrier (cluster_arrive):
+// no CTA writes to another that has not started.  Nothing touches another CTA after the barrier inside.
 template <int W>
 __device__ __forceinline__ void sum_counts(const RouteParams& p, const Counts& c, uint32_t rank, uint32_t ctas) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   __syncthreads();
+  if (ctas > 1) cluster_wait();
   static_assert(W * 32 >= kRouteMaxExperts, "a thread to an expert");
   const int e = tid;
   if (e < p.E) {
@@ -517,6 +519,7 @@ __global__ void __launch_bounds__(kPlaceThreads) route_place_kernel(const __grid
   extern __shared__ int smem[];
   constexpr int W = kPlaceThreads / 32;
   const uint32_t rank = cluster_rank(), ctas = cluster_size();
+  if (ctas > 1) cluster_arrive();
   const Counts c = counts_of<W>(smem, p.E);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int* const mine = c.warp + warp * p.E;
@@ -556,7 +559,6 @@ __global__ void __launch_bounds__(kPlaceThreads) route_place_kernel(const __grid
       p.rows[place] = (int32_t)((uint32_t)(i + 32 * j) / (uint32_t)p.top_k);
     }
   }
-  if (ctas > 1) cluster_sync();  // (others write to this CTA's sums)
 }
 
 // Few tokens: the choice and the places in one launch, a warp's tokens one after the other.
@@ -566,6 +568,7 @@ __global__ void __launch_bounds__(kFewThreads) route_few_kernel(const __grid_con
   constexpr int W = kFewThreads / 32;
   __shared__ alignas(8) int list[W][64];
   const uint32_t rank = cluster_rank(), ctas = cluster_size();
+  if (ctas > 1) cluster_arrive();
   const Counts c = counts_of<W>(smem, p.E);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int* const mine = c.warp + warp * p.E;
@@ -589,7 +592,6 @@ __global__ void __launch_bounds__(kFewThreads) route_few_kernel(const __grid_con
     p.places[i] = place;
     p.rows[place] = t;
   }
-  if (ctas > 1) cluster_sync();
 }
 
 }  // namespace dsa

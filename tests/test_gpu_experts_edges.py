@@ -1,0 +1,26 @@
+"""The products, the router and the experts' sum where their CTAs depend on one another, and at calls that the other tests do
+not make (GPU), against the same 64-bit formulas and bars."""
+
+import pytest
+import torch
+
+from test_gpu_experts import BF, F32, B, check_route  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("T,E,k", [(17, 8, 2), (100, 256, 8), (113, 512, 16), (127, 64, 4), (129, 256, 8), (130, 16, 1)])
+def test_route_where_some_ctas_have_no_tokens(B, T, E, k):  # noqa: F811
+    """A CTA that has nothing to choose is ready to tell the others its counts at once."""
+    torch.manual_seed(T)
+    logits, bias = torch.randn(T, E, device="cuda"), 0.05 * torch.randn(E, device="cuda")
+    check_route(B, logits, k, bias=bias)
+    outs = []
+    for _ in range(50):
+        ids, places, rows = (torch.full(s, -9, dtype=torch.int32, device="cuda") for s in ((T, k), (T, k), (T * k,)))
+        weights, starts = torch.full((T, k), -9.0, device="cuda"), torch.full((E + 1,), -9, dtype=torch.int32, device="cuda")
+        outs.append((ids, weights, starts, rows, places))
+    for o in outs:
+        B.route_experts(logits, k, *o, bias=bias)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for o in outs[1:] for a, b in zip(o, outs[0]))
