@@ -647,6 +647,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__
 
   const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
+  cluster_arrive();
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) mbar_init(full(s), p.rows ? 2 + kGatherLanes : 1), mbar_init(empty(s), 1), mbar_init(landed(s), kGatherLanes);
     for (int b = 0; b < 2; ++b) mbar_init(acc_full(b), 1), mbar_init(acc_empty(b), 16);
@@ -656,6 +657,8 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__
     tma_prefetch_desc(&tx);
     tma_prefetch_desc(&tw);
   }
+  __syncwarp();
+  cluster_wait();  // (tensor memory of a pair is asked for by both)
   if (warp == 9) {
     tmem_alloc_pair(tmem_holder, 512);
     tmem_relinquish_pair();

@@ -45,7 +45,7 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // Its halves, without ordering memory: what lies between them overlaps the wait for CTAs that have not started.  Another CTA's
-// shared memory is touched only after one such barrier, since CTAs of a cluster are placed together but do not
+// shared or tensor memory is touched only after one such barrier, since CTAs of a cluster are placed together but do not
 // start together.
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }

@@ -7,8 +7,8 @@ import pytest
 
 from kernel_source import kernels
 
-# another CTA's shared memory
-PEER = r"\b(?:st_cluster_u32|ld_cluster_v4|mbar_arrive_cluster\w*|mbar_arrive_remote)\s*\("
+# another CTA's shared memory, or tensor memory that a pair of CTAs asks for together
+PEER = r"\b(?:st_cluster_u32|ld_cluster_v4|mbar_arrive_cluster\w*|mbar_arrive_remote|tmem_alloc_pair)\s*\("
 MET = r"\b(?:cluster_sync|cluster_wait)\s*\("
 
 
