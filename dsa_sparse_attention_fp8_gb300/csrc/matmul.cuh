@@ -379,6 +379,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
 
       // rounds of kRound rows: every CTA lays its sums out, then each warp of the cluster takes rows
       for (int r0 = 0; r0 < tile.count && on; r0 += C::kRound) {
+        const bool again = more || r0 + C::kRound < tile.count;  // another round follows, in every CTA of the cluster
         if (joined) on = __all_sync(~0u, mbar_wait_cluster(join_free, (joined - 1) & 1, abort_flag));  // what lies there was read
         if (!on) break;
         if (busy && q * 32 >= r0 && q * 32 < r0 + C::kRound) {
@@ -471,7 +472,8 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
           }
         }
         __syncwarp();
-        if (lane < S) mbar_arrive_remote(map_to(join_free, lane));
+        // (given back with the cluster's scope, since other CTAs' sums were read; after the last round nobody waits)
+        if (again && lane < S) mbar_arrive_cluster(map_to(join_free, lane));
         ++joined;
       }
     }
@@ -871,7 +873,8 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__
       for (int t = blockIdx.x / 2; on && find_tile<C::BM, C::kOut>(p, groups, t, &tile); t += step) {
         for (int k = 0; k < blocks; ++k) {
           if (FP8 || k == 0) on = __all_sync(~0u, mbar_wait(acc_empty(buffer), turn ^ 1, abort_flag));
-          on = on && __all_sync(~0u, mbar_wait(full(s), phase, abort_flag));
+          // (of gathered rows the second CTA's are among what the barrier tells of: written there, multiplied here)
+          if (on) on = __all_sync(~0u, p.rows ? mbar_wait_cluster(full(s), phase, abort_flag) : mbar_wait(full(s), phase, abort_flag));
           if (!on) break;
           if (p.rows) fence_proxy_async_smem();
           tc_fence_after();
@@ -905,7 +908,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__
             on = mbar_wait(landed(s), phase, abort_flag);
             if (!on) break;
             fence_proxy_async_smem();
-            mbar_arrive_remote(map_to(full(s), 0));
+            mbar_arrive_cluster(map_to(full(s), 0));
             if (++s == C::kStages) s = 0, phase ^= 1;
           }
         }

@@ -101,10 +101,6 @@ __device__ __forceinline__ void copies_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void copies_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-// Arrival at a barrier of any CTA of the cluster.
-__device__ __forceinline__ void mbar_arrive_remote(uint32_t addr) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
-}
 
 // D[tmem] (+)= A[smem] B[smem]^T over 128 bytes of K, both operands K-major in the 128-byte swizzle layout, one CTA.  Issued by
 // one thread.

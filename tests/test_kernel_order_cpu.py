@@ -5,7 +5,7 @@ import re
 
 import pytest
 
-from kernel_source import kernels
+from kernel_source import CSRC, kernels
 
 # another CTA's shared memory, or tensor memory that a pair of CTAs asks for together
 PEER = r"\b(?:st_cluster_u32|ld_cluster_v4|mbar_arrive_cluster\w*|mbar_arrive_remote|tmem_alloc_pair)\s*\("
@@ -23,3 +23,19 @@ def test_a_cta_touches_another_only_after_they_have_met(file):
             seen += 1
             assert met and met.start() < touch.start(), f"{name}: {touch.group(0)} before any cluster barrier"
     assert seen == 2
+
+
+def test_arrivals_at_another_cta_have_the_clusters_scope():
+    """An arrival without a scope orders memory within its own CTA alone.  Relaxed ones are for accumulators, whose reads the
+    tensor core's own fences order."""
+    arrivals = re.findall(r'"(mbarrier\.arrive[^ ]*shared::cluster[^ ]*)', (CSRC / "ptx_matmul.cuh").read_text())
+    assert arrivals and all(re.match(r"mbarrier\.arrive\.(release|relaxed)\.cluster\.", a) for a in arrivals), arrivals
+    many = kernels("matmul.cuh")["many_rows_kernel"]
+    assert set(re.findall(r"mbar_arrive_cluster_relaxed\(map_to\((\w+)", many)) == {"acc_empty"}
+
+
+def test_rows_that_the_second_cta_gathered_are_waited_for_with_the_clusters_scope():
+    """The second CTA arrives at the first one's barrier of a stage, and the first multiplies what the second has written."""
+    many = kernels("matmul.cuh")["many_rows_kernel"]
+    product = many[many.index("warp == 9 && rank == 0"):many.index("umma_f8_k128_pair")]
+    assert re.search(r"p\.rows \? mbar_wait_cluster\(full\(s\)", product)
