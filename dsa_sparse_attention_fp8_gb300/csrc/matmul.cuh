@@ -58,7 +58,7 @@ __device__ __forceinline__ void load_groups(const MatmulParams& p, const Groups&
   for (int e = threadIdx.x; e < p.E; e += kMatmulThreads) {
     int b = 0, n = p.M;
     if (p.starts) {
-      b = __ldg(p.starts + e), n = __ldg(p.starts + e + 1);
+      b = ld_early(p.starts + e), n = ld_early(p.starts + e + 1);
       if (b < 0 || n > p.M || n < b) {
         if (blockIdx.x == 0) raise_status(p.status, kStatusBadMetadata);
         b = n = 0;
@@ -156,7 +156,7 @@ __device__ __forceinline__ bool gather_rows(const MatmulParams& p, const Groups&
     uint32_t from[16];  // and start these many pieces into x
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const int r = 8 * i + own < mine ? __ldg(p.rows + tile.row + offset + 8 * i + own) : 0;
+      const int r = 8 * i + own < mine ? ld_early(p.rows + tile.row + offset + 8 * i + own) : 0;
       from[i] = r < 0 || r >= p.x_rows ? 0 : (uint32_t)r * row_pieces;
     }
     const uint8_t* const x = static_cast<const uint8_t*>(p.x) + piece * 16;
@@ -315,7 +315,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
     Tile ahead;
     const auto row_of = [&](const Tile& of) {
       const int row = q * 32 + lane;
-      return row >= of.count ? 0 : p.rows ? ld_ahead(p.rows + of.row + row) : of.row + row;
+      return row >= of.count ? 0 : p.rows ? ld_early(p.rows + of.row + row) : of.row + row;
     };
     const auto scales_of = [&](const Tile& of, int src, const float** xs, const float** ws, const float** wu) {
       const int n0 = GATED ? of.column + 64 * half : WIDE ? of.column + 128 * half : of.column;
@@ -327,7 +327,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
     const auto first_scales = [&](const Tile& of, int src) {
       const float *xs, *ws, *wu;
       scales_of(of, src, &xs, &ws, &wu);
-      s_next = ld_ahead(xs + k0), g_next = ld_ahead(ws + k0), u_next = GATED ? ld_ahead(wu + k0) : 0.f;
+      s_next = ld_early(xs + k0), g_next = ld_early(ws + k0), u_next = GATED ? ld_early(wu + k0) : 0.f;
     };
     int t = blockIdx.x / S;
     bool more = find_tile<BM, C::kOut>(p, groups, t, &ahead);
@@ -352,8 +352,8 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
         for (int k = k0; k < k1; ++k) {
           const float f = s_next * g_next, u = GATED ? s_next * u_next : f;
           const int at = min(k + 1, k1 - 1);
-          s_next = ld_ahead(xs + at), g_next = ld_ahead(ws + at);
-          if (GATED) u_next = ld_ahead(wu + at);
+          s_next = ld_early(xs + at), g_next = ld_early(ws + at);
+          if (GATED) u_next = ld_early(wu + at);
           on = __all_sync(~0u, mbar_wait(acc_full(buffer), turn, abort_flag));
           if (!on) break;
           tc_fence_after();
@@ -700,7 +700,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__
       int src = 0;
       bool bad = false;
       if (lane < rows) {
-        src = p.rows ? __ldg(p.rows + row0 + lane) : (int)row0 + lane;
+        src = p.rows ? ld_early(p.rows + row0 + lane) : (int)row0 + lane;
         bad = src < 0 || src >= p.x_rows;
         if (bad) src = 0;
         if (bad && half == 0) raise_status(p.status, kStatusBadMetadata);
@@ -714,12 +714,12 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__
         const float* const ws = p.w_scales + ((int64_t)tile.e * p.nb + min(p.nb - 1, n0 / kMatmulBlock)) * p.kb;
         const float* const wu = p.w_scales + ((int64_t)tile.e * p.nb + min(p.nb - 1, (p.width + n0) / kMatmulBlock)) * p.kb;
         // (a block's scales are loaded while the block before is summed)
-        float s_next = ld_ahead(xs + 0), g_next = ld_ahead(ws + 0), u_next = GATED ? ld_ahead(wu + 0) : 0.f;
+        float s_next = ld_early(xs + 0), g_next = ld_early(ws + 0), u_next = GATED ? ld_early(wu + 0) : 0.f;
         for (int k = 0; k < blocks; ++k) {
           const float f = s_next * g_next, u = GATED ? s_next * u_next : f;
           const int at = min(k + 1, blocks - 1);
-          s_next = ld_ahead(xs + at), g_next = ld_ahead(ws + at);
-          if (GATED) u_next = ld_ahead(wu + at);
+          s_next = ld_early(xs + at), g_next = ld_early(ws + at);
+          if (GATED) u_next = ld_early(wu + at);
           on = __all_sync(~0u, mbar_wait(acc_full(buffer), turn, abort_flag));
           if (!on) break;
           tc_fence_after();

@@ -8,10 +8,16 @@
 
 namespace dsa {
 
-// A read-only load that stays where it stands, ahead of its use.
-__device__ __forceinline__ float ld_ahead(const float* p) {
+// Loads that stay where they stand, ahead of their use: ordinary ones, as a kernel that is launched programmatically lives
+// while the one before it still writes what is loaded here (read-only loads promise that nobody does).
+__device__ __forceinline__ float ld_early(const float* p) {
   float v;
-  asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ int32_t ld_early(const int32_t* p) {
+  int32_t v;
+  asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p));
   return v;
 }
 

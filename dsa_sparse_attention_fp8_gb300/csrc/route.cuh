@@ -201,7 +201,7 @@ __device__ __forceinline__ F value_keys(const RouteParams& p, const float (&l)[V
   }
   if (p.bias) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) s[i] += (F)__ldg(p.bias + own.at(i));
+    for (int i = 0; i < V; ++i) s[i] += (F)p.bias[own.at(i)];
   }
 #pragma unroll
   for (int i = 0; i < V; ++i) key[i] = i < own.count ? order_key(s[i]) : 0;

@@ -4,7 +4,7 @@ not make (GPU), against the same 64-bit formulas and bars."""
 import pytest
 import torch
 
-from test_gpu_experts import F32, B, Product, check_route  # noqa: F401
+from test_gpu_experts import BF, E4M3, F32, U8, B, Product, check_route  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -42,3 +42,67 @@ def test_what_ctas_hand_to_one_another(B, counts, N, K, gather, gated, calls):  
     want = p.call(B, out_dtype=F32)
     got = [p.call(B, out_dtype=F32) for _ in range(calls)]
     assert all(torch.equal(g, want) for g in got)
+
+
+def e4m3(*shape):
+    return (100 * torch.randn(*shape, device="cuda")).clamp(-448, 448).to(E4M3).view(U8)
+
+
+def test_a_call_right_behind_another_sees_its_scales(B):  # noqa: F811
+    """A chain of products in which each reads the codes and the scales that the one before has just written, of inputs that
+    change from chain to chain in the same buffers: as with a wait after each call."""
+    torch.manual_seed(4)
+    n, sizes = 512, [700, 700, 300, 64, 1]
+    w, ws = e4m3(2 * n, n), torch.full((8, 4), 1.6 * n ** -0.5 / 100, device="cuda")
+    codes, scales = [torch.empty(700, n, dtype=U8, device="cuda") for _ in sizes], [torch.empty(700, 4, device="cuda") for _ in sizes]
+    inputs = [(e4m3(700, n), (0.5 + torch.rand(700, 4, device="cuda")) / 100) for _ in range(10)]
+
+    def chains(wait):
+        got = []
+        for c, s in inputs:
+            codes[0].copy_(c), scales[0].copy_(s)
+            for i in range(1, len(sizes)):
+                t = sizes[i]
+                B.fp8_matmul(codes[i - 1][:t], scales[i - 1][:t], w, ws, gated=True, out_codes=codes[i][:t], out_scales=scales[i][:t])
+                if wait:
+                    torch.cuda.synchronize()
+            got.append([x[i][:sizes[i]].clone() for i in range(1, len(sizes)) for x in (codes, scales)])
+        torch.cuda.synchronize()
+        return got
+    want = chains(True)
+    assert all(s.isfinite().all() and (s > 0).all() for one in want for s in one[1::2])
+    assert len({one[1][0, 0].item() for one in want}) == len(inputs)               # (scales that a stale one would change)
+    for _ in range(10):
+        assert all(torch.equal(a, b) for x, y in zip(chains(False), want) for a, b in zip(x, y))
+
+
+@pytest.mark.parametrize("T", [40, 1500])
+def test_steps_right_behind_one_another_see_each_others_results(B, T):  # noqa: F811
+    """Router, gathered product, product and sum over the same buffers, step after step with nothing between them: groups,
+    rows, scales, places and weights are all fresh from the call before."""
+    torch.manual_seed(T)
+    E, k, n, i32 = 12, 3, 256, torch.int32
+    x, xs = e4m3(T, n), (0.5 + torch.rand(T, 2, device="cuda")) / 100
+    w1, s1 = e4m3(E, 2 * n, n), torch.full((E, 4, 2), n ** -0.5 / 100, device="cuda")
+    w2, s2 = e4m3(E, n, n), torch.full((E, 2, 2), n ** -0.5 / 100, device="cuda")
+    ids, places, rows = (torch.empty(s, dtype=i32, device="cuda") for s in ((T, k), (T, k), (T * k,)))
+    weights, starts = torch.empty(T, k, device="cuda"), torch.empty(E + 1, dtype=i32, device="cuda")
+    h, hs, y = torch.empty(T * k, n, dtype=U8, device="cuda"), torch.empty(T * k, 2, device="cuda"), torch.empty(T * k, n, dtype=BF, device="cuda")
+    logits = [torch.randn(T, E, device="cuda") for _ in range(10)]
+
+    def steps(wait):
+        outs = [torch.empty(T, n, dtype=BF, device="cuda") for _ in logits]
+        for l, out in zip(logits, outs):
+            for call in (lambda: B.route_experts(l, k, ids, weights, starts, rows, places),
+                         lambda: B.grouped_matmul(x, w1, starts, xs, s1, rows=rows, gated=True, out_codes=h, out_scales=hs),
+                         lambda: B.grouped_matmul(h, w2, starts, hs, s2, out=y),
+                         lambda: B.combine_experts(y, places, weights, out=out)):
+                call()
+                if wait:
+                    torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return outs
+    want = steps(True)
+    assert not any(torch.equal(a, want[0]) for a in want[1:])
+    for _ in range(10):
+        assert all(torch.equal(a, b) for a, b in zip(steps(False), want))

@@ -39,3 +39,11 @@ def test_rows_that_the_second_cta_gathered_are_waited_for_with_the_clusters_scop
     many = kernels("matmul.cuh")["many_rows_kernel"]
     product = many[many.index("warp == 9 && rank == 0"):many.index("umma_f8_k128_pair")]
     assert re.search(r"p\.rows \? mbar_wait_cluster\(full\(s\)", product)
+
+
+@pytest.mark.parametrize("file", ["matmul.cuh", "ptx_matmul.cuh", "route.cuh", "combine.cuh"])
+def test_what_the_kernel_before_writes_is_read_by_ordinary_loads(file):
+    """A kernel launched programmatically lives while the one before it writes: read-only loads (__ldg, .nc, and ptx.cuh's
+    ld_ahead, which is one) would promise that nobody does."""
+    text = re.sub(r"//[^\n]*", "", (CSRC / file).read_text())
+    assert not re.search(r"__ldg\b|ld\.global\.nc|\bld_ahead\w*\(|__restrict__", text)
