@@ -249,7 +249,8 @@ int run_matmul(dsa::MatmulParams p, int64_t groups, cudaStream_t st) {
   p.kb = (p.K + dsa::kMatmulBlock - 1) / dsa::kMatmulBlock;
   p.nb = (p.N + dsa::kMatmulBlock - 1) / dsa::kMatmulBlock;
   if (!fp8) p.x_scales = p.w_scales = nullptr;
-  p.give_up = env_int("DSA_WAIT_LIMIT", (int)dsa::kWaitLimit, 0, (int)dsa::kWaitLimit) == 0;
+  p.load_stages = env_int("DSA_LOAD_STAGES", -1, -1, 1 << 20);
+  if (env_int("DSA_WAIT_LIMIT", (int)dsa::kWaitLimit, 0, (int)dsa::kWaitLimit) == 0) p.load_stages = 0;
   if (fp8) return p.gated ? run_variant<true, true>(p, groups, st) : run_variant<true, false>(p, groups, st);
   return p.gated ? run_variant<false, true>(p, groups, st) : run_variant<false, false>(p, groups, st);
 }

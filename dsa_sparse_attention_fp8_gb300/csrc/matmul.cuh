@@ -37,7 +37,8 @@ struct MatmulParams {
   int64_t x_stride, w_stride, w_group, out_stride;  // elements
   int x_rows, M, N, K, E, width, kb, nb;            // width: N, or N / 2 where gated
   int x_type, out_type, most_tiles, box;            // row tiles that there can be, rows of a load
-  bool gated, give_up;
+  int load_stages;  // after so many stages loading warps give up (tests of the unwinding); -1: never
+  bool gated;
 };
 
 // ---------------------------------------------------------------- tiles
@@ -130,6 +131,35 @@ __device__ __forceinline__ void take_block(uint32_t from, uint64_t (&acc)[COLS /
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[16 * c + i] = pack2(__uint_as_float(d[2 * i]), __uint_as_float(d[2 * i + 1]));
   }
+}
+
+// ---------------------------------------------------------------- unwinding
+// Every wait is bounded.  A role whose wait runs out raises the flag of each CTA that works on the tile and leaves; so do the
+// others when they see it.  Copies and products under way then end before the CTA does: the loading and the product warp
+// leave word of where they stopped, which is read once every role has left.  A barrier that copies alone arrive at tells
+// of their end (gathered rows, whose warps wait for their own copies, have barriers of their own).
+struct Stopped {
+  int s, phase;   // the stage that would have come next, and its pass
+  uint32_t used;  // stages that were ever filled
+};
+__device__ __forceinline__ void tell_stop(uint32_t at, int s, int phase, uint32_t used) {
+  if ((threadIdx.x & 31) == 0) sts_u32(at, (uint32_t)s | (uint32_t)phase << 7 | used << 8);
+}
+__device__ __forceinline__ Stopped where_stopped(uint32_t at) {
+  const uint32_t v = lds_u32(at);
+  return {(int)(v & 127), (int)(v >> 7 & 1), v >> 8};
+}
+__device__ __forceinline__ void end_loads(const Stopped& l, uint32_t full, int stages) {
+  for (int i = 0; i < stages; ++i)
+    if (l.used >> i & 1) mbar_wait(full + 8 * i, i < l.s ? l.phase : l.phase ^ 1, nullptr);
+}
+// (the last products' commit is that of the stage before; of none the barrier is as it was made)
+__device__ __forceinline__ void end_products(const Stopped& m, uint32_t empty, int stages) {
+  mbar_wait(empty + 8 * (m.s == 0 ? stages - 1 : m.s - 1), m.s == 0 ? m.phase ^ 1 : m.phase, nullptr);
+}
+// How many stages a loading warp may fill, -1 for all of them; CTAs of odd rank one more or less, so that a pair's stop apart.
+__device__ __forceinline__ int stages_to_fill(const MatmulParams& p, uint32_t rank) {
+  return p.load_stages > 0 ? p.load_stages ^ (int)(rank & 1) : p.load_stages;
 }
 
 // ---------------------------------------------------------------- gathered rows
@@ -264,11 +294,13 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
   const auto acc_full = [&](int b) { return bars + 128 + 8 * b; };
   const auto acc_empty = [&](int b) { return bars + 160 + 8 * b; };
   const uint32_t join_full = bars + 192, join_free = bars + 200;
+  const auto landed = [&](int s) { return bars + 208 + 8 * s; };  // gathered rows
+  const uint32_t loads_stopped = bars + 484, products_stopped = bars + 488;
 
   const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t S = cluster_size(), rank = cluster_rank();
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::kStages; ++s) mbar_init(full(s), p.rows ? 1 + kGatherLanes : 1), mbar_init(empty(s), 1);
+    for (int s = 0; s < C::kStages; ++s) mbar_init(full(s), 1), mbar_init(empty(s), 1), mbar_init(landed(s), kGatherLanes);
     for (int b = 0; b < C::kBuffers; ++b) mbar_init(acc_full(b), 1), mbar_init(acc_empty(b), 8);
     mbar_init(join_full, 8 * S);
     mbar_init(join_free, 8 * S);
@@ -292,6 +324,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
   const uint32_t tmem = lds_u32(tmem_holder);
   const auto quit = [&] {
     *abort_flag = 1;
+    for (uint32_t r = 0; S > 1 && r < S; ++r) st_cluster_u32(map_to(bars + 496, r), 1);
     raise_status(p.status, kStatusTimeout);
   };
 
@@ -482,18 +515,18 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
     regs_shrink<72>();
     if (warp == 8) {
       // ------------------------------------------------ loads
-      int s = 0, phase = 0;
-      uint32_t used = 0;  // stages that were ever filled
-      bool on = !p.give_up;
-      if (!on) quit();
+      int s = 0, phase = 0, left = stages_to_fill(p, rank);
+      uint32_t used = 0;
+      bool on = true;
       for (int t = blockIdx.x / S; on && find_tile<BM, C::kOut>(p, groups, t, &tile); t += step) {
         const int boxes = p.rows ? 0 : (tile.count + p.box - 1) / p.box;
         const uint32_t bytes = C::kStageB + boxes * p.box * 128;
         for (int k = k0; k < k1; ++k) {
-          if (!__all_sync(~0u, mbar_wait(empty(s), phase ^ 1, abort_flag))) {
+          if (left == 0 || !__all_sync(~0u, mbar_wait(empty(s), phase ^ 1, abort_flag))) {
             on = false;
             break;
           }
+          left -= left > 0;
           const uint32_t a = stages + s * C::kStage, b = a + C::kStageA;
           const int x = k * C::kK;
           if (elect_one()) {
@@ -510,12 +543,8 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
           if (++s == C::kStages) s = 0, phase ^= 1;
         }
       }
-      if (!on) {
-        // the copies under way end before the CTA does
-        quit();
-        for (int i = 0; i < C::kStages; ++i)
-          if (used >> i & 1) mbar_wait(full(i), (i < s ? phase : phase ^ 1), nullptr);
-      }
+      tell_stop(loads_stopped, s, phase, used);
+      if (!on) quit();
     } else if (warp == 9) {
       // ------------------------------------------------ products
       const uint32_t idesc = FP8 ? idesc_e4m3_f32(128, C::BN) : idesc_16_f32(p.x_type == 0, 128, C::BN, false);
@@ -525,6 +554,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
         for (int k = k0; k < k1; ++k) {
           if (FP8 || k == k0) on = __all_sync(~0u, mbar_wait(acc_empty(buffer), turn ^ 1, abort_flag));
           on = on && __all_sync(~0u, mbar_wait(full(s), phase, abort_flag));
+          if (on && p.rows) on = __all_sync(~0u, mbar_wait(landed(s), phase, abort_flag));
           if (!on) break;
           if (p.rows) fence_proxy_async_smem();
           tc_fence_after();
@@ -542,18 +572,14 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
           if (++s == C::kStages) s = 0, phase ^= 1;
         }
       }
-      if (!on) {
-        quit();
-        // products under way end before the CTA does: their last commit is that of the stage before
-        const int last = s == 0 ? C::kStages - 1 : s - 1;
-        mbar_wait(empty(last), s == 0 ? phase ^ 1 : phase, nullptr);
-      }
+      tell_stop(products_stopped, s, phase, 0);
+      if (!on) quit();
     } else if (p.rows) {
       // ------------------------------------------------ gathered rows
       const int g = warp - 10;
       if (!gather_rows<C::kStages, C::kStage, BM, C::kOut>(
               p, groups, blockIdx.x / S, step, 0, BM, FP8 ? 1 : 2, k0, k1, stages,
-              g, abort_flag, bars + 64, bars))
+              g, abort_flag, empty(0), landed(0)))
         quit();
     }
   }
@@ -561,6 +587,11 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
   tc_fence_before();
   if (S > 1) cluster_sync(); else __syncthreads();
   tc_fence_after();
+  if (*abort_flag) {
+    if (warp == 8) end_loads(where_stopped(loads_stopped), full(0), C::kStages);
+    if (warp == 9) end_products(where_stopped(products_stopped), empty(0), C::kStages);
+    __syncwarp();
+  }
   if (warp == 9) tmem_dealloc(tmem, 512);
 }
 
@@ -644,14 +675,16 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__
   const auto empty = [&](int s) { return bars + 64 + 8 * s; };
   const auto acc_full = [&](int b) { return bars + 128 + 8 * b; };
   const auto acc_empty = [&](int b) { return bars + 144 + 8 * b; };  // (the first CTA's)
-  const auto landed = [&](int s) { return bars + 200 + 8 * s; };     // the second CTA's gathered rows
+  const auto landed = [&](int s) { return bars + 200 + 8 * s; };     // each CTA's gathered rows, in the first's the second's too
   const auto both = [&](int q) { return bars + 160 + 8 * q; };       // a row's two warps
+  const uint32_t loads_stopped = bars + 484, products_stopped = bars + 488;
+  const uint32_t fills = bars + 464;  // this CTA's: how many, and of the last 32 whether the second CTA had rows; then the other's
 
   const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   cluster_arrive();
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::kStages; ++s) mbar_init(full(s), p.rows ? 2 + kGatherLanes : 1), mbar_init(empty(s), 1), mbar_init(landed(s), kGatherLanes);
+    for (int s = 0; s < C::kStages; ++s) mbar_init(full(s), 1), mbar_init(empty(s), 1), mbar_init(landed(s), rank == 0 ? kGatherLanes + 1 : kGatherLanes);
     for (int b = 0; b < 2; ++b) mbar_init(acc_full(b), 1), mbar_init(acc_empty(b), 16);
     for (int q = 0; q < 4; ++q) mbar_init(both(q), 2);
     *abort_flag = 0;
@@ -830,18 +863,19 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__
     regs_shrink<72>();
     if (warp == 8) {
       // ------------------------------------------------ loads
-      int s = 0, phase = 0;
-      uint32_t used = 0;  // stages that were ever filled
-      bool on = !p.give_up;
+      int s = 0, phase = 0, left = stages_to_fill(p, rank);
+      uint32_t used = 0, filled = 0, seconds = 0;
+      bool on = true;
       for (int t = blockIdx.x / 2; on && find_tile<C::BM, C::kOut>(p, groups, t, &tile); t += step) {
         // a box of 128 rows for each CTA that has some
         const bool second = tile.count > 128, boxed = !p.rows && (rank == 0 || second);
         const uint32_t bytes = 2 * C::kStageB + (p.rows ? 0 : second ? 2 : 1) * C::kStageA;
         for (int k = 0; k < blocks; ++k) {
-          if (!__all_sync(~0u, mbar_wait(empty(s), phase ^ 1, abort_flag))) {
+          if (left == 0 || !__all_sync(~0u, mbar_wait(empty(s), phase ^ 1, abort_flag))) {
             on = false;
             break;
           }
+          left -= left > 0;
           const uint32_t a = stages + s * C::kStage, b = a + C::kStageA, bar = map_to(full(s), 0);
           const int x = k * C::kK;
           if (elect_one()) {
@@ -856,15 +890,13 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__
           }
           __syncwarp();
           used |= 1u << s;
+          ++filled, seconds = seconds << 1 | second;
           if (++s == C::kStages) s = 0, phase ^= 1;
         }
       }
-      if (!on) {
-        // the copies of both CTAs under way end before either does
-        quit();
-        for (int i = 0; i < C::kStages && rank == 0; ++i)
-          if (used >> i & 1) mbar_wait(full(i), (i < s ? phase : phase ^ 1), nullptr);
-      }
+      tell_stop(loads_stopped, s, phase, used);
+      if (lane == 0) sts_u32(fills, filled), sts_u32(fills + 4, seconds);
+      if (!on) quit();
     } else if (warp == 9 && rank == 0) {
       // ------------------------------------------------ products of both CTAs
       const uint32_t idesc = FP8 ? idesc_e4m3_f32(256, 256) : idesc_16_f32(p.x_type == 0, 256, 256, false);
@@ -873,8 +905,9 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__
       for (int t = blockIdx.x / 2; on && find_tile<C::BM, C::kOut>(p, groups, t, &tile); t += step) {
         for (int k = 0; k < blocks; ++k) {
           if (FP8 || k == 0) on = __all_sync(~0u, mbar_wait(acc_empty(buffer), turn ^ 1, abort_flag));
-          // (of gathered rows the second CTA's are among what the barrier tells of: written there, multiplied here)
-          if (on) on = __all_sync(~0u, p.rows ? mbar_wait_cluster(full(s), phase, abort_flag) : mbar_wait(full(s), phase, abort_flag));
+          on = on && __all_sync(~0u, mbar_wait(full(s), phase, abort_flag));
+          // (the second CTA's are among them: written there, multiplied here)
+          if (on && p.rows) on = __all_sync(~0u, mbar_wait_cluster(landed(s), phase, abort_flag));
           if (!on) break;
           if (p.rows) fence_proxy_async_smem();
           tc_fence_after();
@@ -892,12 +925,8 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__
           if (++s == C::kStages) s = 0, phase ^= 1;
         }
       }
-      if (!on) {
-        quit();
-        // products under way end before the CTAs do: their last commit is that of the stage before
-        const int last = s == 0 ? C::kStages - 1 : s - 1;
-        mbar_wait(empty(last), s == 0 ? phase ^ 1 : phase, nullptr);
-      }
+      tell_stop(products_stopped, s, phase, 0);
+      if (!on) quit();
     } else if (warp == 9 && p.rows) {
       // ------------------------------------------------ the second CTA's gathered rows, told to the first
       if (lane == 0) {
@@ -908,7 +937,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__
             on = mbar_wait(landed(s), phase, abort_flag);
             if (!on) break;
             fence_proxy_async_smem();
-            mbar_arrive_cluster(map_to(full(s), 0));
+            mbar_arrive_cluster(map_to(landed(s), 0));
             if (++s == C::kStages) s = 0, phase ^= 1;
           }
         }
@@ -920,7 +949,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__
       const int g = warp - 10;
       if (!gather_rows<C::kStages, C::kStage, C::BM, C::kOut>(
               p, groups, blockIdx.x / 2, step, 128 * (int)rank, 128, FP8 ? 1 : 2, 0, blocks, stages,
-              g, abort_flag, bars + 64, rank ? bars + 200 : bars))
+              g, abort_flag, empty(0), landed(0)))
         quit();
     }
   }
@@ -928,6 +957,29 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__
   tc_fence_before();
   cluster_sync();
   tc_fence_after();
+  if (*abort_flag) {  // (the same in both CTAs)
+    if (rank == 1 && threadIdx.x < 2) st_cluster_u32(map_to(fills + 8 + 4 * threadIdx.x, 0), lds_u32(fills + 4 * threadIdx.x));
+    if (rank == 0 && warp == 9) end_products(where_stopped(products_stopped), empty(0), C::kStages);
+    __syncwarp();
+    cluster_sync();
+    // Both CTAs' copies arrive at the first's barriers, which expect those of both.  Where the second stopped earlier, its
+    // bytes are taken off; where it went on, its copies alone are expected.
+    if (rank == 0 && threadIdx.x == 256) {
+      Stopped l = where_stopped(loads_stopped);
+      const int ahead = (int)(lds_u32(fills + 8) - lds_u32(fills));
+      const auto bytes = [&](bool rows) { return C::kStageB + (rows && !p.rows ? C::kStageA : 0u); };
+      for (int i = 1; i <= -ahead; ++i)
+        mbar_complete_tx(full((l.s + C::kStages - i) % C::kStages), bytes(lds_u32(fills + 4) >> (i - 1) & 1));
+      for (int i = ahead - 1; i >= 0; --i) {
+        mbar_arrive_expect_tx(full(l.s), bytes(lds_u32(fills + 12) >> i & 1));
+        l.used |= 1u << l.s;
+        if (++l.s == C::kStages) l.s = 0, l.phase ^= 1;
+      }
+      end_loads(l, full(0), C::kStages);
+    }
+    __syncwarp();
+    cluster_sync();
+  }
   if (warp == 9) tmem_dealloc_pair(tmem, 512);
 }
 

@@ -97,6 +97,11 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
   return false;
 }
 
+// Takes bytes that no copy will bring off those that a barrier of this CTA expects.
+__device__ __forceinline__ void mbar_complete_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
 // ---------------------------------------------------------------- gathered loads
 // 16 bytes to shared memory, of which the first `bytes` are read and the others are zeros.
 __device__ __forceinline__ void copy16_async(uint32_t dst, const void* src, uint32_t bytes) {

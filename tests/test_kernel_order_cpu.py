@@ -38,7 +38,9 @@ def test_rows_that_the_second_cta_gathered_are_waited_for_with_the_clusters_scop
     """The second CTA arrives at the first one's barrier of a stage, and the first multiplies what the second has written."""
     many = kernels("matmul.cuh")["many_rows_kernel"]
     product = many[many.index("warp == 9 && rank == 0"):many.index("umma_f8_k128_pair")]
-    assert re.search(r"p\.rows \? mbar_wait_cluster\(full\(s\)", product)
+    assert re.search(r"p\.rows\)? .*mbar_wait_cluster\(landed\(s\)", product)
+    told = many[many.index("warp == 9 && p.rows"):many.index("warp >= 10 && p.rows")]
+    assert re.search(r"fence_proxy_async_smem\(\);\s*mbar_arrive_cluster\(map_to\(landed\(s\), 0\)\)", told)
 
 
 @pytest.mark.parametrize("file", ["matmul.cuh", "ptx_matmul.cuh", "route.cuh", "combine.cuh"])
