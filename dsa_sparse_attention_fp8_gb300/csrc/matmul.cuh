@@ -506,7 +506,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
         }
         __syncwarp();
         // (given back with the cluster's scope, since other CTAs' sums were read; after the last round nobody waits)
-        if (again && lane < S) mbar_arrive_cluster(map_to(join_free, lane));
+        if (again && lane < S) S > 1 ? mbar_arrive_cluster(map_to(join_free, lane)) : mbar_arrive(join_free);
         ++joined;
       }
     }
@@ -907,7 +907,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__
           if (FP8 || k == 0) on = __all_sync(~0u, mbar_wait(acc_empty(buffer), turn ^ 1, abort_flag));
           on = on && __all_sync(~0u, mbar_wait(full(s), phase, abort_flag));
           // (the second CTA's are among them: written there, multiplied here)
-          if (on && p.rows) on = __all_sync(~0u, mbar_wait_cluster(landed(s), phase, abort_flag));
+          if (on && p.rows) on = __all_sync(~0u, mbar_wait_cluster<true>(landed(s), phase, abort_flag));
           if (!on) break;
           if (p.rows) fence_proxy_async_smem();
           tc_fence_after();
@@ -937,7 +937,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__
             on = mbar_wait(landed(s), phase, abort_flag);
             if (!on) break;
             fence_proxy_async_smem();
-            mbar_arrive_cluster(map_to(landed(s), 0));
+            mbar_arrive_shared(map_to(landed(s), 0));
             if (++s == C::kStages) s = 0, phase ^= 1;
           }
         }
