@@ -144,9 +144,9 @@ struct Few {
     CUtensorMap tx, tw;
     p.box = p.M <= 32 * groups ? 32 : BM;
     if (const int rc = product_maps(p, p.box, C::kBox, &tx, &tw)) return rc;
-    const int64_t rows = row_tiles(p.M, groups, BM), tiles = rows * ((p.width + C::kOut - 1) / C::kOut);
+    const int64_t columns = (p.width + C::kOut - 1) / C::kOut, tiles = row_tiles(p.M, groups, BM) * columns;
     if (tiles > INT32_MAX / 2) return fail(DSA_ERR_UNSUPPORTED, "%lld tiles of results", (long long)tiles);
-    p.most_tiles = (int)rows;
+    p.most_tiles = (int)(INT32_MAX / 2 / columns);
     set_last_launches(1);
     return launch("few_rows_kernel", kKernel, (unsigned)(std::min<int64_t>(tiles, plan.clusters) * plan.size), dsa::kMatmulThreads, plan.size,
                   C::kSmem, st, tx, tw, p);
@@ -178,9 +178,9 @@ struct Many {
   static int run(dsa::MatmulParams p, int64_t groups, const Plan& plan, cudaStream_t st) {
     CUtensorMap tx, tw;
     if (const int rc = product_maps(p, 128, C::kBox, &tx, &tw)) return rc;
-    const int64_t rows = row_tiles(p.M, groups, C::BM), tiles = rows * ((p.width + C::kOut - 1) / C::kOut);
+    const int64_t columns = (p.width + C::kOut - 1) / C::kOut, tiles = row_tiles(p.M, groups, C::BM) * columns;
     if (tiles > INT32_MAX / 2) return fail(DSA_ERR_UNSUPPORTED, "%lld tiles of results", (long long)tiles);
-    p.most_tiles = (int)rows;
+    p.most_tiles = (int)(INT32_MAX / 2 / columns);
     set_last_launches(1);
     return launch("many_rows_kernel", kKernel, (unsigned)(std::min<int64_t>(tiles, plan.clusters) * 2), dsa::kMatmulThreads, 2, C::kSmem, st, tx, tw, p);
   }

@@ -36,7 +36,7 @@ struct MatmulParams {
   int32_t* status;
   int64_t x_stride, w_stride, w_group, out_stride;  // elements
   int x_rows, M, N, K, E, width, kb, nb;            // width: N, or N / 2 where gated
-  int x_type, out_type, most_tiles, box;            // row tiles that there can be, rows of a load
+  int x_type, out_type, most_tiles, box;            // row tiles whose numbers fit, rows of a load
   int load_stages;  // after so many stages loading warps give up (tests of the unwinding); -1: never
   bool gated;
 };
@@ -69,7 +69,8 @@ __device__ __forceinline__ void load_groups(const MatmulParams& p, const Groups&
     g.end[e] = n;
   }
 }
-// One warp.  Groups that overlap may have more rows than there are: tiles past `most` are dropped.
+// One warp.  Groups that overlap, which only starts that go back make, may together have many times the rows that there are:
+// all their tiles count, up to the `most` whose numbers fit 31 bits.
 template <int BM>
 __device__ __forceinline__ void count_tiles(int E, int most, const Groups& g) {
   const int lane = threadIdx.x & 31;

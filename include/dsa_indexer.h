@@ -611,8 +611,9 @@ int dsa_fp8_matmul(const uint8_t* codes, int64_t stride, const float* scales, in
  * Faults: a group that is not within [0, M] or ends before it starts is
  * skipped, an index in rows outside [0, x_rows) gives a row of zeros:
  * DSA_STATUS_BAD_METADATA.  (Groups that overlap, which only starts that go
- * back make, leave either's result in the rows they share.)  DSA_STATUS_TIMEOUT
- * as above.  Errors: INVALID_ARG, UNSUPPORTED, CUDA.
+ * back make, leave either's result in each element they share, and take the
+ * time of their rows together.)  DSA_STATUS_TIMEOUT as above.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA.
  */
 int dsa_grouped_matmul(const void* x, int64_t x_stride, const float* x_scales, int x_type, int x_rows,
                        const int32_t* rows, int M, const void* weight, int64_t w_row_stride,

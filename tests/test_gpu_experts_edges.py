@@ -4,7 +4,7 @@ not make (GPU), against the same 64-bit formulas and bars."""
 import pytest
 import torch
 
-from test_gpu_experts import BF, E4M3, F32, U8, B, Product, check_route  # noqa: F401
+from test_gpu_experts import BF, E4M3, F32, U8, B, Product, check_route, ints  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -106,3 +106,25 @@ def test_steps_right_behind_one_another_see_each_others_results(B, T):  # noqa: 
     assert not any(torch.equal(a, want[0]) for a in want[1:])
     for _ in range(10):
         assert all(torch.equal(a, b) for a, b in zip(steps(False), want))
+
+
+@pytest.mark.parametrize("N,K,kind,gated", [(128, 256, U8, False), (4096, 256, U8, False), (2048, 2048, BF, False), (8192, 256, U8, True)])
+@pytest.mark.parametrize("starts", [[0, 639, 0, 640], [0, 639, 0, 600, 640], [0, 640] * 8, [0, 300, 100, 640, 639, 0, 640]])
+def test_groups_that_overlap_keep_all_their_rows(B, starts, N, K, kind, gated):  # noqa: F811
+    """Starts that go back: the group that does is skipped, and each element of the others' rows is the result of a group that
+    its row lies in, although together they have more rows than there are.  (A row's columns are written tile by tile, so
+    groups that share it may each have some of them.)"""
+    M, E = 640, len(starts) - 1
+    p = Product([M] + [0] * (E - 1), N, K, kind, gated=gated)
+    each = []
+    for e in range(E):                                           # every row by every group's weights
+        p.starts_list = [0] * (e + 1) + [M] * (E - e)
+        each.append(p.want())
+    status, out = ints([0]), torch.full((M, N // 2 if gated else N), 7.0, device="cuda")
+    p.starts = ints(starts)
+    p.call(B, out=out, status=status)
+    assert status.item() == 2
+    for i in [0, 1, 63, 64, 99, 100, 255, 256, 299, 300, 599, 600, 638, 639]:
+        groups = [e for e in range(E) if starts[e] <= i < starts[e + 1]]
+        near = [(out[i].double() - each[e][0][i]).abs() <= each[e][1][i] + 2.0 ** -23 * each[e][0][i].abs() for e in groups]
+        assert groups and torch.stack(near).any(0).all(), i
