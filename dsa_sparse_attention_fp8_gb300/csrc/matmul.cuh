@@ -210,8 +210,13 @@ __device__ __forceinline__ bool gather_rows(const MatmulParams& p, const Groups&
 }
 
 // ---------------------------------------------------------------- results
-// silu(g) u.  The exponential is off by 2 + 1.17 |g| units in the last place, the quotient by two; below g = -87 it is 0.
-__device__ __forceinline__ float gate(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
+// silu(g) u = g / (1 + e) u, or g e / (1 + e) u of a negative g, with e = exp(-|g|) <= 1: nothing overflows, so that small
+// results are right down to where e is subnormal (g below -87.3).  e is off by a unit in the last place, the quotient by two,
+// the sum and the products by half of one each: five units in all, whatever g.
+__device__ __forceinline__ float gate(float g, float u) {
+  const float e = expf(-fabsf(g));
+  return __fdividef(g < 0.f ? g * e : g, 1.0f + e) * u;
+}
 
 __device__ __forceinline__ uint32_t round_pair(float a, float b, bool bf16) {
   if (bf16) {

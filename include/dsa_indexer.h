@@ -586,7 +586,8 @@ int dsa_add_rms_norm(const void* x, int64_t x_stride, const void* residual, int6
  * both 16-byte aligned.  K and N are any sizes from 1 to 2^28, T at most 2^30.
  * Outputs must not overlap inputs.
  * Computation: tensor-core products with FP32 accumulation over a block of K,
- * its scales and the sums over blocks in FP32, gate in FP32, one rounding.
+ * its scales and the sums over blocks in FP32, gate in FP32 (its exponential
+ * and quotient: five units in the last place together), one rounding.
  * Faults: DSA_STATUS_TIMEOUT (an internal wait ran out; results are invalid).
  * Errors: INVALID_ARG, UNSUPPORTED, CUDA.
  */

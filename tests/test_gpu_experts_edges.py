@@ -128,3 +128,20 @@ def test_groups_that_overlap_keep_all_their_rows(B, starts, N, K, kind, gated): 
         groups = [e for e in range(E) if starts[e] <= i < starts[e + 1]]
         near = [(out[i].double() - each[e][0][i]).abs() <= each[e][1][i] + 2.0 ** -23 * each[e][0][i].abs() for e in groups]
         assert groups and torch.stack(near).any(0).all(), i
+
+
+@pytest.mark.parametrize("T", [3, 100, 2000])
+def test_the_gate_is_exact_to_a_few_units(B, T):  # noqa: F811
+    """silu(g) u of products that are exact (one element of K to the gates, one to what they gate, each with a scale of its
+    own), over all g: five units in the last place, 5 x 2^-23 of the result.  Below -87.3 exp(g) is subnormal, a number in
+    steps of 2^-149 that g multiplies, and silu(g) has such steps too: (|g| + 1) 2^-149 more, times u, and the result's own."""
+    torch.manual_seed(T)
+    g = torch.cat([torch.linspace(-104, 90, T, device="cuda")[: T - 1], torch.full((1,), -88.5, device="cuda")])
+    u = (10.0 ** (8 * torch.rand(T, device="cuda"))) * torch.where(torch.rand(T, device="cuda") < 0.5, -1.0, 1.0)
+    x, w = torch.zeros(T, 256, dtype=U8, device="cuda"), torch.zeros(512, 256, dtype=U8, device="cuda")
+    x[:, 5], x[:, 200], w[:256, 5], w[256:, 200] = 0x38, 0x38, 0x38, 0x38             # ones
+    out = torch.empty(T, 256, device="cuda")
+    B.fp8_matmul(x, torch.stack([g, u], 1).contiguous(), w, torch.ones(4, 2, device="cuda"), gated=True, out=out)
+    want = g.double() / (1 + torch.exp(-g.double())) * u.double()
+    bar = 5 * 2.0 ** -23 * want.abs() + 2.0 ** -149 * (1 + (g.double().abs() + 1) * u.double().abs())
+    assert ((out.double() - want[:, None]).abs() <= bar[:, None]).all()
