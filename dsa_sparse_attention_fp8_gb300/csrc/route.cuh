@@ -317,8 +317,12 @@ __device__ __forceinline__ int choose(const RouteParams& p, const float (&l)[V],
     int ahead = runs_ahead(p, mine, run);
     if (p.top_groups < p.num_groups) {
       const bool kept = ahead < p.top_groups;
-      const float least = key_value(~warp_max(is && kept ? ~mine : 0u)), next = key_value(warp_max(is && !kept ? mine : 0u));
-      if (!(least - next > 4 * bound(least, next))) {
+      // a run's value is off by what its two are off by, however small their sum: the least of the kept runs' and the largest of
+      // the others' as they may be
+      const float off = 2 * bound(key_value(best), key_value(second));
+      const float least = key_value(~warp_max(is && kept ? ~order_key(value - off) : 0u));
+      const float next = key_value(warp_max(is && !kept ? order_key(value + off) : 0u));
+      if (!(least > next)) {
         const float low = p.per > 1 ? key_value(second) : key_value(best);
         int e;
         const int n = candidates<V>(key, is ? order_key(low - 2 * bound(low, low)) : ~0u, own.first, lane, list, &e);

@@ -145,3 +145,16 @@ def test_the_gate_is_exact_to_a_few_units(B, T):  # noqa: F811
     want = g.double() / (1 + torch.exp(-g.double())) * u.double()
     bar = 5 * 2.0 ** -23 * want.abs() + 2.0 ** -149 * (1 + (g.double().abs() + 1) * u.double().abs())
     assert ((out.double() - want[:, None]).abs() <= bar[:, None]).all()
+
+
+@pytest.mark.parametrize("size", [30.0, 1e3, 1e6])
+def test_run_values_whose_large_parts_cancel(B, size):  # noqa: F811
+    """A run's value is the sum of its best two: where a bias makes them large and of opposite signs, the sum is small but as
+    uncertain in FP32 as they are."""
+    torch.manual_seed(2)
+    bias = torch.tensor([size, -size] * 3 + [0.3, 0.2] * 3, device="cuda")
+    for T in (60, 400):
+        logits = torch.randn(T, 12, device="cuda")
+        check_route(B, logits, 4, "sigmoid", bias, 6, 3)
+        check_route(B, logits, 2, "softmax", bias, 6, 2)
+        check_route(B, logits, 2, "softmax", bias[torch.randperm(12)], 3, 1)
