@@ -633,7 +633,9 @@ int dsa_grouped_matmul(const void* x, int64_t x_stride, const float* x_scales, i
  *   index; values are compared as in 64 bits (by the logits themselves where
  *   there is neither a bias nor a run).
  *   expert_ids [T, top_k], weights [T, top_k] FP32: scale * s, divided by the
- *     sum of the chosen s where normalize != 0 (0 where that sum is 0).
+ *     sum of the chosen s where normalize != 0 (0 where that sum is 0).  They
+ *     are computed in FP32: sigmoids' are off by 2^-20 of themselves at most,
+ *     a softmax's by 2^-19 and 2^-23 times the spread of the logits.
  *   group_starts [E + 1], rows [T * top_k], places [T, top_k]: the choices
  *     sorted by expert, and by token within an expert: places is where a
  *     choice went, rows the token of each place, as dsa_grouped_matmul and

@@ -158,3 +158,28 @@ def test_run_values_whose_large_parts_cancel(B, size):  # noqa: F811
         check_route(B, logits, 4, "sigmoid", bias, 6, 3)
         check_route(B, logits, 2, "softmax", bias, 6, 2)
         check_route(B, logits, 2, "softmax", bias[torch.randperm(12)], 3, 1)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_weights_to_a_few_units(B, dtype):  # noqa: F811
+    """A sigmoid: its exponential off by one unit in the last place, sum and quotient by half of one each: two.  Divided by a
+    sum of 16 such in five additions, 2 + 2 + 2.5, a quotient and the scale half each: 7.5 units, below 2^-20, and half a step
+    of a subnormal number.  A softmax's difference is off by 2^-24 |l - max l|, twice (the sum's too), its sum of 16 to a lane
+    and five between lanes by 10.5 units: below 2^-19 with the same quotients."""
+    torch.manual_seed(8)
+    T, E, k, i32 = 300, 64, 16, torch.int32
+    logits = torch.cat([torch.randn(T, E - 8, device="cuda") * 3, torch.linspace(-100, 100, 8 * T, device="cuda").view(8, T).T], 1).to(dtype)
+    logits[0] = -88.5 + 0.01 * logits[0]
+    l = logits.double()
+    for scoring, scale in (("sigmoid", 1.0), ("sigmoid", 2.5), ("softmax", 1.0)):
+        s = 1 / (1 + torch.exp(-l)) if scoring == "sigmoid" else torch.softmax(l, 1)
+        for normalize in (False, True):
+            ids, places, rows = (torch.empty(x, dtype=i32, device="cuda") for x in ((T, k), (T, k), (T * k,)))
+            weights, starts = torch.empty(T, k, device="cuda"), torch.empty(E + 1, dtype=i32, device="cuda")
+            B.route_experts(logits, k, ids, weights, starts, rows, places, scoring=scoring, normalize=normalize, scale=scale)
+            want = s.gather(1, ids.long())
+            if normalize:
+                want = want / want.sum(1, keepdim=True)
+            want = want * scale
+            rel = 2.0 ** -20 if scoring == "sigmoid" else 2.0 ** -19 + 2.0 ** -23 * (l.amax(1, keepdim=True) - l.gather(1, ids.long()))
+            assert ((weights.double() - want).abs() <= rel * want + 2.0 ** -149 * scale).all(), (scoring, scale, normalize)
