@@ -26,9 +26,11 @@ int product_maps(const dsa::MatmulParams& p, int box, int w_box, CUtensorMap* tx
   const int size = element_bytes(p.x_type);
   const CUtensorMapDataType type = size == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                                    : p.x_type == DSA_TYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  const int64_t xd[2] = {p.K, p.x_rows}, xs[1] = {p.x_stride * size};
-  const int xb[2] = {128 / size, box};
-  if (const int rc = make_map(tx, "x", type, size, p.x, 2, xd, xs, xb, true)) return rc;
+  if (!p.rows) {
+    const int64_t xd[2] = {p.K, p.x_rows}, xs[1] = {p.x_stride * size};
+    const int xb[2] = {128 / size, box};
+    if (const int rc = make_map(tx, "x", type, size, p.x, 2, xd, xs, xb, true)) return rc;
+  }
   const int64_t wd[3] = {p.K, p.N, p.E}, ws[2] = {p.w_stride * size, p.w_group * size};
   const int wb[3] = {128 / size, w_box, 1};
   return make_map(tw, "weight", type, size, p.w, 3, wd, ws, wb, true);
@@ -141,7 +143,7 @@ struct Few {
     return run(p, groups, plan, st);
   }
   static int run(dsa::MatmulParams p, int64_t groups, Plan plan, cudaStream_t st) {
-    CUtensorMap tx, tw;
+    CUtensorMap tx{}, tw{};
     p.box = p.M <= 32 * groups ? 32 : BM;
     if (const int rc = product_maps(p, p.box, C::kBox, &tx, &tw)) return rc;
     const int64_t columns = (p.width + C::kOut - 1) / C::kOut, tiles = row_tiles(p.M, groups, BM) * columns;
@@ -176,7 +178,7 @@ struct Many {
     return run(p, groups, plan, st);
   }
   static int run(dsa::MatmulParams p, int64_t groups, const Plan& plan, cudaStream_t st) {
-    CUtensorMap tx, tw;
+    CUtensorMap tx{}, tw{};
     if (const int rc = product_maps(p, 128, C::kBox, &tx, &tw)) return rc;
     const int64_t columns = (p.width + C::kOut - 1) / C::kOut, tiles = row_tiles(p.M, groups, C::BM) * columns;
     if (tiles > INT32_MAX / 2) return fail(DSA_ERR_UNSUPPORTED, "%lld tiles of results", (long long)tiles);

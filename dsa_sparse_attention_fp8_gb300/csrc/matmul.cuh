@@ -312,7 +312,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
     mbar_init(join_free, 8 * S);
     *abort_flag = 0;
     fence_barrier_init();
-    tma_prefetch_desc(&tx);
+    if (!p.rows) tma_prefetch_desc(&tx);
     tma_prefetch_desc(&tw);
   }
   if (warp == 9) {
@@ -695,7 +695,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__
     for (int q = 0; q < 4; ++q) mbar_init(both(q), 2);
     *abort_flag = 0;
     fence_barrier_init();
-    tma_prefetch_desc(&tx);
+    if (!p.rows) tma_prefetch_desc(&tx);
     tma_prefetch_desc(&tw);
   }
   __syncwarp();
