@@ -138,7 +138,12 @@ __device__ __forceinline__ void take_block(uint32_t from, uint64_t (&acc)[COLS /
 // Every wait is bounded.  A role whose wait runs out raises the flag of each CTA that works on the tile and leaves; so do the
 // others when they see it.  Copies and products under way then end before the CTA does: the loading and the product warp
 // leave word of where they stopped, which is read once every role has left.  A barrier that copies alone arrive at tells
-// of their end (gathered rows, whose warps wait for their own copies, have barriers of their own).
+// of their end (gathered rows, whose warps wait for their own copies, have barriers of their own).  Roles give up in one place,
+// behind all of them: four copies of that code took 0.4 us more of each call with 64 gated rows.
+__device__ __forceinline__ void give_up(const MatmulParams& p, uint32_t abort_flag, uint32_t ctas) {
+  for (uint32_t r = 0; r < ctas; ++r) st_cluster_u32(map_to(abort_flag, r), 1);
+  raise_status(p.status, kStatusTimeout);
+}
 struct Stopped {
   int s, phase;   // the stage that would have come next, and its pass
   uint32_t used;  // stages that were ever filled
@@ -256,11 +261,12 @@ __device__ __forceinline__ void store4(const MatmulParams& p, int64_t row, int n
 // Tiles of BM rows and 128 results (WIDE: 256), a CTA or a cluster to a tile, one after the other.  A cluster's CTAs have equal
 // parts of K, and join their sums through each other's shared memory in rank order.
 //
-// Bound, of one tile, by what one SM draws from L2, some 100 GB/s, and so by how many SMs share the weights (a tile of 128
-// weight rows and 7168 elements of K, already in L2: 19.6 us by one CTA, 8.6 by four, 7.2 by eight; this device runs 16
-// clusters of eight at once, 24 of six, so more tiles go to smaller clusters).  64 rows, K 7168, gated N 4096: 14.4 us, of
-// which launch and set-up are 4, the stream of a sixth of K 4 and the join of 64 rows 4.  Bound, of many tiles, by HBM: 64
-// groups of eight rows with such weights, 1.76 GB in 276.6 us, 94 % of the copy rate.
+// Bound, of one tile, by what one SM draws from L2, some 100 GB/s, and so by how many SMs share the weights (a tile of 64 rows,
+// 128 weight rows and 7168 elements of K, already in L2: 21.0 us by one CTA, 9.4 by four, 7.7 by eight).  How many clusters run
+// at once decides where there are more tiles: 15 of eight or seven CTAs, 23 of six, 28 of five, 36 of four as one device
+// tells (64 rows, K 7168, gated N 4096, 16 tiles, from L2: 19.2 us by eight, 12.7 by six, 13.0 by four).  From HBM that
+// takes 14.6 us, of which launch and set-up are 4, the stream of a sixth of K 4 and the join of 64 rows 4.  Bound, of many
+// tiles, by HBM: 64 groups of eight rows with such weights, 1.76 GB in 275 to 281 us, 93 to 95 % of the copy rate.
 // A stage holds BM rows though the instruction reads 128: those past BM are weights, in lanes that nobody reads.
 template <bool FP8, bool GATED, bool WIDE, int BM, int ROUND>
 struct FewCfg {
@@ -306,7 +312,8 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
   const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t S = cluster_size(), rank = cluster_rank();
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::kStages; ++s) mbar_init(full(s), 1), mbar_init(empty(s), 1), mbar_init(landed(s), kGatherLanes);
+    for (int s = 0; s < C::kStages; ++s) mbar_init(full(s), 1), mbar_init(empty(s), 1);
+    for (int s = 0; p.rows && s < C::kStages; ++s) mbar_init(landed(s), kGatherLanes);
     for (int b = 0; b < C::kBuffers; ++b) mbar_init(acc_full(b), 1), mbar_init(acc_empty(b), 8);
     mbar_init(join_full, 8 * S);
     mbar_init(join_free, 8 * S);
@@ -328,11 +335,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
   if (S > 1) cluster_sync(); else __syncthreads();
   tc_fence_after();
   const uint32_t tmem = lds_u32(tmem_holder);
-  const auto quit = [&] {
-    *abort_flag = 1;
-    for (uint32_t r = 0; S > 1 && r < S; ++r) st_cluster_u32(map_to(bars + 496, r), 1);
-    raise_status(p.status, kStatusTimeout);
-  };
+  bool on = true;  // this warp's waits have not run out
 
   // this CTA's part of K, in stages
   const int blocks = (p.K + C::kK - 1) / C::kK;
@@ -348,7 +351,6 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
     const bool vec = p.out && (reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)(p.out_stride * (p.out_type == 2 ? 4 : 2))) % (p.out_type == 2 ? 16 : 8) == 0;
     const bool vec_codes = p.codes && (reinterpret_cast<uintptr_t>(p.codes) | (uintptr_t)p.width) % 4 == 0;
     int buffer = 0, turn = 0, joined = 0;
-    bool on = true;
     // A tile's rows and first scales are asked for a tile ahead: where it is and this lane's row of x before the products of the
     // tile before are summed, the scales before its results are written (experts of a batch of 64, 290 us without it, 279.5).
     Tile ahead;
@@ -516,14 +518,12 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
         ++joined;
       }
     }
-    if (!on) quit();
   } else {
     regs_shrink<72>();
     if (warp == 8) {
       // ------------------------------------------------ loads
       int s = 0, phase = 0, left = stages_to_fill(p, rank);
       uint32_t used = 0;
-      bool on = true;
       for (int t = blockIdx.x / S; on && find_tile<BM, C::kOut>(p, groups, t, &tile); t += step) {
         const int boxes = p.rows ? 0 : (tile.count + p.box - 1) / p.box;
         const uint32_t bytes = C::kStageB + boxes * p.box * 128;
@@ -550,12 +550,10 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
         }
       }
       tell_stop(loads_stopped, s, phase, used);
-      if (!on) quit();
     } else if (warp == 9) {
       // ------------------------------------------------ products
       const uint32_t idesc = FP8 ? idesc_e4m3_f32(128, C::BN) : idesc_16_f32(p.x_type == 0, 128, C::BN, false);
       int s = 0, phase = 0, buffer = 0, turn = 0;
-      bool on = true;
       for (int t = blockIdx.x / S; on && find_tile<BM, C::kOut>(p, groups, t, &tile); t += step) {
         for (int k = k0; k < k1; ++k) {
           if (FP8 || k == k0) on = __all_sync(~0u, mbar_wait(acc_empty(buffer), turn ^ 1, abort_flag));
@@ -579,16 +577,14 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
         }
       }
       tell_stop(products_stopped, s, phase, 0);
-      if (!on) quit();
     } else if (p.rows) {
       // ------------------------------------------------ gathered rows
       const int g = warp - 10;
-      if (!gather_rows<C::kStages, C::kStage, BM, C::kOut>(
-              p, groups, blockIdx.x / S, step, 0, BM, FP8 ? 1 : 2, k0, k1, stages,
-              g, abort_flag, empty(0), landed(0)))
-        quit();
+      on = gather_rows<C::kStages, C::kStage, BM, C::kOut>(p, groups, blockIdx.x / S, step, 0, BM, FP8 ? 1 : 2, k0, k1, stages, g, abort_flag,
+                                                           empty(0), landed(0));
     }
   }
+  if (!on) give_up(p, bars + 496, S);
   __syncwarp();
   tc_fence_before();
   if (S > 1) cluster_sync(); else __syncthreads();
@@ -605,7 +601,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
 // Tiles of 256 rows and 256 weight rows, each shared by a pair of CTAs (cta_group::2): a CTA loads half of the rows and half
 // of the weights, and has half of the rows' sums.
 //
-// 8192 rows, K = N = 7168: 310 us, 2.7 PFLOP/s, 70 % of twice the measured BF16 rate (16 bits: 1.6 PFLOP/s, 82 % of it).  Two
+// 8192 rows, K = N = 7168: 317 us, 2.7 PFLOP/s, 69 % of twice the measured BF16 rate (16 bits: 1.6 PFLOP/s, 82 % of it).  Two
 // things bound it about alike.  The way from L2: a pair takes 64 KB for a block of K, and with a quarter of the products, and
 // no sums, the same loads take 242 us.  And the hand-over of an accumulator, of which tensor memory holds two (products,
 // the sums' reads of 256 columns, and back): without the sums 260 us.  Halves of an accumulator handed over
@@ -690,7 +686,8 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__
   const uint32_t rank = cluster_rank();
   cluster_arrive();
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::kStages; ++s) mbar_init(full(s), 1), mbar_init(empty(s), 1), mbar_init(landed(s), rank == 0 ? kGatherLanes + 1 : kGatherLanes);
+    for (int s = 0; s < C::kStages; ++s) mbar_init(full(s), 1), mbar_init(empty(s), 1);
+    for (int s = 0; p.rows && s < C::kStages; ++s) mbar_init(landed(s), rank == 0 ? kGatherLanes + 1 : kGatherLanes);
     for (int b = 0; b < 2; ++b) mbar_init(acc_full(b), 1), mbar_init(acc_empty(b), 16);
     for (int q = 0; q < 4; ++q) mbar_init(both(q), 2);
     *abort_flag = 0;
@@ -713,11 +710,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = lds_u32(tmem_holder);
-  const auto quit = [&] {
-    *abort_flag = 1;
-    st_cluster_u32(map_to(bars + 496, rank ^ 1), 1);
-    raise_status(p.status, kStatusTimeout);
-  };
+  bool on = true;  // this warp's waits have not run out
   const int blocks = (p.K + C::kK - 1) / C::kK;
   const int step = gridDim.x / 2;
   Tile tile;
@@ -732,7 +725,6 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__
     const bool vec = p.out ? (reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)(p.out_stride * size)) % 16 == 0
                            : (reinterpret_cast<uintptr_t>(p.codes) | (uintptr_t)p.width) % 16 == 0;
     int buffer = 0, turn = 0, tiles = 0;
-    bool on = true;
     for (int t = blockIdx.x / 2; on && find_tile<C::BM, C::kOut>(p, groups, t, &tile); t += step) {
       const int64_t row0 = tile.row + 128 * (int)rank + q * 32;   // the warp's first row
       const int rows = tile.count - 128 * (int)rank - q * 32;      // and how many it has
@@ -864,14 +856,12 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__
       }
       ++tiles;
     }
-    if (!on) quit();
   } else {
     regs_shrink<72>();
     if (warp == 8) {
       // ------------------------------------------------ loads
       int s = 0, phase = 0, left = stages_to_fill(p, rank);
       uint32_t used = 0, filled = 0, seconds = 0;
-      bool on = true;
       for (int t = blockIdx.x / 2; on && find_tile<C::BM, C::kOut>(p, groups, t, &tile); t += step) {
         // a box of 128 rows for each CTA that has some
         const bool second = tile.count > 128, boxed = !p.rows && (rank == 0 || second);
@@ -902,12 +892,10 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__
       }
       tell_stop(loads_stopped, s, phase, used);
       if (lane == 0) sts_u32(fills, filled), sts_u32(fills + 4, seconds);
-      if (!on) quit();
     } else if (warp == 9 && rank == 0) {
       // ------------------------------------------------ products of both CTAs
       const uint32_t idesc = FP8 ? idesc_e4m3_f32(256, 256) : idesc_16_f32(p.x_type == 0, 256, 256, false);
       int s = 0, phase = 0, buffer = 0, turn = 0;
-      bool on = true;
       for (int t = blockIdx.x / 2; on && find_tile<C::BM, C::kOut>(p, groups, t, &tile); t += step) {
         for (int k = 0; k < blocks; ++k) {
           if (FP8 || k == 0) on = __all_sync(~0u, mbar_wait(acc_empty(buffer), turn ^ 1, abort_flag));
@@ -932,12 +920,10 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__
         }
       }
       tell_stop(products_stopped, s, phase, 0);
-      if (!on) quit();
     } else if (warp == 9 && p.rows) {
       // ------------------------------------------------ the second CTA's gathered rows, told to the first
       if (lane == 0) {
         int s = 0, phase = 0;
-        bool on = true;
         for (int t = blockIdx.x / 2; on && find_tile<C::BM, C::kOut>(p, groups, t, &tile); t += step) {
           for (int k = 0; k < blocks; ++k) {
             on = mbar_wait(landed(s), phase, abort_flag);
@@ -947,18 +933,16 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__
             if (++s == C::kStages) s = 0, phase ^= 1;
           }
         }
-        if (!on) quit();
       }
       __syncwarp();
     } else if (warp >= 10 && p.rows) {
       // ------------------------------------------------ gathered rows
       const int g = warp - 10;
-      if (!gather_rows<C::kStages, C::kStage, C::BM, C::kOut>(
-              p, groups, blockIdx.x / 2, step, 128 * (int)rank, 128, FP8 ? 1 : 2, 0, blocks, stages,
-              g, abort_flag, empty(0), landed(0)))
-        quit();
+      on = gather_rows<C::kStages, C::kStage, C::BM, C::kOut>(p, groups, blockIdx.x / 2, step, 128 * (int)rank, 128, FP8 ? 1 : 2, 0, blocks,
+                                                              stages, g, abort_flag, empty(0), landed(0));
     }
   }
+  if (!on) give_up(p, bars + 496, 2);
   __syncwarp();
   tc_fence_before();
   cluster_sync();
