@@ -183,3 +183,47 @@ def test_weights_to_a_few_units(B, dtype):  # noqa: F811
             want = want * scale
             rel = 2.0 ** -20 if scoring == "sigmoid" else 2.0 ** -19 + 2.0 ** -23 * (l.amax(1, keepdim=True) - l.gather(1, ids.long()))
             assert ((weights.double() - want).abs() <= rel * want + 2.0 ** -149 * scale).all(), (scoring, scale, normalize)
+
+
+def test_a_shared_expert_beside_the_others_in_a_graph(B):  # noqa: F811
+    """A captured step that forks: the shared expert's products on a stream of their own beside the router and the experts',
+    joined before the sum, replayed with other inputs, against the same calls one after the other."""
+    torch.manual_seed(9)
+    T, E, k, n, i32 = 70, 8, 2, 512, torch.int32
+    x, xs, logits = e4m3(T, n), (0.5 + torch.rand(T, 4, device="cuda")) / 100, torch.randn(T, E, device="cuda")
+    w1, s1, w2, s2 = e4m3(E + 1, 2 * n, n), torch.full((E + 1, 8, 4), 4e-4, device="cuda"), e4m3(E + 1, n, n), torch.full((E + 1, 4, 4), 4e-4, device="cuda")
+    ids, places, rows = (torch.empty(s, dtype=i32, device="cuda") for s in ((T, k), (T, k), (T * k,)))
+    weights, starts = torch.empty(T, k, device="cuda"), torch.empty(E + 1, dtype=i32, device="cuda")
+    h, hs, y = torch.empty(T * k, n, dtype=U8, device="cuda"), torch.empty(T * k, 4, device="cuda"), torch.empty(T * k, n, dtype=BF, device="cuda")
+    g, gs, shared, out = torch.empty(T, n, dtype=U8, device="cuda"), torch.empty(T, 4, device="cuda"), torch.empty(T, n, dtype=BF, device="cuda"), torch.empty(T, n, dtype=BF, device="cuda")
+
+    def experts():
+        B.route_experts(logits, k, ids, weights, starts, rows, places)
+        B.grouped_matmul(x, w1[:E], starts, xs, s1[:E], rows=rows, gated=True, out_codes=h, out_scales=hs)
+        B.grouped_matmul(h, w2[:E], starts, hs, s2[:E], out=y)
+
+    def beside():
+        B.fp8_matmul(x, xs, w1[E], s1[E], gated=True, out_codes=g, out_scales=gs)
+        B.fp8_matmul(g, gs, w2[E], s2[E], out=shared)
+
+    def plain():
+        experts(), beside()
+        torch.cuda.synchronize()
+        return B.combine_experts(y, places, weights, add=shared).clone()
+    plain()
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            beside()
+        experts()
+        main.wait_stream(side)
+        B.combine_experts(y, places, weights, add=shared, out=out)
+    for _ in range(20):
+        x.copy_(e4m3(T, n)), logits.copy_(torch.randn(T, E, device="cuda")), xs.copy_((0.5 + torch.rand(T, 4, device="cuda")) / 100)
+        want = plain()
+        for t in (ids, places, rows, starts, h, g, y, shared, out, hs, gs, weights):
+            t.zero_()
+        graph.replay()
+        assert torch.equal(out, want)
