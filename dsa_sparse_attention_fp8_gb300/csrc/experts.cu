@@ -118,8 +118,9 @@ struct Few {
   static constexpr auto kKernel = dsa::few_rows_kernel<FP8, GATED, WIDE, BM, ROUND>;
   static inline Ready ready;
 
-  // A CTA alone takes as long for a block of K wherever it lies, bound by what one SM draws from L2 (measured of one tile of
-  // 7168 elements of K, in L2: 22 us by one CTA, 7.5 by eight).  CTAs that share a tile join their sums, round by round.
+  // A CTA alone takes as long for a block of K wherever it lies, bound by what one SM draws from L2 (measured of one tile of 64
+  // rows, 128 weight rows and 7168 elements of K, in L2: 21.0 us by one CTA, 9.4 by four, 7.7 by eight).  CTAs that share a
+  // tile join their sums, round by round.
   static constexpr double kBlock = (C::kStageA + C::kStageB) / 110e3 + 0.06, kRoundUs = C::BN == 256 ? 1.8 : 0.8;
 
   static int plan(const dsa::MatmulParams& p, int64_t groups, const Device& d, Plan* best) {
@@ -192,7 +193,11 @@ struct Many {
 template <bool FP8, bool GATED>
 int run_variant(const dsa::MatmulParams& p, int64_t groups, cudaStream_t st) {
   using Few64 = Few<FP8, GATED, false, 64>;
-  using Joined64 = Few<FP8, GATED, false, 64, 64>;  // (a gated tile joined in one round, for which it has a stage less)
+  // A tile of few joined in one round, for which it has a stage less: a round's sums are given back by a release of the cluster's
+  // scope, which costs a microsecond and more (96 rows, K 7168, N 4096, in two rounds 12.3 us, in one 10.7; of many tiles, which
+  // are not shared, 36 rows to each of 64 groups of BF16, K 2048, N 3584, the stage counts: 154 with it, 161 without).
+  using Joined64 = Few<FP8, GATED, false, 64, 64>;
+  using Joined128 = Few<FP8, GATED, false, 128, GATED ? 32 : 128>;
   using Wide64 = Few<FP8, false, !GATED, 64>;
   using Few128 = Few<FP8, GATED, false, 128>;
   using Pairs = Many<FP8, GATED>;
@@ -201,10 +206,16 @@ int run_variant(const dsa::MatmulParams& p, int64_t groups, cudaStream_t st) {
   const int64_t tiles = row_tiles(p.M, groups, 64) * ((p.width + 127) / 128);
   if (groups > 1 && tiles > 2 * d.sms) {
     // Bound by the weights' way from HBM.  Tiles fit the rows of a group; 256 weight rows to a tile, so that rows are read less
-    // often.  Of 64 groups, in us: K 2048, N 7168, tiles of 128 and of 256 weight rows and by pairs, of 16 rows to a group 199,
-    // 165, 183, of 32 203, 170, 186; tiles of 128 rows and by pairs, of 48 189, 193, of 96 243, 206.  Gated, K 7168, N 4096,
-    // tiles of 64 and of 128 rows and by pairs, of 32 300, 304, 352, of 48 343, 320, 374, of 96 486, 386, 392, of 128 545,
-    // 491, 379.
+    // often.  Of 64 groups, as uneven as a router's choices make them, in us, by rows to a group in the mean:
+    //   E4M3, K 2048, N 7168, tiles of 64 x 128, 64 x 256, 128 x 128 and by pairs: 16 rows 203, 157, 183, 198; 32 207, 163, 188,
+    //     200; 48 234, 189, 196, 205; 96 345, 274, 270, 217.
+    //   E4M3, gated, gathered, K 7168, N 4096, tiles of 64 rows, of 128 and by pairs: 32 300, 310, 395; 48 338, 317, 399; 96 459,
+    //     416, 418; 128 552, 479, 436.
+    //   BF16, K 2048, N 3584, as the first: 32 146, 150, 153, 153; 48 159, 162, 156, 155; 96 217, 183, 175, 161.
+    //   BF16, gated, gathered, K 3584, N 2048, as the second: 32 153, 160, 155; 48 170, 164, 158; 96 186, 185, 163; 128 223, 180, 166.
+    // (So 16-bit gated products of 33 to 96 rows would be better off by pairs, by 4 to 12 %.)  The mean is over all groups, as the
+    // host knows no more: where eight of 256 groups have 256 rows each and the others none (BF16, K = N = 2048), tiles of 64
+    // rows take 32.6 us and pairs would take 18.0.
     if (p.M <= 32 * groups) {
       if constexpr (GATED) return Few64::run(p, groups, d, st);
       else return Wide64::run(p, groups, d, st);
@@ -214,10 +225,10 @@ int run_variant(const dsa::MatmulParams& p, int64_t groups, cudaStream_t st) {
   // Few tiles: as the CTAs that share their K take.
   Plan few, some, many;
   if (const int rc = Joined64::plan(p, groups, d, &few)) return rc;
-  if (const int rc = Few128::plan(p, groups, d, &some)) return rc;
+  if (const int rc = Joined128::plan(p, groups, d, &some)) return rc;
   if (const int rc = Pairs::plan(p, groups, d, &many)) return rc;
   if (many.us < few.us && many.us < some.us) return Pairs::run(p, groups, many, st);
-  return some.us < few.us ? Few128::run(p, groups, some, st) : Joined64::run(p, groups, few, st);
+  return some.us < few.us ? Joined128::run(p, groups, some, st) : Joined64::run(p, groups, few, st);
 }
 
 // The checks that both products share, and their launch.  p has the sizes, strides and pointers.
@@ -367,7 +378,8 @@ int dsa_route_experts(const void* logits, int64_t stride, int type, const float*
   p.num_groups = num_groups, p.top_groups = top_groups, p.per = E / num_groups;
   p.scale = scale, p.softmax = scoring == DSA_SCORE_SOFTMAX, p.normalize = normalize != 0;
   const cudaStream_t st = (cudaStream_t)stream;
-  // a run's lanes: as many as there are for each of so many runs
+  // a run's lanes: as many as there are for each of so many runs.  More than 16 experts to a lane, as 3, 5, 9 or 17 runs of
+  // many experts make, spill registers: 8192 tokens of 510 experts in 3 runs take 48 us, in 17 runs 78, of 512 in 8 runs 36.
   p.lanes = 32;
   while (32 / p.lanes < num_groups) p.lanes /= 2;
   p.wide = (p.per + p.lanes - 1) / p.lanes;
