@@ -3,11 +3,15 @@
 //   the largest sum of their best two v; the top_k largest v there, ties to the lowest index.
 // The choice is the one that 64 bits make.  Without bias and runs it is that of the logits, which are compared as they
 // are.  Otherwise v is computed in FP32 first; where two neighbours among the ordered first top_k + 1 values (or the run
-// values at the cut) lie closer than FP32's error, what is close is done again in FP64, which this GPU has little of: a token
-// in a thousand.
-// Bound by instructions: a token of 256 experts, 8 runs and 8 choices takes a warp some 1000 (a first form, which searched
+// values at the cut) lie closer than FP32's error, what is close is done again in FP64, which this GPU has little of.
+// Bound by instructions: a token of 256 experts, 8 runs and 8 choices takes a warp some 1080 (a first form, which searched
 // every run with a whole warp and all keys for each choice, 2550).  8192 tokens: 23 us, the choice 15 and the places 8 (one
 // CTA, matching choices across a warp, 131); 64 tokens, in one launch, 5.8.
+// How many tokens are done again hangs on the values, since the error that is allowed for is that of a score of 1 (of a softmax,
+// of its largest): of sigmoids of logits of deviation 1.5 around 0 one in a thousand, but most of those that crowd near 0 or 1
+// and have no bias to tell them apart.  8192 such tokens without a bias: around -10 26 us, -12 31, 8 49, 14 115 (then all their
+// values are done again), of deviation 6 around 0 41; softmax of deviation 1.5 34, 8 79, 12 138.  With a bias of deviation
+// 0.05 17 to 25, softmax 35.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -297,8 +301,8 @@ __device__ __forceinline__ uint64_t value64(const RouteParams& p, int64_t row, i
 
 // The choice of one token; lane j gets the j-th expert.  Values in FP32, whose difference is off by less than `close` times
 // the larger of `size` and both: a sigmoid by 2^-21.9 at most (the exponential's 2 + 1.17 |l| ulp count s (1 - s) times, below
-// 0.56 of 2^-23; sum 2^-24, reciprocal 2^-23), a softmax probability by 2^-19 of itself (its sum has 32 + 5 roundings), so `size` is the largest of them; the bias adds
-// 2^-24 of v.  What lies closer is done again in 64 bits: of sigmoids the candidates alone, one to a lane, otherwise all.
+// 0.63 of 2^-23; sum 2^-24, reciprocal 2^-23), a softmax probability by 2^-19 of itself (its sum has 32 + 5 roundings), so `size`
+// is the largest of them; the bias adds 2^-24 of v.  What lies closer is done again in 64 bits: of sigmoids the candidates alone, one to a lane, otherwise all.
 // (A value takes some 30 instructions of the 64-bit unit, 64 cycles each, and a call waits for its last token: with all
 // values again, 8192 tokens took 28 us, of which 14 were for ten of them.)
 template <int V, typename T>
